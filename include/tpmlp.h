@@ -356,6 +356,128 @@ tpmlp_status tpmlp_attention_backward(const void* X, const void* Wqkv, const voi
                                       void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Masked self-attention over query, key and value heads, and what a model runs around it: the
+ * form of the attention block above for long rows, packed documents, prefixes, sliding windows,
+ * grouped heads, capped scores and distance biases, with no matrix of scores in memory. A
+ * training step runs
+ *   QKV = X W_qkv -> tpmlp_qk_norm_rope -> tpmlp_masked_attention_forward -> Y = O W_o
+ * and the backward calls in the reverse order; tpmlp_attention_key_ranges runs once per batch,
+ * its result serves every layer.
+ *
+ * Head layout, all calls: a tensor of heads is addressed as base + token * ld + head * hs (in
+ * elements), token = bi * s + si, so that the packed [b*s][3h] QKV matrix of
+ * tpmlp_attention_forward (head j's q, k, v: base + (0, 1, 2) * head_dim, ld = 3h, hs =
+ * 3 * head_dim), a [all q | all k | all v] matrix (hs = head_dim) and separate [b*s][h] matrices
+ * are all read and written in place. Strides are positive multiples of 8 elements, pointers
+ * 16-byte aligned, and the heads of an output must not overlap. head_dim is a multiple of 8.
+ * heads query heads share kv_heads key and value heads, heads % kv_heads == 0: query head j
+ * reads key head j / (heads / kv_heads).
+ *
+ * Key ranges. Every mask here lets query i see one interval of keys, key_range[bi][i] =
+ * {lo, hi}: keys lo <= j < hi of the same sequence ({0, 0}: none). key_range is int32 [b][s][2],
+ * 8-byte aligned. tpmlp_attention_key_ranges writes it from
+ *   doc_ids     int32 [b][s] or NULL: a document is a run of neighbouring tokens with one id, and
+ *               a token sees its own document only; a negative id is padding, which sees nothing
+ *               and is seen by nobody;
+ *   causal      1: a token sees itself and what stands before it; 0: what stands after it too;
+ *   prefix_len  int32 [b] or NULL, causal only: the tokens of a sequence's first prefix_len[bi]
+ *               positions are visible to every earlier one too (a bidirectional prefix);
+ *   window      0, or w > 0: a token sees itself and the w - 1 tokens before it (and, when not
+ *               causal, the w - 1 after it).
+ * b, s >= 0, b * s <= 2^31-1. Errors: TPMLP_ERR_INVALID (null key_range, causal not 0 or 1, a
+ * prefix without causal, window < 0), TPMLP_ERR_SHAPE, TPMLP_ERR_ALIGN.
+ */
+tpmlp_status tpmlp_attention_key_ranges(const void* doc_ids, const void* prefix_len, int causal, int64_t window,
+                                        void* key_range, int64_t b, int64_t s, void* stream);
+
+/* How tpmlp_qk_norm_rope pairs the rotated columns: (i, i + rot_dim / 2), or (2i, 2i + 1). */
+typedef enum { TPMLP_ROPE_HALF = 0, TPMLP_ROPE_INTERLEAVED = 1 } tpmlp_rope_style;
+
+/*
+ * RMSNorm of every query head and every key head (the "Megatron 训练" notes, section "RMSNorm",
+ * over the head_dim columns of one head) and the rotation by position, in one pass over q and k:
+ *   u = x / sqrt(mean(x^2) + eps) * gamma,   y = R(pos) u
+ * where R turns the first rot_dim columns in pairs (a, b) -> (a cos - b sin, b cos + a sin) with
+ * cos and sin from row pos, column i of cos_table and sin_table [table_len][rot_dim / 2] (fp32),
+ * and passes the others on.
+ *   q, q_out: heads heads; k, k_out: kv_heads heads; dt bf16 or f32. q_out may be q and k_out k
+ *   with the same strides (in place). gamma_q, gamma_k: [head_dim] fp32.
+ *   positions: int32 [b*s], or NULL for the place in the sequence (token % s). A negative
+ *   position marks a row that belongs to no sequence: its heads are written as zeros, whatever it
+ *   holds. A position >= table_len, which the tables do not cover, gives NaN in the rotated columns.
+ *   style: a tpmlp_rope_style. rot_dim is even, 2 <= rot_dim <= head_dim <= 256.
+ * Statistics and arithmetic in fp32, one rounding to dt.
+ */
+tpmlp_status tpmlp_qk_norm_rope(const void* q, const void* k, const float* gamma_q, const float* gamma_k, float eps,
+                                const float* cos_table, const float* sin_table, const void* positions,
+                                int64_t table_len, int rot_dim, int style, void* q_out, void* k_out, int64_t b,
+                                int64_t s, int heads, int kv_heads, int head_dim, int64_t ld_q, int64_t hs_q,
+                                int64_t ld_k, int64_t hs_k, int64_t ld_qo, int64_t hs_qo, int64_t ld_ko,
+                                int64_t hs_ko, tpmlp_dtype dt, void* stream);
+
+/*
+ * Backward of tpmlp_qk_norm_rope from dq_out = dl/dq_out and dk_out (strides ld_qo.., ld_ko..),
+ * with x the heads that went into the forward, r = 1/sqrt(mean(x^2) + eps), x_hat = x r,
+ * du = R(pos)^T dy and g = du gamma:
+ *   dx = r (g - x_hat mean(g x_hat))   into dq, dk (strides ld_dq.., ld_dk..)
+ *   dgamma = sum over tokens and heads of du x_hat   ([head_dim] fp32 each, overwritten; summed in
+ *   a fixed order).
+ * A row of negative position gets zeros in dq and dk and adds nothing to the gains' gradients.
+ * dq may be q or dq_out with the same strides, likewise dk. workspace:
+ * tpmlp_qk_norm_rope_backward_workspace_size(b, s, head_dim) bytes, 16-byte aligned. b * s == 0
+ * zeroes dgamma_q and dgamma_k.
+ */
+size_t tpmlp_qk_norm_rope_backward_workspace_size(int64_t b, int64_t s, int head_dim);
+tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const float* gamma_q, const float* gamma_k,
+                                         float eps, const float* cos_table, const float* sin_table,
+                                         const void* positions, int64_t table_len, int rot_dim, int style,
+                                         const void* dq_out, const void* dk_out, void* dq, void* dk, float* dgamma_q,
+                                         float* dgamma_k, int64_t b, int64_t s, int heads, int kv_heads, int head_dim,
+                                         int64_t ld_q, int64_t hs_q, int64_t ld_k, int64_t hs_k, int64_t ld_qo,
+                                         int64_t hs_qo, int64_t ld_ko, int64_t hs_ko, int64_t ld_dq, int64_t hs_dq,
+                                         int64_t ld_dk, int64_t hs_dk, tpmlp_dtype dt, void* workspace,
+                                         size_t ws_bytes, void* stream);
+
+/*
+ * Masked attention, forward. Per sequence and query head, over the keys of the query's range:
+ *   y_ij = c(scale * q_i . k_j) - slope |i - j|,   c(x) = softcap * tanh(x / softcap), or x when softcap == 0
+ *   lse_i = log sum_j exp(y_ij),   o_i = sum_j exp(y_ij - lse_i) v_j
+ * A query with no keys gets o = 0 and lse = -inf.
+ *   q, o: heads heads; k, v: kv_heads heads, bf16; lse: fp32 [b][heads][s] (kept for the backward).
+ *   key_range: int32 [b][s][2], 8-byte aligned; a range is cut to 0 <= lo, hi <= s.
+ *   slopes: fp32 [heads] (the bias's slope of each head, 4-byte aligned) or NULL for no bias.
+ *   scale > 0 and finite (1 / sqrt(head_dim) in the block above); softcap >= 0 and finite.
+ * bf16 only; head_dim a multiple of 8, 8 <= head_dim <= 128. Scores, statistics and sums are fp32;
+ * the probabilities are rounded to bf16 for the product with V. q, k, v must be finite everywhere,
+ * in masked places too: a hidden value enters the products with weight zero.
+ */
+tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const void* v, const void* key_range,
+                                            const float* slopes, float scale, float softcap, void* o, float* lse,
+                                            int64_t b, int64_t s, int heads, int kv_heads, int head_dim, int64_t ld_q,
+                                            int64_t hs_q, int64_t ld_k, int64_t hs_k, int64_t ld_v, int64_t hs_v,
+                                            int64_t ld_o, int64_t hs_o, tpmlp_dtype dt, void* stream);
+
+/*
+ * Backward of tpmlp_masked_attention_forward from d_o = dl/do (o's strides), o and lse as the
+ * forward wrote them. With P_ij = exp(y_ij - lse_i) recomputed and D_i = d_o_i . o_i,
+ *   dV_j = sum P_ij d_o_i,   dY_ij = P_ij (d_o_i . v_j - D_i),   dX_ij = scale c'(.) dY_ij,
+ *   dQ_i = sum_j dX_ij k_j,   dK_j = sum_i dX_ij q_i,
+ * the sums for a key or value head running over its query heads too. No atomics: every sum has a
+ * fixed order. dq, dk, dv (bf16, strides ld_dq.. and so on) are overwritten; queries without keys
+ * and keys that no query sees get zeros. slopes get no gradient.
+ * workspace: tpmlp_masked_attention_backward_workspace_size bytes, 256-byte aligned.
+ */
+size_t tpmlp_masked_attention_backward_workspace_size(int64_t b, int64_t s, int heads);
+tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const void* v, const void* key_range,
+                                             const float* slopes, float scale, float softcap, const void* o,
+                                             const float* lse, const void* d_o, void* dq, void* dk, void* dv,
+                                             int64_t b, int64_t s, int heads, int kv_heads, int head_dim,
+                                             int64_t ld_q, int64_t hs_q, int64_t ld_k, int64_t hs_k, int64_t ld_v,
+                                             int64_t hs_v, int64_t ld_o, int64_t hs_o, int64_t ld_dq, int64_t hs_dq,
+                                             int64_t ld_dk, int64_t hs_dk, int64_t ld_dv, int64_t hs_dv,
+                                             tpmlp_dtype dt, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Kernel choice for the plain bf16 GEMMs of every later call in this process, for comparing
  * kernels and testing each one; a user of the library never needs it, and nothing else
  * (no environment variable) changes the choice. The defaults, 1, 1, 0, are the fast path:

@@ -21,6 +21,10 @@ What it computes, and which passage of the source pages it follows:
   across shards, softmax(Q K^T / sqrt(head_dim)) V per head, row-parallel output projection) and
   its gradients, from the SenseParrots note's parallel attention code (section 2.1.1) and the
   "Attention 层" section of the "Megatron 训练" notes.
+* ``masked_attention``: attention over one key interval per query (documents, prefixes, causal and
+  sliding windows), with grouped heads, capped scores and distance biases, and its gradients.
+* ``qk_norm_rope``: the per-head RMSNorm of queries and keys with the position rotation, and its
+  gradients.
 * ``collectives``: host "ranks" for all-reduce, all-gather and reduce-scatter, to pin
   AllReduce = AllGather(ReduceScatter(x)) ("Megatron-SP 机制", section
   "f/g 算子怎么定义？").
@@ -32,4 +36,4 @@ closed forms, the block-matrix invariants and the ReLU counterexample. The
 worked example on the pages prints shapes only, so its absolute values are
 parity-unpinned; every other function here is pinned.
 """
-from . import attention, collectives, mlp, sp  # noqa: F401
+from . import attention, collectives, masked_attention, mlp, qk_norm_rope, sp  # noqa: F401

@@ -7,7 +7,9 @@ in the library's kernels; if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -18,6 +20,7 @@ from . import _build
 GELU = {"erf": 0, "tanh": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 RS_MODE = {"fused": 0, "splitk": 1}
+ROPE_STYLE = {"half": 0, "interleaved": 1}
 STATUS = {0: "TPMLP_OK", 1: "TPMLP_ERR_INVALID", 2: "TPMLP_ERR_SHAPE", 3: "TPMLP_ERR_DTYPE", 4: "TPMLP_ERR_ALIGN",
           5: "TPMLP_ERR_CUDA", 6: "TPMLP_ERR_TIMEOUT", 7: "TPMLP_ERR_WORKSPACE"}
 
@@ -55,6 +58,17 @@ SIGNATURES = {
     "tpmlp_attention_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "tpmlp_attention_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _SZ,
                                       _P]),
+    "tpmlp_attention_key_ranges": (_I, [_P, _P, _I, _I64, _P, _I64, _I64, _P]),
+    "tpmlp_qk_norm_rope": (_I, [_P, _P, _P, _P, _F, _P, _P, _P, _I64, _I, _I, _P, _P, _I64, _I64, _I, _I, _I]
+                           + [_I64] * 8 + [_I, _P]),
+    "tpmlp_qk_norm_rope_backward_workspace_size": (_SZ, [_I64, _I64, _I]),
+    "tpmlp_qk_norm_rope_backward": (_I, [_P, _P, _P, _P, _F, _P, _P, _P, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _I64,
+                                         _I64, _I, _I, _I] + [_I64] * 12 + [_I, _P, _SZ, _P]),
+    "tpmlp_masked_attention_forward": (_I, [_P, _P, _P, _P, _P, _F, _F, _P, _P, _I64, _I64, _I, _I, _I] + [_I64] * 8
+                                       + [_I, _P]),
+    "tpmlp_masked_attention_backward_workspace_size": (_SZ, [_I64, _I64, _I]),
+    "tpmlp_masked_attention_backward": (_I, [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I]
+                                        + [_I64] * 14 + [_I, _P, _SZ, _P]),
     "tpmlp_last_error": (ctypes.c_char_p, []),
     "tpmlp_device_status": (_I, [_P, _I]),
     "tpmlp_check_wait_timeout": (_I, [_U64, _P]),
@@ -108,6 +122,46 @@ def _cuda(*ts: torch.Tensor | None) -> None:
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Makes `device` and `stream` (default: the device's current stream) current, so that the kernels run there
+    and what torch allocates meanwhile belongs to that stream. Yields the stream's handle."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _same_device(device: torch.device, *ts: torch.Tensor | None) -> None:
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors are on different devices ({device}, {t.device})")
+
+
+def _heads(t: torch.Tensor, b: int, s: int, heads: int, hd: int, dtype: torch.dtype, name: str) -> tuple[int, int]:
+    """The (token, head) strides of a [b, s, heads, hd] tensor of heads."""
+    if t.shape != (b, s, heads, hd):
+        raise ValueError(f"{name} must be [{b}, {s}, {heads}, {hd}], got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    sb, ss, sh, sc = t.stride()
+    ld = ss if s > 1 else sb if b > 1 else max(heads * hd, 8)
+    if (sc != 1 and hd > 1) or (b > 1 and s > 1 and sb != s * ss):
+        raise ValueError(f"{name} needs contiguous columns and one stride for all tokens of the batch")
+    return ld, sh if heads > 1 else hd
+
+
+def _dense(t: torch.Tensor | None, shape: tuple[int, ...], dtype: torch.dtype, name: str) -> None:
+    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -457,3 +511,138 @@ def attention_backward(X, Wqkv, Wo, G, saves, heads: int, t: int, stream=None):
                                         _ptr(dWqkv), _ptr(dWo), b, s, h, heads, t, _dt(X), _ptr(ws), ws.numel(),
                                         _stream(stream)))
     return dX, dWqkv, dWo
+
+
+# ----------------------------------------------------------------------- masked attention
+
+def attention_key_ranges(b: int, s: int, doc_ids=None, prefix_len=None, causal: bool = True, window: int = 0,
+                         device=None, stream=None):
+    """Runs tpmlp_attention_key_ranges; returns the int32 [b, s, 2] key range of every query, for
+    masked_attention_forward and _backward. doc_ids int32 [b, s], prefix_len int32 [b]; `device` defaults to theirs,
+    else to the current one."""
+    given = doc_ids if doc_ids is not None else prefix_len
+    device = given.device if given is not None else torch.device("cuda" if device is None else device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    _same_device(device, doc_ids, prefix_len)
+    _dense(doc_ids, (b, s), torch.int32, "doc_ids")
+    _dense(prefix_len, (b,), torch.int32, "prefix_len")
+    with _on(device, stream) as st:
+        out = torch.empty((b, s, 2), dtype=torch.int32, device=device)
+        _check(load_library().tpmlp_attention_key_ranges(_ptr(doc_ids), _ptr(prefix_len), int(bool(causal)), window,
+                                                         _ptr(out), b, s, st))
+    return out
+
+
+def rope_tables(table_len: int, rot_dim: int, theta: float = 10000.0, device=None):
+    """The fp32 (cos, sin) tables [table_len, rot_dim / 2] of the angles pos * theta^(-2i / rot_dim), computed in
+    64 bits so that far positions keep their phase."""
+    inv = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    ang = torch.arange(table_len, dtype=torch.float64, device=device)[:, None] * inv
+    return ang.cos().float(), ang.sin().float()
+
+
+def _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions, *others):
+    b, s, heads, hd = q.shape
+    kv = k.shape[2]
+    half = cos.shape[1]
+    _same_device(q.device, k, gamma_q, gamma_k, cos, sin, positions, *others)
+    sq, sk = _heads(q, b, s, heads, hd, q.dtype, "q"), _heads(k, b, s, kv, hd, q.dtype, "k")
+    for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
+        _dense(g, (hd,), torch.float32, name)
+    for name, x in (("cos", cos), ("sin", sin)):
+        _dense(x, (cos.shape[0], half), torch.float32, name)
+    _dense(positions, (b, s), torch.int32, "positions")
+    return b, s, heads, kv, hd, 2 * half, sq, sk
+
+
+def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, eps: float = 1e-5, positions=None, style: str = "half",
+                 q_out=None, k_out=None, stream=None):
+    """q [b, s, heads, head_dim], k [b, s, kv_heads, head_dim] (views of a QKV matrix, for instance). Allocates
+    q_out and k_out unless given (q and k themselves for in place) and runs tpmlp_qk_norm_rope; returns them."""
+    b, s, heads, kv, hd, rot, sq, sk = _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out)
+    with _on(q.device, stream) as st:
+        q_out = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if q_out is None else q_out
+        k_out = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if k_out is None else k_out
+        sqo = _heads(q_out, b, s, heads, hd, q.dtype, "q_out")
+        sko = _heads(k_out, b, s, kv, hd, q.dtype, "k_out")
+        _check(load_library().tpmlp_qk_norm_rope(
+            _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), eps, _ptr(cos), _ptr(sin), _ptr(positions), cos.shape[0],
+            rot, ROPE_STYLE[style], _ptr(q_out), _ptr(k_out), b, s, heads, kv, hd, *sq, *sk, *sqo, *sko, _dt(q), st))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, gamma_q, gamma_k, cos, sin, dq_out, dk_out, eps: float = 1e-5, positions=None,
+                          style: str = "half", dq=None, dk=None, stream=None):
+    """Runs tpmlp_qk_norm_rope_backward from the gradients of q_out and k_out; allocates the workspace, the gains'
+    gradients and, unless given, dq and dk. Returns (dq, dk, dgamma_q, dgamma_k)."""
+    b, s, heads, kv, hd, rot, sq, sk = _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions, dq_out, dk_out, dq, dk)
+    sqo = _heads(dq_out, b, s, heads, hd, q.dtype, "dq_out")
+    sko = _heads(dk_out, b, s, kv, hd, q.dtype, "dk_out")
+    lib = load_library()
+    with _on(q.device, stream) as st:
+        dq = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if dk is None else dk
+        dgq = torch.empty(hd, dtype=torch.float32, device=q.device)
+        dgk = torch.empty(hd, dtype=torch.float32, device=q.device)
+        sdq, sdk = _heads(dq, b, s, heads, hd, q.dtype, "dq"), _heads(dk, b, s, kv, hd, q.dtype, "dk")
+        ws = torch.empty(max(1, lib.tpmlp_qk_norm_rope_backward_workspace_size(b, s, hd)), dtype=torch.uint8,
+                         device=q.device)
+        _check(lib.tpmlp_qk_norm_rope_backward(
+            _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), eps, _ptr(cos), _ptr(sin), _ptr(positions), cos.shape[0],
+            rot, ROPE_STYLE[style], _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dgq), _ptr(dgk), b, s, heads,
+            kv, hd, *sq, *sk, *sqo, *sko, *sdq, *sdk, _dt(q), _ptr(ws), ws.numel(), st))
+    return dq, dk, dgq, dgk
+
+
+def _masked_args(q, k, v, key_range, slopes, *others):
+    b, s, heads, hd = q.shape
+    kv = k.shape[2]
+    _same_device(q.device, k, v, key_range, slopes, *others)
+    _dense(key_range, (b, s, 2), torch.int32, "key_range")
+    _dense(slopes, (heads,), torch.float32, "slopes")
+    strides = (_heads(q, b, s, heads, hd, q.dtype, "q") + _heads(k, b, s, kv, hd, q.dtype, "k")
+               + _heads(v, b, s, kv, hd, q.dtype, "v"))
+    return b, s, heads, kv, hd, strides
+
+
+def masked_attention_forward(q, k, v, key_range, scale: float | None = None, softcap: float = 0.0, slopes=None,
+                             o=None, stream=None):
+    """q [b, s, heads, head_dim], k and v [b, s, kv_heads, head_dim] bf16 (views of a QKV matrix, for instance).
+    Allocates o (unless given) and lse and runs tpmlp_masked_attention_forward; scale defaults to
+    head_dim^-1/2. Returns (o [b, s, heads, head_dim], lse [b, heads, s] fp32)."""
+    b, s, heads, kv, hd, strides = _masked_args(q, k, v, key_range, slopes, o)
+    scale = 1.0 / math.sqrt(hd) if scale is None else scale
+    with _on(q.device, stream) as st:
+        o = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if o is None else o
+        lse = torch.empty((b, heads, s), dtype=torch.float32, device=q.device)
+        so = _heads(o, b, s, heads, hd, q.dtype, "o")
+        _check(load_library().tpmlp_masked_attention_forward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(key_range), _ptr(slopes), scale, softcap, _ptr(o), _ptr(lse), b, s, heads,
+            kv, hd, *strides, *so, _dt(q), st))
+    return o, lse
+
+
+def masked_attention_backward(q, k, v, key_range, o, lse, do, scale: float | None = None, softcap: float = 0.0,
+                              slopes=None, dq=None, dk=None, dv=None, stream=None):
+    """Runs tpmlp_masked_attention_backward from do = dl/do (o's strides); allocates the workspace and, unless given,
+    dq, dk and dv. Returns (dq, dk, dv)."""
+    b, s, heads, kv, hd, strides = _masked_args(q, k, v, key_range, slopes, o, lse, do, dq, dk, dv)
+    scale = 1.0 / math.sqrt(hd) if scale is None else scale
+    _dense(lse, (b, heads, s), torch.float32, "lse")
+    so = _heads(o, b, s, heads, hd, q.dtype, "o")
+    if _heads(do, b, s, heads, hd, q.dtype, "do") != so:
+        raise ValueError("do must have o's strides")
+    lib = load_library()
+    with _on(q.device, stream) as st:
+        dq = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if dk is None else dk
+        dv = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if dv is None else dv
+        grads = (_heads(dq, b, s, heads, hd, q.dtype, "dq") + _heads(dk, b, s, kv, hd, q.dtype, "dk")
+                 + _heads(dv, b, s, kv, hd, q.dtype, "dv"))
+        ws = torch.empty(max(1, lib.tpmlp_masked_attention_backward_workspace_size(b, s, heads)), dtype=torch.uint8,
+                         device=q.device)
+        _check(lib.tpmlp_masked_attention_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(key_range), _ptr(slopes), scale, softcap, _ptr(o), _ptr(lse), _ptr(do),
+            _ptr(dq), _ptr(dk), _ptr(dv), b, s, heads, kv, hd, *strides, *so, *grads, _dt(q), _ptr(ws), ws.numel(), st))
+    return dq, dk, dv

@@ -2029,6 +2029,12 @@ cudaError_t make_tmap_batched(CUtensorMap* map, const BatchedOperand& op, int64_
 
 }  // namespace
 
+cudaError_t make_batched_map(void* map, const BatchedOperand& op, int64_t nz1, int64_t nz2, uint32_t box_inner,
+                             uint32_t box_row, int (&slots)[3]) {
+  return make_tmap_batched(static_cast<CUtensorMap*>(map), op, nz1, nz2, box_inner, box_row, &slots[0], &slots[1],
+                           &slots[2]);
+}
+
 void set_gemm_variant(int pair_kernel, int pair_pacing, int pair_group) {
   g_pair_kernel.store(pair_kernel, std::memory_order_relaxed);
   g_pair_pacing.store(pair_pacing, std::memory_order_relaxed);

@@ -127,6 +127,12 @@ cudaError_t gemm_bf16_tc_batched(int64_t M, int64_t N, int64_t K, const BatchedO
                                  const BatchSpec& bs, EpiKind epi, const EpiParams& ep, cudaStream_t stream,
                                  const DeviceCtx& ctx);
 
+// 4-D bf16 tensor map (128-byte swizzle, zero fill) over `op` batched by z1 (nz1) and z2 (nz2); one copy takes
+// box_inner columns x box_row rows of one batch index. `map` is a CUtensorMap. slots[0..2] receive the coordinate
+// slots (1..3) of the row, z1 and z2 (ordered by stride).
+cudaError_t make_batched_map(void* map, const BatchedOperand& op, int64_t nz1, int64_t nz2, uint32_t box_inner,
+                             uint32_t box_row, int (&slots)[3]);
+
 // fp32 FMA GEMM for the fp32 dtype, same semantics and epilogues (outputs in fp32).
 cudaError_t gemm_f32_simt(int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b, EpiKind epi,
                           const EpiParams& ep, cudaStream_t stream);
@@ -178,5 +184,41 @@ cudaError_t launch_softmax_combine(const void* stats, int nparts, void* rowstats
                                    int num_sms);
 cudaError_t launch_row_dot(const void* dO, const void* O, float* D, int64_t b, int64_t s, int64_t h, int heads,
                            cudaStream_t stream, int num_sms);
+
+// One tensor of heads: element (token, head, column) at ptr + token * ld + head * hs + column.
+struct HeadView {
+  void* ptr;
+  int64_t ld, hs;
+};
+
+// Whether a view's strides can be used: positive multiples of 8, small enough that no offset of b * s tokens (at most
+// 2^31) overflows 64 bits and that a tensor map takes them (strides below 2^40 bytes).
+inline bool good_head_strides(const HeadView& v, int64_t s) {
+  return v.ld > 0 && v.hs > 0 && v.ld % 8 == 0 && v.hs % 8 == 0 && v.ld <= (int64_t{1} << 31) &&
+         v.hs <= (int64_t{1} << 38) && (s < 1 || v.ld <= (int64_t{1} << 38) / s);
+}
+// Whether an output's heads lie apart: all heads of a token before the next token's, or all tokens of a head before
+// the next head's.
+inline bool heads_apart(const HeadView& v, int64_t tokens, int heads, int hd) {
+  if (v.ld < hd || (heads > 1 && v.hs < hd)) return tokens <= 1 && (heads <= 1 || v.hs >= hd);
+  return heads <= 1 || (v.ld - hd) / v.hs >= heads - 1 || (v.hs - hd) / v.ld >= tokens - 1;
+}
+
+// Masked attention (tpmlp_masked_attention_*): everything but the gradients. Sizes are checked by the caller.
+struct MaskedAttention {
+  HeadView q, k, v, o;
+  const int2* range;     // [b][s] {lo, hi}
+  const float* slopes;   // [heads] or null
+  float scale, softcap;
+  float* lse;            // [b][heads][s]
+  int64_t b, s;
+  int heads, kv_heads, head_dim;
+};
+
+cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream_t stream, const DeviceCtx& ctx);
+// dsum: [b][heads][s] floats of workspace, receives D = rowsum(d_o * o).
+cudaError_t launch_masked_attention_backward(const MaskedAttention& a, const HeadView& d_o, const HeadView& dq,
+                                             const HeadView& dk, const HeadView& dv, float* dsum, cudaStream_t stream,
+                                             const DeviceCtx& ctx);
 
 }  // namespace tpmlp

@@ -1,0 +1,271 @@
+// C ABI of masked attention (tpmlp_attention_key_ranges, tpmlp_masked_attention_forward / _backward):
+// the checks of the arguments, and the small kernel that turns a batch's documents, prefixes, causality
+// and window into one key interval per query. The attention kernels are in masked_attention.cu.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdio>
+
+#include "../../include/tpmlp.h"
+#include "tpmlp_internal.h"
+
+namespace tpmlp {
+namespace {
+
+constexpr int kRangeThreads = 1024;
+constexpr int kRangeItems = 8;
+
+// The interval of query i, whose document (or sequence) is [start, end).
+__device__ __forceinline__ int2 query_range(int64_t i, int64_t start, int64_t end, int causal, int64_t prefix,
+                                            int64_t window) {
+  int64_t lo = start, hi = end;
+  if (causal) {
+    hi = min(hi, max(i + 1, prefix));
+  } else if (window > 0) {
+    hi = min(hi, i + window);
+  }
+  if (window > 0) lo = max(lo, i - window + 1);
+  return lo < hi ? make_int2(static_cast<int>(lo), static_cast<int>(hi)) : make_int2(0, 0);
+}
+
+__global__ void __launch_bounds__(256)
+    key_range_kernel(const int* __restrict__ prefix, int causal, int64_t window, int2* __restrict__ out, int64_t b,
+                     int64_t s) {
+  for (int64_t t = blockIdx.x * 256ll + threadIdx.x; t < b * s; t += gridDim.x * 256ll) {
+    const int64_t bi = t / s, i = t - bi * s;
+    out[t] = query_range(i, 0, s, causal, prefix ? prefix[bi] : 0, window);
+  }
+}
+
+// The same with documents, one CTA per sequence. A document is a run of equal ids: token i's starts at the
+// last j <= i whose id differs from its left neighbour's (a running maximum from the left) and ends at the
+// first such j > i (a running minimum from the right). Both scans go tile by tile: eight tokens a thread,
+// warp shuffles, then the warps' totals, with the outermost value carried to the next tile. The first scan
+// parks each start in out[].x, which the thread that wrote it reads back in the second.
+__global__ void __launch_bounds__(kRangeThreads)
+    doc_key_range_kernel(const int* __restrict__ ids_all, const int* __restrict__ prefix, int causal, int64_t window,
+                         int2* __restrict__ out_all, int s) {
+  constexpr int kTile = kRangeThreads * kRangeItems;
+  __shared__ int warp_total[kRangeThreads / 32];
+  const int64_t bi = blockIdx.x;
+  const int* ids = ids_all + bi * s;
+  int2* out = out_all + bi * s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ntiles = (s + kTile - 1) / kTile;
+  int carry = 0;
+  for (int tile = 0; tile < ntiles; ++tile) {
+    const int64_t i0 = static_cast<int64_t>(tile) * kTile + threadIdx.x * kRangeItems;
+    int own[kRangeItems], run = -1;
+#pragma unroll
+    for (int e = 0; e < kRangeItems; ++e) {
+      const int64_t i = i0 + e;
+      if (i < s && (i == 0 || ids[i] != ids[i - 1])) run = static_cast<int>(i);
+      own[e] = run;
+    }
+    int incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = max(incl, v);
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    int before = carry, all = carry;
+    for (int w = 0; w < kRangeThreads / 32; ++w) {
+      const int v = warp_total[w];
+      if (w < warp) before = max(before, v);
+      all = max(all, v);
+    }
+    const int left = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane > 0) before = max(before, left);
+    carry = all;
+#pragma unroll
+    for (int e = 0; e < kRangeItems; ++e)
+      if (i0 + e < s) out[i0 + e].x = max(before, own[e]);
+    __syncthreads();
+  }
+  carry = s;
+  for (int tile = ntiles - 1; tile >= 0; --tile) {
+    const int64_t i0 = static_cast<int64_t>(tile) * kTile + threadIdx.x * kRangeItems;
+    int own[kRangeItems], run = s;
+#pragma unroll
+    for (int e = kRangeItems - 1; e >= 0; --e) {
+      const int64_t i = i0 + e;
+      if (i + 1 < s && ids[i] != ids[i + 1]) run = static_cast<int>(i + 1);
+      own[e] = run;
+    }
+    int incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_down_sync(0xffffffffu, incl, o);
+      if (lane + o < 32) incl = min(incl, v);
+    }
+    if (lane == 0) warp_total[warp] = incl;
+    __syncthreads();
+    int after = carry, all = carry;
+    for (int w = 0; w < kRangeThreads / 32; ++w) {
+      const int v = warp_total[w];
+      if (w > warp) after = min(after, v);
+      all = min(all, v);
+    }
+    const int right = __shfl_down_sync(0xffffffffu, incl, 1);
+    if (lane < 31) after = min(after, right);
+    carry = all;
+#pragma unroll
+    for (int e = 0; e < kRangeItems; ++e) {
+      const int64_t i = i0 + e;
+      if (i < s) {
+        const int2 r = query_range(i, out[i].x, min(after, own[e]), causal, prefix ? prefix[bi] : 0, window);
+        out[i] = ids[i] < 0 ? make_int2(0, 0) : r;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+tpmlp_status err(tpmlp_status st, const char* msg) { return static_cast<tpmlp_status>(report_error(st, msg)); }
+
+tpmlp_status cuda_err(cudaError_t e, const char* what) {
+  char msg[256];
+  snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
+  return err(TPMLP_ERR_CUDA, msg);
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+tpmlp_status check_shape(float scale, float softcap, int64_t b, int64_t s, int heads, int kv_heads, int hd,
+                         tpmlp_dtype dt, std::initializer_list<HeadView> inputs,
+                         std::initializer_list<HeadView> q_outputs, std::initializer_list<HeadView> k_outputs) {
+  if (dt != TPMLP_BF16) return err(TPMLP_ERR_DTYPE, "masked attention runs on the bf16 tensor-core path only");
+  if (b < 0 || s < 0 || heads < 1 || kv_heads < 1)
+    return err(TPMLP_ERR_SHAPE, "need b, s >= 0 and heads, kv_heads >= 1");
+  if (b > 0 && s > INT32_MAX / b) return err(TPMLP_ERR_SHAPE, "b * s exceeds 2^31-1");
+  if (b > 65535 || heads > 65535) return err(TPMLP_ERR_SHAPE, "at most 65535 sequences and heads");
+  if (heads % kv_heads != 0) return err(TPMLP_ERR_SHAPE, "heads must be a multiple of kv_heads");
+  if (hd < 8 || hd % 8 != 0 || hd > 128)
+    return err(TPMLP_ERR_SHAPE, "head_dim must be a multiple of 8, 8 <= head_dim <= 128");
+  for (const auto& list : {inputs, q_outputs, k_outputs})
+    for (const HeadView& v : list)
+      if (!good_head_strides(v, s))
+        return err(TPMLP_ERR_SHAPE, "strides must be positive multiples of 8 (row 2^31, head and sequence 2^38 at most)");
+  for (const HeadView& v : q_outputs)
+    if (!heads_apart(v, b * s, heads, hd)) return err(TPMLP_ERR_SHAPE, "an output's heads overlap");
+  for (const HeadView& v : k_outputs)
+    if (!heads_apart(v, b * s, kv_heads, hd)) return err(TPMLP_ERR_SHAPE, "an output's heads overlap");
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return err(TPMLP_ERR_INVALID, "scale must be positive and finite");
+  if (!(softcap >= 0.0f) || !std::isfinite(softcap)) return err(TPMLP_ERR_INVALID, "softcap must be >= 0 and finite");
+  return TPMLP_OK;
+}
+
+tpmlp_status check_ptrs(std::initializer_list<const void*> ptrs, size_t a, const char* what) {
+  for (const void* p : ptrs) {
+    if (!p) return err(TPMLP_ERR_INVALID, "null pointer");
+    if (!aligned(p, a)) return err(TPMLP_ERR_ALIGN, what);
+  }
+  return TPMLP_OK;
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+using namespace tpmlp;
+
+#define MATT_TRY(expr)                  \
+  do {                                  \
+    tpmlp_status _s = (expr);           \
+    if (_s != TPMLP_OK) return _s;      \
+  } while (0)
+#define MATT_CUDA(expr, what)                       \
+  do {                                              \
+    cudaError_t _e = (expr);                        \
+    if (_e != cudaSuccess) return cuda_err(_e, what); \
+  } while (0)
+
+extern "C" {
+
+tpmlp_status tpmlp_attention_key_ranges(const void* doc_ids, const void* prefix_len, int causal, int64_t window,
+                                        void* key_range, int64_t b, int64_t s, void* stream) {
+  if (b < 0 || s < 0) return err(TPMLP_ERR_SHAPE, "need b, s >= 0");
+  if (b > 0 && s > INT32_MAX / b) return err(TPMLP_ERR_SHAPE, "b * s exceeds 2^31-1");
+  if (causal != 0 && causal != 1) return err(TPMLP_ERR_INVALID, "causal is 0 or 1");
+  if (window < 0) return err(TPMLP_ERR_INVALID, "window must be >= 0");
+  if (prefix_len && !causal) return err(TPMLP_ERR_INVALID, "a prefix needs a causal mask");
+  if (b * s == 0) return TPMLP_OK;
+  MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
+  if (!aligned(doc_ids, 4) || !aligned(prefix_len, 4))
+    return err(TPMLP_ERR_ALIGN, "doc_ids and prefix_len must be 4-byte aligned");
+  if (window > s) window = 0;  // reaches past both ends
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int* prefix = static_cast<const int*>(prefix_len);
+  int2* out = static_cast<int2*>(key_range);
+  if (doc_ids) {
+    doc_key_range_kernel<<<static_cast<unsigned>(b), kRangeThreads, 0, st>>>(static_cast<const int*>(doc_ids), prefix,
+                                                                             causal, window, out, static_cast<int>(s));
+  } else {
+    const int64_t ctas = (b * s + 255) / 256;
+    key_range_kernel<<<static_cast<unsigned>(ctas < 4096 ? ctas : 4096), 256, 0, st>>>(prefix, causal, window, out, b, s);
+  }
+  MATT_CUDA(cudaGetLastError(), "key ranges");
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const void* v, const void* key_range,
+                                            const float* slopes, float scale, float softcap, void* o, float* lse,
+                                            int64_t b, int64_t s, int heads, int kv_heads, int head_dim, int64_t ld_q,
+                                            int64_t hs_q, int64_t ld_k, int64_t hs_k, int64_t ld_v, int64_t hs_v,
+                                            int64_t ld_o, int64_t hs_o, tpmlp_dtype dt, void* stream) {
+  MATT_TRY(check_shape(scale, softcap, b, s, heads, kv_heads, head_dim, dt,
+                       {{nullptr, ld_q, hs_q}, {nullptr, ld_k, hs_k}, {nullptr, ld_v, hs_v}}, {{o, ld_o, hs_o}}, {}));
+  if (b * s == 0) return TPMLP_OK;
+  MATT_TRY(check_ptrs({q, k, v, o}, 16, "pointers must be 16-byte aligned"));
+  MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
+  MATT_TRY(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
+  if (!aligned(slopes, 4)) return err(TPMLP_ERR_ALIGN, "slopes not 4-byte aligned");
+  DeviceCtx ctx;
+  MATT_CUDA(get_device_ctx(&ctx), "device context");
+  MaskedAttention a{{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(k), ld_k, hs_k},
+                    {const_cast<void*>(v), ld_v, hs_v}, {o, ld_o, hs_o}, static_cast<const int2*>(key_range), slopes,
+                    scale, softcap, lse, b, s, heads, kv_heads, head_dim};
+  MATT_CUDA(launch_masked_attention_forward(a, static_cast<cudaStream_t>(stream), ctx), "masked attention");
+  return TPMLP_OK;
+}
+
+size_t tpmlp_masked_attention_backward_workspace_size(int64_t b, int64_t s, int heads) {
+  if (b <= 0 || s <= 0 || heads <= 0) return 0;
+  return (static_cast<size_t>(b) * static_cast<size_t>(s) * static_cast<size_t>(heads) * sizeof(float) + 255) / 256 * 256;
+}
+
+tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const void* v, const void* key_range,
+                                             const float* slopes, float scale, float softcap, const void* o,
+                                             const float* lse, const void* d_o, void* dq, void* dk, void* dv,
+                                             int64_t b, int64_t s, int heads, int kv_heads, int head_dim,
+                                             int64_t ld_q, int64_t hs_q, int64_t ld_k, int64_t hs_k, int64_t ld_v,
+                                             int64_t hs_v, int64_t ld_o, int64_t hs_o, int64_t ld_dq, int64_t hs_dq,
+                                             int64_t ld_dk, int64_t hs_dk, int64_t ld_dv, int64_t hs_dv,
+                                             tpmlp_dtype dt, void* workspace, size_t ws_bytes, void* stream) {
+  MATT_TRY(check_shape(scale, softcap, b, s, heads, kv_heads, head_dim, dt,
+                       {{nullptr, ld_q, hs_q}, {nullptr, ld_k, hs_k}, {nullptr, ld_v, hs_v}, {nullptr, ld_o, hs_o}},
+                       {{dq, ld_dq, hs_dq}}, {{dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}}));
+  if (b * s == 0) return TPMLP_OK;
+  MATT_TRY(check_ptrs({q, k, v, o, d_o, dq, dk, dv}, 16, "pointers must be 16-byte aligned"));
+  MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
+  MATT_TRY(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
+  if (!aligned(slopes, 4)) return err(TPMLP_ERR_ALIGN, "slopes not 4-byte aligned");
+  const size_t need = tpmlp_masked_attention_backward_workspace_size(b, s, heads);
+  if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "masked attention backward workspace too small");
+  if (!aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
+  DeviceCtx ctx;
+  MATT_CUDA(get_device_ctx(&ctx), "device context");
+  MaskedAttention a{{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(k), ld_k, hs_k},
+                    {const_cast<void*>(v), ld_v, hs_v}, {const_cast<void*>(o), ld_o, hs_o},
+                    static_cast<const int2*>(key_range), slopes, scale, softcap, const_cast<float*>(lse), b, s, heads,
+                    kv_heads, head_dim};
+  MATT_CUDA(launch_masked_attention_backward(a, {const_cast<void*>(d_o), ld_o, hs_o}, {dq, ld_dq, hs_dq},
+                                             {dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}, static_cast<float*>(workspace),
+                                             static_cast<cudaStream_t>(stream), ctx),
+            "masked attention backward");
+  return TPMLP_OK;
+}
+
+}  // extern "C"
