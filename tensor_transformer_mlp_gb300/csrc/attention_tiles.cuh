@@ -1,0 +1,130 @@
+// What the masked-attention kernels share: the tensor-core forms with an operand in tensor memory, tiles of heads
+// loaded by tensor copies, key intervals, and the score function.
+#pragma once
+
+#include "device_common.cuh"
+
+namespace tpmlp {
+
+constexpr int kTile = 128;                 // query rows and key rows of a tile
+constexpr int kBoxBytes = kTile * 128;     // 128 rows x 64 bf16 columns, one 128-byte-swizzled box
+
+// ------------------------------------------------------------------ tcgen05
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are the lanes, two bf16 of K per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define TPMLP_R8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+
+// 32 lanes x 32 consecutive 32-bit columns: thread i of the warp writes lane (base + i).
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      TPMLP_R8(r, 0), TPMLP_R8(r, 8), TPMLP_R8(r, 16), TPMLP_R8(r, 24)
+      : "memory");
+}
+
+// The same with 16 columns.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      TPMLP_R8(r, 0), TPMLP_R8(r, 8)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Moves a warpgroup's share of the block's registers (every warp of the warpgroup calls it; the shares of all
+// warpgroups together stay within what the block was launched with).
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ------------------------------------------------------------------ tiles of heads
+
+// Tensor map of one tensor of heads, with the coordinate slots of token, head and sequence.
+struct HeadMap {
+  CUtensorMap map;
+  int row, head, seq;
+};
+
+inline cudaError_t make_head_map(HeadMap* m, const HeadView& v, int64_t b, int64_t s, int heads, int head_dim) {
+  int slots[3];
+  const cudaError_t e = make_batched_map(&m->map, BatchedOperand{v.ptr, s, head_dim, v.ld, v.hs, s * v.ld, false}, heads, b,
+                                         64, kTile, slots);
+  m->row = slots[0];
+  m->head = slots[1];
+  m->seq = slots[2];
+  return e;
+}
+
+// Loads rows [row, row + 128) of one head (columns [0, 64 * boxes)) into consecutive boxes; rows past the sequence and
+// columns past the head are filled with zeros. One thread; completes boxes * kBoxBytes on bar.
+__device__ __forceinline__ void load_head_tile(void* dst, const HeadMap& m, uint64_t* bar, int boxes, int row, int head,
+                                               int seq) {
+  const int c1 = m.row == 1 ? row : (m.head == 1 ? head : seq);
+  const int c2 = m.row == 2 ? row : (m.head == 2 ? head : seq);
+  const int c3 = m.row == 3 ? row : (m.head == 3 ? head : seq);
+  for (int x = 0; x < boxes; ++x)
+    tma_load_4d(static_cast<uint8_t*>(dst) + x * kBoxBytes, &m.map, bar, x * 64, c1, c2, c3);
+}
+
+// Descriptor of K-step kk (16 of the head's columns) of a tile used K-major (rows are M or N).
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int kk) {
+  return smem_desc_sw128(tile + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024);
+}
+// Descriptor of K-step kk (16 of the tile's rows) of a tile used MN-major (the head's columns are N).
+__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int kk) {
+  return smem_desc_sw128(tile + kk * 2048, kBoxBytes, 1024);
+}
+
+// ------------------------------------------------------------------ masks and scores
+
+// The key interval of a query row cut to the sequence; {0, 0} when nothing is left.
+__device__ __forceinline__ int2 clip_range(int2 r, int s) {
+  r.x = max(r.x, 0);
+  r.y = min(r.y, s);
+  return r.x < r.y ? r : make_int2(0, 0);
+}
+
+// Scores in base 2: y log2(e) as a function of q.k. With a cap, cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2x/cap))),
+// whose absolute error, a few 2^-24 of the cap, is what the exponent sees (tanh.approx's 2^-11 would not do).
+struct ScoreParams {
+  float scale2;   // scale * log2(e); with a cap: 2 scale log2(e) / cap
+  float cap2;     // cap * log2(e)
+};
+
+inline ScoreParams score_params(float scale, float softcap) {
+  const double log2e = 1.4426950408889634;
+  return softcap > 0.f ? ScoreParams{static_cast<float>(2.0 * scale * log2e / softcap), static_cast<float>(softcap * log2e)}
+                       : ScoreParams{static_cast<float>(scale * log2e), 0.f};
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / (1 + e^(2x/cap)) = (1 - tanh(x / cap)) / 2 of a raw score.
+__device__ __forceinline__ float cap_sigma(float qk, const ScoreParams& p) {
+  return rcp_approx(1.0f + ex2_approx(qk * p.scale2));
+}
+
+}  // namespace tpmlp

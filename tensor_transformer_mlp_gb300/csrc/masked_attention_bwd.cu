@@ -56,48 +56,6 @@ __device__ __forceinline__ int2 clipped(const MaskedAttention& a, int64_t token)
   return r.x < r.y ? r : make_int2(0, 0);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-__global__ void __launch_bounds__(kWarps * 32) forward_rows_kernel(const MaskedAttention a) {
-  const int lane = threadIdx.x & 31, hd = a.head_dim;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int head = blockIdx.y, kvh = head / (a.heads / a.kv_heads);
-  if (i >= a.s) return;
-  const int64_t base = blockIdx.z * a.s, token = base + i;
-  const int2 r = clipped(a, token);
-  const bf16* q = row_of(a.q, token, head);
-  float m = -INFINITY, l = 0.f, acc[kCols] = {};
-  for (int j0 = r.x; j0 < r.y; j0 += 32) {
-    const int j = j0 + lane;
-    float y = -INFINITY, dcap;
-    if (j < r.y) y = score(a, dot(q, row_of(a.k, base + j, kvh), hd), head, i, j, &dcap);
-    const float m2 = fmaxf(m, warp_max(y)), p = expf(y - m2), f = expf(m - m2);
-    l = l * f + warp_sum(p);
-    m = m2;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) acc[c] *= f;
-    for (int e = 0; e < min(32, r.y - j0); ++e) {
-      const float pe = __shfl_sync(0xffffffffu, p, e);
-      const bf16* v = row_of(a.v, base + j0 + e, kvh);
-#pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        if (lane + 32 * c < hd) acc[c] = fmaf(pe, __bfloat162float(v[lane + 32 * c]), acc[c]);
-    }
-  }
-  bf16* o = const_cast<bf16*>(row_of(a.o, token, head));
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    if (lane + 32 * c < hd) o[lane + 32 * c] = __float2bfloat16(l > 0.f ? acc[c] / l : 0.f);
-  if (lane == 0) a.lse[(blockIdx.z * static_cast<int64_t>(a.heads) + head) * a.s + i] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
 __global__ void __launch_bounds__(kWarps * 32) dq_rows_kernel(const MaskedAttention a, const HeadView d_o,
                                                               const HeadView dq, float* dsum) {
   const int lane = threadIdx.x & 31, hd = a.head_dim;
@@ -186,11 +144,6 @@ dim3 rows_grid(const MaskedAttention& a, int heads) {
 }
 
 }  // namespace
-
-cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream_t stream, const DeviceCtx&) {
-  forward_rows_kernel<<<rows_grid(a, a.heads), kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_masked_attention_backward(const MaskedAttention& a, const HeadView& d_o, const HeadView& dq,
                                              const HeadView& dk, const HeadView& dv, float* dsum, cudaStream_t stream,

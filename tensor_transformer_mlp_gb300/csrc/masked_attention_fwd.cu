@@ -1,0 +1,397 @@
+// Masked attention, forward, on the tensor cores: o = softmax(y) V and the rows' log-sum-exp, in one pass over the
+// keys with running statistics, no score leaving the SM.
+//
+//   y_ij = c(scale q_i.k_j) - slope |i - j| for lo_i <= j < hi_i;   per key tile, with m the running maximum:
+//   P = 2^(y log2 e - m),  l += sum P,  O += P V;   at the end o = O / l,  lse = ln 2 (m + log2 l)
+//
+// A CTA holds two tiles of 128 queries of one head and walks the key tiles that either of them sees:
+//   warps 0-3, 4-7  softmax of query tile 0 and 1, one row per thread (tensor-memory lane)
+//   warp 8          one thread loads Q once and K, V tiles through a ring (tensor copies)
+//   warp 9          one thread issues the products: S = Q K^T into 128 columns per query tile, and O += P V with P
+//                   read from tensor memory (bf16, over the columns of its S)
+// The two tiles take turns: while one's softmax runs, the tensor core works on the other's P V and next S. S of a
+// tile's next step is issued after its P V, and the tensor core runs in order, so P is never overwritten early and a
+// completed S also says that the P V before it is done: O may then be rescaled. That is done only when the maximum
+// grew by more than 2^8 (P then stays below 2^8 and l below 2^8 s, far inside fp32), so almost never: the statistics
+// stay those of one common m and the result does not depend on it.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attention_tiles.cuh"
+
+namespace tpmlp {
+namespace {
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+// Registers: 168 a thread at launch (three warpgroups); the two of the softmax, whose threads hold a row of 128
+// scores, take 216 and the third keeps 72 (2 * 216 + 72 = 3 * 168).
+constexpr int kRegsSoftmax = 216, kRegsIssue = 72;
+constexpr float kRescaleAt = 8.0f;
+
+struct FwdParams {
+  HeadMap q, k, v;
+  HeadView o;
+  const int2* range;
+  const float* slopes;
+  float* lse;
+  ScoreParams sp;
+  int s, heads, group, head_dim, nblocks, bheads;  // bheads: heads * b
+  unsigned int* status;
+};
+
+template <int HD>
+struct FwdSmem {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr int kBytes = 1024 + (2 + kStages) * kTileBytes + 512;
+};
+
+struct Span {  // key tiles [lo, hi) of a query tile
+  int lo, hi;
+  __device__ __forceinline__ bool has(int j) const { return lo <= j && j < hi; }
+};
+
+template <int HD, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(const __grid_constant__ FwdParams p) {
+  using L = FwdSmem<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sq = smem;                                   // two Q tiles
+  uint8_t* ring = smem + 2 * L::kTileBytes;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + L::kStages * L::kTileBytes);
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* kv_full = o_full + 2;
+  uint64_t* kv_empty = kv_full + L::kStages;
+  uint64_t* drain = kv_empty + L::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int2* warp_span = reinterpret_cast<int2*>(tmem_slot + 2);  // min lo, max hi of each softmax warp's rows
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // query blocks with the most keys (the last, under a causal mask) start first
+  const int blk = p.nblocks - 1 - static_cast<int>(blockIdx.x) / p.bheads;
+  const int bh = static_cast<int>(blockIdx.x) % p.bheads;
+  const int seq = bh / p.heads, head = bh - seq * p.heads, kvh = head / p.group;
+  const int q0 = blk * 2 * kTile;
+  const int64_t base = static_cast<int64_t>(seq) * p.s;
+
+  int2 r = make_int2(0, 0);
+  const int row = q0 + static_cast<int>(threadIdx.x);
+  if (warp < kSoftmaxWarps) {
+    if (row < p.s) r = clip_range(p.range[base + row], p.s);
+    const int lo = __reduce_min_sync(0xffffffffu, r.x < r.y ? r.x : INT32_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, r.y);
+    if (lane == 0) warp_span[warp] = make_int2(lo, hi);
+  } else if (warp == kSoftmaxWarps) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&q_full[i], 1);
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], 4);
+        mbar_init(&o_full[i], 1);
+      }
+      for (int i = 0; i < L::kStages; ++i) {
+        mbar_init(&kv_full[i], 1);
+        mbar_init(&kv_empty[i], 1);
+      }
+      mbar_init(drain, 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&p.q.map);
+      tma_prefetch_desc(&p.k.map);
+      tma_prefetch_desc(&p.v.map);
+    }
+  } else if (warp == kSoftmaxWarps + 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Span span[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int lo = INT32_MAX, hi = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int2 v = warp_span[4 * i + w];
+      lo = min(lo, v.x);
+      hi = max(hi, v.y);
+    }
+    span[i] = hi > 0 ? Span{lo / kTile, (hi + kTile - 1) / kTile} : Span{0, 0};
+  }
+  const bool any0 = span[0].lo < span[0].hi, any1 = span[1].lo < span[1].hi;
+  const int j_begin = any0 ? (any1 ? min(span[0].lo, span[1].lo) : span[0].lo) : span[1].lo;
+  const int j_end = max(span[0].hi, span[1].hi);
+  auto next = [&](int j) {  // the next key tile at or after j that some query tile sees
+    while (j < j_end && !span[0].has(j) && !span[1].has(j)) ++j;
+    return j;
+  };
+
+  if (warp >= kSoftmaxWarps) {
+    regs_dec<kRegsIssue>();
+    if (warp == kSoftmaxWarps && lane == 0) {
+      // ---------------------------------------------------------------- loads
+      bool ok = true;
+      int n = 0;
+      for (int i = 0; i < 2; ++i)
+        if (i ? any1 : any0) {
+          mbar_arrive_expect_tx(&q_full[i], L::kTileBytes);
+          load_head_tile(sq + i * L::kTileBytes, p.q, &q_full[i], L::kBoxes, q0 + i * kTile, head, seq);
+        }
+      for (int j = next(j_begin); j < j_end && ok; j = next(j + 1)) {
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int st = n % L::kStages;
+          if (!mbar_wait(&kv_empty[st], ((n / L::kStages) & 1) ^ 1, p.status, 0x20)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&kv_full[st], L::kTileBytes);
+          load_head_tile(ring + st * L::kTileBytes, kv ? p.v : p.k, &kv_full[st], L::kBoxes, j * kTile, kvh, seq);
+        }
+      }
+      // The copies in flight must land before shared memory goes away (those that the products wait for have).
+      if (!ok) {
+        for (int i = 0; i < 2; ++i)
+          if (i ? any1 : any0) mbar_wait(&q_full[i], 0, p.status, 0x21);
+        for (int k = max(0, n - L::kStages); k < n; ++k)
+          mbar_wait(&kv_full[k % L::kStages], (k / L::kStages) & 1, p.status, 0x21);
+      }
+    } else if (warp == kSoftmaxWarps + 1 && lane == 0) {
+      // ---------------------------------------------------------------- products
+      const int ksteps = (p.head_dim + 15) / 16;
+      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
+      const uint32_t idesc_o = idesc_bf16_f32(kTile, ksteps * 16, false, true);
+      const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
+      bool ok = true;
+      auto wait_stage = [&](int n) {
+        if (ok) ok = mbar_wait(&kv_full[n % L::kStages], (n / L::kStages) & 1, p.status, 0x22);
+        tc_fence_after();
+        return ring_addr + (n % L::kStages) * L::kTileBytes;
+      };
+      auto scores = [&](int i, uint32_t k_tile) {
+        for (int kk = 0; kk < ksteps; ++kk)
+          umma_bf16(tmem + i * 128, desc_rows(q_addr + i * L::kTileBytes, kk), desc_rows(k_tile, kk), idesc_s, kk != 0);
+        umma_commit(&s_full[i]);
+      };
+      int j = next(j_begin), n = 0, steps[2] = {0, 0};
+      if (j < j_end) {
+        const uint32_t k_tile = wait_stage(0);
+        for (int i = 0; i < 2 && ok; ++i)
+          if (i ? any1 : any0) {
+            ok = mbar_wait(&q_full[i], 0, p.status, 0x23);
+            tc_fence_after();
+            if (ok && span[i].has(j)) scores(i, k_tile);
+          }
+        if (ok) umma_commit(&kv_empty[0]);
+      }
+      while (j < j_end && ok) {
+        const int jn = next(j + 1);
+        const uint32_t v_tile = wait_stage(2 * n + 1);
+        uint32_t k_next = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (ok && span[i].has(j)) {
+            ok = mbar_wait(&p_full[i], steps[i] & 1, p.status, 0x24);
+            tc_fence_after();
+            if (ok) {
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                umma_bf16_ta(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, desc_cols(v_tile, kk), idesc_o,
+                             (steps[i] | kk) != 0);
+              ++steps[i];
+              if (j + 1 == span[i].hi) umma_commit(&o_full[i]);
+            }
+          }
+          if (ok && jn < j_end && span[i].has(jn)) {
+            if (!k_next) k_next = wait_stage(2 * n + 2);
+            if (ok) scores(i, k_next);
+          }
+        }
+        if (ok) umma_commit(&kv_empty[(2 * n + 1) % L::kStages]);
+        if (ok && jn < j_end) umma_commit(&kv_empty[(2 * n + 2) % L::kStages]);
+        ++n;
+        j = jn;
+      }
+      // every product issued must be done before tensor memory is freed
+      umma_commit(drain);
+      mbar_wait(drain, 0, p.status, 0x25);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    regs_inc<kRegsSoftmax>();
+    const int i = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * 128;
+    const float slope2 = BIAS ? p.slopes[head] * kLog2e : 0.f;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    int step = 0;
+    const Span mine = i ? span[1] : span[0];
+    for (int j = mine.lo; j < mine.hi; ++j, ++step) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], step & 1, p.status, 0x26));
+      if (!ok) break;
+      tc_fence_after();
+      float y[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tmem_ld_32x32b_x32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(y) + c * 32));
+      tmem_ld_wait();
+      const int k0 = j * kTile;
+      if constexpr (CAP) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) y[c] = fmaf(-2.0f * p.sp.cap2, cap_sigma(y[c], p.sp), p.sp.cap2);
+      }
+      if constexpr (BIAS) {
+        const float d0 = static_cast<float>(k0 - row);
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          y[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), CAP ? y[c] : y[c] * p.sp.scale2);
+      }
+      if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + kTile <= r.y)) {
+        const int c0 = r.x - k0;
+        const unsigned width = static_cast<unsigned>(r.y - r.x);
+#pragma unroll
+        for (int c = 0; c < 128; ++c) y[c] = static_cast<unsigned>(c - c0) < width ? y[c] : -INFINITY;
+      }
+      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 128; c += 4) {
+        t0 = fmaxf(t0, y[c]);
+        t1 = fmaxf(t1, y[c + 1]);
+        t2 = fmaxf(t2, y[c + 2]);
+        t3 = fmaxf(t3, y[c + 3]);
+      }
+      float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+      constexpr bool kScaled = CAP || BIAS;  // y is in base 2 already
+      if (!kScaled) top *= p.sp.scale2;
+      const bool grow = top > m + kRescaleAt || (m == -INFINITY && top > -INFINITY);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float m2 = grow ? top : m;
+        const float f = m == -INFINITY ? 0.f : ex2_approx(m - m2);
+        m = m2;
+        l *= f;
+        if (step > 0) {  // the first product overwrites O
+          for (int c = 0; c < p.head_dim; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x32(to + c, o);
+          }
+        }
+      }
+      const float shift = m == -INFINITY ? 0.f : -m;
+      const F2 sc = f2_make(kScaled ? 1.0f : p.sp.scale2, kScaled ? 1.0f : p.sp.scale2), sh = f2_make(shift, shift);
+      F2 sum0 = f2_make(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const F2 v = f2_make(y[h * 64 + 2 * c], y[h * 64 + 2 * c + 1]);
+          const float2 z = f2_split(kScaled ? f2_add(v, sh) : f2_fma(v, sc, sh));
+          const float a = ex2_approx(z.x), b = ex2_approx(z.y);
+          if (c & 1) sum1 = f2_add(sum1, f2_make(a, b));
+          else sum0 = f2_add(sum0, f2_make(a, b));
+          w[c] = pack_bf16x2(a, b);  // P enters its product in bf16: half a step, 2^-9 of each weight
+        }
+        tmem_st_32x32b_x32(ts + h * 32, w);
+      }
+      const float2 su = f2_split(f2_add(sum0, sum1));
+      l += su.x + su.y;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[i]);
+    }
+    if (ok && mine.lo < mine.hi) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, p.status, 0x27));
+      tc_fence_after();
+    }
+    if (ok) {
+      const bool live = l > 0.f;
+      const float inv = live ? 1.0f / l : 0.f;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o.ptr) + (base + row) * p.o.ld + head * p.o.hs;
+      for (int c = 0; c < p.head_dim; c += 32) {
+        uint32_t o[32] = {};
+        if (mine.lo < mine.hi) {
+          tmem_ld_32x32b_x32(to + c, o);
+          tmem_ld_wait();
+        }
+        if (row < p.s) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (c + e >= p.head_dim) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float a = live ? __uint_as_float(o[e + 2 * x]) * inv : 0.f;
+              const float b = live ? __uint_as_float(o[e + 2 * x + 1]) * inv : 0.f;
+              w[x] = pack_bf16x2(a, b);
+            }
+            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (row < p.s) {
+        constexpr float kLn2 = 0.6931471805599453f;
+        p.lse[(static_cast<int64_t>(seq) * p.heads + head) * p.s + row] = live ? kLn2 * (m + log2f(l)) : -INFINITY;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftmaxWarps + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD, bool CAP, bool BIAS>
+cudaError_t launch(const FwdParams& p, int grid, cudaStream_t stream) {
+  auto kernel = masked_attention_forward_kernel<HD, CAP, BIAS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdSmem<HD>::kBytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, FwdSmem<HD>::kBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream_t stream, const DeviceCtx& ctx) {
+  FwdParams p{};
+  const HeadView* views[3] = {&a.q, &a.k, &a.v};
+  HeadMap* maps[3] = {&p.q, &p.k, &p.v};
+  for (int i = 0; i < 3; ++i) {
+    cudaError_t e = make_head_map(maps[i], *views[i], a.b, a.s, i ? a.kv_heads : a.heads, a.head_dim);
+    if (e != cudaSuccess) return e;
+  }
+  p.o = a.o;
+  p.range = a.range;
+  p.slopes = a.slopes;
+  p.lse = a.lse;
+  p.sp = score_params(a.scale, a.softcap);
+  p.s = static_cast<int>(a.s);
+  p.heads = a.heads;
+  p.group = a.heads / a.kv_heads;
+  p.head_dim = a.head_dim;
+  p.nblocks = static_cast<int>((a.s + 2 * kTile - 1) / (2 * kTile));
+  p.bheads = static_cast<int>(a.b) * a.heads;
+  p.status = ctx.status;
+  const int64_t grid = static_cast<int64_t>(p.nblocks) * a.b * a.heads;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const int g = static_cast<int>(grid);
+  const bool wide = a.head_dim > 64, cap = a.softcap > 0.f, bias = a.slopes != nullptr;
+  if (wide)
+    return cap ? (bias ? launch<128, true, true>(p, g, stream) : launch<128, true, false>(p, g, stream))
+               : (bias ? launch<128, false, true>(p, g, stream) : launch<128, false, false>(p, g, stream));
+  return cap ? (bias ? launch<64, true, true>(p, g, stream) : launch<64, true, false>(p, g, stream))
+             : (bias ? launch<64, false, true>(p, g, stream) : launch<64, false, false>(p, g, stream));
+}
+
+}  // namespace tpmlp

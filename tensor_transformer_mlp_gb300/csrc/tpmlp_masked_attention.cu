@@ -141,6 +141,7 @@ tpmlp_status check_shape(float scale, float softcap, int64_t b, int64_t s, int h
   if (b < 0 || s < 0 || heads < 1 || kv_heads < 1)
     return err(TPMLP_ERR_SHAPE, "need b, s >= 0 and heads, kv_heads >= 1");
   if (b > 0 && s > INT32_MAX / b) return err(TPMLP_ERR_SHAPE, "b * s exceeds 2^31-1");
+  if (s > (1 << 30)) return err(TPMLP_ERR_SHAPE, "s must be <= 2^30");
   if (b > 65535 || heads > 65535) return err(TPMLP_ERR_SHAPE, "at most 65535 sequences and heads");
   if (heads % kv_heads != 0) return err(TPMLP_ERR_SHAPE, "heads must be a multiple of kv_heads");
   if (hd < 8 || hd % 8 != 0 || hd > 128)
