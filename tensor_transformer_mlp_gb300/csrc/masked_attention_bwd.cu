@@ -1,158 +1,706 @@
-// Masked attention, forward and backward, on CUDA cores: one warp per query row (forward, dQ) or per key
-// row (dK, dV), 32 keys or queries at a time.
+// Masked attention, backward, on the tensor cores, in two passes without atomics:
 //
-//   y_ij = c(scale q_i.k_j) - slope |i - j|,  lse_i = log sum_j exp(y_ij),  P_ij = exp(y_ij - lse_i)
-//   o_i = sum_j P_ij v_j;  D_i = d_o_i.o_i,  dX_ij = scale c' P_ij (d_o_i.v_j - D_i)
-//   dQ_i = sum_j dX_ij k_j,  dK_j = sum_i dX_ij q_i,  dV_j = sum_i P_ij d_o_i
+//   query pass: per tile of 128 queries, over its key tiles:    dQ_i = sum_j dX_ij k_j
+//   key pass:   per tile of 128 keys, over the query tiles that see it and the query heads that share it:
+//               dV_j = sum_i P_ij d_o_i,  dK_j = sum_i dX_ij q_i
+// with P_ij = exp(y_ij - lse_i) and dX_ij = scale c' P_ij (d_o_i.v_j - D_i) formed again in each (seven products of
+// 128 x 128 x head_dim per pair of tiles instead of five). Joining the passes would need dQ summed over key tiles
+// across CTAs: fp32 atomics on dQ, in an order that changes from run to run, and a buffer and a pass to round it.
+//
+// Both passes keep the scores and the gradients of the probabilities in tensor memory, turn them into P and dX there
+// (bf16, over the columns of the accumulator that they came from), and feed them to the products from there; shared
+// memory only ever holds tiles as they lie in global memory. Warp roles in both:
+//   warps 0-7   one row of the accumulators per thread, columns 0-63 (warps 0-3) or 64-127 (warps 4-7)
+//   warp 8      tensor copies of the tiles through two rings
+//   warp 9      one thread issues the products
+//   warp 10     (key pass) the queries' lse and D, two tiles ahead
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "device_common.cuh"
+#include "attention_tiles.cuh"
 
 namespace tpmlp {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kCols = 128 / 32;  // columns of a head per lane
+constexpr int kWorkWarps = 8;
+constexpr int kThreads = (kWorkWarps + 4) * 32;
+constexpr int kRegsWork = 208, kRegsIssue = 88;  // 2 * 208 + 88 = 3 * 168, the registers at launch
 
-using bf16 = __nv_bfloat16;
+// Summary of a tile of 128 queries: the keys that some row sees lie in [lo, hi), and every row of the tile sees the
+// keys of [all_lo, all_hi).
+struct TileRange {
+  int lo, hi, all_lo, all_hi;
+};
 
-__device__ __forceinline__ const bf16* row_of(const HeadView& v, int64_t token, int head) {
-  return static_cast<const bf16*>(v.ptr) + token * v.ld + head * v.hs;
-}
+struct BwdParams {
+  HeadMap q, k, v, d_o;       // tiles to load
+  HeadView o, g;              // o and d_o, read by rows for D
+  HeadView dq, dk, dv;
+  const int2* range;
+  const float* slopes;
+  const float* lse;           // [b][heads][s]
+  float* dsum;                // [b][heads][s]: D, written by the query pass, read by the key pass
+  TileRange* tiles;           // [b][ntiles], likewise
+  ScoreParams sp;
+  float scale;
+  int s, heads, kv_heads, group, head_dim, ntiles, nseq;
+  unsigned int* status;
+};
 
-__device__ __forceinline__ float dot(const bf16* a, const bf16* b, int hd) {
-  float acc = 0.f;
-  for (int c = 0; c < hd; c += 8) {
-    const uint4 x = *reinterpret_cast<const uint4*>(a + c), y = *reinterpret_cast<const uint4*>(b + c);
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+template <int HD>
+struct BwdSmem {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  // Ring depths. "held" tiles (K of the query pass, Q of the key pass) serve the scores of one step and the product
+  // of a later one, "passing" tiles (V, d_o) two products in a row.
+  static constexpr int kHeld = HD == 128 ? 3 : 4;
+  static constexpr int kPassing = HD == 128 ? 2 : 4;
+  static constexpr int kStatBytes = 2 * 2 * kTile * 4;
+  static constexpr int kTiles = 2 + kHeld + kPassing;
+  static constexpr int kBarrierBytes = 256;
+  static constexpr int kBytes = kTiles * kTileBytes + kStatBytes + kBarrierBytes;  // 231,680 of 232,448 at HD = 128
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+};
+
+// The A operand of K-step kk: bf16 values of columns 16 kk .. 16 kk + 15, in the half of the accumulator that they
+// came from (each warp writes over columns that only it has read).
+__device__ __forceinline__ uint32_t packed_cols(uint32_t acc, int kk) { return acc + (kk >> 2) * 64 + (kk & 3) * 8; }
+
+// ------------------------------------------------------------------ query pass
+
+template <int HD, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const __grid_constant__ BwdParams p) {
+  using L = BwdSmem<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sq = smem;
+  uint8_t* sg = sq + L::kTileBytes;
+  uint8_t* k_ring = sg + L::kTileBytes;
+  uint8_t* v_ring = k_ring + L::kHeld * L::kTileBytes;
+  float* part = reinterpret_cast<float*>(v_ring + L::kPassing * L::kTileBytes);  // [8 warps][32] halves of D, then spans
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(part + L::kStatBytes / 4);
+  uint64_t* s_full = q_full + 1;
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* acc_full = ds_full + 1;
+  uint64_t* k_full = acc_full + 1;
+  uint64_t* k_empty = k_full + L::kHeld;
+  uint64_t* v_full = k_empty + L::kHeld;
+  uint64_t* v_empty = v_full + L::kPassing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + L::kPassing);
+  int4* warp_span = reinterpret_cast<int4*>(part + 8 * 32);
+  static_assert((6 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 4 <= L::kBarrierBytes, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bheads = p.heads * p.nseq;
+  const int tile = p.ntiles - 1 - static_cast<int>(blockIdx.x) / bheads;  // under a causal mask the longest first
+  const int bh = static_cast<int>(blockIdx.x) % bheads;
+  const int seq = bh / p.heads, head = bh - seq * p.heads, kvh = head / p.group;
+  const int q0 = tile * kTile;
+  const int64_t base = static_cast<int64_t>(seq) * p.s;
+  const int row = q0 + (warp & 3) * 32 + lane;
+  const int half = (warp >> 2) & 1;
+  const int64_t stat_at = (static_cast<int64_t>(seq) * p.heads + head) * p.s;
+
+  int2 r = make_int2(0, 0);
+  float lse2 = 0.f;
+  if (warp < kWorkWarps) {
+    const bool in = row < p.s;
+    if (in) r = clip_range(p.range[base + row], p.s);
+    const bool live = r.x < r.y;
+    const int lo = __reduce_min_sync(0xffffffffu, live ? r.x : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, r.y);
+    const int all_lo = __reduce_max_sync(0xffffffffu, live ? r.x : INT32_MAX);
+    const int all_hi = __reduce_min_sync(0xffffffffu, r.y);
+    if (lane == 0) warp_span[warp] = make_int4(lo, hi, all_lo, all_hi);
+    // D = d_o . o of the row, half of the head's columns per warpgroup
+    float d = 0.f;
+    if (live) {
+      lse2 = p.lse[stat_at + row] * kLog2e;
+      const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o.ptr) + (base + row) * p.o.ld + head * p.o.hs;
+      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.g.ptr) + (base + row) * p.g.ld + head * p.g.hs;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 u = unpack_bf16x2(xw[i]), w = unpack_bf16x2(yw[i]);
-      acc = fmaf(u.x, w.x, acc);
-      acc = fmaf(u.y, w.y, acc);
-    }
-  }
-  return acc;
-}
-
-// y_ij, and the cap's derivative
-__device__ __forceinline__ float score(const MaskedAttention& a, float qk, int head, int64_t i, int64_t j, float* dcap) {
-  float y = qk * a.scale;
-  *dcap = 1.f;
-  if (a.softcap > 0.f) {
-    const float t = tanhf(y / a.softcap);
-    y = a.softcap * t;
-    *dcap = 1.f - t * t;
-  }
-  if (a.slopes) y -= a.slopes[head] * fabsf(static_cast<float>(i - j));
-  return y;
-}
-
-__device__ __forceinline__ int2 clipped(const MaskedAttention& a, int64_t token) {
-  int2 r = a.range[token];
-  r.x = max(r.x, 0);
-  r.y = min(static_cast<int64_t>(r.y), a.s);
-  return r.x < r.y ? r : make_int2(0, 0);
-}
-
-__global__ void __launch_bounds__(kWarps * 32) dq_rows_kernel(const MaskedAttention a, const HeadView d_o,
-                                                              const HeadView dq, float* dsum) {
-  const int lane = threadIdx.x & 31, hd = a.head_dim;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int head = blockIdx.y, kvh = head / (a.heads / a.kv_heads);
-  if (i >= a.s) return;
-  const int64_t base = blockIdx.z * a.s, token = base + i;
-  const int64_t at = (blockIdx.z * static_cast<int64_t>(a.heads) + head) * a.s + i;
-  const int2 r = clipped(a, token);
-  const bf16 *q = row_of(a.q, token, head), *g = row_of(d_o, token, head);
-  const float D = dot(g, row_of(a.o, token, head), hd), lse = a.lse[at];
-  if (lane == 0) dsum[at] = D;
-  float acc[kCols] = {};
-  for (int j0 = r.x; j0 < r.y; j0 += 32) {
-    const int j = j0 + lane;
-    float dx = 0.f, dcap;
-    if (j < r.y) {
-      const float y = score(a, dot(q, row_of(a.k, base + j, kvh), hd), head, i, j, &dcap);
-      dx = expf(y - lse) * (dot(g, row_of(a.v, base + j, kvh), hd) - D) * dcap * a.scale;
-    }
-    for (int e = 0; e < min(32, r.y - j0); ++e) {
-      const float de = __shfl_sync(0xffffffffu, dx, e);
-      const bf16* k = row_of(a.k, base + j0 + e, kvh);
+      for (int c = 0; c < HD / 2; c += 8) {
+        const int col = half * (HD / 2) + c;
+        if (col < p.head_dim) {
+          const uint4 x = *reinterpret_cast<const uint4*>(o + col), y = *reinterpret_cast<const uint4*>(g + col);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        if (lane + 32 * c < hd) acc[c] = fmaf(de, __bfloat162float(k[lane + 32 * c]), acc[c]);
-    }
-  }
-  bf16* out = const_cast<bf16*>(row_of(dq, token, head));
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    if (lane + 32 * c < hd) out[lane + 32 * c] = __float2bfloat16(acc[c]);
-}
-
-__global__ void __launch_bounds__(kWarps * 32) dkv_rows_kernel(const MaskedAttention a, const HeadView d_o,
-                                                               const HeadView dk, const HeadView dv, const float* dsum) {
-  const int lane = threadIdx.x & 31, hd = a.head_dim, group = a.heads / a.kv_heads;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int kvh = blockIdx.y;
-  if (j >= a.s) return;
-  const int64_t base = blockIdx.z * a.s, token = base + j;
-  const bf16 *k = row_of(a.k, token, kvh), *v = row_of(a.v, token, kvh);
-  float acck[kCols] = {}, accv[kCols] = {};
-  for (int head = kvh * group; head < (kvh + 1) * group; ++head) {
-    const int64_t at = (blockIdx.z * static_cast<int64_t>(a.heads) + head) * a.s;
-    for (int64_t i0 = 0; i0 < a.s; i0 += 32) {
-      const int64_t i = i0 + lane;
-      bool sees = false;
-      if (i < a.s) {
-        const int2 r = clipped(a, base + i);
-        sees = r.x <= j && j < r.y;
-      }
-      unsigned left = __ballot_sync(0xffffffffu, sees);
-      if (!left) continue;
-      float p = 0.f, dx = 0.f, dcap;
-      if (sees) {
-        const bf16* g = row_of(d_o, base + i, head);
-        p = expf(score(a, dot(row_of(a.q, base + i, head), k, hd), head, i, j, &dcap) - a.lse[at + i]);
-        dx = p * (dot(g, v, hd) - dsum[at + i]) * dcap * a.scale;
-      }
-      for (; left; left &= left - 1) {
-        const int e = __ffs(left) - 1;
-        const float pe = __shfl_sync(0xffffffffu, p, e), de = __shfl_sync(0xffffffffu, dx, e);
-        const bf16 *q = row_of(a.q, base + i0 + e, head), *g = row_of(d_o, base + i0 + e, head);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (lane + 32 * c < hd) {
-            acck[c] = fmaf(de, __bfloat162float(q[lane + 32 * c]), acck[c]);
-            accv[c] = fmaf(pe, __bfloat162float(g[lane + 32 * c]), accv[c]);
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = unpack_bf16x2(xw[e]), b = unpack_bf16x2(yw[e]);
+            d = fmaf(a.x, b.x, d);
+            d = fmaf(a.y, b.y, d);
           }
+        }
+      }
+    }
+    part[warp * 32 + lane] = d;
+  } else if (warp == kWorkWarps) {
+    if (lane == 0) {
+      for (uint64_t* b = q_full; b < v_empty + L::kPassing; ++b) mbar_init(b, b == ds_full ? kWorkWarps : 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&p.q.map);
+      tma_prefetch_desc(&p.k.map);
+      tma_prefetch_desc(&p.v.map);
+      tma_prefetch_desc(&p.d_o.map);
+    }
+  } else if (warp == kWorkWarps + 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
+  TileRange t{INT32_MAX, 0, 0, INT32_MAX};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int4 v = warp_span[w];
+    t = TileRange{min(t.lo, v.x), max(t.hi, v.y), max(t.all_lo, v.z), min(t.all_hi, v.w)};
+  }
+  const bool any = t.hi > 0;
+  const int j0 = any ? t.lo / kTile : 0, steps = any ? (t.hi + kTile - 1) / kTile - j0 : 0;
+  if (head == 0 && threadIdx.x == 0) p.tiles[static_cast<int64_t>(seq) * p.ntiles + tile] = t;
+
+  if (warp >= kWorkWarps) {
+    regs_dec<kRegsIssue>();
+    if (warp == kWorkWarps && lane == 0 && steps > 0) {
+      // ---------------------------------------------------------------- loads
+      mbar_arrive_expect_tx(q_full, 2 * L::kTileBytes);
+      load_head_tile(sq, p.q, q_full, L::kBoxes, q0, head, seq);
+      load_head_tile(sg, p.d_o, q_full, L::kBoxes, q0, head, seq);
+      int n = 0;
+      bool ok = true;
+      for (; n < steps; ++n) {
+        const int ks = n % L::kHeld, vs = n % L::kPassing;
+        ok = mbar_wait(&k_empty[ks], ((n / L::kHeld) & 1) ^ 1, p.status, 0x30);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&k_full[ks], L::kTileBytes);
+        load_head_tile(k_ring + ks * L::kTileBytes, p.k, &k_full[ks], L::kBoxes, (j0 + n) * kTile, kvh, seq);
+        ok = mbar_wait(&v_empty[vs], ((n / L::kPassing) & 1) ^ 1, p.status, 0x31);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&v_full[vs], L::kTileBytes);
+        load_head_tile(v_ring + vs * L::kTileBytes, p.v, &v_full[vs], L::kBoxes, (j0 + n) * kTile, kvh, seq);
+      }
+      if (!ok) {  // the copies in flight must land before shared memory goes away
+        mbar_wait(q_full, 0, p.status, 0x32);
+        for (int k = max(0, n + 1 - L::kHeld); k <= n; ++k) mbar_wait(&k_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x32);
+        for (int k = max(0, n - L::kPassing); k < n; ++k) mbar_wait(&v_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x32);
+      }
+    } else if (warp == kWorkWarps + 1 && lane == 0 && steps > 0) {
+      // ---------------------------------------------------------------- products
+      const int ksteps = (p.head_dim + 15) / 16;
+      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
+      const uint32_t idesc_q = idesc_bf16_f32(kTile, ksteps * 16, false, true);
+      const uint32_t q_addr = smem_u32(sq), g_addr = smem_u32(sg), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
+      bool ok = mbar_wait(q_full, 0, p.status, 0x33);
+      auto scores = [&](int n) {  // S(n) = Q K(n)^T
+        if (ok) ok = mbar_wait(&k_full[n % L::kHeld], (n / L::kHeld) & 1, p.status, 0x34);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t kt = k_addr + (n % L::kHeld) * L::kTileBytes;
+        for (int kk = 0; kk < ksteps; ++kk)
+          umma_bf16(tmem + (n & 1) * 128, desc_rows(q_addr, kk), desc_rows(kt, kk), idesc_s, kk != 0);
+        umma_commit(&s_full[n & 1]);
+      };
+      auto dprobs = [&](int n) {  // dP(n) = d_o V(n)^T
+        if (ok) ok = mbar_wait(&v_full[n % L::kPassing], (n / L::kPassing) & 1, p.status, 0x35);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t vt = v_addr + (n % L::kPassing) * L::kTileBytes;
+        for (int kk = 0; kk < ksteps; ++kk) umma_bf16(t_dp, desc_rows(g_addr, kk), desc_rows(vt, kk), idesc_s, kk != 0);
+        umma_commit(dp_full);
+        umma_commit(&v_empty[n % L::kPassing]);
+      };
+      scores(0);
+      dprobs(0);
+      if (steps > 1) scores(1);
+      for (int n = 0; n < steps && ok; ++n) {
+        ok = mbar_wait(ds_full, n & 1, p.status, 0x36);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t kt = k_addr + (n % L::kHeld) * L::kTileBytes;
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_bf16_ta(t_dq, packed_cols(t_dp, kk), desc_cols(kt, kk), idesc_q, (n | kk) != 0);
+        umma_commit(&k_empty[n % L::kHeld]);
+        if (n + 1 < steps) dprobs(n + 1);
+        if (n + 2 < steps) scores(n + 2);
+      }
+      umma_commit(acc_full);  // also: every product issued is done before tensor memory is freed
+      mbar_wait(acc_full, 0, p.status, 0x37);
+    }
+  } else {
+    // ------------------------------------------------------------------ P, dX
+    regs_inc<kRegsWork>();
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float D = part[(warp & 3) * 32 + lane] + part[((warp & 3) + 4) * 32 + lane];
+    if (half == 0 && row < p.s) p.dsum[stat_at + row] = D;
+    const float slope2 = BIAS ? p.slopes[head] * kLog2e : 0.f;
+    bool ok = true;
+    for (int n = 0; n < steps; ++n) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (n >> 1) & 1, p.status, 0x38));
+      if (!ok) break;
+      tc_fence_after();
+      const int k0 = (j0 + n) * kTile + half * 64;
+      float w[64];  // P, times the cap's derivative
+      const uint32_t ts = tmem + lanes + (n & 1) * 128 + half * 64;
+      tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
+      tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
+      tmem_ld_wait();
+      const float d0 = static_cast<float>(k0 - row);
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        const float sg2 = CAP ? cap_sigma(w[c], p.sp) : 0.f;
+        float y = CAP ? fmaf(-2.0f * p.sp.cap2, sg2, p.sp.cap2) - lse2 : fmaf(w[c], p.sp.scale2, -lse2);
+        if (BIAS) y = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), y);
+        w[c] = ex2_approx(y);
+        if (CAP) w[c] *= 4.0f * sg2 * (1.0f - sg2);
+      }
+      if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + 64 <= r.y)) {
+        const int c0 = r.x - k0;
+        const unsigned width = static_cast<unsigned>(r.y - r.x);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) w[c] = static_cast<unsigned>(c - c0) < width ? w[c] : 0.f;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, n & 1, p.status, 0x39));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dp[64], x[32];
+      const uint32_t td = t_dp + lanes + half * 64;
+      tmem_ld_32x32b_x32(td, *reinterpret_cast<uint32_t(*)[32]>(dp));
+      tmem_ld_32x32b_x32(td + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+      tmem_ld_wait();
+      const F2 d2 = f2_make(D, D);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const F2 g2 = f2_sub(f2_make(__uint_as_float(dp[2 * c]), __uint_as_float(dp[2 * c + 1])), d2);
+        const float2 z = f2_split(f2_mul(f2_make(w[2 * c], w[2 * c + 1]), g2));
+        x[c] = pack_bf16x2(z.x, z.y);  // dX / scale enters its product in bf16: half a step of each term
+      }
+      tmem_st_32x32b_x32(td, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (ok && steps > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.status, 0x3A));
+      tc_fence_after();
+    }
+    if (ok) {
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dq.ptr) + (base + row) * p.dq.ld + head * p.dq.hs;
+      for (int c = half * (HD / 2); c < (half + 1) * (HD / 2) && c < p.head_dim; c += 32) {
+        uint32_t v[32] = {};
+        if (steps > 0) {
+          tmem_ld_32x32b_x32(t_dq + lanes + c, v);
+          tmem_ld_wait();
+        }
+        if (row < p.s) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (c + e >= p.head_dim) break;
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              u[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * p.scale, __uint_as_float(v[e + 2 * i + 1]) * p.scale);
+            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
       }
     }
   }
-  bf16 *ok = const_cast<bf16*>(row_of(dk, token, kvh)), *ov = const_cast<bf16*>(row_of(dv, token, kvh));
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    if (lane + 32 * c < hd) {
-      ok[lane + 32 * c] = __float2bfloat16(acck[c]);
-      ov[lane + 32 * c] = __float2bfloat16(accv[c]);
-    }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWorkWarps + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-dim3 rows_grid(const MaskedAttention& a, int heads) {
-  return dim3(static_cast<unsigned>((a.s + kWarps - 1) / kWarps), static_cast<unsigned>(heads),
-              static_cast<unsigned>(a.b));
+// ------------------------------------------------------------------ key pass
+
+// Walks the query tiles that see some key of [k0, k1), for each query head of a group in turn; a whole warp calls it.
+struct QueryTiles {
+  const TileRange* tiles;
+  int ntiles, k0, k1, heads_left, base;
+  unsigned found;
+  int head, tile;
+  bool full;  // every row of the tile sees every key
+  __device__ __forceinline__ QueryTiles(const TileRange* t, int n, int k0_, int k1_, int first_head, int heads)
+      : tiles(t), ntiles(n), k0(k0_), k1(k1_), heads_left(heads), base(-32), found(0), head(first_head), tile(0), full(false) {}
+  __device__ __forceinline__ bool next() {
+    const int lane = threadIdx.x & 31;
+    while (!found) {
+      base += 32;
+      if (base >= ntiles) {
+        base = -32;
+        ++head;
+        if (--heads_left <= 0) return false;
+        continue;
+      }
+      bool on = false;
+      if (base + lane < ntiles) {
+        const TileRange t = tiles[base + lane];
+        on = t.lo < k1 && t.hi > k0;
+      }
+      found = __ballot_sync(0xffffffffu, on);
+    }
+    tile = base + __ffs(found) - 1;
+    found &= found - 1;
+    const TileRange t = tiles[tile];
+    full = t.all_lo <= k0 && t.all_hi >= k1;
+    return true;
+  }
+};
+
+template <int HD, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const __grid_constant__ BwdParams p) {
+  using L = BwdSmem<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sk = smem;
+  uint8_t* sv = sk + L::kTileBytes;
+  uint8_t* q_ring = sv + L::kTileBytes;
+  uint8_t* g_ring = q_ring + L::kHeld * L::kTileBytes;
+  float* stats = reinterpret_cast<float*>(g_ring + L::kPassing * L::kTileBytes);  // two of {lse2[128], D[128]}
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + L::kStatBytes / 4);
+  uint64_t* s_full = kv_full + 1;
+  uint64_t* p_full = s_full + 1;
+  uint64_t* dp_full = p_full + 1;
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* acc_full = ds_full + 1;
+  uint64_t* st_full = acc_full + 1;
+  uint64_t* st_empty = st_full + 2;
+  uint64_t* q_full = st_empty + 2;
+  uint64_t* q_empty = q_full + L::kHeld;
+  uint64_t* g_full = q_empty + L::kHeld;
+  uint64_t* g_empty = g_full + L::kPassing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g_empty + L::kPassing);
+  static_assert((10 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 4 <= L::kBarrierBytes, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bheads = p.kv_heads * p.nseq;
+  const int tile = static_cast<int>(blockIdx.x) / bheads;  // under a causal mask the first keys have the most queries
+  const int bh = static_cast<int>(blockIdx.x) % bheads;
+  const int seq = bh / p.kv_heads, kvh = bh - seq * p.kv_heads;
+  const int k0 = tile * kTile;
+  const int64_t base = static_cast<int64_t>(seq) * p.s;
+  QueryTiles it(p.tiles + static_cast<int64_t>(seq) * p.ntiles, p.ntiles, k0, min(k0 + kTile, p.s), kvh * p.group, p.group);
+
+  if (warp == kWorkWarps) {
+    if (lane == 0) {
+      for (uint64_t* b = kv_full; b < g_empty + L::kPassing; ++b)
+        mbar_init(b, b == p_full || b == ds_full || b == st_empty || b == st_empty + 1 ? kWorkWarps : 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&p.q.map);
+      tma_prefetch_desc(&p.k.map);
+      tma_prefetch_desc(&p.v.map);
+      tma_prefetch_desc(&p.d_o.map);
+    }
+  } else if (warp == kWorkWarps + 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+
+  if (warp >= kWorkWarps) {
+    regs_dec<kRegsIssue>();
+    if (warp == kWorkWarps) {
+      // ---------------------------------------------------------------- loads
+      bool ok = true, more = it.next();
+      if (more && lane == 0) {
+        mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
+        load_head_tile(sk, p.k, kv_full, L::kBoxes, k0, kvh, seq);
+        load_head_tile(sv, p.v, kv_full, L::kBoxes, k0, kvh, seq);
+      }
+      const bool any = more;
+      int n = 0;
+      for (; more; more = it.next(), ++n) {
+        const int qs = n % L::kHeld, gs = n % L::kPassing;
+        ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[qs], ((n / L::kHeld) & 1) ^ 1, p.status, 0x40));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[qs], L::kTileBytes);
+          load_head_tile(q_ring + qs * L::kTileBytes, p.q, &q_full[qs], L::kBoxes, it.tile * kTile, it.head, seq);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&g_empty[gs], ((n / L::kPassing) & 1) ^ 1, p.status, 0x41));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&g_full[gs], L::kTileBytes);
+          load_head_tile(g_ring + gs * L::kTileBytes, p.d_o, &g_full[gs], L::kBoxes, it.tile * kTile, it.head, seq);
+        }
+      }
+      if (!ok && any) {  // the copies in flight must land before shared memory goes away
+        mbar_wait(kv_full, 0, p.status, 0x42);
+        for (int k = max(0, n - L::kHeld); k < n; ++k) mbar_wait(&q_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x42);
+        mbar_wait(&q_full[n % L::kHeld], (n / L::kHeld) & 1, p.status, 0x42);
+        for (int k = max(0, n - L::kPassing); k < n; ++k) mbar_wait(&g_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x42);
+      }
+    } else if (warp == kWorkWarps + 1) {
+      // ---------------------------------------------------------------- products
+      const int ksteps = (p.head_dim + 15) / 16;
+      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
+      const uint32_t idesc_d = idesc_bf16_f32(kTile, ksteps * 16, false, true);
+      const uint32_t k_addr = smem_u32(sk), v_addr = smem_u32(sv), q_addr = smem_u32(q_ring), g_addr = smem_u32(g_ring);
+      auto agreed = [&](bool got) { return __all_sync(0xffffffffu, got); };
+      bool more = it.next(), ok = true;
+      const bool any = more;
+      auto scores = [&](int n) {  // S(n)^T = K Q(n)^T
+        if (ok) ok = agreed(mbar_wait(&q_full[n % L::kHeld], (n / L::kHeld) & 1, p.status, 0x43));
+        tc_fence_after();
+        if (ok && lane == 0) {
+          const uint32_t qt = q_addr + (n % L::kHeld) * L::kTileBytes;
+          for (int kk = 0; kk < ksteps; ++kk) umma_bf16(tmem, desc_rows(k_addr, kk), desc_rows(qt, kk), idesc_s, kk != 0);
+          umma_commit(s_full);
+        }
+      };
+      auto dprobs = [&](int n) {  // dP(n)^T = V d_o(n)^T
+        if (ok) ok = agreed(mbar_wait(&g_full[n % L::kPassing], (n / L::kPassing) & 1, p.status, 0x44));
+        tc_fence_after();
+        if (ok && lane == 0) {
+          const uint32_t gt = g_addr + (n % L::kPassing) * L::kTileBytes;
+          for (int kk = 0; kk < ksteps; ++kk) umma_bf16(t_dp, desc_rows(v_addr, kk), desc_rows(gt, kk), idesc_s, kk != 0);
+          umma_commit(dp_full);
+        }
+      };
+      if (more) {
+        ok = agreed(mbar_wait(kv_full, 0, p.status, 0x45));
+        scores(0);
+        dprobs(0);
+      }
+      for (int n = 0; more && ok; ++n) {
+        more = it.next();
+        ok = agreed(mbar_wait(p_full, n & 1, p.status, 0x46));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t gt = g_addr + (n % L::kPassing) * L::kTileBytes;
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_bf16_ta(t_dv, packed_cols(tmem, kk), desc_cols(gt, kk), idesc_d, (n | kk) != 0);
+          umma_commit(&g_empty[n % L::kPassing]);
+        }
+        if (more) scores(n + 1);
+        if (ok) ok = agreed(mbar_wait(ds_full, n & 1, p.status, 0x47));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t qt = q_addr + (n % L::kHeld) * L::kTileBytes;
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_bf16_ta(t_dk, packed_cols(t_dp, kk), desc_cols(qt, kk), idesc_d, (n | kk) != 0);
+          umma_commit(&q_empty[n % L::kHeld]);
+        }
+        if (more) dprobs(n + 1);
+      }
+      if (any) {  // also: every product issued is done before tensor memory is freed
+        if (lane == 0) umma_commit(acc_full);
+        __syncwarp();
+        mbar_wait(acc_full, 0, p.status, 0x48);
+      }
+    } else if (warp == kWorkWarps + 2) {
+      // ---------------------------------------------------------------- lse and D of the queries
+      for (int n = 0; it.next(); ++n) {
+        const int q = it.tile * kTile + lane * 4;
+        const int64_t at = (static_cast<int64_t>(seq) * p.heads + it.head) * p.s + q;
+        float l[4], d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          l[e] = q + e < p.s ? p.lse[at + e] * kLog2e : 0.f;
+          d[e] = q + e < p.s ? p.dsum[at + e] : 0.f;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&st_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status, 0x49))) break;
+        float* st = stats + (n & 1) * 2 * kTile;
+        reinterpret_cast<float4*>(st)[lane] = make_float4(l[0], l[1], l[2], l[3]);
+        reinterpret_cast<float4*>(st + kTile)[lane] = make_float4(d[0], d[1], d[2], d[3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_full[n & 1]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ P, dX
+    regs_inc<kRegsWork>();
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int half = warp >> 2;
+    const int key = k0 + (warp & 3) * 32 + lane;
+    bool ok = true;
+    int n = 0;
+    for (; it.next(); ++n) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&st_full[n & 1], (n >> 1) & 1, p.status, 0x4A));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, n & 1, p.status, 0x4B));
+      if (!ok) break;
+      tc_fence_after();
+      const float4* lse2 = reinterpret_cast<const float4*>(stats + (n & 1) * 2 * kTile + half * 64);
+      const float4* dd = reinterpret_cast<const float4*>(stats + (n & 1) * 2 * kTile + kTile + half * 64);
+      const int q0 = it.tile * kTile + half * 64;
+      const float slope2 = BIAS ? p.slopes[it.head] * kLog2e : 0.f;
+      const uint32_t ts = tmem + lanes + half * 64, td = t_dp + lanes + half * 64;
+      float w[64];
+      tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
+      tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
+      tmem_ld_wait();
+      unsigned long long seen = ~0ull;  // which of the 64 queries see this key
+      if (!it.full) {
+        seen = 0;
+#pragma unroll 16
+        for (int c = 0; c < 64; ++c) {
+          const int2 r = q0 + c < p.s ? p.range[base + q0 + c] : make_int2(0, 0);
+          seen |= static_cast<unsigned long long>(r.x <= key && key < r.y) << c;
+        }
+      }
+      const float d0 = static_cast<float>(q0 - key);
+      uint32_t x[32];
+#pragma unroll
+      for (int c4 = 0; c4 < 16; ++c4) {
+        const float4 l4 = lse2[c4];
+        const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = c4 * 4 + e;
+          const float sg2 = CAP ? cap_sigma(w[c], p.sp) : 0.f;
+          float y = CAP ? fmaf(-2.0f * p.sp.cap2, sg2, p.sp.cap2) - l[e] : fmaf(w[c], p.sp.scale2, -l[e]);
+          if (BIAS) y = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), y);
+          pr[e] = (seen >> c) & 1 ? ex2_approx(y) : 0.f;
+          w[c] = CAP ? pr[e] * (4.0f * sg2 * (1.0f - sg2)) : pr[e];
+        }
+        x[2 * c4] = pack_bf16x2(pr[0], pr[1]);
+        x[2 * c4 + 1] = pack_bf16x2(pr[2], pr[3]);
+      }
+      tmem_st_32x32b_x32(ts, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+
+      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, n & 1, p.status, 0x4C));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dp[64];
+      tmem_ld_32x32b_x32(td, *reinterpret_cast<uint32_t(*)[32]>(dp));
+      tmem_ld_32x32b_x32(td + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+      tmem_ld_wait();
+#pragma unroll
+      for (int c4 = 0; c4 < 16; ++c4) {
+        const float4 d4 = dd[c4];
+        const F2 a = f2_sub(f2_make(__uint_as_float(dp[4 * c4]), __uint_as_float(dp[4 * c4 + 1])), f2_make(d4.x, d4.y));
+        const F2 b = f2_sub(f2_make(__uint_as_float(dp[4 * c4 + 2]), __uint_as_float(dp[4 * c4 + 3])), f2_make(d4.z, d4.w));
+        const float2 za = f2_split(f2_mul(f2_make(w[4 * c4], w[4 * c4 + 1]), a));
+        const float2 zb = f2_split(f2_mul(f2_make(w[4 * c4 + 2], w[4 * c4 + 3]), b));
+        x[2 * c4] = pack_bf16x2(za.x, za.y);
+        x[2 * c4 + 1] = pack_bf16x2(zb.x, zb.y);
+      }
+      tmem_st_32x32b_x32(td, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ds_full);
+        mbar_arrive(&st_empty[n & 1]);
+      }
+    }
+    if (ok && n > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.status, 0x4D));
+      tc_fence_after();
+    }
+    if (ok) {
+      // warps 0-3 write dV, warps 4-7 dK, a key's row per thread
+      const HeadView& view = half ? p.dk : p.dv;
+      const float f = half ? p.scale : 1.0f;
+      const uint32_t acc = (half ? t_dk : t_dv) + lanes;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(view.ptr) + (base + key) * view.ld + kvh * view.hs;
+      for (int c = 0; c < p.head_dim; c += 32) {
+        uint32_t v[32] = {};
+        if (n > 0) {
+          tmem_ld_32x32b_x32(acc + c, v);
+          tmem_ld_wait();
+        }
+        if (key < p.s) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (c + e >= p.head_dim) break;
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              u[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * f, __uint_as_float(v[e + 2 * i + 1]) * f);
+            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWorkWarps + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD, bool CAP, bool BIAS>
+cudaError_t launch(const BwdParams& p, cudaStream_t stream) {
+  auto dq = masked_attention_dq_kernel<HD, CAP, BIAS>;
+  auto dkv = masked_attention_dkv_kernel<HD, CAP, BIAS>;
+  const int64_t q_grid = static_cast<int64_t>(p.ntiles) * p.nseq * p.heads, k_grid = q_grid / p.group;
+  if (q_grid > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD>::kBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD>::kBytes);
+  if (e != cudaSuccess) return e;
+  dq<<<static_cast<int>(q_grid), kThreads, BwdSmem<HD>::kBytes, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  dkv<<<static_cast<int>(k_grid), kThreads, BwdSmem<HD>::kBytes, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
+size_t masked_attention_backward_workspace(int64_t b, int64_t s, int heads) {
+  const size_t d = static_cast<size_t>(b) * static_cast<size_t>(s) * static_cast<size_t>(heads) * sizeof(float);
+  const size_t t = static_cast<size_t>(b) * static_cast<size_t>((s + kTile - 1) / kTile) * sizeof(TileRange);
+  return (d + 255) / 256 * 256 + (t + 255) / 256 * 256;
+}
+
 cudaError_t launch_masked_attention_backward(const MaskedAttention& a, const HeadView& d_o, const HeadView& dq,
-                                             const HeadView& dk, const HeadView& dv, float* dsum, cudaStream_t stream,
-                                             const DeviceCtx&) {
-  dq_rows_kernel<<<rows_grid(a, a.heads), kWarps * 32, 0, stream>>>(a, d_o, dq, dsum);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  dkv_rows_kernel<<<rows_grid(a, a.kv_heads), kWarps * 32, 0, stream>>>(a, d_o, dk, dv, dsum);
-  return cudaGetLastError();
+                                             const HeadView& dk, const HeadView& dv, void* workspace, cudaStream_t stream,
+                                             const DeviceCtx& ctx) {
+  BwdParams p{};
+  const HeadView* views[4] = {&a.q, &a.k, &a.v, &d_o};
+  HeadMap* maps[4] = {&p.q, &p.k, &p.v, &p.d_o};
+  for (int i = 0; i < 4; ++i) {
+    cudaError_t e = make_head_map(maps[i], *views[i], a.b, a.s, i == 0 || i == 3 ? a.heads : a.kv_heads, a.head_dim);
+    if (e != cudaSuccess) return e;
+  }
+  p.o = a.o;
+  p.g = d_o;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  p.range = a.range;
+  p.slopes = a.slopes;
+  p.lse = a.lse;
+  p.dsum = static_cast<float*>(workspace);
+  const size_t d = static_cast<size_t>(a.b) * static_cast<size_t>(a.s) * static_cast<size_t>(a.heads) * sizeof(float);
+  p.tiles = reinterpret_cast<TileRange*>(static_cast<char*>(workspace) + (d + 255) / 256 * 256);
+  p.sp = score_params(a.scale, a.softcap);
+  p.scale = a.scale;
+  p.s = static_cast<int>(a.s);
+  p.heads = a.heads;
+  p.kv_heads = a.kv_heads;
+  p.group = a.heads / a.kv_heads;
+  p.head_dim = a.head_dim;
+  p.ntiles = static_cast<int>((a.s + kTile - 1) / kTile);
+  p.nseq = static_cast<int>(a.b);
+  p.status = ctx.status;
+  const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
+  if (a.head_dim > 64)
+    return cap ? (bias ? launch<128, true, true>(p, stream) : launch<128, true, false>(p, stream))
+               : (bias ? launch<128, false, true>(p, stream) : launch<128, false, false>(p, stream));
+  return cap ? (bias ? launch<64, true, true>(p, stream) : launch<64, true, false>(p, stream))
+             : (bias ? launch<64, false, true>(p, stream) : launch<64, false, false>(p, stream));
 }
 
 }  // namespace tpmlp

@@ -216,9 +216,9 @@ struct MaskedAttention {
 };
 
 cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream_t stream, const DeviceCtx& ctx);
-// dsum: [b][heads][s] floats of workspace, receives D = rowsum(d_o * o).
+size_t masked_attention_backward_workspace(int64_t b, int64_t s, int heads);
 cudaError_t launch_masked_attention_backward(const MaskedAttention& a, const HeadView& d_o, const HeadView& dq,
-                                             const HeadView& dk, const HeadView& dv, float* dsum, cudaStream_t stream,
+                                             const HeadView& dk, const HeadView& dv, void* workspace, cudaStream_t stream,
                                              const DeviceCtx& ctx);
 
 }  // namespace tpmlp

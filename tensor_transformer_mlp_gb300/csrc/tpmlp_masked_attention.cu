@@ -1,6 +1,7 @@
 // C ABI of masked attention (tpmlp_attention_key_ranges, tpmlp_masked_attention_forward / _backward):
 // the checks of the arguments, and the small kernel that turns a batch's documents, prefixes, causality
-// and window into one key interval per query. The attention kernels are in masked_attention.cu.
+// and window into one key interval per query. The attention kernels are in
+// masked_attention_fwd.cu and masked_attention_bwd.cu.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -234,7 +235,7 @@ tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const 
 
 size_t tpmlp_masked_attention_backward_workspace_size(int64_t b, int64_t s, int heads) {
   if (b <= 0 || s <= 0 || heads <= 0) return 0;
-  return (static_cast<size_t>(b) * static_cast<size_t>(s) * static_cast<size_t>(heads) * sizeof(float) + 255) / 256 * 256;
+  return masked_attention_backward_workspace(b, s, heads);
 }
 
 tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const void* v, const void* key_range,
@@ -263,7 +264,7 @@ tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const
                     static_cast<const int2*>(key_range), slopes, scale, softcap, const_cast<float*>(lse), b, s, heads,
                     kv_heads, head_dim};
   MATT_CUDA(launch_masked_attention_backward(a, {const_cast<void*>(d_o), ld_o, hs_o}, {dq, ld_dq, hs_dq},
-                                             {dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}, static_cast<float*>(workspace),
+                                             {dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}, workspace,
                                              static_cast<cudaStream_t>(stream), ctx),
             "masked attention backward");
   return TPMLP_OK;
