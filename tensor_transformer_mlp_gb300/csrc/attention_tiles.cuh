@@ -11,14 +11,48 @@ constexpr int kBoxBytes = kTile * 128;     // 128 rows x 64 bf16 columns, one 12
 
 // ------------------------------------------------------------------ tcgen05
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are the lanes, two bf16 of K per 32-bit column.
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// Products are issued by a whole warp that stays converged, each instruction under the predicate of one elected lane:
+// the descriptors then live in uniform registers and step by constants. (Issued from a branch that only one lane
+// takes, with descriptors built per step, a product of 128 x 128 x 16 took 80-125 cycles to issue and 64 to run.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t is;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is;
+}
+
+__device__ __forceinline__ void umma_bf16_by(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are the lanes, two bf16 of K per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ta_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 
@@ -85,13 +119,34 @@ __device__ __forceinline__ void load_head_tile(void* dst, const HeadMap& m, uint
     tma_load_4d(static_cast<uint8_t*>(dst) + x * kBoxBytes, &m.map, bar, x * 64, c1, c2, c3);
 }
 
-// Descriptor of K-step kk (16 of the head's columns) of a tile used K-major (rows are M or N).
-__device__ __forceinline__ uint64_t desc_rows(uint32_t tile, int kk) {
-  return smem_desc_sw128(tile + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024);
+// Descriptors of a tile's first K-step, and what each further step adds (the address field counts 16 bytes and a
+// shared-memory address never carries out of it). K-major, the rows being M or N: a step is 16 columns, 32 bytes, four
+// to a box. MN-major, the head's columns being N: a step is 16 rows.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t tile) { return smem_desc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_cols(uint32_t tile) { return smem_desc_sw128(tile, kBoxBytes, 1024); }
+__host__ __device__ constexpr uint64_t step_rows(int kk) { return ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4; }
+__host__ __device__ constexpr uint64_t step_cols(int kk) { return (kk * 2048) >> 4; }
+
+// D = A B^T over the heads' columns (ksteps of the HD / 16 steps; the rest are zeros), both tiles K-major.
+template <int HD>
+__device__ __forceinline__ void issue_rows(uint32_t leader, uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int ksteps) {
+  constexpr uint32_t kIdesc = idesc_bf16_f32(kTile, kTile, false, false);
+  const uint64_t a = desc_rows(a_tile), b = desc_rows(b_tile);
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk)
+    if (kk < ksteps) umma_bf16_by(leader, d_tmem, a + step_rows(kk), b + step_rows(kk), kIdesc, kk != 0);
 }
-// Descriptor of K-step kk (16 of the tile's rows) of a tile used MN-major (the head's columns are N).
-__device__ __forceinline__ uint64_t desc_cols(uint32_t tile, int kk) {
-  return smem_desc_sw128(tile + kk * 2048, kBoxBytes, 1024);
+
+// D (+)= A B with A's 128 columns packed in tensor memory from a_tmem (kSplit: columns 64.. from a_tmem + 64, else in a
+// row) and B a tile used MN-major.
+template <bool kSplit>
+__device__ __forceinline__ void issue_cols(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_tile,
+                                           uint32_t idesc, uint32_t accumulate) {
+  const uint64_t b = desc_cols(b_tile);
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    umma_bf16_ta_by(leader, d_tmem, a_tmem + (kSplit ? (kk >> 2) * 64 + (kk & 3) * 8 : kk * 8), b + step_cols(kk), idesc,
+                    kk == 0 ? accumulate : 1u);
 }
 
 // ------------------------------------------------------------------ masks and scores

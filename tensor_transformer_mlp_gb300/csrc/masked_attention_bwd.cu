@@ -62,10 +62,6 @@ struct BwdSmem {
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
-// The A operand of K-step kk: bf16 values of columns 16 kk .. 16 kk + 15, in the half of the accumulator that they
-// came from (each warp writes over columns that only it has read).
-__device__ __forceinline__ uint32_t packed_cols(uint32_t acc, int kk) { return acc + (kk >> 2) * 64 + (kk & 3) * 8; }
-
 // ------------------------------------------------------------------ query pass
 
 template <int HD, bool CAP, bool BIAS>
@@ -186,46 +182,43 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         for (int k = max(0, n + 1 - L::kHeld); k <= n; ++k) mbar_wait(&k_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x32);
         for (int k = max(0, n - L::kPassing); k < n; ++k) mbar_wait(&v_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x32);
       }
-    } else if (warp == kWorkWarps + 1 && lane == 0 && steps > 0) {
+    } else if (warp == kWorkWarps + 1 && steps > 0) {
       // ---------------------------------------------------------------- products
+      const uint32_t leader = elect_one();
       const int ksteps = (p.head_dim + 15) / 16;
-      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
       const uint32_t idesc_q = idesc_bf16_f32(kTile, ksteps * 16, false, true);
       const uint32_t q_addr = smem_u32(sq), g_addr = smem_u32(sg), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
-      bool ok = mbar_wait(q_full, 0, p.status, 0x33);
-      auto scores = [&](int n) {  // S(n) = Q K(n)^T
-        if (ok) ok = mbar_wait(&k_full[n % L::kHeld], (n / L::kHeld) & 1, p.status, 0x34);
-        if (!ok) return;
+      bool ok = true;
+      auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
         tc_fence_after();
-        const uint32_t kt = k_addr + (n % L::kHeld) * L::kTileBytes;
-        for (int kk = 0; kk < ksteps; ++kk)
-          umma_bf16(tmem + (n & 1) * 128, desc_rows(q_addr, kk), desc_rows(kt, kk), idesc_s, kk != 0);
-        umma_commit(&s_full[n & 1]);
+      };
+      auto scores = [&](int n) {  // S(n) = Q K(n)^T
+        wait_on(&k_full[n % L::kHeld], (n / L::kHeld) & 1, 0x34);
+        if (!ok) return;
+        issue_rows<HD>(leader, tmem + (n & 1) * 128, q_addr, k_addr + (n % L::kHeld) * L::kTileBytes, ksteps);
+        umma_commit_by(leader, &s_full[n & 1]);
       };
       auto dprobs = [&](int n) {  // dP(n) = d_o V(n)^T
-        if (ok) ok = mbar_wait(&v_full[n % L::kPassing], (n / L::kPassing) & 1, p.status, 0x35);
+        wait_on(&v_full[n % L::kPassing], (n / L::kPassing) & 1, 0x35);
         if (!ok) return;
-        tc_fence_after();
-        const uint32_t vt = v_addr + (n % L::kPassing) * L::kTileBytes;
-        for (int kk = 0; kk < ksteps; ++kk) umma_bf16(t_dp, desc_rows(g_addr, kk), desc_rows(vt, kk), idesc_s, kk != 0);
-        umma_commit(dp_full);
-        umma_commit(&v_empty[n % L::kPassing]);
+        issue_rows<HD>(leader, t_dp, g_addr, v_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
+        umma_commit_by(leader, dp_full);
+        umma_commit_by(leader, &v_empty[n % L::kPassing]);
       };
+      wait_on(q_full, 0, 0x33);
       scores(0);
       dprobs(0);
       if (steps > 1) scores(1);
       for (int n = 0; n < steps && ok; ++n) {
-        ok = mbar_wait(ds_full, n & 1, p.status, 0x36);
+        wait_on(ds_full, n & 1, 0x36);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t kt = k_addr + (n % L::kHeld) * L::kTileBytes;
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_bf16_ta(t_dq, packed_cols(t_dp, kk), desc_cols(kt, kk), idesc_q, (n | kk) != 0);
-        umma_commit(&k_empty[n % L::kHeld]);
+        issue_cols<true>(leader, t_dq, t_dp, k_addr + (n % L::kHeld) * L::kTileBytes, idesc_q, n != 0);
+        umma_commit_by(leader, &k_empty[n % L::kHeld]);
         if (n + 1 < steps) dprobs(n + 1);
         if (n + 2 < steps) scores(n + 2);
       }
-      umma_commit(acc_full);  // also: every product issued is done before tensor memory is freed
+      umma_commit_by(leader, acc_full);  // also: every product issued is done before tensor memory is freed
       mbar_wait(acc_full, 0, p.status, 0x37);
     }
   } else {
@@ -441,62 +434,48 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       }
     } else if (warp == kWorkWarps + 1) {
       // ---------------------------------------------------------------- products
+      const uint32_t leader = elect_one();
       const int ksteps = (p.head_dim + 15) / 16;
-      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
       const uint32_t idesc_d = idesc_bf16_f32(kTile, ksteps * 16, false, true);
       const uint32_t k_addr = smem_u32(sk), v_addr = smem_u32(sv), q_addr = smem_u32(q_ring), g_addr = smem_u32(g_ring);
-      auto agreed = [&](bool got) { return __all_sync(0xffffffffu, got); };
       bool more = it.next(), ok = true;
       const bool any = more;
-      auto scores = [&](int n) {  // S(n)^T = K Q(n)^T
-        if (ok) ok = agreed(mbar_wait(&q_full[n % L::kHeld], (n / L::kHeld) & 1, p.status, 0x43));
+      auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
         tc_fence_after();
-        if (ok && lane == 0) {
-          const uint32_t qt = q_addr + (n % L::kHeld) * L::kTileBytes;
-          for (int kk = 0; kk < ksteps; ++kk) umma_bf16(tmem, desc_rows(k_addr, kk), desc_rows(qt, kk), idesc_s, kk != 0);
-          umma_commit(s_full);
-        }
+      };
+      auto scores = [&](int n) {  // S(n)^T = K Q(n)^T
+        wait_on(&q_full[n % L::kHeld], (n / L::kHeld) & 1, 0x43);
+        if (!ok) return;
+        issue_rows<HD>(leader, tmem, k_addr, q_addr + (n % L::kHeld) * L::kTileBytes, ksteps);
+        umma_commit_by(leader, s_full);
       };
       auto dprobs = [&](int n) {  // dP(n)^T = V d_o(n)^T
-        if (ok) ok = agreed(mbar_wait(&g_full[n % L::kPassing], (n / L::kPassing) & 1, p.status, 0x44));
-        tc_fence_after();
-        if (ok && lane == 0) {
-          const uint32_t gt = g_addr + (n % L::kPassing) * L::kTileBytes;
-          for (int kk = 0; kk < ksteps; ++kk) umma_bf16(t_dp, desc_rows(v_addr, kk), desc_rows(gt, kk), idesc_s, kk != 0);
-          umma_commit(dp_full);
-        }
+        wait_on(&g_full[n % L::kPassing], (n / L::kPassing) & 1, 0x44);
+        if (!ok) return;
+        issue_rows<HD>(leader, t_dp, v_addr, g_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
+        umma_commit_by(leader, dp_full);
       };
       if (more) {
-        ok = agreed(mbar_wait(kv_full, 0, p.status, 0x45));
+        wait_on(kv_full, 0, 0x45);
         scores(0);
         dprobs(0);
       }
       for (int n = 0; more && ok; ++n) {
         more = it.next();
-        ok = agreed(mbar_wait(p_full, n & 1, p.status, 0x46));
+        wait_on(p_full, n & 1, 0x46);
         if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t gt = g_addr + (n % L::kPassing) * L::kTileBytes;
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_bf16_ta(t_dv, packed_cols(tmem, kk), desc_cols(gt, kk), idesc_d, (n | kk) != 0);
-          umma_commit(&g_empty[n % L::kPassing]);
-        }
+        issue_cols<true>(leader, t_dv, tmem, g_addr + (n % L::kPassing) * L::kTileBytes, idesc_d, n != 0);
+        umma_commit_by(leader, &g_empty[n % L::kPassing]);
         if (more) scores(n + 1);
-        if (ok) ok = agreed(mbar_wait(ds_full, n & 1, p.status, 0x47));
+        wait_on(ds_full, n & 1, 0x47);
         if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t qt = q_addr + (n % L::kHeld) * L::kTileBytes;
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_bf16_ta(t_dk, packed_cols(t_dp, kk), desc_cols(qt, kk), idesc_d, (n | kk) != 0);
-          umma_commit(&q_empty[n % L::kHeld]);
-        }
+        issue_cols<true>(leader, t_dk, t_dp, q_addr + (n % L::kHeld) * L::kTileBytes, idesc_d, n != 0);
+        umma_commit_by(leader, &q_empty[n % L::kHeld]);
         if (more) dprobs(n + 1);
       }
       if (any) {  // also: every product issued is done before tensor memory is freed
-        if (lane == 0) umma_commit(acc_full);
-        __syncwarp();
+        umma_commit_by(leader, acc_full);
         mbar_wait(acc_full, 0, p.status, 0x48);
       }
     } else if (warp == kWorkWarps + 2) {

@@ -25,8 +25,8 @@ namespace {
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 // Registers: 168 a thread at launch (three warpgroups); the two of the softmax, whose threads hold a row of 128
-// scores, take 216 and the third keeps 72 (2 * 216 + 72 = 3 * 168).
-constexpr int kRegsSoftmax = 216, kRegsIssue = 72;
+// scores, take 208 and the third keeps 88 (2 * 208 + 88 = 3 * 168).
+constexpr int kRegsSoftmax = 208, kRegsIssue = 88;
 constexpr float kRescaleAt = 8.0f;
 
 struct FwdParams {
@@ -160,63 +160,61 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         for (int k = max(0, n - L::kStages); k < n; ++k)
           mbar_wait(&kv_full[k % L::kStages], (k / L::kStages) & 1, p.status, 0x21);
       }
-    } else if (warp == kSoftmaxWarps + 1 && lane == 0) {
+    } else if (warp == kSoftmaxWarps + 1) {
       // ---------------------------------------------------------------- products
+      const uint32_t leader = elect_one();
       const int ksteps = (p.head_dim + 15) / 16;
-      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
       const uint32_t idesc_o = idesc_bf16_f32(kTile, ksteps * 16, false, true);
       const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
       bool ok = true;
-      auto wait_stage = [&](int n) {
-        if (ok) ok = mbar_wait(&kv_full[n % L::kStages], (n / L::kStages) & 1, p.status, 0x22);
+      auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
         tc_fence_after();
+      };
+      auto wait_stage = [&](int n) {
+        wait_on(&kv_full[n % L::kStages], (n / L::kStages) & 1, 0x22);
         return ring_addr + (n % L::kStages) * L::kTileBytes;
       };
       auto scores = [&](int i, uint32_t k_tile) {
-        for (int kk = 0; kk < ksteps; ++kk)
-          umma_bf16(tmem + i * 128, desc_rows(q_addr + i * L::kTileBytes, kk), desc_rows(k_tile, kk), idesc_s, kk != 0);
-        umma_commit(&s_full[i]);
+        issue_rows<HD>(leader, tmem + i * 128, q_addr + i * L::kTileBytes, k_tile, ksteps);
+        umma_commit_by(leader, &s_full[i]);
       };
       int j = next(j_begin), n = 0, steps[2] = {0, 0};
       if (j < j_end) {
         const uint32_t k_tile = wait_stage(0);
-        for (int i = 0; i < 2 && ok; ++i)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
           if (i ? any1 : any0) {
-            ok = mbar_wait(&q_full[i], 0, p.status, 0x23);
-            tc_fence_after();
+            wait_on(&q_full[i], 0, 0x23);
             if (ok && span[i].has(j)) scores(i, k_tile);
           }
-        if (ok) umma_commit(&kv_empty[0]);
+        if (ok) umma_commit_by(leader, &kv_empty[0]);
       }
       while (j < j_end && ok) {
         const int jn = next(j + 1);
         const uint32_t v_tile = wait_stage(2 * n + 1);
-        uint32_t k_next = 0;
+        const uint32_t k_next = jn < j_end ? wait_stage(2 * n + 2) : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (ok && span[i].has(j)) {
-            ok = mbar_wait(&p_full[i], steps[i] & 1, p.status, 0x24);
-            tc_fence_after();
+          if (span[i].has(j)) {
+            wait_on(&p_full[i], steps[i] & 1, 0x24);
             if (ok) {
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_bf16_ta(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, desc_cols(v_tile, kk), idesc_o,
-                             (steps[i] | kk) != 0);
+              issue_cols<false>(leader, tmem + 256 + i * 128, tmem + i * 128, v_tile, idesc_o, steps[i] != 0);
               ++steps[i];
-              if (j + 1 == span[i].hi) umma_commit(&o_full[i]);
+              if (j + 1 == span[i].hi) umma_commit_by(leader, &o_full[i]);
             }
           }
-          if (ok && jn < j_end && span[i].has(jn)) {
-            if (!k_next) k_next = wait_stage(2 * n + 2);
-            if (ok) scores(i, k_next);
-          }
+          if (ok && jn < j_end && span[i].has(jn)) scores(i, k_next);
         }
-        if (ok) umma_commit(&kv_empty[(2 * n + 1) % L::kStages]);
-        if (ok && jn < j_end) umma_commit(&kv_empty[(2 * n + 2) % L::kStages]);
+        if (ok) {
+          umma_commit_by(leader, &kv_empty[(2 * n + 1) % L::kStages]);
+          if (jn < j_end) umma_commit_by(leader, &kv_empty[(2 * n + 2) % L::kStages]);
+        }
         ++n;
         j = jn;
       }
       // every product issued must be done before tensor memory is freed
-      umma_commit(drain);
+      umma_commit_by(leader, drain);
       mbar_wait(drain, 0, p.status, 0x25);
     }
   } else {
