@@ -7,9 +7,7 @@ in the library's kernels; if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import math
 import os
 import threading
 
@@ -88,6 +86,8 @@ class TpmlpError(RuntimeError):
 def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load (building first if it is missing or stale) libtpmlp.so and declare its signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if build_if_missing and _build.is_stale():
@@ -124,43 +124,60 @@ def _cuda(*ts: torch.Tensor | None) -> None:
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
-    """Makes `device` and `stream` (default: the device's current stream) current, so that the kernels run there
-    and what torch allocates meanwhile belongs to that stream. Yields the stream's handle."""
-    if device.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+class _On:
+    """Makes a device and `stream` (default: the device's current stream) current, so that the kernels run there and
+    what torch allocates meanwhile belongs to that stream; `as` gives the stream's handle. Where both are current
+    already there is nothing to switch."""
+    __slots__ = ("index", "stream", "guard")
+
+    def __init__(self, index: int, stream):
+        if index < 0:
+            raise ValueError("tensors must be CUDA tensors")
+        if stream is not None and stream.device_index != index:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
+        self.index, self.stream, self.guard = index, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            self.guard = torch.cuda.stream(self.stream)  # switches to the stream's device too
+        elif torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+        if self.guard is not None:
+            self.guard.__enter__()
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
 
 
-def _same_device(device: torch.device, *ts: torch.Tensor | None) -> None:
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors are on different devices ({device}, {t.device})")
+def _device(first: torch.Tensor, *rest: torch.Tensor | None) -> int:
+    """The index of the one device that all tensors are on (-1: the CPU)."""
+    index = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors are on different devices ({first.device}, {t.device})")
+    return index
 
 
-def _heads(t: torch.Tensor, b: int, s: int, heads: int, hd: int, dtype: torch.dtype, name: str) -> tuple[int, int]:
+def _heads(t: torch.Tensor, shape: tuple[int, int, int, int], dtype: torch.dtype, name: str) -> tuple[int, int]:
     """The (token, head) strides of a [b, s, heads, hd] tensor of heads."""
-    if t.shape != (b, s, heads, hd):
-        raise ValueError(f"{name} must be [{b}, {s}, {heads}, {hd}], got {list(t.shape)}")
-    if t.dtype != dtype:
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    b, s, heads, hd = shape
     sb, ss, sh, sc = t.stride()
-    ld = ss if s > 1 else sb if b > 1 else max(heads * hd, 8)
     if (sc != 1 and hd > 1) or (b > 1 and s > 1 and sb != s * ss):
         raise ValueError(f"{name} needs contiguous columns and one stride for all tokens of the batch")
-    return ld, sh if heads > 1 else hd
+    return ss if s > 1 else sb if b > 1 else max(heads * hd, 8), sh if heads > 1 else hd
 
 
-def _dense(t: torch.Tensor | None, shape: tuple[int, ...], dtype: torch.dtype, name: str) -> None:
-    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+def _dense(t: torch.Tensor, shape: tuple[int, ...], dtype: torch.dtype, name: str) -> None:
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
 
 
@@ -520,17 +537,21 @@ def attention_key_ranges(b: int, s: int, doc_ids=None, prefix_len=None, causal: 
     """Runs tpmlp_attention_key_ranges; returns the int32 [b, s, 2] key range of every query, for
     masked_attention_forward and _backward. doc_ids int32 [b, s], prefix_len int32 [b]; `device` defaults to theirs,
     else to the current one."""
-    given = doc_ids if doc_ids is not None else prefix_len
-    device = given.device if given is not None else torch.device("cuda" if device is None else device)
-    if device.type == "cuda" and device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    _same_device(device, doc_ids, prefix_len)
-    _dense(doc_ids, (b, s), torch.int32, "doc_ids")
-    _dense(prefix_len, (b,), torch.int32, "prefix_len")
-    with _on(device, stream) as st:
-        out = torch.empty((b, s, 2), dtype=torch.int32, device=device)
-        _check(load_library().tpmlp_attention_key_ranges(_ptr(doc_ids), _ptr(prefix_len), int(bool(causal)), window,
-                                                         _ptr(out), b, s, st))
+    if doc_ids is not None:
+        _dense(doc_ids, (b, s), torch.int32, "doc_ids")
+        index = _device(doc_ids, prefix_len)
+    elif prefix_len is not None:
+        index = _device(prefix_len)
+    else:
+        device = torch.device("cuda" if device is None else device)
+        index = -1 if device.type != "cuda" else torch.cuda.current_device() if device.index is None else device.index
+    if prefix_len is not None:
+        _dense(prefix_len, (b,), torch.int32, "prefix_len")
+    lib = load_library()
+    with _On(index, stream) as st:
+        out = torch.empty((b, s, 2), dtype=torch.int32, device="cuda")
+        _check(lib.tpmlp_attention_key_ranges(_ptr(doc_ids), _ptr(prefix_len), 1 if causal else 0, window, out.data_ptr(),
+                                              b, s, st))
     return out
 
 
@@ -542,33 +563,34 @@ def rope_tables(table_len: int, rot_dim: int, theta: float = 10000.0, device=Non
     return ang.cos().float(), ang.sin().float()
 
 
-def _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions, *others):
-    b, s, heads, hd = q.shape
-    kv = k.shape[2]
-    half = cos.shape[1]
-    _same_device(q.device, k, gamma_q, gamma_k, cos, sin, positions, *others)
-    sq, sk = _heads(q, b, s, heads, hd, q.dtype, "q"), _heads(k, b, s, kv, hd, q.dtype, "k")
-    for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
-        _dense(g, (hd,), torch.float32, name)
-    for name, x in (("cos", cos), ("sin", sin)):
-        _dense(x, (cos.shape[0], half), torch.float32, name)
-    _dense(positions, (b, s), torch.int32, "positions")
-    return b, s, heads, kv, hd, 2 * half, sq, sk
+def _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions):
+    b, s, heads, hd = shape = q.shape
+    kshape = (b, s, k.shape[2], hd)
+    table = cos.shape
+    strides = _heads(q, shape, q.dtype, "q") + _heads(k, kshape, q.dtype, "k")
+    _dense(gamma_q, (hd,), torch.float32, "gamma_q")
+    _dense(gamma_k, (hd,), torch.float32, "gamma_k")
+    _dense(cos, table, torch.float32, "cos")
+    _dense(sin, table, torch.float32, "sin")
+    if positions is not None:
+        _dense(positions, (b, s), torch.int32, "positions")
+    return shape, kshape, table[0], 2 * table[1], strides
 
 
 def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, eps: float = 1e-5, positions=None, style: str = "half",
                  q_out=None, k_out=None, stream=None):
     """q [b, s, heads, head_dim], k [b, s, kv_heads, head_dim] (views of a QKV matrix, for instance). Allocates
     q_out and k_out unless given (q and k themselves for in place) and runs tpmlp_qk_norm_rope; returns them."""
-    b, s, heads, kv, hd, rot, sq, sk = _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out)
-    with _on(q.device, stream) as st:
-        q_out = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if q_out is None else q_out
-        k_out = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if k_out is None else k_out
-        sqo = _heads(q_out, b, s, heads, hd, q.dtype, "q_out")
-        sko = _heads(k_out, b, s, kv, hd, q.dtype, "k_out")
-        _check(load_library().tpmlp_qk_norm_rope(
-            _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), eps, _ptr(cos), _ptr(sin), _ptr(positions), cos.shape[0],
-            rot, ROPE_STYLE[style], _ptr(q_out), _ptr(k_out), b, s, heads, kv, hd, *sq, *sk, *sqo, *sko, _dt(q), st))
+    shape, kshape, table_len, rot, strides = _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions)
+    lib = load_library()
+    with _On(_device(q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out), stream) as st:
+        q_out = torch.empty(shape, dtype=q.dtype, device="cuda") if q_out is None else q_out
+        k_out = torch.empty(kshape, dtype=q.dtype, device="cuda") if k_out is None else k_out
+        strides += _heads(q_out, shape, q.dtype, "q_out") + _heads(k_out, kshape, q.dtype, "k_out")
+        _check(lib.tpmlp_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
+            _ptr(positions), table_len, rot, ROPE_STYLE[style], q_out.data_ptr(), k_out.data_ptr(), shape[0], shape[1],
+            shape[2], kshape[2], shape[3], *strides, _dt(q), st))
     return q_out, k_out
 
 
@@ -576,34 +598,33 @@ def qk_norm_rope_backward(q, k, gamma_q, gamma_k, cos, sin, dq_out, dk_out, eps:
                           style: str = "half", dq=None, dk=None, stream=None):
     """Runs tpmlp_qk_norm_rope_backward from the gradients of q_out and k_out; allocates the workspace, the gains'
     gradients and, unless given, dq and dk. Returns (dq, dk, dgamma_q, dgamma_k)."""
-    b, s, heads, kv, hd, rot, sq, sk = _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions, dq_out, dk_out, dq, dk)
-    sqo = _heads(dq_out, b, s, heads, hd, q.dtype, "dq_out")
-    sko = _heads(dk_out, b, s, kv, hd, q.dtype, "dk_out")
+    shape, kshape, table_len, rot, strides = _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions)
+    b, s, heads, hd = shape
+    strides += _heads(dq_out, shape, q.dtype, "dq_out") + _heads(dk_out, kshape, q.dtype, "dk_out")
     lib = load_library()
-    with _on(q.device, stream) as st:
-        dq = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if dk is None else dk
-        dgq = torch.empty(hd, dtype=torch.float32, device=q.device)
-        dgk = torch.empty(hd, dtype=torch.float32, device=q.device)
-        sdq, sdk = _heads(dq, b, s, heads, hd, q.dtype, "dq"), _heads(dk, b, s, kv, hd, q.dtype, "dk")
-        ws = torch.empty(max(1, lib.tpmlp_qk_norm_rope_backward_workspace_size(b, s, hd)), dtype=torch.uint8,
-                         device=q.device)
+    with _On(_device(q, k, gamma_q, gamma_k, cos, sin, positions, dq_out, dk_out, dq, dk), stream) as st:
+        dq = torch.empty(shape, dtype=q.dtype, device="cuda") if dq is None else dq
+        dk = torch.empty(kshape, dtype=q.dtype, device="cuda") if dk is None else dk
+        dgq, dgk = torch.empty((2, hd), dtype=torch.float32, device="cuda").unbind()
+        strides += _heads(dq, shape, q.dtype, "dq") + _heads(dk, kshape, q.dtype, "dk")
+        ws_bytes = lib.tpmlp_qk_norm_rope_backward_workspace_size(b, s, hd)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
         _check(lib.tpmlp_qk_norm_rope_backward(
-            _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), eps, _ptr(cos), _ptr(sin), _ptr(positions), cos.shape[0],
-            rot, ROPE_STYLE[style], _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dgq), _ptr(dgk), b, s, heads,
-            kv, hd, *sq, *sk, *sqo, *sko, *sdq, *sdk, _dt(q), _ptr(ws), ws.numel(), st))
+            q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
+            _ptr(positions), table_len, rot, ROPE_STYLE[style], dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(), b, s, heads, kshape[2], hd, *strides, _dt(q), ws.data_ptr(),
+            ws_bytes, st))
     return dq, dk, dgq, dgk
 
 
-def _masked_args(q, k, v, key_range, slopes, *others):
-    b, s, heads, hd = q.shape
-    kv = k.shape[2]
-    _same_device(q.device, k, v, key_range, slopes, *others)
+def _masked_args(q, k, v, key_range, slopes):
+    b, s, heads, hd = shape = q.shape
+    kshape = (b, s, k.shape[2], hd)
     _dense(key_range, (b, s, 2), torch.int32, "key_range")
-    _dense(slopes, (heads,), torch.float32, "slopes")
-    strides = (_heads(q, b, s, heads, hd, q.dtype, "q") + _heads(k, b, s, kv, hd, q.dtype, "k")
-               + _heads(v, b, s, kv, hd, q.dtype, "v"))
-    return b, s, heads, kv, hd, strides
+    if slopes is not None:
+        _dense(slopes, (heads,), torch.float32, "slopes")
+    dtype = q.dtype
+    return shape, kshape, _heads(q, shape, dtype, "q") + _heads(k, kshape, dtype, "k") + _heads(v, kshape, dtype, "v")
 
 
 def masked_attention_forward(q, k, v, key_range, scale: float | None = None, softcap: float = 0.0, slopes=None,
@@ -611,15 +632,17 @@ def masked_attention_forward(q, k, v, key_range, scale: float | None = None, sof
     """q [b, s, heads, head_dim], k and v [b, s, kv_heads, head_dim] bf16 (views of a QKV matrix, for instance).
     Allocates o (unless given) and lse and runs tpmlp_masked_attention_forward; scale defaults to
     head_dim^-1/2. Returns (o [b, s, heads, head_dim], lse [b, heads, s] fp32)."""
-    b, s, heads, kv, hd, strides = _masked_args(q, k, v, key_range, slopes, o)
-    scale = 1.0 / math.sqrt(hd) if scale is None else scale
-    with _on(q.device, stream) as st:
-        o = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if o is None else o
-        lse = torch.empty((b, heads, s), dtype=torch.float32, device=q.device)
-        so = _heads(o, b, s, heads, hd, q.dtype, "o")
-        _check(load_library().tpmlp_masked_attention_forward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(key_range), _ptr(slopes), scale, softcap, _ptr(o), _ptr(lse), b, s, heads,
-            kv, hd, *strides, *so, _dt(q), st))
+    shape, kshape, strides = _masked_args(q, k, v, key_range, slopes)
+    b, s, heads, hd = shape
+    lib = load_library()
+    with _On(_device(q, k, v, key_range, slopes, o), stream) as st:
+        o = torch.empty(shape, dtype=q.dtype, device="cuda") if o is None else o
+        lse = torch.empty((b, heads, s), dtype=torch.float32, device="cuda")
+        strides += _heads(o, shape, q.dtype, "o")
+        _check(lib.tpmlp_masked_attention_forward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
+            hd ** -0.5 if scale is None else scale, softcap, o.data_ptr(), lse.data_ptr(), b, s, heads, kshape[2], hd,
+            *strides, _dt(q), st))
     return o, lse
 
 
@@ -627,22 +650,23 @@ def masked_attention_backward(q, k, v, key_range, o, lse, do, scale: float | Non
                               slopes=None, dq=None, dk=None, dv=None, stream=None):
     """Runs tpmlp_masked_attention_backward from do = dl/do (o's strides); allocates the workspace and, unless given,
     dq, dk and dv. Returns (dq, dk, dv)."""
-    b, s, heads, kv, hd, strides = _masked_args(q, k, v, key_range, slopes, o, lse, do, dq, dk, dv)
-    scale = 1.0 / math.sqrt(hd) if scale is None else scale
+    shape, kshape, strides = _masked_args(q, k, v, key_range, slopes)
+    b, s, heads, hd = shape
+    dtype = q.dtype
     _dense(lse, (b, heads, s), torch.float32, "lse")
-    so = _heads(o, b, s, heads, hd, q.dtype, "o")
-    if _heads(do, b, s, heads, hd, q.dtype, "do") != so:
+    so = _heads(o, shape, dtype, "o")
+    if _heads(do, shape, dtype, "do") != so:
         raise ValueError("do must have o's strides")
     lib = load_library()
-    with _on(q.device, stream) as st:
-        dq = torch.empty((b, s, heads, hd), dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if dk is None else dk
-        dv = torch.empty((b, s, kv, hd), dtype=q.dtype, device=q.device) if dv is None else dv
-        grads = (_heads(dq, b, s, heads, hd, q.dtype, "dq") + _heads(dk, b, s, kv, hd, q.dtype, "dk")
-                 + _heads(dv, b, s, kv, hd, q.dtype, "dv"))
-        ws = torch.empty(max(1, lib.tpmlp_masked_attention_backward_workspace_size(b, s, heads)), dtype=torch.uint8,
-                         device=q.device)
+    with _On(_device(q, k, v, key_range, slopes, o, lse, do, dq, dk, dv), stream) as st:
+        dq = torch.empty(shape, dtype=dtype, device="cuda") if dq is None else dq
+        dk = torch.empty(kshape, dtype=dtype, device="cuda") if dk is None else dk
+        dv = torch.empty(kshape, dtype=dtype, device="cuda") if dv is None else dv
+        strides += so + _heads(dq, shape, dtype, "dq") + _heads(dk, kshape, dtype, "dk") + _heads(dv, kshape, dtype, "dv")
+        ws_bytes = lib.tpmlp_masked_attention_backward_workspace_size(b, s, heads)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
         _check(lib.tpmlp_masked_attention_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(key_range), _ptr(slopes), scale, softcap, _ptr(o), _ptr(lse), _ptr(do),
-            _ptr(dq), _ptr(dk), _ptr(dv), b, s, heads, kv, hd, *strides, *so, *grads, _dt(q), _ptr(ws), ws.numel(), st))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
+            hd ** -0.5 if scale is None else scale, softcap, o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), b, s, heads, kshape[2], hd, *strides, _dt(q), ws.data_ptr(), ws_bytes, st))
     return dq, dk, dv

@@ -6,12 +6,14 @@
 //
 // Both are bound by memory (about 4 flops a byte): q and k are read once and written once. A head's
 // columns lie eight to a lane on a group of G lanes (the power of two that covers head_dim / 8), so one
-// 16-byte load fetches a lane's bf16 share and the row sums are log2(G) shuffles. A CTA takes one token
-// at a time and its groups stride over the token's heads: the token's cosines and sines and the gains
-// stay in registers for all of them.
+// 16-byte load fetches a lane's bf16 share and the row sums are log2(G) shuffles. A group takes up to
+// kHeads heads of one token, all queries or all keys, so that what the position and the gain contribute is
+// loaded once for them, and loads kBatch of them ahead of their arithmetic, which runs on fp32 pairs.
+// Pairs of the half style are brought together by shuffles of the loaded words, before the norm is known.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -24,19 +26,30 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 256;
 constexpr int kBwdMaxCtas = 1024;
+constexpr int kHeads = 8;
+// Heads of a group loaded before the first is worked on: 64 bytes a thread of each tensor.
+template <typename T>
+constexpr int kBatch = 8 / sizeof(T);
+
+// Queries and keys go through the same code as parts 0 and 1.
+struct RopePart {
+  HeadView x, y, dx;    // forward: input, output; backward: input, dy, dx
+  const float* gamma;
+  int heads, chunks;    // chunks = ceil(heads / kHeads)
+};
 
 struct RopeParams {
-  HeadView q, k, qo, ko;    // forward: inputs, outputs; backward: x, dy
-  HeadView dq, dk;          // backward: dx
-  const float *gamma_q, *gamma_k;
+  RopePart part[2];
   const float *cos_t, *sin_t;
   const int* pos;
   int64_t table_len;
   int64_t tokens, s;
-  int heads, kv_heads, hd, rot, interleaved, group;
+  int hd, rot, group, ctas0;  // CTAs [0, ctas0) work on the queries, the others on the keys
+  int table_vec;              // the tables can be read 16 bytes at a time
   float eps, inv_hd;
 };
 
+// Eight columns as they lie in memory, and as four fp32 pairs.
 template <typename T>
 struct Vec8;
 template <>
@@ -44,18 +57,25 @@ struct Vec8<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+  __device__ __forceinline__ void unpack(F2 (&f)[4]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = unpack_bf16x2(w[i]);
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
+    for (int i = 0; i < 4; ++i) f[i] = f2_make(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                              pack_bf16x2(f[6], f[7]));
+  __device__ __forceinline__ Vec8 from_lane(int src) const {
+    Vec8 o;
+    o.v = make_uint4(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src),
+                     __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src));
+    return o;
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const F2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = f2_split(f[i]);
+      w[i] = pack_bf16x2(t.x, t.y);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
@@ -66,13 +86,24 @@ struct Vec8<float> {
     b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void unpack(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  __device__ __forceinline__ void unpack(F2 (&f)[4]) const {
+    f[0] = f2_make(a.x, a.y);
+    f[1] = f2_make(a.z, a.w);
+    f[2] = f2_make(b.x, b.y);
+    f[3] = f2_make(b.z, b.w);
   }
-  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ Vec8 from_lane(int src) const {
+    Vec8 o;
+    o.a = make_float4(__shfl_sync(0xffffffffu, a.x, src), __shfl_sync(0xffffffffu, a.y, src),
+                      __shfl_sync(0xffffffffu, a.z, src), __shfl_sync(0xffffffffu, a.w, src));
+    o.b = make_float4(__shfl_sync(0xffffffffu, b.x, src), __shfl_sync(0xffffffffu, b.y, src),
+                      __shfl_sync(0xffffffffu, b.z, src), __shfl_sync(0xffffffffu, b.w, src));
+    return o;
+  }
+  static __device__ __forceinline__ void store(float* p, const F2 (&f)[4]) {
+    const float2 t0 = f2_split(f[0]), t1 = f2_split(f[1]), t2 = f2_split(f[2]), t3 = f2_split(f[3]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(t0.x, t0.y, t1.x, t1.y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(t2.x, t2.y, t3.x, t3.y);
   }
 };
 
@@ -81,202 +112,283 @@ __device__ __forceinline__ float group_sum(float v, int group) {
   return v;
 }
 
-// One lane's share of a head: columns c0 .. c0 + 7 (active lanes), and what turns them. For column e
-// the turned value is f[e] * cs[e] + partner(e) * sn[e], where partner(e) is the pair's other column and
-// sn carries the sign of the forward turn (columns past rot: 1 and 0).
+__device__ __forceinline__ float sum4(const F2 (&f)[4]) {
+  const float2 t = f2_split(f2_add(f2_add(f[0], f[1]), f2_add(f[2], f[3])));
+  return t.x + t.y;
+}
+
+// How a column finds the other column of its pair: in its own lane (interleaved); in one other lane of the
+// group, rot / 16 further or back (half style with rot / 2 a multiple of 8); or through shared memory.
+enum Pairing { kOwnLane, kOtherLane, kAnyLane };
+
+// One lane's share of the work: columns c0 .. c0 + 7, what turns them, and where their partners are. Column e
+// of the turned head is f[e] * cs[e] + partner(e) * sn[e]; sn carries the sign of the forward turn or of its
+// transpose (`back`), and columns past rot have 1 and 0.
+template <int PAIRING>
 struct LaneTurn {
-  float cs[8], sn[8];
-  __device__ __forceinline__ void load(const RopeParams& p, int c0, int64_t pos) {
+  int lane, gl, c0, src;
+  float* xch;  // the warp's 32 x 8 floats
+  __device__ __forceinline__ LaneTurn(const RopeParams& p, float* xch_all) {
+    lane = threadIdx.x & 31;
+    gl = lane & (p.group - 1);
+    c0 = gl * 8;
+    xch = xch_all + (PAIRING == kAnyLane ? (threadIdx.x & ~31) * 8 : 0);
+    const int step = p.rot >> 4;
+    src = PAIRING != kOtherLane ? lane : gl < step ? lane + step : gl < 2 * step ? lane - step : lane;
+  }
+  __device__ __forceinline__ int partner_column(const RopeParams& p, int c) const {
     const int half = p.rot >> 1;
-    const bool in_table = pos < p.table_len;
+    return c >= p.rot ? c : PAIRING == kOwnLane ? c ^ 1 : c < half ? c + half : c - half;
+  }
+  __device__ __forceinline__ void angles(const RopeParams& p, int64_t pos, bool back, float (&cs)[8], float (&sn)[8]) const {
+    const int half = p.rot >> 1;
+    const float* ct = p.cos_t + pos * half;
+    const float* st = p.sin_t + pos * half;
+    if (pos >= p.table_len) {  // not covered: the rotated columns are no numbers
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + e;
-      cs[e] = 1.f;
-      sn[e] = 0.f;
-      if (c < p.rot) {
-        const int i = p.interleaved ? c >> 1 : (c < half ? c : c - half);
-        const bool first = p.interleaved ? (c & 1) == 0 : c < half;
-        const float nan = __int_as_float(0x7fffffff);
-        const float co = in_table ? p.cos_t[pos * half + i] : nan, si = in_table ? p.sin_t[pos * half + i] : nan;
-        cs[e] = co;
-        sn[e] = first ? -si : si;
+      for (int e = 0; e < 8; ++e) {
+        cs[e] = c0 + e < p.rot ? __int_as_float(0x7fffffff) : 1.f;
+        sn[e] = 0.f;
+      }
+    } else if (PAIRING == kOtherLane && p.table_vec) {  // eight columns lie on one side of the pairs
+      if (c0 < p.rot) {
+        const int i = c0 < half ? c0 : c0 - half;
+        const bool minus = (c0 < half) != back;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const float4 c = *reinterpret_cast<const float4*>(ct + i + 4 * v), s = *reinterpret_cast<const float4*>(st + i + 4 * v);
+          cs[4 * v] = c.x; cs[4 * v + 1] = c.y; cs[4 * v + 2] = c.z; cs[4 * v + 3] = c.w;
+          sn[4 * v] = minus ? -s.x : s.x; sn[4 * v + 1] = minus ? -s.y : s.y;
+          sn[4 * v + 2] = minus ? -s.z : s.z; sn[4 * v + 3] = minus ? -s.w : s.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          cs[e] = 1.f;
+          sn[e] = 0.f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = c0 + e;
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+        if (c < p.rot) {
+          const int i = PAIRING == kOwnLane ? c >> 1 : (c < half ? c : c - half);
+          const bool first = PAIRING == kOwnLane ? (c & 1) == 0 : c < half;
+          cs[e] = ct[i];
+          sn[e] = first != back ? -st[i] : st[i];
+        }
       }
     }
   }
-};
-
-// f -> R f (back: R^T f) within each group. xch: the warp's 32 x 8 floats for pairs that do not fall on
-// whole lanes (rot / 2 no multiple of 8, half style); otherwise the partner columns sit in one lane
-// rot / 16 further and a shuffle brings them. Every lane of the warp calls this.
-__device__ __forceinline__ void turn(float (&f)[8], const LaneTurn& t, const RopeParams& p, int lane, int gl, int c0,
-                                     bool back, float* xch) {
-  const float sg = back ? -1.f : 1.f;
-  float other[8];
-  if (p.interleaved) {
+  // Every lane of the warp calls this.
+  template <typename T>
+  __device__ __forceinline__ void partners(const RopeParams& p, const Vec8<T>& x, const F2 (&f)[4], F2 (&other)[4]) const {
+    if constexpr (PAIRING == kOwnLane) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) other[e] = f[e ^ 1];
-  } else if ((p.rot & 15) == 0) {
-    const int step = p.rot >> 4;
-    const int src = gl < step ? lane + step : (gl < 2 * step ? lane - step : lane);
+      for (int e = 0; e < 4; ++e) {
+        const float2 t = f2_split(f[e]);
+        other[e] = f2_make(t.y, t.x);
+      }
+    } else if constexpr (PAIRING == kOtherLane) {
+      x.from_lane(src).unpack(other);
+    } else {
+      __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) other[e] = __shfl_sync(0xffffffffu, f[e], src);
-  } else {
-    float* mine = xch + lane * 8;
-    __syncwarp();
+      for (int e = 0; e < 4; ++e) {
+        const float2 t = f2_split(f[e]);
+        xch[lane * 8 + 2 * e] = t.x;
+        xch[lane * 8 + 2 * e + 1] = t.y;
+      }
+      __syncwarp();
+      const float* head = xch + (lane - gl) * 8;
+      float o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mine[e] = f[e];
-    __syncwarp();
-    const float* head = xch + (lane - gl) * 8;
-    const int half = p.rot >> 1;
+      for (int e = 0; e < 8; ++e) o[e] = head[partner_column(p, c0 + e)];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + e;
-      other[e] = c < p.rot ? head[c < half ? c + half : c - half] : 0.f;
+      for (int e = 0; e < 4; ++e) other[e] = f2_make(o[2 * e], o[2 * e + 1]);
     }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = c0 + e < p.rot ? f[e] * t.cs[e] + other[e] * (sg * t.sn[e]) : f[e];
-}
+};
 
 __device__ __forceinline__ int64_t position_of(const RopeParams& p, int64_t token) {
   return p.pos ? static_cast<int64_t>(p.pos[token]) : token % p.s;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams p) {
-  __shared__ float xch_all[kThreads * 8];
-  const int lane = threadIdx.x & 31, gl = lane & (p.group - 1), c0 = gl * 8;
-  float* xch = xch_all + (threadIdx.x & ~31) * 8;
-  const bool act = c0 < p.hd;
-  const int ngroups = kThreads / p.group, g0 = threadIdx.x / p.group;
-  const int all = p.heads + p.kv_heads;
-  float gq[8], gk[8];
+template <typename T, int PAIRING>
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float xch_all[PAIRING == kAnyLane ? kThreads * 8 : 1];
+  const LaneTurn<PAIRING> t(p, xch_all);
+  const bool keys = static_cast<int>(blockIdx.x) >= p.ctas0;
+  const RopePart& a = p.part[keys ? 1 : 0];
+  const int ngroups = kThreads / p.group;
+  const int64_t item = static_cast<int64_t>(blockIdx.x - (keys ? p.ctas0 : 0)) * ngroups + threadIdx.x / p.group;
+  int64_t token = item / a.chunks;
+  const int h0 = static_cast<int>(item - token * a.chunks) * kHeads;
+  const bool act = t.c0 < p.hd && token < p.tokens;
+  if (token >= p.tokens) token = p.tokens - 1;  // idle, but it takes the shuffles
+  const int64_t pos = position_of(p, token);
+  const bool live = act && pos >= 0;
+  const T* x = static_cast<const T*>(a.x.ptr) + token * a.x.ld + h0 * a.x.hs + t.c0;
+  T* y = static_cast<T*>(a.y.ptr) + token * a.y.ld + h0 * a.y.hs + t.c0;
+  F2 ca[4], cb[4];
+#pragma unroll 1
+  for (int hb = 0; hb < kHeads; hb += kBatch<T>) {
+    Vec8<T> v[kBatch<T>];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    gq[e] = act ? p.gamma_q[c0 + e] : 0.f;
-    gk[e] = act ? p.gamma_k[c0 + e] : 0.f;
-  }
-  for (int64_t token = blockIdx.x; token < p.tokens; token += gridDim.x) {
-    const int64_t pos = position_of(p, token);
-    LaneTurn t;
-    t.load(p, c0, pos < 0 ? 0 : pos);
-    for (int hb = 0; hb < all; hb += ngroups) {  // uniform over the CTA, so every lane takes the shuffles
-      const int h = hb + g0;
-      const bool is_q = h < p.heads, on = act && h < all;
-      const HeadView& in = is_q ? p.q : p.k;
-      const HeadView& out = is_q ? p.qo : p.ko;
-      const int64_t hh = is_q ? h : h - p.heads;
-      Vec8<T> x;
-      x.zero();
-      if (on && pos >= 0) x.load(static_cast<const T*>(in.ptr) + token * in.ld + hh * in.hs + c0);
-      float f[8];
-      x.unpack(f);
-      float ss = 0.f;
+    for (int u = 0; u < kBatch<T>; ++u) {
+      v[u].zero();
+      if (live && h0 + hb + u < a.heads) v[u].load(x + (hb + u) * a.x.hs);
+    }
+    if (hb == 0) {  // y = r (f ca + partner cb)
+      float cs[8], sn[8];
+      t.angles(p, pos < 0 ? 0 : pos, false, cs, sn);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-      ss = group_sum(ss, p.group);
-      const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= r * (is_q ? gq[e] : gk[e]);
-      turn(f, t, p, lane, gl, c0, false, xch);
-      if (pos < 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 0.f;
+      for (int e = 0; e < 8; ++e) {
+        const int c = min(t.c0 + e, p.hd - 1);
+        cs[e] *= a.gamma[c];
+        sn[e] *= a.gamma[t.partner_column(p, c)];
       }
-      if (on) Vec8<T>::store(static_cast<T*>(out.ptr) + token * out.ld + hh * out.hs + c0, f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ca[e] = f2_make(cs[2 * e], cs[2 * e + 1]);
+        cb[e] = f2_make(sn[2 * e], sn[2 * e + 1]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch<T>; ++u) {
+      F2 f[4], other[4], sq[4];
+      v[u].unpack(f);
+      t.partners(p, v[u], f, other);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sq[e] = f2_mul(f[e], f[e]);
+      const float ss = group_sum(sum4(sq), p.group);
+      const float r = pos < 0 ? 0.f : rsqrtf(fmaf(ss, p.inv_hd, p.eps));
+      const F2 r2 = f2_make(r, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = f2_mul(r2, f2_fma(f[e], ca[e], f2_mul(other[e], cb[e])));
+      if (act && h0 + hb + u < a.heads) Vec8<T>::store(y + (hb + u) * a.y.hs, f);
     }
   }
 }
 
-// partials: [gridDim.x][2][hd] (dgamma_q, dgamma_k of the CTA's tokens, its groups added in order).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_backward_kernel(const RopeParams p, float* partials) {
+// partials: [gridDim.x][hd], the gain's gradient from the CTA's items (its groups added in order).
+template <typename T, int PAIRING>
+__global__ void __launch_bounds__(kThreads, 2)
+    qk_norm_rope_backward_kernel(const __grid_constant__ RopeParams p, float* partials) {
   __shared__ float xch_all[kThreads * 8];
-  const int lane = threadIdx.x & 31, gl = lane & (p.group - 1), c0 = gl * 8;
-  float* xch = xch_all + (threadIdx.x & ~31) * 8;
-  const bool act = c0 < p.hd;
-  const int ngroups = kThreads / p.group, g0 = threadIdx.x / p.group;
-  const int all = p.heads + p.kv_heads;
-  float gq[8], gk[8], aq[8], ak[8];
+  const LaneTurn<PAIRING> t(p, xch_all);
+  const bool keys = static_cast<int>(blockIdx.x) >= p.ctas0;
+  const RopePart& a = p.part[keys ? 1 : 0];
+  const int ngroups = kThreads / p.group;
+  const int cta = blockIdx.x - (keys ? p.ctas0 : 0), ctas = keys ? gridDim.x - p.ctas0 : p.ctas0;
+  const int64_t items = p.tokens * a.chunks;
+  F2 acc[4], gain[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    gq[e] = act ? p.gamma_q[c0 + e] : 0.f;
-    gk[e] = act ? p.gamma_k[c0 + e] : 0.f;
-    aq[e] = ak[e] = 0.f;
+  for (int e = 0; e < 4; ++e) {
+    acc[e] = f2_make(0.f, 0.f);
+    gain[e] = f2_make(a.gamma[min(t.c0 + 2 * e, p.hd - 1)], a.gamma[min(t.c0 + 2 * e + 1, p.hd - 1)]);
   }
-  for (int64_t token = blockIdx.x; token < p.tokens; token += gridDim.x) {
+  // every group of the CTA makes the same number of rounds, so that all lanes take the shuffles
+  for (int64_t first = static_cast<int64_t>(cta) * ngroups; first < items; first += static_cast<int64_t>(ctas) * ngroups) {
+    const int64_t item = min(first + threadIdx.x / p.group, items - 1);
+    const bool act = t.c0 < p.hd && first + threadIdx.x / p.group < items;
+    const int64_t token = item / a.chunks;
+    const int h0 = static_cast<int>(item - token * a.chunks) * kHeads;
     const int64_t pos = position_of(p, token);
-    LaneTurn t;
-    t.load(p, c0, pos < 0 ? 0 : pos);
-    for (int hb = 0; hb < all; hb += ngroups) {
-      const int h = hb + g0;
-      const bool is_q = h < p.heads, on = act && h < all;
-      const int64_t hh = is_q ? h : h - p.heads;
-      const HeadView& in = is_q ? p.q : p.k;
-      const HeadView& dyv = is_q ? p.qo : p.ko;
-      const HeadView& out = is_q ? p.dq : p.dk;
-      Vec8<T> x, dy;
-      x.zero();
-      dy.zero();
-      if (on && pos >= 0) {
-        x.load(static_cast<const T*>(in.ptr) + token * in.ld + hh * in.hs + c0);
-        dy.load(static_cast<const T*>(dyv.ptr) + token * dyv.ld + hh * dyv.hs + c0);
-      }
-      float f[8], d[8];
-      x.unpack(f);
-      dy.unpack(d);
-      turn(d, t, p, lane, gl, c0, true, xch);
-      float ss = 0.f, gx = 0.f;
+    const bool live = act && pos >= 0;
+    const T* x = static_cast<const T*>(a.x.ptr) + token * a.x.ld + h0 * a.x.hs + t.c0;
+    const T* y = static_cast<const T*>(a.y.ptr) + token * a.y.ld + h0 * a.y.hs + t.c0;
+    T* dx = static_cast<T*>(a.dx.ptr) + token * a.dx.ld + h0 * a.dx.hs + t.c0;
+    F2 cs[4], sn[4];
+#pragma unroll 1
+    for (int hb = 0; hb < kHeads; hb += kBatch<T>) {
+      Vec8<T> vx[kBatch<T>], vy[kBatch<T>];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(f[e], f[e], ss);
-        gx = fmaf(d[e] * (is_q ? gq[e] : gk[e]), f[e], gx);
+      for (int u = 0; u < kBatch<T>; ++u) {
+        vx[u].zero();
+        vy[u].zero();
+        if (live && h0 + hb + u < a.heads) {
+          vx[u].load(x + (hb + u) * a.x.hs);
+          vy[u].load(y + (hb + u) * a.y.hs);
+        }
       }
-      ss = group_sum(ss, p.group);
-      gx = group_sum(gx, p.group);
-      const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-      const float m = gx * r * p.inv_hd;  // mean(g x_hat)
-      float o[8];
+      if (hb == 0) {
+        float c8[8], s8[8];
+        t.angles(p, pos < 0 ? 0 : pos, true, c8, s8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xh = f[e] * r;
-        o[e] = pos < 0 ? 0.f : r * (d[e] * (is_q ? gq[e] : gk[e]) - xh * m);
-        const float dg = on && pos >= 0 ? d[e] * xh : 0.f;
-        if (is_q) aq[e] += dg; else ak[e] += dg;
+        for (int e = 0; e < 4; ++e) {
+          cs[e] = f2_make(c8[2 * e], c8[2 * e + 1]);
+          sn[e] = f2_make(s8[2 * e], s8[2 * e + 1]);
+        }
       }
-      if (on) Vec8<T>::store(static_cast<T*>(out.ptr) + token * out.ld + hh * out.hs + c0, o);
+#pragma unroll
+      for (int u = 0; u < kBatch<T>; ++u) {
+        F2 f[4], d[4], other[4], s1[4], s2[4];
+        vx[u].unpack(f);
+        vy[u].unpack(d);
+        t.partners(p, vy[u], d, other);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          d[e] = f2_fma(d[e], cs[e], f2_mul(other[e], sn[e]));  // du
+          other[e] = f2_mul(d[e], f[e]);
+          d[e] = f2_mul(d[e], gain[e]);                         // g
+          s1[e] = f2_mul(f[e], f[e]);
+          s2[e] = f2_mul(d[e], f[e]);
+        }
+        const float ss = group_sum(sum4(s1), p.group);
+        const float gx = group_sum(sum4(s2), p.group);
+        const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
+        const float m = -gx * p.inv_hd * r * r * r;  // dx = r g - x r^3 mean(g x)
+        const bool on = act && h0 + hb + u < a.heads;
+        const float ra = pos < 0 || !on ? 0.f : r;
+        const F2 r2 = f2_make(pos < 0 ? 0.f : r, pos < 0 ? 0.f : r), m2 = f2_make(m, m), ra2 = f2_make(ra, ra);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[e] = f2_fma(other[e], ra2, acc[e]);
+          d[e] = f2_fma(f[e], m2, f2_mul(r2, d[e]));
+        }
+        if (on) Vec8<T>::store(dx + (hb + u) * a.dx.hs, d);
+      }
     }
   }
+  __syncthreads();
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) xch_all[threadIdx.x * 8 + e] = part ? ak[e] : aq[e];
-    __syncthreads();
-    for (int c = threadIdx.x; c < p.hd; c += kThreads) {
-      float sum = 0.f;
-      for (int g = 0; g < ngroups; ++g) sum += xch_all[g * p.group * 8 + c];
-      partials[(static_cast<int64_t>(blockIdx.x) * 2 + part) * p.hd + c] = sum;
-    }
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = f2_split(acc[e]);
+    xch_all[threadIdx.x * 8 + 2 * e] = v.x;
+    xch_all[threadIdx.x * 8 + 2 * e + 1] = v.y;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.hd; c += kThreads) {
+    float sum = 0.f;
+    for (int g = 0; g < ngroups; ++g) sum += xch_all[g * p.group * 8 + c];
+    partials[static_cast<int64_t>(blockIdx.x) * p.hd + c] = sum;
   }
 }
 
-// Adds the CTAs' partials in a fixed order: each CTA takes one column of 2 * hd, its 128 threads add every
-// 128th partial in order and a tree joins them.
-__global__ void __launch_bounds__(128)
-    rope_gain_sum_kernel(const float* __restrict__ partials, int nparts, int hd, float* __restrict__ dgamma_q,
+// Adds the CTAs' partials in a fixed order: 32 columns of one gain to a CTA, 32 threads for each, which add
+// every 32nd partial and are joined by a tree. Launched as the backward's programmatic dependent.
+__global__ void __launch_bounds__(1024)
+    rope_gain_sum_kernel(const float* __restrict__ partials, int ctas0, int ctas, int hd, float* __restrict__ dgamma_q,
                          float* __restrict__ dgamma_k) {
-  __shared__ float red[128];
-  const int c = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float red[32][33];
+  const int col = threadIdx.x & 31, row = threadIdx.x >> 5, c = blockIdx.x * 32 + col;
+  const int first = blockIdx.y ? ctas0 : 0, last = blockIdx.y ? ctas : ctas0;
   float sum = 0.f;
-  for (int i = threadIdx.x; i < nparts; i += 128) sum += partials[static_cast<int64_t>(i) * 2 * hd + c];
-  red[threadIdx.x] = sum;
-  for (int o = 64; o > 0; o >>= 1) {
-    __syncthreads();
-    if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+  if (c < hd) {
+#pragma unroll 8
+    for (int i = first + row; i < last; i += 32) sum += partials[static_cast<int64_t>(i) * hd + c];
   }
-  if (threadIdx.x == 0) (c < hd ? dgamma_q[c] : dgamma_k[c - hd]) = red[0];
+  red[row][col] = sum;
+  for (int o = 16; o > 0; o >>= 1) {
+    __syncthreads();
+    if (row < o) red[row][col] += red[row + o][col];
+  }
+  if (row == 0 && c < hd) (blockIdx.y ? dgamma_k : dgamma_q)[c] = red[0][col];
 }
 
 tpmlp_status err(tpmlp_status st, const char* msg) { return static_cast<tpmlp_status>(report_error(st, msg)); }
@@ -324,10 +436,38 @@ tpmlp_status check_ptrs(std::initializer_list<const void*> ptrs, size_t a) {
   return TPMLP_OK;
 }
 
-int group_of(int hd) {
-  int g = 1;
-  while (g * 8 < hd) g *= 2;
-  return g;
+RopeParams make_params(const RopePart& q, const RopePart& k, const float* cos_table, const float* sin_table,
+                       const void* positions, int64_t table_len, int rot, int64_t b, int64_t s, int hd, float eps) {
+  RopeParams p{};
+  p.part[0] = q;
+  p.part[1] = k;
+  for (RopePart& a : p.part) a.chunks = (a.heads + kHeads - 1) / kHeads;
+  p.cos_t = cos_table;
+  p.sin_t = sin_table;
+  p.pos = static_cast<const int*>(positions);
+  p.table_len = table_len;
+  p.tokens = b * s;
+  p.s = s;
+  p.hd = hd;
+  p.rot = rot;
+  for (p.group = 1; p.group * 8 < hd;) p.group *= 2;
+  p.table_vec = aligned(cos_table, 16) && aligned(sin_table, 16) && (rot / 2) % 4 == 0;
+  p.eps = eps;
+  p.inv_hd = 1.0f / static_cast<float>(hd);
+  return p;
+}
+
+// The kernel of a type and a pairing out of K<T, PAIRING>.
+#define ROPE_PICK(K, dt, pairing)                                                                                  \
+  ((dt) == TPMLP_BF16 ? ((pairing) == kOwnLane     ? K<__nv_bfloat16, kOwnLane>                                    \
+                         : (pairing) == kOtherLane ? K<__nv_bfloat16, kOtherLane>                                  \
+                                                   : K<__nv_bfloat16, kAnyLane>)                                   \
+                      : ((pairing) == kOwnLane     ? K<float, kOwnLane>                                            \
+                         : (pairing) == kOtherLane ? K<float, kOtherLane>                                          \
+                                                   : K<float, kAnyLane>))
+
+int pairing_of(int style, int rot) {
+  return style == TPMLP_ROPE_INTERLEAVED ? kOwnLane : rot % 16 == 0 ? kOtherLane : kAnyLane;
 }
 
 }  // namespace
@@ -361,33 +501,24 @@ tpmlp_status tpmlp_qk_norm_rope(const void* q, const void* k, const float* gamma
   ROPE_TRY(check_ptrs({q, k, q_out, k_out}, 16));
   ROPE_TRY(check_ptrs({gamma_q, gamma_k, cos_table, sin_table}, 4));
   if (!aligned(positions, 4)) return err(TPMLP_ERR_ALIGN, "positions not 4-byte aligned");
-  DeviceCtx ctx;
-  ROPE_CUDA(get_device_ctx(&ctx), "device context");
-  RopeParams p{};
-  p.q = {const_cast<void*>(q), ld_q, hs_q};
-  p.k = {const_cast<void*>(k), ld_k, hs_k};
-  p.qo = {q_out, ld_qo, hs_qo};
-  p.ko = {k_out, ld_ko, hs_ko};
-  p.gamma_q = gamma_q; p.gamma_k = gamma_k;
-  p.cos_t = cos_table; p.sin_t = sin_table;
-  p.pos = static_cast<const int*>(positions);
-  p.table_len = table_len;
-  p.tokens = b * s; p.s = s;
-  p.heads = heads; p.kv_heads = kv_heads; p.hd = head_dim; p.rot = rot_dim; p.interleaved = style;
-  p.group = group_of(head_dim);
-  p.eps = eps; p.inv_hd = 1.0f / static_cast<float>(head_dim);
+  RopeParams p = make_params({{const_cast<void*>(q), ld_q, hs_q}, {q_out, ld_qo, hs_qo}, {}, gamma_q, heads, 0},
+                             {{const_cast<void*>(k), ld_k, hs_k}, {k_out, ld_ko, hs_ko}, {}, gamma_k, kv_heads, 0},
+                             cos_table, sin_table, positions, table_len, rot_dim, b, s, head_dim, eps);
+  const int64_t ngroups = kThreads / p.group;
+  const int64_t ctas0 = (p.tokens * p.part[0].chunks + ngroups - 1) / ngroups;
+  const int64_t ctas = ctas0 + (p.tokens * p.part[1].chunks + ngroups - 1) / ngroups;
+  if (ctas > INT32_MAX) return err(TPMLP_ERR_SHAPE, "too many heads in all (b * s * heads)");
+  p.ctas0 = static_cast<int>(ctas0);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = static_cast<int>(std::min<int64_t>(p.tokens, static_cast<int64_t>(ctx.num_sms) * 8));
-  if (dt == TPMLP_BF16) qk_norm_rope_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
-  else qk_norm_rope_kernel<float><<<grid, kThreads, 0, st>>>(p);
+  auto kernel = ROPE_PICK(qk_norm_rope_kernel, dt, pairing_of(style, rot_dim));
+  kernel<<<static_cast<unsigned>(ctas), kThreads, 0, st>>>(p);
   ROPE_CUDA(cudaGetLastError(), "qk_norm_rope");
   return TPMLP_OK;
 }
 
 size_t tpmlp_qk_norm_rope_backward_workspace_size(int64_t b, int64_t s, int head_dim) {
   if (b <= 0 || s <= 0 || head_dim <= 0) return 0;
-  const int64_t ctas = s > kBwdMaxCtas / b ? kBwdMaxCtas : std::min<int64_t>(b * s, kBwdMaxCtas);
-  return static_cast<size_t>(ctas) * 2 * static_cast<size_t>(head_dim) * sizeof(float);
+  return static_cast<size_t>(kBwdMaxCtas) * static_cast<size_t>(head_dim) * sizeof(float);
 }
 
 tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const float* gamma_q, const float* gamma_k,
@@ -418,29 +549,34 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
   if (!aligned(workspace, 16)) return err(TPMLP_ERR_ALIGN, "workspace not 16-byte aligned");
   DeviceCtx ctx;
   ROPE_CUDA(get_device_ctx(&ctx), "device context");
-  RopeParams p{};
-  p.q = {const_cast<void*>(q), ld_q, hs_q};
-  p.k = {const_cast<void*>(k), ld_k, hs_k};
-  p.qo = {const_cast<void*>(dq_out), ld_qo, hs_qo};
-  p.ko = {const_cast<void*>(dk_out), ld_ko, hs_ko};
-  p.dq = {dq, ld_dq, hs_dq};
-  p.dk = {dk, ld_dk, hs_dk};
-  p.gamma_q = gamma_q; p.gamma_k = gamma_k;
-  p.cos_t = cos_table; p.sin_t = sin_table;
-  p.pos = static_cast<const int*>(positions);
-  p.table_len = table_len;
-  p.tokens = b * s; p.s = s;
-  p.heads = heads; p.kv_heads = kv_heads; p.hd = head_dim; p.rot = rot_dim; p.interleaved = style;
-  p.group = group_of(head_dim);
-  p.eps = eps; p.inv_hd = 1.0f / static_cast<float>(head_dim);
-  const int grid = static_cast<int>(
-      std::min<int64_t>(p.tokens, std::min<int64_t>(static_cast<int64_t>(ctx.num_sms) * 4, kBwdMaxCtas)));
+  RopeParams p = make_params(
+      {{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(dq_out), ld_qo, hs_qo}, {dq, ld_dq, hs_dq}, gamma_q, heads, 0},
+      {{const_cast<void*>(k), ld_k, hs_k}, {const_cast<void*>(dk_out), ld_ko, hs_ko}, {dk, ld_dk, hs_dk}, gamma_k, kv_heads, 0},
+      cos_table, sin_table, positions, table_len, rot_dim, b, s, head_dim, eps);
+  // Two CTAs a SM, shared out between queries and keys as their heads are.
+  const int64_t ngroups = kThreads / p.group;
+  const int64_t want0 = (p.tokens * p.part[0].chunks + ngroups - 1) / ngroups;
+  const int64_t want1 = (p.tokens * p.part[1].chunks + ngroups - 1) / ngroups;
+  const int64_t room = std::min<int64_t>(static_cast<int64_t>(ctx.num_sms) * 2, kBwdMaxCtas);
+  const int64_t share0 = std::max<int64_t>(1, std::min<int64_t>(room - 1, room * p.part[0].chunks / (p.part[0].chunks + p.part[1].chunks)));
+  p.ctas0 = static_cast<int>(std::min(want0, share0));
+  const int grid = p.ctas0 + static_cast<int>(std::min(want1, room - share0));
   float* partials = static_cast<float*>(workspace);
-  if (dt == TPMLP_BF16) qk_norm_rope_backward_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p, partials);
-  else qk_norm_rope_backward_kernel<float><<<grid, kThreads, 0, st>>>(p, partials);
+  auto kernel = ROPE_PICK(qk_norm_rope_backward_kernel, dt, pairing_of(style, rot_dim));
+  kernel<<<grid, kThreads, 0, st>>>(p, partials);
   ROPE_CUDA(cudaGetLastError(), "qk_norm_rope backward");
-  rope_gain_sum_kernel<<<2 * head_dim, 128, 0, st>>>(partials, grid, head_dim, dgamma_q, dgamma_k);
-  ROPE_CUDA(cudaGetLastError(), "qk_norm_rope gain sums");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((head_dim + 31) / 32), 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  ROPE_CUDA(cudaLaunchKernelEx(&cfg, rope_gain_sum_kernel, static_cast<const float*>(partials), p.ctas0, grid, head_dim, dgamma_q,
+                               dgamma_k),
+            "qk_norm_rope gain sums");
   return TPMLP_OK;
 }
 

@@ -15,7 +15,6 @@ namespace tpmlp {
 namespace {
 
 constexpr int kRangeThreads = 1024;
-constexpr int kRangeItems = 8;
 
 // The interval of query i, whose document (or sequence) is [start, end).
 __device__ __forceinline__ int2 query_range(int64_t i, int64_t start, int64_t end, int causal, int64_t prefix,
@@ -40,88 +39,79 @@ __global__ void __launch_bounds__(256)
 }
 
 // The same with documents, one CTA per sequence. A document is a run of equal ids: token i's starts at the
-// last j <= i whose id differs from its left neighbour's (a running maximum from the left) and ends at the
-// first such j > i (a running minimum from the right). Both scans go tile by tile: eight tokens a thread,
-// warp shuffles, then the warps' totals, with the outermost value carried to the next tile. The first scan
-// parks each start in out[].x, which the thread that wrote it reads back in the second.
+// last j <= i whose id differs from its left neighbour's and ends at the first such j > i. A warp turns 32
+// tokens into one word of start bits with a ballot, so a tile of kWords words costs one pass over its ids, and
+// the two searches are bit scans within a word and one running maximum (from the left) and minimum (from the
+// right) over the words. A row of one tile (32768 tokens) is done in one go; longer rows sweep their tiles from
+// the left, parking each start in out[].x, and then from the right, the thread that wrote a start reading it back.
 __global__ void __launch_bounds__(kRangeThreads)
     doc_key_range_kernel(const int* __restrict__ ids_all, const int* __restrict__ prefix, int causal, int64_t window,
                          int2* __restrict__ out_all, int s) {
-  constexpr int kTile = kRangeThreads * kRangeItems;
-  __shared__ int warp_total[kRangeThreads / 32];
+  constexpr int kWords = kRangeThreads, kWarps = kRangeThreads / 32;
+  __shared__ unsigned starts[kWords];
+  __shared__ int before[kWords], after[kWords];  // last start left of the word, first start right of it
+  __shared__ int total[2][kWarps];
   const int64_t bi = blockIdx.x;
   const int* ids = ids_all + bi * s;
   int2* out = out_all + bi * s;
+  const int64_t plen = prefix ? prefix[bi] : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ntiles = (s + kTile - 1) / kTile;
-  int carry = 0;
-  for (int tile = 0; tile < ntiles; ++tile) {
-    const int64_t i0 = static_cast<int64_t>(tile) * kTile + threadIdx.x * kRangeItems;
-    int own[kRangeItems], run = -1;
+  const int nwords = (s + 31) / 32, ntiles = (nwords + kWords - 1) / kWords;
+  const int sweeps = ntiles > 1 ? 2 : 1;
+  for (int sweep = 0; sweep < sweeps; ++sweep) {
+    int left = 0, right = s;  // last start in the tiles before (first sweep), first start in those behind (last sweep)
+    for (int n = 0; n < ntiles; ++n) {
+      const int w0 = (sweep == 0 ? n : ntiles - 1 - n) * kWords;  // the tile's first word in the row
+      const int words = min(kWords, nwords - w0);
+#pragma unroll 8
+      for (int w = warp; w < words; w += kWarps) {
+        const int i = (w0 + w) * 32 + lane;
+        const bool in = i < s;
+        const int id = in ? ids[i] : 0;
+        int prev = __shfl_up_sync(0xffffffffu, id, 1);
+        if (lane == 0 && i > 0) prev = ids[i - 1];
+        const unsigned bits = __ballot_sync(0xffffffffu, in && (i == 0 || id != prev));
+        if (lane == 0) starts[w] = bits;
+      }
+      __syncthreads();
+      const int base = (w0 + static_cast<int>(threadIdx.x)) * 32;
+      const unsigned bits = static_cast<int>(threadIdx.x) < words ? starts[threadIdx.x] : 0u;
+      int last = bits ? base + 31 - __clz(bits) : -1, first = bits ? base + __ffs(bits) - 1 : INT32_MAX;
 #pragma unroll
-    for (int e = 0; e < kRangeItems; ++e) {
-      const int64_t i = i0 + e;
-      if (i < s && (i == 0 || ids[i] != ids[i - 1])) run = static_cast<int>(i);
-      own[e] = run;
-    }
-    int incl = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl = max(incl, v);
-    }
-    if (lane == 31) warp_total[warp] = incl;
-    __syncthreads();
-    int before = carry, all = carry;
-    for (int w = 0; w < kRangeThreads / 32; ++w) {
-      const int v = warp_total[w];
-      if (w < warp) before = max(before, v);
-      all = max(all, v);
-    }
-    const int left = __shfl_up_sync(0xffffffffu, incl, 1);
-    if (lane > 0) before = max(before, left);
-    carry = all;
-#pragma unroll
-    for (int e = 0; e < kRangeItems; ++e)
-      if (i0 + e < s) out[i0 + e].x = max(before, own[e]);
-    __syncthreads();
-  }
-  carry = s;
-  for (int tile = ntiles - 1; tile >= 0; --tile) {
-    const int64_t i0 = static_cast<int64_t>(tile) * kTile + threadIdx.x * kRangeItems;
-    int own[kRangeItems], run = s;
-#pragma unroll
-    for (int e = kRangeItems - 1; e >= 0; --e) {
-      const int64_t i = i0 + e;
-      if (i + 1 < s && ids[i] != ids[i + 1]) run = static_cast<int>(i + 1);
-      own[e] = run;
-    }
-    int incl = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_down_sync(0xffffffffu, incl, o);
-      if (lane + o < 32) incl = min(incl, v);
-    }
-    if (lane == 0) warp_total[warp] = incl;
-    __syncthreads();
-    int after = carry, all = carry;
-    for (int w = 0; w < kRangeThreads / 32; ++w) {
-      const int v = warp_total[w];
-      if (w > warp) after = min(after, v);
-      all = min(all, v);
-    }
-    const int right = __shfl_down_sync(0xffffffffu, incl, 1);
-    if (lane < 31) after = min(after, right);
-    carry = all;
-#pragma unroll
-    for (int e = 0; e < kRangeItems; ++e) {
-      const int64_t i = i0 + e;
-      if (i < s) {
-        const int2 r = query_range(i, out[i].x, min(after, own[e]), causal, prefix ? prefix[bi] : 0, window);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, last, o), d = __shfl_down_sync(0xffffffffu, first, o);
+        if (lane >= o) last = max(last, u);
+        if (lane + o < 32) first = min(first, d);
+      }
+      if (lane == 31) total[0][warp] = last;
+      if (lane == 0) total[1][warp] = first;
+      __syncthreads();
+      {
+        const int tl = total[0][lane], tf = total[1][lane];
+        const int prior = __reduce_max_sync(0xffffffffu, lane < warp ? tl : left);
+        const int later = __reduce_min_sync(0xffffffffu, lane > warp ? tf : right);
+        const int lu = __shfl_up_sync(0xffffffffu, last, 1), fd = __shfl_down_sync(0xffffffffu, first, 1);
+        before[threadIdx.x] = lane > 0 ? max(prior, lu) : prior;
+        after[threadIdx.x] = lane < 31 ? min(later, fd) : later;
+        left = max(left, __reduce_max_sync(0xffffffffu, tl));
+        right = min(right, __reduce_min_sync(0xffffffffu, tf));
+      }
+      __syncthreads();
+      for (int w = warp; w < words; w += kWarps) {
+        const int i = (w0 + w) * 32 + lane;
+        if (i >= s) continue;
+        const unsigned b = starts[w], upto = b & (0xffffffffu >> (31 - lane)), past = b & ~(0xffffffffu >> (31 - lane));
+        const int start = upto ? (w0 + w) * 32 + 31 - __clz(upto) : before[w];
+        if (sweep < sweeps - 1) {
+          out[i].x = start;
+          continue;
+        }
+        const int end = past ? (w0 + w) * 32 + __ffs(past) - 1 : after[w];
+        const int2 r = query_range(i, sweeps == 1 ? start : out[i].x, end, causal, plen, window);
         out[i] = ids[i] < 0 ? make_int2(0, 0) : r;
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 

@@ -123,7 +123,7 @@ def test_key_ranges(name, s):
     assert np.array_equal(got, oma.key_ranges(3, s, **mask))
 
 
-@pytest.mark.parametrize("s", [8191, 8192, 8193, 20000])
+@pytest.mark.parametrize("s", [8191, 8192, 8193, 20000, 32768, 32769, 70000])
 def test_key_ranges_over_several_tiles(s):
     ids = np.sort(np.random.default_rng(s).integers(0, 9, (2, s)).astype(np.int32), axis=1)
     ids[0, : s // 2] = 4                                  # one document over more than a tile

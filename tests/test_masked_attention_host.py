@@ -117,7 +117,7 @@ def test_rope_refusals(lib):
         return lib.tpmlp_qk_norm_rope_backward(FAKE, FAKE, FAKE, FAKE, 1e-5, FAKE, FAKE, None, 8, 64, 0, FAKE, FAKE, dq,
                                                FAKE, dgq, FAKE, b, 8, 4, 2, 64, *strides, BF16, ws, wsb, None)
     need = lib.tpmlp_qk_norm_rope_backward_workspace_size(1, 8, 64)
-    assert need == 8 * 2 * 64 * 4 and lib.tpmlp_qk_norm_rope_backward_workspace_size(0, 8, 64) == 0
+    assert need == 1024 * 64 * 4 and lib.tpmlp_qk_norm_rope_backward_workspace_size(0, 8, 64) == 0
     assert back(ws=None) == WORKSPACE and back(wsb=need - 1) == WORKSPACE and back(ws=FAKE + 8) == ALIGN
     assert back(dgq=None) == INVALID and back(dq=None) == INVALID
     assert back(strides=good + (256, 64, 64, 64)) == SHAPE
