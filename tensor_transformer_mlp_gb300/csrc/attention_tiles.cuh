@@ -56,6 +56,34 @@ __device__ __forceinline__ void umma_commit_by(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
+// mbar_wait by polling: for the issuing warp, whose reaction the tensor core waits for. (try_wait suspends the thread;
+// it was seen to return up to 400 cycles after the phase had completed.)
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, unsigned int* status, unsigned int where) {
+  const uint32_t a = smem_u32(bar);
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+      if (done()) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      record_timeout(status, where);
+      return false;
+    }
+  }
+}
+
 #define TPMLP_R8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
 
 // 32 lanes x 32 consecutive 32-bit columns: thread i of the warp writes lane (base + i).
@@ -137,14 +165,14 @@ __device__ __forceinline__ void issue_rows(uint32_t leader, uint32_t d_tmem, uin
     if (kk < ksteps) umma_bf16_by(leader, d_tmem, a + step_rows(kk), b + step_rows(kk), kIdesc, kk != 0);
 }
 
-// D (+)= A B with A's 128 columns packed in tensor memory from a_tmem (kSplit: columns 64.. from a_tmem + 64, else in a
-// row) and B a tile used MN-major.
-template <bool kSplit>
+// D (+)= A B over rows 16 * kFrom .. 16 * kTo - 1 of the tile B, which is used MN-major, with A's columns packed in
+// tensor memory from a_tmem (kSplit: columns 64.. from a_tmem + 64, else in a row).
+template <bool kSplit, int kFrom = 0, int kTo = kTile / 16>
 __device__ __forceinline__ void issue_cols(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_tile,
                                            uint32_t idesc, uint32_t accumulate) {
   const uint64_t b = desc_cols(b_tile);
 #pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk)
+  for (int kk = kFrom; kk < kTo; ++kk)
     umma_bf16_ta_by(leader, d_tmem, a_tmem + (kSplit ? (kk >> 2) * 64 + (kk & 3) * 8 : kk * 8), b + step_cols(kk), idesc,
                     kk == 0 ? accumulate : 1u);
 }

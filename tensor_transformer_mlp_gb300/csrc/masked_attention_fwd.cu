@@ -7,13 +7,17 @@
 // A CTA holds two tiles of 128 queries of one head and walks the key tiles that either of them sees:
 //   warps 0-3, 4-7  softmax of query tile 0 and 1, one row per thread (tensor-memory lane)
 //   warp 8          one thread loads Q once and K, V tiles through a ring (tensor copies)
-//   warp 9          one thread issues the products: S = Q K^T into 128 columns per query tile, and O += P V with P
-//                   read from tensor memory (bf16, over the columns of its S)
-// The two tiles take turns: while one's softmax runs, the tensor core works on the other's P V and next S. S of a
-// tile's next step is issued after its P V, and the tensor core runs in order, so P is never overwritten early and a
-// completed S also says that the P V before it is done: O may then be rescaled. That is done only when the maximum
+//   warp 9          issues the products: S = Q K^T into 128 columns per query tile, and O += P V with P read from
+//                   tensor memory (bf16, over the columns of its S)
+// The two tiles take turns: while one's softmax runs, the tensor core works on the other's P V and next S. (With an
+// issuing warp for each, both softmaxes fell into step and the tensor core waited for them.) S of a tile's next step
+// is issued after its P V, and the tensor core runs a thread's products in order, so P is never overwritten
+// early and a completed S also says that the P V before it is done: O may then be rescaled. That is done only when the maximum
 // grew by more than 2^8 (P then stays below 2^8 and l below 2^8 s, far inside fp32), so almost never: the statistics
-// stay those of one common m and the result does not depend on it.
+// stay those of one common m and the result does not depend on it. With heads of
+// more than 64 columns P is handed over in halves of 64 keys, so that its product starts while the second half's
+// exponents are still being taken.
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,10 +45,11 @@ struct FwdParams {
 };
 
 template <int HD>
-struct FwdSmem {
+struct FwdCfg {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr int kHalves = HD == 128 ? 2 : 1;  // parts in which P is handed over
   static constexpr int kBytes = 1024 + (2 + kStages) * kTileBytes + 512;
 };
 
@@ -55,15 +60,15 @@ struct Span {  // key tiles [lo, hi) of a query tile
 
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(const __grid_constant__ FwdParams p) {
-  using L = FwdSmem<HD>;
+  using L = FwdCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sq = smem;                                   // two Q tiles
   uint8_t* ring = smem + 2 * L::kTileBytes;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + L::kStages * L::kTileBytes);
   uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
+  uint64_t* p_full = s_full + 2;  // [query tile][part of P]
+  uint64_t* o_full = p_full + 4;
   uint64_t* kv_full = o_full + 2;
   uint64_t* kv_empty = kv_full + L::kStages;
   uint64_t* drain = kv_empty + L::kStages;
@@ -87,17 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
     if (lane == 0) warp_span[warp] = make_int2(lo, hi);
   } else if (warp == kSoftmaxWarps) {
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&q_full[i], 1);
-        mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], 4);
-        mbar_init(&o_full[i], 1);
-      }
-      for (int i = 0; i < L::kStages; ++i) {
-        mbar_init(&kv_full[i], 1);
-        mbar_init(&kv_empty[i], 1);
-      }
-      mbar_init(drain, 1);
+      for (uint64_t* bar = q_full; bar <= drain; ++bar)
+        mbar_init(bar, bar >= p_full && bar < p_full + 4 ? 4 : 1);
       fence_mbar_init();
       tma_prefetch_desc(&p.q.map);
       tma_prefetch_desc(&p.k.map);
@@ -162,59 +158,71 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       }
     } else if (warp == kSoftmaxWarps + 1) {
       // ---------------------------------------------------------------- products
+      // A wait that passes and a commit cost 100 to 150 cycles each, which the tensor core must not see: the tiles of
+      // the next step are waited for, and tiles released, between products, and S of tile 1 is followed at once by the
+      // wait for P of tile 0.
       const uint32_t leader = elect_one();
       const int ksteps = (p.head_dim + 15) / 16;
       const uint32_t idesc_o = idesc_bf16_f32(kTile, ksteps * 16, false, true);
       const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
       bool ok = true;
       auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
-        tc_fence_after();
+        if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
       };
-      auto wait_stage = [&](int n) {
-        wait_on(&kv_full[n % L::kStages], (n / L::kStages) & 1, 0x22);
-        return ring_addr + (n % L::kStages) * L::kTileBytes;
+      auto commit = [&](uint64_t* bar) { umma_commit_by(leader, bar); };
+      auto stage_of = [&](int n) { return ring_addr + (n % L::kStages) * L::kTileBytes; };
+      auto wait_tile = [&](int n) { wait_on(&kv_full[n % L::kStages], (n / L::kStages) & 1, 0x22); };
+      auto scores = [&](int i, int n) {  // with the K tile of step n
+        if (!ok) return;
+        issue_rows<HD>(leader, tmem + i * 128, q_addr + i * L::kTileBytes, stage_of(2 * n), ksteps);
+        commit(&s_full[i]);
       };
-      auto scores = [&](int i, uint32_t k_tile) {
-        issue_rows<HD>(leader, tmem + i * 128, q_addr + i * L::kTileBytes, k_tile, ksteps);
-        umma_commit_by(leader, &s_full[i]);
-      };
-      int j = next(j_begin), n = 0, steps[2] = {0, 0};
+      int j = next(j_begin), jn = next(j + 1), steps[2] = {0, 0};
       if (j < j_end) {
-        const uint32_t k_tile = wait_stage(0);
+        wait_tile(0);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (i ? any1 : any0) {
             wait_on(&q_full[i], 0, 0x23);
-            if (ok && span[i].has(j)) scores(i, k_tile);
+            tc_fence_after();
+            if (span[i].has(j)) scores(i, 0);
           }
-        if (ok) umma_commit_by(leader, &kv_empty[0]);
+        wait_tile(1);
       }
-      while (j < j_end && ok) {
-        const int jn = next(j + 1);
-        const uint32_t v_tile = wait_stage(2 * n + 1);
-        const uint32_t k_next = jn < j_end ? wait_stage(2 * n + 2) : 0;
+      for (int n = 0; j < j_end && ok; ++n) {  // V of step n has arrived
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (span[i].has(j)) {
-            wait_on(&p_full[i], steps[i] & 1, 0x24);
-            if (ok) {
-              issue_cols<false>(leader, tmem + 256 + i * 128, tmem + i * 128, v_tile, idesc_o, steps[i] != 0);
-              ++steps[i];
-              if (j + 1 == span[i].hi) umma_commit_by(leader, &o_full[i]);
+            const uint32_t to = tmem + 256 + i * 128, tp = tmem + i * 128;
+            wait_on(&p_full[2 * i], steps[i] & 1, 0x24);
+            tc_fence_after();
+            if (!ok) break;
+            issue_cols<false, 0, 8 / L::kHalves>(leader, to, tp, stage_of(2 * n + 1), idesc_o, steps[i] != 0);
+            if (i == 0) commit(&kv_empty[(2 * n) % L::kStages]);  // K of this step, used before this loop turn
+            if constexpr (L::kHalves == 2) {
+              wait_on(&p_full[2 * i + 1], steps[i] & 1, 0x24);
+              tc_fence_after();
+              if (!ok) break;
+              issue_cols<false, 4, 8>(leader, to, tp, stage_of(2 * n + 1), idesc_o, 1);
             }
+            ++steps[i];
+            if (j + 1 == span[i].hi) commit(&o_full[i]);
+          } else if (i == 0) {
+            commit(&kv_empty[(2 * n) % L::kStages]);
           }
-          if (ok && jn < j_end && span[i].has(jn)) scores(i, k_next);
+          if (i == 1) {
+            commit(&kv_empty[(2 * n + 1) % L::kStages]);
+            if (jn < j_end) wait_tile(2 * n + 3);
+          } else if (jn < j_end) {
+            wait_tile(2 * n + 2);
+          }
+          if (jn < j_end && span[i].has(jn)) scores(i, n + 1);
         }
-        if (ok) {
-          umma_commit_by(leader, &kv_empty[(2 * n + 1) % L::kStages]);
-          if (jn < j_end) umma_commit_by(leader, &kv_empty[(2 * n + 2) % L::kStages]);
-        }
-        ++n;
         j = jn;
+        jn = next(j + 1);
       }
       // every product issued must be done before tensor memory is freed
-      umma_commit_by(leader, drain);
+      commit(drain);
       mbar_wait(drain, 0, p.status, 0x25);
     }
   } else {
@@ -232,6 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], step & 1, p.status, 0x26));
       if (!ok) break;
       tc_fence_after();
+      auto hand_over = [&](int h) {  // part h of P is in tensor memory
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * i + h]);
+      };
       float y[128];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -298,13 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
           w[c] = pack_bf16x2(a, b);  // P enters its product in bf16: half a step, 2^-9 of each weight
         }
         tmem_st_32x32b_x32(ts + h * 32, w);
+        if (L::kHalves == 2 || h == 1) hand_over(h * (L::kHalves - 1));
       }
       const float2 su = f2_split(f2_add(sum0, sum1));
       l += su.x + su.y;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i]);
     }
     if (ok && mine.lo < mine.hi) {
       ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, p.status, 0x27));
@@ -353,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
 template <int HD, bool CAP, bool BIAS>
 cudaError_t launch(const FwdParams& p, int grid, cudaStream_t stream) {
   auto kernel = masked_attention_forward_kernel<HD, CAP, BIAS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdSmem<HD>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<HD>::kBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, FwdSmem<HD>::kBytes, stream>>>(p);
+  kernel<<<grid, kThreads, FwdCfg<HD>::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -381,7 +392,7 @@ cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream
   p.nblocks = static_cast<int>((a.s + 2 * kTile - 1) / (2 * kTile));
   p.bheads = static_cast<int>(a.b) * a.heads;
   p.status = ctx.status;
-  const int64_t grid = static_cast<int64_t>(p.nblocks) * a.b * a.heads;
+  const int64_t grid = static_cast<int64_t>(p.nblocks) * p.bheads;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const int g = static_cast<int>(grid);
   const bool wide = a.head_dim > 64, cap = a.softcap > 0.f, bias = a.slopes != nullptr;
