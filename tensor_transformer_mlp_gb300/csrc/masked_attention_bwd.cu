@@ -33,9 +33,8 @@ struct TileRange {
 };
 
 struct BwdParams {
-  HeadMap q, k, v, d_o;       // tiles to load
-  HeadView o, g;              // o and d_o, read by rows for D
-  HeadView dq, dk, dv;
+  HeadMap q, k, v, o, d_o;    // tiles to load
+  HeadMap dq, dk, dv;         // to store by 32 rows
   const int2* range;
   const float* slopes;
   const float* lse;           // [b][heads][s]
@@ -47,16 +46,17 @@ struct BwdParams {
   unsigned int* status;
 };
 
-template <int HD>
+// Ring depths. "held" tiles (K of the query pass, Q of the key pass) serve the scores of one step and the product of a
+// later one, "passing" tiles (V, d_o) two products in a row. The query pass keeps its own tiles in tensor memory and has
+// shared memory for more of them.
+template <int HD, bool QUERY_PASS>
 struct BwdSmem {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  // Ring depths. "held" tiles (K of the query pass, Q of the key pass) serve the scores of one step and the product
-  // of a later one, "passing" tiles (V, d_o) two products in a row.
-  static constexpr int kHeld = HD == 128 ? 3 : 4;
-  static constexpr int kPassing = HD == 128 ? 2 : 4;
+  static constexpr int kHeld = HD == 128 && !QUERY_PASS ? 3 : 4;
+  static constexpr int kPassing = HD == 128 ? (QUERY_PASS ? 3 : 2) : 4;
   static constexpr int kStatBytes = 2 * 2 * kTile * 4;
-  static constexpr int kTiles = 2 + kHeld + kPassing;
+  static constexpr int kTiles = (QUERY_PASS ? 0 : 2) + kHeld + kPassing;
   static constexpr int kBarrierBytes = 256;
   static constexpr int kBytes = kTiles * kTileBytes + kStatBytes + kBarrierBytes;  // 231,680 of 232,448 at HD = 128
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
@@ -64,18 +64,23 @@ struct BwdSmem {
 
 // ------------------------------------------------------------------ query pass
 
+// S and dP take their query-side operand from tensor memory, like dQ its dX: Q and d_o are the same for every key tile,
+// and with them in shared memory the two products would read all that it delivers (8 KB per 64 cycles each; 2600 cycles
+// a step against 1536 of the products). Tensor memory: S, dP / dX, dQ, 128 columns each, and Q and d_o packed in 64 each.
+// S of the next key tile is issued as soon as this one's has been read, so the exponents run beside dP and dQ.
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const __grid_constant__ BwdParams p) {
-  using L = BwdSmem<HD>;
+  using L = BwdSmem<HD, true>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sq = smem;
-  uint8_t* sg = sq + L::kTileBytes;
-  uint8_t* k_ring = sg + L::kTileBytes;
+  uint8_t* k_ring = smem;
   uint8_t* v_ring = k_ring + L::kHeld * L::kTileBytes;
-  float* part = reinterpret_cast<float*>(v_ring + L::kPassing * L::kTileBytes);  // [8 warps][32] halves of D, then spans
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(part + L::kStatBytes / 4);
+  float* dsum = reinterpret_cast<float*>(v_ring + L::kPassing * L::kTileBytes);  // D of the 128 rows, then spans
+  int4* warp_span = reinterpret_cast<int4*>(dsum + kTile);
+  uint64_t* in_full = reinterpret_cast<uint64_t*>(dsum + L::kStatBytes / 4);
+  uint64_t* q_full = in_full + 1;
   uint64_t* s_full = q_full + 1;
-  uint64_t* dp_full = s_full + 2;
+  uint64_t* s_free = s_full + 1;
+  uint64_t* dp_full = s_free + 1;
   uint64_t* ds_full = dp_full + 1;
   uint64_t* acc_full = ds_full + 1;
   uint64_t* k_full = acc_full + 1;
@@ -83,8 +88,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
   uint64_t* v_full = k_empty + L::kHeld;
   uint64_t* v_empty = v_full + L::kPassing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + L::kPassing);
-  int4* warp_span = reinterpret_cast<int4*>(part + 8 * 32);
-  static_assert((6 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 4 <= L::kBarrierBytes, "barrier area");
+  static_assert((7 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 4 <= L::kBarrierBytes, "barrier area");
+  // Q, d_o and o arrive in ring places that K and V tiles take later, from step 2 on
+  uint8_t* sq = k_ring + 2 * L::kTileBytes;
+  uint8_t* sg = k_ring + 3 * L::kTileBytes;
+  uint8_t* so = v_ring + 2 * L::kTileBytes;
+  static_assert(L::kHeld == 4 && L::kPassing >= 3, "places of Q, d_o and o");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bheads = p.heads * p.nseq;
@@ -100,43 +109,25 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
   int2 r = make_int2(0, 0);
   float lse2 = 0.f;
   if (warp < kWorkWarps) {
-    const bool in = row < p.s;
-    if (in) r = clip_range(p.range[base + row], p.s);
+    if (row < p.s) r = clip_range(p.range[base + row], p.s);
     const bool live = r.x < r.y;
     const int lo = __reduce_min_sync(0xffffffffu, live ? r.x : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, r.y);
     const int all_lo = __reduce_max_sync(0xffffffffu, live ? r.x : INT32_MAX);
     const int all_hi = __reduce_min_sync(0xffffffffu, r.y);
     if (lane == 0) warp_span[warp] = make_int4(lo, hi, all_lo, all_hi);
-    // D = d_o . o of the row, half of the head's columns per warpgroup
-    float d = 0.f;
-    if (live) {
-      lse2 = p.lse[stat_at + row] * kLog2e;
-      const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o.ptr) + (base + row) * p.o.ld + head * p.o.hs;
-      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.g.ptr) + (base + row) * p.g.ld + head * p.g.hs;
-#pragma unroll
-      for (int c = 0; c < HD / 2; c += 8) {
-        const int col = half * (HD / 2) + c;
-        if (col < p.head_dim) {
-          const uint4 x = *reinterpret_cast<const uint4*>(o + col), y = *reinterpret_cast<const uint4*>(g + col);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = unpack_bf16x2(xw[e]), b = unpack_bf16x2(yw[e]);
-            d = fmaf(a.x, b.x, d);
-            d = fmaf(a.y, b.y, d);
-          }
-        }
-      }
-    }
-    part[warp * 32 + lane] = d;
+    if (live) lse2 = p.lse[stat_at + row] * kLog2e;
   } else if (warp == kWorkWarps) {
     if (lane == 0) {
-      for (uint64_t* b = q_full; b < v_empty + L::kPassing; ++b) mbar_init(b, b == ds_full ? kWorkWarps : 1);
+      for (uint64_t* b = in_full; b < v_empty + L::kPassing; ++b)
+        mbar_init(b, b == q_full || b == s_free || b == ds_full ? kWorkWarps : 1);
       fence_mbar_init();
-      tma_prefetch_desc(&p.q.map);
+      mbar_arrive_expect_tx(in_full, 3 * L::kTileBytes);
+      load_head_tile(sq, p.q, in_full, L::kBoxes, q0, head, seq);
+      load_head_tile(sg, p.d_o, in_full, L::kBoxes, q0, head, seq);
+      load_head_tile(so, p.o, in_full, L::kBoxes, q0, head, seq);
       tma_prefetch_desc(&p.k.map);
       tma_prefetch_desc(&p.v.map);
-      tma_prefetch_desc(&p.d_o.map);
+      tma_prefetch_desc(&p.dq.map);
     }
   } else if (warp == kWorkWarps + 1) {
     tmem_alloc(tmem_slot, 512);
@@ -146,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
+  const uint32_t t_dp = tmem + 128, t_dq = tmem + 256, t_q = tmem + 384, t_g = tmem + 448;
   TileRange t{INT32_MAX, 0, 0, INT32_MAX};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
@@ -159,15 +150,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
 
   if (warp >= kWorkWarps) {
     regs_dec<kRegsIssue>();
-    if (warp == kWorkWarps && lane == 0 && steps > 0) {
+    if (warp == kWorkWarps && lane == 0) {
       // ---------------------------------------------------------------- loads
-      mbar_arrive_expect_tx(q_full, 2 * L::kTileBytes);
-      load_head_tile(sq, p.q, q_full, L::kBoxes, q0, head, seq);
-      load_head_tile(sg, p.d_o, q_full, L::kBoxes, q0, head, seq);
       int n = 0;
       bool ok = true;
       for (; n < steps; ++n) {
         const int ks = n % L::kHeld, vs = n % L::kPassing;
+        if (n == 2) ok = mbar_wait(q_full, 0, p.status, 0x2F);  // Q, d_o and o have been read
+        if (!ok) break;
         ok = mbar_wait(&k_empty[ks], ((n / L::kHeld) & 1) ^ 1, p.status, 0x30);
         if (!ok) break;
         mbar_arrive_expect_tx(&k_full[ks], L::kTileBytes);
@@ -178,7 +168,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         load_head_tile(v_ring + vs * L::kTileBytes, p.v, &v_full[vs], L::kBoxes, (j0 + n) * kTile, kvh, seq);
       }
       if (!ok) {  // the copies in flight must land before shared memory goes away
-        mbar_wait(q_full, 0, p.status, 0x32);
         for (int k = max(0, n + 1 - L::kHeld); k <= n; ++k) mbar_wait(&k_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x32);
         for (int k = max(0, n - L::kPassing); k < n; ++k) mbar_wait(&v_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x32);
       }
@@ -187,36 +176,38 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       const uint32_t leader = elect_one();
       const int ksteps = (p.head_dim + 15) / 16;
       const uint32_t idesc_q = idesc_bf16_f32(kTile, ksteps * 16, false, true);
-      const uint32_t q_addr = smem_u32(sq), g_addr = smem_u32(sg), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
+      const uint32_t k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
       bool ok = true;
       auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
         tc_fence_after();
       };
       auto scores = [&](int n) {  // S(n) = Q K(n)^T
         wait_on(&k_full[n % L::kHeld], (n / L::kHeld) & 1, 0x34);
         if (!ok) return;
-        issue_rows<HD>(leader, tmem + (n & 1) * 128, q_addr, k_addr + (n % L::kHeld) * L::kTileBytes, ksteps);
-        umma_commit_by(leader, &s_full[n & 1]);
+        issue_rows_ta<HD>(leader, tmem, t_q, k_addr + (n % L::kHeld) * L::kTileBytes, ksteps);
+        umma_commit_by(leader, s_full);
       };
       auto dprobs = [&](int n) {  // dP(n) = d_o V(n)^T
         wait_on(&v_full[n % L::kPassing], (n / L::kPassing) & 1, 0x35);
         if (!ok) return;
-        issue_rows<HD>(leader, t_dp, g_addr, v_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
+        issue_rows_ta<HD>(leader, t_dp, t_g, v_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
         umma_commit_by(leader, dp_full);
         umma_commit_by(leader, &v_empty[n % L::kPassing]);
       };
       wait_on(q_full, 0, 0x33);
       scores(0);
       dprobs(0);
-      if (steps > 1) scores(1);
       for (int n = 0; n < steps && ok; ++n) {
+        if (n + 1 < steps) {
+          wait_on(s_free, n & 1, 0x36);
+          scores(n + 1);
+        }
         wait_on(ds_full, n & 1, 0x36);
         if (!ok) break;
         issue_cols<true>(leader, t_dq, t_dp, k_addr + (n % L::kHeld) * L::kTileBytes, idesc_q, n != 0);
-        umma_commit_by(leader, &k_empty[n % L::kHeld]);
         if (n + 1 < steps) dprobs(n + 1);
-        if (n + 2 < steps) scores(n + 2);
+        umma_commit_by(leader, &k_empty[n % L::kHeld]);
       }
       umma_commit_by(leader, acc_full);  // also: every product issued is done before tensor memory is freed
       mbar_wait(acc_full, 0, p.status, 0x37);
@@ -225,20 +216,59 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
     // ------------------------------------------------------------------ P, dX
     regs_inc<kRegsWork>();
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float D = part[(warp & 3) * 32 + lane] + part[((warp & 3) + 4) * 32 + lane];
-    if (half == 0 && row < p.s) p.dsum[stat_at + row] = D;
     const float slope2 = BIAS ? p.slopes[head] * kLog2e : 0.f;
+    {
+      // The row of Q (warps 0-3) or d_o (warps 4-7) goes to tensor memory; warps 4-7 also form D = d_o . o.
+      const bool here = __all_sync(0xffffffffu, mbar_wait(in_full, 0, p.status, 0x3B));
+      uint32_t x[HD / 2];
+      const int rr = (warp & 3) * 32 + lane;
+      float d = 0.f;
+#pragma unroll
+      for (int c = 0; c < HD / 8; ++c) {
+        const int at = (c >> 3) * kBoxBytes;
+        const uint4 v = here ? *box_chunk((half ? sg : sq) + at, rr, c & 7) : make_uint4(0, 0, 0, 0);
+        x[4 * c] = v.x;
+        x[4 * c + 1] = v.y;
+        x[4 * c + 2] = v.z;
+        x[4 * c + 3] = v.w;
+        if (half) {
+          const uint4 u = *box_chunk(so + at, rr, c & 7);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = unpack_bf16x2(w[e]), b = unpack_bf16x2(x[4 * c + e]);
+            d = fmaf(a.x, b.x, d);
+            d = fmaf(a.y, b.y, d);
+          }
+        }
+      }
+      if (half) {
+        if (r.x >= r.y) d = 0.f;  // o is zero there; d_o may be anything
+        dsum[rr] = d;
+        if (row < p.s) p.dsum[stat_at + row] = d;
+      }
+      for (int c = 0; c < HD / 64; ++c)
+        tmem_st_32x32b_x32((half ? t_g : t_q) + lanes + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
+      tmem_st_wait();
+      tc_fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // D, among the eight warps
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    const float D = dsum[(warp & 3) * 32 + lane];
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (n >> 1) & 1, p.status, 0x38));
+      ok = __all_sync(0xffffffffu, mbar_wait(s_full, n & 1, p.status, 0x38));
       if (!ok) break;
       tc_fence_after();
       const int k0 = (j0 + n) * kTile + half * 64;
       float w[64];  // P, times the cap's derivative
-      const uint32_t ts = tmem + lanes + (n & 1) * 128 + half * 64;
+      const uint32_t ts = tmem + lanes + half * 64;
       tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
       tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
       tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free);
       const float d0 = static_cast<float>(k0 - row);
 #pragma unroll
       for (int c = 0; c < 64; ++c) {
@@ -280,25 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       tc_fence_after();
     }
     if (ok) {
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dq.ptr) + (base + row) * p.dq.ld + head * p.dq.hs;
-      for (int c = half * (HD / 2); c < (half + 1) * (HD / 2) && c < p.head_dim; c += 32) {
-        uint32_t v[32] = {};
-        if (steps > 0) {
-          tmem_ld_32x32b_x32(t_dq + lanes + c, v);
-          tmem_ld_wait();
-        }
-        if (row < p.s) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e >= p.head_dim) break;
-            uint32_t u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              u[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * p.scale, __uint_as_float(v[e + 2 * i + 1]) * p.scale);
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        }
-      }
+      // K's first tiles make room; warps 4-7 take the second 64 columns
+      if (half < L::kBoxes)
+        store_head_rows(k_ring, p.dq, t_dq + lanes, p.scale, steps > 0, warp & 3, lane, half, half + 1, q0, head, seq, p.s,
+                        p.head_dim);
     }
   }
   tc_fence_before();
@@ -348,7 +363,7 @@ struct QueryTiles {
 
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const __grid_constant__ BwdParams p) {
-  using L = BwdSmem<HD>;
+  using L = BwdSmem<HD, false>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sk = smem;
   uint8_t* sv = sk + L::kTileBytes;
@@ -585,28 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     }
     if (ok) {
       // warps 0-3 write dV, warps 4-7 dK, a key's row per thread
-      const HeadView& view = half ? p.dk : p.dv;
-      const float f = half ? p.scale : 1.0f;
-      const uint32_t acc = (half ? t_dk : t_dv) + lanes;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(view.ptr) + (base + key) * view.ld + kvh * view.hs;
-      for (int c = 0; c < p.head_dim; c += 32) {
-        uint32_t v[32] = {};
-        if (n > 0) {
-          tmem_ld_32x32b_x32(acc + c, v);
-          tmem_ld_wait();
-        }
-        if (key < p.s) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e >= p.head_dim) break;
-            uint32_t u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              u[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * f, __uint_as_float(v[e + 2 * i + 1]) * f);
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        }
-      }
+      store_head_rows(half ? sk : sv, half ? p.dk : p.dv, (half ? t_dk : t_dv) + lanes, half ? p.scale : 1.0f, n > 0,
+                      warp & 3, lane, 0, L::kBoxes, k0, kvh, seq, p.s, p.head_dim);
     }
   }
   tc_fence_before();
@@ -624,14 +619,14 @@ cudaError_t launch(const BwdParams& p, cudaStream_t stream) {
   auto dkv = masked_attention_dkv_kernel<HD, CAP, BIAS>;
   const int64_t q_grid = static_cast<int64_t>(p.ntiles) * p.nseq * p.heads, k_grid = q_grid / p.group;
   if (q_grid > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD, true>::kBytes);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD>::kBytes);
+  e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD, false>::kBytes);
   if (e != cudaSuccess) return e;
-  dq<<<static_cast<int>(q_grid), kThreads, BwdSmem<HD>::kBytes, stream>>>(p);
+  dq<<<static_cast<int>(q_grid), kThreads, BwdSmem<HD, true>::kBytes, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dkv<<<static_cast<int>(k_grid), kThreads, BwdSmem<HD>::kBytes, stream>>>(p);
+  dkv<<<static_cast<int>(k_grid), kThreads, BwdSmem<HD, false>::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -647,17 +642,17 @@ cudaError_t launch_masked_attention_backward(const MaskedAttention& a, const Hea
                                              const HeadView& dk, const HeadView& dv, void* workspace, cudaStream_t stream,
                                              const DeviceCtx& ctx) {
   BwdParams p{};
-  const HeadView* views[4] = {&a.q, &a.k, &a.v, &d_o};
-  HeadMap* maps[4] = {&p.q, &p.k, &p.v, &p.d_o};
-  for (int i = 0; i < 4; ++i) {
-    cudaError_t e = make_head_map(maps[i], *views[i], a.b, a.s, i == 0 || i == 3 ? a.heads : a.kv_heads, a.head_dim);
+  const struct {
+    HeadMap* map;
+    const HeadView* view;
+    int heads, rows;
+  } maps[] = {{&p.q, &a.q, a.heads, kTile}, {&p.k, &a.k, a.kv_heads, kTile}, {&p.v, &a.v, a.kv_heads, kTile},
+              {&p.o, &a.o, a.heads, kTile}, {&p.d_o, &d_o, a.heads, kTile},  {&p.dq, &dq, a.heads, 32},
+              {&p.dk, &dk, a.kv_heads, 32}, {&p.dv, &dv, a.kv_heads, 32}};
+  for (const auto& m : maps) {
+    cudaError_t e = make_head_map(m.map, *m.view, a.b, a.s, m.heads, a.head_dim, m.rows);
     if (e != cudaSuccess) return e;
   }
-  p.o = a.o;
-  p.g = d_o;
-  p.dq = dq;
-  p.dk = dk;
-  p.dv = dv;
   p.range = a.range;
   p.slopes = a.slopes;
   p.lse = a.lse;

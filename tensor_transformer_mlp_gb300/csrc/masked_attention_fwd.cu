@@ -34,8 +34,7 @@ constexpr int kRegsSoftmax = 208, kRegsIssue = 88;
 constexpr float kRescaleAt = 8.0f;
 
 struct FwdParams {
-  HeadMap q, k, v;
-  HeadView o;
+  HeadMap q, k, v, o;
   const int2* range;
   const float* slopes;
   float* lse;
@@ -95,9 +94,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       for (uint64_t* bar = q_full; bar <= drain; ++bar)
         mbar_init(bar, bar >= p_full && bar < p_full + 4 ? 4 : 1);
       fence_mbar_init();
-      tma_prefetch_desc(&p.q.map);
+      for (int i = 0; i < 2; ++i)
+        if (q0 + i * kTile < p.s) {  // on their way while the ranges are read; q_full is waited for whatever they are
+          mbar_arrive_expect_tx(&q_full[i], L::kTileBytes);
+          load_head_tile(sq + i * L::kTileBytes, p.q, &q_full[i], L::kBoxes, q0 + i * kTile, head, seq);
+        }
       tma_prefetch_desc(&p.k.map);
       tma_prefetch_desc(&p.v.map);
+      tma_prefetch_desc(&p.o.map);
     }
   } else if (warp == kSoftmaxWarps + 1) {
     tmem_alloc(tmem_slot, 512);
@@ -133,11 +137,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       // ---------------------------------------------------------------- loads
       bool ok = true;
       int n = 0;
-      for (int i = 0; i < 2; ++i)
-        if (i ? any1 : any0) {
-          mbar_arrive_expect_tx(&q_full[i], L::kTileBytes);
-          load_head_tile(sq + i * L::kTileBytes, p.q, &q_full[i], L::kBoxes, q0 + i * kTile, head, seq);
-        }
       for (int j = next(j_begin); j < j_end && ok; j = next(j + 1)) {
         for (int kv = 0; kv < 2; ++kv, ++n) {
           const int st = n % L::kStages;
@@ -151,8 +150,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       }
       // The copies in flight must land before shared memory goes away (those that the products wait for have).
       if (!ok) {
-        for (int i = 0; i < 2; ++i)
-          if (i ? any1 : any0) mbar_wait(&q_full[i], 0, p.status, 0x21);
         for (int k = max(0, n - L::kStages); k < n; ++k)
           mbar_wait(&kv_full[k % L::kStages], (k / L::kStages) & 1, p.status, 0x21);
       }
@@ -321,31 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, p.status, 0x27));
       tc_fence_after();
     }
+    // Q's place in shared memory takes the tile's output; Q has been loaded, if only for that.
+    if (q0 + i * kTile < p.s && !__all_sync(0xffffffffu, mbar_wait(&q_full[i], 0, p.status, 0x28))) ok = false;
     if (ok) {
       const bool live = l > 0.f;
-      const float inv = live ? 1.0f / l : 0.f;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o.ptr) + (base + row) * p.o.ld + head * p.o.hs;
-      for (int c = 0; c < p.head_dim; c += 32) {
-        uint32_t o[32] = {};
-        if (mine.lo < mine.hi) {
-          tmem_ld_32x32b_x32(to + c, o);
-          tmem_ld_wait();
-        }
-        if (row < p.s) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e >= p.head_dim) break;
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float a = live ? __uint_as_float(o[e + 2 * x]) * inv : 0.f;
-              const float b = live ? __uint_as_float(o[e + 2 * x + 1]) * inv : 0.f;
-              w[x] = pack_bf16x2(a, b);
-            }
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
+      store_head_rows(sq + i * L::kTileBytes, p.o, to, live ? 1.0f / l : 0.f, live, warp & 3, lane, 0, L::kBoxes,
+                      q0 + i * kTile, head, seq, p.s, p.head_dim);
       if (row < p.s) {
         constexpr float kLn2 = 0.6931471805599453f;
         p.lse[(static_cast<int64_t>(seq) * p.heads + head) * p.s + row] = live ? kLn2 * (m + log2f(l)) : -INFINITY;
@@ -380,7 +358,8 @@ cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream
     cudaError_t e = make_head_map(maps[i], *views[i], a.b, a.s, i ? a.kv_heads : a.heads, a.head_dim);
     if (e != cudaSuccess) return e;
   }
-  p.o = a.o;
+  cudaError_t e = make_head_map(&p.o, a.o, a.b, a.s, a.heads, a.head_dim, 32);
+  if (e != cudaSuccess) return e;
   p.range = a.range;
   p.slopes = a.slopes;
   p.lse = a.lse;
