@@ -244,17 +244,26 @@ __device__ __forceinline__ int2 clip_range(int2 r, int s) {
   return r.x < r.y ? r : make_int2(0, 0);
 }
 
-// Scores in base 2: y log2(e) as a function of q.k. With a cap, cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2x/cap))),
-// whose absolute error, a few 2^-24 of the cap, is what the exponent sees (tanh.approx's 2^-11 would not do).
+// What makes a score of q.k, in base 2 (y log2(e)).
 struct ScoreParams {
-  float scale2;   // scale * log2(e); with a cap: 2 scale log2(e) / cap
-  float cap2;     // cap * log2(e)
+  float scale2;          // scale * log2(e)
+  float in_cap;          // scale / cap: x = q.k in_cap is the cap's argument
+  float in_cap2;         // 2 log2(e) scale / cap: e^(2x) = 2^(q.k in_cap2)
+  float cap2;            // cap * log2(e)
+  float small;           // |q.k| up to which |x| <= 1/2
 };
 
 inline ScoreParams score_params(float scale, float softcap) {
   const double log2e = 1.4426950408889634;
-  return softcap > 0.f ? ScoreParams{static_cast<float>(2.0 * scale * log2e / softcap), static_cast<float>(softcap * log2e)}
-                       : ScoreParams{static_cast<float>(scale * log2e), 0.f};
+  ScoreParams p{};
+  p.scale2 = static_cast<float>(scale * log2e);
+  if (softcap > 0.f) {
+    p.in_cap = static_cast<float>(static_cast<double>(scale) / softcap);
+    p.in_cap2 = static_cast<float>(2.0 * scale * log2e / softcap);
+    p.cap2 = static_cast<float>(softcap * log2e);
+    p.small = static_cast<float>(0.5 * softcap / scale);
+  }
+  return p;
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -263,9 +272,79 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// 1 / (1 + e^(2x/cap)) = (1 - tanh(x / cap)) / 2 of a raw score.
-__device__ __forceinline__ float cap_sigma(float qk, const ScoreParams& p) {
-  return rcp_approx(1.0f + ex2_approx(qk * p.scale2));
+// tanh(x) of the cap's argument in two ways, both off by a few 2^-24 in absolute terms, which the cap multiplies into the
+// exponent (tanh.approx's 2^-11 would not do). Any x: 1 - 2 / (1 + e^(2x)), two special-function operations. |x| <= 1/2:
+// x times a polynomial of degree 3 in x^2, fitted to tanh(x) / x for the smallest largest error of the product,
+// 1.3e-7 = 2.1 * 2^-24; on pairs, six operations of the FMA pipe for two scores.
+__device__ __forceinline__ float cap_tanh(float qk, const ScoreParams& p) {
+  return fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(qk * p.in_cap2)), 1.0f);
+}
+__device__ __forceinline__ F2 cap_tanh_small(F2 qk, const ScoreParams& p) {
+  auto both = [](float v) { return f2_make(v, v); };
+  const F2 x = f2_mul(qk, both(p.in_cap)), z = f2_mul(x, x);
+  const F2 r = f2_fma(f2_fma(f2_fma(both(-0.04337248f), z, both(0.13145145f)), z, both(-0.33320655f)), z, both(0.99999768f));
+  return f2_mul(x, r);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// tanh of N capped scores in place. The special-function unit, with an exponent of every score to take besides, is what
+// bounds the first way (masked rows of 4096, 32 heads of 128: forward 387 us); a warp whose scores are all small takes
+// the polynomial (306 us; with two of every eight pairs left to the first way 357 us).
+template <int N>
+__device__ __forceinline__ void cap_tanh_all(float (&y)[N], const ScoreParams& p) {
+  float m[4] = {};
+#pragma unroll
+  for (int c = 0; c < N; c += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = max3(m[e], fabsf(y[c + 2 * e]), fabsf(y[c + 2 * e + 1]));
+  if (__all_sync(0xffffffffu, max3(fmaxf(m[0], m[1]), m[2], m[3]) <= p.small)) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float2 v = f2_split(cap_tanh_small(f2_make(y[c], y[c + 1]), p));
+      y[c] = v.x;
+      y[c + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) y[c] = cap_tanh(y[c], p);
+  }
+}
+
+// y <- a y - slope2 |d0 + c| for N columns c, d0 the first column's place less the row's (or the other way round). A
+// warp whose rows all lie on one side of its columns takes the bias as a line.
+template <int N>
+__device__ __forceinline__ void add_bias(float (&y)[N], float a, float slope2, float d0, int side) {
+  if (side != 0) {
+    const float k = side > 0 ? -slope2 : slope2, off = k * d0;
+#pragma unroll
+    for (int c = 0; c < N; ++c) y[c] = fmaf(y[c], a, fmaf(k, static_cast<float>(c), off));
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) y[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), y[c] * a);
+  }
+}
+
+// 1 if columns [col0, col0 + n) all lie at or behind the warp's rows [row0, row0 + 32), -1 if at or before them, else 0.
+__device__ __forceinline__ int side_of(int col0, int n, int row0) {
+  return col0 >= row0 + 31 ? 1 : col0 + n - 1 <= row0 ? -1 : 0;
+}
+
+// Bit b of the result in lane i is bit i of lane b's word.
+__device__ __forceinline__ unsigned transpose_bits(unsigned x) {
+  const int lane = threadIdx.x & 31;
+  constexpr unsigned kKeep[5] = {0x0000ffffu, 0x00ff00ffu, 0x0f0f0f0fu, 0x33333333u, 0x55555555u};
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int o = 16 >> i;
+    const unsigned y = __shfl_xor_sync(0xffffffffu, x, o);
+    x = lane & o ? (x & ~kKeep[i]) | ((y & ~kKeep[i]) >> o) : (x & kKeep[i]) | ((y & kKeep[i]) << o);
+  }
+  return x;
 }
 
 }  // namespace tpmlp

@@ -62,6 +62,49 @@ struct BwdSmem {
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
+
+// 64 scores q.k to probabilities in place: 2^(y + shift(c)) for columns c, c + 1 (the pair of -lse in base 2). done(c, a,
+// b) may change a pair and sees it before the cap's derivative is multiplied in.
+template <bool CAP, bool BIAS, typename Shift, typename Done>
+__device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,
+                                              int row0, Shift shift, Done done) {
+  float t[CAP ? 64 : 1];  // tanh
+  if constexpr (CAP) {
+    cap_tanh_all(w, sp);
+#pragma unroll
+    for (int c = 0; c < 64; ++c) t[c] = w[c];
+  }
+  const float unit = BIAS ? 1.0f : CAP ? sp.cap2 : sp.scale2;
+  if constexpr (BIAS)
+    add_bias(w, CAP ? sp.cap2 : sp.scale2, slope2, static_cast<float>(col0 - row), side_of(col0, 64, row0));
+  const F2 u2 = f2_make(unit, unit);
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    const F2 v = f2_make(w[c], w[c + 1]), s = shift(c);
+    const float2 z = f2_split(BIAS ? f2_add(v, s) : f2_fma(v, u2, s));
+    float a = ex2_approx(z.x), b = ex2_approx(z.y);
+    done(c, a, b);
+    if constexpr (CAP) {
+      const F2 tt = f2_make(t[c], t[c + 1]), ab = f2_make(a, b);
+      const float2 m = f2_split(f2_sub(ab, f2_mul(ab, f2_mul(tt, tt))));  // times 1 - t^2
+      w[c] = m.x;
+      w[c + 1] = m.y;
+    } else {
+      w[c] = a;
+      w[c + 1] = b;
+    }
+  }
+}
+template <bool CAP, bool BIAS, typename Shift>
+__device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,
+                                              int row0, Shift shift) {
+  probabilities<CAP, BIAS>(w, sp, slope2, col0, row, row0, shift, [](int, float&, float&) {});
+}
+
 // ------------------------------------------------------------------ query pass
 
 // S and dP take their query-side operand from tensor memory, like dQ its dX: Q and d_o are the same for every key tile,
@@ -269,15 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_free);
-      const float d0 = static_cast<float>(k0 - row);
-#pragma unroll
-      for (int c = 0; c < 64; ++c) {
-        const float sg2 = CAP ? cap_sigma(w[c], p.sp) : 0.f;
-        float y = CAP ? fmaf(-2.0f * p.sp.cap2, sg2, p.sp.cap2) - lse2 : fmaf(w[c], p.sp.scale2, -lse2);
-        if (BIAS) y = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), y);
-        w[c] = ex2_approx(y);
-        if (CAP) w[c] *= 4.0f * sg2 * (1.0f - sg2);
-      }
+      probabilities<CAP, BIAS>(w, p.sp, slope2, k0, row, row - lane, [&](int) { return f2_make(-lse2, -lse2); });
       if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + 64 <= r.y)) {
         const int c0 = r.x - k0;
         const unsigned width = static_cast<unsigned>(r.y - r.x);
@@ -369,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   uint8_t* sv = sk + L::kTileBytes;
   uint8_t* q_ring = sv + L::kTileBytes;
   uint8_t* g_ring = q_ring + L::kHeld * L::kTileBytes;
-  float* stats = reinterpret_cast<float*>(g_ring + L::kPassing * L::kTileBytes);  // two of {lse2[128], D[128]}
+  float* stats = reinterpret_cast<float*>(g_ring + L::kPassing * L::kTileBytes);  // two of {-lse log2(e) [128], D[128]}
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + L::kStatBytes / 4);
   uint64_t* s_full = kv_full + 1;
   uint64_t* p_full = s_full + 1;
@@ -501,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         float l[4], d[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          l[e] = q + e < p.s ? p.lse[at + e] * kLog2e : 0.f;
+          l[e] = q + e < p.s ? -p.lse[at + e] * kLog2e : 0.f;  // queries without keys: +inf, and masked
           d[e] = q + e < p.s ? p.dsum[at + e] : 0.f;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&st_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status, 0x49))) break;
@@ -525,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, n & 1, p.status, 0x4B));
       if (!ok) break;
       tc_fence_after();
-      const float4* lse2 = reinterpret_cast<const float4*>(stats + (n & 1) * 2 * kTile + half * 64);
+      const float2* lse2 = reinterpret_cast<const float2*>(stats + (n & 1) * 2 * kTile + half * 64);
       const float4* dd = reinterpret_cast<const float4*>(stats + (n & 1) * 2 * kTile + kTile + half * 64);
       const int q0 = it.tile * kTile + half * 64;
       const float slope2 = BIAS ? p.slopes[it.head] * kLog2e : 0.f;
@@ -534,33 +569,35 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
       tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
       tmem_ld_wait();
-      unsigned long long seen = ~0ull;  // which of the 64 queries see this key
-      if (!it.full) {
-        seen = 0;
-#pragma unroll 16
-        for (int c = 0; c < 64; ++c) {
-          const int2 r = q0 + c < p.s ? p.range[base + q0 + c] : make_int2(0, 0);
-          seen |= static_cast<unsigned long long>(r.x <= key && key < r.y) << c;
-        }
-      }
-      const float d0 = static_cast<float>(q0 - key);
+      // P as it is, packed in x, and times the cap's derivative in w
       uint32_t x[32];
-#pragma unroll
-      for (int c4 = 0; c4 < 16; ++c4) {
-        const float4 l4 = lse2[c4];
-        const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = c4 * 4 + e;
-          const float sg2 = CAP ? cap_sigma(w[c], p.sp) : 0.f;
-          float y = CAP ? fmaf(-2.0f * p.sp.cap2, sg2, p.sp.cap2) - l[e] : fmaf(w[c], p.sp.scale2, -l[e]);
-          if (BIAS) y = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), y);
-          pr[e] = (seen >> c) & 1 ? ex2_approx(y) : 0.f;
-          w[c] = CAP ? pr[e] * (4.0f * sg2 * (1.0f - sg2)) : pr[e];
-        }
-        x[2 * c4] = pack_bf16x2(pr[0], pr[1]);
-        x[2 * c4 + 1] = pack_bf16x2(pr[2], pr[3]);
+      auto pack_seen = [&](auto masked, unsigned lo, unsigned hi) {
+        probabilities<CAP, BIAS>(
+            w, p.sp, slope2, q0, key, key - lane,
+            [&](int c) {
+              const float2 l = lse2[c / 2];
+              return f2_make(l.x, l.y);
+            },
+            [&](int c, float& a, float& b) {
+              if constexpr (decltype(masked)::value) {
+                const unsigned bits = c < 32 ? lo : hi;
+                a = (bits >> (c & 31)) & 1 ? a : 0.f;
+                b = (bits >> ((c & 31) + 1)) & 1 ? b : 0.f;
+              }
+              x[c / 2] = pack_bf16x2(a, b);  // P enters its product in bf16: half a step of each weight
+            });
+      };
+      if (it.full) {
+        pack_seen(Flag<false>{}, 0, 0);
+      } else {
+        // Each lane marks which of the warp's 32 keys two queries see; transposed, which queries see its own key.
+        auto mark = [&](int q) {
+          const int2 r = q < p.s ? clip_range(p.range[base + q], p.s) : make_int2(0, 0);
+          const int from = min(max(r.x - (key - lane), 0), 32), to = min(max(r.y - (key - lane), 0), 32);
+          return from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+        };
+        const unsigned lo = transpose_bits(mark(q0 + lane)), hi = transpose_bits(mark(q0 + 32 + lane));
+        pack_seen(Flag<true>{}, lo, hi);
       }
       tmem_st_32x32b_x32(ts, x);
       tmem_st_wait();

@@ -249,33 +249,23 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         tmem_ld_32x32b_x32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(y) + c * 32));
       tmem_ld_wait();
       const int k0 = j * kTile;
-      if constexpr (CAP) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c) y[c] = fmaf(-2.0f * p.sp.cap2, cap_sigma(y[c], p.sp), p.sp.cap2);
-      }
-      if constexpr (BIAS) {
-        const float d0 = static_cast<float>(k0 - row);
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          y[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), CAP ? y[c] : y[c] * p.sp.scale2);
-      }
+      if constexpr (CAP) cap_tanh_all(y, p.sp);
+      if constexpr (BIAS)
+        add_bias(y, CAP ? p.sp.cap2 : p.sp.scale2, slope2, static_cast<float>(k0 - row), side_of(k0, kTile, row - lane));
       if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + kTile <= r.y)) {
         const int c0 = r.x - k0;
         const unsigned width = static_cast<unsigned>(r.y - r.x);
 #pragma unroll
         for (int c = 0; c < 128; ++c) y[c] = static_cast<unsigned>(c - c0) < width ? y[c] : -INFINITY;
       }
-      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+      float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; c += 4) {
-        t0 = fmaxf(t0, y[c]);
-        t1 = fmaxf(t1, y[c + 1]);
-        t2 = fmaxf(t2, y[c + 2]);
-        t3 = fmaxf(t3, y[c + 3]);
-      }
-      float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
-      constexpr bool kScaled = CAP || BIAS;  // y is in base 2 already
-      if (!kScaled) top *= p.sp.scale2;
+      for (int c = 0; c < 128; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = max3(t[e], y[c + 2 * e], y[c + 2 * e + 1]);
+      float top = max3(fmaxf(t[0], t[1]), t[2], t[3]);
+      const float unit = BIAS ? 1.0f : CAP ? p.sp.cap2 : p.sp.scale2;  // what brings y to base 2
+      top *= unit;
       const bool grow = top > m + kRescaleAt || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xffffffffu, grow)) {
         const float m2 = grow ? top : m;
@@ -294,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         }
       }
       const float shift = m == -INFINITY ? 0.f : -m;
-      const F2 sc = f2_make(kScaled ? 1.0f : p.sp.scale2, kScaled ? 1.0f : p.sp.scale2), sh = f2_make(shift, shift);
+      const F2 sc = f2_make(unit, unit), sh = f2_make(shift, shift);
       F2 sum0 = f2_make(0.f, 0.f), sum1 = sum0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -302,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           const F2 v = f2_make(y[h * 64 + 2 * c], y[h * 64 + 2 * c + 1]);
-          const float2 z = f2_split(kScaled ? f2_add(v, sh) : f2_fma(v, sc, sh));
+          const float2 z = f2_split(BIAS ? f2_add(v, sh) : f2_fma(v, sc, sh));
           const float a = ex2_approx(z.x), b = ex2_approx(z.y);
           if (c & 1) sum1 = f2_add(sum1, f2_make(a, b));
           else sum0 = f2_add(sum0, f2_make(a, b));
