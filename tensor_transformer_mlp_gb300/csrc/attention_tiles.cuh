@@ -118,6 +118,36 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ------------------------------------------------------------------ work
+
+// A kernel's grid has a CTA for every piece of work, but a running CTA takes over the pieces of CTAs that have not
+// started (cluster launch control) until none is left, so that a piece's loads begin while the one before it is being
+// finished and tensor memory is set up once. One thread asks, for its CTA: returns the piece (a blockIdx.x) or -1, and
+// must not ask again after -1. `response` is 16-byte aligned, `bar` an mbarrier of count 1 for this alone.
+__device__ __forceinline__ int take_work(uint4* response, uint64_t* bar, uint32_t parity, unsigned int* status,
+                                         unsigned int where) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(response)),
+      "r"(smem_u32(bar))
+      : "memory");
+  if (!mbar_wait(bar, parity, status, where)) return -1;
+  uint32_t taken, first;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=r"(taken), "=r"(first)
+      : "r"(smem_u32(response))
+      : "memory");
+  fence_proxy_async_smem();  // the response is read before the next one may be written
+  return taken ? static_cast<int>(first) : -1;
+}
+
 // ------------------------------------------------------------------ tiles of heads
 
 // Tensor map of one tensor of heads, with the coordinate slots of token, head and sequence.
@@ -152,6 +182,9 @@ __device__ __forceinline__ void load_head_tile(void* dst, const HeadMap& m, uint
 // The 16 bytes of columns 8 c .. 8 c + 7 (c < 8) of row r in a box.
 __device__ __forceinline__ uint4* box_chunk(uint8_t* box, int r, int c) {
   return reinterpret_cast<uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ const uint4* box_chunk(const uint8_t* box, int r, int c) {
+  return reinterpret_cast<const uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4));
 }
 
 // Writes 32 rows of an accumulator to a tensor of heads: warp `w` of a tile's four takes lanes 32 w .. 32 w + 31, row
@@ -192,6 +225,41 @@ __device__ __forceinline__ void store_head_rows(uint8_t* tile, const HeadMap& m,
       tma_store_4d(&m.map, tile + x * kBoxBytes + w * 32 * 128, x * 64, c1, c2, c3);
     bulk_commit_group();
     bulk_wait_group_read<0>();
+  }
+}
+
+// The same one box at a time through a warp's own 4 KB. Returns once the accumulator has been read; the copies may still
+// read `stage` (a later call waits, and so must the warp's lane 0 before it ends: bulk_wait_group_read<0>).
+__device__ __forceinline__ void store_head_rows_staged(uint8_t* stage, const HeadMap& m, uint32_t acc, float f, bool live,
+                                                       int w, int lane, int box0, int box1, int row0, int head, int seq,
+                                                       int s, int head_dim) {
+  const int row = row0 + w * 32;
+  for (int x = box0; x < box1 && x * 64 < head_dim; ++x) {
+    uint32_t v[64];
+    tmem_ld_32x32b_x32(acc + x * 64, *reinterpret_cast<uint32_t(*)[32]>(v));
+    tmem_ld_32x32b_x32(acc + x * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = __uint_as_float(v[8 * e + 2 * i]) * f, b = __uint_as_float(v[8 * e + 2 * i + 1]) * f;
+        u[i] = live ? pack_bf16x2(a, b) : 0u;
+      }
+      *box_chunk(stage, lane, e) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row < s) {
+      const int c1 = m.row == 1 ? row : (m.head == 1 ? head : seq);
+      const int c2 = m.row == 2 ? row : (m.head == 2 ? head : seq);
+      const int c3 = m.row == 3 ? row : (m.head == 3 ? head : seq);
+      tma_store_4d(&m.map, stage, x * 64, c1, c2, c3);
+      bulk_commit_group();
+    }
   }
 }
 

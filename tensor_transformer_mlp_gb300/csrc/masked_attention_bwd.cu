@@ -12,8 +12,10 @@
 // memory only ever holds tiles as they lie in global memory. Warp roles in both:
 //   warps 0-7   one row of the accumulators per thread, columns 0-63 (warps 0-3) or 64-127 (warps 4-7)
 //   warp 8      tensor copies of the tiles through two rings
-//   warp 9      one thread issues the products
-//   warp 10     (key pass) the queries' lse and D, two tiles ahead
+//   warp 9      issues the products
+//   warp 10     takes the CTA's next piece of work (a tile of queries, or of keys) and, in the query pass, finds the key
+//               tiles that it sees
+//   warp 11     (key pass) the queries' lse and D, two tiles ahead
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,6 +26,7 @@ namespace {
 
 constexpr int kWorkWarps = 8;
 constexpr int kThreads = (kWorkWarps + 4) * 32;
+constexpr int kTakeAhead = 2;  // a CTA takes its next tile of queries when this many key tiles are left to load
 constexpr int kRegsWork = 208, kRegsIssue = 88;  // 2 * 208 + 88 = 3 * 168, the registers at launch
 
 // Summary of a tile of 128 queries: the keys that some row sees lie in [lo, hi), and every row of the tile sees the
@@ -47,19 +50,20 @@ struct BwdParams {
 };
 
 // Ring depths. "held" tiles (K of the query pass, Q of the key pass) serve the scores of one step and the product of a
-// later one, "passing" tiles (V, d_o) two products in a row. The query pass keeps its own tiles in tensor memory and has
-// shared memory for more of them.
+// later one, "passing" tiles (V, d_o) two products in a row. In the query pass the tile's own Q and d_o come through the
+// first ring and its o through the second, on their way to tensor memory; the key pass keeps its K and V beside the rings.
 template <int HD, bool QUERY_PASS>
 struct BwdSmem {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kHeld = HD == 128 && !QUERY_PASS ? 3 : 4;
-  static constexpr int kPassing = HD == 128 ? (QUERY_PASS ? 3 : 2) : 4;
+  static constexpr int kPassing = HD == 128 ? 2 : 4;
   static constexpr int kStatBytes = 2 * 2 * kTile * 4;
+  static constexpr int kStageBytes = QUERY_PASS ? 32 * 128 : 0;  // of output, per working warp
   static constexpr int kTiles = (QUERY_PASS ? 0 : 2) + kHeld + kPassing;
-  static constexpr int kBarrierBytes = 256;
-  static constexpr int kBytes = kTiles * kTileBytes + kStatBytes + kBarrierBytes;  // 231,680 of 232,448 at HD = 128
-  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+  static constexpr int kBarrierBytes = 320;
+  static constexpr int kBytes = kTiles * kTileBytes + kWorkWarps * kStageBytes + kStatBytes + kBarrierBytes;
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");  // 231,744 of 232,448 at HD = 128
 };
 
 template <bool V>
@@ -111,65 +115,68 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
 // and with them in shared memory the two products would read all that it delivers (8 KB per 64 cycles each; 2600 cycles
 // a step against 1536 of the products). Tensor memory: S, dP / dX, dQ, 128 columns each, and Q and d_o packed in 64 each.
 // S of the next key tile is issued as soon as this one's has been read, so the exponents run beside dP and dQ.
+struct QueryWork {
+  int piece;      // -1: none left
+  int j0, steps;  // its key tiles
+};
+
+// Under a causal mask the tiles with the most keys, the last, come first.
+struct QueryPlace {
+  int tile, q0, seq, head, kvh;
+  int64_t base, stat;  // the sequence's first token, and where the head's lse and D start
+  __device__ __forceinline__ QueryPlace(const BwdParams& p, int piece) {
+    const int bheads = p.heads * p.nseq, bh = piece % bheads;
+    tile = p.ntiles - 1 - piece / bheads;
+    seq = bh / p.heads;
+    head = bh - seq * p.heads;
+    kvh = head / p.group;
+    q0 = tile * kTile;
+    base = static_cast<int64_t>(seq) * p.s;
+    stat = (static_cast<int64_t>(seq) * p.heads + head) * p.s;
+  }
+};
+
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = BwdSmem<HD, true>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* k_ring = smem;
   uint8_t* v_ring = k_ring + L::kHeld * L::kTileBytes;
-  float* dsum = reinterpret_cast<float*>(v_ring + L::kPassing * L::kTileBytes);  // D of the 128 rows, then spans
-  int4* warp_span = reinterpret_cast<int4*>(dsum + kTile);
-  uint64_t* in_full = reinterpret_cast<uint64_t*>(dsum + L::kStatBytes / 4);
-  uint64_t* q_full = in_full + 1;
+  uint8_t* staging = v_ring + L::kPassing * L::kTileBytes;
+  float* dsum = reinterpret_cast<float*>(staging + kWorkWarps * L::kStageBytes);  // D of the tile's rows
+  uint4* response = reinterpret_cast<uint4*>(dsum + L::kStatBytes / 4);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(response + 1);
   uint64_t* s_full = q_full + 1;
   uint64_t* s_free = s_full + 1;
   uint64_t* dp_full = s_free + 1;
   uint64_t* ds_full = dp_full + 1;
   uint64_t* acc_full = ds_full + 1;
-  uint64_t* k_full = acc_full + 1;
+  uint64_t* work_full = acc_full + 1;
+  uint64_t* work_empty = work_full + 2;
+  uint64_t* ending = work_empty + 2;
+  uint64_t* taken = ending + 1;
+  uint64_t* drain = taken + 1;
+  uint64_t* k_full = drain + 1;
   uint64_t* k_empty = k_full + L::kHeld;
   uint64_t* v_full = k_empty + L::kHeld;
   uint64_t* v_empty = v_full + L::kPassing;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + L::kPassing);
-  static_assert((7 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 4 <= L::kBarrierBytes, "barrier area");
-  // Q, d_o and o arrive in ring places that K and V tiles take later, from step 2 on
-  uint8_t* sq = k_ring + 2 * L::kTileBytes;
-  uint8_t* sg = k_ring + 3 * L::kTileBytes;
-  uint8_t* so = v_ring + 2 * L::kTileBytes;
-  static_assert(L::kHeld == 4 && L::kPassing >= 3, "places of Q, d_o and o");
+  QueryWork* works = reinterpret_cast<QueryWork*>(v_empty + L::kPassing);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(works + 2);
+  static_assert(16 + (13 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 2 * sizeof(QueryWork) + 4 <= L::kBarrierBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bheads = p.heads * p.nseq;
-  const int tile = p.ntiles - 1 - static_cast<int>(blockIdx.x) / bheads;  // under a causal mask the longest first
-  const int bh = static_cast<int>(blockIdx.x) % bheads;
-  const int seq = bh / p.heads, head = bh - seq * p.heads, kvh = head / p.group;
-  const int q0 = tile * kTile;
-  const int64_t base = static_cast<int64_t>(seq) * p.s;
-  const int row = q0 + (warp & 3) * 32 + lane;
-  const int half = (warp >> 2) & 1;
-  const int64_t stat_at = (static_cast<int64_t>(seq) * p.heads + head) * p.s;
-
-  int2 r = make_int2(0, 0);
-  float lse2 = 0.f;
-  if (warp < kWorkWarps) {
-    if (row < p.s) r = clip_range(p.range[base + row], p.s);
-    const bool live = r.x < r.y;
-    const int lo = __reduce_min_sync(0xffffffffu, live ? r.x : INT32_MAX), hi = __reduce_max_sync(0xffffffffu, r.y);
-    const int all_lo = __reduce_max_sync(0xffffffffu, live ? r.x : INT32_MAX);
-    const int all_hi = __reduce_min_sync(0xffffffffu, r.y);
-    if (lane == 0) warp_span[warp] = make_int4(lo, hi, all_lo, all_hi);
-    if (live) lse2 = p.lse[stat_at + row] * kLog2e;
-  } else if (warp == kWorkWarps) {
+  if (warp == kWorkWarps) {
     if (lane == 0) {
-      for (uint64_t* b = in_full; b < v_empty + L::kPassing; ++b)
-        mbar_init(b, b == q_full || b == s_free || b == ds_full ? kWorkWarps : 1);
+      for (uint64_t* b = q_full; b < v_empty + L::kPassing; ++b)
+        mbar_init(b, b == q_full || b == s_free || b == ds_full    ? kWorkWarps
+                     : b >= work_empty && b < work_empty + 2 ? kWorkWarps + 1
+                                                             : 1);
       fence_mbar_init();
-      mbar_arrive_expect_tx(in_full, 3 * L::kTileBytes);
-      load_head_tile(sq, p.q, in_full, L::kBoxes, q0, head, seq);
-      load_head_tile(sg, p.d_o, in_full, L::kBoxes, q0, head, seq);
-      load_head_tile(so, p.o, in_full, L::kBoxes, q0, head, seq);
+      tma_prefetch_desc(&p.q.map);
       tma_prefetch_desc(&p.k.map);
       tma_prefetch_desc(&p.v.map);
+      tma_prefetch_desc(&p.o.map);
+      tma_prefetch_desc(&p.d_o.map);
       tma_prefetch_desc(&p.dq.map);
     }
   } else if (warp == kWorkWarps + 1) {
@@ -181,40 +188,50 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_dp = tmem + 128, t_dq = tmem + 256, t_q = tmem + 384, t_g = tmem + 448;
-  TileRange t{INT32_MAX, 0, 0, INT32_MAX};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const int4 v = warp_span[w];
-    t = TileRange{min(t.lo, v.x), max(t.hi, v.y), max(t.all_lo, v.z), min(t.all_hi, v.w)};
-  }
-  const bool any = t.hi > 0;
-  const int j0 = any ? t.lo / kTile : 0, steps = any ? (t.hi + kTile - 1) / kTile - j0 : 0;
-  if (head == 0 && threadIdx.x == 0) p.tiles[static_cast<int64_t>(seq) * p.ntiles + tile] = t;
+  auto work_of = [&](int it) {  // the CTA's it-th piece
+    QueryWork w{-1, 0, 0};
+    if (mbar_wait(&work_full[it & 1], (it >> 1) & 1, p.status, 0x2E)) w = works[it & 1];
+    return w;
+  };
 
   if (warp >= kWorkWarps) {
     regs_dec<kRegsIssue>();
     if (warp == kWorkWarps && lane == 0) {
       // ---------------------------------------------------------------- loads
-      int n = 0;
+      int kn = 0, vn = 0;  // tiles loaded through the two rings
       bool ok = true;
-      for (; n < steps; ++n) {
-        const int ks = n % L::kHeld, vs = n % L::kPassing;
-        if (n == 2) ok = mbar_wait(q_full, 0, p.status, 0x2F);  // Q, d_o and o have been read
-        if (!ok) break;
-        ok = mbar_wait(&k_empty[ks], ((n / L::kHeld) & 1) ^ 1, p.status, 0x30);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&k_full[ks], L::kTileBytes);
-        load_head_tile(k_ring + ks * L::kTileBytes, p.k, &k_full[ks], L::kBoxes, (j0 + n) * kTile, kvh, seq);
-        ok = mbar_wait(&v_empty[vs], ((n / L::kPassing) & 1) ^ 1, p.status, 0x31);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&v_full[vs], L::kTileBytes);
-        load_head_tile(v_ring + vs * L::kTileBytes, p.v, &v_full[vs], L::kBoxes, (j0 + n) * kTile, kvh, seq);
+      auto load = [&](bool held, const HeadMap& m, int row, int head, int seq) {
+        const int st = held ? kn % L::kHeld : vn % L::kPassing;
+        uint64_t* full = held ? &k_full[st] : &v_full[st];
+        if (ok) ok = held ? mbar_wait(&k_empty[st], ((kn / L::kHeld) & 1) ^ 1, p.status, 0x30)
+                          : mbar_wait(&v_empty[st], ((vn / L::kPassing) & 1) ^ 1, p.status, 0x31);
+        if (!ok) return;
+        mbar_arrive_expect_tx(full, L::kTileBytes);
+        load_head_tile((held ? k_ring : v_ring) + st * L::kTileBytes, m, full, L::kBoxes, row, head, seq);
+        ++(held ? kn : vn);
+      };
+      for (int it = 0; ok; ++it) {
+        const QueryWork w = work_of(it);
+        if (w.piece < 0) break;
+        const QueryPlace at(p, w.piece);
+        if (w.steps > 0) {
+          load(true, p.q, at.q0, at.head, at.seq);
+          load(true, p.d_o, at.q0, at.head, at.seq);
+          load(false, p.o, at.q0, at.head, at.seq);
+        }
+        for (int n = 0; n < w.steps && ok; ++n) {
+          if (n == max(0, w.steps - kTakeAhead)) mbar_arrive(ending);
+          load(true, p.k, (w.j0 + n) * kTile, at.kvh, at.seq);
+          load(false, p.v, (w.j0 + n) * kTile, at.kvh, at.seq);
+        }
+        if (w.steps == 0) mbar_arrive(ending);
       }
       if (!ok) {  // the copies in flight must land before shared memory goes away
-        for (int k = max(0, n + 1 - L::kHeld); k <= n; ++k) mbar_wait(&k_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x32);
-        for (int k = max(0, n - L::kPassing); k < n; ++k) mbar_wait(&v_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x32);
+        for (int k = max(0, kn - L::kHeld); k < kn; ++k) mbar_wait(&k_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x32);
+        for (int k = max(0, vn - L::kPassing); k < vn; ++k)
+          mbar_wait(&v_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x32);
       }
-    } else if (warp == kWorkWarps + 1 && steps > 0) {
+    } else if (warp == kWorkWarps + 1) {
       // ---------------------------------------------------------------- products
       const uint32_t leader = elect_one();
       const int ksteps = (p.head_dim + 15) / 16;
@@ -225,131 +242,226 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
         tc_fence_after();
       };
-      auto scores = [&](int n) {  // S(n) = Q K(n)^T
-        wait_on(&k_full[n % L::kHeld], (n / L::kHeld) & 1, 0x34);
+      auto scores = [&](int k) {  // S = Q K^T with the ring's k-th tile
+        wait_on(&k_full[k % L::kHeld], (k / L::kHeld) & 1, 0x34);
         if (!ok) return;
-        issue_rows_ta<HD>(leader, tmem, t_q, k_addr + (n % L::kHeld) * L::kTileBytes, ksteps);
+        issue_rows_ta<HD>(leader, tmem, t_q, k_addr + (k % L::kHeld) * L::kTileBytes, ksteps);
         umma_commit_by(leader, s_full);
       };
-      auto dprobs = [&](int n) {  // dP(n) = d_o V(n)^T
-        wait_on(&v_full[n % L::kPassing], (n / L::kPassing) & 1, 0x35);
+      auto dprobs = [&](int v) {  // dP = d_o V^T with the ring's v-th tile
+        wait_on(&v_full[v % L::kPassing], (v / L::kPassing) & 1, 0x35);
         if (!ok) return;
-        issue_rows_ta<HD>(leader, t_dp, t_g, v_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
+        issue_rows_ta<HD>(leader, t_dp, t_g, v_addr + (v % L::kPassing) * L::kTileBytes, ksteps);
         umma_commit_by(leader, dp_full);
-        umma_commit_by(leader, &v_empty[n % L::kPassing]);
+        umma_commit_by(leader, &v_empty[v % L::kPassing]);
       };
-      wait_on(q_full, 0, 0x33);
-      scores(0);
-      dprobs(0);
-      for (int n = 0; n < steps && ok; ++n) {
-        if (n + 1 < steps) {
-          wait_on(s_free, n & 1, 0x36);
-          scores(n + 1);
+      int kn = 0, vn = 0, step = 0, pieces = 0;  // ring tiles, steps and pieces so far
+      for (int it = 0; ok; ++it) {
+        const QueryWork w = work_of(it);
+        if (__any_sync(0xffffffffu, w.piece < 0)) break;
+        if (w.steps > 0) {
+          kn += 2;  // Q, d_o
+          vn += 1;  // o
+          wait_on(q_full, pieces & 1, 0x33);
+          scores(kn);
+          dprobs(vn);
+          for (int n = 0; n < w.steps && ok; ++n, ++step) {
+            const bool more = n + 1 < w.steps;
+            if (more) {
+              wait_on(s_free, step & 1, 0x36);
+              scores(kn + n + 1);
+            }
+            wait_on(ds_full, step & 1, 0x36);
+            if (!ok) break;
+            issue_cols<true>(leader, t_dq, t_dp, k_addr + ((kn + n) % L::kHeld) * L::kTileBytes, idesc_q, n != 0);
+            if (!more) umma_commit_by(leader, acc_full);
+            if (more) dprobs(vn + n + 1);
+            umma_commit_by(leader, &k_empty[(kn + n) % L::kHeld]);
+          }
+          // the last step's S has been read too, which nobody waits for otherwise
+          if (ok) wait_on(s_free, (step - 1) & 1, 0x36);
+          kn += w.steps;
+          vn += w.steps;
+          ++pieces;
         }
-        wait_on(ds_full, n & 1, 0x36);
-        if (!ok) break;
-        issue_cols<true>(leader, t_dq, t_dp, k_addr + (n % L::kHeld) * L::kTileBytes, idesc_q, n != 0);
-        if (n + 1 < steps) dprobs(n + 1);
-        umma_commit_by(leader, &k_empty[n % L::kHeld]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&work_empty[it & 1]);
       }
-      umma_commit_by(leader, acc_full);  // also: every product issued is done before tensor memory is freed
-      mbar_wait(acc_full, 0, p.status, 0x37);
+      umma_commit_by(leader, drain);  // every product issued is done before tensor memory is freed
+      mbar_wait(drain, 0, p.status, 0x37);
+    } else if (warp == kWorkWarps + 2) {
+      // ---------------------------------------------------------------- work
+      int piece = static_cast<int>(blockIdx.x);
+      for (int it = 0;; ++it) {
+        QueryWork w{piece, 0, 0};
+        if (piece >= 0) {
+          const QueryPlace at(p, piece);
+          TileRange t{INT32_MAX, 0, 0, INT32_MAX};
+#pragma unroll
+          for (int k = 0; k < kTile; k += 32) {
+            const int row = at.q0 + k + lane;
+            const int2 r = row < p.s ? clip_range(p.range[at.base + row], p.s) : make_int2(0, 0);
+            const int lo = r.x < r.y ? r.x : INT32_MAX;
+            t = TileRange{min(t.lo, lo), max(t.hi, r.y), max(t.all_lo, lo), min(t.all_hi, r.y)};
+          }
+          t = TileRange{__reduce_min_sync(0xffffffffu, t.lo), __reduce_max_sync(0xffffffffu, t.hi),
+                        __reduce_max_sync(0xffffffffu, t.all_lo), __reduce_min_sync(0xffffffffu, t.all_hi)};
+          if (t.hi > 0) {
+            w.j0 = t.lo / kTile;
+            w.steps = (t.hi + kTile - 1) / kTile - w.j0;
+          }
+          if (at.head == 0 && lane == 0) p.tiles[static_cast<int64_t>(at.seq) * p.ntiles + at.tile] = t;
+        }
+        if (lane == 0) {
+          works[it & 1] = w;
+          mbar_arrive(&work_full[it & 1]);
+        }
+        if (piece < 0) break;
+        // The next piece is taken when this one nears its end (taken at its start, it would wait behind a long piece
+        // while other CTAs ran out of work), in the place in `works` of the one before, which is done with then.
+        int next = -1;
+        if (lane == 0 && mbar_wait(ending, it & 1, p.status, 0x2D) &&
+            (it == 0 || mbar_wait(&work_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, 0x2D)))
+          next = take_work(response, taken, it & 1, p.status, 0x2C);
+        piece = __shfl_sync(0xffffffffu, next, 0);
+      }
     }
   } else {
     // ------------------------------------------------------------------ P, dX
     regs_inc<kRegsWork>();
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float slope2 = BIAS ? p.slopes[head] * kLog2e : 0.f;
-    {
-      // The row of Q (warps 0-3) or d_o (warps 4-7) goes to tensor memory; warps 4-7 also form D = d_o . o.
-      const bool here = __all_sync(0xffffffffu, mbar_wait(in_full, 0, p.status, 0x3B));
-      uint32_t x[HD / 2];
-      const int rr = (warp & 3) * 32 + lane;
-      float d = 0.f;
+    const int half = warp >> 2, rr = (warp & 3) * 32 + lane;
+    uint8_t* stage = staging + warp * L::kStageBytes;
+    auto range_of = [&](const QueryWork& w, float* lse2) {  // the row's keys and lse
+      *lse2 = 0.f;
+      if (w.piece < 0) return make_int2(0, 0);
+      const QueryPlace at(p, w.piece);
+      if (at.q0 + rr >= p.s) return make_int2(0, 0);
+      *lse2 = p.lse[at.stat + at.q0 + rr];
+      return p.range[at.base + at.q0 + rr];
+    };
+    bool ok = true;
+    int kn = 0, vn = 0, step = 0, pieces = 0;  // as the products count them
+    QueryWork w = work_of(0);
+    float lse_next;
+    int2 r_next = range_of(w, &lse_next);
+    for (int it = 0; __all_sync(0xffffffffu, ok && w.piece >= 0); ++it) {
+      const QueryPlace at(p, w.piece);
+      const int row = at.q0 + rr, steps = w.steps, j0 = w.j0;
+      const int2 r = clip_range(r_next, p.s);
+      const bool live = r.x < r.y;
+      const float lse2 = live ? lse_next * kLog2e : 0.f;
+      const float slope2 = BIAS ? p.slopes[at.head] * kLog2e : 0.f;
+      float D = 0.f;
+      if (steps > 0) {
+        // The row of Q (warps 0-3) or d_o (warps 4-7) goes to tensor memory; warps 4-7 also form D = d_o . o.
+        const int mine = kn + half, os = vn % L::kPassing;
+        ok = mbar_wait(&k_full[mine % L::kHeld], (mine / L::kHeld) & 1, p.status, 0x3B);
+        if (half) ok = ok && mbar_wait(&v_full[os], (vn / L::kPassing) & 1, p.status, 0x3B);
+        const bool here = __all_sync(0xffffffffu, ok);
+        const uint8_t* src = k_ring + (mine % L::kHeld) * L::kTileBytes;
+        const uint8_t* so = v_ring + os * L::kTileBytes;
+        uint32_t x[HD / 2];
 #pragma unroll
-      for (int c = 0; c < HD / 8; ++c) {
-        const int at = (c >> 3) * kBoxBytes;
-        const uint4 v = here ? *box_chunk((half ? sg : sq) + at, rr, c & 7) : make_uint4(0, 0, 0, 0);
-        x[4 * c] = v.x;
-        x[4 * c + 1] = v.y;
-        x[4 * c + 2] = v.z;
-        x[4 * c + 3] = v.w;
-        if (half) {
-          const uint4 u = *box_chunk(so + at, rr, c & 7);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int c = 0; c < HD / 8; ++c) {
+          const int box = (c >> 3) * kBoxBytes;
+          const uint4 v = here ? *box_chunk(src + box, rr, c & 7) : make_uint4(0, 0, 0, 0);
+          x[4 * c] = v.x;
+          x[4 * c + 1] = v.y;
+          x[4 * c + 2] = v.z;
+          x[4 * c + 3] = v.w;
+          if (half) {
+            const uint4 u = *box_chunk(so + box, rr, c & 7);
+            const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = unpack_bf16x2(w[e]), b = unpack_bf16x2(x[4 * c + e]);
-            d = fmaf(a.x, b.x, d);
-            d = fmaf(a.y, b.y, d);
+            for (int e = 0; e < 4; ++e) {
+              const float2 a = unpack_bf16x2(uw[e]), b = unpack_bf16x2(x[4 * c + e]);
+              D = fmaf(a.x, b.x, D);
+              D = fmaf(a.y, b.y, D);
+            }
           }
         }
+        if (half) {
+          if (!live) D = 0.f;  // o is zero there; d_o may be anything
+          dsum[rr] = D;
+          if (row < p.s) p.dsum[at.stat + row] = D;
+        }
+        for (int c = 0; c < HD / 64; ++c)
+          tmem_st_32x32b_x32((half ? t_g : t_q) + lanes + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
+        tmem_st_wait();
+        tc_fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // all rows read, D written
+        if (lane == 0) {
+          mbar_arrive(q_full);
+          if (warp == 0) {
+            mbar_arrive(&k_empty[kn % L::kHeld]);
+            mbar_arrive(&k_empty[(kn + 1) % L::kHeld]);
+            mbar_arrive(&v_empty[os]);
+          }
+        }
+        D = dsum[rr];
+        kn += 2 + steps;
+        vn += 1 + steps;
       }
-      if (half) {
-        if (r.x >= r.y) d = 0.f;  // o is zero there; d_o may be anything
-        dsum[rr] = d;
-        if (row < p.s) p.dsum[stat_at + row] = d;
-      }
-      for (int c = 0; c < HD / 64; ++c)
-        tmem_st_32x32b_x32((half ? t_g : t_q) + lanes + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
-      tmem_st_wait();
-      tc_fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // D, among the eight warps
-      if (lane == 0) mbar_arrive(q_full);
-    }
-    const float D = dsum[(warp & 3) * 32 + lane];
-    bool ok = true;
-    for (int n = 0; n < steps; ++n) {
-      ok = __all_sync(0xffffffffu, mbar_wait(s_full, n & 1, p.status, 0x38));
-      if (!ok) break;
-      tc_fence_after();
-      const int k0 = (j0 + n) * kTile + half * 64;
-      float w[64];  // P, times the cap's derivative
-      const uint32_t ts = tmem + lanes + half * 64;
-      tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
-      tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_free);
-      probabilities<CAP, BIAS>(w, p.sp, slope2, k0, row, row - lane, [&](int) { return f2_make(-lse2, -lse2); });
-      if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + 64 <= r.y)) {
-        const int c0 = r.x - k0;
-        const unsigned width = static_cast<unsigned>(r.y - r.x);
+      for (int n = 0; n < steps && ok; ++n, ++step) {
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full, step & 1, p.status, 0x38));
+        if (!ok) break;
+        tc_fence_after();
+        const int k0 = (j0 + n) * kTile + half * 64;
+        float w[64];  // P, times the cap's derivative
+        const uint32_t ts = tmem + lanes + half * 64;
+        tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
+        tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
+        probabilities<CAP, BIAS>(w, p.sp, slope2, k0, row, row - lane, [&](int) { return f2_make(-lse2, -lse2); });
+        if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + 64 <= r.y)) {
+          const int c0 = r.x - k0;
+          const unsigned width = static_cast<unsigned>(r.y - r.x);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) w[c] = static_cast<unsigned>(c - c0) < width ? w[c] : 0.f;
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, n & 1, p.status, 0x39));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t dp[64], x[32];
-      const uint32_t td = t_dp + lanes + half * 64;
-      tmem_ld_32x32b_x32(td, *reinterpret_cast<uint32_t(*)[32]>(dp));
-      tmem_ld_32x32b_x32(td + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
-      tmem_ld_wait();
-      const F2 d2 = f2_make(D, D);
+          for (int c = 0; c < 64; ++c) w[c] = static_cast<unsigned>(c - c0) < width ? w[c] : 0.f;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, step & 1, p.status, 0x39));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dp[64], x[32];
+        const uint32_t td = t_dp + lanes + half * 64;
+        tmem_ld_32x32b_x32(td, *reinterpret_cast<uint32_t(*)[32]>(dp));
+        tmem_ld_32x32b_x32(td + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+        tmem_ld_wait();
+        const F2 d2 = f2_make(D, D);
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const F2 g2 = f2_sub(f2_make(__uint_as_float(dp[2 * c]), __uint_as_float(dp[2 * c + 1])), d2);
-        const float2 z = f2_split(f2_mul(f2_make(w[2 * c], w[2 * c + 1]), g2));
-        x[c] = pack_bf16x2(z.x, z.y);  // dX / scale enters its product in bf16: half a step of each term
+        for (int c = 0; c < 32; ++c) {
+          const F2 g2 = f2_sub(f2_make(__uint_as_float(dp[2 * c]), __uint_as_float(dp[2 * c + 1])), d2);
+          const float2 z = f2_split(f2_mul(f2_make(w[2 * c], w[2 * c + 1]), g2));
+          x[c] = pack_bf16x2(z.x, z.y);  // dX / scale enters its product in bf16: half a step of each term
+        }
+        tmem_st_32x32b_x32(td, x);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
       }
-      tmem_st_32x32b_x32(td, x);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      if (!ok) break;
+      w = work_of(it + 1);
+      r_next = range_of(w, &lse_next);  // on its way during the output
+      if (steps > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, pieces & 1, p.status, 0x3A));
+        tc_fence_after();
+        ++pieces;
+      }
+      if (ok) {
+        if (half < L::kBoxes)  // warps 4-7 take the second 64 columns
+          store_head_rows_staged(stage, p.dq, t_dq + lanes, p.scale, steps > 0, warp & 3, lane, half, half + 1, at.q0, at.head,
+                          at.seq, p.s, p.head_dim);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&work_empty[it & 1]);
+      }
     }
-    if (ok && steps > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.status, 0x3A));
-      tc_fence_after();
-    }
-    if (ok) {
-      // K's first tiles make room; warps 4-7 take the second 64 columns
-      if (half < L::kBoxes)
-        store_head_rows(k_ring, p.dq, t_dq + lanes, p.scale, steps > 0, warp & 3, lane, half, half + 1, q0, head, seq, p.s,
-                        p.head_dim);
-    }
+    if (lane == 0) bulk_wait_group_read<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -396,6 +508,23 @@ struct QueryTiles {
   }
 };
 
+// Under a causal mask the first keys have the most queries and come first.
+struct KeyPlace {
+  int k0, seq, kvh;
+  int64_t base;
+  __device__ __forceinline__ KeyPlace(const BwdParams& p, int piece) {
+    const int bheads = p.kv_heads * p.nseq, bh = piece % bheads;
+    k0 = piece / bheads * kTile;
+    seq = bh / p.kv_heads;
+    kvh = bh - seq * p.kv_heads;
+    base = static_cast<int64_t>(seq) * p.s;
+  }
+  __device__ __forceinline__ QueryTiles queries(const BwdParams& p) const {
+    return QueryTiles(p.tiles + static_cast<int64_t>(seq) * p.ntiles, p.ntiles, k0, min(k0 + kTile, p.s), kvh * p.group,
+                      p.group);
+  }
+};
+
 template <int HD, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const __grid_constant__ BwdParams p) {
   using L = BwdSmem<HD, false>;
@@ -405,39 +534,43 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   uint8_t* q_ring = sv + L::kTileBytes;
   uint8_t* g_ring = q_ring + L::kHeld * L::kTileBytes;
   float* stats = reinterpret_cast<float*>(g_ring + L::kPassing * L::kTileBytes);  // two of {-lse log2(e) [128], D[128]}
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + L::kStatBytes / 4);
-  uint64_t* s_full = kv_full + 1;
+  uint4* response = reinterpret_cast<uint4*>(stats + L::kStatBytes / 4);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(response + 1);
+  uint64_t* kv_empty = kv_full + 1;
+  uint64_t* s_full = kv_empty + 1;
   uint64_t* p_full = s_full + 1;
   uint64_t* dp_full = p_full + 1;
   uint64_t* ds_full = dp_full + 1;
   uint64_t* acc_full = ds_full + 1;
   uint64_t* st_full = acc_full + 1;
   uint64_t* st_empty = st_full + 2;
-  uint64_t* q_full = st_empty + 2;
+  uint64_t* work_full = st_empty + 2;
+  uint64_t* work_empty = work_full + 2;
+  uint64_t* ending = work_empty + 2;
+  uint64_t* taken = ending + 1;
+  uint64_t* drain = taken + 1;
+  uint64_t* q_full = drain + 1;
   uint64_t* q_empty = q_full + L::kHeld;
   uint64_t* g_full = q_empty + L::kHeld;
   uint64_t* g_empty = g_full + L::kPassing;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g_empty + L::kPassing);
-  static_assert((10 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 4 <= L::kBarrierBytes, "barrier area");
+  int* works = reinterpret_cast<int*>(g_empty + L::kPassing);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(works + 2);
+  static_assert(16 + (18 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 8 + 4 <= L::kBarrierBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bheads = p.kv_heads * p.nseq;
-  const int tile = static_cast<int>(blockIdx.x) / bheads;  // under a causal mask the first keys have the most queries
-  const int bh = static_cast<int>(blockIdx.x) % bheads;
-  const int seq = bh / p.kv_heads, kvh = bh - seq * p.kv_heads;
-  const int k0 = tile * kTile;
-  const int64_t base = static_cast<int64_t>(seq) * p.s;
-  QueryTiles it(p.tiles + static_cast<int64_t>(seq) * p.ntiles, p.ntiles, k0, min(k0 + kTile, p.s), kvh * p.group, p.group);
-
   if (warp == kWorkWarps) {
     if (lane == 0) {
       for (uint64_t* b = kv_full; b < g_empty + L::kPassing; ++b)
-        mbar_init(b, b == p_full || b == ds_full || b == st_empty || b == st_empty + 1 ? kWorkWarps : 1);
+        mbar_init(b, b == kv_empty || b == p_full || b == ds_full || b == st_empty || b == st_empty + 1 ? kWorkWarps
+                     : b >= work_empty && b < work_empty + 2                                              ? kWorkWarps + 2
+                                                                                                          : 1);
       fence_mbar_init();
       tma_prefetch_desc(&p.q.map);
       tma_prefetch_desc(&p.k.map);
       tma_prefetch_desc(&p.v.map);
       tma_prefetch_desc(&p.d_o.map);
+      tma_prefetch_desc(&p.dk.map);
+      tma_prefetch_desc(&p.dv.map);
     }
   } else if (warp == kWorkWarps + 1) {
     tmem_alloc(tmem_slot, 512);
@@ -448,38 +581,59 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
+  auto work_of = [&](int it) {  // the CTA's it-th piece, -1 past the last; a whole warp calls it
+    int piece = -1;
+    if (mbar_wait(&work_full[it & 1], (it >> 1) & 1, p.status, 0x4E)) piece = works[it & 1];
+    return __all_sync(0xffffffffu, piece >= 0) ? piece : -1;
+  };
+  auto done_with = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&work_empty[it & 1]);
+  };
 
   if (warp >= kWorkWarps) {
     regs_dec<kRegsIssue>();
     if (warp == kWorkWarps) {
       // ---------------------------------------------------------------- loads
-      bool ok = true, more = it.next();
-      if (more && lane == 0) {
-        mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
-        load_head_tile(sk, p.k, kv_full, L::kBoxes, k0, kvh, seq);
-        load_head_tile(sv, p.v, kv_full, L::kBoxes, k0, kvh, seq);
-      }
-      const bool any = more;
-      int n = 0;
-      for (; more; more = it.next(), ++n) {
-        const int qs = n % L::kHeld, gs = n % L::kPassing;
-        ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[qs], ((n / L::kHeld) & 1) ^ 1, p.status, 0x40));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[qs], L::kTileBytes);
-          load_head_tile(q_ring + qs * L::kTileBytes, p.q, &q_full[qs], L::kBoxes, it.tile * kTile, it.head, seq);
+      bool ok = true;
+      int n = 0, pieces = 0;
+      for (int it = 0; ok; ++it) {
+        const int piece = work_of(it);
+        if (piece < 0) break;
+        const KeyPlace at(p, piece);
+        QueryTiles qt = at.queries(p);
+        const int n0 = n;
+        for (; ok && qt.next(); ++n) {
+          const int qs = n % L::kHeld, gs = n % L::kPassing;
+          ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[qs], ((n / L::kHeld) & 1) ^ 1, p.status, 0x40));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[qs], L::kTileBytes);
+            load_head_tile(q_ring + qs * L::kTileBytes, p.q, &q_full[qs], L::kBoxes, qt.tile * kTile, qt.head, at.seq);
+          }
+          if (n == n0) {  // K and V, once the outputs that went through their place have left it
+            ok = __all_sync(0xffffffffu, mbar_wait(kv_empty, (pieces & 1) ^ 1, p.status, 0x42));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
+              load_head_tile(sk, p.k, kv_full, L::kBoxes, at.k0, at.kvh, at.seq);
+              load_head_tile(sv, p.v, kv_full, L::kBoxes, at.k0, at.kvh, at.seq);
+            }
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&g_empty[gs], ((n / L::kPassing) & 1) ^ 1, p.status, 0x41));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&g_full[gs], L::kTileBytes);
+            load_head_tile(g_ring + gs * L::kTileBytes, p.d_o, &g_full[gs], L::kBoxes, qt.tile * kTile, qt.head, at.seq);
+          }
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&g_empty[gs], ((n / L::kPassing) & 1) ^ 1, p.status, 0x41));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&g_full[gs], L::kTileBytes);
-          load_head_tile(g_ring + gs * L::kTileBytes, p.d_o, &g_full[gs], L::kBoxes, it.tile * kTile, it.head, seq);
-        }
+        ++pieces;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ending);
       }
-      if (!ok && any) {  // the copies in flight must land before shared memory goes away
-        mbar_wait(kv_full, 0, p.status, 0x42);
-        for (int k = max(0, n - L::kHeld); k < n; ++k) mbar_wait(&q_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x42);
-        mbar_wait(&q_full[n % L::kHeld], (n / L::kHeld) & 1, p.status, 0x42);
+      if (!ok) {  // the copies in flight must land before shared memory goes away
+        if (pieces > 0) mbar_wait(kv_full, (pieces - 1) & 1, p.status, 0x42);
+        for (int k = max(0, n + 1 - L::kHeld); k <= n; ++k) mbar_wait(&q_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x42);
         for (int k = max(0, n - L::kPassing); k < n; ++k) mbar_wait(&g_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x42);
       }
     } else if (warp == kWorkWarps + 1) {
@@ -488,10 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       const int ksteps = (p.head_dim + 15) / 16;
       const uint32_t idesc_d = idesc_bf16_f32(kTile, ksteps * 16, false, true);
       const uint32_t k_addr = smem_u32(sk), v_addr = smem_u32(sv), q_addr = smem_u32(q_ring), g_addr = smem_u32(g_ring);
-      bool more = it.next(), ok = true;
-      const bool any = more;
+      bool ok = true;
       auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
         tc_fence_after();
       };
       auto scores = [&](int n) {  // S(n)^T = K Q(n)^T
@@ -506,45 +659,78 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         issue_rows<HD>(leader, t_dp, v_addr, g_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
         umma_commit_by(leader, dp_full);
       };
-      if (more) {
-        wait_on(kv_full, 0, 0x45);
-        scores(0);
-        dprobs(0);
-      }
-      for (int n = 0; more && ok; ++n) {
-        more = it.next();
-        wait_on(p_full, n & 1, 0x46);
-        if (!ok) break;
-        issue_cols<true>(leader, t_dv, tmem, g_addr + (n % L::kPassing) * L::kTileBytes, idesc_d, n != 0);
-        umma_commit_by(leader, &g_empty[n % L::kPassing]);
-        if (more) scores(n + 1);
-        wait_on(ds_full, n & 1, 0x47);
-        if (!ok) break;
-        issue_cols<true>(leader, t_dk, t_dp, q_addr + (n % L::kHeld) * L::kTileBytes, idesc_d, n != 0);
-        umma_commit_by(leader, &q_empty[n % L::kHeld]);
-        if (more) dprobs(n + 1);
-      }
-      if (any) {  // also: every product issued is done before tensor memory is freed
-        umma_commit_by(leader, acc_full);
-        mbar_wait(acc_full, 0, p.status, 0x48);
-      }
-    } else if (warp == kWorkWarps + 2) {
-      // ---------------------------------------------------------------- lse and D of the queries
-      for (int n = 0; it.next(); ++n) {
-        const int q = it.tile * kTile + lane * 4;
-        const int64_t at = (static_cast<int64_t>(seq) * p.heads + it.head) * p.s + q;
-        float l[4], d[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          l[e] = q + e < p.s ? -p.lse[at + e] * kLog2e : 0.f;  // queries without keys: +inf, and masked
-          d[e] = q + e < p.s ? p.dsum[at + e] : 0.f;
+      int n = 0, loaded = 0;
+      for (int it = 0; ok; ++it) {
+        const int piece = work_of(it);
+        if (piece < 0) break;
+        QueryTiles qt = KeyPlace(p, piece).queries(p);
+        bool more = qt.next();
+        if (more) {
+          wait_on(kv_full, loaded & 1, 0x45);
+          ++loaded;
+          scores(n);
+          dprobs(n);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&st_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status, 0x49))) break;
-        float* st = stats + (n & 1) * 2 * kTile;
-        reinterpret_cast<float4*>(st)[lane] = make_float4(l[0], l[1], l[2], l[3]);
-        reinterpret_cast<float4*>(st + kTile)[lane] = make_float4(d[0], d[1], d[2], d[3]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&st_full[n & 1]);
+        for (bool first = true; more && ok; ++n, first = false) {
+          more = qt.next();
+          wait_on(p_full, n & 1, 0x46);
+          if (!ok) break;
+          issue_cols<true>(leader, t_dv, tmem, g_addr + (n % L::kPassing) * L::kTileBytes, idesc_d, !first);
+          umma_commit_by(leader, &g_empty[n % L::kPassing]);
+          if (more) scores(n + 1);
+          wait_on(ds_full, n & 1, 0x47);
+          if (!ok) break;
+          issue_cols<true>(leader, t_dk, t_dp, q_addr + (n % L::kHeld) * L::kTileBytes, idesc_d, !first);
+          umma_commit_by(leader, &q_empty[n % L::kHeld]);
+          if (more) dprobs(n + 1);
+          else umma_commit_by(leader, acc_full);
+        }
+        done_with(it);
+      }
+      umma_commit_by(leader, drain);  // every product issued is done before tensor memory is freed
+      mbar_wait(drain, 0, p.status, 0x48);
+    } else if (warp == kWorkWarps + 2) {
+      // ---------------------------------------------------------------- work
+      if (lane == 0) {
+        int piece = static_cast<int>(blockIdx.x);
+        for (int it = 0;; ++it) {
+          works[it & 1] = piece;
+          mbar_arrive(&work_full[it & 1]);
+          if (piece < 0) break;
+          // as in the query pass
+          piece = mbar_wait(ending, it & 1, p.status, 0x2D) &&
+                          (it == 0 || mbar_wait(&work_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, 0x2D))
+                      ? take_work(response, taken, it & 1, p.status, 0x2C)
+                      : -1;
+        }
+      }
+    } else {
+      // ---------------------------------------------------------------- lse and D of the queries
+      bool ok = true;
+      int n = 0;
+      for (int it = 0; ok; ++it) {
+        const int piece = work_of(it);
+        if (piece < 0) break;
+        const KeyPlace place(p, piece);
+        QueryTiles qt = place.queries(p);
+        for (; qt.next(); ++n) {
+          const int q = qt.tile * kTile + lane * 4;
+          const int64_t at = (static_cast<int64_t>(place.seq) * p.heads + qt.head) * p.s + q;
+          float l[4], d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[e] = q + e < p.s ? -p.lse[at + e] * kLog2e : 0.f;  // queries without keys: +inf, and masked
+            d[e] = q + e < p.s ? p.dsum[at + e] : 0.f;
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&st_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status, 0x49));
+          if (!ok) break;
+          float* st = stats + (n & 1) * 2 * kTile;
+          reinterpret_cast<float4*>(st)[lane] = make_float4(l[0], l[1], l[2], l[3]);
+          reinterpret_cast<float4*>(st + kTile)[lane] = make_float4(d[0], d[1], d[2], d[3]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st_full[n & 1]);
+        }
+        done_with(it);
       }
     }
   } else {
@@ -552,93 +738,107 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     regs_inc<kRegsWork>();
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int half = warp >> 2;
-    const int key = k0 + (warp & 3) * 32 + lane;
     bool ok = true;
-    int n = 0;
-    for (; it.next(); ++n) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&st_full[n & 1], (n >> 1) & 1, p.status, 0x4A));
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, n & 1, p.status, 0x4B));
-      if (!ok) break;
-      tc_fence_after();
-      const float2* lse2 = reinterpret_cast<const float2*>(stats + (n & 1) * 2 * kTile + half * 64);
-      const float4* dd = reinterpret_cast<const float4*>(stats + (n & 1) * 2 * kTile + kTile + half * 64);
-      const int q0 = it.tile * kTile + half * 64;
-      const float slope2 = BIAS ? p.slopes[it.head] * kLog2e : 0.f;
-      const uint32_t ts = tmem + lanes + half * 64, td = t_dp + lanes + half * 64;
-      float w[64];
-      tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
-      tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
-      tmem_ld_wait();
-      // P as it is, packed in x, and times the cap's derivative in w
-      uint32_t x[32];
-      auto pack_seen = [&](auto masked, unsigned lo, unsigned hi) {
-        probabilities<CAP, BIAS>(
-            w, p.sp, slope2, q0, key, key - lane,
-            [&](int c) {
-              const float2 l = lse2[c / 2];
-              return f2_make(l.x, l.y);
-            },
-            [&](int c, float& a, float& b) {
-              if constexpr (decltype(masked)::value) {
-                const unsigned bits = c < 32 ? lo : hi;
-                a = (bits >> (c & 31)) & 1 ? a : 0.f;
-                b = (bits >> ((c & 31) + 1)) & 1 ? b : 0.f;
-              }
-              x[c / 2] = pack_bf16x2(a, b);  // P enters its product in bf16: half a step of each weight
-            });
-      };
-      if (it.full) {
-        pack_seen(Flag<false>{}, 0, 0);
-      } else {
-        // Each lane marks which of the warp's 32 keys two queries see; transposed, which queries see its own key.
-        auto mark = [&](int q) {
-          const int2 r = q < p.s ? clip_range(p.range[base + q], p.s) : make_int2(0, 0);
-          const int from = min(max(r.x - (key - lane), 0), 32), to = min(max(r.y - (key - lane), 0), 32);
-          return from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+    int n = 0, pieces = 0;  // steps so far, and pieces with any
+    for (int it = 0; ok; ++it) {
+      const int piece = work_of(it);
+      if (piece < 0) break;
+      const KeyPlace at(p, piece);
+      const int key = at.k0 + (warp & 3) * 32 + lane;
+      QueryTiles qt = at.queries(p);
+      bool any = false;
+      for (; qt.next(); ++n, any = true) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&st_full[n & 1], (n >> 1) & 1, p.status, 0x4A));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, n & 1, p.status, 0x4B));
+        if (!ok) break;
+        tc_fence_after();
+        const float2* lse2 = reinterpret_cast<const float2*>(stats + (n & 1) * 2 * kTile + half * 64);
+        const float4* dd = reinterpret_cast<const float4*>(stats + (n & 1) * 2 * kTile + kTile + half * 64);
+        const int q0 = qt.tile * kTile + half * 64;
+        const float slope2 = BIAS ? p.slopes[qt.head] * kLog2e : 0.f;
+        const uint32_t ts = tmem + lanes + half * 64, td = t_dp + lanes + half * 64;
+        float w[64];
+        tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w)));
+        tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(w) + 32));
+        tmem_ld_wait();
+        // P as it is, packed in x, and times the cap's derivative in w
+        uint32_t x[32];
+        auto pack_seen = [&](auto masked, unsigned lo, unsigned hi) {
+          probabilities<CAP, BIAS>(
+              w, p.sp, slope2, q0, key, key - lane,
+              [&](int c) {
+                const float2 l = lse2[c / 2];
+                return f2_make(l.x, l.y);
+              },
+              [&](int c, float& a, float& b) {
+                if constexpr (decltype(masked)::value) {
+                  const unsigned bits = c < 32 ? lo : hi;
+                  a = (bits >> (c & 31)) & 1 ? a : 0.f;
+                  b = (bits >> ((c & 31) + 1)) & 1 ? b : 0.f;
+                }
+                x[c / 2] = pack_bf16x2(a, b);  // P enters its product in bf16: half a step of each weight
+              });
         };
-        const unsigned lo = transpose_bits(mark(q0 + lane)), hi = transpose_bits(mark(q0 + 32 + lane));
-        pack_seen(Flag<true>{}, lo, hi);
-      }
-      tmem_st_32x32b_x32(ts, x);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+        if (qt.full) {
+          pack_seen(Flag<false>{}, 0, 0);
+        } else {
+          // Each lane marks which of the warp's 32 keys two queries see; transposed, which queries see its own key.
+          auto mark = [&](int q) {
+            const int2 r = q < p.s ? clip_range(p.range[at.base + q], p.s) : make_int2(0, 0);
+            const int from = min(max(r.x - (key - lane), 0), 32), to = min(max(r.y - (key - lane), 0), 32);
+            return from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+          };
+          const unsigned lo = transpose_bits(mark(q0 + lane)), hi = transpose_bits(mark(q0 + 32 + lane));
+          pack_seen(Flag<true>{}, lo, hi);
+        }
+        tmem_st_32x32b_x32(ts, x);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
 
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, n & 1, p.status, 0x4C));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t dp[64];
-      tmem_ld_32x32b_x32(td, *reinterpret_cast<uint32_t(*)[32]>(dp));
-      tmem_ld_32x32b_x32(td + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
-      tmem_ld_wait();
+        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, n & 1, p.status, 0x4C));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dp[64];
+        tmem_ld_32x32b_x32(td, *reinterpret_cast<uint32_t(*)[32]>(dp));
+        tmem_ld_32x32b_x32(td + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+        tmem_ld_wait();
 #pragma unroll
-      for (int c4 = 0; c4 < 16; ++c4) {
-        const float4 d4 = dd[c4];
-        const F2 a = f2_sub(f2_make(__uint_as_float(dp[4 * c4]), __uint_as_float(dp[4 * c4 + 1])), f2_make(d4.x, d4.y));
-        const F2 b = f2_sub(f2_make(__uint_as_float(dp[4 * c4 + 2]), __uint_as_float(dp[4 * c4 + 3])), f2_make(d4.z, d4.w));
-        const float2 za = f2_split(f2_mul(f2_make(w[4 * c4], w[4 * c4 + 1]), a));
-        const float2 zb = f2_split(f2_mul(f2_make(w[4 * c4 + 2], w[4 * c4 + 3]), b));
-        x[2 * c4] = pack_bf16x2(za.x, za.y);
-        x[2 * c4 + 1] = pack_bf16x2(zb.x, zb.y);
+        for (int c4 = 0; c4 < 16; ++c4) {
+          const float4 d4 = dd[c4];
+          const F2 a = f2_sub(f2_make(__uint_as_float(dp[4 * c4]), __uint_as_float(dp[4 * c4 + 1])), f2_make(d4.x, d4.y));
+          const F2 b = f2_sub(f2_make(__uint_as_float(dp[4 * c4 + 2]), __uint_as_float(dp[4 * c4 + 3])), f2_make(d4.z, d4.w));
+          const float2 za = f2_split(f2_mul(f2_make(w[4 * c4], w[4 * c4 + 1]), a));
+          const float2 zb = f2_split(f2_mul(f2_make(w[4 * c4 + 2], w[4 * c4 + 3]), b));
+          x[2 * c4] = pack_bf16x2(za.x, za.y);
+          x[2 * c4 + 1] = pack_bf16x2(zb.x, zb.y);
+        }
+        tmem_st_32x32b_x32(td, x);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ds_full);
+          mbar_arrive(&st_empty[n & 1]);
+        }
       }
-      tmem_st_32x32b_x32(td, x);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(ds_full);
-        mbar_arrive(&st_empty[n & 1]);
+      if (ok && any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, pieces & 1, p.status, 0x4D));
+        tc_fence_after();
+        ++pieces;
       }
-    }
-    if (ok && n > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, p.status, 0x4D));
-      tc_fence_after();
-    }
-    if (ok) {
-      // warps 0-3 write dV, warps 4-7 dK, a key's row per thread
-      store_head_rows(half ? sk : sv, half ? p.dk : p.dv, (half ? t_dk : t_dv) + lanes, half ? p.scale : 1.0f, n > 0,
-                      warp & 3, lane, 0, L::kBoxes, k0, kvh, seq, p.s, p.head_dim);
+      if (ok) {
+        // warps 0-3 write dV, warps 4-7 dK, a key's row per thread
+        store_head_rows(half ? sk : sv, half ? p.dk : p.dv, (half ? t_dk : t_dv) + lanes, half ? p.scale : 1.0f, any,
+                        warp & 3, lane, 0, L::kBoxes, at.k0, at.kvh, at.seq, p.s, p.head_dim);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kv_empty);
+          mbar_arrive(&work_empty[it & 1]);
+        }
+      }
     }
   }
   tc_fence_before();
