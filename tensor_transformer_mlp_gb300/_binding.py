@@ -7,6 +7,7 @@ in the library's kernels; if the library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -125,33 +126,35 @@ def _cuda(*ts: torch.Tensor | None) -> None:
 
 
 class _On:
-    """Makes a device and `stream` (default: the device's current stream) current, so that the kernels run there and
-    what torch allocates meanwhile belongs to that stream; `as` gives the stream's handle. Where both are current
-    already there is nothing to switch."""
-    __slots__ = ("index", "stream", "guard")
+    """Makes a device and a stream current for a while, so that what torch allocates meanwhile belongs to that stream."""
+    __slots__ = ("guard",)
 
     def __init__(self, index: int, stream):
-        if index < 0:
-            raise ValueError("tensors must be CUDA tensors")
-        if stream is not None and stream.device_index != index:
-            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
-        self.index, self.stream, self.guard = index, stream, None
+        # torch.cuda.stream switches to the stream's device too
+        self.guard = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self) -> int:
-        if self.stream is not None:
-            self.guard = torch.cuda.stream(self.stream)  # switches to the stream's device too
-        elif torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.stream is not None:
-            return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.index)
+    def __enter__(self):
+        self.guard.__enter__()
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        self.guard.__exit__(*exc)
         return False
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _where(index: int, stream):
+    """A context in which the device `index` and `stream` (default: the device's current stream) are current, and the
+    stream's handle. Where both are current already there is nothing to switch."""
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if stream is None:
+        here = _HERE if torch._C._cuda_getDevice() == index else _On(index, None)
+        return here, torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
+    return _On(index, stream), stream.cuda_stream
 
 
 def _device(first: torch.Tensor, *rest: torch.Tensor | None) -> int:
@@ -548,7 +551,8 @@ def attention_key_ranges(b: int, s: int, doc_ids=None, prefix_len=None, causal: 
     if prefix_len is not None:
         _dense(prefix_len, (b,), torch.int32, "prefix_len")
     lib = load_library()
-    with _On(index, stream) as st:
+    here, st = _where(index, stream)
+    with here:
         out = torch.empty((b, s, 2), dtype=torch.int32, device="cuda")
         _check(lib.tpmlp_attention_key_ranges(_ptr(doc_ids), _ptr(prefix_len), 1 if causal else 0, window, out.data_ptr(),
                                               b, s, st))
@@ -583,9 +587,10 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, eps: float = 1e-5, positions=
     q_out and k_out unless given (q and k themselves for in place) and runs tpmlp_qk_norm_rope; returns them."""
     shape, kshape, table_len, rot, strides = _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions)
     lib = load_library()
-    with _On(_device(q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out), stream) as st:
-        q_out = torch.empty(shape, dtype=q.dtype, device="cuda") if q_out is None else q_out
-        k_out = torch.empty(kshape, dtype=q.dtype, device="cuda") if k_out is None else k_out
+    here, st = _where(_device(q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out), stream)
+    with here:
+        q_out = q.new_empty(shape) if q_out is None else q_out
+        k_out = q.new_empty(kshape) if k_out is None else k_out
         strides += _heads(q_out, shape, q.dtype, "q_out") + _heads(k_out, kshape, q.dtype, "k_out")
         _check(lib.tpmlp_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
@@ -602,13 +607,14 @@ def qk_norm_rope_backward(q, k, gamma_q, gamma_k, cos, sin, dq_out, dk_out, eps:
     b, s, heads, hd = shape
     strides += _heads(dq_out, shape, q.dtype, "dq_out") + _heads(dk_out, kshape, q.dtype, "dk_out")
     lib = load_library()
-    with _On(_device(q, k, gamma_q, gamma_k, cos, sin, positions, dq_out, dk_out, dq, dk), stream) as st:
-        dq = torch.empty(shape, dtype=q.dtype, device="cuda") if dq is None else dq
-        dk = torch.empty(kshape, dtype=q.dtype, device="cuda") if dk is None else dk
-        dgq, dgk = torch.empty((2, hd), dtype=torch.float32, device="cuda").unbind()
+    here, st = _where(_device(q, k, gamma_q, gamma_k, cos, sin, positions, dq_out, dk_out, dq, dk), stream)
+    with here:
+        dq = q.new_empty(shape) if dq is None else dq
+        dk = q.new_empty(kshape) if dk is None else dk
+        dgq, dgk = q.new_empty((2, hd), dtype=torch.float32).unbind()
         strides += _heads(dq, shape, q.dtype, "dq") + _heads(dk, kshape, q.dtype, "dk")
         ws_bytes = lib.tpmlp_qk_norm_rope_backward_workspace_size(b, s, hd)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
+        ws = q.new_empty(ws_bytes, dtype=torch.uint8)
         _check(lib.tpmlp_qk_norm_rope_backward(
             q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
             _ptr(positions), table_len, rot, ROPE_STYLE[style], dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
@@ -635,9 +641,10 @@ def masked_attention_forward(q, k, v, key_range, scale: float | None = None, sof
     shape, kshape, strides = _masked_args(q, k, v, key_range, slopes)
     b, s, heads, hd = shape
     lib = load_library()
-    with _On(_device(q, k, v, key_range, slopes, o), stream) as st:
-        o = torch.empty(shape, dtype=q.dtype, device="cuda") if o is None else o
-        lse = torch.empty((b, heads, s), dtype=torch.float32, device="cuda")
+    here, st = _where(_device(q, k, v, key_range, slopes, o), stream)
+    with here:
+        o = q.new_empty(shape) if o is None else o
+        lse = q.new_empty((b, heads, s), dtype=torch.float32)
         strides += _heads(o, shape, q.dtype, "o")
         _check(lib.tpmlp_masked_attention_forward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
@@ -658,13 +665,14 @@ def masked_attention_backward(q, k, v, key_range, o, lse, do, scale: float | Non
     if _heads(do, shape, dtype, "do") != so:
         raise ValueError("do must have o's strides")
     lib = load_library()
-    with _On(_device(q, k, v, key_range, slopes, o, lse, do, dq, dk, dv), stream) as st:
-        dq = torch.empty(shape, dtype=dtype, device="cuda") if dq is None else dq
-        dk = torch.empty(kshape, dtype=dtype, device="cuda") if dk is None else dk
-        dv = torch.empty(kshape, dtype=dtype, device="cuda") if dv is None else dv
+    here, st = _where(_device(q, k, v, key_range, slopes, o, lse, do, dq, dk, dv), stream)
+    with here:
+        dq = q.new_empty(shape) if dq is None else dq
+        dk = q.new_empty(kshape) if dk is None else dk
+        dv = q.new_empty(kshape) if dv is None else dv
         strides += so + _heads(dq, shape, dtype, "dq") + _heads(dk, kshape, dtype, "dk") + _heads(dv, kshape, dtype, "dv")
         ws_bytes = lib.tpmlp_masked_attention_backward_workspace_size(b, s, heads)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
+        ws = q.new_empty(ws_bytes, dtype=torch.uint8)
         _check(lib.tpmlp_masked_attention_backward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
             hd ** -0.5 if scale is None else scale, softcap, o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),

@@ -851,14 +851,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
 }
 
 template <int HD, bool CAP, bool BIAS>
-cudaError_t launch(const BwdParams& p, cudaStream_t stream) {
+cudaError_t launch(const BwdParams& p, cudaStream_t stream, const DeviceCtx& ctx) {
+  static SmemLimit dq_done, dkv_done;
   auto dq = masked_attention_dq_kernel<HD, CAP, BIAS>;
   auto dkv = masked_attention_dkv_kernel<HD, CAP, BIAS>;
   const int64_t q_grid = static_cast<int64_t>(p.ntiles) * p.nseq * p.heads, k_grid = q_grid / p.group;
   if (q_grid > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD, true>::kBytes);
+  cudaError_t e = allow_smem(&dq_done, dq, BwdSmem<HD, true>::kBytes, ctx);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<HD, false>::kBytes);
+  e = allow_smem(&dkv_done, dkv, BwdSmem<HD, false>::kBytes, ctx);
   if (e != cudaSuccess) return e;
   dq<<<static_cast<int>(q_grid), kThreads, BwdSmem<HD, true>::kBytes, stream>>>(p);
   e = cudaGetLastError();
@@ -908,10 +909,10 @@ cudaError_t launch_masked_attention_backward(const MaskedAttention& a, const Hea
   p.status = ctx.status;
   const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
   if (a.head_dim > 64)
-    return cap ? (bias ? launch<128, true, true>(p, stream) : launch<128, true, false>(p, stream))
-               : (bias ? launch<128, false, true>(p, stream) : launch<128, false, false>(p, stream));
-  return cap ? (bias ? launch<64, true, true>(p, stream) : launch<64, true, false>(p, stream))
-             : (bias ? launch<64, false, true>(p, stream) : launch<64, false, false>(p, stream));
+    return cap ? (bias ? launch<128, true, true>(p, stream, ctx) : launch<128, true, false>(p, stream, ctx))
+               : (bias ? launch<128, false, true>(p, stream, ctx) : launch<128, false, false>(p, stream, ctx));
+  return cap ? (bias ? launch<64, true, true>(p, stream, ctx) : launch<64, true, false>(p, stream, ctx))
+             : (bias ? launch<64, false, true>(p, stream, ctx) : launch<64, false, false>(p, stream, ctx));
 }
 
 }  // namespace tpmlp

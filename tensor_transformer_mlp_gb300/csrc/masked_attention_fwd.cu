@@ -437,9 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
 }
 
 template <int HD, bool CAP, bool BIAS>
-cudaError_t launch(const FwdParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch(const FwdParams& p, int grid, cudaStream_t stream, const DeviceCtx& ctx) {
+  static SmemLimit done;
   auto kernel = masked_attention_forward_kernel<HD, CAP, BIAS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<HD>::kBytes);
+  const cudaError_t e = allow_smem(&done, kernel, FwdCfg<HD>::kBytes, ctx);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, FwdCfg<HD>::kBytes, stream>>>(p);
   return cudaGetLastError();
@@ -473,10 +474,10 @@ cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream
   const int g = static_cast<int>(grid);
   const bool wide = a.head_dim > 64, cap = a.softcap > 0.f, bias = a.slopes != nullptr;
   if (wide)
-    return cap ? (bias ? launch<128, true, true>(p, g, stream) : launch<128, true, false>(p, g, stream))
-               : (bias ? launch<128, false, true>(p, g, stream) : launch<128, false, false>(p, g, stream));
-  return cap ? (bias ? launch<64, true, true>(p, g, stream) : launch<64, true, false>(p, g, stream))
-             : (bias ? launch<64, false, true>(p, g, stream) : launch<64, false, false>(p, g, stream));
+    return cap ? (bias ? launch<128, true, true>(p, g, stream, ctx) : launch<128, true, false>(p, g, stream, ctx))
+               : (bias ? launch<128, false, true>(p, g, stream, ctx) : launch<128, false, false>(p, g, stream, ctx));
+  return cap ? (bias ? launch<64, true, true>(p, g, stream, ctx) : launch<64, true, false>(p, g, stream, ctx))
+             : (bias ? launch<64, false, true>(p, g, stream, ctx) : launch<64, false, false>(p, g, stream, ctx));
 }
 
 }  // namespace tpmlp

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace tpmlp {
 
 constexpr int kGeluErf = 0;
@@ -104,6 +106,19 @@ struct DeviceCtx {
 };
 
 cudaError_t get_device_ctx(DeviceCtx* ctx);
+
+// Raises a kernel's dynamic shared memory limit, once per device and kernel (`done` is the caller's, one for each kernel).
+struct SmemLimit {
+  std::atomic<unsigned long long> devices{0};  // bit d: set on device d
+};
+template <typename Kernel>
+cudaError_t allow_smem(SmemLimit* done, Kernel kernel, int bytes, const DeviceCtx& ctx) {
+  const unsigned long long bit = 1ull << ctx.device;  // get_device_ctx takes 64 devices
+  if (done->devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->devices.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Sets the calling thread's tpmlp_last_error() message; returns `status`.
 int report_error(int status, const char* msg);
