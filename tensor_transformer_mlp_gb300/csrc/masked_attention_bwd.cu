@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -576,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the query pass's D and tile summaries
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -864,8 +866,18 @@ cudaError_t launch(const BwdParams& p, cudaStream_t stream, const DeviceCtx& ctx
   dq<<<static_cast<int>(q_grid), kThreads, BwdSmem<HD, true>::kBytes, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dkv<<<static_cast<int>(k_grid), kThreads, BwdSmem<HD, false>::kBytes, stream>>>(p);
-  return cudaGetLastError();
+  // the key pass sets itself up while the last CTAs of the query pass finish (programmatic dependent launch)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(k_grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = BwdSmem<HD, false>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dkv, p);
 }
 
 }  // namespace

@@ -117,7 +117,40 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
   static_assert(16 + (21 + 2 * L::kStages) * 8 + 2 * sizeof(Work) + 4 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == kSoftmaxWarps) {
+  // A piece's key tiles, by a whole warp; and the keys of this thread's row of a piece.
+  auto find_work = [&](int piece) {
+    Work w{piece, {}};
+    if (piece < 0) return w;
+    const Place at(p, piece);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      int lo = INT32_MAX, hi = 0;
+#pragma unroll
+      for (int k = 0; k < kTile; k += 32) {
+        const int row = at.q0 + i * kTile + k + lane;
+        const int2 r = row < p.s ? clip_range(p.range[at.base + row], p.s) : make_int2(0, 0);
+        lo = min(lo, r.x < r.y ? r.x : INT32_MAX);
+        hi = max(hi, r.y);
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (hi > 0) w.span[i] = Span{lo / kTile, (hi + kTile - 1) / kTile};
+    }
+    return w;
+  };
+  auto range_of = [&](int piece) {
+    if (piece < 0) return make_int2(0, 0);
+    const Place at(p, piece);
+    const int row = at.q0 + static_cast<int>(threadIdx.x);
+    return row < p.s ? p.range[at.base + row] : make_int2(0, 0);
+  };
+  Work first{};
+  int2 r_next = make_int2(0, 0);
+  if (warp < kSoftmaxWarps) {
+    r_next = range_of(static_cast<int>(blockIdx.x));
+  } else if (warp == kSoftmaxWarps + 2) {
+    first = find_work(static_cast<int>(blockIdx.x));
+  } else if (warp == kSoftmaxWarps) {
     if (lane == 0) {
       for (uint64_t* bar = q_full; bar < kv_empty + L::kStages; ++bar)
         mbar_init(bar, (bar >= p_full && bar < p_full + 4) || (bar >= o_empty && bar < o_empty + 2) ? 4
@@ -273,24 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       // ---------------------------------------------------------------- work
       int piece = static_cast<int>(blockIdx.x);
       for (int it = 0;; ++it) {
-        Work w{piece, {}};
-        if (piece >= 0) {
-          const Place at(p, piece);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            int lo = INT32_MAX, hi = 0;
-#pragma unroll
-            for (int k = 0; k < kTile; k += 32) {
-              const int row = at.q0 + i * kTile + k + lane;
-              const int2 r = row < p.s ? clip_range(p.range[at.base + row], p.s) : make_int2(0, 0);
-              lo = min(lo, r.x < r.y ? r.x : INT32_MAX);
-              hi = max(hi, r.y);
-            }
-            lo = __reduce_min_sync(0xffffffffu, lo);
-            hi = __reduce_max_sync(0xffffffffu, hi);
-            if (hi > 0) w.span[i] = Span{lo / kTile, (hi + kTile - 1) / kTile};
-          }
-        }
+        const Work w = it == 0 ? first : find_work(piece);
         if (lane == 0) {
           works[it & 1] = w;
           mbar_arrive(&work_full[it & 1]);
@@ -314,14 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
     uint8_t* stage = staging + warp * L::kStageBytes;
     bool ok = true;
     int step = 0, pieces = 0;  // of this query tile, so far
-    auto range_of = [&](const Work& w) {  // the row's keys
-      if (w.piece < 0) return make_int2(0, 0);
-      const Place at(p, w.piece);
-      const int row = at.q0 + static_cast<int>(threadIdx.x);
-      return row < p.s ? p.range[at.base + row] : make_int2(0, 0);
-    };
     Work w = work_of(0);
-    int2 r_next = range_of(w);
     for (int it = 0; __all_sync(0xffffffffu, ok && w.piece >= 0); ++it) {
       const Place at(p, w.piece);
       const int row = at.q0 + static_cast<int>(threadIdx.x);
@@ -403,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       if (!ok) break;
       const bool any = mine.lo < mine.hi;
       w = work_of(it + 1);
-      r_next = range_of(w);  // on its way during the output
+      r_next = range_of(w.piece);  // on its way during the output
       if (any) {
         ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], pieces & 1, p.status, 0x27));
         tc_fence_after();
