@@ -51,6 +51,9 @@ def test_forward_refusals(lib):
     assert fwd(lib, kv=3) == SHAPE and fwd(lib, heads=0) == SHAPE and fwd(lib, kv=0) == SHAPE
     assert fwd(lib, hd=60) == SHAPE and fwd(lib, hd=136) == SHAPE and fwd(lib, hd=0) == SHAPE
     assert fwd(lib, b=-1) == SHAPE and fwd(lib, s=-1) == SHAPE and fwd(lib, b=1 << 16, s=1 << 16) == SHAPE
+    assert fwd(lib, b=1, s=(1 << 30) + 1, ldq=8) == SHAPE and fwd(lib, b=65536, s=1) == SHAPE
+    assert fwd(lib, heads=65536, kv=1) == SHAPE
+    assert fwd(lib, b=1, s=1 << 20, ldk=1 << 20) == SHAPE    # a sequence's keys span 2^40 elements
     for name in ("ldq", "hsq", "ldk", "hsk", "ldv", "hsv", "ldo", "hso"):
         assert fwd(lib, **{name: 0}) == SHAPE, name      # a broadcast tensor
         assert fwd(lib, **{name: -64}) == SHAPE, name
