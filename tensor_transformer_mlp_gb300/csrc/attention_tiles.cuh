@@ -56,8 +56,8 @@ __device__ __forceinline__ void umma_commit_by(uint32_t leader, uint64_t* bar) {
       : "memory");
 }
 
-// mbar_wait by polling: for the issuing warp, whose reaction the tensor core waits for. (try_wait suspends the thread;
-// it was seen to return up to 400 cycles after the phase had completed.)
+// mbar_wait by polling: for the issuing warp, whose reaction the tensor core waits for. (In the working warps it gains
+// nothing over try_wait: causal forward 66.0 and 66.4 us, its step 273 and 275 us.)
 __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, unsigned int* status, unsigned int where) {
   const uint32_t a = smem_u32(bar);
   auto done = [&] {
@@ -95,16 +95,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       TPMLP_R8(r, 0), TPMLP_R8(r, 8), TPMLP_R8(r, 16), TPMLP_R8(r, 24)
       : "memory");
 }
-
-// The same with 16 columns.
-__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      TPMLP_R8(r, 0), TPMLP_R8(r, 8)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Moves a warpgroup's share of the block's registers (every warp of the warpgroup calls it; the shares of all
@@ -347,6 +337,17 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ float cap_tanh(float qk, const ScoreParams& p) {
   return fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(qk * p.in_cap2)), 1.0f);
 }
+// The first way of a pair with the derivative: with E = e^(2x) and r = 1 / (1 + E) it is 4 E r^2, right relative to itself
+// where 1 - tanh^2 would leave nothing of it. 4 E stops at 2^120, lest it meets r as infinity.
+__device__ __forceinline__ F2 cap_tanh(F2 qk, const ScoreParams& p, F2& d) {
+  auto both = [](float v) { return f2_make(v, v); };
+  const float2 x = f2_split(f2_fma(qk, both(p.in_cap2), both(2.0f)));
+  const F2 e4 = f2_make(ex2_approx(fminf(x.x, 120.0f)), ex2_approx(fminf(x.y, 120.0f)));
+  const float2 n = f2_split(f2_fma(e4, both(0.25f), both(1.0f)));
+  const F2 r = f2_make(rcp_approx(n.x), rcp_approx(n.y));
+  d = f2_mul(r, f2_mul(r, e4));
+  return f2_fma(both(-2.0f), r, both(1.0f));
+}
 __device__ __forceinline__ F2 cap_tanh_small(F2 qk, const ScoreParams& p) {
   auto both = [](float v) { return f2_make(v, v); };
   const F2 x = f2_mul(qk, both(p.in_cap)), z = f2_mul(x, x);
@@ -360,17 +361,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// tanh of N capped scores in place. The special-function unit, with an exponent of every score to take besides, is what
-// bounds the first way (masked rows of 4096, 32 heads of 128: forward 387 us); a warp whose scores are all small takes
-// the polynomial (306 us; with two of every eight pairs left to the first way 357 us).
+// Whether all N scores of a warp's lanes may take the cap's polynomial.
 template <int N>
-__device__ __forceinline__ void cap_tanh_all(float (&y)[N], const ScoreParams& p) {
+__device__ __forceinline__ bool cap_is_small(const float (&y)[N], const ScoreParams& p) {
   float m[4] = {};
 #pragma unroll
   for (int c = 0; c < N; c += 8)
 #pragma unroll
     for (int e = 0; e < 4; ++e) m[e] = max3(m[e], fabsf(y[c + 2 * e]), fabsf(y[c + 2 * e + 1]));
-  if (__all_sync(0xffffffffu, max3(fmaxf(m[0], m[1]), m[2], m[3]) <= p.small)) {
+  return __all_sync(0xffffffffu, max3(fmaxf(m[0], m[1]), m[2], m[3]) <= p.small);
+}
+
+// tanh of N capped scores in place. The special-function unit, with an exponent of every score to take besides, is what
+// bounds the first way (masked rows of 4096, 32 heads of 128: forward 387 us); a warp whose scores are all small takes
+// the polynomial (306 us; with two of every eight pairs left to the first way 357 us).
+template <int N>
+__device__ __forceinline__ void cap_tanh_all(float (&y)[N], const ScoreParams& p) {
+  if (cap_is_small(y, p)) {
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
       const float2 v = f2_split(cap_tanh_small(f2_make(y[c], y[c + 1]), p));

@@ -76,32 +76,49 @@ struct Flag {
 template <bool CAP, bool BIAS, typename Shift, typename Done>
 __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,
                                               int row0, Shift shift, Done done) {
-  float t[CAP ? 64 : 1];  // tanh
-  if constexpr (CAP) {
-    cap_tanh_all(w, sp);
+  const int side = BIAS ? side_of(col0, 64, row0) : 0;
+  const float d0 = static_cast<float>(col0 - row), k = side > 0 ? -slope2 : slope2, off = k * d0;
+  const float unit = CAP ? sp.cap2 : sp.scale2;
+  const F2 u2 = f2_make(unit, unit), one = f2_make(1.0f, 1.0f);
+  auto all = [&](auto small, auto line) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) t[c] = w[c];
-  }
-  const float unit = BIAS ? 1.0f : CAP ? sp.cap2 : sp.scale2;
-  if constexpr (BIAS)
-    add_bias(w, CAP ? sp.cap2 : sp.scale2, slope2, static_cast<float>(col0 - row), side_of(col0, 64, row0));
-  const F2 u2 = f2_make(unit, unit);
-#pragma unroll
-  for (int c = 0; c < 64; c += 2) {
-    const F2 v = f2_make(w[c], w[c + 1]), s = shift(c);
-    const float2 z = f2_split(BIAS ? f2_add(v, s) : f2_fma(v, u2, s));
-    float a = ex2_approx(z.x), b = ex2_approx(z.y);
-    done(c, a, b);
-    if constexpr (CAP) {
-      const F2 tt = f2_make(t[c], t[c + 1]), ab = f2_make(a, b);
-      const float2 m = f2_split(f2_sub(ab, f2_mul(ab, f2_mul(tt, tt))));  // times 1 - t^2
-      w[c] = m.x;
-      w[c + 1] = m.y;
-    } else {
-      w[c] = a;
-      w[c + 1] = b;
+    for (int c = 0; c < 64; c += 2) {
+      F2 v = f2_make(w[c], w[c + 1]), d = one;  // d: the cap's derivative
+      if constexpr (CAP) {
+        if constexpr (decltype(small)::value) {
+          v = cap_tanh_small(v, sp);
+          d = f2_sub(one, f2_mul(v, v));  // >= 3/4, so the difference loses nothing
+        } else {
+          v = cap_tanh(v, sp, d);
+        }
+      }
+      F2 s = shift(c);
+      if constexpr (BIAS) {
+        const float c0 = static_cast<float>(c), c1 = static_cast<float>(c + 1);
+        if constexpr (decltype(line)::value)
+          s = f2_add(s, f2_fma(f2_make(k, k), f2_make(c0, c1), f2_make(off, off)));
+        else
+          s = f2_add(s, f2_make(-slope2 * fabsf(d0 + c0), -slope2 * fabsf(d0 + c1)));
+      }
+      const float2 z = f2_split(f2_fma(v, u2, s));
+      float a = ex2_approx(z.x), b = ex2_approx(z.y);
+      done(c, a, b);
+      if constexpr (CAP) {
+        const float2 m = f2_split(f2_mul(f2_make(a, b), d));
+        w[c] = m.x;
+        w[c + 1] = m.y;
+      } else {
+        w[c] = a;
+        w[c + 1] = b;
+      }
     }
-  }
+  };
+  auto both = [&](auto small) {
+    if (BIAS && side == 0) all(small, Flag<false>{});
+    else all(small, Flag<true>{});
+  };
+  if (CAP && !cap_is_small(w, sp)) both(Flag<false>{});
+  else both(Flag<true>{});
 }
 template <bool CAP, bool BIAS, typename Shift>
 __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,

@@ -257,6 +257,71 @@ def test_longer_rows_and_many_heads():
     _check(q, k, v, dO, oma.key_ranges(1, 1500, doc_ids=ids), cap=40.0)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_more_pieces_than_resident_ctas(hd):
+    # 480 tiles of queries and 240 of keys, long and short ones mixed, on at most a CTA per SM
+    b, s, heads, kv = 20, 140, 12, 6
+    q, k, v, dO = _draw(hd, b, s, heads, kv, hd, "joined")
+    ids = _docs(b, s, 4, 5)
+    ids[3] = -1                                            # a sequence of padding alone
+    _check(q, k, v, dO, oma.key_ranges(b, s, doc_ids=ids))
+
+
+@pytest.mark.parametrize("hd,std,cap", [(64, 4.0, 3.0), (128, 0.3, 100.0), (128, 3.0, 20.0)])
+def test_both_ways_of_the_cap(hd, std, cap):
+    # scores far past the cap, scores that it hardly bends, and tiles of either kind in one call
+    q, k, v, dO = _draw(hd + 1, 1, 300, 2, 1, hd, std=std)
+    if cap == 20.0:
+        k[:, :128] *= 0.05
+    _check(q, k, v, dO, oma.key_ranges(1, 300), cap=cap)
+
+
+def test_two_calls_at_once():
+    # two streams, each with its own tensors and workspaces, in flight together
+    sets = [_draw(20 + n, 2, 700, 8, 4, 128 if n else 64) for n in range(2)]
+    ranges = tp.attention_key_ranges(2, 700, device="cuda")
+
+    def step(t, stream=None):
+        o, lse = tp.masked_attention_forward(t[0], t[1], t[2], ranges, stream=stream)
+        return (o, lse) + tp.masked_attention_backward(t[0], t[1], t[2], ranges, o, lse, t[3], stream=stream)
+
+    want = [step(t) for t in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[step(t, st) for t, st in zip(sets, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    tp.tpmlp_device_status()
+    for run in got:
+        for a, b in zip(want, run):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+
+
+def test_two_graphs_of_one_step():
+    # each graph holds its own workspace; replayed in turn and with other inputs in between
+    q, k, v, dO = _draw(30, 1, 390, 4, 4, 64)
+    ranges = tp.attention_key_ranges(1, 390, device="cuda")
+    graphs, outs = [], []
+    tp.masked_attention_backward(q, k, v, ranges, *tp.masked_attention_forward(q, k, v, ranges), dO)
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o, lse = tp.masked_attention_forward(q, k, v, ranges)
+            outs.append((o, lse) + tp.masked_attention_backward(q, k, v, ranges, o, lse, dO))
+        graphs.append(g)
+    first = q.clone()
+    q.mul_(-0.5)
+    graphs[0].replay()
+    other = [t.clone() for t in outs[0]]
+    q.copy_(first)
+    graphs[1].replay()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(outs[0], outs[1], other):
+        assert torch.equal(a, b)
+    assert not torch.equal(outs[0][0], other[0])
+
+
 def test_same_inputs_same_bits():
     q, k, v, dO = _draw(4, 2, 500, 8, 2, 64)
     ranges = tp.attention_key_ranges(2, 500, device="cuda")
