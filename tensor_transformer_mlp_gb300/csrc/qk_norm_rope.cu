@@ -341,14 +341,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float ss = group_sum(sum4(s1), p.group);
         const float gx = group_sum(sum4(s2), p.group);
         const float r = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-        const float m = -gx * p.inv_hd * r * r * r;  // dx = r g - x r^3 mean(g x)
+        const float m = -gx * p.inv_hd * r * r;  // dx = r (g - x r^2 mean(g x)); r^3 would overflow from eps = 1e-26 down
         const bool on = act && h0 + hb + u < a.heads;
         const float ra = pos < 0 || !on ? 0.f : r;
         const F2 r2 = f2_make(pos < 0 ? 0.f : r, pos < 0 ? 0.f : r), m2 = f2_make(m, m), ra2 = f2_make(ra, ra);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           acc[e] = f2_fma(other[e], ra2, acc[e]);
-          d[e] = f2_fma(f[e], m2, f2_mul(r2, d[e]));
+          d[e] = f2_mul(r2, f2_fma(f[e], m2, d[e]));
         }
         if (on) Vec8<T>::store(dx + (hb + u) * a.dx.hs, d);
       }

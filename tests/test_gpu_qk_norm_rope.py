@@ -91,6 +91,15 @@ def test_large_eps_and_zero_rows():
     _check(inp, "half", True, eps=0.5)
 
 
+@pytest.mark.parametrize("eps", [1e-12, 1e-30])
+def test_tiny_eps_and_zero_rows(eps):
+    # 1 / sqrt(eps) is 1e15 there, and its cube is past fp32
+    inp = _inputs(9, 1, 20, 2, 2, 64, 64, torch.float32)
+    inp[0][0, 3] = 0
+    inp[1][0, 5] = 0
+    _check(inp, "interleaved", True, eps=eps)
+
+
 def test_in_place_and_into_views():
     q, k, gq, gk, cos, sin, pos, dyq, dyk = _inputs(5, 2, 31, 6, 6, 40, 20, torch.bfloat16, packed=True)
     want = tp.qk_norm_rope(q, k, gq, gk, cos, sin, positions=pos)
