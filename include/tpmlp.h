@@ -369,7 +369,8 @@ tpmlp_status tpmlp_attention_backward(const void* X, const void* Wqkv, const voi
  * tpmlp_attention_forward (head j's q, k, v: base + (0, 1, 2) * head_dim, ld = 3h, hs =
  * 3 * head_dim), a [all q | all k | all v] matrix (hs = head_dim) and separate [b*s][h] matrices
  * are all read and written in place. Strides are positive multiples of 8 elements, pointers
- * 16-byte aligned, and the heads of an output must not overlap. head_dim is a multiple of 8.
+ * 16-byte aligned, and the heads of an output must not overlap, nor an output anything else that
+ * the call reads or writes unless it says so. head_dim is a multiple of 8.
  * heads query heads share kv_heads key and value heads, heads % kv_heads == 0: query head j
  * reads key head j / (heads / kv_heads).
  *
@@ -384,7 +385,7 @@ tpmlp_status tpmlp_attention_backward(const void* X, const void* Wqkv, const voi
  *               positions are visible to every earlier one too (a bidirectional prefix);
  *   window      0, or w > 0: a token sees itself and the w - 1 tokens before it (and, when not
  *               causal, the w - 1 after it).
- * b, s >= 0, b * s <= 2^31-1. Errors: TPMLP_ERR_INVALID (null key_range, causal not 0 or 1, a
+ * b, s >= 0, s <= 2^30, b * s <= 2^31-1. Errors: TPMLP_ERR_INVALID (null key_range, causal not 0 or 1, a
  * prefix without causal, window < 0), TPMLP_ERR_SHAPE, TPMLP_ERR_ALIGN.
  */
 tpmlp_status tpmlp_attention_key_ranges(const void* doc_ids, const void* prefix_len, int causal, int64_t window,
@@ -446,10 +447,12 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
  *   q, o: heads heads; k, v: kv_heads heads, bf16; lse: fp32 [b][heads][s] (kept for the backward).
  *   key_range: int32 [b][s][2], 8-byte aligned; a range is cut to 0 <= lo, hi <= s.
  *   slopes: fp32 [heads] (the bias's slope of each head, 4-byte aligned) or NULL for no bias.
- *   scale > 0 and finite (1 / sqrt(head_dim) in the block above); softcap >= 0 and finite.
+ *   scale > 0 (1 / sqrt(head_dim) in the block above), softcap >= 0; they and scale / softcap at
+ *   most 1e30.
  * bf16 only; head_dim a multiple of 8, 8 <= head_dim <= 128. Scores, statistics and sums are fp32;
- * the probabilities are rounded to bf16 for the product with V. q, k, v must be finite everywhere,
- * in masked places too: a hidden value enters the products with weight zero.
+ * the probabilities are rounded to bf16 for the product with V. q, k, v and slopes must be finite
+ * everywhere, in masked places too: a hidden value enters the products with weight zero.
+ * b, heads <= 65535, s <= 2^30, b * s <= 2^31-1, and at most 2^31-1 tiles of 128 queries in all heads.
  */
 tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const void* v, const void* key_range,
                                             const float* slopes, float scale, float softcap, void* o, float* lse,
@@ -464,7 +467,8 @@ tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const 
  *   dQ_i = sum_j dX_ij k_j,   dK_j = sum_i dX_ij q_i,
  * the sums for a key or value head running over its query heads too. No atomics: every sum has a
  * fixed order. dq, dk, dv (bf16, strides ld_dq.. and so on) are overwritten; queries without keys
- * and keys that no query sees get zeros. slopes get no gradient.
+ * and keys that no query sees get zeros. slopes get no gradient. P_ij and dX_ij / scale are rounded
+ * to bf16 for their products. o and d_o, too, must be finite everywhere.
  * workspace: tpmlp_masked_attention_backward_workspace_size bytes, 256-byte aligned.
  */
 size_t tpmlp_masked_attention_backward_workspace_size(int64_t b, int64_t s, int heads);

@@ -571,6 +571,8 @@ def _rope_args(q, k, gamma_q, gamma_k, cos, sin, positions):
     b, s, heads, hd = shape = q.shape
     kshape = (b, s, k.shape[2], hd)
     table = cos.shape
+    if len(table) != 2:
+        raise ValueError("cos and sin must be [table_len, rot_dim / 2]")
     strides = _heads(q, shape, q.dtype, "q") + _heads(k, kshape, q.dtype, "k")
     _dense(gamma_q, (hd,), torch.float32, "gamma_q")
     _dense(gamma_k, (hd,), torch.float32, "gamma_k")

@@ -874,13 +874,12 @@ cudaError_t launch(const BwdParams& p, cudaStream_t stream, const DeviceCtx& ctx
   static SmemLimit dq_done, dkv_done;
   auto dq = masked_attention_dq_kernel<HD, CAP, BIAS>;
   auto dkv = masked_attention_dkv_kernel<HD, CAP, BIAS>;
-  const int64_t q_grid = static_cast<int64_t>(p.ntiles) * p.nseq * p.heads, k_grid = q_grid / p.group;
-  if (q_grid > INT32_MAX) return cudaErrorInvalidValue;
+  const int q_grid = p.ntiles * p.nseq * p.heads, k_grid = q_grid / p.group;
   cudaError_t e = allow_smem(&dq_done, dq, BwdSmem<HD, true>::kBytes, ctx);
   if (e != cudaSuccess) return e;
   e = allow_smem(&dkv_done, dkv, BwdSmem<HD, false>::kBytes, ctx);
   if (e != cudaSuccess) return e;
-  dq<<<static_cast<int>(q_grid), kThreads, BwdSmem<HD, true>::kBytes, stream>>>(p);
+  dq<<<q_grid, kThreads, BwdSmem<HD, true>::kBytes, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the key pass sets itself up while the last CTAs of the query pass finish (programmatic dependent launch)

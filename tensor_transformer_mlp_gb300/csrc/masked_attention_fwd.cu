@@ -476,11 +476,9 @@ cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream
   p.group = a.heads / a.kv_heads;
   p.head_dim = a.head_dim;
   p.nblocks = static_cast<int>((a.s + 2 * kTile - 1) / (2 * kTile));
-  const int64_t bheads = a.b * a.heads, grid = p.nblocks * bheads;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  p.bheads = static_cast<int>(bheads);
+  p.bheads = static_cast<int>(a.b * a.heads);
   p.status = ctx.status;
-  const int g = static_cast<int>(grid);
+  const int g = p.nblocks * p.bheads;
   const bool wide = a.head_dim > 64, cap = a.softcap > 0.f, bias = a.slopes != nullptr;
   if (wide)
     return cap ? (bias ? launch<128, true, true>(p, g, stream, ctx) : launch<128, true, false>(p, g, stream, ctx))

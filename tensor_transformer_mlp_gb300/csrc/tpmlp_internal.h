@@ -219,7 +219,8 @@ inline bool heads_apart(const HeadView& v, int64_t tokens, int heads, int hd) {
   return heads <= 1 || (v.ld - hd) / v.hs >= heads - 1 || (v.hs - hd) / v.ld >= tokens - 1;
 }
 
-// Masked attention (tpmlp_masked_attention_*): everything but the gradients. Sizes are checked by the caller.
+// Masked attention (tpmlp_masked_attention_*): everything but the gradients. Sizes are checked by the caller; the tiles
+// of 128 queries of all heads are at most 2^31-1.
 struct MaskedAttention {
   HeadView q, k, v, o;
   const int2* range;     // [b][s] {lo, hi}

@@ -137,6 +137,8 @@ tpmlp_status check_shape(float scale, float softcap, int64_t b, int64_t s, int h
   if (heads % kv_heads != 0) return err(TPMLP_ERR_SHAPE, "heads must be a multiple of kv_heads");
   if (hd < 8 || hd % 8 != 0 || hd > 128)
     return err(TPMLP_ERR_SHAPE, "head_dim must be a multiple of 8, 8 <= head_dim <= 128");
+  if ((s + 127) / 128 * b * heads > INT32_MAX)
+    return err(TPMLP_ERR_SHAPE, "more than 2^31-1 tiles of 128 queries in all heads");
   for (const auto& list : {inputs, q_outputs, k_outputs})
     for (const HeadView& v : list)
       if (!good_head_strides(v, s))
@@ -147,6 +149,8 @@ tpmlp_status check_shape(float scale, float softcap, int64_t b, int64_t s, int h
     if (!heads_apart(v, b * s, kv_heads, hd)) return err(TPMLP_ERR_SHAPE, "an output's heads overlap");
   if (!(scale > 0.0f) || !std::isfinite(scale)) return err(TPMLP_ERR_INVALID, "scale must be positive and finite");
   if (!(softcap >= 0.0f) || !std::isfinite(softcap)) return err(TPMLP_ERR_INVALID, "softcap must be >= 0 and finite");
+  if (scale > 1e30f || softcap > 1e30f || (softcap > 0.0f && scale / softcap > 1e30f))
+    return err(TPMLP_ERR_INVALID, "scale, softcap and scale / softcap must be at most 1e30");
   return TPMLP_OK;
 }
 
@@ -180,6 +184,7 @@ tpmlp_status tpmlp_attention_key_ranges(const void* doc_ids, const void* prefix_
                                         void* key_range, int64_t b, int64_t s, void* stream) {
   if (b < 0 || s < 0) return err(TPMLP_ERR_SHAPE, "need b, s >= 0");
   if (b > 0 && s > INT32_MAX / b) return err(TPMLP_ERR_SHAPE, "b * s exceeds 2^31-1");
+  if (s > (1 << 30)) return err(TPMLP_ERR_SHAPE, "s must be <= 2^30");
   if (causal != 0 && causal != 1) return err(TPMLP_ERR_INVALID, "causal is 0 or 1");
   if (window < 0) return err(TPMLP_ERR_INVALID, "window must be >= 0");
   if (prefix_len && !causal) return err(TPMLP_ERR_INVALID, "a prefix needs a causal mask");

@@ -32,6 +32,7 @@ def test_key_range_refusals(lib):
     assert call(prefix=FAKE + 1) == ALIGN
     assert call(b=-1) == SHAPE and call(s=-1) == SHAPE
     assert call(b=1 << 20, s=1 << 20) == SHAPE
+    assert call(b=1, s=2 ** 31 - 1) == SHAPE and call(b=1, s=(1 << 30) + 1) == SHAPE
     assert call(b=0, out=None) == OK and call(s=0) == OK
 
 
@@ -65,6 +66,8 @@ def test_forward_refusals(lib):
         assert fwd(lib, scale=bad) == INVALID
     for bad in (-1.0, float("inf"), float("nan")):
         assert fwd(lib, cap=bad) == INVALID
+    assert fwd(lib, scale=2e30) == INVALID and fwd(lib, cap=2e30) == INVALID and fwd(lib, scale=1.0, cap=1e-38) == INVALID
+    assert fwd(lib, b=65535, s=1, heads=65535, kv=1, ldq=65535 * 64, ldo=65535 * 64) == SHAPE   # 2^32 pieces of work
     assert fwd(lib, b=0, q=None) == OK and fwd(lib, s=0, o=None) == OK
 
 
@@ -148,6 +151,8 @@ def test_binding_refuses_what_the_library_cannot_see():
         tp.masked_attention_forward(q, q.float(), q, r)
     with pytest.raises(ValueError):
         tp.attention_key_ranges(1, 8, doc_ids=torch.zeros(1, 7, dtype=torch.int32))
+    with pytest.raises(ValueError):                         # a table of no rows and columns
+        tp.qk_norm_rope(q, q, torch.ones(64), torch.ones(64), torch.ones(64), torch.ones(64))
 
 
 # ------------------------------------------------------------------------- the oracles' pins
