@@ -51,6 +51,7 @@ struct FwdCfg {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr bool kOwnP = HD == 64;            // P has tensor memory of its own, and the two products a warp each
   static constexpr int kHalves = HD == 128 ? 2 : 1;  // parts in which P is handed over
   static constexpr int kStageBytes = 32 * 128;       // of output, per softmax warp
   static constexpr int kBytes = (2 + kStages) * kTileBytes + kSoftmaxWarps * kStageBytes + 512;  // 229,888 at HD = 128
@@ -110,11 +111,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
   uint64_t* ending = work_empty + 2;
   uint64_t* taken = ending + 1;
   uint64_t* drain = taken + 1;
-  uint64_t* kv_full = drain + 1;
+  uint64_t* s_free = drain + 2;
+  uint64_t* kv_full = s_free + 2;
   uint64_t* kv_empty = kv_full + L::kStages;
   Work* works = reinterpret_cast<Work*>(kv_empty + L::kStages);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(works + 2);
-  static_assert(16 + (21 + 2 * L::kStages) * 8 + 2 * sizeof(Work) + 4 <= 512, "barrier area");
+  static_assert(16 + (24 + 2 * L::kStages) * 8 + 2 * sizeof(Work) + 4 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // A piece's key tiles, by a whole warp; and the keys of this thread's row of a piece.
@@ -153,8 +155,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
   } else if (warp == kSoftmaxWarps) {
     if (lane == 0) {
       for (uint64_t* bar = q_full; bar < kv_empty + L::kStages; ++bar)
-        mbar_init(bar, (bar >= p_full && bar < p_full + 4) || (bar >= o_empty && bar < o_empty + 2) ? 4
-                       : bar >= work_empty && bar < work_empty + 2 ? kSoftmaxWarps + 1
+        mbar_init(bar, (bar >= p_full && bar < p_full + 4) || (bar >= o_empty && bar < o_empty + 2) ||
+                               (bar >= s_free && bar < s_free + 2)
+                           ? 4
+                       : bar >= work_empty && bar < work_empty + 2 ? kSoftmaxWarps + (L::kOwnP ? 2 : 1)
                                                                    : 1);
       fence_mbar_init();
       tma_prefetch_desc(&p.q.map);
@@ -220,88 +224,138 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         for (int k = max(0, n - L::kStages); k < n; ++k)
           mbar_wait(&kv_full[k % L::kStages], (k / L::kStages) & 1, p.status, 0x21);
       }
-    } else if (warp == kSoftmaxWarps + 1) {
+    } else if (warp == kSoftmaxWarps + 1 || (L::kOwnP && warp == kSoftmaxWarps + 3)) {
       // ---------------------------------------------------------------- products
-      // A wait that passes and a commit cost 100 to 150 cycles each, which the tensor core must not see: the tiles of
-      // the next step are waited for, and tiles released, between products, and S of tile 1 is followed at once by the
-      // wait for P of tile 0.
       const uint32_t leader = elect_one();
       const int ksteps = (p.head_dim + 15) / 16;
       const uint32_t idesc_o = idesc_bf16_f32(kTile, ksteps * 16, false, true);
       const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
-      bool ok = true;
-      auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
-      };
       auto commit = [&](uint64_t* bar) { umma_commit_by(leader, bar); };
-      auto stage_of = [&](int n) { return ring_addr + (n % L::kStages) * L::kTileBytes; };
-      auto wait_tile = [&](int n) { wait_on(&kv_full[n % L::kStages], (n / L::kStages) & 1, 0x22); };
-      int n0 = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};  // key tiles, and per query tile steps and pieces, so far
-      for (int it = 0; ok; ++it) {
-        const Work w = work_of(it);
-        if (__any_sync(0xffffffffu, w.piece < 0)) break;
-        const int j_end = w.end();
-        auto scores = [&](int i, int n, int j) {  // with the K tile j of step n
-          if (!ok) return;
-          issue_rows<HD>(leader, tmem + i * 128, q_addr + i * L::kTileBytes, stage_of(2 * n), ksteps);
-          commit(&s_full[i]);
-          if (j + 1 == w.span[i].hi) commit(&q_empty[i]);
+      if constexpr (L::kOwnP) {
+        // One warp issues the scores, the other P V.
+        const bool pv = warp == kSoftmaxWarps + 3;
+        bool ok = true;
+        auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
         };
-        int j = w.next(w.begin()), jn = w.next(j + 1), n = n0;
-        if (j < j_end) {
-          wait_tile(2 * n);
+        int n = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
+        for (int it = 0; ok; ++it) {
+          const Work w = work_of(it);
+          if (__any_sync(0xffffffffu, w.piece < 0)) break;
+          const int j_end = w.end();
+          for (int j = w.next(w.begin()); j < j_end && ok; j = w.next(j + 1), ++n) {
+            const int t = 2 * n + pv, st = t % L::kStages;
+            wait_on(&kv_full[st], (t / L::kStages) & 1, 0x22);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (w.any(i)) {
-              wait_on(&q_full[i], pieces[i] & 1, 0x23);
-              tc_fence_after();
-              if (w.span[i].has(j)) scores(i, n, j);
-            }
-          wait_tile(2 * n + 1);
-        }
-        for (; j < j_end && ok; ++n) {  // V of step n has arrived
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (w.span[i].has(j)) {
-              const uint32_t to = tmem + 256 + i * 128, tp = tmem + i * 128;
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || !w.span[i].has(j)) continue;
               const bool first = j == w.span[i].lo;
-              if (first && pieces[i] > 0) wait_on(&o_empty[i], (pieces[i] - 1) & 1, 0x2A);
-              wait_on(&p_full[2 * i], steps[i] & 1, 0x24);
-              tc_fence_after();
-              if (!ok) break;
-              issue_cols<false, 0, 8 / L::kHalves>(leader, to, tp, stage_of(2 * n + 1), idesc_o, !first);
-              if (i == 0) commit(&kv_empty[(2 * n) % L::kStages]);  // K of this step, used before this loop turn
-              if constexpr (L::kHalves == 2) {
-                wait_on(&p_full[2 * i + 1], steps[i] & 1, 0x24);
+              if (!pv) {
+                if (first) wait_on(&q_full[i], pieces[i] & 1, 0x23);
+                wait_on(&s_free[i], (steps[i] & 1) ^ 1, 0x2F);
                 tc_fence_after();
                 if (!ok) break;
-                issue_cols<false, 4, 8>(leader, to, tp, stage_of(2 * n + 1), idesc_o, 1);
+                issue_rows<HD>(leader, tmem + i * 128, q_addr + i * L::kTileBytes, ring_addr + st * L::kTileBytes, ksteps);
+                commit(&s_full[i]);
+                if (j + 1 == w.span[i].hi) commit(&q_empty[i]);
+              } else {
+                if (first && pieces[i] > 0) wait_on(&o_empty[i], (pieces[i] - 1) & 1, 0x2A);
+                wait_on(&p_full[2 * i], steps[i] & 1, 0x24);
+                tc_fence_after();
+                if (!ok) break;
+                issue_cols<false>(leader, tmem + 256 + i * 64, tmem + 384 + i * 64, ring_addr + st * L::kTileBytes, idesc_o,
+                                  !first);
+                commit(&o_full[i]);
               }
               ++steps[i];
-              if (j + 1 == w.span[i].hi) commit(&o_full[i]);
-            } else if (i == 0) {
-              commit(&kv_empty[(2 * n) % L::kStages]);
             }
-            if (i == 1) {
-              commit(&kv_empty[(2 * n + 1) % L::kStages]);
-              if (jn < j_end) wait_tile(2 * n + 3);
-            } else if (jn < j_end) {
-              wait_tile(2 * n + 2);
-            }
-            if (jn < j_end && w.span[i].has(jn)) scores(i, n + 1, jn);
+            commit(&kv_empty[st]);
           }
-          j = jn;
-          jn = w.next(j + 1);
+          pieces[0] += w.any(0);
+          pieces[1] += w.any(1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&work_empty[it & 1]);
         }
-        n0 = n;
-        pieces[0] += w.any(0);
-        pieces[1] += w.any(1);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&work_empty[it & 1]);
+        // every product issued must be done before tensor memory is freed
+        commit(drain + pv);
+        mbar_wait(drain + pv, 0, p.status, 0x25);
+      } else {
+        // A wait that passes and a commit cost 100 to 150 cycles each, which the tensor core must not see: the tiles of
+        // the next step are waited for, and tiles released, between products, and S of tile 1 is followed at once by the
+        // wait for P of tile 0.
+        bool ok = true;
+        auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
+        };
+        auto stage_of = [&](int n) { return ring_addr + (n % L::kStages) * L::kTileBytes; };
+        auto wait_tile = [&](int n) { wait_on(&kv_full[n % L::kStages], (n / L::kStages) & 1, 0x22); };
+        int n0 = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};  // key tiles, and per query tile steps and pieces, so far
+        for (int it = 0; ok; ++it) {
+          const Work w = work_of(it);
+          if (__any_sync(0xffffffffu, w.piece < 0)) break;
+          const int j_end = w.end();
+          auto scores = [&](int i, int n, int j) {  // with the K tile j of step n
+            if (!ok) return;
+            issue_rows<HD>(leader, tmem + i * 128, q_addr + i * L::kTileBytes, stage_of(2 * n), ksteps);
+            commit(&s_full[i]);
+            if (j + 1 == w.span[i].hi) commit(&q_empty[i]);
+          };
+          int j = w.next(w.begin()), jn = w.next(j + 1), n = n0;
+          if (j < j_end) {
+            wait_tile(2 * n);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (w.any(i)) {
+                wait_on(&q_full[i], pieces[i] & 1, 0x23);
+                tc_fence_after();
+                if (w.span[i].has(j)) scores(i, n, j);
+              }
+            wait_tile(2 * n + 1);
+          }
+          for (; j < j_end && ok; ++n) {  // V of step n has arrived
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (w.span[i].has(j)) {
+                const uint32_t to = tmem + 256 + i * 128, tp = tmem + i * 128;
+                const bool first = j == w.span[i].lo;
+                if (first && pieces[i] > 0) wait_on(&o_empty[i], (pieces[i] - 1) & 1, 0x2A);
+                wait_on(&p_full[2 * i], steps[i] & 1, 0x24);
+                tc_fence_after();
+                if (!ok) break;
+                issue_cols<false, 0, 8 / L::kHalves>(leader, to, tp, stage_of(2 * n + 1), idesc_o, !first);
+                if (i == 0) commit(&kv_empty[(2 * n) % L::kStages]);  // K of this step, used before this loop turn
+                if constexpr (L::kHalves == 2) {
+                  wait_on(&p_full[2 * i + 1], steps[i] & 1, 0x24);
+                  tc_fence_after();
+                  if (!ok) break;
+                  issue_cols<false, 4, 8>(leader, to, tp, stage_of(2 * n + 1), idesc_o, 1);
+                }
+                ++steps[i];
+                if (j + 1 == w.span[i].hi) commit(&o_full[i]);
+              } else if (i == 0) {
+                commit(&kv_empty[(2 * n) % L::kStages]);
+              }
+              if (i == 1) {
+                commit(&kv_empty[(2 * n + 1) % L::kStages]);
+                if (jn < j_end) wait_tile(2 * n + 3);
+              } else if (jn < j_end) {
+                wait_tile(2 * n + 2);
+              }
+              if (jn < j_end && w.span[i].has(jn)) scores(i, n + 1, jn);
+            }
+            j = jn;
+            jn = w.next(j + 1);
+          }
+          n0 = n;
+          pieces[0] += w.any(0);
+          pieces[1] += w.any(1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&work_empty[it & 1]);
+        }
+        // every product issued must be done before tensor memory is freed
+        commit(drain);
+        mbar_wait(drain, 0, p.status, 0x25);
       }
-      // every product issued must be done before tensor memory is freed
-      commit(drain);
-      mbar_wait(drain, 0, p.status, 0x25);
     } else if (warp == kSoftmaxWarps + 2) {
       // ---------------------------------------------------------------- work
       int piece = static_cast<int>(blockIdx.x);
@@ -326,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
     regs_inc<kRegsSoftmax>();
     const int i = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * 128;
+    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * (L::kOwnP ? 64 : 128);
+    const uint32_t tp = L::kOwnP ? tmem + lanes + 384 + i * 64 : ts;
     uint8_t* stage = staging + warp * L::kStageBytes;
     bool ok = true;
     int step = 0, pieces = 0;  // of this query tile, so far
@@ -353,6 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         for (int c = 0; c < 4; ++c)
           tmem_ld_32x32b_x32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(reinterpret_cast<uint32_t*>(y) + c * 32));
         tmem_ld_wait();
+        if constexpr (L::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[i]);
+        }
         const int k0 = j * kTile;
         if constexpr (CAP) cap_tanh_all(y, p.sp);
         if constexpr (BIAS)
@@ -372,6 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         const float unit = BIAS ? 1.0f : CAP ? p.sp.cap2 : p.sp.scale2;  // what brings y to base 2
         top *= unit;
         const bool grow = top > m + kRescaleAt || (m == -INFINITY && top > -INFINITY);
+        if (L::kOwnP && step > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (step - 1) & 1, p.status, 0x27));
+          if (!ok) break;
+          tc_fence_after();
+        }
         if (__any_sync(0xffffffffu, grow)) {
           const float m2 = grow ? top : m;
           const float f = m == -INFINITY ? 0.f : ex2_approx(m - m2);
@@ -403,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
             else sum0 = f2_add(sum0, f2_make(a, b));
             w[c] = pack_bf16x2(a, b);  // P enters its product in bf16: half a step, 2^-9 of each weight
           }
-          tmem_st_32x32b_x32(ts + h * 32, w);
+          tmem_st_32x32b_x32(tp + h * 32, w);
           if (L::kHalves == 2 || h == 1) hand_over(h * (L::kHalves - 1));
         }
         const float2 su = f2_split(f2_add(sum0, sum1));
@@ -414,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       w = work_of(it + 1);
       r_next = range_of(w.piece);  // on its way during the output
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], pieces & 1, p.status, 0x27));
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (L::kOwnP ? step - 1 : pieces) & 1, p.status, 0x27));
         tc_fence_after();
         ++pieces;
       }
