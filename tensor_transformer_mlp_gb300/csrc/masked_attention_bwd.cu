@@ -11,11 +11,10 @@
 // (bf16, over the columns of the accumulator that they came from), and feed them to the products from there; shared
 // memory only ever holds tiles as they lie in global memory. Warp roles in both:
 //   warps 0-7   one row of the accumulators per thread, columns 0-63 (warps 0-3) or 64-127 (warps 4-7)
-//   warp 8      tensor copies of the tiles through two rings
+//   warp 8      tensor copies of the tiles through two rings; in the key pass it takes the CTA's next tile of keys
 //   warp 9      issues the products
-//   warp 10     takes the CTA's next piece of work (a tile of queries, or of keys) and, in the query pass, finds the key
-//               tiles that it sees
-//   warp 11     (key pass) the queries' lse and D, two tiles ahead
+//   warp 10     query pass: takes the CTA's next tile of queries and finds the key tiles that it sees;
+//               key pass: the queries' lse and D, two tiles ahead
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -83,7 +82,8 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
   auto all = [&](auto small, auto line) {
 #pragma unroll
     for (int c = 0; c < 64; c += 2) {
-      F2 v = f2_make(w[c], w[c + 1]), d = one;  // d: the cap's derivative
+      F2 v = f2_make(w[c], w[c + 1]);
+      [[maybe_unused]] F2 d = one;  // the cap's derivative
       if constexpr (CAP) {
         if constexpr (decltype(small)::value) {
           v = cap_tanh_small(v, sp);
@@ -564,8 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   uint64_t* st_empty = st_full + 2;
   uint64_t* work_full = st_empty + 2;
   uint64_t* work_empty = work_full + 2;
-  uint64_t* ending = work_empty + 2;
-  uint64_t* taken = ending + 1;
+  uint64_t* taken = work_empty + 2;
   uint64_t* drain = taken + 1;
   uint64_t* q_full = drain + 1;
   uint64_t* q_empty = q_full + L::kHeld;
@@ -573,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   uint64_t* g_empty = g_full + L::kPassing;
   int* works = reinterpret_cast<int*>(g_empty + L::kPassing);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(works + 2);
-  static_assert(16 + (18 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 8 + 4 <= L::kBarrierBytes, "barrier area");
+  static_assert(16 + (17 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 8 + 4 <= L::kBarrierBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kWorkWarps) {
@@ -616,8 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       // ---------------------------------------------------------------- loads
       bool ok = true;
       int n = 0, pieces = 0;
-      for (int it = 0; ok; ++it) {
-        const int piece = work_of(it);
+      int piece = static_cast<int>(blockIdx.x);
+      for (int it = 0;; ++it) {
+        if (lane == 0) {
+          works[it & 1] = piece;
+          mbar_arrive(&work_full[it & 1]);
+        }
         if (piece < 0) break;
         const KeyPlace at(p, piece);
         QueryTiles qt = at.queries(p);
@@ -647,8 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
           }
         }
         ++pieces;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ending);
+        // The next piece, in the place in `works` of the one before this, which is done with then.
+        int next = -1;
+        if (lane == 0 && ok && (it == 0 || mbar_wait(&work_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, 0x2D)))
+          next = take_work(response, taken, it & 1, p.status, 0x2C);
+        piece = __shfl_sync(0xffffffffu, next, 0);
       }
       if (!ok) {  // the copies in flight must land before shared memory goes away
         if (pieces > 0) mbar_wait(kv_full, (pieces - 1) & 1, p.status, 0x42);
@@ -709,21 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       umma_commit_by(leader, drain);  // every product issued is done before tensor memory is freed
       mbar_wait(drain, 0, p.status, 0x48);
     } else if (warp == kWorkWarps + 2) {
-      // ---------------------------------------------------------------- work
-      if (lane == 0) {
-        int piece = static_cast<int>(blockIdx.x);
-        for (int it = 0;; ++it) {
-          works[it & 1] = piece;
-          mbar_arrive(&work_full[it & 1]);
-          if (piece < 0) break;
-          // as in the query pass
-          piece = mbar_wait(ending, it & 1, p.status, 0x2D) &&
-                          (it == 0 || mbar_wait(&work_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, 0x2D))
-                      ? take_work(response, taken, it & 1, p.status, 0x2C)
-                      : -1;
-        }
-      }
-    } else {
       // ---------------------------------------------------------------- lse and D of the queries
       bool ok = true;
       int n = 0;

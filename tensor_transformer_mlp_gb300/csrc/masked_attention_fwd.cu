@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
     const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * (L::kOwnP ? 64 : 128);
     const uint32_t tp = L::kOwnP ? tmem + lanes + 384 + i * 64 : ts;
     uint8_t* stage = staging + warp * L::kStageBytes;
-    bool ok = true;
+    bool ok = true, s_ready = false;  // s_ready: seen ahead of time (kOwnP)
     int step = 0, pieces = 0;  // of this query tile, so far
     Work w = work_of(0);
     for (int it = 0; __all_sync(0xffffffffu, ok && w.piece >= 0); ++it) {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       float m = -INFINITY, l = 0.f;
       const Span mine = i ? w.span[1] : w.span[0];
       for (int j = mine.lo; j < mine.hi; ++j, ++step) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i], step & 1, p.status, 0x26));
+        ok = __all_sync(0xffffffffu, s_ready || mbar_wait(&s_full[i], step & 1, p.status, 0x26));
         if (!ok) break;
         tc_fence_after();
         auto hand_over = [&](int h) {  // part h of P is in tensor memory
@@ -423,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
 #pragma unroll
           for (int c = 0; c < 128; ++c) y[c] = static_cast<unsigned>(c - c0) < width ? y[c] : -INFINITY;
         }
+        bool o_ready = false;
+        if constexpr (L::kOwnP) o_ready = step > 0 && mbar_done(&o_full[i], (step - 1) & 1);
         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 128; c += 8)
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         top *= unit;
         const bool grow = top > m + kRescaleAt || (m == -INFINITY && top > -INFINITY);
         if (L::kOwnP && step > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (step - 1) & 1, p.status, 0x27));
+          ok = __all_sync(0xffffffffu, o_ready || mbar_wait(&o_full[i], (step - 1) & 1, p.status, 0x27));
           if (!ok) break;
           tc_fence_after();
         }
@@ -458,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         F2 sum0 = f2_make(0.f, 0.f), sum1 = sum0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          if (L::kOwnP && h == 1) s_ready = mbar_done(&s_full[i], (step + 1) & 1);
           uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
