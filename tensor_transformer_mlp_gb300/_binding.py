@@ -591,8 +591,10 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, eps: float = 1e-5, positions=
     lib = load_library()
     here, st = _where(_device(q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out), stream)
     with here:
-        q_out = q.new_empty(shape) if q_out is None else q_out
-        k_out = q.new_empty(kshape) if k_out is None else k_out
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty(kshape, dtype=q.dtype, device=q.device)
         strides += _heads(q_out, shape, q.dtype, "q_out") + _heads(k_out, kshape, q.dtype, "k_out")
         _check(lib.tpmlp_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
@@ -611,12 +613,16 @@ def qk_norm_rope_backward(q, k, gamma_q, gamma_k, cos, sin, dq_out, dk_out, eps:
     lib = load_library()
     here, st = _where(_device(q, k, gamma_q, gamma_k, cos, sin, positions, dq_out, dk_out, dq, dk), stream)
     with here:
-        dq = q.new_empty(shape) if dq is None else dq
-        dk = q.new_empty(kshape) if dk is None else dk
-        dgq, dgk = q.new_empty((2, hd), dtype=torch.float32).unbind()
+        device = q.device
+        if dq is None:
+            dq = torch.empty(shape, dtype=q.dtype, device=device)
+        if dk is None:
+            dk = torch.empty(kshape, dtype=q.dtype, device=device)
+        dgq = torch.empty(hd, dtype=torch.float32, device=device)
+        dgk = torch.empty(hd, dtype=torch.float32, device=device)
         strides += _heads(dq, shape, q.dtype, "dq") + _heads(dk, kshape, q.dtype, "dk")
         ws_bytes = lib.tpmlp_qk_norm_rope_backward_workspace_size(b, s, hd)
-        ws = q.new_empty(ws_bytes, dtype=torch.uint8)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         _check(lib.tpmlp_qk_norm_rope_backward(
             q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
             _ptr(positions), table_len, rot, ROPE_STYLE[style], dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
@@ -645,8 +651,9 @@ def masked_attention_forward(q, k, v, key_range, scale: float | None = None, sof
     lib = load_library()
     here, st = _where(_device(q, k, v, key_range, slopes, o), stream)
     with here:
-        o = q.new_empty(shape) if o is None else o
-        lse = q.new_empty((b, heads, s), dtype=torch.float32)
+        if o is None:
+            o = torch.empty(shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty((b, heads, s), dtype=torch.float32, device=q.device)
         strides += _heads(o, shape, q.dtype, "o")
         _check(lib.tpmlp_masked_attention_forward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
@@ -669,12 +676,16 @@ def masked_attention_backward(q, k, v, key_range, o, lse, do, scale: float | Non
     lib = load_library()
     here, st = _where(_device(q, k, v, key_range, slopes, o, lse, do, dq, dk, dv), stream)
     with here:
-        dq = q.new_empty(shape) if dq is None else dq
-        dk = q.new_empty(kshape) if dk is None else dk
-        dv = q.new_empty(kshape) if dv is None else dv
+        device = q.device
+        if dq is None:
+            dq = torch.empty(shape, dtype=dtype, device=device)
+        if dk is None:
+            dk = torch.empty(kshape, dtype=dtype, device=device)
+        if dv is None:
+            dv = torch.empty(kshape, dtype=dtype, device=device)
         strides += so + _heads(dq, shape, dtype, "dq") + _heads(dk, kshape, dtype, "dk") + _heads(dv, kshape, dtype, "dv")
         ws_bytes = lib.tpmlp_masked_attention_backward_workspace_size(b, s, heads)
-        ws = q.new_empty(ws_bytes, dtype=torch.uint8)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         _check(lib.tpmlp_masked_attention_backward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
             hd ** -0.5 if scale is None else scale, softcap, o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
