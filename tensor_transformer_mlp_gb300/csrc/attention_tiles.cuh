@@ -182,48 +182,11 @@ __device__ __forceinline__ const uint4* box_chunk(const uint8_t* box, int r, int
 
 // Writes 32 rows of an accumulator to a tensor of heads: warp `w` of a tile's four takes lanes 32 w .. 32 w + 31, row
 // row0 + 32 w + lane, the columns of boxes [box0, box1), scaled by f (per row) and rounded to bf16; zeros if not live.
-// They leave through the warp's part of `tile` (shared memory that nothing else uses any more) by tensor copies, which
-// cut rows past the sequence and columns past the head: written from the threads that hold the rows, 16 bytes here and
-// there, a tile took 6500 to 8200 cycles. Returns when shared memory has been read.
-__device__ __forceinline__ void store_head_rows(uint8_t* tile, const HeadMap& m, uint32_t acc, float f, bool live, int w,
-                                                int lane, int box0, int box1, int row0, int head, int seq, int s,
-                                                int head_dim) {
-  for (int x = box0; x < box1 && x * 64 < head_dim; ++x) {
-    uint8_t* box = tile + x * kBoxBytes + w * 32 * 128;
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-      uint32_t v[32];
-      tmem_ld_32x32b_x32(acc + x * 64 + c, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = __uint_as_float(v[8 * e + 2 * i]) * f, b = __uint_as_float(v[8 * e + 2 * i + 1]) * f;
-          u[i] = live ? pack_bf16x2(a, b) : 0u;
-        }
-        *box_chunk(box, lane, c / 8 + e) = make_uint4(u[0], u[1], u[2], u[3]);
-      }
-    }
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  const int row = row0 + w * 32;
-  if (lane == 0 && row < s) {
-    const int c1 = m.row == 1 ? row : (m.head == 1 ? head : seq);
-    const int c2 = m.row == 2 ? row : (m.head == 2 ? head : seq);
-    const int c3 = m.row == 3 ? row : (m.head == 3 ? head : seq);
-    for (int x = box0; x < box1 && x * 64 < head_dim; ++x)
-      tma_store_4d(&m.map, tile + x * kBoxBytes + w * 32 * 128, x * 64, c1, c2, c3);
-    bulk_commit_group();
-    bulk_wait_group_read<0>();
-  }
-}
-
-// The same one box at a time through a warp's own 4 KB. Returns once the accumulator has been read; the copies may still
-// read `stage` (a later call waits, and so must the warp's lane 0 before it ends: bulk_wait_group_read<0>).
-__device__ __forceinline__ void store_head_rows_staged(uint8_t* stage, const HeadMap& m, uint32_t acc, float f, bool live,
+// They leave box by box through the warp's own 4 KB at `stage` by tensor copies, which cut rows past the sequence and
+// columns past the head: written from the threads that hold the rows, 16 bytes here and there, a tile took 6500 to 8200
+// cycles. Returns once the accumulator has been read; the copies may still read `stage` (a later call waits, and so must
+// the warp's lane 0 before it gives the place away: bulk_wait_group_read<0>).
+__device__ __forceinline__ void store_head_rows(uint8_t* stage, const HeadMap& m, uint32_t acc, float f, bool live,
                                                        int w, int lane, int box0, int box1, int row0, int head, int seq,
                                                        int s, int head_dim) {
   const int row = row0 + w * 32;

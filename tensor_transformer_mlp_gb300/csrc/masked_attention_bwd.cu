@@ -58,7 +58,9 @@ struct BwdSmem {
   static constexpr int kHeld = HD == 128 && !QUERY_PASS ? 3 : 4;
   static constexpr int kPassing = HD == 128 ? 2 : 4;
   static constexpr int kStatBytes = 2 * 2 * kTile * 4;
-  static constexpr int kStageBytes = QUERY_PASS ? 32 * 128 : 0;  // of output, per working warp
+  // Of output, per working warp; in the key pass with heads of more than 64 columns V's place serves for it.
+  static constexpr bool kOwnStage = QUERY_PASS || HD == 64;
+  static constexpr int kStageBytes = kOwnStage ? 32 * 128 : 0;
   static constexpr int kTiles = (QUERY_PASS ? 0 : 2) + kHeld + kPassing;
   static constexpr int kBarrierBytes = 320;
   static constexpr int kBytes = kTiles * kTileBytes + kWorkWarps * kStageBytes + kStatBytes + kBarrierBytes;
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       }
       if (ok) {
         if (half < L::kBoxes)  // warps 4-7 take the second 64 columns
-          store_head_rows_staged(stage, p.dq, t_dq + lanes, p.scale, steps > 0, warp & 3, lane, half, half + 1, at.q0, at.head,
+          store_head_rows(stage, p.dq, t_dq + lanes, p.scale, steps > 0, warp & 3, lane, half, half + 1, at.q0, at.head,
                           at.seq, p.s, p.head_dim);
         tc_fence_before();
         __syncwarp();
@@ -551,11 +553,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   uint8_t* sv = sk + L::kTileBytes;
   uint8_t* q_ring = sv + L::kTileBytes;
   uint8_t* g_ring = q_ring + L::kHeld * L::kTileBytes;
-  float* stats = reinterpret_cast<float*>(g_ring + L::kPassing * L::kTileBytes);  // two of {-lse log2(e) [128], D[128]}
+  uint8_t* staging = L::kOwnStage ? g_ring + L::kPassing * L::kTileBytes : sv;
+  // two of {-lse log2(e) [128], D[128]}
+  float* stats = reinterpret_cast<float*>(g_ring + L::kPassing * L::kTileBytes + kWorkWarps * L::kStageBytes);
   uint4* response = reinterpret_cast<uint4*>(stats + L::kStatBytes / 4);
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(response + 1);
-  uint64_t* kv_empty = kv_full + 1;
-  uint64_t* s_full = kv_empty + 1;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(response + 1);
+  uint64_t* k_empty = k_full + 1;
+  uint64_t* v_full = k_empty + 1;
+  uint64_t* v_empty = v_full + 1;
+  uint64_t* s_full = v_empty + 1;
   uint64_t* p_full = s_full + 1;
   uint64_t* dp_full = p_full + 1;
   uint64_t* ds_full = dp_full + 1;
@@ -572,13 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   uint64_t* g_empty = g_full + L::kPassing;
   int* works = reinterpret_cast<int*>(g_empty + L::kPassing);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(works + 2);
-  static_assert(16 + (17 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 8 + 4 <= L::kBarrierBytes, "barrier area");
+  static_assert(16 + (19 + 2 * L::kHeld + 2 * L::kPassing) * 8 + 8 + 4 <= L::kBarrierBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kWorkWarps) {
     if (lane == 0) {
-      for (uint64_t* b = kv_full; b < g_empty + L::kPassing; ++b)
-        mbar_init(b, b == kv_empty || b == p_full || b == ds_full || b == st_empty || b == st_empty + 1 ? kWorkWarps
+      for (uint64_t* b = k_full; b < g_empty + L::kPassing; ++b)
+        mbar_init(b, (b == v_empty && !L::kOwnStage) || b == p_full || b == ds_full || b == st_empty || b == st_empty + 1 ? kWorkWarps
                      : b >= work_empty && b < work_empty + 2                                              ? kWorkWarps + 2
                                                                                                           : 1);
       fence_mbar_init();
@@ -614,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     if (warp == kWorkWarps) {
       // ---------------------------------------------------------------- loads
       bool ok = true;
-      int n = 0, pieces = 0;
+      int n = 0, pieces = 0, loaded = 0, loaded_v = 0;  // steps, pieces, and pieces with any steps
       int piece = static_cast<int>(blockIdx.x);
       for (int it = 0;; ++it) {
         if (lane == 0) {
@@ -633,20 +639,29 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
             mbar_arrive_expect_tx(&q_full[qs], L::kTileBytes);
             load_head_tile(q_ring + qs * L::kTileBytes, p.q, &q_full[qs], L::kBoxes, qt.tile * kTile, qt.head, at.seq);
           }
-          if (n == n0) {  // K and V, once the outputs that went through their place have left it
-            ok = __all_sync(0xffffffffu, mbar_wait(kv_empty, (pieces & 1) ^ 1, p.status, 0x42));
+          if (n == n0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(k_empty, (loaded & 1) ^ 1, p.status, 0x42));
             if (!ok) break;
             if (lane == 0) {
-              mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
-              load_head_tile(sk, p.k, kv_full, L::kBoxes, at.k0, at.kvh, at.seq);
-              load_head_tile(sv, p.v, kv_full, L::kBoxes, at.k0, at.kvh, at.seq);
+              mbar_arrive_expect_tx(k_full, L::kTileBytes);
+              load_head_tile(sk, p.k, k_full, L::kBoxes, at.k0, at.kvh, at.seq);
             }
+            ++loaded;
           }
           ok = __all_sync(0xffffffffu, mbar_wait(&g_empty[gs], ((n / L::kPassing) & 1) ^ 1, p.status, 0x41));
           if (!ok) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&g_full[gs], L::kTileBytes);
             load_head_tile(g_ring + gs * L::kTileBytes, p.d_o, &g_full[gs], L::kBoxes, qt.tile * kTile, qt.head, at.seq);
+          }
+          if (n == n0) {  // V, perhaps once the outputs that went through its place have left it
+            ok = __all_sync(0xffffffffu, mbar_wait(v_empty, ((L::kOwnStage ? loaded - 1 : pieces) & 1) ^ 1, p.status, 0x42));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(v_full, L::kTileBytes);
+              load_head_tile(sv, p.v, v_full, L::kBoxes, at.k0, at.kvh, at.seq);
+            }
+            ++loaded_v;
           }
         }
         ++pieces;
@@ -657,9 +672,11 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         piece = __shfl_sync(0xffffffffu, next, 0);
       }
       if (!ok) {  // the copies in flight must land before shared memory goes away
-        if (pieces > 0) mbar_wait(kv_full, (pieces - 1) & 1, p.status, 0x42);
+        if (loaded > 0) mbar_wait(k_full, (loaded - 1) & 1, p.status, 0x42);
+        if (loaded_v > 0) mbar_wait(v_full, (loaded_v - 1) & 1, p.status, 0x42);
         for (int k = max(0, n + 1 - L::kHeld); k <= n; ++k) mbar_wait(&q_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x42);
-        for (int k = max(0, n - L::kPassing); k < n; ++k) mbar_wait(&g_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x42);
+        for (int k = max(0, n + 1 - L::kPassing); k <= n; ++k)
+          mbar_wait(&g_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x42);
       }
     } else if (warp == kWorkWarps + 1) {
       // ---------------------------------------------------------------- products
@@ -684,20 +701,25 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         issue_rows<HD>(leader, t_dp, v_addr, g_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
         umma_commit_by(leader, dp_full);
       };
-      int n = 0, loaded = 0;
+      int n = 0, pieces = 0;  // steps, and pieces with any
       for (int it = 0; ok; ++it) {
         const int piece = work_of(it);
         if (piece < 0) break;
         QueryTiles qt = KeyPlace(p, piece).queries(p);
         bool more = qt.next();
         if (more) {
-          wait_on(kv_full, loaded & 1, 0x45);
-          ++loaded;
-          scores(n);
-          dprobs(n);
+          wait_on(k_full, pieces & 1, 0x45);
+          if (ok) scores(n);
+          wait_on(v_full, pieces & 1, 0x45);
+          if (ok) dprobs(n);
+          ++pieces;
         }
         for (bool first = true; more && ok; ++n, first = false) {
           more = qt.next();
+          if (!more) {  // S and dP of the last step are on their way: K, and V, may be replaced after them
+            umma_commit_by(leader, k_empty);
+            if (L::kOwnStage) umma_commit_by(leader, v_empty);
+          }
           wait_on(p_full, n & 1, 0x46);
           if (!ok) break;
           issue_cols<true>(leader, t_dv, tmem, g_addr + (n % L::kPassing) * L::kTileBytes, idesc_d, !first);
@@ -840,16 +862,21 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       }
       if (ok) {
         // warps 0-3 write dV, warps 4-7 dK, a key's row per thread
-        store_head_rows(half ? sk : sv, half ? p.dk : p.dv, (half ? t_dk : t_dv) + lanes, half ? p.scale : 1.0f, any,
-                        warp & 3, lane, 0, L::kBoxes, at.k0, at.kvh, at.seq, p.s, p.head_dim);
+        store_head_rows(staging + warp * 32 * 128, half ? p.dk : p.dv, (half ? t_dk : t_dv) + lanes,
+                               half ? p.scale : 1.0f, any, warp & 3, lane, 0, L::kBoxes, at.k0, at.kvh, at.seq, p.s,
+                               p.head_dim);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(kv_empty);
+          if (!L::kOwnStage) {
+            bulk_wait_group_read<0>();
+            mbar_arrive(v_empty);
+          }
           mbar_arrive(&work_empty[it & 1]);
         }
       }
     }
+    if (lane == 0) bulk_wait_group_read<0>();
   }
   tc_fence_before();
   __syncthreads();

@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       }
       if (ok) {
         const bool live = l > 0.f;
-        store_head_rows_staged(stage, p.o, to, live ? 1.0f / l : 0.f, live, warp & 3, lane, 0, L::kBoxes, at.q0 + i * kTile,
+        store_head_rows(stage, p.o, to, live ? 1.0f / l : 0.f, live, warp & 3, lane, 0, L::kBoxes, at.q0 + i * kTile,
                                at.head, at.seq, p.s, p.head_dim);
         tc_fence_before();
         __syncwarp();
