@@ -374,41 +374,42 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       const float slope2 = BIAS ? p.slopes[at.head] * kLog2e : 0.f;
       float D = 0.f;
       if (steps > 0) {
-        // The row of Q (warps 0-3) or d_o (warps 4-7) goes to tensor memory; warps 4-7 also form D = d_o . o.
-        const int mine = kn + half, os = vn % L::kPassing;
-        ok = mbar_wait(&k_full[mine % L::kHeld], (mine / L::kHeld) & 1, p.status, 0x3B);
-        if (half) ok = ok && mbar_wait(&v_full[os], (vn / L::kPassing) & 1, p.status, 0x3B);
-        const bool here = __all_sync(0xffffffffu, ok);
-        const uint8_t* src = k_ring + (mine % L::kHeld) * L::kTileBytes;
-        const uint8_t* so = v_ring + os * L::kTileBytes;
-        uint32_t x[HD / 2];
+        // The row of Q (warps 0-3) or d_o (warps 4-7) goes to tensor memory; each forms half of D = d_o . o.
+        const int os = vn % L::kPassing;
+        ok = mbar_wait(&k_full[kn % L::kHeld], (kn / L::kHeld) & 1, p.status, 0x3B) &&
+             mbar_wait(&k_full[(kn + 1) % L::kHeld], ((kn + 1) / L::kHeld) & 1, p.status, 0x3B) &&
+             mbar_wait(&v_full[os], (vn / L::kPassing) & 1, p.status, 0x3B);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          const uint8_t* sg = k_ring + ((kn + 1) % L::kHeld) * L::kTileBytes;
+          const uint8_t* src = half ? sg : k_ring + (kn % L::kHeld) * L::kTileBytes;
+          const uint8_t* so = v_ring + os * L::kTileBytes;
+          uint32_t x[HD / 2];
 #pragma unroll
-        for (int c = 0; c < HD / 8; ++c) {
-          const int box = (c >> 3) * kBoxBytes;
-          const uint4 v = here ? *box_chunk(src + box, rr, c & 7) : make_uint4(0, 0, 0, 0);
-          x[4 * c] = v.x;
-          x[4 * c + 1] = v.y;
-          x[4 * c + 2] = v.z;
-          x[4 * c + 3] = v.w;
-          if (half) {
-            const uint4 u = *box_chunk(so + box, rr, c & 7);
-            const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+          for (int c = 0; c < HD / 8; ++c) {
+            const uint4 v = *box_chunk(src + (c >> 3) * kBoxBytes, rr, c & 7);
+            x[4 * c] = v.x;
+            x[4 * c + 1] = v.y;
+            x[4 * c + 2] = v.z;
+            x[4 * c + 3] = v.w;
+          }
+          for (int c = 0; c < HD / 64; ++c)
+            tmem_st_32x32b_x32((half ? t_g : t_q) + lanes + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
+          float d[4] = {};
+#pragma unroll
+          for (int c = 0; c < HD / 16; ++c) {
+            const int at = half * (HD / 16) + c, box = (at >> 3) * kBoxBytes;
+            const uint4 g = *box_chunk(sg + box, rr, at & 7), u = *box_chunk(so + box, rr, at & 7);
+            const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 a = unpack_bf16x2(uw[e]), b = unpack_bf16x2(x[4 * c + e]);
-              D = fmaf(a.x, b.x, D);
-              D = fmaf(a.y, b.y, D);
+              const float2 a = unpack_bf16x2(uw[e]), b = unpack_bf16x2(gw[e]);
+              d[e] = fmaf(a.y, b.y, fmaf(a.x, b.x, d[e]));
             }
           }
+          dsum[half * kTile + rr] = (d[0] + d[1]) + (d[2] + d[3]);
+          tmem_st_wait();
         }
-        if (half) {
-          if (!live) D = 0.f;  // o is zero there; d_o may be anything
-          dsum[rr] = D;
-          if (row < p.s) p.dsum[at.stat + row] = D;
-        }
-        for (int c = 0; c < HD / 64; ++c)
-          tmem_st_32x32b_x32((half ? t_g : t_q) + lanes + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
-        tmem_st_wait();
         tc_fence_before();
         asm volatile("bar.sync 1, 256;" ::: "memory");  // all rows read, D written
         if (lane == 0) {
@@ -419,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
             mbar_arrive(&v_empty[os]);
           }
         }
-        D = dsum[rr];
+        D = live ? dsum[rr] + dsum[kTile + rr] : 0.f;  // without keys o is zero; d_o may be anything
+        if (half && row < p.s) p.dsum[at.stat + row] = D;
         kn += 2 + steps;
         vn += 1 + steps;
       }
