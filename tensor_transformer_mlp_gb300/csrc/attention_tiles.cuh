@@ -191,22 +191,19 @@ __device__ __forceinline__ void store_head_rows(uint8_t* stage, const HeadMap& m
                                                        int s, int head_dim) {
   const int row = row0 + w * 32;
   for (int x = box0; x < box1 && x * 64 < head_dim; ++x) {
-    uint32_t v[64];
+    uint32_t v[64], u[32];
     tmem_ld_32x32b_x32(acc + x * 64, *reinterpret_cast<uint32_t(*)[32]>(v));
     tmem_ld_32x32b_x32(acc + x * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-    if (lane == 0) bulk_wait_group_read<0>();
-    __syncwarp();
     tmem_ld_wait();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = __uint_as_float(v[8 * e + 2 * i]) * f, b = __uint_as_float(v[8 * e + 2 * i + 1]) * f;
-        u[i] = live ? pack_bf16x2(a, b) : 0u;
-      }
-      *box_chunk(stage, lane, e) = make_uint4(u[0], u[1], u[2], u[3]);
+    for (int e = 0; e < 32; ++e) {
+      const float a = __uint_as_float(v[2 * e]) * f, b = __uint_as_float(v[2 * e + 1]) * f;
+      u[e] = live ? pack_bf16x2(a, b) : 0u;
     }
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) *box_chunk(stage, lane, e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && row < s) {
