@@ -360,7 +360,12 @@ __device__ __forceinline__ void add_bias(float (&y)[N], float a, float slope2, f
   if (side != 0) {
     const float k = side > 0 ? -slope2 : slope2, off = k * d0;
 #pragma unroll
-    for (int c = 0; c < N; ++c) y[c] = fmaf(y[c], a, fmaf(k, static_cast<float>(c), off));
+    for (int c = 0; c < N; c += 2) {
+      const F2 b = f2_fma(f2_make(k, k), f2_make(static_cast<float>(c), static_cast<float>(c + 1)), f2_make(off, off));
+      const float2 v = f2_split(f2_fma(f2_make(y[c], y[c + 1]), f2_make(a, a), b));
+      y[c] = v.x;
+      y[c + 1] = v.y;
+    }
   } else {
 #pragma unroll
     for (int c = 0; c < N; ++c) y[c] = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), y[c] * a);

@@ -119,6 +119,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
   static_assert(16 + (24 + 2 * L::kStages) * 8 + 2 * sizeof(Work) + 4 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // With a bias, key tiles are counted from the sequence's end: most rows then meet their nearest keys first, and with
+  // them their maximum, where the other way every tile would raise it and have O rescaled.
+  const int ktiles = (p.s + kTile - 1) / kTile;
+  auto key_of = [&](int j) { return (BIAS ? ktiles - 1 - j : j) * kTile; };  // the first key of tile j
   // A piece's key tiles, by a whole warp; and the keys of this thread's row of a piece.
   auto find_work = [&](int piece) {
     Work w{piece, {}};
@@ -136,7 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       }
       lo = __reduce_min_sync(0xffffffffu, lo);
       hi = __reduce_max_sync(0xffffffffu, hi);
-      if (hi > 0) w.span[i] = Span{lo / kTile, (hi + kTile - 1) / kTile};
+      if (hi > 0) {
+        const int a = lo / kTile, b = (hi + kTile - 1) / kTile;
+        w.span[i] = BIAS ? Span{ktiles - b, ktiles - a} : Span{a, b};
+      }
     }
     return w;
   };
@@ -212,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
               break;
             }
             mbar_arrive_expect_tx(&kv_full[st], L::kTileBytes);
-            load_head_tile(ring + st * L::kTileBytes, kv ? p.v : p.k, &kv_full[st], L::kBoxes, j * kTile, at.kvh, at.seq);
+            load_head_tile(ring + st * L::kTileBytes, kv ? p.v : p.k, &kv_full[st], L::kBoxes, key_of(j), at.kvh, at.seq);
           }
         }
         if (!told) mbar_arrive(ending);
@@ -413,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_free[i]);
         }
-        const int k0 = j * kTile;
+        const int k0 = key_of(j);
         if constexpr (CAP) cap_tanh_all(y, p.sp);
         if constexpr (BIAS)
           add_bias(y, CAP ? p.sp.cap2 : p.sp.scale2, slope2, static_cast<float>(k0 - row), side_of(k0, kTile, row - lane));
