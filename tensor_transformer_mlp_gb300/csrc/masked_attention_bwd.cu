@@ -72,7 +72,8 @@ struct Flag {
   static constexpr bool value = V;
 };
 
-// 64 scores q.k to probabilities in place: 2^(y + shift(c)) for columns c, c + 1 (the pair of -lse in base 2). done(c, a,
+// 64 scores q.k to probabilities in place: 2^(y + shift(c, 0)) for columns c, c + 1 (the pair of -lse in base 2; shift(c, x)
+// is it with x added to both). done(c, a,
 // b) may change a pair and sees it before the cap's derivative is multiplied in.
 template <bool CAP, bool BIAS, typename Shift, typename Done>
 __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,
@@ -94,11 +95,11 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
           v = cap_tanh(v, sp, d);
         }
       }
-      F2 s = shift(c);
+      F2 s = shift(c, BIAS && decltype(line)::value ? off : 0.f);
       if constexpr (BIAS) {
         const float c0 = static_cast<float>(c), c1 = static_cast<float>(c + 1);
         if constexpr (decltype(line)::value)
-          s = f2_add(s, f2_fma(f2_make(k, k), f2_make(c0, c1), f2_make(off, off)));
+          s = f2_fma(f2_make(k, k), f2_make(c0, c1), s);
         else
           s = f2_add(s, f2_make(-slope2 * fabsf(d0 + c0), -slope2 * fabsf(d0 + c1)));
       }
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
-        probabilities<CAP, BIAS>(w, p.sp, slope2, k0, row, row - lane, [&](int) { return f2_make(-lse2, -lse2); });
+        probabilities<CAP, BIAS>(w, p.sp, slope2, k0, row, row - lane, [&](int, float add) { return f2_make(add - lse2, add - lse2); });
         if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + 64 <= r.y)) {
           const int c0 = r.x - k0;
           const unsigned width = static_cast<unsigned>(r.y - r.x);
@@ -800,9 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         auto pack_seen = [&](auto masked, unsigned lo, unsigned hi) {
           probabilities<CAP, BIAS>(
               w, p.sp, slope2, q0, key, key - lane,
-              [&](int c) {
+              [&](int c, float add) {
                 const float2 l = lse2[c / 2];
-                return f2_make(l.x, l.y);
+                return BIAS ? f2_add(f2_make(l.x, l.y), f2_make(add, add)) : f2_make(l.x, l.y);
               },
               [&](int c, float& a, float& b) {
                 if constexpr (decltype(masked)::value) {
