@@ -268,10 +268,10 @@ __device__ __forceinline__ int2 clip_range(int2 r, int s) {
 // What makes a score of q.k, in base 2 (y log2(e)).
 struct ScoreParams {
   float scale2;          // scale * log2(e)
-  float in_cap;          // scale / cap: x = q.k in_cap is the cap's argument
   float in_cap2;         // 2 log2(e) scale / cap: e^(2x) = 2^(q.k in_cap2)
   float cap2;            // cap * log2(e)
-  float small;           // |q.k| up to which |x| <= 1/2
+  float poly2[3], poly3[4];  // tanh(x) = q.k times a polynomial of (q.k)^2, for |x| <= 0.3 and |x| <= 1/2
+  float small2, small3;      // |q.k| up to which they hold; 0: never
 };
 
 inline ScoreParams score_params(float scale, float softcap) {
@@ -279,10 +279,20 @@ inline ScoreParams score_params(float scale, float softcap) {
   ScoreParams p{};
   p.scale2 = static_cast<float>(scale * log2e);
   if (softcap > 0.f) {
-    p.in_cap = static_cast<float>(static_cast<double>(scale) / softcap);
     p.in_cap2 = static_cast<float>(2.0 * scale * log2e / softcap);
     p.cap2 = static_cast<float>(softcap * log2e);
-    p.small = static_cast<float>(0.5 * softcap / scale);
+    const double fit2[3] = {0.9999960105, -0.332974805, 0.125225976};
+    const double fit3[4] = {0.9999976754, -0.3332065329, 0.1314513258, -0.04337221447};
+    const double in = static_cast<double>(scale) / softcap;
+    double u = in;
+    bool good = true;  // no coefficient and no power of q.k leaves fp32
+    for (int i = 0; i < 4; ++i, u *= in * in) {
+      good = good && u > 1e-34 && u < 1e34;
+      if (i < 3) p.poly2[i] = static_cast<float>(u * fit2[i]);
+      p.poly3[i] = static_cast<float>(u * fit3[i]);
+    }
+    p.small2 = good ? static_cast<float>(0.3 / in) : 0.f;
+    p.small3 = good ? static_cast<float>(0.5 / in) : 0.f;
   }
   return p;
 }
@@ -293,10 +303,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh(x) of the cap's argument in two ways, both off by a few 2^-24 in absolute terms, which the cap multiplies into the
-// exponent (tanh.approx's 2^-11 would not do). Any x: 1 - 2 / (1 + e^(2x)), two special-function operations. |x| <= 1/2:
-// x times a polynomial of degree 3 in x^2, fitted to tanh(x) / x for the smallest largest error of the product,
-// 1.3e-7 = 2.1 * 2^-24; on pairs, six operations of the FMA pipe for two scores.
+// tanh(x) of the cap's argument x = q.k scale / cap in two ways, both off by a few 2^-24 in absolute terms, which the cap
+// multiplies into the exponent (tanh.approx's 2^-11 would not do). Any x: 1 - 2 / (1 + e^(2x)), two special-function
+// operations. Small x: x times a polynomial of x^2, fitted to tanh(x) / x for the smallest largest error of the product,
+// with x's factor in the coefficients: degree 2 up to 0.3 (1.7e-7 = 2.9 * 2^-24) and 3 up to 1/2 (1.3e-7); on pairs, four
+// and five operations of the FMA pipe for two scores.
 __device__ __forceinline__ float cap_tanh(float qk, const ScoreParams& p) {
   return fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(qk * p.in_cap2)), 1.0f);
 }
@@ -311,11 +322,14 @@ __device__ __forceinline__ F2 cap_tanh(F2 qk, const ScoreParams& p, F2& d) {
   d = f2_mul(r, f2_mul(r, e4));
   return f2_fma(both(-2.0f), r, both(1.0f));
 }
-__device__ __forceinline__ F2 cap_tanh_small(F2 qk, const ScoreParams& p) {
+template <int N>
+__device__ __forceinline__ F2 cap_tanh_small(F2 qk, const float (&poly)[N]) {
   auto both = [](float v) { return f2_make(v, v); };
-  const F2 x = f2_mul(qk, both(p.in_cap)), z = f2_mul(x, x);
-  const F2 r = f2_fma(f2_fma(f2_fma(both(-0.04337248f), z, both(0.13145145f)), z, both(-0.33320655f)), z, both(0.99999768f));
-  return f2_mul(x, r);
+  const F2 z = f2_mul(qk, qk);
+  F2 r = both(poly[N - 1]);
+#pragma unroll
+  for (int i = N - 2; i >= 0; --i) r = f2_fma(r, z, both(poly[i]));
+  return f2_mul(qk, r);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -324,29 +338,37 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Whether all N scores of a warp's lanes may take the cap's polynomial.
+// The largest |q.k| of a warp's N scores in every lane.
 template <int N>
-__device__ __forceinline__ bool cap_is_small(const float (&y)[N], const ScoreParams& p) {
+__device__ __forceinline__ float largest(const float (&y)[N]) {
   float m[4] = {};
 #pragma unroll
   for (int c = 0; c < N; c += 8)
 #pragma unroll
     for (int e = 0; e < 4; ++e) m[e] = max3(m[e], fabsf(y[c + 2 * e]), fabsf(y[c + 2 * e + 1]));
-  return __all_sync(0xffffffffu, max3(fmaxf(m[0], m[1]), m[2], m[3]) <= p.small);
+  // as numbers of one sign their bits have their order
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max3(fmaxf(m[0], m[1]), m[2], m[3]))));
 }
 
-// tanh of N capped scores in place. The special-function unit, with an exponent of every score to take besides, is what
-// bounds the first way (masked rows of 4096, 32 heads of 128: forward 387 us); a warp whose scores are all small takes
-// the polynomial (306 us; with two of every eight pairs left to the first way 357 us).
+// tanh of N capped scores in place, by the cheapest form that all of a warp's allow. Causal forward of b2 s4096, 32 heads
+// of 128 on 8, cap 50 on scores of deviation 1, 30 on 2.6 and 30 on 16: 264, 303 and 398 us; without degree 2 299, 304
+// and 394 us, and the first way alone takes as long as the last everywhere. Taken together with the exponents, in copies
+// of that loop, the polynomials cost more than they save (248, 368 and 411 us; one loop for all 273, 276 and 483 us).
 template <int N>
 __device__ __forceinline__ void cap_tanh_all(float (&y)[N], const ScoreParams& p) {
-  if (cap_is_small(y, p)) {
+  auto all = [&](const auto& poly) {
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const float2 v = f2_split(cap_tanh_small(f2_make(y[c], y[c + 1]), p));
+      const float2 v = f2_split(cap_tanh_small(f2_make(y[c], y[c + 1]), poly));
       y[c] = v.x;
       y[c + 1] = v.y;
     }
+  };
+  const float most = largest(y);
+  if (most <= p.small2) {
+    all(p.poly2);
+  } else if (most <= p.small3) {
+    all(p.poly3);
   } else {
 #pragma unroll
     for (int c = 0; c < N; ++c) y[c] = cap_tanh(y[c], p);

@@ -89,7 +89,7 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
       [[maybe_unused]] F2 d = one;  // the cap's derivative
       if constexpr (CAP) {
         if constexpr (decltype(small)::value) {
-          v = cap_tanh_small(v, sp);
+          v = cap_tanh_small(v, sp.poly3);
           d = f2_sub(one, f2_mul(v, v));  // >= 3/4, so the difference loses nothing
         } else {
           v = cap_tanh(v, sp, d);
@@ -120,7 +120,7 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
     if (BIAS && side == 0) all(small, Flag<false>{});
     else all(small, Flag<true>{});
   };
-  if (CAP && !cap_is_small(w, sp)) both(Flag<false>{});
+  if (CAP && largest(w) > sp.small3) both(Flag<false>{});
   else both(Flag<true>{});
 }
 template <bool CAP, bool BIAS, typename Shift>
