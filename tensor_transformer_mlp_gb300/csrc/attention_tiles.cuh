@@ -2,6 +2,8 @@
 // loaded by tensor copies, key intervals, and the score function.
 #pragma once
 
+#include <cmath>
+
 #include "device_common.cuh"
 
 namespace tpmlp {
@@ -271,7 +273,7 @@ struct ScoreParams {
   float in_cap2;         // 2 log2(e) scale / cap: e^(2x) = 2^(q.k in_cap2)
   float cap2;            // cap * log2(e)
   float poly2[3], poly3[4];  // tanh(x) = q.k times a polynomial of (q.k)^2, for |x| <= 0.3 and |x| <= 1/2
-  float small2, small3;      // |q.k| up to which they hold; 0: never
+  float small2, small3;      // |q.k| up to which they hold
 };
 
 inline ScoreParams score_params(float scale, float softcap) {
@@ -284,15 +286,15 @@ inline ScoreParams score_params(float scale, float softcap) {
     const double fit2[3] = {0.9999960105, -0.332974805, 0.125225976};
     const double fit3[4] = {0.9999976754, -0.3332065329, 0.1314513258, -0.04337221447};
     const double in = static_cast<double>(scale) / softcap;
-    double u = in;
-    bool good = true;  // no coefficient and no power of q.k leaves fp32
-    for (int i = 0; i < 4; ++i, u *= in * in) {
-      good = good && u > 1e-34 && u < 1e34;
-      if (i < 3) p.poly2[i] = static_cast<float>(u * fit2[i]);
-      p.poly3[i] = static_cast<float>(u * fit3[i]);
-    }
-    p.small2 = good ? static_cast<float>(0.3 / in) : 0.f;
-    p.small3 = good ? static_cast<float>(0.5 / in) : 0.f;
+    auto fits = [&](int power) { return std::pow(in, power) > 1e-37 && std::pow(in, power) < 1e37; };
+    // Where a coefficient would leave fp32, the shorter polynomial, or x itself (x^2 / 3 < 2^-24 of it).
+    const bool two = fits(5), three = fits(7);
+    p.poly2[0] = static_cast<float>(in);
+    for (int i = 0; two && i < 3; ++i) p.poly2[i] = static_cast<float>(std::pow(in, 2 * i + 1) * fit2[i]);
+    p.small2 = static_cast<float>(std::fmin((two ? 0.3 : 4e-4) / in, 1e18));
+    for (int i = 0; i < 4; ++i)
+      p.poly3[i] = three ? static_cast<float>(std::pow(in, 2 * i + 1) * fit3[i]) : i < 3 ? p.poly2[i] : 0.f;
+    p.small3 = three ? static_cast<float>(0.5 / in) : p.small2;
   }
   return p;
 }

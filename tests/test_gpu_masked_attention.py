@@ -70,6 +70,8 @@ def _check(q, k, v, dO, ranges, cap=0.0, slopes=None, scale=None, backward=True)
     got, none = lse.double().cpu().numpy(), np.isneginf(f["lse"])
     assert np.array_equal(np.isneginf(got), none)
     tol = hd * 2.0 ** -24 * f["y_abs"] + 2.0 ** -20 * (1 + np.abs(np.where(none, 0, f["lse"]))) + 2.0 ** -21 * cap
+    if slopes is not None:  # a row's part and a column's part, up to 256 slope in the tiles near a row; three roundings
+        tol = tol + 3 * 2.0 ** -24 * 256 * np.abs(slopes).max()
     assert (np.abs(np.where(none, 0, got) - np.where(none, 0, f["lse"])) <= tol).all()
     if not backward:
         return o, lse
@@ -267,13 +269,34 @@ def test_more_pieces_than_resident_ctas(hd):
     _check(q, k, v, dO, oma.key_ranges(b, s, doc_ids=ids))
 
 
-@pytest.mark.parametrize("hd,std,cap", [(64, 4.0, 3.0), (128, 0.3, 100.0), (128, 3.0, 20.0)])
+@pytest.mark.parametrize("hd,std,cap", [(64, 4.0, 3.0), (64, 1.0, 10.0), (128, 0.3, 100.0), (128, 1.0, 9.0),
+                                        (128, 3.0, 20.0)])
 def test_both_ways_of_the_cap(hd, std, cap):
     # scores far past the cap, scores that it hardly bends, and tiles of either kind in one call
     q, k, v, dO = _draw(hd + 1, 1, 300, 2, 1, hd, std=std)
     if cap == 20.0:
         k[:, :128] *= 0.05
     _check(q, k, v, dO, oma.key_ranges(1, 300), cap=cap)
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("hd,causal,window", [(64, True, 0), (64, False, 0), (128, True, 150), (128, False, 150), (40, False, 1)])
+def test_steep_and_rising_slopes(hd, causal, window, cap):
+    # slopes that raise a row's maximum from tile to tile, and one that favours far keys
+    q, k, v, dO = _draw(hd + window, 1, 450, 4, 2, hd)
+    _check(q, k, v, dO, oma.key_ranges(1, 450, causal=causal, window=window), cap=cap, slopes=[3.0, 0.4, 0.0, -0.02])
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 30.0])
+@pytest.mark.parametrize("cap", [0.0, 1e-6, 1e9])
+def test_scales_out_of_the_ordinary(scale, cap):
+    # where a cap's polynomial would leave fp32 it is not used
+    q, k, v, dO = _draw(5, 1, 140, 2, 1, 64)
+    ranges = oma.key_ranges(1, 140)
+    lse = _check(q, k, v, dO, ranges, cap=cap, scale=scale, backward=scale < 1)[1]
+    if cap == 1e9:   # a cap that no score comes near changes nothing: x^2 / 3 < 1e-11
+        free = tp.masked_attention_forward(q, k, v, torch.from_numpy(ranges).cuda(), scale=scale)[1]
+        assert ((lse - free).abs() <= 2.0 ** -20 * (1 + free.abs())).all()
 
 
 def test_two_calls_at_once():
