@@ -8,17 +8,24 @@
 // after another:
 //   warps 0-3, 4-7  softmax of query tile 0 and 1, one row per thread (tensor-memory lane), and its output
 //   warp 8          one thread loads Q, and K and V tiles through a ring (tensor copies)
-//   warp 9          issues the products: S = Q K^T into 128 columns per query tile, and O += P V with P read from
-//                   tensor memory (bf16, over the columns of its S)
+//   warp 9          issues the products: S = Q K^T into 128 columns per query tile, and O += P V with P (bf16) read from
+//                   tensor memory
 //   warp 10         takes the next piece of work and finds the key tiles that it sees
-// The two tiles take turns: while one's softmax runs, the tensor core works on the other's P V and next S. (With an
-// issuing warp for each, both softmaxes fell into step and the tensor core waited for them.) S of a tile's next step
-// is issued after its P V, and the tensor core runs a thread's products in order, so P is never overwritten
-// early and a completed S also says that the P V before it is done: O may then be rescaled. That is done only when the maximum
-// grew by more than 2^8 (P then stays below 2^8 and l below 2^8 s, far inside fp32), so almost never: the statistics
-// stay those of one common m and the result does not depend on it. With heads of
-// more than 64 columns P is handed over in halves of 64 keys, so that its product starts while the second half's
-// exponents are still being taken.
+//   warp 11         heads of up to 64 columns: issues O += P V, and warp 9 only S
+// O is rescaled only when the maximum grew by more than 2^8 (P then stays below 2^8 and l below 2^8 s, far inside fp32),
+// so almost never: the statistics stay those of one common m and the result does not depend on it.
+//
+// Heads of more than 64 columns: S and O of two query tiles fill tensor memory, and P goes over its S. The tiles take
+// turns: while one's softmax runs, the tensor core works on the other's P V and next S. (With an issuing warp for each
+// tile, both softmaxes fell into step and the tensor core waited for them.) S of a tile's next step is issued after its
+// P V, and the tensor core runs a thread's products in order, so P is never overwritten early and a completed S also
+// says that the P V before it is done. P is handed over in halves of 64 keys, so that its product starts while the second
+// half's exponents are still being taken. Bound by shared memory, of which S = Q K^T, with both operands there, wants all
+// (2840 cycles a step of two tiles for 2048 of products): full masks, b2 s4096, 32 heads of 128, 366 us = 1500 TFLOP/s;
+// causal, b2 s2048, 66 us = 1040 TFLOP/s of the unmasked pairs.
+// Heads of up to 64 columns: the products take half of that and the softmax would wait for them, so P has columns of its
+// own and S of the next step is issued as soon as this one has been read (b2 s4096, 32 heads of 64: 250 us; as above
+// 299 us). Bound by the softmax: 2300 cycles a step, 1024 of them exponents.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,9 +58,9 @@ struct FwdCfg {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kStages = HD == 128 ? 4 : 8;
-  static constexpr bool kOwnP = HD == 64;            // P has tensor memory of its own, and the two products a warp each
-  static constexpr int kHalves = HD == 128 ? 2 : 1;  // parts in which P is handed over
-  static constexpr int kStageBytes = 32 * 128;       // of output, per softmax warp
+  static constexpr bool kOwnP = HD == 64;       // P has tensor memory of its own, and the two products a warp each
+  static constexpr int kHalves = kOwnP ? 1 : 2;  // parts in which P is handed over
+  static constexpr int kStageBytes = 32 * 128;   // of output, per softmax warp
   static constexpr int kBytes = (2 + kStages) * kTileBytes + kSoftmaxWarps * kStageBytes + 512;  // 229,888 at HD = 128
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
         };
-        int n = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
+        int n = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};  // key tiles, and per query tile steps and pieces, so far
         for (int it = 0; ok; ++it) {
           const Work w = work_of(it);
           if (__any_sync(0xffffffffu, w.piece < 0)) break;
@@ -329,14 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
                 wait_on(&p_full[2 * i], steps[i] & 1, 0x24);
                 tc_fence_after();
                 if (!ok) break;
-                issue_cols<false, 0, 8 / L::kHalves>(leader, to, tp, stage_of(2 * n + 1), idesc_o, !first);
+                issue_cols<false, 0, 4>(leader, to, tp, stage_of(2 * n + 1), idesc_o, !first);
                 if (i == 0) commit(&kv_empty[(2 * n) % L::kStages]);  // K of this step, used before this loop turn
-                if constexpr (L::kHalves == 2) {
-                  wait_on(&p_full[2 * i + 1], steps[i] & 1, 0x24);
-                  tc_fence_after();
-                  if (!ok) break;
-                  issue_cols<false, 4, 8>(leader, to, tp, stage_of(2 * n + 1), idesc_o, 1);
-                }
+                wait_on(&p_full[2 * i + 1], steps[i] & 1, 0x24);
+                tc_fence_after();
+                if (!ok) break;
+                issue_cols<false, 4, 8>(leader, to, tp, stage_of(2 * n + 1), idesc_o, 1);
                 ++steps[i];
                 if (j + 1 == w.span[i].hi) commit(&o_full[i]);
               } else if (i == 0) {
