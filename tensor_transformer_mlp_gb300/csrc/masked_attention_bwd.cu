@@ -193,12 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kWorkWarps) {
+    for (uint64_t* b = q_full + lane; b < v_empty + L::kPassing; b += 32)
+      mbar_init(b, b == q_full || b == s_free || b == ds_full ? kWorkWarps
+                   : b >= work_empty && b < work_empty + 2    ? kWorkWarps + 1
+                                                              : 1);
+    fence_mbar_init();
     if (lane == 0) {
-      for (uint64_t* b = q_full; b < v_empty + L::kPassing; ++b)
-        mbar_init(b, b == q_full || b == s_free || b == ds_full    ? kWorkWarps
-                     : b >= work_empty && b < work_empty + 2 ? kWorkWarps + 1
-                                                             : 1);
-      fence_mbar_init();
       tma_prefetch_desc(&p.q.map);
       tma_prefetch_desc(&p.k.map);
       tma_prefetch_desc(&p.v.map);
@@ -592,12 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kWorkWarps) {
+    for (uint64_t* b = k_full + lane; b < g_empty + L::kPassing; b += 32)
+      mbar_init(b, (b == v_empty && !L::kOwnStage) || b == p_full || b == ds_full || b == st_empty || b == st_empty + 1
+                       ? kWorkWarps
+                   : b >= work_empty && b < work_empty + 2 ? kWorkWarps + 2
+                                                           : 1);
+    fence_mbar_init();
     if (lane == 0) {
-      for (uint64_t* b = k_full; b < g_empty + L::kPassing; ++b)
-        mbar_init(b, (b == v_empty && !L::kOwnStage) || b == p_full || b == ds_full || b == st_empty || b == st_empty + 1 ? kWorkWarps
-                     : b >= work_empty && b < work_empty + 2                                              ? kWorkWarps + 2
-                                                                                                          : 1);
-      fence_mbar_init();
       tma_prefetch_desc(&p.q.map);
       tma_prefetch_desc(&p.k.map);
       tma_prefetch_desc(&p.v.map);

@@ -167,14 +167,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
   } else if (warp == kSoftmaxWarps + 2) {
     first = find_work(static_cast<int>(blockIdx.x));
   } else if (warp == kSoftmaxWarps) {
+    // a barrier to a lane: one after another they took a fifth of a short prompt (8.2 us against 6.6 in all)
+    for (uint64_t* bar = q_full + lane; bar < kv_empty + L::kStages; bar += 32)
+      mbar_init(bar, (bar >= p_full && bar < p_full + 4) || (bar >= o_empty && bar < o_empty + 2) ||
+                             (bar >= s_free && bar < s_free + 2)
+                         ? 4
+                     : bar >= work_empty && bar < work_empty + 2 ? kSoftmaxWarps + (L::kOwnP ? 2 : 1)
+                                                                 : 1);
+    fence_mbar_init();
     if (lane == 0) {
-      for (uint64_t* bar = q_full; bar < kv_empty + L::kStages; ++bar)
-        mbar_init(bar, (bar >= p_full && bar < p_full + 4) || (bar >= o_empty && bar < o_empty + 2) ||
-                               (bar >= s_free && bar < s_free + 2)
-                           ? 4
-                       : bar >= work_empty && bar < work_empty + 2 ? kSoftmaxWarps + (L::kOwnP ? 2 : 1)
-                                                                   : 1);
-      fence_mbar_init();
       tma_prefetch_desc(&p.q.map);
       tma_prefetch_desc(&p.k.map);
       tma_prefetch_desc(&p.v.map);
