@@ -80,8 +80,7 @@ struct Flag {
 };
 
 // 64 scores q.k to probabilities in place: 2^(y + shift(c, 0)) for columns c, c + 1 (the pair of -lse in base 2; shift(c, x)
-// is it with x added to both). done(c, a,
-// b) may change a pair and sees it before the cap's derivative is multiplied in.
+// is it with x added to both). done(c, a, b) may change a pair and sees it before the cap's derivative is multiplied in.
 template <bool CAP, bool BIAS, typename Shift, typename Done>
 __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,
                                               int row0, Shift shift, Done done) {
