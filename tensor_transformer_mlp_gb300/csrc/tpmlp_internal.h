@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 
 namespace tpmlp {
 
@@ -217,6 +218,17 @@ inline bool good_head_strides(const HeadView& v, int64_t s) {
 inline bool heads_apart(const HeadView& v, int64_t tokens, int heads, int hd) {
   if (v.ld < hd || (heads > 1 && v.hs < hd)) return tokens <= 1 && (heads <= 1 || v.hs >= hd);
   return heads <= 1 || (v.ld - hd) / v.hs >= heads - 1 || (v.hs - hd) / v.ld >= tokens - 1;
+}
+
+// Whether one of `outputs` is one of `others`, or twice among them.
+inline bool shared_tensor(std::initializer_list<const void*> outputs, std::initializer_list<const void*> others) {
+  for (const void* const* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const void* const* p = outputs.begin(); p != o; ++p)
+      if (*p == *o) return true;
+    for (const void* p : others)
+      if (p == *o) return true;
+  }
+  return false;
 }
 
 // Masked attention (tpmlp_masked_attention_*): everything but the gradients. Sizes are checked by the caller; the tiles

@@ -219,6 +219,7 @@ tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const 
   MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
   MATT_TRY(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
   if (!aligned(slopes, 4)) return err(TPMLP_ERR_ALIGN, "slopes not 4-byte aligned");
+  if (shared_tensor({o, lse}, {q, k, v, key_range, slopes})) return err(TPMLP_ERR_INVALID, "o or lse is another tensor");
   DeviceCtx ctx;
   MATT_CUDA(get_device_ctx(&ctx), "device context");
   MaskedAttention a{{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(k), ld_k, hs_k},
@@ -252,6 +253,8 @@ tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const
   const size_t need = tpmlp_masked_attention_backward_workspace_size(b, s, heads);
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "masked attention backward workspace too small");
   if (!aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
+  if (shared_tensor({dq, dk, dv, workspace}, {q, k, v, key_range, slopes, o, lse, d_o}))
+    return err(TPMLP_ERR_INVALID, "dq, dk, dv or the workspace is another tensor");
   DeviceCtx ctx;
   MATT_CUDA(get_device_ctx(&ctx), "device context");
   MaskedAttention a{{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(k), ld_k, hs_k},

@@ -129,6 +129,40 @@ def test_rope_refusals(lib):
     assert back(strides=good + (256, 64, 64, 64)) == SHAPE
 
 
+def test_outputs_that_are_inputs_are_refused(lib):
+    at = [FAKE + 4096 * n for n in range(12)]
+    good = (256, 64, 128, 64, 256, 64, 128, 64)
+
+    def forward(**kw):
+        ptrs = dict(q=at[0], k=at[1], v=at[2], rng=at[3], o=at[4], lse=at[5])
+        return fwd(lib, **{**ptrs, **kw})
+    for name in ("q", "k", "v"):
+        assert forward(o=dict(q=at[0], k=at[1], v=at[2])[name]) == INVALID, name
+    assert forward(lse=at[4]) == INVALID and forward(lse=at[3]) == INVALID and forward(slopes=at[5]) == INVALID
+
+    size = lib.tpmlp_masked_attention_backward_workspace_size(2, 16, 4)
+
+    def backward(dq=at[6], dk=at[7], dv=at[8], ws=at[9]):
+        return lib.tpmlp_masked_attention_backward(at[0], at[1], at[2], at[3], None, 0.1, 0.0, at[4], at[5], at[10], dq, dk,
+                                                   dv, 2, 16, 4, 2, 64, *(good[:4] + good[2:4] + good[:2] + good[:4]
+                                                                          + good[2:4]), BF16, ws, size, None)
+    assert backward(dq=at[0]) == INVALID and backward(dq=at[10]) == INVALID and backward(dk=at[8]) == INVALID
+    assert backward(dv=at[2]) == INVALID and backward(ws=at[5]) == INVALID
+
+    def rope(qo=at[8], ko=at[9], strides=good):
+        return lib.tpmlp_qk_norm_rope(at[0], at[1], at[2], at[3], 1e-5, at[4], at[5], None, 8, 64, 0, qo, ko, 1, 8, 4, 2, 64,
+                                      *strides, BF16, None)
+    assert rope(qo=at[1]) == INVALID and rope(ko=at[0]) == INVALID and rope(qo=at[9]) == INVALID and rope(ko=at[2]) == INVALID
+    assert rope(qo=at[0], strides=good[:4] + (512, 64, 128, 64)) == INVALID    # in place, but elsewhere
+
+    def rope_back(dq=at[8], dk=at[9], dgq=at[10], ws=at[11], strides=good + good[4:]):
+        return lib.tpmlp_qk_norm_rope_backward(at[0], at[1], at[2], at[3], 1e-5, at[4], at[5], None, 8, 64, 0, at[6], at[7],
+                                               dq, dk, dgq, at[10] + 2048, 1, 8, 4, 2, 64, *strides, BF16, ws, 1 << 20, None)
+    assert rope_back(dq=at[1]) == INVALID and rope_back(dk=at[6]) == INVALID and rope_back(dq=at[9]) == INVALID
+    assert rope_back(dgq=at[2]) == INVALID and rope_back(ws=at[8]) == INVALID
+    assert rope_back(dq=at[6], strides=good + (512, 64, 128, 64)) == INVALID
+
+
 def test_binding_refuses_what_the_library_cannot_see():
     import tensor_transformer_mlp_gb300 as tp
     q = torch.zeros(1, 8, 2, 64, dtype=torch.bfloat16)
