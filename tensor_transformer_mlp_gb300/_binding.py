@@ -179,6 +179,13 @@ def _heads(t: torch.Tensor, shape: tuple[int, int, int, int], dtype: torch.dtype
     return ss if s > 1 else sb if b > 1 else max(heads * hd, 8), sh if heads > 1 else hd
 
 
+def _out(t, shape: tuple[int, int, int, int], like: torch.Tensor, name: str):
+    """The output `t`, or a new contiguous one of like's type, and its (token, head) strides."""
+    if t is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device), (shape[2] * shape[3], shape[3])
+    return t, _heads(t, shape, like.dtype, name)
+
+
 def _dense(t: torch.Tensor, shape: tuple[int, ...], dtype: torch.dtype, name: str) -> None:
     if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
@@ -591,15 +598,12 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, eps: float = 1e-5, positions=
     lib = load_library()
     here, st = _where(_device(q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out), stream)
     with here:
-        if q_out is None:
-            q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        if k_out is None:
-            k_out = torch.empty(kshape, dtype=q.dtype, device=q.device)
-        strides += _heads(q_out, shape, q.dtype, "q_out") + _heads(k_out, kshape, q.dtype, "k_out")
+        q_out, sq = _out(q_out, shape, q, "q_out")
+        k_out, sk = _out(k_out, kshape, q, "k_out")
         _check(lib.tpmlp_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
             _ptr(positions), table_len, rot, ROPE_STYLE[style], q_out.data_ptr(), k_out.data_ptr(), shape[0], shape[1],
-            shape[2], kshape[2], shape[3], *strides, _dt(q), st))
+            shape[2], kshape[2], shape[3], *strides, *sq, *sk, _dt(q), st))
     return q_out, k_out
 
 
@@ -614,20 +618,17 @@ def qk_norm_rope_backward(q, k, gamma_q, gamma_k, cos, sin, dq_out, dk_out, eps:
     here, st = _where(_device(q, k, gamma_q, gamma_k, cos, sin, positions, dq_out, dk_out, dq, dk), stream)
     with here:
         device = q.device
-        if dq is None:
-            dq = torch.empty(shape, dtype=q.dtype, device=device)
-        if dk is None:
-            dk = torch.empty(kshape, dtype=q.dtype, device=device)
+        dq, sq = _out(dq, shape, q, "dq")
+        dk, sk = _out(dk, kshape, q, "dk")
         dgq = torch.empty(hd, dtype=torch.float32, device=device)
         dgk = torch.empty(hd, dtype=torch.float32, device=device)
-        strides += _heads(dq, shape, q.dtype, "dq") + _heads(dk, kshape, q.dtype, "dk")
         ws_bytes = lib.tpmlp_qk_norm_rope_backward_workspace_size(b, s, hd)
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         _check(lib.tpmlp_qk_norm_rope_backward(
             q.data_ptr(), k.data_ptr(), gamma_q.data_ptr(), gamma_k.data_ptr(), eps, cos.data_ptr(), sin.data_ptr(),
             _ptr(positions), table_len, rot, ROPE_STYLE[style], dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(), b, s, heads, kshape[2], hd, *strides, _dt(q), ws.data_ptr(),
-            ws_bytes, st))
+            dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(), b, s, heads, kshape[2], hd, *strides, *sq, *sk, _dt(q),
+            ws.data_ptr(), ws_bytes, st))
     return dq, dk, dgq, dgk
 
 
@@ -651,14 +652,12 @@ def masked_attention_forward(q, k, v, key_range, scale: float | None = None, sof
     lib = load_library()
     here, st = _where(_device(q, k, v, key_range, slopes, o), stream)
     with here:
-        if o is None:
-            o = torch.empty(shape, dtype=q.dtype, device=q.device)
+        o, so = _out(o, shape, q, "o")
         lse = torch.empty((b, heads, s), dtype=torch.float32, device=q.device)
-        strides += _heads(o, shape, q.dtype, "o")
         _check(lib.tpmlp_masked_attention_forward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
             hd ** -0.5 if scale is None else scale, softcap, o.data_ptr(), lse.data_ptr(), b, s, heads, kshape[2], hd,
-            *strides, _dt(q), st))
+            *strides, *so, _dt(q), st))
     return o, lse
 
 
@@ -676,18 +675,14 @@ def masked_attention_backward(q, k, v, key_range, o, lse, do, scale: float | Non
     lib = load_library()
     here, st = _where(_device(q, k, v, key_range, slopes, o, lse, do, dq, dk, dv), stream)
     with here:
-        device = q.device
-        if dq is None:
-            dq = torch.empty(shape, dtype=dtype, device=device)
-        if dk is None:
-            dk = torch.empty(kshape, dtype=dtype, device=device)
-        if dv is None:
-            dv = torch.empty(kshape, dtype=dtype, device=device)
-        strides += so + _heads(dq, shape, dtype, "dq") + _heads(dk, kshape, dtype, "dk") + _heads(dv, kshape, dtype, "dv")
+        dq, sq = _out(dq, shape, q, "dq")
+        dk, sk = _out(dk, kshape, q, "dk")
+        dv, sv = _out(dv, kshape, q, "dv")
         ws_bytes = lib.tpmlp_masked_attention_backward_workspace_size(b, s, heads)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
         _check(lib.tpmlp_masked_attention_backward(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), key_range.data_ptr(), _ptr(slopes),
             hd ** -0.5 if scale is None else scale, softcap, o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), b, s, heads, kshape[2], hd, *strides, _dt(q), ws.data_ptr(), ws_bytes, st))
+            dk.data_ptr(), dv.data_ptr(), b, s, heads, kshape[2], hd, *strides, *so, *sq, *sk, *sv, _dt(q), ws.data_ptr(),
+            ws_bytes, st))
     return dq, dk, dv
