@@ -81,11 +81,12 @@ struct Flag {
 
 // 64 scores q.k to probabilities in place: 2^(y + shift(c, 0)) for columns c, c + 1 (the pair of -lse in base 2; shift(c, x)
 // is it with x added to both). done(c, a, b) may change a pair and sees it before the cap's derivative is multiplied in.
-template <bool CAP, bool BIAS, typename Shift, typename Done>
+// With a bias: side as in side_of, off the bias of the columns' first place where they lie on one side of the row, and
+// TILTED if shift has the rest of it already.
+template <bool CAP, bool BIAS, bool TILTED, typename Shift, typename Done>
 __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,
-                                              int row0, Shift shift, Done done) {
-  const int side = BIAS ? side_of(col0, 64, row0) : 0;
-  const float d0 = static_cast<float>(col0 - row), k = side > 0 ? -slope2 : slope2, off = k * d0;
+                                              int side, float off, Shift shift, Done done) {
+  const float d0 = static_cast<float>(col0 - row), k = side > 0 ? -slope2 : slope2;
   const float unit = CAP ? sp.cap2 : sp.scale2;
   const F2 u2 = f2_make(unit, unit), one = f2_make(1.0f, 1.0f);
   auto all = [&](auto small, auto line) {
@@ -104,9 +105,9 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
       F2 s = shift(c, BIAS && decltype(line)::value ? off : 0.f);
       if constexpr (BIAS) {
         const float c0 = static_cast<float>(c), c1 = static_cast<float>(c + 1);
-        if constexpr (decltype(line)::value)
+        if constexpr (decltype(line)::value && !TILTED)
           s = f2_fma(f2_make(k, k), f2_make(c0, c1), s);
-        else
+        else if constexpr (!decltype(line)::value)
           s = f2_add(s, f2_make(-slope2 * fabsf(d0 + c0), -slope2 * fabsf(d0 + c1)));
       }
       const float2 z = f2_split(f2_fma(v, u2, s));
@@ -128,11 +129,6 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
   };
   if (CAP && largest(w) > sp.small3) both(Flag<false>{});
   else both(Flag<true>{});
-}
-template <bool CAP, bool BIAS, typename Shift>
-__device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams& sp, float slope2, int col0, int row,
-                                              int row0, Shift shift) {
-  probabilities<CAP, BIAS>(w, sp, slope2, col0, row, row0, shift, [](int, float&, float&) {});
 }
 
 // ------------------------------------------------------------------ query pass
@@ -445,7 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
-        probabilities<CAP, BIAS>(w, p.sp, slope2, k0, row, row - lane, [&](int, float add) { return f2_make(add - lse2, add - lse2); });
+        const int side = BIAS ? side_of(k0, 64, row - lane) : 0;
+        probabilities<CAP, BIAS, false>(
+            w, p.sp, slope2, k0, row, side, (side > 0 ? -slope2 : slope2) * static_cast<float>(k0 - row),
+            [&](int, float add) { return f2_make(add - lse2, add - lse2); }, [](int, float&, float&) {});
         if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + 64 <= r.y)) {
           const int c0 = r.x - k0;
           const unsigned width = static_cast<unsigned>(r.y - r.x);
@@ -563,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   uint8_t* q_ring = sv + L::kTileBytes;
   uint8_t* g_ring = q_ring + L::kHeld * L::kTileBytes;
   uint8_t* staging = L::kOwnStage ? g_ring + L::kPassing * L::kTileBytes : sv;
-  // two of {-lse log2(e) [128], D[128]}
+  // two of {-lse log2(e), with a bias its part within the tile added, [128], D[128]}
   float* stats = reinterpret_cast<float*>(g_ring + L::kPassing * L::kTileBytes + kWorkWarps * L::kStageBytes);
   uint4* response = reinterpret_cast<uint4*>(stats + L::kStatBytes / 4);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(response + 1);
@@ -764,6 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
             l[e] = q + e < p.s ? -p.lse[at + e] * kLog2e : 0.f;  // queries without keys: +inf, and masked
             d[e] = q + e < p.s ? p.dsum[at + e] : 0.f;
           }
+          // Where queries and keys are different tiles the bias grows with the query: its part within the tile.
+          if (BIAS && qt.tile * kTile != place.k0) {
+            const float slope2 = p.slopes[qt.head] * kLog2e, k = qt.tile * kTile > place.k0 ? -slope2 : slope2;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l[e] = fmaf(k, static_cast<float>(lane * 4 + e), l[e]);
+          }
           ok = __all_sync(0xffffffffu, mbar_wait(&st_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status, 0x49));
           if (!ok) break;
           float* st = stats + (n & 1) * 2 * kTile;
@@ -806,8 +811,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         // P as it is, packed in x, and times the cap's derivative in w
         uint32_t x[32];
         auto pack_seen = [&](auto masked, unsigned lo, unsigned hi) {
-          probabilities<CAP, BIAS>(
-              w, p.sp, slope2, q0, key, key - lane,
+          const int apart = qt.tile * kTile - at.k0;
+          probabilities<CAP, BIAS, true>(
+              w, p.sp, slope2, q0, key, apart, (apart > 0 ? -slope2 : slope2) * static_cast<float>(apart + at.k0 - key),
               [&](int c, float add) {
                 const float2 l = lse2[c / 2];
                 return BIAS ? f2_add(f2_make(l.x, l.y), f2_make(add, add)) : f2_make(l.x, l.y);
