@@ -385,7 +385,8 @@ __device__ __forceinline__ void add_bias(float (&y)[N], float a, float slope2, f
     const float k = side > 0 ? -slope2 : slope2, off = k * d0;
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const F2 b = f2_fma(f2_make(k, k), f2_make(static_cast<float>(c), static_cast<float>(c + 1)), f2_make(off, off));
+      // c stands in the instruction; as a pair it would be two moves (forward with window and bias 112 -> 106 us)
+      const F2 b = f2_make(fmaf(k, static_cast<float>(c), off), fmaf(k, static_cast<float>(c + 1), off));
       const float2 v = f2_split(f2_fma(f2_make(y[c], y[c + 1]), f2_make(a, a), b));
       y[c] = v.x;
       y[c + 1] = v.y;

@@ -105,9 +105,11 @@ __device__ __forceinline__ void probabilities(float (&w)[64], const ScoreParams&
       F2 s = shift(c, BIAS && decltype(line)::value ? off : 0.f);
       if constexpr (BIAS) {
         const float c0 = static_cast<float>(c), c1 = static_cast<float>(c + 1);
-        if constexpr (decltype(line)::value && !TILTED)
-          s = f2_fma(f2_make(k, k), f2_make(c0, c1), s);
-        else if constexpr (!decltype(line)::value)
+        if constexpr (decltype(line)::value && !TILTED) {
+          const float2 s1 = f2_split(s);
+          s = f2_make(fmaf(k, c0, s1.x), fmaf(k, c1, s1.y));
+        }
+        if constexpr (!decltype(line)::value)
           s = f2_add(s, f2_make(-slope2 * fabsf(d0 + c0), -slope2 * fabsf(d0 + c1)));
       }
       const float2 z = f2_split(f2_fma(v, u2, s));
