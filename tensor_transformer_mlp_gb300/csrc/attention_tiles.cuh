@@ -402,6 +402,12 @@ __device__ __forceinline__ int side_of(int col0, int n, int row0) {
   return col0 >= row0 + 31 ? 1 : col0 + n - 1 <= row0 ? -1 : 0;
 }
 
+// Bits [lo, hi) of a word, cut to 0..32.
+__device__ __forceinline__ unsigned bit_range(int lo, int hi) {
+  const int from = min(max(lo, 0), 32), to = min(max(hi, 0), 32);
+  return from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+}
+
 // Bit b of the result in lane i is bit i of lane b's word.
 __device__ __forceinline__ unsigned transpose_bits(unsigned x) {
   const int lane = threadIdx.x & 31;

@@ -448,10 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
             w, p.sp, slope2, k0, row, side, (side > 0 ? -slope2 : slope2) * static_cast<float>(k0 - row),
             [&](int, float add) { return f2_make(add - lse2, add - lse2); }, [](int, float&, float&) {});
         if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + 64 <= r.y)) {
-          const int c0 = r.x - k0;
-          const unsigned width = static_cast<unsigned>(r.y - r.x);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) w[c] = static_cast<unsigned>(c - c0) < width ? w[c] : 0.f;
+          for (int c = 0; c < 64; c += 32) {
+            const unsigned seen = bit_range(r.x - k0 - c, r.y - k0 - c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[c + e] = (seen >> e) & 1 ? w[c + e] : 0.f;
+          }
         }
         ok = __all_sync(0xffffffffu, mbar_wait(dp_full, step & 1, p.status, 0x39));
         if (!ok) break;
@@ -835,8 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
           // Each lane marks which of the warp's 32 keys two queries see; transposed, which queries see its own key.
           auto mark = [&](int q) {
             const int2 r = q < p.s ? clip_range(p.range[at.base + q], p.s) : make_int2(0, 0);
-            const int from = min(max(r.x - (key - lane), 0), 32), to = min(max(r.y - (key - lane), 0), 32);
-            return from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+            return bit_range(r.x - (key - lane), r.y - (key - lane));
           };
           const unsigned lo = transpose_bits(mark(q0 + lane)), hi = transpose_bits(mark(q0 + 32 + lane));
           pack_seen(Flag<true>{}, lo, hi);

@@ -431,10 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         if constexpr (BIAS)
           add_bias(y, CAP ? p.sp.cap2 : p.sp.scale2, slope2, static_cast<float>(k0 - row), side_of(k0, kTile, row - lane));
         if (!__all_sync(0xffffffffu, r.x <= k0 && k0 + kTile <= r.y)) {
-          const int c0 = r.x - k0;
-          const unsigned width = static_cast<unsigned>(r.y - r.x);
 #pragma unroll
-          for (int c = 0; c < 128; ++c) y[c] = static_cast<unsigned>(c - c0) < width ? y[c] : -INFINITY;
+          for (int c = 0; c < 128; c += 32) {
+            const unsigned seen = bit_range(r.x - k0 - c, r.y - k0 - c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[c + e] = (seen >> e) & 1 ? y[c + e] : -INFINITY;
+          }
         }
         bool o_ready = false;
         if constexpr (L::kOwnP) o_ready = step > 0 && mbar_done(&o_full[i], (step - 1) & 1);
