@@ -353,7 +353,7 @@ __device__ __forceinline__ float largest(const float (&y)[N]) {
 }
 
 // tanh of N capped scores in place, by the cheapest form that all of a warp's allow. Causal forward of b2 s4096, 32 heads
-// of 128 on 8, cap 50 on scores of deviation 1, 30 on 2.6 and 30 on 16: 264, 303 and 398 us; without degree 2 299, 304
+// of 128 on 8, cap 50 on scores of deviation 1, 30 on 2.6 and 30 on 16: 264, 303 and 398 us then; without degree 2 299, 304
 // and 394 us, and the first way alone takes as long as the last everywhere. Taken together with the exponents, in copies
 // of that loop, the polynomials cost more than they save (248, 368 and 411 us; one loop for all 273, 276 and 483 us).
 template <int N>
