@@ -189,7 +189,7 @@ __device__ __forceinline__ const uint4* box_chunk(const uint8_t* box, int r, int
 // cycles. Returns once the accumulator has been read; the copies may still read `stage` (a later call waits, and so must
 // the warp's lane 0 before it gives the place away: bulk_wait_group_read<0>).
 __device__ __forceinline__ void store_head_rows(uint8_t* stage, const HeadMap& m, uint32_t acc, float f, bool live,
-                                                       int w, int lane, int box0, int box1, int row0, int head, int seq,
+                                                int w, int lane, int box0, int box1, int row0, int head, int seq,
                                                        int s, int head_dim) {
   const int row = row0 + w * 32;
   for (int x = box0; x < box1 && x * 64 < head_dim; ++x) {

@@ -799,7 +799,24 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       QueryTiles qt = at.queries(p);
       bool any = false;
       for (; qt.next(); ++n, any = true) {
+        // ranges of the warp's queries, on their way during the waits
+        int2 ra = make_int2(0, 0), rb = ra;
+        if (!qt.full) {
+          const int q = qt.tile * kTile + half * 64 + lane;
+          if (q < p.s) ra = p.range[at.base + q];
+          if (q + 32 < p.s) rb = p.range[at.base + q + 32];
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(&st_full[n & 1], (n >> 1) & 1, p.status, 0x4A));
+        // Each lane marks which of the warp's 32 keys two queries see; transposed, which queries see its own key.
+        unsigned lo = 0, hi = 0;
+        if (!qt.full) {
+          auto mark = [&](int2 r) {
+            r = clip_range(r, p.s);
+            return bit_range(r.x - (key - lane), r.y - (key - lane));
+          };
+          lo = transpose_bits(mark(ra));
+          hi = transpose_bits(mark(rb));
+        }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, n & 1, p.status, 0x4B));
         if (!ok) break;
         tc_fence_after();
@@ -814,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         tmem_ld_wait();
         // P as it is, packed in x, and times the cap's derivative in w
         uint32_t x[32];
-        auto pack_seen = [&](auto masked, unsigned lo, unsigned hi) {
+        auto pack_seen = [&](auto masked) {
           const int apart = qt.tile * kTile - at.k0;
           probabilities<CAP, BIAS, true>(
               w, p.sp, slope2, q0, key, apart, (apart > 0 ? -slope2 : slope2) * static_cast<float>(apart + at.k0 - key),
@@ -832,15 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
               });
         };
         if (qt.full) {
-          pack_seen(Flag<false>{}, 0, 0);
+          pack_seen(Flag<false>{});
         } else {
-          // Each lane marks which of the warp's 32 keys two queries see; transposed, which queries see its own key.
-          auto mark = [&](int q) {
-            const int2 r = q < p.s ? clip_range(p.range[at.base + q], p.s) : make_int2(0, 0);
-            return bit_range(r.x - (key - lane), r.y - (key - lane));
-          };
-          const unsigned lo = transpose_bits(mark(q0 + lane)), hi = transpose_bits(mark(q0 + 32 + lane));
-          pack_seen(Flag<true>{}, lo, hi);
+          pack_seen(Flag<true>{});
         }
         tmem_st_32x32b_x32(ts, x);
         tmem_st_wait();
