@@ -11,7 +11,7 @@
 // loaded once for them, and loads some of them ahead of their arithmetic, which runs on fp32 pairs.
 // Pairs of the half style are brought together by shuffles of the loaded words, before the norm is known.
 // Measured at b2 s2048, 32 + 32 heads of 128 in bf16: forward 29.9 us (4.5 TB/s, 67 % of the copy rate), backward with
-// the gains' sums 47.8 us (64 %). What is left is latency at the ends of the grid's waves and 55 to 67 % of the issue slots.
+// the gains' sums 47.8 us (64 %). What is left is latency at the ends of the grid's waves and 54 to 58 % of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
