@@ -443,7 +443,8 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
  * Masked attention, forward. Per sequence and query head, over the keys of the query's range:
  *   y_ij = c(scale * q_i . k_j) - slope |i - j|,   c(x) = softcap * tanh(x / softcap), or x when softcap == 0
  *   lse_i = log sum_j exp(y_ij),   o_i = sum_j exp(y_ij - lse_i) v_j
- * A query with no keys gets o = 0 and lse = -inf.
+ * A query with no keys gets o = 0 and lse = -inf, and so does one whose scores are all -inf (a product past fp32). One
+ * with NaN or +inf among its scores y gets NaN in o and lse.
  *   q, o: heads heads; k, v: kv_heads heads, bf16; lse: fp32 [b][heads][s] (kept for the backward).
  *   key_range: int32 [b][s][2], 8-byte aligned; a range is cut to 0 <= lo, hi <= s.
  *   slopes: fp32 [heads] (the bias's slope of each head, 4-byte aligned) or NULL for no bias.

@@ -503,7 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         ++pieces;
       }
       if (ok) {
-        const bool live = l > 0.f;
+        // Nothing was seen, or scores of -inf alone. A row with NaN or +inf among its scores is not that: its l is NaN, or,
+        // where the score overflows only with the scale (the exponents' fma then subtracts infinity from a finite
+        // product), 0 beside m = +inf; o and lse get NaN from either.
+        const bool live = !(m == -INFINITY && l == 0.f);
         store_head_rows(stage, p.o, to, live ? 1.0f / l : 0.f, live, warp & 3, lane, 0, L::kBoxes, at.q0 + i * kTile,
                                at.head, at.seq, p.s, p.head_dim);
         tc_fence_before();

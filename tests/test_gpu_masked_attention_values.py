@@ -1,0 +1,138 @@
+"""Masked attention on values at the ends of the number range: NaN, infinities and products past fp32 in visible
+places. Most expectations are exact: a row that does not see the value keeps its bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import tensor_transformer_mlp_gb300 as tp
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8        # half a step of bf16
+SLACK = 2.0 ** -12   # fp32 sums and exponents, 1/16 of it
+S = 300
+FORMS = [(64, 0.0, False), (64, 20.0, False), (64, 0.0, True), (128, 0.0, False), (128, 20.0, False), (128, 0.0, True),
+         (128, 20.0, True)]
+
+
+def _inputs(hd, seed=0):
+    gen = torch.Generator("cuda").manual_seed(seed + hd)
+    return [torch.randn(1, S, 2, hd, generator=gen, device="cuda").bfloat16() for _ in range(4)]
+
+
+def _kw(cap, bias, **kw):
+    return dict(softcap=cap, slopes=torch.tensor([0.02, 0.003], device="cuda") if bias else None, **kw)
+
+
+def _forward(q, k, v, ranges, kw):
+    out = tp.masked_attention_forward(q, k, v, ranges, **kw)
+    torch.cuda.synchronize()
+    tp.tpmlp_device_status()
+    return out
+
+
+@pytest.mark.parametrize("hd,cap,bias", FORMS)
+def test_nan_in_a_query_or_key_reaches_the_rows_that_see_it(hd, cap, bias):
+    q, k, v, _ = _inputs(hd)
+    ranges = tp.attention_key_ranges(1, S, device="cuda")
+    kw = _kw(cap, bias)
+    o, lse = _forward(q, k, v, ranges, kw)
+    bad = q.clone()
+    bad[0, 140, 1, 3] = float("nan")
+    o1, lse1 = _forward(bad, k, v, ranges, kw)
+    assert torch.isnan(o1[0, 140, 1]).all() and torch.isnan(lse1[0, 1, 140])
+    o1[0, 140, 1], lse1[0, 1, 140] = o[0, 140, 1], lse[0, 1, 140]
+    assert torch.equal(o1, o) and torch.equal(lse1, lse)
+    bad = k.clone()
+    bad[0, 140, 0, 5] = float("nan")
+    o1, lse1 = _forward(q, bad, v, ranges, kw)
+    assert torch.isnan(o1[0, 140:, 0]).all() and torch.isnan(lse1[0, 0, 140:]).all()
+    assert torch.equal(o1[:, :140], o[:, :140]) and torch.equal(lse1[:, :, :140], lse[:, :, :140])
+    assert torch.equal(o1[:, :, 1], o[:, :, 1]) and torch.equal(lse1[:, 1], lse[:, 1])
+
+
+@pytest.mark.parametrize("hd,cap,bias", FORMS)
+def test_all_scores_nan(hd, cap, bias):
+    # the maximum of such a row stays at its start
+    q, k, v, _ = _inputs(hd)
+    q[0, 7] = float("nan")
+    o, lse = _forward(q, k, v, tp.attention_key_ranges(1, S, device="cuda"), _kw(cap, bias))
+    assert torch.isnan(o[0, 7]).all() and torch.isnan(lse[0, :, 7]).all()
+    o[0, 7], lse[0, :, 7] = 0, 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("hd,cap,bias", FORMS)
+def test_values_that_are_no_numbers(hd, cap, bias):
+    q, k, v, _ = _inputs(hd)
+    ranges = tp.attention_key_ranges(1, S, causal=False, device="cuda")
+    kw = _kw(cap, bias)
+    o, lse = _forward(q, k, v, ranges, kw)
+    bad = v.clone()
+    bad[0, 200, 0, 3], bad[0, 9, 1, 4], bad[0, 290, 1, 5] = float("nan"), float("inf"), -float("inf")
+    o1, lse1 = _forward(q, k, bad, ranges, kw)
+    assert torch.isnan(o1[0, :, 0, 3]).all()
+    assert (o1[0, :, 1, 4] == float("inf")).all() and (o1[0, :, 1, 5] == -float("inf")).all()
+    o1[0, :, 0, 3], o1[0, :, 1, 4:6] = o[0, :, 0, 3], o[0, :, 1, 4:6]
+    assert torch.equal(o1, o) and torch.equal(lse1, lse)
+
+
+@pytest.mark.parametrize("how", ["infinite key", "product past fp32", "scale past fp32"])
+@pytest.mark.parametrize("hd,cap,bias", FORMS)
+def test_infinite_scores(hd, cap, bias, how):
+    # key 150 scores +inf with one half of the queries and -inf with the other
+    q, k, v, _ = _inputs(hd)
+    sign = torch.where(torch.arange(S, device="cuda") % 3 == 0, 1.0, -1.0).bfloat16()
+    scale = 1 / math.sqrt(hd)
+    if how == "infinite key":
+        q[:, :, :, 0] = sign[None, :, None]
+        k[0, 150, :, 0] = float("inf")
+    elif how == "product past fp32":
+        q[:, :, :, 0] = sign[None, :, None] * 2.0 ** 66
+        k[:, :, :, 0] = 0
+        k[0, 150, :, 0] = 2.0 ** 66
+    else:  # 2^32 as a product, finite; past fp32 with the scale; all other scores are zeros
+        q.zero_(), k.zero_()
+        q[:, :, :, 0] = sign[None, :, None] * 2.0 ** 16
+        k[0, 150, :, 0] = 2.0 ** 16
+        scale = 1e30
+    ranges = tp.attention_key_ranges(1, S, causal=False, device="cuda")
+    o, lse = _forward(q, k, v, ranges, _kw(cap, bias, scale=scale))
+    i = torch.arange(S, device="cuda")
+    for h in range(2):
+        x = q[0, :, h].double() @ k[0, :, h].double().T
+        x[x.abs() > 3.5e38] = x[x.abs() > 3.5e38].sign() * float("inf")
+        x = x * scale
+        x[x.abs() > 3.5e38] = x[x.abs() > 3.5e38].sign() * float("inf")
+        y = cap * torch.tanh(x / cap) if cap else x
+        if bias:
+            y = y - [0.02, 0.003][h] * (i[:, None] - i).abs()
+        p = torch.softmax(y, -1)                       # NaN in a row with +inf
+        none = p.isnan().any(-1)
+        assert bool(none.any()) == (cap == 0.0)
+        assert torch.equal(o[0, :, h].isnan().all(-1), none) and torch.equal(lse[0, h].isnan(), none)
+        p, vh = p[~none], v[0, :, h].double()
+        tol = U * (p @ vh.abs() + (p @ vh).abs()) + SLACK * (p @ vh.abs())
+        assert ((o[0, ~none, h].double() - p @ vh).abs() <= tol).all()
+        want = torch.logsumexp(y[~none], -1)
+        mag = (q[0, :, h].double().abs() @ k[0, :, h].double().abs().T * scale)[~none]
+        mag = torch.where(mag > 1e6, 0.0, mag).amax(-1)  # where it counts scores are ordinary
+        near = hd * 2.0 ** -24 * mag + 2.0 ** -20 * (1 + want.abs()) + 2.0 ** -21 * cap + 3 * 2.0 ** -24 * 256 * 0.02
+        assert ((lse[0, h, ~none].double() - want).abs() <= near).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_position_past_the_table_is_seen_in_the_loss(hd):
+    # the norm with rotation writes NaN for it; no later row of the sequence may come out as a number
+    q, k, v, _ = _inputs(hd)
+    g = torch.ones(hd, device="cuda")
+    cos, sin = tp.rope_tables(64, hd, device="cuda")
+    pos = torch.full((1, S), 5, dtype=torch.int32, device="cuda")
+    pos[0, 100] = 64
+    qn, kn = tp.qk_norm_rope(q, k, g, g, cos, sin, positions=pos)
+    o, lse = _forward(qn, kn, v, tp.attention_key_ranges(1, S, device="cuda"), {})
+    assert torch.isnan(o[0, 100:]).all() and torch.isnan(lse[0, :, 100:]).all()
+    assert torch.isfinite(o[0, :100]).all() and torch.isfinite(lse[0, :, :100]).all()
+    assert np.isnan(o.float().sum().item())
