@@ -468,7 +468,7 @@ tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const 
  *   dQ_i = sum_j dX_ij k_j,   dK_j = sum_i dX_ij q_i,
  * the sums for a key or value head running over its query heads too. No atomics: every sum has a
  * fixed order. dq, dk, dv (bf16, strides ld_dq.. and so on) are overwritten; queries without keys
- * and keys that no query sees get zeros. slopes get no gradient. P_ij and dX_ij / scale are rounded
+ * and keys that no query sees get zeros, and a query whose lse is -inf adds nothing. slopes get no gradient. P_ij and dX_ij / scale are rounded
  * to bf16 for their products. o and d_o, too, must be finite everywhere.
  * workspace: tpmlp_masked_attention_backward_workspace_size bytes, 256-byte aligned.
  */

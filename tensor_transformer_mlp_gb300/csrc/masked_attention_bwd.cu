@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       const QueryPlace at(p, w.piece);
       const int row = at.q0 + rr, steps = w.steps, j0 = w.j0;
       const int2 r = clip_range(r_next, p.s);
-      const bool live = r.x < r.y;
+      const bool live = r.x < r.y && lse_next != -INFINITY;  // scores of -inf alone give probabilities of zero
       const float lse2 = live ? lse_next * kLog2e : 0.f;
       const float slope2 = BIAS ? p.slopes[at.head] * kLog2e : 0.f;
       float D = 0.f;
@@ -764,7 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
           float l[4], d[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            l[e] = q + e < p.s ? -p.lse[at + e] * kLog2e : 0.f;  // queries without keys: +inf, and masked
+            l[e] = q + e < p.s ? p.lse[at + e] : 0.f;
+            l[e] = l[e] == -INFINITY ? 0.f : -l[e] * kLog2e;  // nothing visible, and masked, or scores of -inf alone
             d[e] = q + e < p.s ? p.dsum[at + e] : 0.f;
           }
           // Where queries and keys are different tiles the bias grows with the query: its part within the tile.

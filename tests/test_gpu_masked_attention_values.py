@@ -136,3 +136,27 @@ def test_position_past_the_table_is_seen_in_the_loss(hd):
     assert torch.isnan(o[0, 100:]).all() and torch.isnan(lse[0, :, 100:]).all()
     assert torch.isfinite(o[0, :100]).all() and torch.isfinite(lse[0, :, :100]).all()
     assert np.isnan(o.float().sum().item())
+
+
+@pytest.mark.parametrize("hd,bias", [(64, False), (64, True), (128, False), (128, True)])
+def test_gradients_of_rows_whose_scores_are_all_minus_infinity(hd, bias):
+    # such a row weighs nothing: every gradient has the bits that it has without the row
+    q, k, v, dO = _inputs(hd)
+    q[..., 0], k[..., 0] = 0, -2.0 ** 66
+    rows = [7, 140, 141, 299]
+    q[0, rows, :, 0] = 2.0 ** 66
+    ranges = tp.attention_key_ranges(1, S, causal=False, device="cuda")
+    none = ranges.clone()
+    none[0, rows] = 0
+    runs = []
+    for r in (ranges, none):
+        o, lse = _forward(q, k, v, r, _kw(0.0, bias))
+        assert torch.isneginf(lse[:, :, rows]).all() and torch.count_nonzero(o[:, rows]) == 0
+        runs.append((o, lse) + tp.masked_attention_backward(q, k, v, r, o, lse, dO, **_kw(0.0, bias)))
+    torch.cuda.synchronize()
+    tp.tpmlp_device_status()
+    assert torch.count_nonzero(runs[0][2][:, rows]) == 0
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    for t in runs[0][2:]:
+        assert torch.isfinite(t).all()
