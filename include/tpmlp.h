@@ -451,7 +451,8 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
  *   scale > 0 (1 / sqrt(head_dim) in the block above), softcap >= 0; they and scale / softcap at
  *   most 1e30.
  * bf16 only; head_dim a multiple of 8, 8 <= head_dim <= 128. Scores, statistics and sums are fp32;
- * the probabilities are rounded to bf16 for the product with V. q, k, v and slopes must be finite
+ * the probabilities are rounded to bf16 for the product with V. Scores y keep their value while they stay below 2^30 in
+ * magnitude; a row with larger ones may come out as NaN. q, k, v and slopes must be finite
  * everywhere, in masked places too: a hidden value enters the products with weight zero.
  * b, heads <= 65535, s <= 2^30, b * s <= 2^31-1, and at most 2^31-1 tiles of 128 queries in all heads.
  */

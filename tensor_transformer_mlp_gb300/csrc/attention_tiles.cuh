@@ -272,7 +272,7 @@ struct ScoreParams {
   float scale2;          // scale * log2(e)
   float in_cap2;         // 2 log2(e) scale / cap: e^(2x) = 2^(q.k in_cap2)
   float cap2;            // cap * log2(e)
-  float poly2[3], poly3[4];  // tanh(x) = q.k times a polynomial of (q.k)^2, for |x| <= 0.3 and |x| <= 1/2
+  float poly2[3], poly3[4];  // tanh(x) = q.k times a polynomial of (q.k)^2, for |x| <= 0.25 and |x| <= 0.48
   float small2, small3;      // |q.k| up to which they hold
 };
 
@@ -283,18 +283,22 @@ inline ScoreParams score_params(float scale, float softcap) {
   if (softcap > 0.f) {
     p.in_cap2 = static_cast<float>(2.0 * scale * log2e / softcap);
     p.cap2 = static_cast<float>(softcap * log2e);
-    const double fit2[3] = {0.9999960105, -0.332974805, 0.125225976};
-    const double fit3[4] = {0.9999976754, -0.3332065329, 0.1314513258, -0.04337221447};
+    // Fits of tanh(x) / x - 1 in powers of x^2 up to 0.068, 0.25 and 0.48.
+    const double fit1 = -0.3328233848, fit2[2] = {-0.3332457116, 0.1287641663};
+    const double fit3[3] = {-0.3332922397, 0.1322320644, -0.0453897898};
     const double in = static_cast<double>(scale) / softcap;
-    auto fits = [&](int power) { return std::pow(in, power) > 1e-37 && std::pow(in, power) < 1e37; };
-    // Where a coefficient would leave fp32, the shorter polynomial, or x itself (x^2 / 3 < 2^-24 of it).
-    const bool two = fits(5), three = fits(7);
-    p.poly2[0] = static_cast<float>(in);
-    for (int i = 0; two && i < 3; ++i) p.poly2[i] = static_cast<float>(std::pow(in, 2 * i + 1) * fit2[i]);
-    p.small2 = static_cast<float>(std::fmin((two ? 0.3 : 4e-4) / in, 1e18));
-    for (int i = 0; i < 4; ++i)
-      p.poly3[i] = three ? static_cast<float>(std::pow(in, 2 * i + 1) * fit3[i]) : i < 3 ? p.poly2[i] : 0.f;
-    p.small3 = three ? static_cast<float>(0.5 / in) : p.small2;
+    auto fits = [&](int power) { return std::pow(in, power) > 1e-35 && std::pow(in, power) < 1e37; };
+    // Where a coefficient would leave fp32, the next shorter polynomial on its own range, down to x itself up to 0.0097,
+    // where what it leaves out (x^2 / 3) is what the other form is off by.
+    const bool one = fits(3), two = fits(5), three = fits(7);
+    p.poly2[0] = p.poly3[0] = static_cast<float>(in);
+    for (int i = 1; i < 3; ++i)
+      p.poly2[i] = two ? static_cast<float>(std::pow(in, 2 * i + 1) * fit2[i - 1])
+                       : one && i == 1 ? static_cast<float>(std::pow(in, 3) * fit1) : 0.f;
+    p.small2 = static_cast<float>(std::fmin((two ? 0.25 : one ? 0.068 : 0.0097) / in, 1e18));
+    for (int i = 1; i < 4; ++i)
+      p.poly3[i] = three ? static_cast<float>(std::pow(in, 2 * i + 1) * fit3[i - 1]) : i < 3 ? p.poly2[i] : 0.f;
+    p.small3 = three ? static_cast<float>(0.48 / in) : p.small2;
   }
   return p;
 }
@@ -305,11 +309,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh(x) of the cap's argument x = q.k scale / cap in two ways, both off by a few 2^-24 in absolute terms, which the cap
-// multiplies into the exponent (tanh.approx's 2^-11 would not do). Any x: 1 - 2 / (1 + e^(2x)), two special-function
-// operations. Small x: x times a polynomial of x^2, fitted to tanh(x) / x for the smallest largest error of the product,
-// with x's factor in the coefficients: degree 2 up to 0.3 (1.7e-7 = 2.9 * 2^-24) and 3 up to 1/2 (1.3e-7); on pairs, four
-// and five operations of the FMA pipe for two scores.
+// tanh(x) of the cap's argument x = q.k scale / cap in two ways (tanh.approx's 2^-11 would not do: the cap multiplies the
+// error into the exponent). Any x: 1 - 2 / (1 + e^(2x)), two special-function operations, off by up to 2.7e-7 = 4.5 * 2^-24
+// in absolute terms, so taken only where some score of the warp's tile is not small. Small x: x times a polynomial of x^2
+// with x's factor in the coefficients. Its first coefficient is x's factor itself and the others are fitted for the smallest
+// largest relative error, so that a cap far above the scores leaves them what they are: degree 2 up to 0.25 and 3 up to
+// 0.48, either off by 4.9e-7 = 8 * 2^-24 at worst (with the first coefficient fitted too, for the absolute error, small
+// scores were off by 4e-6 of themselves: 4e-4 at 100 under a cap of 1e5). On pairs, four and five operations of the FMA
+// pipe for two scores.
 __device__ __forceinline__ float cap_tanh(float qk, const ScoreParams& p) {
   return fmaf(-2.0f, rcp_approx(1.0f + ex2_approx(qk * p.in_cap2)), 1.0f);
 }

@@ -160,3 +160,56 @@ def test_gradients_of_rows_whose_scores_are_all_minus_infinity(hd, bias):
         assert torch.equal(a, b)
     for t in runs[0][2:]:
         assert torch.isfinite(t).all()
+
+
+CAPS = [(1e2, 90.0), (1e3, 3.0), (1e3, 200.0), (1e4, 100.0), (1e5, 100.0), (1e5, 1000.0), (1e6, 1000.0), (1e7, 1e4),
+        (1e10, 1e4)]
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("cap,most", CAPS)
+def test_caps_far_above_the_scores(hd, cap, most):
+    """A capped score is good relative to itself, not to the cap: tanh to 1.1e-6 of itself (its forms' 4.9e-7, or 2.6e-7 in
+    absolute terms from |x| = 0.25 on), the roundings of its factors and of the row's statistics 2^-24 each: 2^-19 in all.
+    The products q.k are sums of small whole numbers and carry no error."""
+    gen = torch.Generator("cuda").manual_seed(hd)
+    q, k = (torch.randint(-8, 9, (1, S, 2, hd), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    v, dO = (torch.randn(1, S, 2, hd, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    qd, kd, vd, gd = (t[0].double().transpose(0, 1) for t in (q, k, v, dO))
+    whole = qd @ kd.transpose(1, 2)
+    scale = float(np.float32(most / whole.abs().max().item()))
+    ranges = tp.attention_key_ranges(1, S, causal=False, device="cuda")
+    kw = dict(scale=scale, softcap=cap)
+    o, lse = _forward(q, k, v, ranges, kw)
+    dq, dk, dv = tp.masked_attention_backward(q, k, v, ranges, o, lse, dO, **kw)
+    y = cap * torch.tanh(whole * scale / float(np.float32(cap)))
+    want = torch.logsumexp(y, -1)
+    assert ((lse[0].double() - want).abs() <= 2.0 ** -19 * y.abs().amax(-1) + 2.0 ** -20).all()
+    free = tp.masked_attention_forward(q, k, v, ranges, scale=scale)[1][0]
+    if most / cap <= 1e-3:  # the cap takes x^2 / 3 = 3e-7 of a score at most
+        assert ((lse[0] - free).abs() <= 2.0 ** -20 * (1 + y.abs().amax(-1))).all()
+    p = torch.softmax(y, -1)
+    off = SLACK + 2 * 2.0 ** -19 * 2 * most   # P from a score and from lse
+    gone = 300 * 8 * 2.0 ** -126              # a probability below 2^-126 is zero in fp32: 300 of them, |v| and |dO| below 8
+    assert max(vd.abs().max(), gd.abs().max()) < 8
+    for got, to, x in ((o, p, vd), (dv, p.transpose(1, 2), gd)):
+        ref, size = to @ x, to @ x.abs()
+        assert ((got[0].transpose(0, 1).double() - ref).abs() <= U * (size + ref.abs()) + off * size + gone).all()
+    assert torch.isfinite(dq).all() and torch.isfinite(dk).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_scores_of_2_to_the_29(hd):
+    # whole products of unlike size lie 10^5 apart there: a row's output is the mean of the values of its largest
+    gen = torch.Generator("cuda").manual_seed(hd + 1)
+    q, k = (torch.randint(-8, 9, (1, S, 2, hd), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    v = torch.randn(1, S, 2, hd, generator=gen, device="cuda").bfloat16()
+    qd, kd, vd = (t[0].double().transpose(0, 1) for t in (q, k, v))
+    whole = qd @ kd.transpose(1, 2)
+    scale = float(np.float32(2.0 ** 29 / whole.abs().max().item()))
+    o, lse = _forward(q, k, v, tp.attention_key_ranges(1, S, causal=False, device="cuda"), dict(scale=scale))
+    y = whole * scale
+    p = torch.softmax(y, -1)
+    assert ((lse[0].double() - torch.logsumexp(y, -1)).abs() <= 2.0 ** -21 * y.abs().amax(-1)).all()
+    ref, size = p @ vd, p @ vd.abs()
+    assert ((o[0].transpose(0, 1).double() - ref).abs() <= U * (size + ref.abs()) + SLACK * size).all()
