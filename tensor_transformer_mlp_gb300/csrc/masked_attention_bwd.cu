@@ -416,17 +416,18 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
           tmem_st_wait();
         }
         tc_fence_before();
-        asm volatile("bar.sync 1, 256;" ::: "memory");  // all rows read, D written
-        if (lane == 0) {
-          mbar_arrive(q_full);
-          if (warp == 0) {
-            mbar_arrive(&k_empty[kn % L::kHeld]);
-            mbar_arrive(&k_empty[(kn + 1) % L::kHeld]);
-            mbar_arrive(&v_empty[os]);
-          }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(q_full);
+        // All rows read and D written, which the working warps wait for like the products (a named barrier has no limit: a
+        // warp that gave up in the piece before would leave the others in it).
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(q_full, pieces & 1, p.status, 0x3C));
+        if (ok && warp == 0 && lane == 0) {
+          mbar_arrive(&k_empty[kn % L::kHeld]);
+          mbar_arrive(&k_empty[(kn + 1) % L::kHeld]);
+          mbar_arrive(&v_empty[os]);
         }
         D = live ? dsum[rr] + dsum[kTile + rr] : 0.f;  // without keys o is zero; d_o may be anything
-        if (half && row < p.s) p.dsum[at.stat + row] = D;
+        if (ok && half && row < p.s) p.dsum[at.stat + row] = D;
         kn += 2 + steps;
         vn += 1 + steps;
       }
