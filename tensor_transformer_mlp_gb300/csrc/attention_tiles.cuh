@@ -89,6 +89,27 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, unsign
   }
 }
 
+// mbar_wait for the end of work whose length has no bound, as that of a piece with many key tiles: the limit counts from
+// the last phase that `stage`, a barrier of the ring through which the work goes, was seen to change to.
+__device__ __forceinline__ bool mbar_wait_moving(uint64_t* bar, uint32_t parity, uint64_t* stage, unsigned int* status,
+                                                 unsigned int where) {
+  const uint32_t a = smem_u32(bar);
+  bool seen = false;
+  uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    const bool now = mbar_done(stage, 0);
+    const uint64_t t = global_timer_ns();
+    if (now != seen) {
+      seen = now;
+      t0 = t;
+    } else if (t - t0 > kWaitLimitNs) {
+      record_timeout(status, where);
+      return false;
+    }
+  }
+  return true;
+}
+
 #define TPMLP_R8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
 
 // 32 lanes x 32 consecutive 32-bit columns: thread i of the warp writes lane (base + i).

@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         // The next piece is taken when this one nears its end (taken at its start, it would wait behind a long piece
         // while other CTAs ran out of work), in the place in `works` of the one before, which is done with then.
         int next = -1;
-        if (lane == 0 && mbar_wait(ending, it & 1, p.status, 0x2B) &&
+        if (lane == 0 && mbar_wait_moving(ending, it & 1, kv_full, p.status, 0x2B) &&
             (it == 0 || mbar_wait(&work_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, p.status, 0x2B)))
           next = take_work(response, taken, it & 1, p.status, 0x2C);
         piece = __shfl_sync(0xffffffffu, next, 0);

@@ -213,3 +213,21 @@ def test_scores_of_2_to_the_29(hd):
     assert ((lse[0].double() - torch.logsumexp(y, -1)).abs() <= 2.0 ** -21 * y.abs().amax(-1)).all()
     ref, size = p @ vd, p @ vd.abs()
     assert ((o[0].transpose(0, 1).double() - ref).abs() <= U * (size + ref.abs()) + SLACK * size).all()
+
+
+def test_a_piece_of_work_longer_than_the_limit_of_a_wait():
+    # one block of queries sees 402 million keys, which takes 3.6 s, past the 2 s that a wait may last without progress
+    s, hd = 3 << 27, 8
+    q = torch.zeros(1, s, 1, hd, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(q)
+    v[0, -1, 0, 0] = s / 2
+    ranges = torch.zeros(1, s, 2, dtype=torch.int32, device="cuda")
+    ranges[0, -256:, 1] = s
+    ranges[0, 5, 1] = 6
+    o, lse = tp.masked_attention_forward(q, q, v, ranges)
+    torch.cuda.synchronize()
+    tp.tpmlp_device_status()
+    assert ((lse[0, 0, -256:] - math.log(s)).abs() < 1e-5).all()
+    assert (o[0, -256:, 0, 0] > o[0, -256:, 0, 1]).all()          # the last key is among them
+    assert torch.equal(o[0, 5, 0].float(), torch.ones(hd, device="cuda"))
+    assert torch.count_nonzero(o[0, :, 0, 1]) == 257 and torch.isfinite(lse).sum() == 257

@@ -19,3 +19,12 @@ def test_no_wait_without_a_limit(name):
     assert not re.search(r"\bbar(rier)?(\.cta)?\.(sync|red)", source)
     for kernel in source.split("__global__")[1:]:
         assert "__syncthreads" not in kernel.split("regs_dec<")[-1].split("tc_fence_before();\n  __syncthreads();")[0]
+
+
+@pytest.mark.parametrize("name", KERNELS[:2])
+def test_the_wait_for_a_pieces_end_counts_from_its_last_progress(name):
+    # A piece of work lasts as long as it has key tiles (2 s from 2^27 or so on), so its end may only be waited for that way.
+    with open(os.path.join(_build.CSRC, name)) as f:
+        source = f.read()
+    assert len(re.findall(r"mbar_wait_moving\(ending, it & 1, k?v_full,", source)) == 1
+    assert not re.search(r"mbar_(wait|poll)\(ending", source)
