@@ -94,9 +94,13 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, unsign
 __device__ __forceinline__ bool mbar_wait_moving(uint64_t* bar, uint32_t parity, uint64_t* stage, unsigned int* status,
                                                  unsigned int where) {
   const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
   bool seen = false;
   uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(a, parity)) {
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(a, parity)) return true;
     const bool now = mbar_done(stage, 0);
     const uint64_t t = global_timer_ns();
     if (now != seen) {
@@ -107,7 +111,6 @@ __device__ __forceinline__ bool mbar_wait_moving(uint64_t* bar, uint32_t parity,
       return false;
     }
   }
-  return true;
 }
 
 #define TPMLP_R8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
