@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 
@@ -280,6 +281,59 @@ __device__ __forceinline__ void issue_cols(uint32_t leader, uint32_t d_tmem, uin
   for (int kk = kFrom; kk < kTo; ++kk)
     umma_bf16_ta_by(leader, d_tmem, a_tmem + (kSplit ? (kk >> 2) * 64 + (kk & 3) * 8 : kk * 8), b + step_cols(kk), idesc,
                     kk == 0 ? accumulate : 1u);
+}
+
+// ------------------------------------------------------------------ long sums
+
+// The tensor core cuts each product off some 25 bits below its accumulator: sums over many rows of like weight drift towards
+// zero (means of uniform values over 2^16 keys by 5e-4, 2^17 by 1e-3, 2^20 by 7e-3, 2^23 by 5e-2 of themselves; a bf16
+// rounding is 4e-3). Where a sum can have more than kLongSum steps, the kernels are the LONG ones: after every kPart steps
+// the warps that will write an accumulator out add it to rows of their own in local memory, and the next product overwrites
+// it. The rows take some 2000 cycles every 256 steps of as many, but the code around them would cost shorter sums 1 to 4 %
+// (in one kernel: causal forward 65.4 -> 66.4 us, step with window and bias 381 -> 398 us), hence two.
+constexpr int kPart = 256, kLongSum = 512;
+__device__ __forceinline__ bool part_begins(int step) { return (step & (kPart - 1)) == 0; }
+
+// part[c] = part[c] f + accumulator's column c (the latter alone if it is the first), a row per thread; the tile's lanes.
+template <int COLS>
+__device__ __forceinline__ void take_part(float* part, uint32_t acc, bool first, float f) {
+#pragma unroll 1
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t o[32];
+    tmem_ld_32x32b_x32(acc + c, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      part[c + e] = first ? __uint_as_float(o[e]) : fmaf(part[c + e], f, __uint_as_float(o[e]));
+  }
+}
+
+// The accumulator += part f.
+template <int COLS>
+__device__ __forceinline__ void give_part(const float* part, uint32_t acc, float f) {
+#pragma unroll 1
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t o[32];
+    tmem_ld_32x32b_x32(acc + c, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(part[c + e], f, __uint_as_float(o[e])));
+    tmem_st_32x32b_x32(acc + c, o);
+  }
+  tmem_st_wait();
+}
+
+// What `use` returns for a call's kernels, which it gets as constants: the columns of a tile (64 or 128), whether scores are
+// capped, whether they have a bias.
+template <typename Use>
+cudaError_t pick_kernel(bool wide, bool cap, bool bias, Use use) {
+  using N64 = std::integral_constant<int, 64>;
+  using N128 = std::integral_constant<int, 128>;
+  auto width = [&](auto hd) {
+    return cap ? (bias ? use(hd, std::true_type{}, std::true_type{}) : use(hd, std::true_type{}, std::false_type{}))
+               : (bias ? use(hd, std::false_type{}, std::true_type{}) : use(hd, std::false_type{}, std::false_type{}));
+  };
+  return wide ? width(N128{}) : width(N64{});
 }
 
 // ------------------------------------------------------------------ masks and scores

@@ -160,7 +160,7 @@ struct QueryPlace {
   }
 };
 
-template <int HD, bool CAP, bool BIAS>
+template <int HD, bool CAP, bool BIAS, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = BwdSmem<HD, true>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -298,8 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
             }
             wait_on(ds_full, step & 1, 0x36);
             if (!ok) break;
-            issue_cols<true>(leader, t_dq, t_dp, k_addr + ((kn + n) % L::kHeld) * L::kTileBytes, idesc_q, n != 0);
-            if (!more) umma_commit_by(leader, acc_full);
+            issue_cols<true>(leader, t_dq, t_dp, k_addr + ((kn + n) % L::kHeld) * L::kTileBytes, idesc_q,
+                             LONG ? !part_begins(n) : n != 0);
+            if (!more || (LONG && part_begins(n + 1))) umma_commit_by(leader, acc_full);
             if (more) dprobs(vn + n + 1);
             umma_commit_by(leader, &k_empty[(kn + n) % L::kHeld]);
           }
@@ -367,6 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
     };
     bool ok = true;
     int kn = 0, vn = 0, step = 0, pieces = 0;  // as the products count them
+    int parts = 0;   // of dQ, so far
+    [[maybe_unused]] float part[LONG ? 64 : 1];  // of a row's dQ (warps 4-7: its second 64 columns), for many key tiles
     QueryWork w = work_of(0);
     float lse_next;
     int2 r_next = range_of(w, &lse_next);
@@ -431,7 +434,19 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         kn += 2 + steps;
         vn += 1 + steps;
       }
+      auto wait_for_dq = [&] {  // all products of this part
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, parts & 1, p.status, 0x3A));
+        tc_fence_after();
+        ++parts;
+      };
       for (int n = 0; n < steps && ok; ++n, ++step) {
+        if constexpr (LONG) {
+          if (n > 0 && part_begins(n)) {
+            wait_for_dq();
+            if (!ok) break;
+            if (half < L::kBoxes) take_part<64>(part, t_dq + lanes + half * 64, n == kPart, 1.0f);
+          }
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(s_full, step & 1, p.status, 0x38));
         if (!ok) break;
         tc_fence_after();
@@ -481,11 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       w = work_of(it + 1);
       r_next = range_of(w, &lse_next);  // on its way during the output
       if (steps > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, pieces & 1, p.status, 0x3A));
-        tc_fence_after();
+        wait_for_dq();
         ++pieces;
       }
       if (ok) {
+        if constexpr (LONG) {
+          if (steps > kPart && half < L::kBoxes) give_part<64>(part, t_dq + lanes + half * 64, 1.0f);
+        }
         if (half < L::kBoxes)  // warps 4-7 take the second 64 columns
           store_head_rows(stage, p.dq, t_dq + lanes, p.scale, steps > 0, warp & 3, lane, half, half + 1, at.q0, at.head,
                           at.seq, p.s, p.head_dim);
@@ -558,7 +575,7 @@ struct KeyPlace {
   }
 };
 
-template <int HD, bool CAP, bool BIAS>
+template <int HD, bool CAP, bool BIAS, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const __grid_constant__ BwdParams p) {
   using L = BwdSmem<HD, false>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -728,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
           if (ok) dprobs(n);
           ++pieces;
         }
-        for (bool first = true; more && ok; ++n, first = false) {
+        for (int k = 0; more && ok; ++n, ++k) {
           more = qt.next();
           if (!more) {  // S and dP of the last step are on their way: K, and V, may be replaced after them
             umma_commit_by(leader, k_empty);
@@ -736,15 +753,17 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
           }
           wait_on(p_full, n & 1, 0x46);
           if (!ok) break;
-          issue_cols<true>(leader, t_dv, tmem, g_addr + (n % L::kPassing) * L::kTileBytes, idesc_d, !first);
+          issue_cols<true>(leader, t_dv, tmem, g_addr + (n % L::kPassing) * L::kTileBytes, idesc_d,
+                           LONG ? !part_begins(k) : k != 0);
           umma_commit_by(leader, &g_empty[n % L::kPassing]);
           if (more) scores(n + 1);
           wait_on(ds_full, n & 1, 0x47);
           if (!ok) break;
-          issue_cols<true>(leader, t_dk, t_dp, q_addr + (n % L::kHeld) * L::kTileBytes, idesc_d, !first);
+          issue_cols<true>(leader, t_dk, t_dp, q_addr + (n % L::kHeld) * L::kTileBytes, idesc_d,
+                           LONG ? !part_begins(k) : k != 0);
           umma_commit_by(leader, &q_empty[n % L::kHeld]);
+          if (!more || (LONG && part_begins(k + 1))) umma_commit_by(leader, acc_full);
           if (more) dprobs(n + 1);
-          else umma_commit_by(leader, acc_full);
         }
         done_with(it);
       }
@@ -792,15 +811,29 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int half = warp >> 2;
     bool ok = true;
-    int n = 0, pieces = 0;  // steps so far, and pieces with any
+    int n = 0, parts = 0;  // steps, and parts of dK and dV, so far
+    [[maybe_unused]] float part[LONG ? HD : 1];  // of a row's dV (warps 0-3) or dK, where there are many query tiles
     for (int it = 0; ok; ++it) {
       const int piece = work_of(it);
       if (piece < 0) break;
       const KeyPlace at(p, piece);
       const int key = at.k0 + (warp & 3) * 32 + lane;
       QueryTiles qt = at.queries(p);
-      bool any = false;
-      for (; qt.next(); ++n, any = true) {
+      const uint32_t acc = (half ? t_dk : t_dv) + lanes;
+      auto wait_for_acc = [&] {  // all products of this part
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, parts & 1, p.status, 0x4D));
+        tc_fence_after();
+        ++parts;
+      };
+      int k = 0;  // the piece's steps
+      for (; qt.next(); ++n, ++k) {
+        if constexpr (LONG) {
+          if (k > 0 && part_begins(k)) {
+            wait_for_acc();
+            if (!ok) break;
+            take_part<HD>(part, acc, k == kPart, 1.0f);
+          }
+        }
         // ranges of the warp's queries, on their way during the waits
         int2 ra = make_int2(0, 0), rb = ra;
         if (!qt.full) {
@@ -887,16 +920,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
           mbar_arrive(&st_empty[n & 1]);
         }
       }
-      if (ok && any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, pieces & 1, p.status, 0x4D));
-        tc_fence_after();
-        ++pieces;
-      }
+      if (ok && k > 0) wait_for_acc();
       if (ok) {
+        if constexpr (LONG) {
+          if (k > kPart) give_part<HD>(part, acc, 1.0f);
+        }
         // warps 0-3 write dV, warps 4-7 dK, a key's row per thread
-        store_head_rows(staging + warp * 32 * 128, half ? p.dk : p.dv, (half ? t_dk : t_dv) + lanes,
-                               half ? p.scale : 1.0f, any, warp & 3, lane, 0, L::kBoxes, at.k0, at.kvh, at.seq, p.s,
-                               p.head_dim);
+        store_head_rows(staging + warp * 32 * 128, half ? p.dk : p.dv, acc, half ? p.scale : 1.0f, k > 0, warp & 3, lane, 0, L::kBoxes, at.k0,
+                               at.kvh, at.seq, p.s, p.head_dim);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -919,22 +950,25 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
   }
 }
 
-template <int HD, bool CAP, bool BIAS>
-cudaError_t launch(const BwdParams& p, cudaStream_t stream, const DeviceCtx& ctx) {
-  static SmemLimit dq_done, dkv_done;
-  auto dq = masked_attention_dq_kernel<HD, CAP, BIAS>;
-  auto dkv = masked_attention_dkv_kernel<HD, CAP, BIAS>;
-  const int q_grid = p.ntiles * p.nseq * p.heads, k_grid = q_grid / p.group;
-  cudaError_t e = allow_smem(&dq_done, dq, BwdSmem<HD, true>::kBytes, ctx);
+template <int HD, bool CAP, bool BIAS, bool LONG>
+cudaError_t launch_queries(const BwdParams& p, cudaStream_t stream, const DeviceCtx& ctx) {
+  static SmemLimit done;
+  auto dq = masked_attention_dq_kernel<HD, CAP, BIAS, LONG>;
+  const cudaError_t e = allow_smem(&done, dq, BwdSmem<HD, true>::kBytes, ctx);
   if (e != cudaSuccess) return e;
-  e = allow_smem(&dkv_done, dkv, BwdSmem<HD, false>::kBytes, ctx);
-  if (e != cudaSuccess) return e;
-  dq<<<q_grid, kThreads, BwdSmem<HD, true>::kBytes, stream>>>(p);
-  e = cudaGetLastError();
+  dq<<<p.ntiles * p.nseq * p.heads, kThreads, BwdSmem<HD, true>::kBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int HD, bool CAP, bool BIAS, bool LONG>
+cudaError_t launch_keys(const BwdParams& p, cudaStream_t stream, const DeviceCtx& ctx) {
+  static SmemLimit done;
+  auto dkv = masked_attention_dkv_kernel<HD, CAP, BIAS, LONG>;
+  const cudaError_t e = allow_smem(&done, dkv, BwdSmem<HD, false>::kBytes, ctx);
   if (e != cudaSuccess) return e;
   // the key pass sets itself up while the last CTAs of the query pass finish (programmatic dependent launch)
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(k_grid));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ntiles * p.nseq * p.kv_heads));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = BwdSmem<HD, false>::kBytes;
   cfg.stream = stream;
@@ -986,11 +1020,16 @@ cudaError_t launch_masked_attention_backward(const MaskedAttention& a, const Hea
   p.nseq = static_cast<int>(a.b);
   p.status = ctx.status;
   const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
-  if (a.head_dim > 64)
-    return cap ? (bias ? launch<128, true, true>(p, stream, ctx) : launch<128, true, false>(p, stream, ctx))
-               : (bias ? launch<128, false, true>(p, stream, ctx) : launch<128, false, false>(p, stream, ctx));
-  return cap ? (bias ? launch<64, true, true>(p, stream, ctx) : launch<64, true, false>(p, stream, ctx))
-             : (bias ? launch<64, false, true>(p, stream, ctx) : launch<64, false, false>(p, stream, ctx));
+  auto both = [&](auto hd, auto c, auto bi) {
+    constexpr int HD = decltype(hd)::value;
+    constexpr bool CAP = decltype(c)::value, BIAS = decltype(bi)::value;
+    const cudaError_t e = p.ntiles > kLongSum ? launch_queries<HD, CAP, BIAS, true>(p, stream, ctx)
+                                              : launch_queries<HD, CAP, BIAS, false>(p, stream, ctx);
+    if (e != cudaSuccess) return e;
+    return static_cast<int64_t>(p.ntiles) * p.group > kLongSum ? launch_keys<HD, CAP, BIAS, true>(p, stream, ctx)
+                                                               : launch_keys<HD, CAP, BIAS, false>(p, stream, ctx);
+  };
+  return pick_kernel(a.head_dim > 64, cap, bias, both);
 }
 
 }  // namespace tpmlp

@@ -100,7 +100,7 @@ struct Place {
   }
 };
 
-template <int HD, bool CAP, bool BIAS>
+template <int HD, bool CAP, bool BIAS, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(const __grid_constant__ FwdParams p) {
   using L = FwdCfg<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
                 tc_fence_after();
                 if (!ok) break;
                 issue_cols<false>(leader, tmem + 256 + i * 64, tmem + 384 + i * 64, ring_addr + st * L::kTileBytes, idesc_o,
-                                  !first);
+                                  LONG ? !part_begins(j - w.span[i].lo) : !first);
                 commit(&o_full[i]);
               }
               ++steps[i];
@@ -338,14 +338,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
                 wait_on(&p_full[2 * i], steps[i] & 1, 0x24);
                 tc_fence_after();
                 if (!ok) break;
-                issue_cols<false, 0, 4>(leader, to, tp, stage_of(2 * n + 1), idesc_o, !first);
+                issue_cols<false, 0, 4>(leader, to, tp, stage_of(2 * n + 1), idesc_o,
+                                        LONG ? !part_begins(j - w.span[i].lo) : !first);
                 if (i == 0) commit(&kv_empty[(2 * n) % L::kStages]);  // K of this step, used before this loop turn
                 wait_on(&p_full[2 * i + 1], steps[i] & 1, 0x24);
                 tc_fence_after();
                 if (!ok) break;
                 issue_cols<false, 4, 8>(leader, to, tp, stage_of(2 * n + 1), idesc_o, 1);
                 ++steps[i];
-                if (j + 1 == w.span[i].hi) commit(&o_full[i]);
+                if (j + 1 == w.span[i].hi || (LONG && part_begins(j + 1 - w.span[i].lo))) commit(&o_full[i]);
               } else if (i == 0) {
                 commit(&kv_empty[(2 * n) % L::kStages]);
               }
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
     const uint32_t tp = L::kOwnP ? tmem + lanes + 384 + i * 64 : ts;
     uint8_t* stage = staging + warp * L::kStageBytes;
     bool ok = true, s_ready = false;  // s_ready: seen ahead of time (kOwnP)
-    int step = 0, pieces = 0;  // of this query tile, so far
+    int step = 0, parts = 0;  // of this query tile, so far
+    [[maybe_unused]] float part[LONG ? HD : 1];           // of a row's O, where there are many key tiles
     Work w = work_of(0);
     for (int it = 0; __all_sync(0xffffffffu, ok && w.piece >= 0); ++it) {
       const Place at(p, w.piece);
@@ -407,7 +409,19 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       const float slope2 = BIAS ? p.slopes[at.head] * kLog2e : 0.f;
       float m = -INFINITY, l = 0.f;
       const Span mine = i ? w.span[1] : w.span[0];
+      [[maybe_unused]] float part_m = -INFINITY;  // the maximum that part goes by
+      [[maybe_unused]] auto part_scale = [&] { return part_m == -INFINITY ? 0.f : ex2_approx(part_m - m); };
       for (int j = mine.lo; j < mine.hi; ++j, ++step) {
+        if constexpr (LONG) {
+          if (j > mine.lo && part_begins(j - mine.lo)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (L::kOwnP ? step - 1 : parts) & 1, p.status, 0x27));
+            if (!ok) break;
+            tc_fence_after();
+            ++parts;
+            take_part<HD>(part, to, j - mine.lo == kPart, part_scale());
+            part_m = m;
+          }
+        }
         ok = __all_sync(0xffffffffu, s_ready || mbar_wait(&s_full[i], step & 1, p.status, 0x26));
         if (!ok) break;
         tc_fence_after();
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
           const float f = m == -INFINITY ? 0.f : ex2_approx(m - m2);
           m = m2;
           l *= f;
-          if (j > mine.lo) {  // the first product overwrites O
+          if (LONG ? !part_begins(j - mine.lo) : j > mine.lo) {  // the first product overwrites O
             for (int c = 0; c < p.head_dim; c += 32) {
               uint32_t o[32];
               tmem_ld_32x32b_x32(to + c, o);
@@ -498,11 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       w = work_of(it + 1);
       r_next = range_of(w.piece);  // on its way during the output
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (L::kOwnP ? step - 1 : pieces) & 1, p.status, 0x27));
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], (L::kOwnP ? step - 1 : parts) & 1, p.status, 0x27));
         tc_fence_after();
-        ++pieces;
+        ++parts;
       }
       if (ok) {
+        if constexpr (LONG) {
+          if (mine.hi - mine.lo > kPart) give_part<HD>(part, to, part_scale());
+        }
         // Nothing was seen, or scores of -inf alone. A row with NaN or +inf among its scores is not that: its l is NaN, or,
         // where the score overflows only with the scale (the exponents' fma then subtracts infinity from a finite
         // product), 0 beside m = +inf; o and lse get NaN from either.
@@ -532,10 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
   }
 }
 
-template <int HD, bool CAP, bool BIAS>
+template <int HD, bool CAP, bool BIAS, bool LONG>
 cudaError_t launch(const FwdParams& p, int grid, cudaStream_t stream, const DeviceCtx& ctx) {
   static SmemLimit done;
-  auto kernel = masked_attention_forward_kernel<HD, CAP, BIAS>;
+  auto kernel = masked_attention_forward_kernel<HD, CAP, BIAS, LONG>;
   const cudaError_t e = allow_smem(&done, kernel, FwdCfg<HD>::kBytes, ctx);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, FwdCfg<HD>::kBytes, stream>>>(p);
@@ -567,11 +584,13 @@ cudaError_t launch_masked_attention_forward(const MaskedAttention& a, cudaStream
   p.status = ctx.status;
   const int g = p.nblocks * p.bheads;
   const bool wide = a.head_dim > 64, cap = a.softcap > 0.f, bias = a.slopes != nullptr;
-  if (wide)
-    return cap ? (bias ? launch<128, true, true>(p, g, stream, ctx) : launch<128, true, false>(p, g, stream, ctx))
-               : (bias ? launch<128, false, true>(p, g, stream, ctx) : launch<128, false, false>(p, g, stream, ctx));
-  return cap ? (bias ? launch<64, true, true>(p, g, stream, ctx) : launch<64, true, false>(p, g, stream, ctx))
-             : (bias ? launch<64, false, true>(p, g, stream, ctx) : launch<64, false, false>(p, g, stream, ctx));
+  auto by_length = [&](auto hd, auto c, auto bi) {
+    constexpr int HD = decltype(hd)::value;
+    constexpr bool CAP = decltype(c)::value, BIAS = decltype(bi)::value;
+    return (a.s + kTile - 1) / kTile > kLongSum ? launch<HD, CAP, BIAS, true>(p, g, stream, ctx)
+                                                : launch<HD, CAP, BIAS, false>(p, g, stream, ctx);
+  };
+  return pick_kernel(wide, cap, bias, by_length);
 }
 
 }  // namespace tpmlp

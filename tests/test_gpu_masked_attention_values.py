@@ -7,6 +7,8 @@ import pytest
 import torch
 
 import tensor_transformer_mlp_gb300 as tp
+from oracle import masked_attention as oma
+from test_gpu_masked_attention import _check, _draw
 
 pytestmark = pytest.mark.gpu
 
@@ -231,3 +233,71 @@ def test_a_piece_of_work_longer_than_the_limit_of_a_wait():
     assert (o[0, -256:, 0, 0] > o[0, -256:, 0, 1]).all()          # the last key is among them
     assert torch.equal(o[0, 5, 0].float(), torch.ones(hd, device="cuda"))
     assert torch.count_nonzero(o[0, :, 0, 1]) == 257 and torch.isfinite(lse).sum() == 257
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_sums_over_a_million_rows(hd, cap, bias):
+    """Sums of a million terms of one sign and size, in every accumulator: O and dQ of the last 128 queries over all keys,
+    dK and dV of the first 64 keys over all queries. All scores are zero (queries and keys use different columns, the
+    slopes are zero), so P is 2^-20 or 2^-6; the first column of V is 0 or 2 and that of dO 1, so dX is P or -P: no term is
+    rounded. What is left is the result's rounding, and what an accumulator loses over the 2^15 rows that it holds at most:
+    2^-26 of it a row, 2^-11 in all."""
+    s, half = 1 << 20, hd // 2
+    gen = torch.Generator("cuda").manual_seed(hd)
+    rand = lambda: torch.rand(s, half, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, dO = (torch.zeros(1, s, 1, hd, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    sign = torch.where(torch.arange(s, device="cuda") % 2 == 0, 1.0, -1.0)
+    q[0, :, 0, :half] = rand()
+    k[0, :, 0, half:] = rand() * sign[:, None].bfloat16()
+    v[0, :, 0, 0] = 1 + sign
+    v[0, :, 0, half:] = rand()
+    dO[0, :, 0, 0] = 1
+    dO[0, :, 0, 1:half] = rand()[:, 1:]
+    ranges = torch.zeros(1, s, 2, dtype=torch.int32, device="cuda")
+    ranges[0, :, 1] = 64
+    ranges[0, -128:, 1] = s
+    kw = dict(softcap=cap, slopes=torch.zeros(1, device="cuda") if bias else None, scale=0.25)
+    o, lse = _forward(q, k, v, ranges, kw)
+    dq, dk, dv = tp.masked_attention_backward(q, k, v, ranges, o, lse, dO, **kw)
+    torch.cuda.synchronize()
+    tp.tpmlp_device_status()
+    assert (lse[0, 0, :-128] - math.log(64)).abs().max() < 1e-6 and (lse[0, 0, -128:] - math.log(s)).abs().max() < 4e-6
+    qd, kd, vd, gd, sg = q[0, :, 0].double(), k[0, :, 0].double(), v[0, :, 0].double(), dO[0, :, 0].double(), sign.double()
+    few, all_q, all_g = slice(0, 64), qd[-128:].sum(0) / s, gd[-128:].sum(0) / s
+    want = {"o": vd.mean(0), "dq": 0.25 * (sg[:, None] * kd).mean(0),
+            "dv": gd[:-128].sum(0) / 64 + all_g, "dk": 0.25 * (qd[:-128].sum(0) / 64 + all_q)}
+    got = {"o": o[0, -128:, 0], "dq": dq[0, -128:, 0], "dv": dv[0, few, 0], "dk": dk[0, few, 0].double() * sg[few, None]}
+    for name, w in want.items():
+        off = (got[name].double() - w).abs()
+        assert (off <= (U + 2.0 ** -11) * w.abs()).all(), (name, (off / w.abs().clamp(min=1e-30)).max().item())
+    rest = (dv[0, 64:, 0].double() - all_g).abs() <= (U + 2.0 ** -11) * all_g.abs()
+    assert rest.all()
+
+
+@pytest.mark.parametrize("hd,cap,bias", [(64, 0.0, True), (128, 20.0, False)])
+def test_keys_shared_by_many_heads(hd, cap, bias):
+    # a key is seen by 17 tiles of 32 heads' queries: its sums are long though the sequence is not
+    q, k, v, dO = _draw(hd, 1, 2100, 32, 1, hd, "joined")
+    _check(q, k, v, dO, oma.key_ranges(1, 2100, causal=False), cap=cap, slopes=[2.0 ** -(4 + h / 8) for h in range(32)] if bias else None)
+
+
+def test_a_long_row_whose_maximum_moves():
+    # parts of O under maxima of their own, falling and rising, against 64 bits; some rows see the middle only
+    s, hd = 70000, 64
+    gen = torch.Generator("cuda").manual_seed(7)
+    q, k, v = (torch.randn(1, s, 1, hd, generator=gen, device="cuda").bfloat16() for _ in range(3))
+    q, k = q.abs(), k.abs() * torch.linspace(0.1, 3, s, device="cuda")[None, :, None, None].bfloat16()
+    ranges = torch.zeros(1, s, 2, dtype=torch.int32, device="cuda")
+    ranges[0, -200:, 1] = s
+    ranges[0, -100:-50, 0], ranges[0, -100:-50, 1] = 33000, 65600
+    for keys in (k, k.flip(1)):
+        o, lse = _forward(q, keys, v, ranges, {})
+        x = q[0, -200:, 0].double() @ keys[0, :, 0].double().T / 8
+        j = torch.arange(s, device="cuda")
+        x[(j < ranges[0, -200:, :1]) | (j >= ranges[0, -200:, 1:])] = -math.inf
+        p, vd = torch.softmax(x, -1), v[0, :, 0].double()
+        size = p @ vd.abs()
+        assert ((o[0, -200:, 0].double() - p @ vd).abs() <= U * (size + (p @ vd).abs()) + SLACK * size).all()
+        want = torch.logsumexp(x, -1)
+        assert ((lse[0, 0, -200:].double() - want).abs() <= 2.0 ** -20 * (1 + want.abs()) + hd * 2.0 ** -24 * x.amax(-1)).all()
