@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
     regs_dec<kRegsIssue>();
     if (warp == kWorkWarps && lane == 0) {
       // ---------------------------------------------------------------- loads
-      int kn = 0, vn = 0;  // tiles loaded through the two rings
+      uint32_t kn = 0, vn = 0;  // tiles loaded through the two rings; they may wrap
       bool ok = true;
       auto load = [&](bool held, const HeadMap& m, int row, int head, int seq) {
-        const int st = held ? kn % L::kHeld : vn % L::kPassing;
+        const uint32_t st = held ? kn % L::kHeld : vn % L::kPassing;
         uint64_t* full = held ? &k_full[st] : &v_full[st];
         if (ok) ok = held ? mbar_wait(&k_empty[st], ((kn / L::kHeld) & 1) ^ 1, p.status, 0x30)
                           : mbar_wait(&v_empty[st], ((vn / L::kPassing) & 1) ^ 1, p.status, 0x31);
@@ -252,8 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         if (w.steps == 0) mbar_arrive(ending);
       }
       if (!ok) {  // the copies in flight must land before shared memory goes away
-        for (int k = max(0, kn - L::kHeld); k < kn; ++k) mbar_wait(&k_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x32);
-        for (int k = max(0, vn - L::kPassing); k < vn; ++k)
+        for (uint32_t k = kn - min(kn, static_cast<uint32_t>(L::kHeld)); k != kn; ++k)
+          mbar_wait(&k_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x32);
+        for (uint32_t k = vn - min(vn, static_cast<uint32_t>(L::kPassing)); k != vn; ++k)
           mbar_wait(&v_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x32);
       }
     } else if (warp == kWorkWarps + 1) {
@@ -267,20 +268,20 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
         if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
         tc_fence_after();
       };
-      auto scores = [&](int k) {  // S = Q K^T with the ring's k-th tile
+      auto scores = [&](uint32_t k) {  // S = Q K^T with the ring's k-th tile
         wait_on(&k_full[k % L::kHeld], (k / L::kHeld) & 1, 0x34);
         if (!ok) return;
         issue_rows_ta<HD>(leader, tmem, t_q, k_addr + (k % L::kHeld) * L::kTileBytes, ksteps);
         umma_commit_by(leader, s_full);
       };
-      auto dprobs = [&](int v) {  // dP = d_o V^T with the ring's v-th tile
+      auto dprobs = [&](uint32_t v) {  // dP = d_o V^T with the ring's v-th tile
         wait_on(&v_full[v % L::kPassing], (v / L::kPassing) & 1, 0x35);
         if (!ok) return;
         issue_rows_ta<HD>(leader, t_dp, t_g, v_addr + (v % L::kPassing) * L::kTileBytes, ksteps);
         umma_commit_by(leader, dp_full);
         umma_commit_by(leader, &v_empty[v % L::kPassing]);
       };
-      int kn = 0, vn = 0, step = 0, pieces = 0;  // ring tiles, steps and pieces so far
+      uint32_t kn = 0, vn = 0, step = 0, pieces = 0;  // ring tiles, steps and pieces so far; they may wrap
       for (int it = 0; ok; ++it) {
         const QueryWork w = work_of(it);
         if (__any_sync(0xffffffffu, w.piece < 0)) break;
@@ -367,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       return p.range[at.base + at.q0 + rr];
     };
     bool ok = true;
-    int kn = 0, vn = 0, step = 0, pieces = 0;  // as the products count them
-    int parts = 0;   // of dQ, so far
+    uint32_t kn = 0, vn = 0, step = 0, pieces = 0;  // as the products count them
+    uint32_t parts = 0;  // of dQ, so far
     [[maybe_unused]] float part[LONG ? 64 : 1];  // of a row's dQ (warps 4-7: its second 64 columns), for many key tiles
     QueryWork w = work_of(0);
     float lse_next;
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dq_kernel(const 
       float D = 0.f;
       if (steps > 0) {
         // The row of Q (warps 0-3) or d_o (warps 4-7) goes to tensor memory; each forms half of D = d_o . o.
-        const int os = vn % L::kPassing;
+        const uint32_t os = vn % L::kPassing;
         ok = mbar_wait(&k_full[kn % L::kHeld], (kn / L::kHeld) & 1, p.status, 0x3B) &&
              mbar_wait(&k_full[(kn + 1) % L::kHeld], ((kn + 1) / L::kHeld) & 1, p.status, 0x3B) &&
              mbar_wait(&v_full[os], (vn / L::kPassing) & 1, p.status, 0x3B);
@@ -651,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     if (warp == kWorkWarps) {
       // ---------------------------------------------------------------- loads
       bool ok = true;
-      int n = 0, pieces = 0, loaded = 0, loaded_v = 0;  // steps, pieces, and pieces with any steps
+      uint32_t n = 0;  // steps; it may wrap
+      int pieces = 0, loaded = 0, loaded_v = 0;  // pieces, and pieces with any steps
       int piece = static_cast<int>(blockIdx.x);
       for (int it = 0;; ++it) {
         if (lane == 0) {
@@ -661,9 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         if (piece < 0) break;
         const KeyPlace at(p, piece);
         QueryTiles qt = at.queries(p);
-        const int n0 = n;
+        const uint32_t n0 = n;
         for (; ok && qt.next(); ++n) {
-          const int qs = n % L::kHeld, gs = n % L::kPassing;
+          const uint32_t qs = n % L::kHeld, gs = n % L::kPassing;
           ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[qs], ((n / L::kHeld) & 1) ^ 1, p.status, 0x40));
           if (!ok) break;
           if (lane == 0) {
@@ -705,8 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
       if (!ok) {  // the copies in flight must land before shared memory goes away
         if (loaded > 0) mbar_wait(k_full, (loaded - 1) & 1, p.status, 0x42);
         if (loaded_v > 0) mbar_wait(v_full, (loaded_v - 1) & 1, p.status, 0x42);
-        for (int k = max(0, n + 1 - L::kHeld); k <= n; ++k) mbar_wait(&q_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x42);
-        for (int k = max(0, n + 1 - L::kPassing); k <= n; ++k)
+        const uint32_t end = n + 1;  // the step that failed may have begun
+        for (uint32_t k = end - min(end, static_cast<uint32_t>(L::kHeld)); k != end; ++k)
+          mbar_wait(&q_full[k % L::kHeld], (k / L::kHeld) & 1, p.status, 0x42);
+        for (uint32_t k = end - min(end, static_cast<uint32_t>(L::kPassing)); k != end; ++k)
           mbar_wait(&g_full[k % L::kPassing], (k / L::kPassing) & 1, p.status, 0x42);
       }
     } else if (warp == kWorkWarps + 1) {
@@ -720,19 +724,19 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
         if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
         tc_fence_after();
       };
-      auto scores = [&](int n) {  // S(n)^T = K Q(n)^T
+      auto scores = [&](uint32_t n) {  // S(n)^T = K Q(n)^T
         wait_on(&q_full[n % L::kHeld], (n / L::kHeld) & 1, 0x43);
         if (!ok) return;
         issue_rows<HD>(leader, tmem, k_addr, q_addr + (n % L::kHeld) * L::kTileBytes, ksteps);
         umma_commit_by(leader, s_full);
       };
-      auto dprobs = [&](int n) {  // dP(n)^T = V d_o(n)^T
+      auto dprobs = [&](uint32_t n) {  // dP(n)^T = V d_o(n)^T
         wait_on(&g_full[n % L::kPassing], (n / L::kPassing) & 1, 0x44);
         if (!ok) return;
         issue_rows<HD>(leader, t_dp, v_addr, g_addr + (n % L::kPassing) * L::kTileBytes, ksteps);
         umma_commit_by(leader, dp_full);
       };
-      int n = 0, pieces = 0;  // steps, and pieces with any
+      uint32_t n = 0, pieces = 0;  // steps, and pieces with any
       for (int it = 0; ok; ++it) {
         const int piece = work_of(it);
         if (piece < 0) break;
@@ -772,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     } else if (warp == kWorkWarps + 2) {
       // ---------------------------------------------------------------- lse and D of the queries
       bool ok = true;
-      int n = 0;
+      uint32_t n = 0;
       for (int it = 0; ok; ++it) {
         const int piece = work_of(it);
         if (piece < 0) break;
@@ -811,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int half = warp >> 2;
     bool ok = true;
-    int n = 0, parts = 0;  // steps, and parts of dK and dV, so far
+    uint32_t n = 0, parts = 0;  // steps, and parts of dK and dV, so far
     [[maybe_unused]] float part[LONG ? HD : 1];  // of a row's dV (warps 0-3) or dK, where there are many query tiles
     for (int it = 0; ok; ++it) {
       const int piece = work_of(it);
@@ -926,8 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_dkv_kernel(const
           if (k > kPart) give_part<HD>(part, acc, 1.0f);
         }
         // warps 0-3 write dV, warps 4-7 dK, a key's row per thread
-        store_head_rows(staging + warp * 32 * 128, half ? p.dk : p.dv, acc, half ? p.scale : 1.0f, k > 0, warp & 3, lane, 0, L::kBoxes, at.k0,
-                               at.kvh, at.seq, p.s, p.head_dim);
+        store_head_rows(staging + warp * 32 * 128, half ? p.dk : p.dv, acc, half ? p.scale : 1.0f, k > 0, warp & 3, lane, 0,
+                        L::kBoxes, at.k0, at.kvh, at.seq, p.s, p.head_dim);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {

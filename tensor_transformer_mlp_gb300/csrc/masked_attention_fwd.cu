@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
     if (warp == kSoftmaxWarps && lane == 0) {
       // ---------------------------------------------------------------- loads
       bool ok = true;
-      int n = 0, loaded[2] = {0, 0};
+      uint32_t n = 0;  // tiles through the ring; it may wrap
+      int loaded[2] = {0, 0};
       for (int it = 0; ok; ++it) {
         const Work w = work_of(it);
         if (w.piece < 0) break;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
             told = true;
           }
           for (int kv = 0; kv < 2; ++kv, ++n) {
-            const int st = n % L::kStages;
+            const uint32_t st = n % L::kStages;
             if (!mbar_wait(&kv_empty[st], ((n / L::kStages) & 1) ^ 1, p.status, 0x20)) {
               ok = false;
               break;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
       if (!ok) {
         for (int i = 0; i < 2; ++i)
           if (loaded[i] > 0) mbar_wait(&q_full[i], (loaded[i] - 1) & 1, p.status, 0x21);
-        for (int k = max(0, n - L::kStages); k < n; ++k)
+        for (uint32_t k = n - min(n, static_cast<uint32_t>(L::kStages)); k != n; ++k)
           mbar_wait(&kv_full[k % L::kStages], (k / L::kStages) & 1, p.status, 0x21);
       }
     } else if (warp == kSoftmaxWarps + 1 || (L::kOwnP && warp == kSoftmaxWarps + 3)) {
@@ -254,13 +255,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, where));
         };
-        int n = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};  // key tiles, and per query tile steps and pieces, so far
+        uint32_t n = 0, steps[2] = {0, 0};  // key tiles, and steps of each query tile, so far; they may wrap
+        int pieces[2] = {0, 0};
         for (int it = 0; ok; ++it) {
           const Work w = work_of(it);
           if (__any_sync(0xffffffffu, w.piece < 0)) break;
           const int j_end = w.end();
           for (int j = w.next(w.begin()); j < j_end && ok; j = w.next(j + 1), ++n) {
-            const int t = 2 * n + pv, st = t % L::kStages;
+            const uint32_t t = 2 * n + pv, st = t % L::kStages;
             wait_on(&kv_full[st], (t / L::kStages) & 1, 0x22);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -303,20 +305,22 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
         auto wait_on = [&](uint64_t* bar, uint32_t parity, unsigned where) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, p.status, where));
         };
-        auto stage_of = [&](int n) { return ring_addr + (n % L::kStages) * L::kTileBytes; };
-        auto wait_tile = [&](int n) { wait_on(&kv_full[n % L::kStages], (n / L::kStages) & 1, 0x22); };
-        int n0 = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};  // key tiles, and per query tile steps and pieces, so far
+        auto stage_of = [&](uint32_t n) { return ring_addr + (n % L::kStages) * L::kTileBytes; };
+        auto wait_tile = [&](uint32_t n) { wait_on(&kv_full[n % L::kStages], (n / L::kStages) & 1, 0x22); };
+        uint32_t n0 = 0, steps[2] = {0, 0};  // key tiles, and steps of each query tile, so far; they may wrap
+        int pieces[2] = {0, 0};
         for (int it = 0; ok; ++it) {
           const Work w = work_of(it);
           if (__any_sync(0xffffffffu, w.piece < 0)) break;
           const int j_end = w.end();
-          auto scores = [&](int i, int n, int j) {  // with the K tile j of step n
+          auto scores = [&](int i, uint32_t n, int j) {  // with the K tile j of step n
             if (!ok) return;
             issue_rows<HD>(leader, tmem + i * 128, q_addr + i * L::kTileBytes, stage_of(2 * n), ksteps);
             commit(&s_full[i]);
             if (j + 1 == w.span[i].hi) commit(&q_empty[i]);
           };
-          int j = w.next(w.begin()), jn = w.next(j + 1), n = n0;
+          int j = w.next(w.begin()), jn = w.next(j + 1);
+          uint32_t n = n0;
           if (j < j_end) {
             wait_tile(2 * n);
 #pragma unroll
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_attention_forward_kernel(c
     const uint32_t tp = L::kOwnP ? tmem + lanes + 384 + i * 64 : ts;
     uint8_t* stage = staging + warp * L::kStageBytes;
     bool ok = true, s_ready = false;  // s_ready: seen ahead of time (kOwnP)
-    int step = 0, parts = 0;  // of this query tile, so far
+    uint32_t step = 0, parts = 0;  // of this query tile, so far; they may wrap
     [[maybe_unused]] float part[LONG ? HD : 1];           // of a row's O, where there are many key tiles
     Work w = work_of(0);
     for (int it = 0; __all_sync(0xffffffffu, ok && w.piece >= 0); ++it) {

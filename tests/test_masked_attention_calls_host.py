@@ -28,3 +28,17 @@ def test_the_wait_for_a_pieces_end_counts_from_its_last_progress(name):
         source = f.read()
     assert len(re.findall(r"mbar_wait_moving\(ending, it & 1, k?v_full,", source)) == 1
     assert not re.search(r"mbar_(wait|poll)\(ending", source)
+
+
+@pytest.mark.parametrize("name", KERNELS[:2])
+def test_what_indexes_a_ring_does_not_go_negative(name):
+    # A CTA's count of tiles has no bound (2^31 take some minutes), and its remainder is an address in shared memory.
+    with open(os.path.join(_build.CSRC, name)) as f:
+        source = re.sub(r"//[^\n]*", "", f.read())
+    for kernel in source.split("__global__")[1:]:
+        roles = kernel[kernel.index("regs_dec<"):]
+        signed = re.findall(r"(?<!\()\bint ([^;{}()]*);", roles)            # declarations, but not a loop's own
+        names = {part.split("=")[0].strip() for decl in signed for part in decl.split(",")}
+        assert not names & {"n", "n0", "kn", "vn", "t", "st", "qs", "gs", "os"}
+        assert not re.search(r"\[&\]\((int \w+, )?int [nkv]\b", roles)     # parameters that take them
+        assert re.search(r"uint32_t (n|kn) = 0", roles)
