@@ -370,7 +370,8 @@ tpmlp_status tpmlp_attention_backward(const void* X, const void* Wqkv, const voi
  * 3 * head_dim), a [all q | all k | all v] matrix (hs = head_dim) and separate [b*s][h] matrices
  * are all read and written in place. Strides are positive multiples of 8 elements, pointers
  * 16-byte aligned, and the heads of an output must not overlap, nor an output anything else that
- * the call reads or writes unless it says so. head_dim is a multiple of 8.
+ * the call reads or writes unless it says so (TPMLP_ERR_INVALID; not found out where two tensors interleave with row
+ * strides and head strides that both differ). head_dim is a multiple of 8.
  * heads query heads share kv_heads key and value heads, heads % kv_heads == 0: query head j
  * reads key head j / (heads / kv_heads).
  *

@@ -507,9 +507,19 @@ tpmlp_status tpmlp_qk_norm_rope(const void* q, const void* k, const float* gamma
   ROPE_TRY(check_ptrs({q, k, q_out, k_out}, 16));
   ROPE_TRY(check_ptrs({gamma_q, gamma_k, cos_table, sin_table}, 4));
   if (!aligned(positions, 4)) return err(TPMLP_ERR_ALIGN, "positions not 4-byte aligned");
-  if (shared_tensor({q_out, k_out}, {gamma_q, gamma_k, cos_table, sin_table, positions}) || q_out == k || k_out == q ||
-      (q_out == q && (ld_q != ld_qo || hs_q != hs_qo)) || (k_out == k && (ld_k != ld_ko || hs_k != hs_ko)))
-    return err(TPMLP_ERR_INVALID, "in place q_out is q and k_out is k, with the same strides");
+  const int64_t tokens = b * s, size = dt == TPMLP_BF16 ? 2 : 4;
+  auto of = [&](const void* p, int64_t ld, int64_t hs, int n) {
+    return heads_region({const_cast<void*>(p), ld, hs}, tokens, n, head_dim, size);
+  };
+  const Region rq = of(q, ld_q, hs_q, heads), rk = of(k, ld_k, hs_k, kv_heads);
+  const Region rqo = of(q_out, ld_qo, hs_qo, heads), rko = of(k_out, ld_ko, hs_ko, kv_heads);
+  if (any_overlap({rqo, rko}, {flat_region(gamma_q, head_dim, 4), flat_region(gamma_k, head_dim, 4),
+                               flat_region(cos_table, table_len, 2 * rot_dim), flat_region(sin_table, table_len, 2 * rot_dim),
+                               flat_region(positions, tokens, 4)}) ||
+      overlap(rqo, rk) || overlap(rko, rq) || (!same_region(rqo, rq) && overlap(rqo, rq)) ||
+      (!same_region(rko, rk) && overlap(rko, rk)))
+    return err(TPMLP_ERR_INVALID,
+               "an output overlaps another tensor of the call (in place q_out is q and k_out is k, with the same strides)");
   RopeParams p = make_params({{const_cast<void*>(q), ld_q, hs_q}, {q_out, ld_qo, hs_qo}, {}, gamma_q, heads, 0},
                              {{const_cast<void*>(k), ld_k, hs_k}, {k_out, ld_ko, hs_ko}, {}, gamma_k, kv_heads, 0},
                              cos_table, sin_table, positions, table_len, rot_dim, b, s, head_dim, eps);
@@ -556,12 +566,22 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
   const size_t need = tpmlp_qk_norm_rope_backward_workspace_size(b, s, head_dim);
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "qk_norm_rope backward workspace too small");
   if (!aligned(workspace, 16)) return err(TPMLP_ERR_ALIGN, "workspace not 16-byte aligned");
-  auto other_strides = [](int64_t ld, int64_t hs, int64_t ld2, int64_t hs2) { return ld != ld2 || hs != hs2; };
-  if (shared_tensor({dq, dk, dgamma_q, dgamma_k, workspace}, {gamma_q, gamma_k, cos_table, sin_table, positions}) ||
-      dq == k || dq == dk_out || dk == q || dk == dq_out ||
-      (dq == q && other_strides(ld_dq, hs_dq, ld_q, hs_q)) || (dq == dq_out && other_strides(ld_dq, hs_dq, ld_qo, hs_qo)) ||
-      (dk == k && other_strides(ld_dk, hs_dk, ld_k, hs_k)) || (dk == dk_out && other_strides(ld_dk, hs_dk, ld_ko, hs_ko)))
-    return err(TPMLP_ERR_INVALID, "in place dq is q or dq_out and dk is k or dk_out, with the same strides");
+  const int64_t tokens = b * s, size = dt == TPMLP_BF16 ? 2 : 4;
+  auto of = [&](const void* p, int64_t ld, int64_t hs, int n) {
+    return heads_region({const_cast<void*>(p), ld, hs}, tokens, n, head_dim, size);
+  };
+  const Region rq = of(q, ld_q, hs_q, heads), rk = of(k, ld_k, hs_k, kv_heads), rqo = of(dq_out, ld_qo, hs_qo, heads),
+               rko = of(dk_out, ld_ko, hs_ko, kv_heads), rdq = of(dq, ld_dq, hs_dq, heads), rdk = of(dk, ld_dk, hs_dk, kv_heads);
+  const Region rgq = flat_region(dgamma_q, head_dim, 4), rgk = flat_region(dgamma_k, head_dim, 4),
+               rws = flat_region(workspace, static_cast<int64_t>(need), 1);
+  auto beside = [](const Region& out, const Region& in) { return !same_region(out, in) && overlap(out, in); };
+  if (any_overlap({rdq, rdk, rgq, rgk, rws}, {flat_region(gamma_q, head_dim, 4), flat_region(gamma_k, head_dim, 4),
+                                              flat_region(cos_table, table_len, 2 * rot_dim), flat_region(sin_table, table_len, 2 * rot_dim),
+                                              flat_region(positions, tokens, 4)}) ||
+      any_overlap({rgq, rgk, rws}, {rq, rk, rqo, rko}) || overlap(rdq, rk) || overlap(rdq, rko) || overlap(rdk, rq) ||
+      overlap(rdk, rqo) || beside(rdq, rq) || beside(rdq, rqo) || beside(rdk, rk) || beside(rdk, rko))
+    return err(TPMLP_ERR_INVALID, "an output overlaps another tensor of the call (in place dq is q or dq_out and dk is k or "
+                                  "dk_out, with the same strides)");
   DeviceCtx ctx;
   ROPE_CUDA(get_device_ctx(&ctx), "device context");
   RopeParams p = make_params(

@@ -8,6 +8,8 @@
 #include <atomic>
 #include <initializer_list>
 
+#include "overlap.h"
+
 namespace tpmlp {
 
 constexpr int kGeluErf = 0;
@@ -220,15 +222,8 @@ inline bool heads_apart(const HeadView& v, int64_t tokens, int heads, int hd) {
   return heads <= 1 || (v.ld - hd) / v.hs >= heads - 1 || (v.hs - hd) / v.ld >= tokens - 1;
 }
 
-// Whether one of `outputs` is one of `others`, or twice among them.
-inline bool shared_tensor(std::initializer_list<const void*> outputs, std::initializer_list<const void*> others) {
-  for (const void* const* o = outputs.begin(); o != outputs.end(); ++o) {
-    for (const void* const* p = outputs.begin(); p != o; ++p)
-      if (*p == *o) return true;
-    for (const void* p : others)
-      if (p == *o) return true;
-  }
-  return false;
+inline Region heads_region(const HeadView& v, int64_t tokens, int heads, int hd, int64_t size) {
+  return {reinterpret_cast<uintptr_t>(v.ptr), tokens, v.ld * size, heads, v.hs * size, v.ptr ? hd * size : 0};
 }
 
 // Masked attention (tpmlp_masked_attention_*): everything but the gradients. Sizes are checked by the caller; the tiles

@@ -192,6 +192,8 @@ tpmlp_status tpmlp_attention_key_ranges(const void* doc_ids, const void* prefix_
   MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
   if (!aligned(doc_ids, 4) || !aligned(prefix_len, 4))
     return err(TPMLP_ERR_ALIGN, "doc_ids and prefix_len must be 4-byte aligned");
+  if (any_overlap({flat_region(key_range, b * s, 8)}, {flat_region(doc_ids, b * s, 4), flat_region(prefix_len, b, 4)}))
+    return err(TPMLP_ERR_INVALID, "key_range overlaps doc_ids or prefix_len");
   if (window > s) window = 0;  // reaches past both ends
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int* prefix = static_cast<const int*>(prefix_len);
@@ -219,12 +221,16 @@ tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const 
   MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
   MATT_TRY(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
   if (!aligned(slopes, 4)) return err(TPMLP_ERR_ALIGN, "slopes not 4-byte aligned");
-  if (shared_tensor({o, lse}, {q, k, v, key_range, slopes})) return err(TPMLP_ERR_INVALID, "o or lse is another tensor");
-  DeviceCtx ctx;
-  MATT_CUDA(get_device_ctx(&ctx), "device context");
   MaskedAttention a{{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(k), ld_k, hs_k},
                     {const_cast<void*>(v), ld_v, hs_v}, {o, ld_o, hs_o}, static_cast<const int2*>(key_range), slopes,
                     scale, softcap, lse, b, s, heads, kv_heads, head_dim};
+  auto of = [&](const HeadView& view, int n) { return heads_region(view, b * s, n, head_dim, 2); };
+  if (any_overlap({of(a.o, heads), flat_region(lse, b * s * heads, 4)},
+                  {of(a.q, heads), of(a.k, kv_heads), of(a.v, kv_heads), flat_region(key_range, b * s, 8),
+                   flat_region(slopes, heads, 4)}))
+    return err(TPMLP_ERR_INVALID, "o or lse overlaps another tensor of the call");
+  DeviceCtx ctx;
+  MATT_CUDA(get_device_ctx(&ctx), "device context");
   MATT_CUDA(launch_masked_attention_forward(a, static_cast<cudaStream_t>(stream), ctx), "masked attention");
   return TPMLP_OK;
 }
@@ -253,17 +259,19 @@ tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const
   const size_t need = tpmlp_masked_attention_backward_workspace_size(b, s, heads);
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "masked attention backward workspace too small");
   if (!aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
-  if (shared_tensor({dq, dk, dv, workspace}, {q, k, v, key_range, slopes, o, lse, d_o}))
-    return err(TPMLP_ERR_INVALID, "dq, dk, dv or the workspace is another tensor");
-  DeviceCtx ctx;
-  MATT_CUDA(get_device_ctx(&ctx), "device context");
   MaskedAttention a{{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(k), ld_k, hs_k},
                     {const_cast<void*>(v), ld_v, hs_v}, {const_cast<void*>(o), ld_o, hs_o},
                     static_cast<const int2*>(key_range), slopes, scale, softcap, const_cast<float*>(lse), b, s, heads,
                     kv_heads, head_dim};
-  MATT_CUDA(launch_masked_attention_backward(a, {const_cast<void*>(d_o), ld_o, hs_o}, {dq, ld_dq, hs_dq},
-                                             {dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}, workspace,
-                                             static_cast<cudaStream_t>(stream), ctx),
+  const HeadView g{const_cast<void*>(d_o), ld_o, hs_o}, gq{dq, ld_dq, hs_dq}, gk{dk, ld_dk, hs_dk}, gv{dv, ld_dv, hs_dv};
+  auto of = [&](const HeadView& view, int n) { return heads_region(view, b * s, n, head_dim, 2); };
+  if (any_overlap({of(gq, heads), of(gk, kv_heads), of(gv, kv_heads), flat_region(workspace, static_cast<int64_t>(need), 1)},
+                  {of(a.q, heads), of(a.k, kv_heads), of(a.v, kv_heads), flat_region(key_range, b * s, 8),
+                   flat_region(slopes, heads, 4), of(a.o, heads), flat_region(lse, b * s * heads, 4), of(g, heads)}))
+    return err(TPMLP_ERR_INVALID, "dq, dk, dv or the workspace overlaps another tensor of the call");
+  DeviceCtx ctx;
+  MATT_CUDA(get_device_ctx(&ctx), "device context");
+  MATT_CUDA(launch_masked_attention_backward(a, g, gq, gk, gv, workspace, static_cast<cudaStream_t>(stream), ctx),
             "masked attention backward");
   return TPMLP_OK;
 }
