@@ -569,6 +569,8 @@ def attention_key_ranges(b: int, s: int, doc_ids=None, prefix_len=None, causal: 
 def rope_tables(table_len: int, rot_dim: int, theta: float = 10000.0, device=None):
     """The fp32 (cos, sin) tables [table_len, rot_dim / 2] of the angles pos * theta^(-2i / rot_dim), computed in
     64 bits so that far positions keep their phase."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim must be even and at least 2, got {rot_dim}")
     inv = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
     ang = torch.arange(table_len, dtype=torch.float64, device=device)[:, None] * inv
     return ang.cos().float(), ang.sin().float()

@@ -10,6 +10,7 @@ import subprocess
 import pytest
 import torch
 
+import tensor_transformer_mlp_gb300 as tp
 from tensor_transformer_mlp_gb300 import _binding, _build
 
 OK, INVALID, SHAPE, DTYPE, ALIGN, CUDA, TIMEOUT, WORKSPACE = range(8)
@@ -208,3 +209,14 @@ def test_one_packed_matrix_may_hold_all_inputs_or_all_gradients(lib):
                  lambda: _ranges(lib), lambda: _rope(lib), lambda: _rope_backward(lib), lambda: _forward(lib),
                  lambda: _backward(lib)):
         assert call() == CUDA
+
+
+# ------------------------------------------------------------------------- the Python functions
+
+def test_rope_tables_of_odd_widths_are_refused():
+    # 7 columns would get a table of 4 pairs, and the norm with rotation would then turn 8 by other angles
+    for rot in (7, 1, 0, -2):
+        with pytest.raises(ValueError, match="rot_dim must be even"):
+            tp.rope_tables(16, rot)
+    cos, sin = tp.rope_tables(16, 6)
+    assert cos.shape == sin.shape == (16, 3)
