@@ -547,13 +547,17 @@ def attention_key_ranges(b: int, s: int, doc_ids=None, prefix_len=None, causal: 
     """Runs tpmlp_attention_key_ranges; returns the int32 [b, s, 2] key range of every query, for
     masked_attention_forward and _backward. doc_ids int32 [b, s], prefix_len int32 [b]; `device` defaults to theirs,
     else to the current one."""
+    if device is not None:
+        device = torch.device(device)
+    given = doc_ids if doc_ids is not None else prefix_len
     if doc_ids is not None:
         _dense(doc_ids, (b, s), torch.int32, "doc_ids")
-        index = _device(doc_ids, prefix_len)
-    elif prefix_len is not None:
-        index = _device(prefix_len)
+    if given is not None:
+        index = _device(given, prefix_len)
+        if device is not None and (device.type != given.device.type or device.index not in (None, given.device.index)):
+            raise ValueError(f"doc_ids or prefix_len are on {given.device}, not on {device}")
     else:
-        device = torch.device("cuda" if device is None else device)
+        device = torch.device("cuda") if device is None else device
         index = -1 if device.type != "cuda" else torch.cuda.current_device() if device.index is None else device.index
     if prefix_len is not None:
         _dense(prefix_len, (b,), torch.int32, "prefix_len")

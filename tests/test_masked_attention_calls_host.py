@@ -220,3 +220,13 @@ def test_rope_tables_of_odd_widths_are_refused():
             tp.rope_tables(16, rot)
     cos, sin = tp.rope_tables(16, 6)
     assert cos.shape == sin.shape == (16, 3)
+
+
+def test_key_ranges_on_another_device_than_their_tensors_are_refused():
+    ids, prefix = torch.zeros(1, 8, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for kw in (dict(doc_ids=ids), dict(prefix_len=prefix), dict(doc_ids=ids, prefix_len=prefix)):
+        for device in ("cuda", "cuda:1", torch.device("cuda", 0)):
+            with pytest.raises(ValueError, match="on cpu, not on cuda"):
+                tp.attention_key_ranges(1, 8, device=device, **kw)
+        with pytest.raises(ValueError, match="must be CUDA tensors"):
+            tp.attention_key_ranges(1, 8, device="cpu", **kw)
