@@ -565,8 +565,8 @@ def attention_key_ranges(b: int, s: int, doc_ids=None, prefix_len=None, causal: 
     here, st = _where(index, stream)
     with here:
         out = torch.empty((b, s, 2), dtype=torch.int32, device="cuda")
-        _check(lib.tpmlp_attention_key_ranges(_ptr(doc_ids), _ptr(prefix_len), 1 if causal else 0, window, out.data_ptr(),
-                                              b, s, st))
+        _check(lib.tpmlp_attention_key_ranges(_ptr(doc_ids), _ptr(prefix_len), 1 if causal else 0, max(-1, min(window, s)),
+                                              out.data_ptr(), b, s, st))  # a longer window hides nothing; -1: refused
     return out
 
 

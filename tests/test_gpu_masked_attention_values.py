@@ -301,3 +301,19 @@ def test_a_long_row_whose_maximum_moves():
         assert ((o[0, -200:, 0].double() - p @ vd).abs() <= U * (size + (p @ vd).abs()) + SLACK * size).all()
         want = torch.logsumexp(x, -1)
         assert ((lse[0, 0, -200:].double() - want).abs() <= 2.0 ** -20 * (1 + want.abs()) + hd * 2.0 ** -24 * x.amax(-1)).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_windows_of_any_length(causal):
+    # past 64 bits too, of which ctypes would pass the lower ones
+    free = tp.attention_key_ranges(2, 40, causal=causal, device="cuda")
+    for window in (40, 41, 2 ** 31, 2 ** 63 - 1, 2 ** 63, 2 ** 64, 2 ** 64 + 5):
+        assert torch.equal(tp.attention_key_ranges(2, 40, causal=causal, window=window, device="cuda"), free)
+    assert not torch.equal(tp.attention_key_ranges(2, 40, causal=causal, window=39, device="cuda"), free)
+    for window in (-1, -2 ** 64, -2 ** 64 + 5):
+        with pytest.raises(tp.TpmlpError, match="window must be >= 0"):
+            tp.attention_key_ranges(2, 40, window=window, device="cuda")
+    ids = torch.zeros(2, 40, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="not on cpu"):
+        tp.attention_key_ranges(2, 40, doc_ids=ids, device="cpu")
+    assert torch.equal(tp.attention_key_ranges(2, 40, doc_ids=ids, causal=causal, device="cuda"), free)
