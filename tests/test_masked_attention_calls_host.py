@@ -211,6 +211,89 @@ def test_one_packed_matrix_may_hold_all_inputs_or_all_gradients(lib):
         assert call() == CUDA
 
 
+# ------------------------------------------------------------------------- refusals, each by its own message
+
+POINTERS = {_ranges: "ids? prefix? out", _forward: "q k v rng slopes? o lse", _backward: "q k v rng slopes? o lse do dq dk dv",
+            _rope: "q k gq gk cos sin pos? qo ko", _rope_backward: "q k gq gk cos sin pos? dqo dko dq dk dgq dgk"}
+FOURS = "ids prefix slopes lse gq gk cos sin pos dgq dgk".split()     # 4-byte aligned; ranges 8, tensors of heads 16
+
+
+@pytest.mark.parametrize("call", list(POINTERS))
+def test_pointers_are_looked_at(lib, call):
+    place = dict(zip(call.__code__.co_varnames[1:call.__code__.co_argcount], call.__defaults__))
+    for name in POINTERS[call].split():
+        if not name.endswith("?"):
+            _message(lib, call(lib, **{name: None}), INVALID, "null pointer")
+        name = name.rstrip("?")
+        off = 2 if name in FOURS else 4 if name in ("rng", "out") else 8
+        _message(lib, call(lib, **{name: place[name] + off}), ALIGN, "aligned")
+
+
+@pytest.mark.parametrize("call", [_forward, _backward])
+def test_numbers_of_attention_are_looked_at(lib, call):
+    inf, nan = float("inf"), float("nan")
+    for bad in (0.0, -1.0, inf, nan):
+        _message(lib, call(lib, scale=bad), INVALID, "scale must be positive and finite")
+    for bad in (-1.0, inf, nan):
+        _message(lib, call(lib, cap=bad), INVALID, "softcap must be >= 0 and finite")
+    for bad in (dict(scale=2e30), dict(cap=2e30), dict(scale=1.0, cap=1e-38)):
+        _message(lib, call(lib, **bad), INVALID, "at most 1e30")
+    _message(lib, call(lib, dt=F32), DTYPE, "bf16")
+    for bad in (dict(heads=0), dict(kv=0), dict(b=-1), dict(s=-1)):
+        _message(lib, call(lib, **bad), SHAPE, "need b, s >= 0")
+    _message(lib, call(lib, kv=3), SHAPE, "multiple of kv_heads")
+    for hd in (0, 4, 60, 136):
+        _message(lib, call(lib, hd=hd), SHAPE, "head_dim must be a multiple of 8")
+    _message(lib, call(lib, b=1 << 16, s=1 << 16), SHAPE, "2^31-1")
+    _message(lib, call(lib, b=1, s=(1 << 30) + 1), SHAPE, "2^30")
+    _message(lib, call(lib, b=65536, s=1), SHAPE, "at most 65535")
+    strides = call.__defaults__[call.__code__.co_varnames[1:].index("st")]
+    for n in range(len(strides)):
+        for bad in (0, -64, 68, 1 << 50):
+            _message(lib, call(lib, st=strides[:n] + (bad,) + strides[n + 1:]), SHAPE, "strides must be positive multiples of 8")
+    for n in ((6, 7) if call is _forward else range(8, 14)):
+        _message(lib, call(lib, st=strides[:n] + (56 if n % 2 else strides[n] // 2,) + strides[n + 1:]), SHAPE, "heads overlap")
+
+
+@pytest.mark.parametrize("call", [_rope, _rope_backward])
+def test_numbers_of_the_norm_are_looked_at(lib, call):
+    for eps in (0.0, -1.0, float("nan")):
+        _message(lib, call(lib, eps=eps), INVALID, "eps must be > 0")
+    for style in (-1, 2):
+        _message(lib, call(lib, style=style), INVALID, "unknown rope style")
+    _message(lib, call(lib, dt=3), DTYPE, "unsupported dtype")
+    for rot in (0, 63, 66, -2):
+        _message(lib, call(lib, rot=rot), SHAPE, "rot_dim must be even")
+    for hd in (0, 60, 264):
+        _message(lib, call(lib, hd=hd), SHAPE, "head_dim must be a multiple of 8")
+    _message(lib, call(lib, table=0), SHAPE, "table_len must be >= 1")
+    _message(lib, call(lib, heads=0), SHAPE, "need b, s >= 0")
+    _message(lib, call(lib, heads=65537), SHAPE, "at most 65536 heads")
+    strides = call.__defaults__[call.__code__.co_varnames[1:].index("st")]
+    for n in range(len(strides)):
+        for bad in (0, -64, 68, 1 << 50):
+            _message(lib, call(lib, st=strides[:n] + (bad,) + strides[n + 1:]), SHAPE, "strides must be positive multiples of 8")
+    for n in range(len(strides) - 4, len(strides)):
+        _message(lib, call(lib, st=strides[:n] + (56 if n % 2 else strides[n] // 2,) + strides[n + 1:]), SHAPE, "heads overlap")
+
+
+def test_numbers_of_key_ranges_are_looked_at(lib):
+    for causal in (-1, 2):
+        _message(lib, _ranges(lib, causal=causal), INVALID, "causal is 0 or 1")
+    _message(lib, _ranges(lib, window=-1), INVALID, "window must be >= 0")
+    _message(lib, _ranges(lib, causal=0), INVALID, "a prefix needs a causal mask")
+    _message(lib, _ranges(lib, b=-1), SHAPE, "need b, s >= 0")
+    _message(lib, _ranges(lib, b=1, s=(1 << 30) + 1), SHAPE, "2^30")
+
+
+def test_workspaces_are_looked_at(lib):
+    for call, size, name in ((_backward, lib.tpmlp_masked_attention_backward_workspace_size(2, 16, 4), "masked attention"),
+                             (_rope_backward, lib.tpmlp_qk_norm_rope_backward_workspace_size(1, 8, 64), "qk_norm_rope")):
+        _message(lib, call(lib, ws=None), WORKSPACE, name)
+        _message(lib, call(lib, wsb=size - 1), WORKSPACE, name)
+        _message(lib, call(lib, ws=AT[13] + 8), ALIGN, "workspace not")
+
+
 # ------------------------------------------------------------------------- the Python functions
 
 def test_rope_tables_of_odd_widths_are_refused():
@@ -230,3 +313,91 @@ def test_key_ranges_on_another_device_than_their_tensors_are_refused():
                 tp.attention_key_ranges(1, 8, device=device, **kw)
         with pytest.raises(ValueError, match="must be CUDA tensors"):
             tp.attention_key_ranges(1, 8, device="cpu", **kw)
+
+
+def _cpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+@pytest.mark.parametrize("message,change", [
+    ("key_range must be a contiguous torch.int32", dict(key_range=_cpu(1, 8, 2, dtype=torch.int64))),
+    ("key_range must be a contiguous torch.int32", dict(key_range=_cpu(1, 4, 2, dtype=torch.int32))),
+    ("key_range must be a contiguous torch.int32", dict(key_range=_cpu(1, 8, 4, dtype=torch.int32)[..., :2])),
+    ("slopes must be a contiguous torch.float32", dict(slopes=torch.zeros(3))),
+    ("slopes must be a contiguous torch.float32", dict(slopes=torch.zeros(2, dtype=torch.float64))),
+    (r"k must be \[1, 8, 1, 64\]", dict(k=_cpu(1, 7, 1, 64))),
+    (r"v must be \[1, 8, 1, 64\]", dict(v=_cpu(1, 8, 2, 64))),
+    ("k must be torch.bfloat16", dict(k=_cpu(1, 8, 1, 64, dtype=torch.float32))),
+    ("v must be torch.bfloat16", dict(v=_cpu(1, 8, 1, 64, dtype=torch.float16))),
+    ("q needs contiguous columns", dict(q=_cpu(1, 8, 64, 2).transpose(2, 3))),
+    ("must be CUDA tensors", {}),
+])
+def test_python_attention_names_what_it_refuses(message, change):
+    args = dict(q=_cpu(1, 8, 2, 64), k=_cpu(1, 8, 1, 64), v=_cpu(1, 8, 1, 64), key_range=_cpu(1, 8, 2, dtype=torch.int32))
+    args.update(change)
+    with pytest.raises(ValueError, match=message):
+        tp.masked_attention_forward(**args)
+    grads = dict(o=_cpu(1, 8, 2, 64), lse=torch.zeros(1, 2, 8), do=_cpu(1, 8, 2, 64))
+    with pytest.raises(ValueError, match=message):
+        tp.masked_attention_backward(**args, **grads)
+
+
+@pytest.mark.parametrize("message,change", [
+    ("lse must be a contiguous torch.float32", dict(lse=torch.zeros(1, 8, 2))),
+    ("lse must be a contiguous torch.float32", dict(lse=torch.zeros(1, 2, 8, dtype=torch.float64))),
+    (r"o must be \[1, 8, 2, 64\]", dict(o=_cpu(1, 8, 2, 32))),
+    ("o must be torch.bfloat16", dict(o=torch.zeros(1, 8, 2, 64))),
+    (r"do must be \[1, 8, 2, 64\]", dict(do=_cpu(2, 8, 2, 64))),
+    ("do must have o's strides", dict(do=_cpu(1, 8, 2, 128)[..., :64])),
+])
+def test_python_attention_backward_names_what_it_refuses(message, change):
+    args = dict(o=_cpu(1, 8, 2, 64), lse=torch.zeros(1, 2, 8), do=_cpu(1, 8, 2, 64))
+    args.update(change)
+    with pytest.raises(ValueError, match=message):
+        tp.masked_attention_backward(_cpu(1, 8, 2, 64), _cpu(1, 8, 1, 64), _cpu(1, 8, 1, 64), _cpu(1, 8, 2, dtype=torch.int32),
+                                     **args)
+
+
+def test_python_attention_names_strides_it_cannot_take():
+    t, r = _cpu(2, 2, 8, 64).transpose(1, 2), _cpu(2, 8, 2, dtype=torch.int32)      # [b, heads, s, hd] memory
+    with pytest.raises(ValueError, match="q needs contiguous columns and one stride for all tokens"):
+        tp.masked_attention_forward(t, t, t, r)
+    q = _cpu(2, 8, 2, 64)
+    with pytest.raises(ValueError, match="k needs contiguous columns and one stride for all tokens"):
+        tp.masked_attention_forward(q, t, t, r)
+    with pytest.raises(ValueError, match="v needs contiguous columns and one stride for all tokens"):
+        tp.masked_attention_forward(q, q, _cpu(2, 9, 2, 64)[:, 1:], r)              # a slice of the tokens
+
+
+@pytest.mark.parametrize("message,change", [
+    (r"cos and sin must be \[table_len, rot_dim / 2\]", dict(cos=torch.ones(64), sin=torch.ones(64))),
+    ("sin must be a contiguous torch.float32", dict(sin=torch.ones(16, 31))),
+    ("cos must be a contiguous torch.float32", dict(cos=torch.ones(16, 32, dtype=torch.float64))),
+    ("gamma_q must be a contiguous torch.float32", dict(gamma_q=torch.ones(32))),
+    ("gamma_k must be a contiguous torch.float32", dict(gamma_k=torch.ones(64, dtype=torch.bfloat16))),
+    ("positions must be a contiguous torch.int32", dict(positions=torch.zeros(1, 8, dtype=torch.int64))),
+    ("positions must be a contiguous torch.int32", dict(positions=torch.zeros(8, dtype=torch.int32))),
+    (r"k must be \[1, 8, 1, 64\]", dict(k=_cpu(1, 8, 1, 32))),
+    ("k must be torch.bfloat16", dict(k=torch.zeros(1, 8, 1, 64))),
+    ("q needs contiguous columns", dict(q=_cpu(1, 8, 64, 2).transpose(2, 3))),
+    ("must be CUDA tensors", {}),
+])
+def test_python_norm_names_what_it_refuses(message, change):
+    args = dict(q=_cpu(1, 8, 2, 64), k=_cpu(1, 8, 1, 64), gamma_q=torch.ones(64), gamma_k=torch.ones(64),
+                cos=torch.ones(16, 32), sin=torch.ones(16, 32))
+    args.update(change)
+    with pytest.raises(ValueError, match=message):
+        tp.qk_norm_rope(**args)
+    with pytest.raises(ValueError, match=message):
+        tp.qk_norm_rope_backward(**args, dq_out=_cpu(1, 8, 2, 64), dk_out=_cpu(1, 8, 1, 64))
+
+
+@pytest.mark.parametrize("message,change", [
+    ("doc_ids must be a contiguous torch.int32", dict(doc_ids=torch.zeros(1, 7, dtype=torch.int32))),
+    ("doc_ids must be a contiguous torch.int32", dict(doc_ids=torch.zeros(1, 8, dtype=torch.int64))),
+    ("prefix_len must be a contiguous torch.int32", dict(prefix_len=torch.zeros(2, dtype=torch.int32))),
+    ("must be CUDA tensors", dict(device="cpu")),
+])
+def test_python_key_ranges_name_what_they_refuse(message, change):
+    with pytest.raises(ValueError, match=message):
+        tp.attention_key_ranges(1, 8, **change)
