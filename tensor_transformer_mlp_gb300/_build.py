@@ -18,7 +18,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libtpmlp.so")
 SOURCES = ["tpmlp_api.cu", "gemm_tc.cu", "gemm_simt.cu", "sp_kernels.cu", "tpmlp_noalloc.cu", "tpmlp_attention.cu",
            "qk_norm_rope.cu", "masked_attention_fwd.cu", "masked_attention_bwd.cu", "tpmlp_masked_attention.cu"]
-HEADERS = ["device_common.cuh", "tpmlp_internal.h", "attention_tiles.cuh", "overlap.h"]
+HEADERS = ["device_common.cuh", "tpmlp_internal.h", "attention_tiles.cuh", "overlap.h",
+           "abi_checks.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

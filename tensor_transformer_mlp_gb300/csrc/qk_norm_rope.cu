@@ -17,9 +17,8 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdio>
 
-#include "../../include/tpmlp.h"
+#include "abi_checks.h"
 #include "device_common.cuh"
 
 namespace tpmlp {
@@ -397,16 +396,6 @@ __global__ void __launch_bounds__(1024)
   if (row == 0 && c < hd) (blockIdx.y ? dgamma_k : dgamma_q)[c] = red[0][col];
 }
 
-tpmlp_status err(tpmlp_status st, const char* msg) { return static_cast<tpmlp_status>(report_error(st, msg)); }
-
-tpmlp_status cuda_err(cudaError_t e, const char* what) {
-  char msg[256];
-  snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
-  return err(TPMLP_ERR_CUDA, msg);
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 tpmlp_status check_strides(int64_t b, int64_t s, int heads, int kv_heads, int hd, std::initializer_list<HeadView> inputs,
                            const HeadView& q_out, const HeadView& k_out) {
   for (const HeadView& v : inputs)
@@ -431,14 +420,6 @@ tpmlp_status check(float eps, int64_t table_len, int rot, int style, int64_t b, 
   if (table_len < 1) return err(TPMLP_ERR_SHAPE, "table_len must be >= 1");
   if (style != TPMLP_ROPE_HALF && style != TPMLP_ROPE_INTERLEAVED) return err(TPMLP_ERR_INVALID, "unknown rope style");
   if (!(eps > 0.0f)) return err(TPMLP_ERR_INVALID, "eps must be > 0");
-  return TPMLP_OK;
-}
-
-tpmlp_status check_ptrs(std::initializer_list<const void*> ptrs, size_t a) {
-  for (const void* p : ptrs) {
-    if (!p) return err(TPMLP_ERR_INVALID, "null pointer");
-    if (!aligned(p, a)) return err(TPMLP_ERR_ALIGN, a == 16 ? "pointer not 16-byte aligned" : "pointer not 4-byte aligned");
-  }
   return TPMLP_OK;
 }
 
@@ -481,17 +462,6 @@ int pairing_of(int style, int rot) {
 
 using namespace tpmlp;
 
-#define ROPE_TRY(expr)                  \
-  do {                                  \
-    tpmlp_status _s = (expr);           \
-    if (_s != TPMLP_OK) return _s;      \
-  } while (0)
-#define ROPE_CUDA(expr, what)                       \
-  do {                                              \
-    cudaError_t _e = (expr);                        \
-    if (_e != cudaSuccess) return cuda_err(_e, what); \
-  } while (0)
-
 extern "C" {
 
 tpmlp_status tpmlp_qk_norm_rope(const void* q, const void* k, const float* gamma_q, const float* gamma_k, float eps,
@@ -500,12 +470,12 @@ tpmlp_status tpmlp_qk_norm_rope(const void* q, const void* k, const float* gamma
                                 int64_t s, int heads, int kv_heads, int head_dim, int64_t ld_q, int64_t hs_q,
                                 int64_t ld_k, int64_t hs_k, int64_t ld_qo, int64_t hs_qo, int64_t ld_ko,
                                 int64_t hs_ko, tpmlp_dtype dt, void* stream) {
-  ROPE_TRY(check(eps, table_len, rot_dim, style, b, s, heads, kv_heads, head_dim, dt));
-  ROPE_TRY(check_strides(b, s, heads, kv_heads, head_dim, {{nullptr, ld_q, hs_q}, {nullptr, ld_k, hs_k}},
+  TPMLP_PASS(check(eps, table_len, rot_dim, style, b, s, heads, kv_heads, head_dim, dt));
+  TPMLP_PASS(check_strides(b, s, heads, kv_heads, head_dim, {{nullptr, ld_q, hs_q}, {nullptr, ld_k, hs_k}},
                          {q_out, ld_qo, hs_qo}, {k_out, ld_ko, hs_ko}));
   if (b * s == 0) return TPMLP_OK;
-  ROPE_TRY(check_ptrs({q, k, q_out, k_out}, 16));
-  ROPE_TRY(check_ptrs({gamma_q, gamma_k, cos_table, sin_table}, 4));
+  TPMLP_PASS(check_ptrs({q, k, q_out, k_out}, 16, "pointer not 16-byte aligned"));
+  TPMLP_PASS(check_ptrs({gamma_q, gamma_k, cos_table, sin_table}, 4, "pointer not 4-byte aligned"));
   if (!aligned(positions, 4)) return err(TPMLP_ERR_ALIGN, "positions not 4-byte aligned");
   const int64_t tokens = b * s, size = dt == TPMLP_BF16 ? 2 : 4;
   auto of = [&](const void* p, int64_t ld, int64_t hs, int n) {
@@ -531,7 +501,7 @@ tpmlp_status tpmlp_qk_norm_rope(const void* q, const void* k, const float* gamma
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto kernel = ROPE_PICK(qk_norm_rope_kernel, dt, pairing_of(style, rot_dim));
   kernel<<<static_cast<unsigned>(ctas), kThreads, 0, st>>>(p);
-  ROPE_CUDA(cudaGetLastError(), "qk_norm_rope");
+  TPMLP_PASS_CUDA(cudaGetLastError(), "qk_norm_rope");
   return TPMLP_OK;
 }
 
@@ -549,19 +519,19 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
                                          int64_t hs_qo, int64_t ld_ko, int64_t hs_ko, int64_t ld_dq, int64_t hs_dq,
                                          int64_t ld_dk, int64_t hs_dk, tpmlp_dtype dt, void* workspace,
                                          size_t ws_bytes, void* stream) {
-  ROPE_TRY(check(eps, table_len, rot_dim, style, b, s, heads, kv_heads, head_dim, dt));
-  ROPE_TRY(check_strides(b, s, heads, kv_heads, head_dim,
+  TPMLP_PASS(check(eps, table_len, rot_dim, style, b, s, heads, kv_heads, head_dim, dt));
+  TPMLP_PASS(check_strides(b, s, heads, kv_heads, head_dim,
                          {{nullptr, ld_q, hs_q}, {nullptr, ld_k, hs_k}, {nullptr, ld_qo, hs_qo}, {nullptr, ld_ko, hs_ko}},
                          {dq, ld_dq, hs_dq}, {dk, ld_dk, hs_dk}));
-  ROPE_TRY(check_ptrs({dgamma_q, dgamma_k}, 4));
+  TPMLP_PASS(check_ptrs({dgamma_q, dgamma_k}, 4, "pointer not 4-byte aligned"));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (b * s == 0) {  // no tokens: the gains' gradients are empty sums
-    ROPE_CUDA(cudaMemsetAsync(dgamma_q, 0, static_cast<size_t>(head_dim) * sizeof(float), st), "zero dgamma_q");
-    ROPE_CUDA(cudaMemsetAsync(dgamma_k, 0, static_cast<size_t>(head_dim) * sizeof(float), st), "zero dgamma_k");
+    TPMLP_PASS_CUDA(cudaMemsetAsync(dgamma_q, 0, static_cast<size_t>(head_dim) * sizeof(float), st), "zero dgamma_q");
+    TPMLP_PASS_CUDA(cudaMemsetAsync(dgamma_k, 0, static_cast<size_t>(head_dim) * sizeof(float), st), "zero dgamma_k");
     return TPMLP_OK;
   }
-  ROPE_TRY(check_ptrs({q, k, dq_out, dk_out, dq, dk}, 16));
-  ROPE_TRY(check_ptrs({gamma_q, gamma_k, cos_table, sin_table}, 4));
+  TPMLP_PASS(check_ptrs({q, k, dq_out, dk_out, dq, dk}, 16, "pointer not 16-byte aligned"));
+  TPMLP_PASS(check_ptrs({gamma_q, gamma_k, cos_table, sin_table}, 4, "pointer not 4-byte aligned"));
   if (!aligned(positions, 4)) return err(TPMLP_ERR_ALIGN, "positions not 4-byte aligned");
   const size_t need = tpmlp_qk_norm_rope_backward_workspace_size(b, s, head_dim);
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "qk_norm_rope backward workspace too small");
@@ -583,7 +553,7 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
     return err(TPMLP_ERR_INVALID, "an output overlaps another tensor of the call (in place dq is q or dq_out and dk is k or "
                                   "dk_out, with the same strides)");
   DeviceCtx ctx;
-  ROPE_CUDA(get_device_ctx(&ctx), "device context");
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
   RopeParams p = make_params(
       {{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(dq_out), ld_qo, hs_qo}, {dq, ld_dq, hs_dq}, gamma_q, heads, 0},
       {{const_cast<void*>(k), ld_k, hs_k}, {const_cast<void*>(dk_out), ld_ko, hs_ko}, {dk, ld_dk, hs_dk}, gamma_k, kv_heads, 0},
@@ -599,7 +569,7 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
   float* partials = static_cast<float*>(workspace);
   auto kernel = ROPE_PICK(qk_norm_rope_backward_kernel, dt, pairing_of(style, rot_dim));
   kernel<<<grid, kThreads, 0, st>>>(p, partials);
-  ROPE_CUDA(cudaGetLastError(), "qk_norm_rope backward");
+  TPMLP_PASS_CUDA(cudaGetLastError(), "qk_norm_rope backward");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((head_dim + 31) / 32), 2);
   cfg.blockDim = dim3(1024);
@@ -609,7 +579,7 @@ tpmlp_status tpmlp_qk_norm_rope_backward(const void* q, const void* k, const flo
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  ROPE_CUDA(cudaLaunchKernelEx(&cfg, rope_gain_sum_kernel, static_cast<const float*>(partials), p.ctas0, grid, head_dim, dgamma_q,
+  TPMLP_PASS_CUDA(cudaLaunchKernelEx(&cfg, rope_gain_sum_kernel, static_cast<const float*>(partials), p.ctas0, grid, head_dim, dgamma_q,
                                dgamma_k),
             "qk_norm_rope gain sums");
   return TPMLP_OK;

@@ -8,10 +8,8 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstdio>
 
-#include "../../include/tpmlp.h"
-#include "tpmlp_internal.h"
+#include "abi_checks.h"
 
 using namespace tpmlp;
 
@@ -20,20 +18,6 @@ namespace {
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-tpmlp_status err(tpmlp_status st, const char* msg) { return static_cast<tpmlp_status>(report_error(st, msg)); }
-
-tpmlp_status cuda_err(cudaError_t e, const char* what) {
-  char msg[256];
-  snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
-  return err(TPMLP_ERR_CUDA, msg);
-}
-
-#define ATT_CUDA(expr, what)                        \
-  do {                                              \
-    cudaError_t _e = (expr);                        \
-    if (_e != cudaSuccess) return cuda_err(_e, what); \
-  } while (0)
 
 EpiParams plain_epi(void* out, int64_t ldo) {
   EpiParams e{};
@@ -114,14 +98,14 @@ tpmlp_status tpmlp_attention_forward(const void* X, const void* Wqkv, const void
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "attention forward workspace too small");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
   DeviceCtx ctx;
-  ATT_CUDA(get_device_ctx(&ctx), "device context");
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
   cudaStream_t stm = static_cast<cudaStream_t>(stream);
   const int64_t n = b * s, dh = h / heads;
   const int64_t rows = b * heads * s;
   void* stats = workspace;
   void* rowstats = static_cast<char*>(workspace) + round_up(static_cast<size_t>(rows * stat_parts(s)) * 8, 256);
   // QKV = X W_qkv (column-parallel: every shard's heads at once)
-  ATT_CUDA(gemm_bf16_tc(n, 3 * h, h, Operand{X, n, h, h, false}, Operand{Wqkv, h, 3 * h, 3 * h, true}, kEpiStore,
+  TPMLP_PASS_CUDA(gemm_bf16_tc(n, 3 * h, h, Operand{X, n, h, h, false}, Operand{Wqkv, h, 3 * h, 3 * h, true}, kEpiStore,
                         plain_epi(QKV_save, 3 * h), stm, ctx),
            "QKV GEMM");
   // P = softmax(Q K^T / sqrt(dh)) per (head, sequence) in two passes over the same scores: the
@@ -130,23 +114,23 @@ tpmlp_status tpmlp_attention_forward(const void* X, const void* Wqkv, const void
   BatchSpec bs_s{heads, b, s * s, heads * s * s, static_cast<float>(1.0 / std::sqrt(static_cast<double>(dh)))};
   EpiParams ep_stats = plain_epi(nullptr, s);
   ep_stats.stats = stats;
-  ATT_CUDA(gemm_bf16_tc_batched(s, s, dh, qkv_view(QKV_save, 0, s, h, dh, false), qkv_view(QKV_save, 1, s, h, dh, false),
+  TPMLP_PASS_CUDA(gemm_bf16_tc_batched(s, s, dh, qkv_view(QKV_save, 0, s, h, dh, false), qkv_view(QKV_save, 1, s, h, dh, false),
                                 bs_s, kEpiRowStats, ep_stats, stm, ctx),
            "scores GEMM (row statistics)");
-  ATT_CUDA(launch_softmax_combine(stats, static_cast<int>(stat_parts(s)), rowstats, rows, stm, ctx.num_sms),
+  TPMLP_PASS_CUDA(launch_softmax_combine(stats, static_cast<int>(stat_parts(s)), rowstats, rows, stm, ctx.num_sms),
            "softmax statistics");
   EpiParams ep_p = plain_epi(P_save, s);
   ep_p.rowvec = rowstats;
-  ATT_CUDA(gemm_bf16_tc_batched(s, s, dh, qkv_view(QKV_save, 0, s, h, dh, false), qkv_view(QKV_save, 1, s, h, dh, false),
+  TPMLP_PASS_CUDA(gemm_bf16_tc_batched(s, s, dh, qkv_view(QKV_save, 0, s, h, dh, false), qkv_view(QKV_save, 1, s, h, dh, false),
                                 bs_s, kEpiSoftmax, ep_p, stm, ctx),
            "scores GEMM (softmax)");
   // O_head = P V, written into the head's columns of O [b*s][h]
   BatchSpec bs_o{heads, b, dh, s * h, 1.0f};
-  ATT_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(P_save, s, heads, false), qkv_view(QKV_save, 2, s, h, dh, true),
+  TPMLP_PASS_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(P_save, s, heads, false), qkv_view(QKV_save, 2, s, h, dh, true),
                                 bs_o, kEpiStore, plain_epi(O_save, h), stm, ctx),
            "PV GEMM");
   // Y = O W_o (row-parallel: the K-loop over every head sums the shards' partials)
-  ATT_CUDA(gemm_bf16_tc(n, h, h, Operand{O_save, n, h, h, false}, Operand{Wo, h, h, h, true}, kEpiStore,
+  TPMLP_PASS_CUDA(gemm_bf16_tc(n, h, h, Operand{O_save, n, h, h, false}, Operand{Wo, h, h, h, true}, kEpiStore,
                         plain_epi(Y, h), stm, ctx),
            "output projection GEMM");
   return TPMLP_OK;
@@ -173,8 +157,8 @@ tpmlp_status tpmlp_attention_backward(const void* X, const void* Wqkv, const voi
   }
   if (b == 0) {  // no tokens: the weight gradients are empty sums
     cudaStream_t stm = static_cast<cudaStream_t>(stream);
-    ATT_CUDA(cudaMemsetAsync(dWqkv, 0, static_cast<size_t>(h) * 3 * h * sizeof(float), stm), "zero dWqkv");
-    ATT_CUDA(cudaMemsetAsync(dWo, 0, static_cast<size_t>(h) * h * sizeof(float), stm), "zero dWo");
+    TPMLP_PASS_CUDA(cudaMemsetAsync(dWqkv, 0, static_cast<size_t>(h) * 3 * h * sizeof(float), stm), "zero dWqkv");
+    TPMLP_PASS_CUDA(cudaMemsetAsync(dWo, 0, static_cast<size_t>(h) * h * sizeof(float), stm), "zero dWo");
     return TPMLP_OK;
   }
   for (const void* p : {X, G, QKV_save, P_save, O_save, static_cast<const void*>(dX)}) {
@@ -185,7 +169,7 @@ tpmlp_status tpmlp_attention_backward(const void* X, const void* Wqkv, const voi
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "attention backward workspace too small");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
   DeviceCtx ctx;
-  ATT_CUDA(get_device_ctx(&ctx), "device context");
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
   cudaStream_t stm = static_cast<cudaStream_t>(stream);
   const int64_t n = b * s, dh = h / heads;
   const size_t sc = scores_elems(b, s, heads);
@@ -205,40 +189,40 @@ tpmlp_status tpmlp_attention_backward(const void* X, const void* Wqkv, const voi
     ep_do.rowdot_s = s;
     ep_do.rowdot_heads = heads;
   }
-  ATT_CUDA(gemm_bf16_tc(n, h, h, Operand{G, n, h, h, false}, Operand{Wo, h, h, h, false},
+  TPMLP_PASS_CUDA(gemm_bf16_tc(n, h, h, Operand{G, n, h, h, false}, Operand{Wo, h, h, h, false},
                         fused_rowdot ? kEpiStoreRowDot : kEpiStore, ep_do, stm, ctx),
            "dO GEMM");
-  ATT_CUDA(gemm_bf16_tc(h, h, n, Operand{O_save, n, h, h, true}, Operand{G, n, h, h, true}, kEpiStoreF32,
+  TPMLP_PASS_CUDA(gemm_bf16_tc(h, h, n, Operand{O_save, n, h, h, true}, Operand{G, n, h, h, true}, kEpiStoreF32,
                         plain_epi(dWo, h), stm, ctx),
            "dWo GEMM");
   // per head: dV = P^T dO, dP = dO V^T, dS = softmax'(dP) / sqrt(dh), dQ = dS K, dK = dS^T Q
   const BatchSpec bs_qkv{heads, b, 3 * dh, s * 3 * h, 1.0f};
   char* dq = static_cast<char*>(dQKV);
-  ATT_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(P_save, s, heads, true), heads_view(dO, s, h, dh, true), bs_qkv,
+  TPMLP_PASS_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(P_save, s, heads, true), heads_view(dO, s, h, dh, true), bs_qkv,
                                 kEpiStore, plain_epi(dq + 2 * dh * 2, 3 * h), stm, ctx),
            "dV GEMM");
   // dS = P * (dP - D) / sqrt(dh) with dP = dO V^T computed and consumed in the same GEMM's
   // epilogue; D = rowsum(P * dP) = rowsum(dO * O) per (head, query row), from dO and O alone.
-  if (!fused_rowdot) ATT_CUDA(launch_row_dot(dO, O_save, D, b, s, h, heads, stm, ctx.num_sms), "rowsum(dO * O)");
+  if (!fused_rowdot) TPMLP_PASS_CUDA(launch_row_dot(dO, O_save, D, b, s, h, heads, stm, ctx.num_sms), "rowsum(dO * O)");
   const BatchSpec bs_p{heads, b, s * s, heads * s * s, 1.0f};
   EpiParams ep_ds = plain_epi(dS, s);
   ep_ds.aux = P_save;
   ep_ds.rowvec = D;
   ep_ds.escale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(dh)));
-  ATT_CUDA(gemm_bf16_tc_batched(s, s, dh, heads_view(dO, s, h, dh, false), qkv_view(QKV_save, 2, s, h, dh, false),
+  TPMLP_PASS_CUDA(gemm_bf16_tc_batched(s, s, dh, heads_view(dO, s, h, dh, false), qkv_view(QKV_save, 2, s, h, dh, false),
                                 bs_p, kEpiSoftmaxGrad, ep_ds, stm, ctx),
            "dP GEMM (softmax backward)");
-  ATT_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(dS, s, heads, false), qkv_view(QKV_save, 1, s, h, dh, true),
+  TPMLP_PASS_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(dS, s, heads, false), qkv_view(QKV_save, 1, s, h, dh, true),
                                 bs_qkv, kEpiStore, plain_epi(dq, 3 * h), stm, ctx),
            "dQ GEMM");
-  ATT_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(dS, s, heads, true), qkv_view(QKV_save, 0, s, h, dh, true),
+  TPMLP_PASS_CUDA(gemm_bf16_tc_batched(s, dh, s, scores_view(dS, s, heads, true), qkv_view(QKV_save, 0, s, h, dh, true),
                                 bs_qkv, kEpiStore, plain_epi(dq + dh * 2, 3 * h), stm, ctx),
            "dK GEMM");
   // QKV projection: dX = dQKV W_qkv^T (K-loop over every shard's heads), dW_qkv = X^T dQKV
-  ATT_CUDA(gemm_bf16_tc(n, h, 3 * h, Operand{dQKV, n, 3 * h, 3 * h, false}, Operand{Wqkv, h, 3 * h, 3 * h, false},
+  TPMLP_PASS_CUDA(gemm_bf16_tc(n, h, 3 * h, Operand{dQKV, n, 3 * h, 3 * h, false}, Operand{Wqkv, h, 3 * h, 3 * h, false},
                         kEpiStore, plain_epi(dX, h), stm, ctx),
            "dX GEMM");
-  ATT_CUDA(gemm_bf16_tc(h, 3 * h, n, Operand{X, n, h, h, true}, Operand{dQKV, n, 3 * h, 3 * h, true}, kEpiStoreF32,
+  TPMLP_PASS_CUDA(gemm_bf16_tc(h, 3 * h, n, Operand{X, n, h, h, true}, Operand{dQKV, n, 3 * h, 3 * h, true}, kEpiStoreF32,
                         plain_epi(dWqkv, 3 * h), stm, ctx),
            "dWqkv GEMM");
   return TPMLP_OK;

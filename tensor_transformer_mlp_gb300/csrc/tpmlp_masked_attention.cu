@@ -6,10 +6,8 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstdio>
 
-#include "../../include/tpmlp.h"
-#include "tpmlp_internal.h"
+#include "abi_checks.h"
 
 namespace tpmlp {
 namespace {
@@ -115,16 +113,6 @@ __global__ void __launch_bounds__(kRangeThreads)
   }
 }
 
-tpmlp_status err(tpmlp_status st, const char* msg) { return static_cast<tpmlp_status>(report_error(st, msg)); }
-
-tpmlp_status cuda_err(cudaError_t e, const char* what) {
-  char msg[256];
-  snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
-  return err(TPMLP_ERR_CUDA, msg);
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 tpmlp_status check_shape(float scale, float softcap, int64_t b, int64_t s, int heads, int kv_heads, int hd,
                          tpmlp_dtype dt, std::initializer_list<HeadView> inputs,
                          std::initializer_list<HeadView> q_outputs, std::initializer_list<HeadView> k_outputs) {
@@ -154,29 +142,10 @@ tpmlp_status check_shape(float scale, float softcap, int64_t b, int64_t s, int h
   return TPMLP_OK;
 }
 
-tpmlp_status check_ptrs(std::initializer_list<const void*> ptrs, size_t a, const char* what) {
-  for (const void* p : ptrs) {
-    if (!p) return err(TPMLP_ERR_INVALID, "null pointer");
-    if (!aligned(p, a)) return err(TPMLP_ERR_ALIGN, what);
-  }
-  return TPMLP_OK;
-}
-
 }  // namespace
 }  // namespace tpmlp
 
 using namespace tpmlp;
-
-#define MATT_TRY(expr)                  \
-  do {                                  \
-    tpmlp_status _s = (expr);           \
-    if (_s != TPMLP_OK) return _s;      \
-  } while (0)
-#define MATT_CUDA(expr, what)                       \
-  do {                                              \
-    cudaError_t _e = (expr);                        \
-    if (_e != cudaSuccess) return cuda_err(_e, what); \
-  } while (0)
 
 extern "C" {
 
@@ -189,7 +158,7 @@ tpmlp_status tpmlp_attention_key_ranges(const void* doc_ids, const void* prefix_
   if (window < 0) return err(TPMLP_ERR_INVALID, "window must be >= 0");
   if (prefix_len && !causal) return err(TPMLP_ERR_INVALID, "a prefix needs a causal mask");
   if (b * s == 0) return TPMLP_OK;
-  MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
+  TPMLP_PASS(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
   if (!aligned(doc_ids, 4) || !aligned(prefix_len, 4))
     return err(TPMLP_ERR_ALIGN, "doc_ids and prefix_len must be 4-byte aligned");
   if (any_overlap({flat_region(key_range, b * s, 8)}, {flat_region(doc_ids, b * s, 4), flat_region(prefix_len, b, 4)}))
@@ -205,7 +174,7 @@ tpmlp_status tpmlp_attention_key_ranges(const void* doc_ids, const void* prefix_
     const int64_t ctas = (b * s + 255) / 256;
     key_range_kernel<<<static_cast<unsigned>(ctas < 4096 ? ctas : 4096), 256, 0, st>>>(prefix, causal, window, out, b, s);
   }
-  MATT_CUDA(cudaGetLastError(), "key ranges");
+  TPMLP_PASS_CUDA(cudaGetLastError(), "key ranges");
   return TPMLP_OK;
 }
 
@@ -214,12 +183,12 @@ tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const 
                                             int64_t b, int64_t s, int heads, int kv_heads, int head_dim, int64_t ld_q,
                                             int64_t hs_q, int64_t ld_k, int64_t hs_k, int64_t ld_v, int64_t hs_v,
                                             int64_t ld_o, int64_t hs_o, tpmlp_dtype dt, void* stream) {
-  MATT_TRY(check_shape(scale, softcap, b, s, heads, kv_heads, head_dim, dt,
+  TPMLP_PASS(check_shape(scale, softcap, b, s, heads, kv_heads, head_dim, dt,
                        {{nullptr, ld_q, hs_q}, {nullptr, ld_k, hs_k}, {nullptr, ld_v, hs_v}}, {{o, ld_o, hs_o}}, {}));
   if (b * s == 0) return TPMLP_OK;
-  MATT_TRY(check_ptrs({q, k, v, o}, 16, "pointers must be 16-byte aligned"));
-  MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
-  MATT_TRY(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
+  TPMLP_PASS(check_ptrs({q, k, v, o}, 16, "pointers must be 16-byte aligned"));
+  TPMLP_PASS(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
+  TPMLP_PASS(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
   if (!aligned(slopes, 4)) return err(TPMLP_ERR_ALIGN, "slopes not 4-byte aligned");
   MaskedAttention a{{const_cast<void*>(q), ld_q, hs_q}, {const_cast<void*>(k), ld_k, hs_k},
                     {const_cast<void*>(v), ld_v, hs_v}, {o, ld_o, hs_o}, static_cast<const int2*>(key_range), slopes,
@@ -230,8 +199,8 @@ tpmlp_status tpmlp_masked_attention_forward(const void* q, const void* k, const 
                    flat_region(slopes, heads, 4)}))
     return err(TPMLP_ERR_INVALID, "o or lse overlaps another tensor of the call");
   DeviceCtx ctx;
-  MATT_CUDA(get_device_ctx(&ctx), "device context");
-  MATT_CUDA(launch_masked_attention_forward(a, static_cast<cudaStream_t>(stream), ctx), "masked attention");
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
+  TPMLP_PASS_CUDA(launch_masked_attention_forward(a, static_cast<cudaStream_t>(stream), ctx), "masked attention");
   return TPMLP_OK;
 }
 
@@ -248,13 +217,13 @@ tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const
                                              int64_t hs_v, int64_t ld_o, int64_t hs_o, int64_t ld_dq, int64_t hs_dq,
                                              int64_t ld_dk, int64_t hs_dk, int64_t ld_dv, int64_t hs_dv,
                                              tpmlp_dtype dt, void* workspace, size_t ws_bytes, void* stream) {
-  MATT_TRY(check_shape(scale, softcap, b, s, heads, kv_heads, head_dim, dt,
+  TPMLP_PASS(check_shape(scale, softcap, b, s, heads, kv_heads, head_dim, dt,
                        {{nullptr, ld_q, hs_q}, {nullptr, ld_k, hs_k}, {nullptr, ld_v, hs_v}, {nullptr, ld_o, hs_o}},
                        {{dq, ld_dq, hs_dq}}, {{dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}}));
   if (b * s == 0) return TPMLP_OK;
-  MATT_TRY(check_ptrs({q, k, v, o, d_o, dq, dk, dv}, 16, "pointers must be 16-byte aligned"));
-  MATT_TRY(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
-  MATT_TRY(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
+  TPMLP_PASS(check_ptrs({q, k, v, o, d_o, dq, dk, dv}, 16, "pointers must be 16-byte aligned"));
+  TPMLP_PASS(check_ptrs({key_range}, 8, "key_range not 8-byte aligned"));
+  TPMLP_PASS(check_ptrs({lse}, 4, "lse not 4-byte aligned"));
   if (!aligned(slopes, 4)) return err(TPMLP_ERR_ALIGN, "slopes not 4-byte aligned");
   const size_t need = tpmlp_masked_attention_backward_workspace_size(b, s, heads);
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "masked attention backward workspace too small");
@@ -270,8 +239,8 @@ tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const
                    flat_region(slopes, heads, 4), of(a.o, heads), flat_region(lse, b * s * heads, 4), of(g, heads)}))
     return err(TPMLP_ERR_INVALID, "dq, dk, dv or the workspace overlaps another tensor of the call");
   DeviceCtx ctx;
-  MATT_CUDA(get_device_ctx(&ctx), "device context");
-  MATT_CUDA(launch_masked_attention_backward(a, g, gq, gk, gv, workspace, static_cast<cudaStream_t>(stream), ctx),
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
+  TPMLP_PASS_CUDA(launch_masked_attention_backward(a, g, gq, gk, gv, workspace, static_cast<cudaStream_t>(stream), ctx),
             "masked attention backward");
   return TPMLP_OK;
 }
