@@ -73,8 +73,8 @@ __device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// mbar_wait by polling: for the issuing warp, whose reaction the tensor core waits for. (In the working warps it gains
-// nothing over try_wait: causal forward 66.0 and 66.4 us, its step 273 and 275 us.)
+// mbar_wait by polling: for the issuing warp, whose reaction the tensor core waits for. (In the working warps it gained
+// nothing over try_wait: 66.0 and 66.4 us when the causal forward took that long.)
 __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, unsigned int* status, unsigned int where) {
   auto done = [&] { return mbar_done(bar, parity); };
   if (done()) return true;
@@ -438,9 +438,10 @@ __device__ __forceinline__ float largest(const float (&y)[N]) {
 }
 
 // tanh of N capped scores in place, by the cheapest form that all of a warp's allow. Causal forward of b2 s4096, 32 heads
-// of 128 on 8, cap 50 on scores of deviation 1, 30 on 2.6 and 30 on 16: 264, 303 and 398 us then; without degree 2 299, 304
-// and 394 us, and the first way alone takes as long as the last everywhere. Taken together with the exponents, in copies
-// of that loop, the polynomials cost more than they save (248, 368 and 411 us; one loop for all 273, 276 and 483 us).
+// of 128 on 8, cap 50 on scores of deviation 1, 30 on 2.6 and 30 on 16: 251, 298 and 391 us. Against 264, 303 and 398 us in an
+// earlier state: without degree 2 299, 304 and 394 us, and the first way alone as long as the last everywhere; taken together
+// with the exponents, in copies of that loop, the polynomials cost more than they save (248, 368 and 411 us; one loop for
+// all 273, 276 and 483 us).
 template <int N>
 __device__ __forceinline__ void cap_tanh_all(float (&y)[N], const ScoreParams& p) {
   auto all = [&](const auto& poly) {

@@ -15,7 +15,7 @@
 //   warp 9      issues the products
 //   warp 10     query pass: takes the CTA's next tile of queries and finds the key tiles that it sees;
 //               key pass: the queries' lse and D, two tiles ahead
-// Measured with heads of 128 at b2 s2048, 32 heads, causal: query pass 86 us, key pass 105 us, together 192 us = 890
+// Measured with heads of 128 at b2 s2048, 32 heads, causal: query pass 87 us, key pass 105 us, together 187 us = 920
 // TFLOP/s on the five products that a backward cannot do without. A step takes 2070 cycles of the query pass for 1536 of
 // products and 2650 of the key pass for 2048: a chain of products, their hand-over (250 cycles each way) and the work on
 // P and dX, all eight warps in step. A tile costs some 5000 cycles beside its steps (output, first loads). Heads of 64

@@ -21,10 +21,10 @@
 // P V, and the tensor core runs a thread's products in order, so P is never overwritten early and a completed S also
 // says that the P V before it is done. P is handed over in halves of 64 keys, so that its product starts while the second
 // half's exponents are still being taken. Bound by shared memory, of which S = Q K^T, with both operands there, wants all
-// (2840 cycles a step of two tiles for 2048 of products): full masks, b2 s4096, 32 heads of 128, 356 to 366 us = 1500 to
-// 1540 TFLOP/s; causal, b2 s2048, 62 us = 1120 TFLOP/s of the unmasked pairs.
+// (2840 cycles a step of two tiles for 2048 of products): full masks, b2 s4096, 32 heads of 128, 356 to 371 us = 1480 to
+// 1540 TFLOP/s; causal, b2 s2048, 62 us = 1120 TFLOP/s of the unmasked pairs; causal over 131072 keys 1590 TFLOP/s.
 // Heads of up to 64 columns: the products take half of that and the softmax would wait for them, so P has columns of its
-// own and S of the next step is issued as soon as this one has been read (b2 s4096, 32 heads of 64: 243 us; as above
+// own and S of the next step is issued as soon as this one has been read (b2 s4096, 32 heads of 64: 241 us; as above
 // 299 us). Bound by the softmax: 2200 cycles a step, 1024 of them exponents. It is one straight piece of code on purpose:
 // a branch around hidden halves of a tile cost more (277 us) than the exponents that it saved.
 

@@ -10,8 +10,12 @@
 // kHeads heads of one token, all queries or all keys, so that what the position and the gain contribute is
 // loaded once for them, and loads some of them ahead of their arithmetic, which runs on fp32 pairs.
 // Pairs of the half style are brought together by shuffles of the loaded words, before the norm is known.
-// Measured at b2 s2048, 32 + 32 heads of 128 in bf16: forward 29.9 us (4.5 TB/s, 67 % of the copy rate), backward with
-// the gains' sums 47.8 us (64 %). What is left is latency at the ends of the grid's waves and 54 to 58 % of the issue slots.
+// Measured at b2 s2048, 32 + 32 heads of 128, share of the copy rate: bf16 half style forward 29.0 us (0.69), backward with
+// the gains' sums 48.0 us (0.63); interleaved 28.0 (0.72) and 49.4 us (0.61); 40 columns turned in halves, which pair up
+// through shared memory, 46 (0.44) and 66 us (0.46). fp32: 47.8 (0.84) and 69.8 us (0.86), interleaved 48.5 (0.83) and 68.6 us
+// (0.88), 40 columns 63.7 (0.63) and 84.8 us (0.71). In bf16 what is left is latency at the ends of the grid's waves and 54
+// to 58 % of the issue slots.
+// The inverse root is rsqrtf (2 units in the last place at most) and the gains' gradients are summed in fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +34,8 @@ constexpr int kBwdMaxCtas = 1024;
 constexpr int kHeads = 8;
 // Heads of a group loaded before the first is worked on: forward 128 bytes a thread (with three CTAs an SM 29.9 us at the
 // size of a GPT layer, b2 s2048, 32 heads of 128; 64 bytes and four CTAs 30.4, and single tokens 4.6 us for 4.0),
-// backward 64 of each of its two tensors.
+// backward 64 of each of its two tensors. The fp32 forwards do not quite fit three CTAs' registers (36 to 124 bytes a thread
+// go through the L1) and run at 0.83 of the copy rate all the same.
 template <typename T>
 constexpr int kForwardBatch = 16 / sizeof(T);
 template <typename T>
