@@ -485,13 +485,54 @@ tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const
                                              tpmlp_dtype dt, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * The gated feed-forward block: the MLP of the top of this file with a second, gating projection, its shards laid out
+ * and summed in the same way.
+ *   Z = X A,   Y = act(Z_gate) * Z_up,   O = Y B
+ *   X [n][d], A [d][2m], B [m][d], O [n][d], Z [n][2m], Y [n][m], all bf16
+ * Shard i (of t, m / t columns of Y each) holds the 2m/t columns of A and Z from 2i * m/t on: first its gate columns,
+ * then its up columns, and the rows of B from i * m/t on, so that a rank's slice of A is one [gate | up] matrix. t = 1
+ * is one [gate | up] matrix of 2m columns.
+ *   act: a tpmlp_gate_act, evaluated in fp32 on the fp32 accumulators.
+ *   Z_save: output, may be NULL (then Z is not stored and the backward cannot run). Y_save: output, required.
+ * Rounded to bf16: Z_save and Y once each from fp32 (Y from the unrounded Z), O once.
+ * d and m / t are multiples of 8, pointers 16-byte aligned; n, d < 2^31 - 1024, m < 2^30 - 1024. n == 0: nothing is
+ * launched and X, O, Z_save, Y_save may be NULL. Outputs must not overlap each other nor anything that the call reads
+ * (TPMLP_ERR_INVALID), in the backward too.
+ * workspace: tpmlp_gated_forward_workspace_size bytes, 256-byte aligned (may be 0 bytes, then it may be NULL).
+ */
+typedef enum { TPMLP_GATE_GELU_ERF = 0, TPMLP_GATE_GELU_TANH = 1, TPMLP_GATE_SILU = 2 } tpmlp_gate_act;
+size_t tpmlp_gated_forward_workspace_size(int64_t n, int64_t d, int64_t m, tpmlp_dtype dt);
+tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, void* O, void* Z_save, void* Y_save,
+                                 int64_t n, int64_t d, int64_t m, int t, int act, tpmlp_dtype dt, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* What tpmlp_gated_backward does with the weights' gradients: fp32, overwritten; fp32, added to what is there; bf16,
+ * overwritten. */
+typedef enum { TPMLP_WGRAD_F32 = 0, TPMLP_WGRAD_F32_ADD = 1, TPMLP_WGRAD_OPERAND = 2 } tpmlp_wgrad;
+
+/*
+ * Backward of the gated block from G = dl/dO, and Z_save and Y_save as the forward wrote them. With dY = G B^T and
+ * D [n][2m] laid out as Z (in the workspace, bf16, formed in fp32 from the stored Z):
+ *   D_gate = dY * Z_up * act'(Z_gate),   D_up = dY * act(Z_gate),
+ *   dX = D A^T   [n][d] bf16,   dA = X^T D   [d][2m],   dB = Y^T G   [m][d]
+ * wgrad: a tpmlp_wgrad, the form of dA and dB. workspace: tpmlp_gated_backward_workspace_size bytes, 256-byte aligned.
+ * n == 0 gives dA = dB = 0 (TPMLP_WGRAD_F32_ADD: leaves them) and the token buffers may be NULL.
+ */
+size_t tpmlp_gated_backward_workspace_size(int64_t n, int64_t m, tpmlp_dtype dt);
+tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, const void* G, const void* Z_save,
+                                  const void* Y_save, void* dX, void* dA, void* dB, int64_t n, int64_t d, int64_t m,
+                                  int t, int act, int wgrad, tpmlp_dtype dt, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/*
  * Kernel choice for the plain bf16 GEMMs of every later call in this process, for comparing
  * kernels and testing each one; a user of the library never needs it, and nothing else
  * (no environment variable) changes the choice. The defaults, 1, 1, 0, are the fast path:
  *   pair_kernel 1: clusters of two SMs, on 256 x 512 or 256 x 256 tiles per GEMM by a model of
  *                  the launch's waves; 2: clusters of two SMs on 256 x 256 tiles only; 3: on
  *                  256 x 512 tiles only (a last round that would keep at most half the SM pairs
- *                  busy runs as 256 x 256 half-tiles, one per pair); 0: 128 x 256 tiles on one SM.
+ *                  busy runs as 256 x 256 half-tiles, one per pair); 0: 128 x 256 tiles on one SM (the gated
+ *                  block's products with an elementwise part then run as with 2).
  *   pair_pacing 1: pairs wait at intervals of 16 k-blocks for the pairs of the same round of
  *                  tiles, which keeps shared operand panels in L2; 0: no pacing.
  *   pair_group  0: the default tile band (16 pair-rows walked along N, for 256 x 256 and

@@ -19,6 +19,8 @@ from . import _build
 GELU = {"erf": 0, "tanh": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 RS_MODE = {"fused": 0, "splitk": 1}
+GATE_ACT = {"gelu_erf": 0, "gelu_tanh": 1, "silu": 2}
+WGRAD = {"f32": 0, "f32_add": 1, "operand": 2}
 ROPE_STYLE = {"half": 0, "interleaved": 1}
 STATUS = {0: "TPMLP_OK", 1: "TPMLP_ERR_INVALID", 2: "TPMLP_ERR_SHAPE", 3: "TPMLP_ERR_DTYPE", 4: "TPMLP_ERR_ALIGN",
           5: "TPMLP_ERR_CUDA", 6: "TPMLP_ERR_TIMEOUT", 7: "TPMLP_ERR_WORKSPACE"}
@@ -68,6 +70,10 @@ SIGNATURES = {
     "tpmlp_masked_attention_backward_workspace_size": (_SZ, [_I64, _I64, _I]),
     "tpmlp_masked_attention_backward": (_I, [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I]
                                         + [_I64] * 14 + [_I, _P, _SZ, _P]),
+    "tpmlp_gated_forward_workspace_size": (_SZ, [_I64, _I64, _I64, _I]),
+    "tpmlp_gated_forward": (_I, [_P] * 6 + [_I64, _I64, _I64, _I, _I, _I, _P, _SZ, _P]),
+    "tpmlp_gated_backward_workspace_size": (_SZ, [_I64, _I64, _I]),
+    "tpmlp_gated_backward": (_I, [_P] * 9 + [_I64, _I64, _I64, _I, _I, _I, _I, _P, _SZ, _P]),
     "tpmlp_last_error": (ctypes.c_char_p, []),
     "tpmlp_device_status": (_I, [_P, _I]),
     "tpmlp_check_wait_timeout": (_I, [_U64, _P]),
@@ -692,3 +698,73 @@ def masked_attention_backward(q, k, v, key_range, o, lse, do, scale: float | Non
             dk.data_ptr(), dv.data_ptr(), b, s, heads, kshape[2], hd, *strides, *so, *sq, *sk, *sv, _dt(q), ws.data_ptr(),
             ws_bytes, st))
     return dq, dk, dv
+
+
+# ----------------------------------------------------------------------- gated feed-forward block
+
+def _gated_args(X, A, B):
+    n, d = X.shape
+    m = B.shape[0]
+    dtype = X.dtype
+    _dense(X, (n, d), dtype, "X")
+    _dense(A, (d, 2 * m), dtype, "A")
+    _dense(B, (m, d), dtype, "B")
+    return n, d, m, _dt(X)
+
+
+def _scratch(nbytes: int, device):
+    """A workspace of nbytes and its address; none for 0 bytes."""
+    if nbytes == 0:
+        return None, None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr()
+
+
+def gated_forward(X, A, B, t: int = 1, act: str = "silu", save: bool = True, stream=None):
+    """X [n, d], A [d, 2m] (shard by shard [gate | up]), B [m, d], bf16. Allocates O, Y and, with `save`, Z and runs
+    tpmlp_gated_forward. Returns (O, Z or None, Y); gated_backward needs Z and Y."""
+    n, d, m, dt = _gated_args(X, A, B)
+    lib = load_library()
+    here, st = _where(_device(X, A, B), stream)
+    with here:
+        device = X.device
+        O = torch.empty((n, d), dtype=X.dtype, device=device)
+        Z = torch.empty((n, 2 * m), dtype=X.dtype, device=device) if save else None
+        Y = torch.empty((n, m), dtype=X.dtype, device=device)
+        ws_bytes = lib.tpmlp_gated_forward_workspace_size(n, d, m, dt)
+        ws, ws_ptr = _scratch(ws_bytes, device)
+        _check(lib.tpmlp_gated_forward(X.data_ptr(), A.data_ptr(), B.data_ptr(), O.data_ptr(), _ptr(Z), Y.data_ptr(), n, d,
+                                       m, t, GATE_ACT[act], dt, ws_ptr, ws_bytes, st))
+    return O, Z, Y
+
+
+def gated_backward(X, A, B, G, Z, Y, t: int = 1, act: str = "silu", wgrad: str = "f32", dA=None, dB=None, stream=None):
+    """Runs tpmlp_gated_backward from G = dl/dO and the forward's Z and Y; allocates dX, the workspace and, unless given,
+    dA and dB. wgrad: "f32" (overwritten), "f32_add" (added to the given dA and dB) or "operand" (bf16). Returns
+    (dX, dA, dB)."""
+    n, d, m, dt = _gated_args(X, A, B)
+    dtype = X.dtype
+    _dense(G, (n, d), dtype, "G")
+    _dense(Z, (n, 2 * m), dtype, "Z")
+    _dense(Y, (n, m), dtype, "Y")
+    act_kind, mode = GATE_ACT[act], WGRAD[wgrad]
+    wtype = dtype if wgrad == "operand" else torch.float32
+    if wgrad == "f32_add" and (dA is None or dB is None):
+        raise ValueError("f32_add needs dA and dB")
+    if dA is not None:
+        _dense(dA, (d, 2 * m), wtype, "dA")
+    if dB is not None:
+        _dense(dB, (m, d), wtype, "dB")
+    lib = load_library()
+    here, st = _where(_device(X, A, B, G, Z, Y, dA, dB), stream)
+    with here:
+        device = X.device
+        dX = torch.empty((n, d), dtype=dtype, device=device)
+        dA = torch.empty((d, 2 * m), dtype=wtype, device=device) if dA is None else dA
+        dB = torch.empty((m, d), dtype=wtype, device=device) if dB is None else dB
+        ws_bytes = lib.tpmlp_gated_backward_workspace_size(n, m, dt)
+        ws, ws_ptr = _scratch(ws_bytes, device)
+        _check(lib.tpmlp_gated_backward(X.data_ptr(), A.data_ptr(), B.data_ptr(), G.data_ptr(), Z.data_ptr(), Y.data_ptr(),
+                                        dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), n, d, m, t, act_kind, mode, dt,
+                                        ws_ptr, ws_bytes, st))
+    return dX, dA, dB

@@ -381,12 +381,6 @@ inline ScoreParams score_params(float scale, float softcap) {
   return p;
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // tanh(x) of the cap's argument x = q.k scale / cap in two ways (tanh.approx's 2^-11 would not do: the cap multiplies the
 // error into the exponent). Any x: 1 - 2 / (1 + e^(2x)), two special-function operations, off by up to 2.7e-7 = 4.5 * 2^-24
 // in absolute terms, so taken only where some score of the warp's tile is not small. Small x: x times a polynomial of x^2

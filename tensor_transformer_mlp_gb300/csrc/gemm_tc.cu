@@ -1059,6 +1059,215 @@ __device__ __forceinline__ void pace_wait(const unsigned int* ctr, unsigned int 
   }
 }
 
+// ---------------------------------------------------------------------- gated block's epilogues
+// Columns of Z, D and A are addressed through 3-D maps {column in the part, part, row}: part 2 i is shard i's gate
+// columns, 2 i + 1 its up columns, so copies are clipped where a shard ends inside a block. Tiles divide runs of
+// ep.unit columns: all of them where shards end on the epilogue's column blocks, else shard by shard (the columns a
+// block has past its shard are computed and dropped).
+template <int EPI>
+constexpr bool kGated = EPI == kEpiGate || EPI == kEpiGateGrad;
+
+// N-blocks of width w, and the first column of block nb.
+__host__ __device__ __forceinline__ int gated_blocks(int N, int unit, int w) { return N / unit * ((unit + w - 1) / w); }
+__device__ __forceinline__ int gated_column(int nb, int unit, int w) {
+  const int per = (unit + w - 1) / w;
+  return nb / per * unit + nb % per * w;
+}
+// Whether column y, in a block that starts at column y_block, still belongs to the block's run.
+__device__ __forceinline__ bool gated_in_run(int y, int y_block, int unit) { return y / unit == y_block / unit; }
+
+// The column of A that column y of Y takes its gate (part 0) or up (part 1) from.
+__device__ __forceinline__ int gate_column(const EpiParams& ep, int y, uint32_t part) {
+  const int shard = y / ep.shard;
+  return y + (shard + static_cast<int>(part)) * ep.shard;  // = (2 shard + part) * ep.shard + (y - shard * ep.shard)
+}
+
+// act(g) * u of two columns, for the forms that are kept out of line (see gelu_other8).
+__device__ __noinline__ uint32_t gate_other2(float g0, float g1, float u0, float u1, int kind) {
+  return pack_bf16x2(gelu_f<false>(g0, kind) * u0, gelu_f<false>(g1, kind) * u1);
+}
+__device__ __forceinline__ float silu_fast(float g) { return g * sigmoid_fast(g); }
+
+// Y = act(g) u for 32 columns of the lane's row, as 16 packed words.
+__device__ __forceinline__ void gate_32(const uint32_t (&g)[32], const uint32_t (&u)[32], uint4* y, int act) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(y);
+  if (act == kGateSilu) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i] = pack_bf16x2(silu_fast(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
+                         silu_fast(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+  } else if (act == kGeluTanh) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 y2 = f2_split(f2_mul(gelu_tanh2(f2_make(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]))),
+                                        f2_make(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))));
+      w[i] = pack_bf16x2(y2.x, y2.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i] = gate_other2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i]),
+                         __uint_as_float(u[2 * i + 1]), act);
+  }
+}
+
+// 64 columns x 32 rows through the warp's buffer to a 3-D map (as store_tma).
+__device__ __forceinline__ void store_tma_3d(uint8_t* buf, const uint4 (&seg)[8], int lane, const CUtensorMap* map,
+                                             int col, int part, int row0) {
+  buf_acquire(lane);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = seg[j];
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(map, buf, col, part, row0);
+    bulk_commit_group();
+  }
+}
+
+// 64 accumulator columns rounded to bf16 (Z).
+__device__ __forceinline__ void tmem_to_bf16_64(uint32_t t_addr, uint4 (&seg)[8]) {
+  uint32_t v[64];
+  tmem_ld_32x32b_x32(t_addr, *reinterpret_cast<uint32_t(*)[32]>(v));
+  tmem_ld_32x32b_x32(t_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+  tmem_ld_wait();
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = pack_bf16x2(__uint_as_float(v[g * 8 + 2 * i]), __uint_as_float(v[g * 8 + 2 * i + 1]));
+    seg[g] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// One epilogue warp's 64 columns of Y of a 256-column accumulator whose first half is the gate's 128 columns and whose
+// second half is the up projection's: t_gate is the tensor-memory address of its gate columns, y its first column.
+// Z_gate leaves while Y is computed; all three go through the warp's buffer.
+__device__ __forceinline__ void gate_epilogue(const EpiParams& ep, uint8_t* buf, int lane, int row0, int y, uint32_t t_gate,
+                                              const CUtensorMap* tm_z, const CUtensorMap* tm_y) {
+  const int shard = y / ep.shard, j = y - shard * ep.shard;
+  uint4 seg[8];
+  if (ep.out) {
+    tmem_to_bf16_64(t_gate, seg);
+    store_tma_3d(buf, seg, lane, tm_z, j, 2 * shard, row0);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t g[32], u[32];
+    tmem_ld_32x32b_x32(t_gate + c * 32, g);
+    tmem_ld_32x32b_x32(t_gate + BN_HALF + c * 32, u);
+    tmem_ld_wait();
+    gate_32(g, u, seg + 4 * c, ep.gelu);
+  }
+  store_tma_3d(buf, seg, lane, tm_y, j, shard, row0);
+  if (ep.out) {
+    tmem_to_bf16_64(t_gate + BN_HALF, seg);
+    store_tma_3d(buf, seg, lane, tm_z, j, 2 * shard + 1, row0);
+  }
+}
+
+// The lane's row of Z, 32 columns of the gate and of the up part from column y on, in a block of tiles that starts at
+// y_block (zeros past M, past the shard and past the block's run).
+__device__ __forceinline__ void load_gate_z(uint4 (&zg)[4], uint4 (&zu)[4], const EpiParams& ep, int64_t row, int M, int y,
+                                            int y_block) {
+  const int shard = y / ep.shard, j = y - shard * ep.shard;
+  const bool in = row < M && gated_in_run(y, y_block, ep.unit);
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(ep.aux) + row * ep.ldo +
+                             2 * static_cast<int64_t>(shard) * ep.shard + j;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    zg[i] = zu[i] = make_uint4(0, 0, 0, 0);
+    if (in && j + 8 * i < ep.shard) {
+      zg[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+      zu[i] = *reinterpret_cast<const uint4*>(src + ep.shard + 8 * i);
+    }
+  }
+}
+
+// D of two columns for the forms kept out of line: {gate word, up word}.
+__device__ __noinline__ uint2 gate_grad_other2(float a0, float a1, uint32_t zg, uint32_t zu, int kind) {
+  const float2 g = unpack_bf16x2(zg), u = unpack_bf16x2(zu);
+  return make_uint2(pack_bf16x2(a0 * u.x * gelu_grad_f<false>(g.x, kind), a1 * u.y * gelu_grad_f<false>(g.y, kind)),
+                    pack_bf16x2(a0 * gelu_f<false>(g.x, kind), a1 * gelu_f<false>(g.y, kind)));
+}
+
+// D for 32 columns of the lane's row: zg, zu hold Z and receive D; v is dY.
+__device__ __forceinline__ void gate_grad_32(uint4 (&zg)[4], uint4 (&zu)[4], const uint32_t (&v)[32], int act) {
+  uint32_t *gw = reinterpret_cast<uint32_t*>(zg), *uw = reinterpret_cast<uint32_t*>(zu);
+  auto pair = [](uint32_t w) { return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); };
+  if (act == kGateSilu) {
+    // s = g sigma, act' = sigma + s (1 - sigma)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const F2 a = f2_make(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), g = pair(gw[i]);
+      const float2 gs = f2_split(g);
+      const F2 sig = f2_make(sigmoid_fast(gs.x), sigmoid_fast(gs.y)), s = f2_mul(g, sig);
+      const F2 slope = f2_fma(s, f2_sub(f2_make(1.f, 1.f), sig), sig);
+      const float2 dg = f2_split(f2_mul(f2_mul(a, pair(uw[i])), slope)), du = f2_split(f2_mul(a, s));
+      gw[i] = pack_bf16x2(dg.x, dg.y);
+      uw[i] = pack_bf16x2(du.x, du.y);
+    }
+  } else if (act == kGeluTanh) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const F2 a = f2_make(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), g = pair(gw[i]);
+      const float2 dg = f2_split(f2_mul(f2_mul(a, pair(uw[i])), gelu_grad_tanh2(g)));
+      const float2 du = f2_split(f2_mul(a, gelu_tanh2(g)));
+      gw[i] = pack_bf16x2(dg.x, dg.y);
+      uw[i] = pack_bf16x2(du.x, du.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint2 d = gate_grad_other2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), gw[i], uw[i], act);
+      gw[i] = d.x;
+      uw[i] = d.y;
+    }
+  }
+}
+
+// One epilogue warp's `passes` blocks of 32 columns of dY from column y on (t_addr: their tensor-memory address): D of
+// both parts. zg, zu hold the first block's Z and receive that of the block at y_next (< 0: none), so that a block's Z is
+// on its way while the one before is worked on. The two 2 KB blocks of a pass leave through the warp's buffer in the
+// 64-byte-swizzled layout of the map.
+__device__ __forceinline__ void gate_grad_epilogue(const EpiParams& ep, uint8_t* buf, int lane, int64_t row, int M, int y,
+                                                   int y_block, uint32_t t_addr, int y_next, uint4 (&zg)[4], uint4 (&zu)[4],
+                                                   const CUtensorMap* tm_d) {
+#pragma unroll 1
+  for (int p = 0; p < kEpiChunks; ++p) {
+    const int col = y + p * 32;
+    uint4 dg[4], du[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dg[i] = zg[i];
+      du[i] = zu[i];
+    }
+    const int next = p + 1 < kEpiChunks ? col + 32 : y_next;
+    if (next >= 0) load_gate_z(zg, zu, ep, row, M, next, y_block);
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(t_addr + static_cast<uint32_t>(p * 32), v);
+    tmem_ld_wait();
+    gate_grad_32(dg, du, v, ep.gelu);
+    if (!gated_in_run(col, y_block, ep.unit)) continue;  // uniform across the warp
+    buf_acquire(lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4);
+      *reinterpret_cast<uint4*>(buf + at) = dg[i];
+      *reinterpret_cast<uint4*>(buf + 2048 + at) = du[i];
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      const int shard = col / ep.shard, j = col - shard * ep.shard, row0 = static_cast<int>(row);
+      tma_store_3d(tm_d, buf, j, 2 * shard, row0);
+      tma_store_3d(tm_d, buf + 2048, j, 2 * shard + 1, row0);
+      bulk_commit_group();
+    }
+  }
+}
+
 template <bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -1082,7 +1291,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int num_pairs = static_cast<int>(gridDim.x >> 1);
   const int num_mb = (M + 2 * BM - 1) / (2 * BM);
-  const int num_nb = (N + BN - 1) / BN;
+  // kEpiGate: 128 columns of Y a tile, from 128 gate and 128 up columns of A
+  constexpr int kTileN = EPI == kEpiGate ? BN_HALF : BN;
+  const int num_nb = kGated<EPI> ? gated_blocks(N, ep.unit, kTileN) : (N + BN - 1) / BN;
   const int num_tiles = num_mb * num_nb;
   // group > 0: bands of `group` pair-rows, each walked N-block by N-block (M fastest);
   // group < 0: bands of -group N-blocks, walked pair-row by pair-row (N fastest).
@@ -1150,7 +1361,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int mb, nb;
         coords(tile, mb, nb);
         const int a_row = mb * 2 * BM + static_cast<int>(rank) * BM;
-        const int b_col = nb * BN + static_cast<int>(rank) * BN_HALF;
+        const int y0 = kGated<EPI> ? gated_column(nb, ep.unit, kTileN) : nb * BN;
+        const int b_col = y0 + static_cast<int>(rank) * BN_HALF;
         const unsigned int active = static_cast<unsigned int>(min(num_pairs, num_tiles - round * num_pairs));
         for (int kb = 0; kb < num_kb; ++kb) {
           if (pacer && kb % kPaceKb == 0) {
@@ -1182,7 +1394,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           } else {
 #pragma unroll
             for (int j = 0; j < BN_HALF / 64; ++j)
-              tma_load_2d_pair(sb + j * MN_BOX_BYTES, &tmap_b, full0, b_col + j * 64, kbl * BK);
+              tma_load_2d_pair(sb + j * MN_BOX_BYTES, &tmap_b, full0,
+                               EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_col + j * 64, kbl * BK);
           }
           ++kiter;
         }
@@ -1251,9 +1464,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       coords(tile, mb, nb);
       const int64_t row = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32 + lane;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
-      epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, epi_stage + (warp - 2) * EPI_STAGE_BYTES, lane, row, M,
-                                                          N, nb * BN, c_begin, t_row, 0, 1.f, row, nb, num_nb,
-                                                          tm_out, tm_out2);
+      uint8_t* buf = epi_stage + (warp - 2) * EPI_STAGE_BYTES;
+      if constexpr (EPI == kEpiGate) {
+        const int y0 = gated_column(nb, ep.unit, kTileN), y = y0 + c_begin * 16;  // 64 columns a warp
+        if (gated_in_run(y, y0, ep.unit))
+          gate_epilogue(ep, buf, lane, static_cast<int>(row) - lane, y, t_row + c_begin * 16, tm_out, tm_out2);
+      } else if constexpr (EPI == kEpiGateGrad) {
+        const int y0 = gated_column(nb, ep.unit, kTileN), y = y0 + c_begin * 32;
+        uint4 zg[4], zu[4];
+        load_gate_z(zg, zu, ep, row, M, y, y0);
+        gate_grad_epilogue(ep, buf, lane, row, M, y, y0, t_row + c_begin * 32, -1, zg, zu, tm_out);
+      } else {
+        epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, buf, lane, row, M, N, nb * BN, c_begin, t_row, 0, 1.f,
+                                                            row, nb, num_nb, tm_out, tm_out2);
+      }
       tc_fence_before();
       mbar_arrive_cluster(map_to_cta(&tempty_bar[acc], 0));
     }
@@ -1357,7 +1581,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int num_pairs = static_cast<int>(gridDim.x >> 1);
   const int num_mb = (M + 2 * BM - 1) / (2 * BM);
-  const int num_nb = (N + WIDE_BN - 1) / WIDE_BN;
+  // kEpiGate: a half is 128 columns of Y, from 128 gate and 128 up columns of A
+  constexpr int kHalfN = EPI == kEpiGate ? BN_HALF : BN;
+  const int num_nb = kGated<EPI> ? gated_blocks(N, ep.unit, 2 * kHalfN) : (N + WIDE_BN - 1) / WIDE_BN;
   const int num_tiles = num_mb * num_nb;
   // group > 0: bands of `group` pair-rows walked along N; group < 0: bands of -group N-blocks
   // walked along M (as in the 256 x 256 pair kernel).
@@ -1449,6 +1675,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               for (int j = (half == 1 ? 4 : 0); j < (half == 0 ? 4 : 8); ++j)
                 tma_prefetch_l2_2d(&tmap_c2, nb * WIDE_BN + j * 64, a_row);
           }
+          if constexpr (EPI == kEpiGateGrad) {
+            if (kb == max(0, num_kb - kAuxPrefetchKb)) {
+              const int y0 = gated_column(nb, ep.unit, 2 * kHalfN);
+              for (int j = (half == 1 ? 4 : 0); j < (half == 0 ? 4 : 8); ++j) {
+                const int y = y0 + j * 64, shard = y / ep.shard;
+                if (!gated_in_run(y, y0, ep.unit)) break;
+                tma_prefetch_l2_3d(&tmap_c2, y - shard * ep.shard, 2 * shard, a_row);
+                tma_prefetch_l2_3d(&tmap_c2, y - shard * ep.shard, 2 * shard + 1, a_row);
+              }
+            }
+          }
           if (pacer && kb % kPaceKb == 0) {
             pace_wait(pace, pace_target, kPaceWaitNs);
             atomicAdd(pace, 1u);
@@ -1474,14 +1711,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // this CTA's 128 columns of each 256-column half
             if (half >= 0 && h != half) continue;
-            const int b_col = nb * WIDE_BN + h * BN + static_cast<int>(rank) * BN_HALF;
+            const int y0 = kGated<EPI> ? gated_column(nb, ep.unit, 2 * kHalfN) + h * kHalfN : nb * WIDE_BN + h * BN;
+            const int b_col = y0 + static_cast<int>(rank) * BN_HALF;
             uint8_t* sbh = sb + h * WIDE_CHUNK_BYTES;
             if constexpr (!B_MN) {
               tma_load_2d_pair(sbh, &tmap_b, full0, kbl * BK, b_col);
             } else {
 #pragma unroll
               for (int j = 0; j < BN_HALF / 64; ++j)
-                tma_load_2d_pair(sbh + j * MN_BOX_BYTES, &tmap_b, full0, b_col + j * 64, kbl * BK);
+                tma_load_2d_pair(sbh + j * MN_BOX_BYTES, &tmap_b, full0,
+                                 EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_col + j * 64, kbl * BK);
             }
           }
           ++kiter;
@@ -1658,6 +1897,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_arrive_cluster(map_to_cta(&tempty_bar[h], 0));
         }
       }
+    } else if constexpr (EPI == kEpiGateGrad) {
+      uint8_t* buf = epi_stage + (warp - 2) * EPI_STAGE_BYTES;
+      int tile, half;
+      for (; ok && work(it, tile, half); ++it) {
+        int mb, nb;
+        coords(tile, mb, nb);
+        const int64_t row = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32 + lane;
+        const int y0 = gated_column(nb, ep.unit, 2 * kHalfN);
+        const int h_first = half < 0 ? 0 : half, h_last = half < 0 ? 1 : half;
+        uint4 zg[4], zu[4];
+        load_gate_z(zg, zu, ep, row, M, y0 + h_first * BN + c_begin * 32, y0);
+#pragma unroll 1
+        for (int h = h_first; h <= h_last; ++h) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[h], static_cast<uint32_t>(it & 1), status, 36));
+          if (!ok) break;
+          tc_fence_after();
+          const int y = y0 + h * BN + c_begin * 32;
+          gate_grad_epilogue(ep, buf, lane, row, M, y, y0,
+                             tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * BN + c_begin * 32),
+                             h < h_last ? y + BN : -1, zg, zu, tm_out);
+          tc_fence_before();
+          mbar_arrive_cluster(map_to_cta(&tempty_bar[h], 0));
+        }
+      }
     } else {
       int tile, half;
       for (; ok && work(it, tile, half); ++it) {
@@ -1670,9 +1933,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * BN);
-          epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, epi_stage + (warp - 2) * EPI_STAGE_BYTES, lane, row,
-                                                              M, N, nb * WIDE_BN + h * BN, c_begin, t_row, 0, 1.f, row,
-                                                              2 * nb + h, 2 * num_nb, tm_out, tm_out2);
+          uint8_t* buf = epi_stage + (warp - 2) * EPI_STAGE_BYTES;
+          if constexpr (EPI == kEpiGate) {
+            const int y0 = gated_column(nb, ep.unit, 2 * kHalfN), y = y0 + h * kHalfN + c_begin * 16;  // 64 columns a warp
+            if (gated_in_run(y, y0, ep.unit))
+              gate_epilogue(ep, buf, lane, static_cast<int>(row) - lane, y, t_row + c_begin * 16, tm_out, tm_out2);
+          } else {
+            epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, buf, lane, row, M, N, nb * WIDE_BN + h * BN, c_begin,
+                                                                t_row, 0, 1.f, row, 2 * nb + h, 2 * num_nb, tm_out,
+                                                                tm_out2);
+          }
           tc_fence_before();
           mbar_arrive_cluster(map_to_cta(&tempty_bar[h], 0));
         }
@@ -1824,6 +2094,13 @@ unsigned int* next_pace_counter() {
   return base[dev] + (next.fetch_add(1) % 64);
 }
 
+// Tile columns of a pair kernel (wide: 256 x 512 accumulators): plain GEMMs, or the gated block's in runs of ep.unit.
+template <int EPI>
+int64_t n_blocks(int N, const EpiParams& ep, bool wide) {
+  const int w = (EPI == kEpiGate ? BN_HALF : BN) * (wide ? 2 : 1);
+  return kGated<EPI> ? gated_blocks(N, ep.unit, w) : (N + w - 1) / w;
+}
+
 // Tile-order band of the pair kernels (see gemm_bf16_pair_kernel): PAIR_GROUP_M pair-rows for
 // 256 x 256 tiles and WIDE_GROUP_M for 256 x 512 tiles, unless tpmlp_set_gemm_variant chose
 // another band.
@@ -1838,7 +2115,8 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutM
   auto kernel = gemm_bf16_pair_kernel<A_MN, B_MN, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((M + 2 * BM - 1) / (2 * BM)) * ((N + BN - 1) / BN);
+  const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * n_blocks<EPI>(N, ep, false);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = PAIR_SMEM_BYTES;
@@ -1884,7 +2162,8 @@ cudaError_t launch_wide(const CUtensorMap& ta, const CUtensorMap& tb, const OutM
   auto kernel = gemm_bf16_wide_kernel<A_MN, B_MN, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((M + 2 * BM - 1) / (2 * BM)) * ((N + WIDE_BN - 1) / WIDE_BN);
+  const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * n_blocks<EPI>(N, ep, true);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = WIDE_SMEM_BYTES;
@@ -1940,12 +2219,15 @@ cudaError_t dispatch_pair(bool a_mn, bool b_mn, EpiKind epi, const CUtensorMap& 
     if (epi == kEpiStore) TPMLP_PAIR_LAUNCH(false, true, kEpiStore);
     if (epi == kEpiStoreF32) TPMLP_PAIR_LAUNCH(false, true, kEpiStoreF32);
     if (epi == kEpiDropoutResidual) TPMLP_PAIR_LAUNCH(false, true, kEpiDropoutResidual);
+    if (epi == kEpiGate) TPMLP_PAIR_LAUNCH(false, true, kEpiGate);
   } else if (!a_mn && !b_mn) {
     if (epi == kEpiDGelu) TPMLP_PAIR_LAUNCH(false, false, kEpiDGelu);
+    if (epi == kEpiGateGrad) TPMLP_PAIR_LAUNCH(false, false, kEpiGateGrad);
     if (epi == kEpiStore) TPMLP_PAIR_LAUNCH(false, false, kEpiStore);
     if (epi == kEpiStoreRowDot) TPMLP_PAIR_LAUNCH(false, false, kEpiStoreRowDot);
     if (epi == kEpiStoreF32) TPMLP_PAIR_LAUNCH(false, false, kEpiStoreF32);
   } else if (a_mn && b_mn) {
+    if (epi == kEpiStore) TPMLP_PAIR_LAUNCH(true, true, kEpiStore);
     if (epi == kEpiStoreF32) TPMLP_PAIR_LAUNCH(true, true, kEpiStoreF32);
     if (epi == kEpiAccumF32) TPMLP_PAIR_LAUNCH(true, true, kEpiAccumF32);
   }
@@ -1969,9 +2251,9 @@ int pair_kernel_choice() { return g_pair_kernel.load(std::memory_order_relaxed);
 // dropout + residual (per-thread hash, residual loads, remapped stores) u 0.91, e 2000 (the SP
 // block's FC2: 602 us on 256 x 256 tiles, 618 us on split 256 x 512 ones). The fp32
 // read-add-write epilogue is not fitted and keeps the earlier, cautious u 0.91 with e 400.
-bool prefer_wide(int64_t M, int64_t N, int64_t K, EpiKind epi, int pairs) {
+bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiKind epi, int pairs) {
   const int64_t mb = (M + 2 * BM - 1) / (2 * BM);
-  const int64_t t256 = mb * ((N + BN - 1) / BN), t512 = mb * ((N + WIDE_BN - 1) / WIDE_BN);
+  const int64_t t256 = mb * nb256, t512 = mb * nb512;
   const int64_t w256 = (t256 + pairs - 1) / pairs, w512 = (t512 + pairs - 1) / pairs;
   double u = 0.905, e = 180.0;  // bf16 stores
   switch (epi) {
@@ -1990,6 +2272,9 @@ bool prefer_wide(int64_t M, int64_t N, int64_t K, EpiKind epi, int pairs) {
   const double wide = 2 * tail <= pairs ? 2.0 * unit * static_cast<double>(w512 - 1) + 1.0
                                         : 2.0 * unit * static_cast<double>(w512);
   return wide < static_cast<double>(w256);
+}
+bool prefer_wide(int64_t M, int64_t N, int64_t K, EpiKind epi, int pairs) {
+  return prefer_wide_blocks(M, (N + BN - 1) / BN, (N + WIDE_BN - 1) / WIDE_BN, K, epi, pairs);
 }
 
 // 4-D bf16 tensor map over a batched operand: dimension 0 is the contiguous column index; the
@@ -2079,10 +2364,84 @@ cudaError_t gemm_bf16_tc(int64_t M, int64_t N, int64_t K, const Operand& a, cons
     if (epi == kEpiStoreRowDot) return launch<false, false, kEpiStoreRowDot>(ta, tb, m, n, k, ep, stream, ctx);
     if (epi == kEpiStoreF32) return launch<false, false, kEpiStoreF32>(ta, tb, m, n, k, ep, stream, ctx);
   } else if (a.mn_major && b.mn_major) {
+    if (epi == kEpiStore) return launch<true, true, kEpiStore>(ta, tb, m, n, k, ep, stream, ctx);
     if (epi == kEpiStoreF32) return launch<true, true, kEpiStoreF32>(ta, tb, m, n, k, ep, stream, ctx);
     if (epi == kEpiAccumF32) return launch<true, true, kEpiAccumF32>(ta, tb, m, n, k, ep, stream, ctx);
   }
   return cudaErrorNotSupported;
+}
+
+namespace {
+
+// 3-D bf16 map {column in the part, part, row} over rows of `parts` parts of `width` columns each.
+cudaError_t make_part_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t parts, int64_t width, uint32_t box_cols,
+                          uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+  cudaError_t e = get_encode(&encode);
+  if (e != cudaSuccess) return e;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(parts), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(width) * 2, static_cast<cuuint64_t>(parts * width) * 2};
+  cuuint32_t box[3] = {box_cols, 1, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int EPI>
+cudaError_t gated_gemm(int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b, const EpiParams& ep,
+                       const OutMaps& om, cudaStream_t stream, const DeviceCtx& ctx) {
+  const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
+  const int choice = pair_kernel_choice();
+  const bool wide = choice == 3 || (choice == 1 && prefer_wide_blocks(M, n_blocks<EPI>(n, ep, false),
+                                                                      n_blocks<EPI>(n, ep, true), K, static_cast<EpiKind>(EPI), ctx.num_sms / 2));
+  CUtensorMap ta, tb;
+  cudaError_t e = make_tmap(&ta, a, 64, BM);
+  if (e != cudaSuccess) return e;
+  e = make_tmap(&tb, b, 64, b.mn_major ? BK : BN_HALF);
+  if (e != cudaSuccess) return e;
+  const EpiKind epi = static_cast<EpiKind>(EPI);
+  return wide ? dispatch_pair<true>(false, b.mn_major, epi, ta, tb, om, m, n, k, ep, stream, ctx)
+              : dispatch_pair<false>(false, b.mn_major, epi, ta, tb, om, m, n, k, ep, stream, ctx);
+}
+
+EpiParams gated_params(void* out, void* out2, const void* aux, int64_t ldo, int64_t m, int t, int act, int block) {
+  EpiParams ep{};
+  ep.out = out;
+  ep.out2 = out2;
+  ep.aux = aux;
+  ep.ldo = ldo;
+  ep.gelu = act;
+  ep.shard = static_cast<int>(m / t);
+  ep.unit = ep.shard % block == 0 ? static_cast<int>(m) : ep.shard;
+  return ep;
+}
+
+}  // namespace
+
+cudaError_t gated_fc1_tc(const void* x, const void* a, void* z, void* y, int64_t n, int64_t d, int64_t m, int t, int act,
+                         cudaStream_t stream, const DeviceCtx& ctx) {
+  const EpiParams ep = gated_params(z, y, nullptr, m, m, t, act, 64);
+  OutMaps om;
+  cudaError_t e = make_part_map(&om.c2, y, n, t, ep.shard, 64, 32);
+  if (e != cudaSuccess) return e;
+  om.c = om.c2;
+  if (z && (e = make_part_map(&om.c, z, n, 2 * t, ep.shard, 64, 32)) != cudaSuccess) return e;
+  om.flags = 3;
+  return gated_gemm<kEpiGate>(n, m, d, Operand{x, n, d, d, false}, Operand{a, d, 2 * m, 2 * m, true}, ep, om, stream, ctx);
+}
+
+cudaError_t gated_dgrad1_tc(const void* g, const void* b, const void* z, void* dz, int64_t n, int64_t d, int64_t m, int t,
+                            int act, cudaStream_t stream, const DeviceCtx& ctx) {
+  const EpiParams ep = gated_params(dz, nullptr, z, 2 * m, m, t, act, 32);
+  OutMaps om;
+  cudaError_t e = make_part_map(&om.c, dz, n, 2 * t, ep.shard, 32, 32);
+  if (e != cudaSuccess) return e;
+  e = make_part_map(&om.c2, z, n, 2 * t, ep.shard, 64, BM);  // for the producer's L2 prefetch
+  if (e != cudaSuccess) return e;
+  om.flags = 1;
+  return gated_gemm<kEpiGateGrad>(n, m, d, Operand{g, n, d, d, false}, Operand{b, m, d, d, false}, ep, om, stream, ctx);
 }
 
 cudaError_t gemm_bf16_tc_batched(int64_t M, int64_t N, int64_t K, const BatchedOperand& a, const BatchedOperand& b,

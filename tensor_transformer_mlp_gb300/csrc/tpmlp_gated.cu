@@ -1,0 +1,123 @@
+// C ABI of the gated feed-forward block (tpmlp_gated_forward, tpmlp_gated_backward): the checks of the arguments and the
+// sequence of products. The products with an elementwise part are in gemm_tc.cu (kEpiGate, kEpiGateGrad).
+#include <cuda_runtime.h>
+
+#include "abi_checks.h"
+
+namespace tpmlp {
+namespace {
+
+tpmlp_status check_gated_shape(int64_t n, int64_t d, int64_t m, int t, int act, tpmlp_dtype dt) {
+  if (dt != TPMLP_BF16) return err(TPMLP_ERR_DTYPE, "the gated block runs on the bf16 tensor-core path only");
+  if (act != TPMLP_GATE_GELU_ERF && act != TPMLP_GATE_GELU_TANH && act != TPMLP_GATE_SILU)
+    return err(TPMLP_ERR_INVALID, "unknown gate activation");
+  if (n < 0 || d < 1 || m < 1) return err(TPMLP_ERR_SHAPE, "need n >= 0, d >= 1, m >= 1");
+  if (t < 1) return err(TPMLP_ERR_SHAPE, "t must be >= 1");
+  if (m % t != 0) return err(TPMLP_ERR_SHAPE, "m is not divisible by t (shards are an equal split)");
+  if (d % 8 != 0 || (m / t) % 8 != 0) return err(TPMLP_ERR_SHAPE, "d and m / t must be multiples of 8");
+  if (n > INT32_MAX - 1024 || d > INT32_MAX - 1024 || m > (1 << 30) - 1024)
+    return err(TPMLP_ERR_SHAPE, "n and d must be below 2^31 - 1024, m below 2^30 - 1024");
+  return TPMLP_OK;
+}
+
+Region matrix(const void* p, int64_t rows, int64_t cols, int64_t size = 2) {
+  return flat_region(p, rows * cols, size);  // both below 2^31
+}
+
+EpiParams plain(void* out, int64_t ldo) {
+  EpiParams ep{};
+  ep.out = out;
+  ep.ldo = ldo;
+  ep.remap.b = ep.remap.s = ep.remap.s_per_shard = 1;
+  return ep;
+}
+
+size_t dz_bytes(int64_t n, int64_t m) { return n <= 0 || m <= 0 ? 0 : (static_cast<size_t>(n) * m * 4 + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace tpmlp
+
+using namespace tpmlp;
+
+extern "C" {
+
+size_t tpmlp_gated_forward_workspace_size(int64_t n, int64_t d, int64_t m, tpmlp_dtype dt) {
+  (void)n, (void)d, (void)m, (void)dt;
+  return 0;
+}
+
+tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, void* O, void* Z_save, void* Y_save,
+                                 int64_t n, int64_t d, int64_t m, int t, int act, tpmlp_dtype dt, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  TPMLP_PASS(check_gated_shape(n, d, m, t, act, dt));
+  TPMLP_PASS(check_ptrs({A, B}, 16, "pointers must be 16-byte aligned"));
+  if (n == 0) return TPMLP_OK;
+  TPMLP_PASS(check_ptrs({X, O, Y_save}, 16, "pointers must be 16-byte aligned"));
+  if (!aligned(Z_save, 16)) return err(TPMLP_ERR_ALIGN, "pointers must be 16-byte aligned");
+  const size_t need = tpmlp_gated_forward_workspace_size(n, d, m, dt);
+  if (need > 0 && (!workspace || ws_bytes < need)) return err(TPMLP_ERR_WORKSPACE, "gated forward workspace too small");
+  if (need > 0 && !aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
+  if (any_overlap({matrix(O, n, d), matrix(Z_save, n, 2 * m), matrix(Y_save, n, m),
+                   flat_region(need ? workspace : nullptr, static_cast<int64_t>(need), 1)},
+                  {matrix(X, n, d), matrix(A, d, 2 * m), matrix(B, m, d)}))
+    return err(TPMLP_ERR_INVALID, "O, Z_save, Y_save or the workspace overlaps another tensor of the call");
+  DeviceCtx ctx;
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  TPMLP_PASS_CUDA(gated_fc1_tc(X, A, Z_save, Y_save, n, d, m, t, act, st, ctx), "gated FC1 GEMM");
+  TPMLP_PASS_CUDA(gemm_bf16_tc(n, d, m, Operand{Y_save, n, m, m, false}, Operand{B, m, d, d, true}, kEpiStore, plain(O, d),
+                               st, ctx),
+                  "gated FC2 GEMM");
+  return TPMLP_OK;
+}
+
+size_t tpmlp_gated_backward_workspace_size(int64_t n, int64_t m, tpmlp_dtype dt) {
+  (void)dt;
+  return dz_bytes(n, m);
+}
+
+tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, const void* G, const void* Z_save,
+                                  const void* Y_save, void* dX, void* dA, void* dB, int64_t n, int64_t d, int64_t m, int t,
+                                  int act, int wgrad, tpmlp_dtype dt, void* workspace, size_t ws_bytes, void* stream) {
+  TPMLP_PASS(check_gated_shape(n, d, m, t, act, dt));
+  if (wgrad != TPMLP_WGRAD_F32 && wgrad != TPMLP_WGRAD_F32_ADD && wgrad != TPMLP_WGRAD_OPERAND)
+    return err(TPMLP_ERR_INVALID, "unknown form of the weights' gradients");
+  TPMLP_PASS(check_ptrs({A, B, dA, dB}, 16, "pointers must be 16-byte aligned"));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t size = wgrad == TPMLP_WGRAD_OPERAND ? 2 : 4;
+  if (any_overlap({matrix(dA, d, 2 * m, size), matrix(dB, m, d, size)}, {matrix(A, d, 2 * m), matrix(B, m, d)}))
+    return err(TPMLP_ERR_INVALID, "dA or dB overlaps another tensor of the call");
+  if (n == 0) {
+    if (wgrad == TPMLP_WGRAD_F32_ADD) return TPMLP_OK;  // nothing to add
+    TPMLP_PASS_CUDA(cudaMemsetAsync(dA, 0, static_cast<size_t>(size) * d * 2 * m, st), "zero dA");
+    TPMLP_PASS_CUDA(cudaMemsetAsync(dB, 0, static_cast<size_t>(size) * m * d, st), "zero dB");
+    return TPMLP_OK;
+  }
+  TPMLP_PASS(check_ptrs({X, G, Z_save, Y_save, dX}, 16, "pointers must be 16-byte aligned"));
+  const size_t need = dz_bytes(n, m);
+  if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "gated backward workspace too small");
+  if (!aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
+  if (any_overlap({matrix(dX, n, d), matrix(dA, d, 2 * m, size), matrix(dB, m, d, size),
+                   flat_region(workspace, static_cast<int64_t>(need), 1)},
+                  {matrix(X, n, d), matrix(A, d, 2 * m), matrix(B, m, d), matrix(G, n, d), matrix(Z_save, n, 2 * m),
+                   matrix(Y_save, n, m)}))
+    return err(TPMLP_ERR_INVALID, "dX, dA, dB or the workspace overlaps another tensor of the call");
+  DeviceCtx ctx;
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
+  const EpiKind wepi = wgrad == TPMLP_WGRAD_OPERAND ? kEpiStore : wgrad == TPMLP_WGRAD_F32 ? kEpiStoreF32 : kEpiAccumF32;
+  // D = [dY act'(Z_gate) Z_up | dY act(Z_gate)] shard by shard, laid out as Z
+  TPMLP_PASS_CUDA(gated_dgrad1_tc(G, B, Z_save, workspace, n, d, m, t, act, st, ctx), "gated dgrad-1 GEMM");
+  TPMLP_PASS_CUDA(gemm_bf16_tc(m, d, n, Operand{Y_save, n, m, m, true}, Operand{G, n, d, d, true}, wepi, plain(dB, d), st,
+                               ctx),
+                  "gated wgrad-2 GEMM");
+  TPMLP_PASS_CUDA(gemm_bf16_tc(d, 2 * m, n, Operand{X, n, d, d, true}, Operand{workspace, n, 2 * m, 2 * m, true}, wepi,
+                               plain(dA, 2 * m), st, ctx),
+                  "gated wgrad-1 GEMM");
+  // both projections' shares of dX are one sum over the 2 m columns of D
+  TPMLP_PASS_CUDA(gemm_bf16_tc(n, d, 2 * m, Operand{workspace, n, 2 * m, 2 * m, false}, Operand{A, d, 2 * m, 2 * m, false},
+                               kEpiStore, plain(dX, d), st, ctx),
+                  "gated dgrad-2 GEMM");
+  return TPMLP_OK;
+}
+
+}  // extern "C"

@@ -14,6 +14,7 @@ namespace tpmlp {
 
 constexpr int kGeluErf = 0;
 constexpr int kGeluTanh = 1;
+constexpr int kGateSilu = 2;  // gated block only
 
 // Device status word: bit 0 = a bounded in-kernel wait expired; bits 8.. = where.
 constexpr unsigned int kStatusTimeoutBit = 1u;
@@ -36,6 +37,10 @@ enum EpiKind : int {
   // = sum over the head's columns of out[r][c] * aux[r][c], with r = bi * s + si (plain GEMMs;
   // the attention backward's dO GEMM, aux = O: D = rowsum(dO * O) per head and query row)
   kEpiStoreRowDot = 9,
+  // Gated feed-forward block. Z and D are [rows][2 N]: shard i of `shard` columns holds its gate columns at
+  // 2 i shard and its up columns at (2 i + 1) shard.
+  kEpiGate = 10,      // accumulators g (gate) and u (up): out = Z (may be null), out2[r][c] = act(g) * u  (Y)
+  kEpiGateGrad = 11,  // acc = dY; out = D: acc * u * act'(g) in the gate column, acc * act(g) in the up column, aux = Z
 };
 
 // Dropout of the sequence-parallel block applied in a GEMM epilogue: element (r, c) of the
@@ -74,6 +79,9 @@ struct EpiParams {
   float* rowdot;
   int64_t rowdot_s;
   int rowdot_heads;
+  // kEpiGate, kEpiGateGrad: columns of one shard (m / t), and the run of columns that tiles divide: all of them where
+  // shards end on the epilogue's column blocks, else one shard
+  int shard, unit;
 };
 
 // A stored operand matrix [rows][cols] with row stride `ld` elements.
@@ -138,6 +146,13 @@ void set_gemm_variant(int pair_kernel, int pair_pacing, int pair_group);
 // bf16 tensor-core GEMM (tcgen05 + TMA). C = Aop(M x K) * Bop(K x N), fp32 accumulation.
 cudaError_t gemm_bf16_tc(int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b, EpiKind epi,
                          const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx);
+
+// The gated block's two products with an elementwise part, on SM pairs whatever the variant (bf16, m / t a multiple of 8):
+//   Z = X A and Y = act(Z_gate) * Z_up (z may be null);   D from dY = G B^T and Z.
+cudaError_t gated_fc1_tc(const void* x, const void* a, void* z, void* y, int64_t n, int64_t d, int64_t m, int t, int act,
+                         cudaStream_t stream, const DeviceCtx& ctx);
+cudaError_t gated_dgrad1_tc(const void* g, const void* b, const void* z, void* dz, int64_t n, int64_t d, int64_t m, int t,
+                            int act, cudaStream_t stream, const DeviceCtx& ctx);
 
 // Batched bf16 tensor-core GEMM: C_z = alpha * Aop_z(M x K) * Bop_z(K x N) for every batch index;
 // epilogues kEpiStore (bf16) and kEpiStoreF32, written at ep.out + out offsets of z.
