@@ -525,6 +525,41 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, c
                                   void* stream);
 
 /*
+ * The norms before and after a block, with the block's gate and the residual's scale, in one pass: what stands between
+ * the output y of one block and the input u of the next. Per token, with the RMSNorm of tpmlp_rmsnorm,
+ *   p = rmsnorm(y) gamma_post,   r = alpha x + gate * p,   u = rmsnorm(r) gamma_pre
+ *   x (the residual), y, r, u: [b][s][h], dt bf16 or f32; gamma_post, gamma_pre: [h] fp32
+ *   gate: [b][h] fp32, one row for each sequence (a learned vector: b = 1 and s all tokens)
+ * gamma_post NULL: p = y. gate NULL: all ones. gamma_pre and u NULL: u is not formed. r may be x or y, and so may u (in
+ * place), but not both the same; nothing else that the call reads or writes may overlap (TPMLP_ERR_INVALID).
+ * Statistics and arithmetic in fp32; r and u are rounded once each (u from the unrounded r). h is a multiple of 8, at
+ * most 8192; eps > 0, alpha finite; pointers 16-byte aligned. b * s == 0: nothing is launched.
+ */
+tpmlp_status tpmlp_residual_norm(const void* x, const void* y, const float* gamma_post, const float* gate,
+                                 const float* gamma_pre, float alpha, float eps, void* r, void* u, int64_t b, int64_t s,
+                                 int64_t h, tpmlp_dtype dt, void* stream);
+
+/*
+ * Its backward from dr = dl/dr (from the residual's further way) and du = dl/du, with y and r as the forward had them.
+ * With r_hat and y_hat the normalised rows (y_hat = y without gamma_post), rr and ry their factors 1 / sqrt(mean + eps):
+ *   g = dr + rr (du gamma_pre - r_hat mean(du gamma_pre r_hat)),   dx = alpha g
+ *   dy = ry (w g - y_hat mean(w g y_hat)),  w = gate gamma_post    (without gamma_post: dy = gate g)
+ *   dgamma_pre = sum du r_hat,   dgamma_post = sum gate g y_hat   [h] over all tokens
+ *   dgate = sum gamma_post g y_hat                                [b][h] over each sequence's tokens
+ * The gains' and the gate's gradients are fp32, overwritten, summed in a fixed order, and given exactly where the gain or
+ * gate is. du goes with gamma_pre; dr may be NULL beside du. r may be NULL without gamma_pre, y without gamma_post and
+ * gate. dx and dy may each be y, r, dr or du (in place); nothing else may overlap. workspace:
+ * tpmlp_residual_norm_backward_workspace_size bytes (gate: whether there is one), 256-byte aligned. b * s == 0 zeroes the
+ * gains' and the gate's gradients.
+ */
+size_t tpmlp_residual_norm_backward_workspace_size(int64_t b, int64_t s, int64_t h, int gate);
+tpmlp_status tpmlp_residual_norm_backward(const void* y, const void* r, const void* dr, const void* du,
+                                          const float* gamma_post, const float* gate, const float* gamma_pre, float alpha,
+                                          float eps, void* dx, void* dy, float* dgamma_post, float* dgate,
+                                          float* dgamma_pre, int64_t b, int64_t s, int64_t h, tpmlp_dtype dt,
+                                          void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Kernel choice for the plain bf16 GEMMs of every later call in this process, for comparing
  * kernels and testing each one; a user of the library never needs it, and nothing else
  * (no environment variable) changes the choice. The defaults, 1, 1, 0, are the fast path:

@@ -25,6 +25,8 @@ What it computes, and which passage of the source pages it follows:
   sliding windows), with grouped heads, capped scores and distance biases, and its gradients.
 * ``qk_norm_rope``: the per-head RMSNorm of queries and keys with the position rotation, and its
   gradients.
+* ``gated``: the gated feed-forward block and its gradients.
+* ``residual_norm``: the norms before and after a block with its gate and residual scale, and their gradients.
 * ``collectives``: host "ranks" for all-reduce, all-gather and reduce-scatter, to pin
   AllReduce = AllGather(ReduceScatter(x)) ("Megatron-SP 机制", section
   "f/g 算子怎么定义？").
@@ -36,4 +38,4 @@ closed forms, the block-matrix invariants and the ReLU counterexample. The
 worked example on the pages prints shapes only, so its absolute values are
 parity-unpinned; every other function here is pinned.
 """
-from . import attention, collectives, masked_attention, mlp, qk_norm_rope, sp  # noqa: F401
+from . import attention, collectives, gated, masked_attention, mlp, qk_norm_rope, residual_norm, sp  # noqa: F401

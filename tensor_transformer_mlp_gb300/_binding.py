@@ -74,6 +74,9 @@ SIGNATURES = {
     "tpmlp_gated_forward": (_I, [_P] * 6 + [_I64, _I64, _I64, _I, _I, _I, _P, _SZ, _P]),
     "tpmlp_gated_backward_workspace_size": (_SZ, [_I64, _I64, _I]),
     "tpmlp_gated_backward": (_I, [_P] * 9 + [_I64, _I64, _I64, _I, _I, _I, _I, _P, _SZ, _P]),
+    "tpmlp_residual_norm": (_I, [_P] * 5 + [_F, _F, _P, _P, _I64, _I64, _I64, _I, _P]),
+    "tpmlp_residual_norm_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I]),
+    "tpmlp_residual_norm_backward": (_I, [_P] * 7 + [_F, _F] + [_P] * 5 + [_I64, _I64, _I64, _I, _P, _SZ, _P]),
     "tpmlp_last_error": (ctypes.c_char_p, []),
     "tpmlp_device_status": (_I, [_P, _I]),
     "tpmlp_check_wait_timeout": (_I, [_U64, _P]),
@@ -768,3 +771,74 @@ def gated_backward(X, A, B, G, Z, Y, t: int = 1, act: str = "silu", wgrad: str =
                                         dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), n, d, m, t, act_kind, mode, dt,
                                         ws_ptr, ws_bytes, st))
     return dX, dA, dB
+
+
+# ----------------------------------------------------------------------- norms around a block
+
+def _residual_args(y, gamma_post, gate, gamma_pre):
+    """(b, s, h) that the gate's rows divide the tokens of y [..., h] into."""
+    shape = y.shape
+    h = shape[-1]
+    for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
+        if g is not None:
+            _dense(g, (h,), torch.float32, name)
+    tokens = y.numel() // h if h else 0
+    if gate is None or gate.dim() == 1:
+        if gate is not None:
+            _dense(gate, (h,), torch.float32, "gate")
+        return 1, tokens, h
+    if len(shape) < 3:
+        raise ValueError("a gate of [b, h] needs tensors of [b, ..., h]")
+    _dense(gate, (shape[0], h), torch.float32, "gate")
+    return shape[0], tokens // shape[0] if shape[0] else 0, h
+
+
+def residual_norm(x, y, gamma_post=None, gate=None, gamma_pre=None, alpha: float = 1.0, eps: float = 1e-5, r=None, u=None,
+                  stream=None):
+    """x (the residual) and y (a block's output) [..., h]; gains fp32 [h]; gate fp32 [h], or [b, h] for tensors [b, ..., h].
+    Allocates r and u unless given (x or y for in place) and runs tpmlp_residual_norm. Returns (r, u), u None without
+    gamma_pre."""
+    shape, dtype = y.shape, y.dtype
+    _dense(y, shape, dtype, "y")
+    _dense(x, shape, dtype, "x")
+    if u is not None and gamma_pre is None:
+        raise ValueError("u needs gamma_pre")
+    for name, out in (("r", r), ("u", u)):
+        if out is not None:
+            _dense(out, shape, dtype, name)
+    b, s, h = _residual_args(y, gamma_post, gate, gamma_pre)
+    dt = _dt(y)
+    lib = load_library()
+    here, st = _where(_device(y, x, gamma_post, gate, gamma_pre, r, u), stream)
+    with here:
+        r = torch.empty_like(y) if r is None else r
+        u = torch.empty_like(y) if u is None and gamma_pre is not None else u
+        _check(lib.tpmlp_residual_norm(x.data_ptr(), y.data_ptr(), _ptr(gamma_post), _ptr(gate), _ptr(gamma_pre), alpha, eps,
+                                       r.data_ptr(), _ptr(u), b, s, h, dt, st))
+    return r, u
+
+
+def residual_norm_backward(y, r, dr, du, gamma_post=None, gate=None, gamma_pre=None, alpha: float = 1.0, eps: float = 1e-5,
+                           dx=None, dy=None, stream=None):
+    """Runs tpmlp_residual_norm_backward from dr = dl/dr and du = dl/du (either may be None: du without gamma_pre, dr beside
+    du); r may be None without gamma_pre. Allocates the workspace, the gains' and the gate's gradients and, unless given,
+    dx and dy. Returns (dx, dy, dgamma_post, dgate, dgamma_pre), None for a gain or gate that is not there."""
+    like = y if y is not None else dr if dr is not None else du
+    shape, dtype = like.shape, like.dtype
+    for name, t in (("y", y), ("r", r), ("dr", dr), ("du", du), ("dx", dx), ("dy", dy)):
+        if t is not None:
+            _dense(t, shape, dtype, name)
+    b, s, h = _residual_args(like, gamma_post, gate, gamma_pre)
+    dt = _dt(like)
+    lib = load_library()
+    here, st = _where(_device(like, r, dr, du, gamma_post, gate, gamma_pre, dx, dy), stream)
+    with here:
+        dx = torch.empty_like(like) if dx is None else dx
+        dy = torch.empty_like(like) if dy is None else dy
+        dpost, dgate, dpre = (None if g is None else torch.empty_like(g) for g in (gamma_post, gate, gamma_pre))
+        ws_bytes = lib.tpmlp_residual_norm_backward_workspace_size(b, s, h, gate is not None)
+        ws, ws_ptr = _scratch(ws_bytes, like.device)
+        _check(lib.tpmlp_residual_norm_backward(_ptr(y), _ptr(r), _ptr(dr), _ptr(du), _ptr(gamma_post), _ptr(gate),
+                                                _ptr(gamma_pre), alpha, eps, dx.data_ptr(), dy.data_ptr(), _ptr(dpost),
+                                                _ptr(dgate), _ptr(dpre), b, s, h, dt, ws_ptr, ws_bytes, st))
+    return dx, dy, dpost, dgate, dpre

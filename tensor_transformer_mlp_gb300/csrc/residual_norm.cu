@@ -1,0 +1,965 @@
+// The norms before and after a block with its gate and residual scale in one pass, and the backward
+// (tpmlp_residual_norm, tpmlp_residual_norm_backward). Per token, over the h columns:
+//
+//   y_hat = y ry, ry = 1 / sqrt(mean(y^2) + eps);   r = alpha x + gate gamma_post y_hat;   u = r rr gamma_pre
+//   g = dr + rr (du gamma_pre - r_hat c), c = mean(du gamma_pre r_hat);   dx = alpha g
+//   dy = ry (w g - y_hat mean(w g y_hat)), w = gate gamma_post
+//   dgamma_pre = sum du r_hat;   dgate = gamma_post S, dgamma_post = gate S summed over the sequences, where
+//   S = sum over a sequence's tokens of g y_hat
+//
+// Without gamma_post y_hat is y (and dy = w g), without a gate or gamma_pre they are one or their half of the work is
+// left out. Both directions are bound by memory: 4 values of T a column forward, 6 backward.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "abi_checks.h"
+#include "device_common.cuh"
+
+namespace tpmlp {
+namespace {
+
+constexpr int kMaxH = 8192;
+constexpr int kSmallH = 512;        // up to here a lane group takes a row, above a CTA does
+constexpr int kSmallThreads = 256;
+constexpr int kMaxCtas = 1024;      // of the backward, each with a row of partial sums
+
+// Eight columns as they lie in memory, and as four fp32 pairs.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  // Keeps the compiler from holding unpacked values (twice the registers) from one use to the next.
+  __device__ __forceinline__ void stay_packed() { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+  __device__ __forceinline__ void unpack(F2 (&f)[4]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2_make(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const F2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = f2_split(f[i]);
+      w[i] = pack_bf16x2(t.x, t.y);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void stay_packed() {}
+  __device__ __forceinline__ void unpack(F2 (&f)[4]) const {
+    f[0] = f2_make(a.x, a.y);
+    f[1] = f2_make(a.z, a.w);
+    f[2] = f2_make(b.x, b.y);
+    f[3] = f2_make(b.z, b.w);
+  }
+  static __device__ __forceinline__ void store(float* p, const F2 (&f)[4]) {
+    const float2 t0 = f2_split(f[0]), t1 = f2_split(f[1]), t2 = f2_split(f[2]), t3 = f2_split(f[3]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(t0.x, t0.y, t1.x, t1.y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(t2.x, t2.y, t3.x, t3.y);
+  }
+};
+
+__device__ __forceinline__ float sum2(F2 a) {
+  const float2 t = f2_split(a);
+  return t.x + t.y;
+}
+// Eight fp32 gains from column col on; ones where there are none, zeros past h.
+__device__ __forceinline__ void load_gain(F2 (&f)[4], const float* gain, int col, int h) {
+  if (col >= h || !gain) {
+    const float v = col >= h ? 0.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = f2_make(v, v);
+  } else {
+    Vec8<float> t;
+    t.load(gain + col);
+    t.unpack(f);
+  }
+}
+
+struct Forward {
+  const void *x, *y;
+  const float *post, *gate, *pre;
+  void *r, *u;
+  float alpha, eps, inv_h;
+  int64_t rows, s;
+  int h;
+};
+
+struct Backward {
+  const void *y, *r, *dr, *du;
+  const float *post, *gate, *pre;
+  void *dx, *dy;
+  // partials [gridDim.x][2][h]: the CTA's shares of dgamma_post and dgamma_pre; slots [gridDim.x + b][h]: S of CTA c's
+  // rows of sequence q at c + q (both only grow along the rows, so no two share a slot)
+  float *partials, *slots;
+  float alpha, eps, inv_h;
+  int64_t rows, s;
+  int h;
+};
+
+// CTA c's rows.
+__host__ __device__ __forceinline__ int64_t first_row(int64_t rows, int64_t c, int64_t ctas) {
+  return rows / ctas * c + min(c, rows % ctas);
+}
+
+// ------------------------------------------------------------------ a CTA for a row
+
+// A ring of bulk copies: stage st holds one row of each of the kernel's tensors. Thread 0 issues.
+template <int NTEN>
+struct RowRing {
+  uint8_t* smem;
+  uint64_t* full;
+  uint32_t row_bytes;
+  int stages;
+  const uint8_t* src[NTEN];  // the CTA's first row of each tensor; null: none
+  __device__ __forceinline__ uint32_t stage_bytes() const { return NTEN * row_bytes; }
+  __device__ __forceinline__ void init() const {
+    for (int st = 0; st < stages; ++st) mbar_init(&full[st], 1);
+    fence_mbar_init();
+  }
+  __device__ __forceinline__ void issue(int64_t i) const {
+    const int st = static_cast<int>(i % stages);
+    uint8_t* dst = smem + static_cast<size_t>(st) * stage_bytes();
+    uint32_t n = 0;
+#pragma unroll
+    for (int k = 0; k < NTEN; ++k) n += src[k] ? row_bytes : 0;
+    mbar_arrive_expect_tx(&full[st], n);
+#pragma unroll
+    for (int k = 0; k < NTEN; ++k)
+      if (src[k]) bulk_load(dst + k * row_bytes, src[k] + i * row_bytes, row_bytes, &full[st]);
+  }
+  __device__ __forceinline__ bool wait(int64_t i, unsigned int* status, unsigned int where) const {
+    return mbar_wait(&full[i % stages], static_cast<uint32_t>((i / stages) & 1), status, where);
+  }
+  template <typename T>
+  __device__ __forceinline__ const T* at(int64_t i, int k) const {
+    return reinterpret_cast<const T*>(smem + static_cast<size_t>(i % stages) * stage_bytes() + k * row_bytes);
+  }
+};
+
+template <int N>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Rows [first, first + n) go through the ring; a row's two sums each meet behind one barrier, every warp adding the
+// warps' shares in the same order. A wait that runs out ends the CTA at the next barrier.
+template <typename T, int NT, int CH>
+__global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_constant__ Forward p, int stages,
+                                                               unsigned int* status) {
+  constexpr int NW = NT / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2][2][NW];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), n = first_row(p.rows, blockIdx.x + 1, gridDim.x) - first;
+  RowRing<2> ring;
+  ring.smem = smem;
+  ring.row_bytes = static_cast<uint32_t>(p.h) * sizeof(T);
+  ring.stages = stages;
+  ring.full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(stages) * ring.stage_bytes());
+  ring.src[0] = static_cast<const uint8_t*>(p.x) + first * ring.row_bytes;
+  ring.src[1] = static_cast<const uint8_t*>(p.y) + first * ring.row_bytes;
+  if (tid == 0) ring.init();
+  __syncthreads();
+  int64_t issued = min(n, static_cast<int64_t>(stages));  // meaningful in thread 0
+  if (tid == 0)
+    for (int64_t i = 0; i < issued; ++i) ring.issue(i);
+
+  F2 wt[CH][4], pre[CH][4];
+  int64_t seq = -1, seq_end = 0;  // the sequence whose gate wt holds, and its last row's successor
+#pragma unroll
+  for (int c = 0; c < CH; ++c) load_gain(pre[c], p.pre, (tid + c * NT) * 8, p.h);
+  const F2 alpha = f2_make(p.alpha, p.alpha), zero = f2_make(0.f, 0.f);
+  int64_t i = 0;
+  int aborted = 0;
+  for (; i < n; ++i) {
+    const int64_t row = first + i;
+    if (row >= seq_end) {
+      seq = row / p.s;
+      seq_end = (seq + 1) * p.s;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (tid + c * NT) * 8;
+        F2 g[4];
+        load_gain(wt[c], p.post, col, p.h);
+        load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wt[c][e] = f2_mul(wt[c][e], g[e]);
+      }
+    }
+    const bool ok = ring.wait(i, status, 61);
+    Vec8<T> xv[CH], yv[CH];
+    F2 ss = zero;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (tid + c * NT) * 8;
+      xv[c].zero();
+      yv[c].zero();
+      if (col < p.h) {
+        xv[c].load(ring.at<T>(i, 0) + col);
+        yv[c].load(ring.at<T>(i, 1) + col);
+      }
+      F2 f[4];
+      yv[c].unpack(f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ss = f2_fma(f[e], f[e], ss);
+    }
+    const int par = static_cast<int>(i & 1);
+    const float ys = lane_sum<32>(sum2(ss));
+    if (lane == 0) red[par][0][w] = ys;
+    aborted = __syncthreads_or(!ok);  // the row is in registers everywhere
+    if (aborted) break;
+    if (tid == 0 && i + stages < n) {
+      ring.issue(i + stages);
+      issued = i + stages + 1;
+    }
+    const float ry = p.post ? rsqrtf(fmaf(lane_sum<NW>(red[par][0][lane & (NW - 1)]), p.inv_h, p.eps)) : 1.f;
+    F2 rf[CH][4];
+    ss = zero;
+    const F2 ry2 = f2_make(ry, ry);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (tid + c * NT) * 8;
+      F2 xf[4], yf[4];
+      yv[c].stay_packed();
+      xv[c].unpack(xf);
+      yv[c].unpack(yf);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        rf[c][e] = f2_fma(f2_mul(yf[e], ry2), wt[c][e], f2_mul(alpha, xf[e]));
+        ss = f2_fma(rf[c][e], rf[c][e], ss);
+      }
+      if (col < p.h) Vec8<T>::store(static_cast<T*>(p.r) + row * p.h + col, rf[c]);
+    }
+    if (p.pre) {
+      const float rs = lane_sum<32>(sum2(ss));
+      if (lane == 0) red[par][1][w] = rs;
+      __syncthreads();
+      const float rr = rsqrtf(fmaf(lane_sum<NW>(red[par][1][lane & (NW - 1)]), p.inv_h, p.eps));
+      const F2 rr2 = f2_make(rr, rr);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (tid + c * NT) * 8;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rf[c][e] = f2_mul(f2_mul(rf[c][e], rr2), pre[c][e]);
+        if (col < p.h) Vec8<T>::store(static_cast<T*>(p.u) + row * p.h + col, rf[c]);
+      }
+    }
+  }
+  if (aborted && tid == 0)
+    for (int64_t k = i; k < issued; ++k) ring.wait(k, status, 62);  // copies in flight
+}
+
+// The backward's six sums of a row; everything that follows from them.
+//   sums: r^2, du' r, y^2, (w y) dr, (w y) du', (w y) r with du' = du gamma_pre
+struct RowFactors {
+  float rr, kr;  // g = dr + rr du' - kr r
+  float ry, ky;  // dy = ry w g - ky y
+  __device__ __forceinline__ RowFactors(const float (&s)[6], const Backward& p) {
+    rr = p.pre ? rsqrtf(fmaf(s[0], p.inv_h, p.eps)) : 0.f;
+    kr = rr * rr * rr * s[1] * p.inv_h;
+    ry = p.post ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.f;
+    // the sum of w g y needs no pass of its own: g is a sum of three terms
+    ky = p.post ? ry * ry * ry * p.inv_h * (s[3] + (rr * s[4] - kr * s[5])) : 0.f;
+  }
+};
+
+// One thread's eight columns of a row.
+template <typename T>
+struct GradColumns {
+  Vec8<T> y, r, dr, du;
+  __device__ __forceinline__ void zero() {
+    y.zero();
+    r.zero();
+    dr.zero();
+    du.zero();
+  }
+  __device__ __forceinline__ void stay_packed() {
+    y.stay_packed();
+    r.stay_packed();
+    dr.stay_packed();
+    du.stay_packed();
+  }
+  __device__ __forceinline__ void sums(const F2 (&wt)[4], const F2 (&pre)[4], F2 (&s)[6]) const {
+    F2 yf[4], rf[4], drf[4], duf[4];
+    y.unpack(yf);
+    r.unpack(rf);
+    dr.unpack(drf);
+    du.unpack(duf);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const F2 d = f2_mul(duf[e], pre[e]), wy = f2_mul(wt[e], yf[e]);
+      s[0] = f2_fma(rf[e], rf[e], s[0]);
+      s[1] = f2_fma(d, rf[e], s[1]);
+      s[2] = f2_fma(yf[e], yf[e], s[2]);
+      s[3] = f2_fma(wy, drf[e], s[3]);
+      s[4] = f2_fma(wy, d, s[4]);
+      s[5] = f2_fma(wy, rf[e], s[5]);
+    }
+  }
+  // dx and dy into ox, oy; adds to S and dgamma_pre.
+  __device__ __forceinline__ void grads(const F2 (&wt)[4], const F2 (&pre)[4], const RowFactors& k, float alpha, F2 (&ox)[4],
+                                        F2 (&oy)[4], F2 (&acc_s)[4], F2 (&acc_pre)[4]) const {
+    F2 yf[4], rf[4], drf[4], duf[4];
+    y.unpack(yf);
+    r.unpack(rf);
+    dr.unpack(drf);
+    du.unpack(duf);
+    const F2 rr = f2_make(k.rr, k.rr), nkr = f2_make(-k.kr, -k.kr), ry = f2_make(k.ry, k.ry), nky = f2_make(-k.ky, -k.ky),
+             a = f2_make(alpha, alpha);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const F2 drr = f2_mul(duf[e], rr);
+      const F2 g = f2_add(drf[e], f2_fma(drr, pre[e], f2_mul(nkr, rf[e])));
+      acc_pre[e] = f2_fma(drr, rf[e], acc_pre[e]);
+      const F2 gy = f2_mul(g, ry);
+      acc_s[e] = f2_fma(gy, yf[e], acc_s[e]);
+      ox[e] = f2_mul(a, g);
+      oy[e] = f2_fma(gy, wt[e], f2_mul(nky, yf[e]));
+    }
+  }
+};
+
+// A thread's share of what a CTA leaves of a sequence: S to its slot, and gate S added to the CTA's dgamma_post.
+__device__ __forceinline__ void leave_sequence(const Backward& p, int64_t seq, int col, const F2 (&acc)[4], bool first) {
+  F2 g[4];
+  load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+  if (p.slots) Vec8<float>::store(p.slots + (blockIdx.x + seq) * p.h + col, acc);
+  if (p.post) {
+    float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.h + col;
+    F2 old[4] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f), f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+    if (!first) {
+      Vec8<float> t;
+      t.load(out);
+      t.unpack(old);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) old[e] = f2_fma(g[e], acc[e], old[e]);
+    Vec8<float>::store(out, old);
+  }
+}
+
+// Sums eight values a lane over the warp; lane l ends with the total of value (l >> 2) & 7 (9 shuffles).
+__device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
+#pragma unroll
+  for (int half = 4, o = 16; half > 0; half >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < half; ++k) {
+      const float send = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// One barrier a row: all six sums are taken at once.
+template <typename T, int NT, int CH, int MINB>
+__global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(const __grid_constant__ Backward p, int stages,
+                                                                              unsigned int* status) {
+  constexpr int NW = NT / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2][NW][8];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), n = first_row(p.rows, blockIdx.x + 1, gridDim.x) - first;
+  RowRing<4> ring;
+  ring.smem = smem;
+  ring.row_bytes = static_cast<uint32_t>(p.h) * sizeof(T);
+  ring.stages = stages;
+  ring.full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(stages) * ring.stage_bytes());
+  const void* src[4] = {p.y, p.r, p.dr, p.du};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ring.src[k] = src[k] ? static_cast<const uint8_t*>(src[k]) + first * ring.row_bytes : nullptr;
+  if (tid == 0) ring.init();
+  __syncthreads();
+  int64_t issued = min(n, static_cast<int64_t>(stages));  // meaningful in thread 0
+  if (tid == 0)
+    for (int64_t i = 0; i < issued; ++i) ring.issue(i);
+
+  const F2 zero = f2_make(0.f, 0.f);
+  F2 wt[CH][4], pre[CH][4], acc_s[CH][4], acc_pre[CH][4];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_gain(pre[c], p.pre, (tid + c * NT) * 8, p.h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc_s[c][e] = acc_pre[c][e] = zero;
+  }
+  int64_t seq = -1, seq_end = first;
+  bool none_left = true;  // no sequence of the CTA has ended yet
+  int64_t i = 0;
+  int aborted = 0;
+  for (; i < n; ++i) {
+    const int64_t row = first + i;
+    if (row >= seq_end) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (tid + c * NT) * 8;
+        if (seq >= 0 && col < p.h) leave_sequence(p, seq, col, acc_s[c], none_left);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc_s[c][e] = zero;
+      }
+      none_left = seq < 0;
+      seq = row / p.s;
+      seq_end = (seq + 1) * p.s;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (tid + c * NT) * 8;
+        F2 g[4];
+        load_gain(wt[c], p.post, col, p.h);
+        load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wt[c][e] = f2_mul(wt[c][e], g[e]);
+      }
+    }
+    const bool ok = ring.wait(i, status, 63);
+    GradColumns<T> v[CH];
+    F2 s2[6] = {zero, zero, zero, zero, zero, zero};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (tid + c * NT) * 8;
+      v[c].zero();
+      if (col < p.h) {
+        if (p.y) v[c].y.load(ring.at<T>(i, 0) + col);
+        if (p.r) v[c].r.load(ring.at<T>(i, 1) + col);
+        if (p.dr) v[c].dr.load(ring.at<T>(i, 2) + col);
+        if (p.du) v[c].du.load(ring.at<T>(i, 3) + col);
+      }
+      v[c].sums(wt[c], pre[c], s2);
+    }
+    const int par = static_cast<int>(i & 1);
+    float s8[8] = {sum2(s2[0]), sum2(s2[1]), sum2(s2[2]), sum2(s2[3]), sum2(s2[4]), sum2(s2[5]), 0.f, 0.f};
+    const float mine = warp_sums8(s8, lane);
+    if ((lane & 3) == 0) red[par][w][lane >> 2] = mine;
+    aborted = __syncthreads_or(!ok);  // the row is in registers everywhere, the warps' sums are out
+    if (aborted) break;
+    if (tid == 0 && i + stages < n) {
+      ring.issue(i + stages);
+      issued = i + stages + 1;
+    }
+    // lane l adds value l & 7 of the warps l >> 3, + 4, ..: the same order in every warp
+    float part = 0.f;
+#pragma unroll
+    for (int k = 0; k < (NW + 3) / 4; ++k) {
+      const int warp = (lane >> 3) + 4 * k;
+      if (warp < NW) part += red[par][warp][lane & 7];
+    }
+    part += __shfl_xor_sync(0xffffffffu, part, 8);
+    part += __shfl_xor_sync(0xffffffffu, part, 16);
+    float total[6];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) total[k] = __shfl_sync(0xffffffffu, part, k);
+    const RowFactors f(total, p);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (tid + c * NT) * 8;
+      F2 ox[4], oy[4];
+      v[c].stay_packed();
+      v[c].grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
+      if (col < p.h) {
+        Vec8<T>::store(static_cast<T*>(p.dx) + row * p.h + col, ox);
+        Vec8<T>::store(static_cast<T*>(p.dy) + row * p.h + col, oy);
+      }
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;");  // the sums below may be scheduled; they wait for this grid's end
+  if (aborted && tid == 0)
+    for (int64_t k = i; k < issued; ++k) ring.wait(k, status, 64);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (tid + c * NT) * 8;
+    if (col < p.h) {
+      leave_sequence(p, seq, col, acc_s[c], none_left);
+      Vec8<float>::store(p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * p.h + col, acc_pre[c]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ a lane group for a row
+
+// Up to 512 columns: `group` lanes (a power of two) take a row, CH vectors of 8 columns each.
+__device__ __forceinline__ float group_sum(float v, int group) {
+  for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int CH>
+__global__ void __launch_bounds__(kSmallThreads) residual_norm_small_kernel(const __grid_constant__ Forward p, int group) {
+  const int gl = threadIdx.x & (group - 1);
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kSmallThreads / group);
+  const F2 alpha = f2_make(p.alpha, p.alpha), zero = f2_make(0.f, 0.f);
+  // all lanes of a warp make the same number of rounds: the shuffles need them
+  const int64_t lead = static_cast<int64_t>(blockIdx.x) * (kSmallThreads / group) + threadIdx.x / group;
+  const int64_t warp_lead = lead - (threadIdx.x & 31) / group;
+  for (int64_t at = 0; warp_lead + at < p.rows; at += groups) {
+    const bool live = lead + at < p.rows;
+    const int64_t row = live ? lead + at : p.rows - 1;
+    const int64_t seq = p.gate ? row / p.s : 0;
+    Vec8<T> xv[CH], yv[CH];
+    F2 ss = zero;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (gl + c * group) * 8;
+      xv[c].zero();
+      yv[c].zero();
+      if (col < p.h) {
+        xv[c].load(static_cast<const T*>(p.x) + row * p.h + col);
+        yv[c].load(static_cast<const T*>(p.y) + row * p.h + col);
+      }
+      F2 f[4];
+      yv[c].unpack(f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ss = f2_fma(f[e], f[e], ss);
+    }
+    float sum = group_sum(sum2(ss), group);
+    const float ry = p.post ? rsqrtf(fmaf(sum, p.inv_h, p.eps)) : 1.f;
+    const F2 ry2 = f2_make(ry, ry);
+    F2 rf[CH][4];
+    ss = zero;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (gl + c * group) * 8;
+      F2 xf[4], yf[4], wt[4], g[4];
+      xv[c].unpack(xf);
+      yv[c].unpack(yf);
+      load_gain(wt, p.post, col, p.h);
+      load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        rf[c][e] = f2_fma(f2_mul(yf[e], ry2), f2_mul(wt[e], g[e]), f2_mul(alpha, xf[e]));
+        ss = f2_fma(rf[c][e], rf[c][e], ss);
+      }
+    }
+    sum = group_sum(sum2(ss), group);
+    const float rr = rsqrtf(fmaf(sum, p.inv_h, p.eps));
+    const F2 rr2 = f2_make(rr, rr);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (gl + c * group) * 8;
+      if (!live || col >= p.h) continue;
+      Vec8<T>::store(static_cast<T*>(p.r) + row * p.h + col, rf[c]);
+      if (p.pre) {
+        F2 pre[4];
+        load_gain(pre, p.pre, col, p.h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rf[c][e] = f2_mul(f2_mul(rf[c][e], rr2), pre[e]);
+        Vec8<T>::store(static_cast<T*>(p.u) + row * p.h + col, rf[c]);
+      }
+    }
+  }
+}
+
+// A CTA's rows are worked on sequence by sequence, each group taking every (256 / group)-th row; what the groups have
+// added up meets in shared memory when the sequence, or the CTA's part of it, ends.
+template <typename T, int CH>
+__global__ void __launch_bounds__(kSmallThreads, 2)
+    residual_norm_small_backward_kernel(const __grid_constant__ Backward p, int group) {
+  constexpr int NW = kSmallThreads / 32;
+  __shared__ float4 red[NW][kSmallH / 4];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gl = tid & (group - 1), ngroups = kSmallThreads / group;
+  const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), last = first_row(p.rows, blockIdx.x + 1, gridDim.x);
+  const F2 zero = f2_make(0.f, 0.f);
+  F2 wt[CH][4], pre[CH][4], acc_s[CH][4], acc_pre[CH][4];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_gain(pre[c], p.pre, (gl + c * group) * 8, p.h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc_pre[c][e] = zero;
+  }
+  // the CTA's sum of acc: columns 8 tid .. 8 tid + 7 end in thread tid's `out`
+  auto gather = [&](F2 (&acc)[CH][4], F2 (&out)[4]) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 t = f2_split(acc[c][e]);
+        v[2 * e] = t.x;
+        v[2 * e + 1] = t.y;
+      }
+      for (int o = 16; o >= group; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+      const int col = (gl + c * group) * 8;
+      if (lane < group && col < p.h) {
+        red[w][col / 4] = make_float4(v[0], v[1], v[2], v[3]);
+        red[w][col / 4 + 1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = zero;
+    if (tid * 8 < p.h)
+      for (int k = 0; k < NW; ++k) {
+        const float4 a = red[k][2 * tid], b = red[k][2 * tid + 1];
+        out[0] = f2_add(out[0], f2_make(a.x, a.y));
+        out[1] = f2_add(out[1], f2_make(a.z, a.w));
+        out[2] = f2_add(out[2], f2_make(b.x, b.y));
+        out[3] = f2_add(out[3], f2_make(b.z, b.w));
+      }
+    __syncthreads();
+  };
+  bool none_left = true;
+  for (int64_t at = first; at < last;) {
+    const int64_t seq = at / p.s, end = min(last, (seq + 1) * p.s);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (gl + c * group) * 8;
+      F2 g[4];
+      load_gain(wt[c], p.post, col, p.h);
+      load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        wt[c][e] = f2_mul(wt[c][e], g[e]);
+        acc_s[c][e] = zero;
+      }
+    }
+    for (; at < end; at += ngroups) {  // the same for every thread
+      const int64_t row = at + tid / group;
+      const bool live = row < end;
+      GradColumns<T> v[CH];
+      F2 s2[6] = {zero, zero, zero, zero, zero, zero};
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (gl + c * group) * 8;
+        v[c].zero();
+        if (live && col < p.h) {
+          if (p.y) v[c].y.load(static_cast<const T*>(p.y) + row * p.h + col);
+          if (p.r) v[c].r.load(static_cast<const T*>(p.r) + row * p.h + col);
+          if (p.dr) v[c].dr.load(static_cast<const T*>(p.dr) + row * p.h + col);
+          if (p.du) v[c].du.load(static_cast<const T*>(p.du) + row * p.h + col);
+        }
+        v[c].sums(wt[c], pre[c], s2);
+      }
+      float total[6];
+#pragma unroll
+      for (int k = 0; k < 6; ++k) total[k] = group_sum(sum2(s2[k]), group);
+      const RowFactors f(total, p);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (gl + c * group) * 8;
+        F2 ox[4], oy[4];
+        v[c].stay_packed();
+        v[c].grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
+        if (live && col < p.h) {
+          Vec8<T>::store(static_cast<T*>(p.dx) + row * p.h + col, ox);
+          Vec8<T>::store(static_cast<T*>(p.dy) + row * p.h + col, oy);
+        }
+      }
+    }
+    at = end;
+    if (p.slots || p.post) {
+      F2 sum[4];
+      gather(acc_s, sum);
+      if (tid * 8 < p.h) leave_sequence(p, seq, tid * 8, sum, none_left);
+    }
+    none_left = false;
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  F2 sum[4];
+  gather(acc_pre, sum);
+  if (tid * 8 < p.h) Vec8<float>::store(p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * p.h + tid * 8, sum);
+}
+
+// ------------------------------------------------------------------ the sums over CTAs
+
+// 32 columns a CTA. Groups of 8 threads each add every 32nd row of partials, then the groups' sums are added by a fixed
+// tree. CTAs [0, slices) sum dgamma_post, [slices, 2 slices) dgamma_pre, the others dgate, a sequence's slices after
+// another's. Launched as a programmatic dependent of the backward kernel.
+constexpr int kFinishThreads = 256;
+struct Finish {
+  const float *partials, *slots, *post;
+  float *dpost, *dpre, *dgate;
+  int64_t rows, s;
+  int h, slices, ctas;
+};
+__global__ void __launch_bounds__(kFinishThreads) residual_norm_finish_kernel(const __grid_constant__ Finish p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kQuads = 8, kGroups = kFinishThreads / kQuads;
+  __shared__ float4 grp[kGroups][kQuads];
+  const int q = threadIdx.x % kQuads, g = threadIdx.x / kQuads;
+  const int64_t part = blockIdx.x / p.slices;
+  const int col = (blockIdx.x % p.slices) * 32 + q * 4;
+  const bool in = col < p.h;
+  const float* src;
+  int64_t n, stride;
+  float* out;
+  if (part < 2) {
+    src = p.partials + part * p.h;
+    n = p.ctas;
+    stride = 2 * static_cast<int64_t>(p.h);
+    out = part == 0 ? p.dpost : p.dpre;
+    if (!out) return;
+  } else {
+    // sequence seq's rows: those of the CTAs c0 .. c1, CTA c's at slot c + seq
+    const int64_t seq = part - 2, a = seq * p.s, z = a + p.s - 1, each = p.rows / p.ctas, more = p.rows % p.ctas;
+    auto cta_of = [&](int64_t row) { return row < more * (each + 1) ? row / (each + 1) : more + (row - more * (each + 1)) / each; };
+    const int64_t c0 = cta_of(a);
+    n = cta_of(z) - c0 + 1;
+    src = p.slots + (c0 + seq) * p.h;
+    stride = p.h;
+    out = p.dgate + seq * p.h;
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (in) {
+#pragma unroll 8
+    for (int64_t k = g; k < n; k += kGroups) {
+      const float4 v = *reinterpret_cast<const float4*>(src + k * stride + col);
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+  }
+  grp[g][q] = acc;
+#pragma unroll
+  for (int half = kGroups / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (g < half) {
+      const float4 o = grp[g + half][q];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+      grp[g][q] = acc;
+    }
+  }
+  if (g == 0 && in) {
+    if (part >= 2 && p.post) {
+      const float4 w = *reinterpret_cast<const float4*>(p.post + col);
+      acc = make_float4(acc.x * w.x, acc.y * w.y, acc.z * w.z, acc.w * w.w);
+    }
+    *reinterpret_cast<float4*>(out + col) = acc;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+int small_group(int h) {
+  int group = 4;
+  while (group < 32 && group * 8 < h) group *= 2;
+  return group;
+}
+
+// CTAs of one resident wave of `kernel`, at most `most`.
+template <typename K>
+cudaError_t wave(int64_t* ctas, K kernel, int threads, size_t smem, int64_t most, const DeviceCtx& ctx) {
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
+  *ctas = std::max<int64_t>(1, std::min<int64_t>(most, static_cast<int64_t>(std::max(per_sm, 1)) * ctx.num_sms));
+  return cudaSuccess;
+}
+
+size_t ring_smem(int tensors, int h, size_t size, int stages) {
+  return stages * (static_cast<size_t>(tensors) * h * size + sizeof(uint64_t));
+}
+
+template <typename T, int NT, int CH>
+cudaError_t forward_rows(const Forward& p, cudaStream_t stream, const DeviceCtx& ctx) {
+  static SmemLimit limit;
+  const int stages = std::min<int>(4, static_cast<int>(100 * 1024 / ring_smem(2, p.h, sizeof(T), 1)));
+  auto kernel = residual_norm_row_kernel<T, NT, CH>;
+  const size_t smem = ring_smem(2, p.h, sizeof(T), std::max(stages, 2));
+  cudaError_t e = allow_smem(&limit, kernel, 200 * 1024, ctx);
+  if (e != cudaSuccess) return e;
+  int64_t ctas;
+  if ((e = wave(&ctas, kernel, NT, smem, p.rows, ctx)) != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(ctas), NT, smem, stream>>>(p, std::max(stages, 2), ctx.status);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward_for(const Forward& p, cudaStream_t stream, const DeviceCtx& ctx) {
+  if (p.h <= kSmallH) {
+    const int group = small_group(p.h);
+    const int64_t need = (p.rows * group + kSmallThreads - 1) / kSmallThreads;
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(ctx.num_sms) * 32));
+    if (p.h <= 256)
+      residual_norm_small_kernel<T, 1><<<ctas, kSmallThreads, 0, stream>>>(p, group);
+    else
+      residual_norm_small_kernel<T, 2><<<ctas, kSmallThreads, 0, stream>>>(p, group);
+    return cudaGetLastError();
+  }
+  if (p.h <= 1024) return forward_rows<T, 128, 1>(p, stream, ctx);
+  if (p.h <= 2048) return forward_rows<T, 128, 2>(p, stream, ctx);
+  if (p.h <= 4096) return forward_rows<T, 256, 2>(p, stream, ctx);
+  return forward_rows<T, 512, 2>(p, stream, ctx);
+}
+
+template <typename T, int NT, int CH, int MINB>
+cudaError_t backward_rows(Backward p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
+  static SmemLimit limit;
+  const int stages = std::max(1, std::min<int>(3, static_cast<int>(200 * 1024 / ring_smem(4, p.h, sizeof(T), 1))));
+  auto kernel = residual_norm_row_backward_kernel<T, NT, CH, MINB>;
+  const size_t smem = ring_smem(4, p.h, sizeof(T), stages);
+  cudaError_t e = allow_smem(&limit, kernel, 200 * 1024, ctx);
+  if (e != cudaSuccess) return e;
+  if ((e = wave(ctas, kernel, NT, smem, std::min<int64_t>(p.rows, kMaxCtas), ctx)) != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(*ctas), NT, smem, stream>>>(p, stages, ctx.status);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
+  if (p.h <= kSmallH) {
+    const int group = small_group(p.h);
+    const int64_t need = (p.rows * group + kSmallThreads - 1) / kSmallThreads;
+    *ctas = std::min<int64_t>(need, std::min<int64_t>(static_cast<int64_t>(ctx.num_sms) * 2, kMaxCtas));
+    if (p.h <= 256)
+      residual_norm_small_backward_kernel<T, 1><<<static_cast<unsigned>(*ctas), kSmallThreads, 0, stream>>>(p, group);
+    else
+      residual_norm_small_backward_kernel<T, 2><<<static_cast<unsigned>(*ctas), kSmallThreads, 0, stream>>>(p, group);
+    return cudaGetLastError();
+  }
+  if (p.h <= 1024) return backward_rows<T, 128, 1, 4>(p, ctas, stream, ctx);
+  if constexpr (sizeof(T) == 2) {
+    if (p.h <= 2048) return backward_rows<T, 128, 2, 4>(p, ctas, stream, ctx);
+    if (p.h <= 4096) return backward_rows<T, 256, 2, 2>(p, ctas, stream, ctx);
+  } else {
+    if (p.h <= 2048) return backward_rows<T, 256, 1, 2>(p, ctas, stream, ctx);
+    if (p.h <= 4096) return backward_rows<T, 512, 1, 1>(p, ctas, stream, ctx);
+  }
+  return backward_rows<T, 512, 2, 1>(p, ctas, stream, ctx);
+}
+
+tpmlp_status check_norm_shape(float alpha, float eps, int64_t b, int64_t s, int64_t h, tpmlp_dtype dt) {
+  if (dt != TPMLP_BF16 && dt != TPMLP_F32) return err(TPMLP_ERR_DTYPE, "unsupported dtype");
+  if (b < 0 || s < 0) return err(TPMLP_ERR_SHAPE, "need b, s >= 0");
+  if (b > 0 && s > INT32_MAX / b) return err(TPMLP_ERR_SHAPE, "b * s exceeds 2^31-1");
+  if (h < 8 || h % 8 != 0 || h > kMaxH) return err(TPMLP_ERR_SHAPE, "h must be a multiple of 8, 8 <= h <= 8192");
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return err(TPMLP_ERR_INVALID, "eps must be positive and finite");
+  if (!std::isfinite(alpha)) return err(TPMLP_ERR_INVALID, "alpha must be finite");
+  return TPMLP_OK;
+}
+
+constexpr const char* kAlign = "pointers must be 16-byte aligned";
+
+size_t partials_bytes(int64_t b, int64_t s, int64_t h, bool gate) {
+  const int64_t rows = std::min<int64_t>(b * s, kMaxCtas);
+  return static_cast<size_t>(2 * rows + (gate ? rows + b : 0)) * h * sizeof(float);
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+using namespace tpmlp;
+
+extern "C" {
+
+tpmlp_status tpmlp_residual_norm(const void* x, const void* y, const float* gamma_post, const float* gate,
+                                 const float* gamma_pre, float alpha, float eps, void* r, void* u, int64_t b, int64_t s,
+                                 int64_t h, tpmlp_dtype dt, void* stream) {
+  TPMLP_PASS(check_norm_shape(alpha, eps, b, s, h, dt));
+  if (b * s == 0) return TPMLP_OK;
+  if (!gamma_pre != !u) return err(TPMLP_ERR_INVALID, "gamma_pre and u go together");
+  TPMLP_PASS(check_ptrs({x, y, r}, 16, kAlign));
+  for (const void* p : {static_cast<const void*>(gamma_post), static_cast<const void*>(gate),
+                        static_cast<const void*>(gamma_pre), static_cast<const void*>(u)})
+    if (!aligned(p, 16)) return err(TPMLP_ERR_ALIGN, kAlign);
+  const int64_t rows = b * s, size = dt == TPMLP_BF16 ? 2 : 4;
+  auto of = [&](const void* p) { return flat_region(p, rows * h, size); };
+  auto meets = [&](const void* out, const void* in) { return out && out != in && overlap(of(out), of(in)); };
+  if (any_overlap({of(r), of(u)}, {flat_region(gamma_post, h, 4), flat_region(gate, b * h, 4), flat_region(gamma_pre, h, 4)}) ||
+      meets(r, x) || meets(r, y) || meets(u, x) || meets(u, y))
+    return err(TPMLP_ERR_INVALID, "r or u overlaps another tensor of the call (they may be x or y)");
+  DeviceCtx ctx;
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
+  const Forward p{x, y, gamma_post, gate, gamma_pre, r, u, alpha, eps, 1.0f / static_cast<float>(h), rows, s, static_cast<int>(h)};
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  TPMLP_PASS_CUDA(dt == TPMLP_BF16 ? forward_for<__nv_bfloat16>(p, st, ctx) : forward_for<float>(p, st, ctx), "residual norm");
+  return TPMLP_OK;
+}
+
+size_t tpmlp_residual_norm_backward_workspace_size(int64_t b, int64_t s, int64_t h, int gate) {
+  if (b <= 0 || s <= 0 || h <= 0) return 0;
+  return partials_bytes(b, s, h, gate != 0);
+}
+
+tpmlp_status tpmlp_residual_norm_backward(const void* y, const void* r, const void* dr, const void* du,
+                                          const float* gamma_post, const float* gate, const float* gamma_pre, float alpha,
+                                          float eps, void* dx, void* dy, float* dgamma_post, float* dgate, float* dgamma_pre,
+                                          int64_t b, int64_t s, int64_t h, tpmlp_dtype dt, void* workspace, size_t ws_bytes,
+                                          void* stream) {
+  TPMLP_PASS(check_norm_shape(alpha, eps, b, s, h, dt));
+  if (!gamma_post != !dgamma_post || !gate != !dgate || !gamma_pre != !dgamma_pre)
+    return err(TPMLP_ERR_INVALID, "gamma_post, gate and gamma_pre go with their gradients");
+  for (const void* p : {static_cast<const void*>(dgamma_post), static_cast<const void*>(dgate),
+                        static_cast<const void*>(dgamma_pre)})
+    if (!aligned(p, 16)) return err(TPMLP_ERR_ALIGN, kAlign);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (b * s == 0) {
+    if (dgamma_post) TPMLP_PASS_CUDA(cudaMemsetAsync(dgamma_post, 0, h * sizeof(float), st), "zero dgamma_post");
+    if (dgamma_pre) TPMLP_PASS_CUDA(cudaMemsetAsync(dgamma_pre, 0, h * sizeof(float), st), "zero dgamma_pre");
+    if (dgate && b > 0) TPMLP_PASS_CUDA(cudaMemsetAsync(dgate, 0, b * h * sizeof(float), st), "zero dgate");
+    return TPMLP_OK;
+  }
+  if (!gamma_pre != !du) return err(TPMLP_ERR_INVALID, "gamma_pre and du go together");
+  if (!dr && !du) return err(TPMLP_ERR_INVALID, "dr may be NULL only beside du");
+  TPMLP_PASS(check_ptrs({dx, dy}, 16, kAlign));
+  if (gamma_post || gate) TPMLP_PASS(check_ptrs({y}, 16, kAlign));
+  if (gamma_pre) TPMLP_PASS(check_ptrs({r}, 16, kAlign));
+  if (!gamma_post && !gate) y = nullptr;  // not read
+  if (!gamma_pre) r = nullptr;
+  for (const void* p : {static_cast<const void*>(gamma_post), static_cast<const void*>(gate),
+                        static_cast<const void*>(gamma_pre), dr, du})
+    if (!aligned(p, 16)) return err(TPMLP_ERR_ALIGN, kAlign);
+  const size_t need = partials_bytes(b, s, h, gate != nullptr);
+  if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "residual norm backward workspace too small");
+  if (!aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
+  const int64_t rows = b * s, size = dt == TPMLP_BF16 ? 2 : 4;
+  auto of = [&](const void* p) { return flat_region(p, rows * h, size); };
+  const Region gains[] = {flat_region(gamma_post, h, 4), flat_region(gate, b * h, 4), flat_region(gamma_pre, h, 4)};
+  bool bad = any_overlap({of(dx), of(dy), flat_region(dgamma_post, h, 4), flat_region(dgate, b * h, 4),
+                          flat_region(dgamma_pre, h, 4), flat_region(workspace, static_cast<int64_t>(need), 1)},
+                         {gains[0], gains[1], gains[2]}) ||
+             any_overlap({flat_region(dgamma_post, h, 4), flat_region(dgate, b * h, 4), flat_region(dgamma_pre, h, 4),
+                          flat_region(workspace, static_cast<int64_t>(need), 1)},
+                         {of(y), of(r), of(dr), of(du)});
+  for (const void* in : {y, r, dr, du})
+    for (const void* out : {static_cast<const void*>(dx), static_cast<const void*>(dy)})
+      bad = bad || (in && in != out && overlap(of(out), of(in)));
+  if (bad) return err(TPMLP_ERR_INVALID, "an output or the workspace overlaps another tensor of the call (dx and dy may be y, r, dr or du)");
+  DeviceCtx ctx;
+  TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
+  float* partials = static_cast<float*>(workspace);
+  float* slots = gate ? partials + 2 * std::min<int64_t>(rows, kMaxCtas) * h : nullptr;
+  const Backward p{y, r, dr, du, gamma_post, gate, gamma_pre, dx, dy, partials, slots, alpha, eps,
+                   1.0f / static_cast<float>(h), rows, s, static_cast<int>(h)};
+  int64_t ctas = 0;
+  TPMLP_PASS_CUDA(dt == TPMLP_BF16 ? backward_for<__nv_bfloat16>(p, &ctas, st, ctx) : backward_for<float>(p, &ctas, st, ctx),
+                  "residual norm backward");
+  if (!dgamma_post && !dgamma_pre && !dgate) return TPMLP_OK;
+  const int slices = static_cast<int>((h + 31) / 32);
+  const Finish f{partials, slots, gamma_post, dgamma_post, dgamma_pre, dgate, rows, s, static_cast<int>(h), slices,
+                 static_cast<int>(ctas)};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((2 + (gate ? b : 0)) * slices), 1, 1);
+  cfg.blockDim = dim3(kFinishThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  TPMLP_PASS_CUDA(cudaLaunchKernelEx(&cfg, residual_norm_finish_kernel, f), "residual norm sums");
+  return TPMLP_OK;
+}
+
+}  // extern "C"
