@@ -501,7 +501,7 @@ tpmlp_status tpmlp_masked_attention_backward(const void* q, const void* k, const
  * workspace: tpmlp_gated_forward_workspace_size bytes, 256-byte aligned (may be 0 bytes, then it may be NULL).
  */
 typedef enum { TPMLP_GATE_GELU_ERF = 0, TPMLP_GATE_GELU_TANH = 1, TPMLP_GATE_SILU = 2 } tpmlp_gate_act;
-size_t tpmlp_gated_forward_workspace_size(int64_t n, int64_t d, int64_t m, tpmlp_dtype dt);
+size_t tpmlp_gated_forward_workspace_size(int64_t n, int64_t d, int64_t m, int t, tpmlp_dtype dt);
 tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, void* O, void* Z_save, void* Y_save,
                                  int64_t n, int64_t d, int64_t m, int t, int act, tpmlp_dtype dt, void* workspace,
                                  size_t ws_bytes, void* stream);
@@ -518,7 +518,7 @@ typedef enum { TPMLP_WGRAD_F32 = 0, TPMLP_WGRAD_F32_ADD = 1, TPMLP_WGRAD_OPERAND
  * wgrad: a tpmlp_wgrad, the form of dA and dB. workspace: tpmlp_gated_backward_workspace_size bytes, 256-byte aligned.
  * n == 0 gives dA = dB = 0 (TPMLP_WGRAD_F32_ADD: leaves them) and the token buffers may be NULL.
  */
-size_t tpmlp_gated_backward_workspace_size(int64_t n, int64_t m, tpmlp_dtype dt);
+size_t tpmlp_gated_backward_workspace_size(int64_t n, int64_t d, int64_t m, tpmlp_dtype dt);
 tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, const void* G, const void* Z_save,
                                   const void* Y_save, void* dX, void* dA, void* dB, int64_t n, int64_t d, int64_t m,
                                   int t, int act, int wgrad, tpmlp_dtype dt, void* workspace, size_t ws_bytes,
@@ -567,7 +567,8 @@ tpmlp_status tpmlp_residual_norm_backward(const void* y, const void* r, const vo
  *                  the launch's waves; 2: clusters of two SMs on 256 x 256 tiles only; 3: on
  *                  256 x 512 tiles only (a last round that would keep at most half the SM pairs
  *                  busy runs as 256 x 256 half-tiles, one per pair); 0: 128 x 256 tiles on one SM (the gated
- *                  block's products with an elementwise part then run as with 2).
+ *                  block's products with an elementwise part then run as with 2). The gated block's products of few
+ *                  tokens, which split their sum over the SMs, run with 1 only.
  *   pair_pacing 1: pairs wait at intervals of 16 k-blocks for the pairs of the same round of
  *                  tiles, which keeps shared operand panels in L2; 0: no pacing.
  *   pair_group  0: the default tile band (16 pair-rows walked along N, for 256 x 256 and

@@ -70,9 +70,9 @@ SIGNATURES = {
     "tpmlp_masked_attention_backward_workspace_size": (_SZ, [_I64, _I64, _I]),
     "tpmlp_masked_attention_backward": (_I, [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I]
                                         + [_I64] * 14 + [_I, _P, _SZ, _P]),
-    "tpmlp_gated_forward_workspace_size": (_SZ, [_I64, _I64, _I64, _I]),
+    "tpmlp_gated_forward_workspace_size": (_SZ, [_I64, _I64, _I64, _I, _I]),
     "tpmlp_gated_forward": (_I, [_P] * 6 + [_I64, _I64, _I64, _I, _I, _I, _P, _SZ, _P]),
-    "tpmlp_gated_backward_workspace_size": (_SZ, [_I64, _I64, _I]),
+    "tpmlp_gated_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I]),
     "tpmlp_gated_backward": (_I, [_P] * 9 + [_I64, _I64, _I64, _I, _I, _I, _I, _P, _SZ, _P]),
     "tpmlp_residual_norm": (_I, [_P] * 5 + [_F, _F, _P, _P, _I64, _I64, _I64, _I, _P]),
     "tpmlp_residual_norm_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I]),
@@ -734,7 +734,7 @@ def gated_forward(X, A, B, t: int = 1, act: str = "silu", save: bool = True, str
         O = torch.empty((n, d), dtype=X.dtype, device=device)
         Z = torch.empty((n, 2 * m), dtype=X.dtype, device=device) if save else None
         Y = torch.empty((n, m), dtype=X.dtype, device=device)
-        ws_bytes = lib.tpmlp_gated_forward_workspace_size(n, d, m, dt)
+        ws_bytes = lib.tpmlp_gated_forward_workspace_size(n, d, m, t, dt)
         ws, ws_ptr = _scratch(ws_bytes, device)
         _check(lib.tpmlp_gated_forward(X.data_ptr(), A.data_ptr(), B.data_ptr(), O.data_ptr(), _ptr(Z), Y.data_ptr(), n, d,
                                        m, t, GATE_ACT[act], dt, ws_ptr, ws_bytes, st))
@@ -765,7 +765,7 @@ def gated_backward(X, A, B, G, Z, Y, t: int = 1, act: str = "silu", wgrad: str =
         dX = torch.empty((n, d), dtype=dtype, device=device)
         dA = torch.empty((d, 2 * m), dtype=wtype, device=device) if dA is None else dA
         dB = torch.empty((m, d), dtype=wtype, device=device) if dB is None else dB
-        ws_bytes = lib.tpmlp_gated_backward_workspace_size(n, m, dt)
+        ws_bytes = lib.tpmlp_gated_backward_workspace_size(n, d, m, dt)
         ws, ws_ptr = _scratch(ws_bytes, device)
         _check(lib.tpmlp_gated_backward(X.data_ptr(), A.data_ptr(), B.data_ptr(), G.data_ptr(), Z.data_ptr(), Y.data_ptr(),
                                         dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), n, d, m, t, act_kind, mode, dt,

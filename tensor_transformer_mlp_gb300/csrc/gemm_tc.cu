@@ -2320,6 +2320,8 @@ cudaError_t make_batched_map(void* map, const BatchedOperand& op, int64_t nz1, i
                            &slots[2]);
 }
 
+bool few_rows_allowed() { return pair_kernel_choice() == 1; }
+
 void set_gemm_variant(int pair_kernel, int pair_pacing, int pair_group) {
   g_pair_kernel.store(pair_kernel, std::memory_order_relaxed);
   g_pair_pacing.store(pair_pacing, std::memory_order_relaxed);

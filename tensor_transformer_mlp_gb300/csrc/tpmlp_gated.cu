@@ -32,6 +32,16 @@ EpiParams plain(void* out, int64_t ldo) {
   return ep;
 }
 
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Workspaces of the products that may run with few rows: one after another in the forward.
+size_t fc1_bytes(int64_t n, int64_t d, int64_t m, int t) {
+  return gated_fc1_takes_few_rows(n, d, m) ? round256(gated_fc1_few_rows_workspace(n, d, m, t)) : 0;
+}
+size_t rows_bytes(int64_t n, int64_t cols, int64_t k) {
+  return gemm_takes_few_rows(n, cols, k) ? round256(gemm_few_rows_workspace(n, cols, k)) : 0;
+}
+
 size_t dz_bytes(int64_t n, int64_t m) { return n <= 0 || m <= 0 ? 0 : (static_cast<size_t>(n) * m * 4 + 255) / 256 * 256; }
 
 }  // namespace
@@ -41,9 +51,9 @@ using namespace tpmlp;
 
 extern "C" {
 
-size_t tpmlp_gated_forward_workspace_size(int64_t n, int64_t d, int64_t m, tpmlp_dtype dt) {
-  (void)n, (void)d, (void)m, (void)dt;
-  return 0;
+size_t tpmlp_gated_forward_workspace_size(int64_t n, int64_t d, int64_t m, int t, tpmlp_dtype dt) {
+  if (n <= 0 || check_gated_shape(n, d, m, t, TPMLP_GATE_SILU, dt) != TPMLP_OK) return 0;
+  return fc1_bytes(n, d, m, t) + rows_bytes(n, d, m);
 }
 
 tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, void* O, void* Z_save, void* Y_save,
@@ -54,7 +64,7 @@ tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, vo
   if (n == 0) return TPMLP_OK;
   TPMLP_PASS(check_ptrs({X, O, Y_save}, 16, "pointers must be 16-byte aligned"));
   if (!aligned(Z_save, 16)) return err(TPMLP_ERR_ALIGN, "pointers must be 16-byte aligned");
-  const size_t need = tpmlp_gated_forward_workspace_size(n, d, m, dt);
+  const size_t need = tpmlp_gated_forward_workspace_size(n, d, m, t, dt);
   if (need > 0 && (!workspace || ws_bytes < need)) return err(TPMLP_ERR_WORKSPACE, "gated forward workspace too small");
   if (need > 0 && !aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
   if (any_overlap({matrix(O, n, d), matrix(Z_save, n, 2 * m), matrix(Y_save, n, m),
@@ -64,16 +74,27 @@ tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, vo
   DeviceCtx ctx;
   TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  TPMLP_PASS_CUDA(gated_fc1_tc(X, A, Z_save, Y_save, n, d, m, t, act, st, ctx), "gated FC1 GEMM");
-  TPMLP_PASS_CUDA(gemm_bf16_tc(n, d, m, Operand{Y_save, n, m, m, false}, Operand{B, m, d, d, true}, kEpiStore, plain(O, d),
-                               st, ctx),
-                  "gated FC2 GEMM");
+  const bool few = few_rows_allowed(), few1 = few && gated_fc1_takes_few_rows(n, d, m);
+  if (few1) {
+    TPMLP_PASS_CUDA(gated_fc1_few_rows(X, A, Z_save, Y_save, n, d, m, t, act, workspace, st, ctx), "gated FC1, few rows");
+  } else {
+    TPMLP_PASS_CUDA(gated_fc1_tc(X, A, Z_save, Y_save, n, d, m, t, act, st, ctx), "gated FC1 GEMM");
+  }
+  if (few && gemm_takes_few_rows(n, d, m)) {
+    TPMLP_PASS_CUDA(gemm_few_rows(Y_save, B, true, O, n, d, m, static_cast<char*>(workspace) + fc1_bytes(n, d, m, t), few1, st,
+                                  ctx),
+                    "gated FC2, few rows");
+  } else {
+    TPMLP_PASS_CUDA(gemm_bf16_tc(n, d, m, Operand{Y_save, n, m, m, false}, Operand{B, m, d, d, true}, kEpiStore, plain(O, d),
+                                 st, ctx),
+                    "gated FC2 GEMM");
+  }
   return TPMLP_OK;
 }
 
-size_t tpmlp_gated_backward_workspace_size(int64_t n, int64_t m, tpmlp_dtype dt) {
-  (void)dt;
-  return dz_bytes(n, m);
+size_t tpmlp_gated_backward_workspace_size(int64_t n, int64_t d, int64_t m, tpmlp_dtype dt) {
+  if (n <= 0 || check_gated_shape(n, d, m, 1, TPMLP_GATE_SILU, dt) != TPMLP_OK) return 0;
+  return dz_bytes(n, m) + rows_bytes(n, d, 2 * m);
 }
 
 tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, const void* G, const void* Z_save,
@@ -94,7 +115,7 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, c
     return TPMLP_OK;
   }
   TPMLP_PASS(check_ptrs({X, G, Z_save, Y_save, dX}, 16, "pointers must be 16-byte aligned"));
-  const size_t need = dz_bytes(n, m);
+  const size_t need = tpmlp_gated_backward_workspace_size(n, d, m, dt);
   if (!workspace || ws_bytes < need) return err(TPMLP_ERR_WORKSPACE, "gated backward workspace too small");
   if (!aligned(workspace, 256)) return err(TPMLP_ERR_ALIGN, "workspace not 256-byte aligned");
   if (any_overlap({matrix(dX, n, d), matrix(dA, d, 2 * m, size), matrix(dB, m, d, size),
@@ -114,6 +135,12 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, c
                                plain(dA, 2 * m), st, ctx),
                   "gated wgrad-1 GEMM");
   // both projections' shares of dX are one sum over the 2 m columns of D
+  if (few_rows_allowed() && gemm_takes_few_rows(n, d, 2 * m)) {
+    TPMLP_PASS_CUDA(gemm_few_rows(workspace, A, false, dX, n, d, 2 * m, static_cast<char*>(workspace) + dz_bytes(n, m), false, st,
+                                  ctx),
+                    "gated dgrad-2, few rows");
+    return TPMLP_OK;
+  }
   TPMLP_PASS_CUDA(gemm_bf16_tc(n, d, 2 * m, Operand{workspace, n, 2 * m, 2 * m, false}, Operand{A, d, 2 * m, 2 * m, false},
                                kEpiStore, plain(dX, d), st, ctx),
                   "gated dgrad-2 GEMM");

@@ -154,6 +154,20 @@ cudaError_t gated_fc1_tc(const void* x, const void* a, void* z, void* y, int64_t
 cudaError_t gated_dgrad1_tc(const void* g, const void* b, const void* z, void* dz, int64_t n, int64_t d, int64_t m, int t,
                             int act, cudaStream_t stream, const DeviceCtx& ctx);
 
+// The same for few tokens, with the sum over K split across the SMs (gemm_few_rows.cu), where it is the faster one:
+// gated_fc1_few_rows as gated_fc1_tc; gemm_few_rows: out [n][cols] = tokens [n][k] W, W stored [k][cols] (w_mn) or
+// [cols][k], bf16. `dependent`: the kernel in front on the stream is this file's, and only `tokens` depends on it. Workspaces
+// 256-byte aligned, their sizes independent of the device.
+bool few_rows_allowed();  // by tpmlp_set_gemm_variant: the per-product choice is on
+bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m);
+size_t gated_fc1_few_rows_workspace(int64_t n, int64_t d, int64_t m, int t);
+cudaError_t gated_fc1_few_rows(const void* x, const void* a, void* z, void* y, int64_t n, int64_t d, int64_t m, int t, int act,
+                               void* workspace, cudaStream_t stream, const DeviceCtx& ctx);
+bool gemm_takes_few_rows(int64_t n, int64_t cols, int64_t k);
+size_t gemm_few_rows_workspace(int64_t n, int64_t cols, int64_t k);
+cudaError_t gemm_few_rows(const void* tokens, const void* w, bool w_mn, void* out, int64_t n, int64_t cols, int64_t k,
+                          void* workspace, bool dependent, cudaStream_t stream, const DeviceCtx& ctx);
+
 // Batched bf16 tensor-core GEMM: C_z = alpha * Aop_z(M x K) * Bop_z(K x N) for every batch index;
 // epilogues kEpiStore (bf16) and kEpiStoreF32, written at ep.out + out offsets of z.
 cudaError_t gemm_bf16_tc_batched(int64_t M, int64_t N, int64_t K, const BatchedOperand& a, const BatchedOperand& b,

@@ -80,7 +80,7 @@ def fwd(lib, X=AT[0], A=AT[1], B=AT[2], O=AT[3], Z=AT[4], Y=AT[5], n=256, d=512,
 def bwd(lib, X=AT[0], A=AT[1], B=AT[2], G=AT[3], Z=AT[4], Y=AT[5], dX=AT[6], dA=AT[7], dB=AT[8], n=256, d=512, m=1024, t=2,
         act=2, wgrad=0, dt=BF16, ws=AT[9], ws_bytes=None):
     if ws_bytes is None:
-        ws_bytes = lib.tpmlp_gated_backward_workspace_size(n, m, dt)
+        ws_bytes = lib.tpmlp_gated_backward_workspace_size(n, d, m, dt)
     return lib.tpmlp_gated_backward(X, A, B, G, Z, Y, dX, dA, dB, n, d, m, t, act, wgrad, dt, ws, ws_bytes, None)
 
 
@@ -111,7 +111,7 @@ def test_backward_refusals_of_its_own(lib):
     assert bwd(lib, wgrad=3) == INVALID and bwd(lib, wgrad=-1) == INVALID
     for name in ("G", "Z", "dX", "dA", "dB"):
         assert bwd(lib, **{name: None}) == INVALID, name
-    need = lib.tpmlp_gated_backward_workspace_size(256, 1024, BF16)
+    need = lib.tpmlp_gated_backward_workspace_size(256, 512, 1024, BF16)
     assert need >= 256 * 2048 * 2
     assert bwd(lib, ws_bytes=need - 1) == WORKSPACE and bwd(lib, ws=None) == WORKSPACE
     assert bwd(lib, ws=AT[9] + 16) == ALIGN
@@ -126,8 +126,8 @@ def test_no_tokens(lib):
     assert fwd(lib, n=0, X=None, O=None, Z=None, Y=None, ws=None, ws_bytes=0) == OK
     assert fwd(lib, n=0, A=None) == INVALID
     assert bwd(lib, n=0, X=None, G=None, Z=None, Y=None, dX=None, ws=None, ws_bytes=0, wgrad=1) == OK
-    assert lib.tpmlp_gated_backward_workspace_size(0, 64, BF16) == 0
-    assert lib.tpmlp_gated_forward_workspace_size(0, 64, 64, BF16) == 0
+    assert lib.tpmlp_gated_backward_workspace_size(0, 64, 64, BF16) == 0
+    assert lib.tpmlp_gated_forward_workspace_size(0, 64, 64, 1, BF16) == 0
 
 
 def test_python_refusals():
