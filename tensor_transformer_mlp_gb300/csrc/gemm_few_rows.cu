@@ -29,26 +29,29 @@ constexpr int kBoxBytes = 64 * kBK * 2;  // one 64 x 64 box of weights stored [K
 constexpr int kMaxStages = 6;
 constexpr int kSmemBudget = 220 * 1024;
 constexpr int kBarrierBytes = 256;
-constexpr int kThreads = 192;           // producer, MMA issuer, four epilogue warps
+constexpr int kThreads = 320;           // producer, MMA issuer, eight epilogue warps
 constexpr int kSms = 152;               // what splits and workspaces are chosen for, with or without a device
-constexpr int kMaxItems = 4 * kSms;
+constexpr int kMaxItems = 4 * kSms;     // CTAs' shares of a product
 
 struct Plan {
   int n, cols, num_kb;   // tokens, output columns (of Y for the gate), k-blocks
   int nt, token_tiles;   // tokens of a tile (a multiple of 16) and tiles of them
   int col_tiles, tiles, splits, items, ctas;  // items = tiles * splits
   int shard, unit;       // the gated block's columns (EpiParams), 0: plain
+  int ranks;             // CTAs of a tile: 2 are a pair of SMs that take half of the tokens in each
   int stages;
 };
 
-__host__ __device__ __forceinline__ int plan_stage_bytes(const Plan& p) { return kWeightBytes + p.nt * kBK * 2; }
+__host__ __device__ __forceinline__ int plan_stage_bytes(const Plan& p) { return kWeightBytes + p.nt / p.ranks * kBK * 2; }
 
-// Tile -> its first column and token. Tiles of the same columns are neighbours: their weights meet in L2.
+// Tile -> its first column and token. Tiles of the same columns are neighbours: their weights meet in L2. A CTA of a
+// tile takes 256 columns of the weights: 256 of the output, or 128 (gate and up) of Y.
+__host__ __device__ __forceinline__ int cta_columns(const Plan& p) { return p.shard ? kBlock : kTileCols; }
 __device__ __forceinline__ int tile_column(const Plan& p, int tile) {
-  const int ct = tile / p.token_tiles;
-  if (!p.shard) return ct * kTileCols;
-  const int per = (p.unit + kBlock - 1) / kBlock;
-  return ct / per * p.unit + ct % per * kBlock;
+  const int ct = tile / p.token_tiles, w = cta_columns(p) * p.ranks;
+  if (!p.shard) return ct * w;
+  const int per = (p.unit + w - 1) / w;
+  return ct / per * p.unit + ct % per * w;
 }
 __device__ __forceinline__ int tile_token(const Plan& p, int tile) { return tile % p.token_tiles * p.nt; }
 
@@ -61,10 +64,10 @@ struct Walk {
     kb = static_cast<int>(static_cast<int64_t>(split) * p.num_kb / p.splits);
     end = static_cast<int>(static_cast<int64_t>(split + 1) * p.num_kb / p.splits);
   }
-  __device__ __forceinline__ explicit Walk(const Plan& p) : item(blockIdx.x), tile(0), kb(0), end(0) { enter(p); }
+  __device__ __forceinline__ explicit Walk(const Plan& p) : item(blockIdx.x / p.ranks), tile(0), kb(0), end(0) { enter(p); }
   __device__ __forceinline__ bool more(const Plan& p) const { return item < p.items; }
   __device__ __forceinline__ void next_item(const Plan& p) {
-    item += p.ctas;
+    item += p.ctas / p.ranks;
     if (item < p.items) enter(p);
   }
   __device__ __forceinline__ void next(const Plan& p) {
@@ -72,7 +75,11 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ float gate_f(float g, int act) { return act == kGateSilu ? g * sigmoid_fast(g) : gelu_f<false>(g, act); }
+// act(g) u; the forms other than silu out of line, as their code would be there 32 times.
+__device__ __noinline__ float gate_other(float g, float u, int act) { return gelu_f<false>(g, act) * u; }
+__device__ __forceinline__ float gate_f(float g, float u, int act) {
+  return act == kGateSilu ? g * sigmoid_fast(g) * u : gate_other(g, u, act);
+}
 
 // What a product leaves: plain: out[n][cols]; gate: out = Y [n][cols], z [n][2 cols] or null. slots (more than one split):
 // [items][nt][256] fp32.
@@ -82,7 +89,10 @@ struct Outputs {
   int act;
 };
 
-template <bool W_MN, bool GATE>
+// PAIR: a cluster of two CTAs on two SMs works on a tile (tcgen05 cta_group::2): each has its own 256 weight columns and
+// half of the tokens in shared memory, and all tokens in its accumulators, so that a token tile enters an SM only half.
+// Barriers as in the SM-pair GEMM (gemm_tc.cu): full and tempty in the even CTA, empty and tfull in both.
+template <bool W_MN, bool GATE, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_t,
                     const __grid_constant__ Plan p, const __grid_constant__ Outputs o, unsigned int* status) {
@@ -96,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int ntp = (p.nt + 31) & ~31;              // accumulator columns of a block of 128 weight columns
   const int sets = ntp <= 128 ? 2 : 1;            // of two blocks each
   uint32_t tmem_cols = 64;
@@ -108,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 128);
+      mbar_init(&tempty[a], PAIR ? 512 : 256);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -116,21 +127,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmap_t);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, tmem_cols);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, tmem_cols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, tmem_cols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR)
+    cluster_sync_all();
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.launch_dependents;");
 
   if (warp == 0) {
     if (lane == 0) {
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, int s, int x, int y) {
+        if constexpr (PAIR)
+          tma_load_2d_pair(dst, map, map_to_cta(&full[s], 0), x, y);
+        else
+          tma_load_2d(dst, map, &full[s], x, y);
+      };
       auto load_weights = [&](const Walk& at, int s) {
-        const int col = tile_column(p, at.tile), kb = at.kb;
+        const int col = tile_column(p, at.tile) + rank * cta_columns(p), kb = at.kb;
         uint8_t* dst = smem + s * stage_bytes;
-        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], p.ranks * stage_bytes);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           if constexpr (W_MN) {
@@ -141,15 +166,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int y = col + j * 64;
                 c = y + (y / p.shard + b) * p.shard;
               }
-              tma_load_2d(dst + (2 * b + j) * kBoxBytes, &tmap_w, &full[s], c, kb * kBK);
+              load(dst + (2 * b + j) * kBoxBytes, &tmap_w, s, c, kb * kBK);
             }
           } else {
-            tma_load_2d(dst + 2 * b * kBoxBytes, &tmap_w, &full[s], kb * kBK, col + b * kBlock);
+            load(dst + 2 * b * kBoxBytes, &tmap_w, s, kb * kBK, col + b * kBlock);
           }
         }
       };
       auto load_tokens = [&](const Walk& at, int s) {
-        tma_load_2d(smem + s * stage_bytes + kWeightBytes, &tmap_t, &full[s], at.kb * kBK, tile_token(p, at.tile));
+        load(smem + s * stage_bytes + kWeightBytes, &tmap_t, s, at.kb * kBK, tile_token(p, at.tile) + rank * (p.nt / 2));
       };
       // The weights are there before the kernel in front has ended; the tokens may be what it writes.
       Walk w(p), tok(p);
@@ -163,12 +188,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_weights(w, s);
         load_tokens(w, s);
       }
-      if (w.more(p))  // copies still in flight
+      // The even CTA's full barriers count both CTAs' copies: none is in flight when it leaves (at once on the normal path).
+      if (rank == 0 && (PAIR || w.more(p)))
         for (int i = max(0, it - stages); i < it; ++i) mbar_wait(&full[i % stages], (i / stages) & 1, status, 72);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kBlock, p.nt, W_MN, false);
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(PAIR ? 2 * kBlock : kBlock, p.nt, W_MN, false);
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (PAIR)
+          umma_commit_pair_mc(bar, 0x3);
+        else
+          umma_commit(bar);
+      };
       int it = 0, seg = 0;
       bool ok = true;
       for (Walk at(p); at.more(p) && ok; at.next_item(p), ++seg) {
@@ -191,91 +223,115 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < 2; ++b) {
               const uint32_t wb = w + 2 * b * kBoxBytes;
               const uint64_t wdesc = W_MN ? smem_desc_sw128(wb + kk * 2048, kBoxBytes, 1024) : smem_desc_sw128(wb + kk * 32, 16, 1024);
-              umma_bf16(d + static_cast<uint32_t>(b * ntp), wdesc, tdesc, idesc, at.kb != first || kk != 0 ? 1u : 0u);
+              const uint32_t acc = at.kb != first || kk != 0 ? 1u : 0u;
+              if constexpr (PAIR)
+                umma_bf16_pair(d + static_cast<uint32_t>(b * ntp), wdesc, tdesc, idesc, acc);
+              else
+                umma_bf16(d + static_cast<uint32_t>(b * ntp), wdesc, tdesc, idesc, acc);
             }
           }
-          umma_commit(&empty[s]);
+          commit(&empty[s]);
         }
-        if (ok) umma_commit(&tfull[set]);
+        if (ok) commit(&tfull[set]);
       }
-      umma_commit(drain);
+      if constexpr (PAIR)
+        umma_commit_pair(drain);
+      else
+        umma_commit(drain);
       mbar_wait(drain, 0, status, 75);
     }
   } else {
-    // A thread has one weight column of each block and all tokens: for one token, a warp's 32 lanes write 128 bytes of
-    // a slot, or 64 of the outputs.
+    // A thread has one weight column of each block and every other 32 tokens: for one token, a warp's 32 lanes write 128
+    // bytes of a slot, or 64 of the outputs.
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what is written may still be read by what ran before
-    const int q = warp & 3;
+    const int q = warp & 3, t_first = (warp - 2) / 4 * 32;
+    // f(i) for the tokens i < n of 32, without a test for each where all are there
+    auto each = [](int n, auto&& f) {
+      if (n >= 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f(i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < n) f(i);
+      }
+    };
     int seg = 0;
     for (Walk at(p); at.more(p); at.next_item(p), ++seg) {
       const int set = seg % sets;
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[set], (seg / sets) & 1, status, 76))) break;
       tc_fence_after();
-      const int token0 = tile_token(p, at.tile), tokens = min(p.nt, p.n - token0), col0 = tile_column(p, at.tile);
+      const int token0 = tile_token(p, at.tile), tokens = min(p.nt, p.n - token0);
+      const int tile_col = tile_column(p, at.tile), col0 = tile_col + rank * cta_columns(p) + q * 32 + lane;
       const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(set * 2 * ntp);
-      if (p.splits > 1) {
-        float* out = o.slots + static_cast<int64_t>(at.item) * p.nt * kTileCols + q * 32 + lane;
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll 1
-          for (int t0 = 0; t0 < tokens; t0 += 32) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(b * ntp + t0), v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (t0 + i < tokens) out[(t0 + i) * kTileCols + b * kBlock] = __uint_as_float(v[i]);
-          }
-        }
-      } else if constexpr (GATE) {
-        const int y = col0 + q * 32 + lane;
-        const bool in = y / p.unit == col0 / p.unit;
-        __nv_bfloat16* out = o.out + static_cast<int64_t>(token0) * p.cols + y;
-        __nv_bfloat16* z = o.z ? o.z + static_cast<int64_t>(token0) * 2 * p.cols + y + static_cast<int64_t>(y / p.shard) * p.shard : nullptr;
-#pragma unroll 1
-        for (int t0 = 0; t0 < tokens; t0 += 32) {
-          uint32_t g[32], u[32];
-          tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(t0), g);
-          tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(ntp + t0), u);
-          tmem_ld_wait();
-          if (!in) continue;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (t0 + i >= tokens) break;
-            const float gi = __uint_as_float(g[i]), ui = __uint_as_float(u[i]);
-            out[static_cast<int64_t>(t0 + i) * p.cols] = __float2bfloat16_rn(gate_f(gi, o.act) * ui);
-            if (z) {
-              z[static_cast<int64_t>(t0 + i) * 2 * p.cols] = __float2bfloat16_rn(gi);
-              z[static_cast<int64_t>(t0 + i) * 2 * p.cols + p.shard] = __float2bfloat16_rn(ui);
+      for (int t0 = t_first; t0 < tokens; t0 += 64) {
+        uint32_t a[32], b[32];
+        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(t0), a);
+        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(ntp + t0), b);
+        tmem_ld_wait();
+        const int64_t token = token0 + t0;
+        if (p.splits > 1) {
+          float* out = o.slots + ((static_cast<int64_t>(at.item) * p.ranks + rank) * p.nt + t0) * kTileCols + q * 32 + lane;
+          each(tokens - t0, [&](int i) {
+            out[i * kTileCols] = __uint_as_float(a[i]);
+            out[i * kTileCols + kBlock] = __uint_as_float(b[i]);
+          });
+        } else if constexpr (GATE) {
+          if (col0 / p.unit == tile_col / p.unit) {
+            __nv_bfloat16* out = o.out + token * p.cols + col0;
+            if (o.act == kGateSilu) {
+              each(tokens - t0, [&](int i) {
+                const float g = __uint_as_float(a[i]);
+                *out = __float2bfloat16_rn(g * sigmoid_fast(g) * __uint_as_float(b[i]));
+                out += p.cols;
+              });
+            } else {
+              each(tokens - t0, [&](int i) {
+                *out = __float2bfloat16_rn(gate_other(__uint_as_float(a[i]), __uint_as_float(b[i]), o.act));
+                out += p.cols;
+              });
+            }
+            if (o.z) {
+              __nv_bfloat16* z = o.z + token * 2 * p.cols + col0 + static_cast<int64_t>(col0 / p.shard) * p.shard;
+              each(tokens - t0, [&](int i) {
+                z[0] = __float2bfloat16_rn(__uint_as_float(a[i]));
+                z[p.shard] = __float2bfloat16_rn(__uint_as_float(b[i]));
+                z += 2 * p.cols;
+              });
             }
           }
-        }
-      } else {
-#pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-          const int col = col0 + b * kBlock + q * 32 + lane;
-          __nv_bfloat16* out = o.out + static_cast<int64_t>(token0) * p.cols + col;
-#pragma unroll 1
-          for (int t0 = 0; t0 < tokens; t0 += 32) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(b * ntp + t0), v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (t0 + i < tokens && col < p.cols) out[static_cast<int64_t>(t0 + i) * p.cols] = __float2bfloat16_rn(__uint_as_float(v[i]));
-          }
+        } else {
+          __nv_bfloat16* out = o.out + token * p.cols + col0;
+          const bool in0 = col0 < p.cols, in1 = col0 + kBlock < p.cols;
+          each(tokens - t0, [&](int i) {
+            if (in0) out[0] = __float2bfloat16_rn(__uint_as_float(a[i]));
+            if (in1) out[kBlock] = __float2bfloat16_rn(__uint_as_float(b[i]));
+            out += p.cols;
+          });
         }
       }
       tc_fence_before();
-      mbar_arrive(&tempty[set]);
+      if constexpr (PAIR)
+        mbar_arrive_cluster(map_to_cta(&tempty[set], 0));
+      else
+        mbar_arrive(&tempty[set]);
     }
   }
+  // Neither CTA of a pair leaves while the other may still signal its barriers.
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if constexpr (PAIR)
+    cluster_sync_all();
+  else
+    __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, tmem_cols);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, tmem_cols);
+    else
+      tmem_dealloc(tmem, tmem_cols);
   }
 }
 
@@ -303,20 +359,21 @@ __global__ void __launch_bounds__(256) few_rows_join_kernel(const __grid_constan
   const int quad = static_cast<int>(item % kQuads);
   const int64_t rest = item / kQuads;
   const int ct = static_cast<int>(rest / p.n), token = static_cast<int>(rest - static_cast<int64_t>(ct) * p.n);
-  if (ct >= p.col_tiles) return;
-  const int ti = token / p.nt, tile = ct * p.token_tiles + ti;
-  const int col0 = tile_column(p, tile), col = col0 + quad * 4;
+  if (ct >= p.col_tiles * p.ranks) return;
+  const int ti = token / p.nt, tile = ct / p.ranks * p.token_tiles + ti, rank = ct % p.ranks;
+  const int col0 = tile_column(p, tile), col = col0 + rank * cta_columns(p) + quad * 4;
   if (GATE ? col / p.unit != col0 / p.unit : col >= p.cols) return;
   const int64_t share = static_cast<int64_t>(p.nt) * kTileCols;
-  const float* src = o.slots + tile * share + (token - ti * p.nt) * kTileCols + quad * 4;
-  const float4 a = sum_shares(src, p.splits, p.tiles * share);
+  const float* src = o.slots + (static_cast<int64_t>(tile) * p.ranks + rank) * share + (token - ti * p.nt) * kTileCols + quad * 4;
+  const int64_t stride = p.ranks * p.tiles * share;
+  const float4 a = sum_shares(src, p.splits, stride);
   uint2* out = reinterpret_cast<uint2*>(o.out + static_cast<int64_t>(token) * p.cols + col);
   if constexpr (!GATE) {
     *out = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   } else {
-    const float4 u = sum_shares(src + kBlock, p.splits, p.tiles * share);
-    *out = make_uint2(pack_bf16x2(gate_f(a.x, o.act) * u.x, gate_f(a.y, o.act) * u.y),
-                      pack_bf16x2(gate_f(a.z, o.act) * u.z, gate_f(a.w, o.act) * u.w));
+    const float4 u = sum_shares(src + kBlock, p.splits, stride);
+    *out = make_uint2(pack_bf16x2(gate_f(a.x, u.x, o.act), gate_f(a.y, u.y, o.act)),
+                      pack_bf16x2(gate_f(a.z, u.z, o.act), gate_f(a.w, u.w, o.act)));
     if (o.z) {
       __nv_bfloat16* row = o.z + static_cast<int64_t>(token) * 2 * p.cols + col + static_cast<int64_t>(col / p.shard) * p.shard;
       *reinterpret_cast<uint2*>(row) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
@@ -327,52 +384,53 @@ __global__ void __launch_bounds__(256) few_rows_join_kernel(const __grid_constan
 
 // ---------------------------------------------------------------------- host side
 
-// Estimated time of a product with `splits` splits, in us: rounds of items, each k-block at the slowest of the weights' share
-// of HBM (6.7 TB/s), the tensor core (12.7 TFLOP/s an SM) and what an SM takes in (60 KB a us); the shares' way to L2 and
-// back (8 TB/s) and the second kernel.
-double split_time(const Plan& p, int splits, int sms) {
-  const double items = static_cast<double>(p.tiles) * splits, busy = std::min<double>(items, sms);
-  const double kb = std::max({kWeightBytes * busy / 6.7e6, 2.0 * kTileCols * p.nt * kBK / 12.7e6, plan_stage_bytes(p) / 60e3});
-  const double rounds = std::ceil(items / sms), blocks = std::ceil(static_cast<double>(p.num_kb) / splits);
-  return rounds * (blocks * kb + 1.0) + (splits > 1 ? 3.0 + items * p.nt * kTileCols * 8.0 / 8e6 : 0.0);
+// Estimated time of a product, in us: rounds of items, each k-block at the slowest of the weights' share of HBM
+// (6.7 TB/s), the tensor core (12.7 TFLOP/s an SM) and what an SM takes in (83 KB a us: 200 and 256 tokens, K = 4096 to
+// 16384); what a round costs beside its k-blocks; the shares' way to L2 and back (8 TB/s) and the second kernel; the
+// launch of pairs.
+double plan_time(const Plan& p) {
+  const double ctas = static_cast<double>(p.items) * p.ranks, busy = std::min<double>(ctas, kSms);
+  const double kb = std::max({kWeightBytes * busy / 6.7e6, 2.0 * kTileCols * p.nt * kBK / 12.7e6, plan_stage_bytes(p) / 83e3});
+  const double rounds = std::ceil(ctas / kSms), blocks = std::ceil(static_cast<double>(p.num_kb) / p.splits);
+  return rounds * (blocks * kb + 1.0 + p.nt / 64.0) + (p.splits > 1 ? 3.0 + ctas * p.nt * kTileCols * 8.0 / 8e6 : 0.0) +
+         (p.ranks - 1) * 2.0;
 }
 
-void choose_splits(Plan* p, int sms) {
-  double best = split_time(*p, 1, sms);
-  p->splits = 1;
-  const int most = std::min(p->num_kb, std::max(1, kMaxItems / p->tiles));
-  for (int s = 2; s <= most; ++s) {
-    const double t = split_time(*p, s, sms);
-    if (t < best) {
-      best = t;
-      p->splits = s;
+// The plan with the least estimated time over single CTAs and pairs and the number of splits.
+Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool gate) {
+  Plan best{};
+  double best_time = 0;
+  for (int ranks = 1; ranks <= 2; ++ranks) {
+    Plan p{};
+    p.n = static_cast<int>(n);
+    p.cols = static_cast<int>(cols);
+    p.num_kb = static_cast<int>((k + kBK - 1) / kBK);
+    p.token_tiles = static_cast<int>((n + kMaxTokens - 1) / kMaxTokens);
+    p.nt = static_cast<int>(((n + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16);
+    p.ranks = ranks;
+    if (gate) {
+      p.shard = static_cast<int>(m / t);
+      p.unit = p.shard % 64 == 0 ? static_cast<int>(m) : p.shard;
+    }
+    const int64_t w = static_cast<int64_t>(cta_columns(p)) * ranks;
+    p.col_tiles = static_cast<int>(gate ? m / p.unit * ((p.unit + w - 1) / w) : (cols + w - 1) / w);
+    p.tiles = p.col_tiles * p.token_tiles;
+    p.stages = std::min<int>(kMaxStages, (kSmemBudget - kBarrierBytes - 1024) / plan_stage_bytes(p));
+    const int most = std::min(p.num_kb, std::max(1, kMaxItems / (p.tiles * ranks)));
+    for (p.splits = 1; p.splits <= most; ++p.splits) {
+      p.items = p.tiles * p.splits;
+      const double time = plan_time(p);
+      if (best.tiles == 0 || time < best_time) {
+        best = p;
+        best_time = time;
+      }
     }
   }
-}
-
-Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool gate) {
-  Plan p{};
-  p.n = static_cast<int>(n);
-  p.cols = static_cast<int>(cols);
-  p.num_kb = static_cast<int>((k + kBK - 1) / kBK);
-  p.token_tiles = static_cast<int>((n + kMaxTokens - 1) / kMaxTokens);
-  p.nt = static_cast<int>(((n + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16);
-  if (gate) {
-    p.shard = static_cast<int>(m / t);
-    p.unit = p.shard % 64 == 0 ? static_cast<int>(m) : p.shard;
-    p.col_tiles = static_cast<int>(m / p.unit * ((p.unit + kBlock - 1) / kBlock));
-  } else {
-    p.col_tiles = static_cast<int>((cols + kTileCols - 1) / kTileCols);
-  }
-  p.tiles = p.col_tiles * p.token_tiles;
-  choose_splits(&p, kSms);
-  p.items = p.tiles * p.splits;
-  p.stages = std::min<int>(kMaxStages, (kSmemBudget - kBarrierBytes - 1024) / plan_stage_bytes(p));
-  return p;
+  return best;
 }
 
 size_t slot_bytes(const Plan& p) {
-  return p.splits > 1 ? static_cast<size_t>(p.items) * p.nt * kTileCols * sizeof(float) : 0;
+  return p.splits > 1 ? static_cast<size_t>(p.items) * p.ranks * p.nt * kTileCols * sizeof(float) : 0;
 }
 
 cudaError_t encode_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, uint32_t box_rows) {
@@ -397,37 +455,55 @@ cudaError_t encode_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t c
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), int64_t ctas, int threads, int smem, bool dependent, cudaStream_t stream, A... args) {
+cudaError_t launch_after(void (*kernel)(P...), int64_t ctas, int cluster, int threads, int smem, bool dependent,
+                         cudaStream_t stream, A... args) {
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool W_MN, bool GATE>
-cudaError_t run(Plan p, const void* tokens, int64_t k, const void* w, int64_t w_rows, int64_t w_cols, const Outputs& o,
+template <bool W_MN, bool GATE, bool PAIR>
+cudaError_t run_ranks(Plan p, const void* tokens, int64_t k, const void* w, int64_t w_rows, int64_t w_cols, const Outputs& o,
                 bool dependent, cudaStream_t stream, const DeviceCtx& ctx) {
   CUtensorMap tw, tt;
   cudaError_t e = encode_2d(&tw, w, w_rows, w_cols, W_MN ? kBK : kBlock);
   if (e != cudaSuccess) return e;
-  if ((e = encode_2d(&tt, tokens, p.n, k, p.nt)) != cudaSuccess) return e;
+  if ((e = encode_2d(&tt, tokens, p.n, k, p.nt / p.ranks)) != cudaSuccess) return e;
   static SmemLimit limit;
-  auto kernel = few_rows_kernel<W_MN, GATE>;
+  auto kernel = few_rows_kernel<W_MN, GATE, PAIR>;
   if ((e = allow_smem(&limit, kernel, kSmemBudget, ctx)) != cudaSuccess) return e;
-  p.ctas = std::min(p.items, ctx.num_sms);
+  p.ctas = std::min(p.items, ctx.num_sms / p.ranks) * p.ranks;
   const int smem = p.stages * plan_stage_bytes(p) + kBarrierBytes + 1024;
-  if ((e = launch_after(kernel, p.ctas, kThreads, smem, dependent, stream, tw, tt, p, o, ctx.status)) != cudaSuccess) return e;
+  if ((e = launch_after(kernel, p.ctas, p.ranks, kThreads, smem, dependent, stream, tw, tt, p, o, ctx.status)) != cudaSuccess) return e;
   if (p.splits == 1) return cudaSuccess;
-  const int64_t threads = static_cast<int64_t>(p.col_tiles) * p.n * ((GATE ? kBlock : kTileCols) / 4);
-  return launch_after(few_rows_join_kernel<GATE>, (threads + 255) / 256, 256, 0, true, stream, p, o);
+  const int64_t threads = static_cast<int64_t>(p.col_tiles) * p.ranks * p.n * ((GATE ? kBlock : kTileCols) / 4);
+  return launch_after(few_rows_join_kernel<GATE>, (threads + 255) / 256, 1, 256, 0, true, stream, p, o);
+}
+
+template <bool W_MN, bool GATE>
+cudaError_t run(const Plan& p, const void* tokens, int64_t k, const void* w, int64_t w_rows, int64_t w_cols, const Outputs& o,
+                bool dependent, cudaStream_t stream, const DeviceCtx& ctx) {
+  return p.ranks == 2 ? run_ranks<W_MN, GATE, true>(p, tokens, k, w, w_rows, w_cols, o, dependent, stream, ctx)
+                      : run_ranks<W_MN, GATE, false>(p, tokens, k, w, w_rows, w_cols, o, dependent, stream, ctx);
 }
 
 }  // namespace
