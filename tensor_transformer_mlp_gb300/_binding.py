@@ -705,21 +705,27 @@ def masked_attention_backward(q, k, v, key_range, o, lse, do, scale: float | Non
 
 # ----------------------------------------------------------------------- gated feed-forward block
 
+def _matrix(t: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, name: str) -> None:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {[rows, cols]}")
+
+
 def _gated_args(X, A, B):
     n, d = X.shape
     m = B.shape[0]
     dtype = X.dtype
-    _dense(X, (n, d), dtype, "X")
-    _dense(A, (d, 2 * m), dtype, "A")
-    _dense(B, (m, d), dtype, "B")
+    _matrix(X, n, d, dtype, "X")
+    _matrix(A, d, 2 * m, dtype, "A")
+    _matrix(B, m, d, dtype, "B")
     return n, d, m, _dt(X)
 
 
-def _scratch(nbytes: int, device):
-    """A workspace of nbytes and its address; none for 0 bytes."""
+def _scratch(nbytes: int, like: torch.Tensor):
+    """A workspace of nbytes on like's device and its address; none for 0 bytes."""
     if nbytes == 0:
         return None, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
     return ws, ws.data_ptr()
 
 
@@ -730,12 +736,11 @@ def gated_forward(X, A, B, t: int = 1, act: str = "silu", save: bool = True, str
     lib = load_library()
     here, st = _where(_device(X, A, B), stream)
     with here:
-        device = X.device
-        O = torch.empty((n, d), dtype=X.dtype, device=device)
-        Z = torch.empty((n, 2 * m), dtype=X.dtype, device=device) if save else None
-        Y = torch.empty((n, m), dtype=X.dtype, device=device)
+        O = torch.empty_like(X)
+        Z = X.new_empty(n, 2 * m) if save else None
+        Y = X.new_empty(n, m)
         ws_bytes = lib.tpmlp_gated_forward_workspace_size(n, d, m, t, dt)
-        ws, ws_ptr = _scratch(ws_bytes, device)
+        ws, ws_ptr = _scratch(ws_bytes, X)
         _check(lib.tpmlp_gated_forward(X.data_ptr(), A.data_ptr(), B.data_ptr(), O.data_ptr(), _ptr(Z), Y.data_ptr(), n, d,
                                        m, t, GATE_ACT[act], dt, ws_ptr, ws_bytes, st))
     return O, Z, Y
@@ -747,26 +752,25 @@ def gated_backward(X, A, B, G, Z, Y, t: int = 1, act: str = "silu", wgrad: str =
     (dX, dA, dB)."""
     n, d, m, dt = _gated_args(X, A, B)
     dtype = X.dtype
-    _dense(G, (n, d), dtype, "G")
-    _dense(Z, (n, 2 * m), dtype, "Z")
-    _dense(Y, (n, m), dtype, "Y")
+    _matrix(G, n, d, dtype, "G")
+    _matrix(Z, n, 2 * m, dtype, "Z")
+    _matrix(Y, n, m, dtype, "Y")
     act_kind, mode = GATE_ACT[act], WGRAD[wgrad]
     wtype = dtype if wgrad == "operand" else torch.float32
     if wgrad == "f32_add" and (dA is None or dB is None):
         raise ValueError("f32_add needs dA and dB")
     if dA is not None:
-        _dense(dA, (d, 2 * m), wtype, "dA")
+        _matrix(dA, d, 2 * m, wtype, "dA")
     if dB is not None:
-        _dense(dB, (m, d), wtype, "dB")
+        _matrix(dB, m, d, wtype, "dB")
     lib = load_library()
     here, st = _where(_device(X, A, B, G, Z, Y, dA, dB), stream)
     with here:
-        device = X.device
-        dX = torch.empty((n, d), dtype=dtype, device=device)
-        dA = torch.empty((d, 2 * m), dtype=wtype, device=device) if dA is None else dA
-        dB = torch.empty((m, d), dtype=wtype, device=device) if dB is None else dB
+        dX = torch.empty_like(X)
+        dA = torch.empty_like(A, dtype=wtype) if dA is None else dA
+        dB = torch.empty_like(B, dtype=wtype) if dB is None else dB
         ws_bytes = lib.tpmlp_gated_backward_workspace_size(n, d, m, dt)
-        ws, ws_ptr = _scratch(ws_bytes, device)
+        ws, ws_ptr = _scratch(ws_bytes, X)
         _check(lib.tpmlp_gated_backward(X.data_ptr(), A.data_ptr(), B.data_ptr(), G.data_ptr(), Z.data_ptr(), Y.data_ptr(),
                                         dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), n, d, m, t, act_kind, mode, dt,
                                         ws_ptr, ws_bytes, st))
@@ -775,22 +779,35 @@ def gated_backward(X, A, B, G, Z, Y, t: int = 1, act: str = "silu", wgrad: str =
 
 # ----------------------------------------------------------------------- norms around a block
 
+def _gain(g: torch.Tensor, h: int, name: str) -> None:
+    if g.dim() != 1 or g.numel() != h or g.dtype is not torch.float32 or not g.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous torch.float32 tensor of shape {[h]}")
+
+
 def _residual_args(y, gamma_post, gate, gamma_pre):
     """(b, s, h) that the gate's rows divide the tokens of y [..., h] into."""
     shape = y.shape
     h = shape[-1]
-    for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
-        if g is not None:
-            _dense(g, (h,), torch.float32, name)
+    if gamma_post is not None:
+        _gain(gamma_post, h, "gamma_post")
+    if gamma_pre is not None:
+        _gain(gamma_pre, h, "gamma_pre")
     tokens = y.numel() // h if h else 0
-    if gate is None or gate.dim() == 1:
-        if gate is not None:
-            _dense(gate, (h,), torch.float32, "gate")
+    if gate is None:
+        return 1, tokens, h
+    if gate.dim() == 1:
+        _gain(gate, h, "gate")
         return 1, tokens, h
     if len(shape) < 3:
         raise ValueError("a gate of [b, h] needs tensors of [b, ..., h]")
-    _dense(gate, (shape[0], h), torch.float32, "gate")
-    return shape[0], tokens // shape[0] if shape[0] else 0, h
+    b = shape[0]
+    _matrix(gate, b, h, torch.float32, "gate")
+    return b, tokens // b if b else 0, h
+
+
+def _alike(t: torch.Tensor, shape: torch.Size, dtype: torch.dtype, name: str) -> None:
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
 
 
 def residual_norm(x, y, gamma_post=None, gate=None, gamma_pre=None, alpha: float = 1.0, eps: float = 1e-5, r=None, u=None,
@@ -799,13 +816,14 @@ def residual_norm(x, y, gamma_post=None, gate=None, gamma_pre=None, alpha: float
     Allocates r and u unless given (x or y for in place) and runs tpmlp_residual_norm. Returns (r, u), u None without
     gamma_pre."""
     shape, dtype = y.shape, y.dtype
-    _dense(y, shape, dtype, "y")
-    _dense(x, shape, dtype, "x")
-    if u is not None and gamma_pre is None:
-        raise ValueError("u needs gamma_pre")
-    for name, out in (("r", r), ("u", u)):
-        if out is not None:
-            _dense(out, shape, dtype, name)
+    _alike(y, shape, dtype, "y")
+    _alike(x, shape, dtype, "x")
+    if r is not None:
+        _alike(r, shape, dtype, "r")
+    if u is not None:
+        _alike(u, shape, dtype, "u")
+        if gamma_pre is None:
+            raise ValueError("u needs gamma_pre")
     b, s, h = _residual_args(y, gamma_post, gate, gamma_pre)
     dt = _dt(y)
     lib = load_library()
@@ -827,7 +845,7 @@ def residual_norm_backward(y, r, dr, du, gamma_post=None, gate=None, gamma_pre=N
     shape, dtype = like.shape, like.dtype
     for name, t in (("y", y), ("r", r), ("dr", dr), ("du", du), ("dx", dx), ("dy", dy)):
         if t is not None:
-            _dense(t, shape, dtype, name)
+            _alike(t, shape, dtype, name)
     b, s, h = _residual_args(like, gamma_post, gate, gamma_pre)
     dt = _dt(like)
     lib = load_library()
@@ -835,9 +853,11 @@ def residual_norm_backward(y, r, dr, du, gamma_post=None, gate=None, gamma_pre=N
     with here:
         dx = torch.empty_like(like) if dx is None else dx
         dy = torch.empty_like(like) if dy is None else dy
-        dpost, dgate, dpre = (None if g is None else torch.empty_like(g) for g in (gamma_post, gate, gamma_pre))
+        dpost = None if gamma_post is None else torch.empty_like(gamma_post)
+        dgate = None if gate is None else torch.empty_like(gate)
+        dpre = None if gamma_pre is None else torch.empty_like(gamma_pre)
         ws_bytes = lib.tpmlp_residual_norm_backward_workspace_size(b, s, h, gate is not None)
-        ws, ws_ptr = _scratch(ws_bytes, like.device)
+        ws, ws_ptr = _scratch(ws_bytes, like)
         _check(lib.tpmlp_residual_norm_backward(_ptr(y), _ptr(r), _ptr(dr), _ptr(du), _ptr(gamma_post), _ptr(gate),
                                                 _ptr(gamma_pre), alpha, eps, dx.data_ptr(), dy.data_ptr(), _ptr(dpost),
                                                 _ptr(dgate), _ptr(dpre), b, s, h, dt, ws_ptr, ws_bytes, st))

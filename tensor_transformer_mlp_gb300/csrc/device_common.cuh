@@ -110,6 +110,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// ------------------------------------------------------------------ programmatic dependent launches
+// grid_dependents_may_start: a kernel launched as this grid's programmatic dependent may be scheduled once every CTA has
+// come here. grid_wait_for_previous: such a kernel waits for the end of the grid in front, and for its memory, which every
+// thread that touches global memory (or issues a copy that does) does first. Without that attribute both do nothing.
+
+__device__ __forceinline__ void grid_dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void grid_wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.launch_dependents;");
+  grid_dependents_may_start();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk w(p), tok(p);
       int it = 0;
       for (; it < stages && w.more(p); ++it, w.next(p)) load_weights(w, it);
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      grid_wait_for_previous();
       for (int i = 0; i < it; ++i, tok.next(p)) load_tokens(tok, i);
       for (; w.more(p); ++it, w.next(p)) {
         const int s = it % stages;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // A thread has one weight column of each block and every other 32 tokens: for one token, a warp's 32 lanes write 128
     // bytes of a slot, or 64 of the outputs.
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what is written may still be read by what ran before
+    grid_wait_for_previous();  // what is written may still be read by what ran before
     const int q = warp & 3, t_first = (warp - 2) / 4 * 32;
     // f(i) for the tokens i < n of 32, without a test for each where all are there
     auto each = [](int n, auto&& f) {
@@ -335,43 +335,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The splits' shares of four columns of a tile, added in order: all of a thread's loads are independent.
-__device__ __forceinline__ float4 sum_shares(const float* src, int n, int64_t stride) {
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int c = 0; c < n; ++c) {
-    const float4 v = *reinterpret_cast<const float4*>(src + c * stride);
-    a.x += v.x;
-    a.y += v.y;
-    a.z += v.z;
-    a.w += v.w;
-  }
-  return a;
+// The second kernel: a quad of columns of one token is added up by `subs` threads (a power of two, in warps of their own),
+// thread i taking the shares i, i + subs, .. in order; then their sums are added in order. All loads of a thread are
+// independent of one another, and few, whatever the splits.
+constexpr int kJoinThreads = 256;
+// As many as the splits give two shares each, while the CTAs stay one wave (8 an SM).
+inline int join_subs(int splits, int64_t threads) {
+  int subs = 1;
+  while (subs < 8 && 4 * subs <= splits && 2 * subs * threads <= 8ll * kSms * kJoinThreads) subs *= 2;
+  return subs;
 }
 
-// A thread 4 columns of one token.
+__device__ __forceinline__ void add4(float4& a, const float4& v) {
+  a.x += v.x;
+  a.y += v.y;
+  a.z += v.z;
+  a.w += v.w;
+}
+
 template <bool GATE>
-__global__ void __launch_bounds__(256) few_rows_join_kernel(const __grid_constant__ Plan p, const __grid_constant__ Outputs o) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kJoinThreads) few_rows_join_kernel(const __grid_constant__ Plan p, const __grid_constant__ Outputs o,
+                                                                     int subs) {
+  grid_dependents_may_start();
+  grid_wait_for_previous();
   constexpr int kQuads = (GATE ? kBlock : kTileCols) / 4;
-  const int64_t item = blockIdx.x * 256ll + threadIdx.x;
+  __shared__ float4 sums[GATE ? 2 : 1][kJoinThreads];
+  const int here = kJoinThreads / subs, sub = threadIdx.x / here;  // quads of this CTA; 32 or more, so a warp has one sub
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * here + threadIdx.x % here;
   const int quad = static_cast<int>(item % kQuads);
   const int64_t rest = item / kQuads;
   const int ct = static_cast<int>(rest / p.n), token = static_cast<int>(rest - static_cast<int64_t>(ct) * p.n);
-  if (ct >= p.col_tiles * p.ranks) return;
   const int ti = token / p.nt, tile = ct / p.ranks * p.token_tiles + ti, rank = ct % p.ranks;
   const int col0 = tile_column(p, tile), col = col0 + rank * cta_columns(p) + quad * 4;
-  if (GATE ? col / p.unit != col0 / p.unit : col >= p.cols) return;
-  const int64_t share = static_cast<int64_t>(p.nt) * kTileCols;
-  const float* src = o.slots + (static_cast<int64_t>(tile) * p.ranks + rank) * share + (token - ti * p.nt) * kTileCols + quad * 4;
-  const int64_t stride = p.ranks * p.tiles * share;
-  const float4 a = sum_shares(src, p.splits, stride);
+  const bool in = ct < p.col_tiles * p.ranks && (GATE ? col / p.unit == col0 / p.unit : col < p.cols);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), u = a;
+  if (in) {
+    const int64_t share = static_cast<int64_t>(p.nt) * kTileCols, stride = p.ranks * p.tiles * share;
+    const float* src = o.slots + (static_cast<int64_t>(tile) * p.ranks + rank) * share + (token - ti * p.nt) * kTileCols + quad * 4;
+#pragma unroll 4
+    for (int c = sub; c < p.splits; c += subs) {
+      add4(a, *reinterpret_cast<const float4*>(src + c * stride));
+      if constexpr (GATE) add4(u, *reinterpret_cast<const float4*>(src + c * stride + kBlock));
+    }
+  }
+  if (subs > 1) {
+    sums[0][threadIdx.x] = a;
+    if constexpr (GATE) sums[1][threadIdx.x] = u;
+    __syncthreads();
+    if (sub > 0) return;
+    for (int i = 1; i < subs; ++i) {
+      add4(a, sums[0][threadIdx.x + i * here]);
+      if constexpr (GATE) add4(u, sums[1][threadIdx.x + i * here]);
+    }
+  }
+  if (!in) return;
   uint2* out = reinterpret_cast<uint2*>(o.out + static_cast<int64_t>(token) * p.cols + col);
   if constexpr (!GATE) {
     *out = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   } else {
-    const float4 u = sum_shares(src + kBlock, p.splits, stride);
     *out = make_uint2(pack_bf16x2(gate_f(a.x, u.x, o.act), gate_f(a.y, u.y, o.act)),
                       pack_bf16x2(gate_f(a.z, u.z, o.act), gate_f(a.w, u.w, o.act)));
     if (o.z) {
@@ -385,14 +406,14 @@ __global__ void __launch_bounds__(256) few_rows_join_kernel(const __grid_constan
 // ---------------------------------------------------------------------- host side
 
 // Estimated time of a product, in us: rounds of items, each k-block at the slowest of the weights' share of HBM
-// (6.7 TB/s), the tensor core (12.7 TFLOP/s an SM) and what an SM takes in (83 KB a us: 200 and 256 tokens, K = 4096 to
-// 16384); what a round costs beside its k-blocks; the shares' way to L2 and back (8 TB/s) and the second kernel; the
+// (6.7 TB/s), the tensor core (12.7 TFLOP/s an SM) and what an SM takes in (72 KB a us; measured 65 at 37 tokens and
+// K = 1024, 83 at 256 and K = 16384); what a round costs beside its k-blocks; the shares' way to L2 and back (8 TB/s) and the second kernel; the
 // launch of pairs.
 double plan_time(const Plan& p) {
   const double ctas = static_cast<double>(p.items) * p.ranks, busy = std::min<double>(ctas, kSms);
-  const double kb = std::max({kWeightBytes * busy / 6.7e6, 2.0 * kTileCols * p.nt * kBK / 12.7e6, plan_stage_bytes(p) / 83e3});
+  const double kb = std::max({kWeightBytes * busy / 6.7e6, 2.0 * kTileCols * p.nt * kBK / 12.7e6, plan_stage_bytes(p) / 72e3});
   const double rounds = std::ceil(ctas / kSms), blocks = std::ceil(static_cast<double>(p.num_kb) / p.splits);
-  return rounds * (blocks * kb + 1.0 + p.nt / 64.0) + (p.splits > 1 ? 3.0 + ctas * p.nt * kTileCols * 8.0 / 8e6 : 0.0) +
+  return rounds * (blocks * kb + 1.0 + p.nt / 64.0) + (p.splits > 1 ? 5.0 + ctas * p.nt * kTileCols * 8.0 / 8e6 : 0.0) +
          (p.ranks - 1) * 2.0;
 }
 
@@ -496,7 +517,8 @@ cudaError_t run_ranks(Plan p, const void* tokens, int64_t k, const void* w, int6
   if ((e = launch_after(kernel, p.ctas, p.ranks, kThreads, smem, dependent, stream, tw, tt, p, o, ctx.status)) != cudaSuccess) return e;
   if (p.splits == 1) return cudaSuccess;
   const int64_t threads = static_cast<int64_t>(p.col_tiles) * p.ranks * p.n * ((GATE ? kBlock : kTileCols) / 4);
-  return launch_after(few_rows_join_kernel<GATE>, (threads + 255) / 256, 1, 256, 0, true, stream, p, o);
+  const int subs = join_subs(p.splits, threads), here = kJoinThreads / subs;
+  return launch_after(few_rows_join_kernel<GATE>, (threads + here - 1) / here, 1, kJoinThreads, 0, true, stream, p, o, subs);
 }
 
 template <bool W_MN, bool GATE>
@@ -508,8 +530,14 @@ cudaError_t run(const Plan& p, const void* tokens, int64_t k, const void* w, int
 
 }  // namespace
 
-bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m) { return n <= 512; }
-bool gemm_takes_few_rows(int64_t n, int64_t cols, int64_t k) { return n <= 512 || ((n + 255) / 256) * ((cols + 255) / 256) <= 38; }
+// Against the SM-pair GEMM (gemm_tc.cu), whose launch takes some 7 us and 0.36 us a k-block for each wave of 256 x 256
+// tiles over 76 pairs.
+bool gemm_takes_few_rows(int64_t n, int64_t cols, int64_t k) {
+  const int64_t tiles = (n + 255) / 256 * ((cols + 255) / 256);
+  if (tiles > 76) return false;
+  return 5.0 + plan_time(make_plan(n, cols, k, 0, 1, false)) < 7.0 + 0.36 * static_cast<double>((k + kBK - 1) / kBK);
+}
+bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m) { return n <= kMaxTokens; }
 
 size_t gated_fc1_few_rows_workspace(int64_t n, int64_t d, int64_t m, int t) { return slot_bytes(make_plan(n, m, d, m, t, true)); }
 

@@ -1343,10 +1343,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   cluster_sync_all();  // barriers initialised in both CTAs before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_dependents_may_start();
 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------------- TMA producer (both CTAs)
+      grid_wait_for_previous();
       int kiter = 0;
       bool ok = true;
       // Pacing (even CTAs, when pace != null): every kPaceKb k-blocks a pair announces itself on
@@ -1449,6 +1451,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue (both CTAs)
+    grid_wait_for_previous();  // Z may be what it writes, the outputs what it reads
     const int q = warp & 3;
     const int c_begin = ((warp - 2) / 4) * kEpiChunks;
     const CUtensorMap* tm_out = (tma_out & 1) ? &tmap_c : nullptr;  // bulk stores of ep.out / ep.out2
@@ -1648,10 +1651,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   cluster_sync_all();  // barriers initialised in both CTAs before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_dependents_may_start();
 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------------- TMA producer (both CTAs)
+      grid_wait_for_previous();
       int kiter = 0;
       bool ok = true;
       const bool pacer = pace != nullptr && rank == 0;  // pacing as in the 256 x 256 pair kernel
@@ -1849,6 +1854,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue (both CTAs)
+    grid_wait_for_previous();  // Z may be what it writes, the outputs what it reads
     const int q = warp & 3;
     const int c_begin = ((warp - 2) / 4) * kEpiChunks;
     const CUtensorMap* tm_out = (tma_out & 1) ? &tmap_c : nullptr;  // bulk stores of ep.out / ep.out2
@@ -2076,8 +2082,11 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, int M, int N, i
 // stream before the launch. Pacing is on unless tpmlp_set_gemm_variant turned it off.
 __device__ unsigned int g_pace_counters[64];
 
-unsigned int* next_pace_counter() {
+// A launch of at most 4 pacing intervals a pair gets none: its pairs start together and have little time to drift apart, and
+// the counter's memset would cost a small GEMM 2.5 us of its 12 to 20.
+unsigned int* next_pace_counter(int64_t rounds, int num_kb) {
   if (!g_pair_pacing.load(std::memory_order_relaxed)) return nullptr;
+  if (rounds * num_kb <= 4 * kPaceKb) return nullptr;
   static std::atomic<unsigned int> next{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return nullptr;
@@ -2121,11 +2130,13 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutM
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = PAIR_SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // The persistent grid (and the pacing, which waits for every pair of a round) assumes all
@@ -2146,11 +2157,12 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutM
   }
   const int pairs = static_cast<int>(tiles < max_pairs ? tiles : max_pairs);
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  unsigned int* pace = next_pace_counter();
+  unsigned int* pace = next_pace_counter((tiles + max_pairs - 1) / max_pairs, (K + BK - 1) / BK);
   if (pace) {
     e = cudaMemsetAsync(pace, 0, sizeof(unsigned int), stream);
     if (e != cudaSuccess) return e;
   }
+  cfg.numAttrs = ep.dependent ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, ta, tb, om.c, om.c2, om.flags, M, N, K, ep, ctx.status, pair_group(), pace);
 }
 
@@ -2168,11 +2180,13 @@ cudaError_t launch_wide(const CUtensorMap& ta, const CUtensorMap& tb, const OutM
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = WIDE_SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static int resident_pairs[16] = {};
@@ -2197,11 +2211,12 @@ cudaError_t launch_wide(const CUtensorMap& ta, const CUtensorMap& tb, const OutM
     pairs = static_cast<int>(waves > 1 ? max_pairs : 2 * tail);
   }
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  unsigned int* pace = next_pace_counter();
+  unsigned int* pace = next_pace_counter((tiles + max_pairs - 1) / max_pairs, (K + BK - 1) / BK);
   if (pace) {
     e = cudaMemsetAsync(pace, 0, sizeof(unsigned int), stream);
     if (e != cudaSuccess) return e;
   }
+  cfg.numAttrs = ep.dependent ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, ta, tb, om.c, om.c2, om.flags, M, N, K, ep, ctx.status, pair_group(true),
                             pace, tail_split);
 }
@@ -2409,7 +2424,7 @@ cudaError_t gated_gemm(int64_t M, int64_t N, int64_t K, const Operand& a, const 
 }
 
 EpiParams gated_params(void* out, void* out2, const void* aux, int64_t ldo, int64_t m, int t, int act, int block) {
-  EpiParams ep{};
+  EpiParams ep{};  // not dependent: the first kernel of its call
   ep.out = out;
   ep.out2 = out2;
   ep.aux = aux;

@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
       }
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;");  // the sums below may be scheduled; they wait for this grid's end
+  grid_dependents_may_start();  // the sums below may be scheduled; they wait for this grid's end
   if (aborted && tid == 0)
     for (int64_t k = i; k < issued; ++k) ring.wait(k, status, 64);
 #pragma unroll
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     }
     none_left = false;
   }
-  asm volatile("griddepcontrol.launch_dependents;");
+  grid_dependents_may_start();
   F2 sum[4];
   gather(acc_pre, sum);
   if (tid * 8 < p.h) Vec8<float>::store(p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * p.h + tid * 8, sum);
@@ -690,7 +690,7 @@ struct Finish {
   int h, slices, ctas;
 };
 __global__ void __launch_bounds__(kFinishThreads) residual_norm_finish_kernel(const __grid_constant__ Finish p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait_for_previous();
   constexpr int kQuads = 8, kGroups = kFinishThreads / kQuads;
   __shared__ float4 grp[kGroups][kQuads];
   const int q = threadIdx.x % kQuads, g = threadIdx.x / kQuads;

@@ -24,8 +24,11 @@ Region matrix(const void* p, int64_t rows, int64_t cols, int64_t size = 2) {
   return flat_region(p, rows * cols, size);  // both below 2^31
 }
 
+// The products behind a call's first one: each is launched as a programmatic dependent of the kernel in front of it, and
+// waits for that kernel's end before it touches memory.
 EpiParams plain(void* out, int64_t ldo) {
   EpiParams ep{};
+  ep.dependent = true;
   ep.out = out;
   ep.ldo = ldo;
   ep.remap.b = ep.remap.s = ep.remap.s_per_shard = 1;
@@ -81,7 +84,7 @@ tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, vo
     TPMLP_PASS_CUDA(gated_fc1_tc(X, A, Z_save, Y_save, n, d, m, t, act, st, ctx), "gated FC1 GEMM");
   }
   if (few && gemm_takes_few_rows(n, d, m)) {
-    TPMLP_PASS_CUDA(gemm_few_rows(Y_save, B, true, O, n, d, m, static_cast<char*>(workspace) + fc1_bytes(n, d, m, t), few1, st,
+    TPMLP_PASS_CUDA(gemm_few_rows(Y_save, B, true, O, n, d, m, static_cast<char*>(workspace) + fc1_bytes(n, d, m, t), true, st,
                                   ctx),
                     "gated FC2, few rows");
   } else {
@@ -136,7 +139,7 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, c
                   "gated wgrad-1 GEMM");
   // both projections' shares of dX are one sum over the 2 m columns of D
   if (few_rows_allowed() && gemm_takes_few_rows(n, d, 2 * m)) {
-    TPMLP_PASS_CUDA(gemm_few_rows(workspace, A, false, dX, n, d, 2 * m, static_cast<char*>(workspace) + dz_bytes(n, m), false, st,
+    TPMLP_PASS_CUDA(gemm_few_rows(workspace, A, false, dX, n, d, 2 * m, static_cast<char*>(workspace) + dz_bytes(n, m), true, st,
                                   ctx),
                     "gated dgrad-2, few rows");
     return TPMLP_OK;

@@ -82,6 +82,9 @@ struct EpiParams {
   // kEpiGate, kEpiGateGrad: columns of one shard (m / t), and the run of columns that tiles divide: all of them where
   // shards end on the epilogue's column blocks, else one shard
   int shard, unit;
+  // SM-pair kernels: launched as a programmatic dependent of the kernel in front on the stream, which is one of this
+  // library's that lets its dependents start early
+  bool dependent = false;
 };
 
 // A stored operand matrix [rows][cols] with row stride `ld` elements.
@@ -156,7 +159,7 @@ cudaError_t gated_dgrad1_tc(const void* g, const void* b, const void* z, void* d
 
 // The same for few tokens, with the sum over K split across the SMs (gemm_few_rows.cu), where it is the faster one:
 // gated_fc1_few_rows as gated_fc1_tc; gemm_few_rows: out [n][cols] = tokens [n][k] W, W stored [k][cols] (w_mn) or
-// [cols][k], bf16. `dependent`: the kernel in front on the stream is this file's, and only `tokens` depends on it. Workspaces
+// [cols][k], bf16. `dependent`: a programmatic dependent (EpiParams::dependent) of the kernel in front, which writes no weights. Workspaces
 // 256-byte aligned, their sizes independent of the device.
 bool few_rows_allowed();  // by tpmlp_set_gemm_variant: the per-product choice is on
 bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m);
