@@ -55,16 +55,30 @@ __device__ __forceinline__ int tile_column(const Plan& p, int tile) {
 }
 __device__ __forceinline__ int tile_token(const Plan& p, int tile) { return tile % p.token_tiles * p.nt; }
 
-// A CTA's way along its items (item = split * tiles + tile) and their k-blocks.
+// A CTA's way along its items (item = split * tiles + tile) and their k-blocks: the tile's first column and token, and the
+// k-block (divisions once an item).
 struct Walk {
-  int item, tile, kb, end;
+  int item, col, token, kb, end;
+  int rank, gate[2];  // the gated block's gate columns in A of this CTA's two 64-column boxes
   __device__ __forceinline__ void enter(const Plan& p) {
     const int split = item / p.tiles;
-    tile = item - split * p.tiles;
+    const int tile = item - split * p.tiles;
+    col = tile_column(p, tile);
+    token = tile_token(p, tile);
+    if (p.shard) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int y = col + rank * kBlock + j * 64;
+        gate[j] = y + y / p.shard * p.shard;
+      }
+    }
     kb = static_cast<int>(static_cast<int64_t>(split) * p.num_kb / p.splits);
     end = static_cast<int>(static_cast<int64_t>(split + 1) * p.num_kb / p.splits);
   }
-  __device__ __forceinline__ explicit Walk(const Plan& p) : item(blockIdx.x / p.ranks), tile(0), kb(0), end(0) { enter(p); }
+  __device__ __forceinline__ Walk(const Plan& p, int cta_rank)
+      : item(blockIdx.x / p.ranks), col(0), token(0), kb(0), end(0), rank(cta_rank), gate{0, 0} {
+    enter(p);
+  }
   __device__ __forceinline__ bool more(const Plan& p) const { return item < p.items; }
   __device__ __forceinline__ void next_item(const Plan& p) {
     item += p.ctas / p.ranks;
@@ -153,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(dst, map, &full[s], x, y);
       };
       auto load_weights = [&](const Walk& at, int s) {
-        const int col = tile_column(p, at.tile) + rank * cta_columns(p), kb = at.kb;
+        const int col = at.col + rank * cta_columns(p), kb = at.kb;
         uint8_t* dst = smem + s * stage_bytes;
         if (rank == 0) mbar_arrive_expect_tx(&full[s], p.ranks * stage_bytes);
 #pragma unroll
@@ -162,10 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               int c = col + b * kBlock + j * 64;
-              if constexpr (GATE) {  // block 0: gate columns, block 1: up columns
-                const int y = col + j * 64;
-                c = y + (y / p.shard + b) * p.shard;
-              }
+              if constexpr (GATE) c = at.gate[j] + b * p.shard;  // block 0: gate columns, block 1: up columns
               load(dst + (2 * b + j) * kBoxBytes, &tmap_w, s, c, kb * kBK);
             }
           } else {
@@ -174,10 +185,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto load_tokens = [&](const Walk& at, int s) {
-        load(smem + s * stage_bytes + kWeightBytes, &tmap_t, s, at.kb * kBK, tile_token(p, at.tile) + rank * (p.nt / 2));
+        load(smem + s * stage_bytes + kWeightBytes, &tmap_t, s, at.kb * kBK, at.token + rank * (p.nt / 2));
       };
       // The weights are there before the kernel in front has ended; the tokens may be what it writes.
-      Walk w(p), tok(p);
+      Walk w(p, rank), tok(p, rank);
       int it = 0;
       for (; it < stages && w.more(p); ++it, w.next(p)) load_weights(w, it);
       grid_wait_for_previous();
@@ -203,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int it = 0, seg = 0;
       bool ok = true;
-      for (Walk at(p); at.more(p) && ok; at.next_item(p), ++seg) {
+      for (Walk at(p, rank); at.more(p) && ok; at.next_item(p), ++seg) {
         const int set = seg % sets;
         if (!mbar_wait(&tempty[set], ((seg / sets) & 1) ^ 1, status, 73)) break;
         tc_fence_after();
@@ -257,12 +268,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     int seg = 0;
-    for (Walk at(p); at.more(p); at.next_item(p), ++seg) {
+    for (Walk at(p, rank); at.more(p); at.next_item(p), ++seg) {
       const int set = seg % sets;
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[set], (seg / sets) & 1, status, 76))) break;
       tc_fence_after();
-      const int token0 = tile_token(p, at.tile), tokens = min(p.nt, p.n - token0);
-      const int tile_col = tile_column(p, at.tile), col0 = tile_col + rank * cta_columns(p) + q * 32 + lane;
+      const int token0 = at.token, tokens = min(p.nt, p.n - token0);
+      const int tile_col = at.col, col0 = tile_col + rank * cta_columns(p) + q * 32 + lane;
       const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(set * 2 * ntp);
 #pragma unroll 1
       for (int t0 = t_first; t0 < tokens; t0 += 64) {

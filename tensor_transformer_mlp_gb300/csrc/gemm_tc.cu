@@ -1227,15 +1227,16 @@ __device__ __forceinline__ void gate_grad_32(uint4 (&zg)[4], uint4 (&zu)[4], con
   }
 }
 
-// One epilogue warp's `passes` blocks of 32 columns of dY from column y on (t_addr: their tensor-memory address): D of
+// One epilogue warp's kPasses blocks of 32 columns of dY from column y on (t_addr: their tensor-memory address): D of
 // both parts. zg, zu hold the first block's Z and receive that of the block at y_next (< 0: none), so that a block's Z is
 // on its way while the one before is worked on. The two 2 KB blocks of a pass leave through the warp's buffer in the
 // 64-byte-swizzled layout of the map.
+template <int kPasses>
 __device__ __forceinline__ void gate_grad_epilogue(const EpiParams& ep, uint8_t* buf, int lane, int64_t row, int M, int y,
                                                    int y_block, uint32_t t_addr, int y_next, uint4 (&zg)[4], uint4 (&zu)[4],
                                                    const CUtensorMap* tm_d) {
 #pragma unroll 1
-  for (int p = 0; p < kEpiChunks; ++p) {
+  for (int p = 0; p < kPasses; ++p) {
     const int col = y + p * 32;
     uint4 dg[4], du[4];
 #pragma unroll
@@ -1243,7 +1244,7 @@ __device__ __forceinline__ void gate_grad_epilogue(const EpiParams& ep, uint8_t*
       dg[i] = zg[i];
       du[i] = zu[i];
     }
-    const int next = p + 1 < kEpiChunks ? col + 32 : y_next;
+    const int next = p + 1 < kPasses ? col + 32 : y_next;
     if (next >= 0) load_gate_z(zg, zu, ep, row, M, next, y_block);
     uint32_t v[32];
     tmem_ld_32x32b_x32(t_addr + static_cast<uint32_t>(p * 32), v);
@@ -1268,7 +1269,9 @@ __device__ __forceinline__ void gate_grad_epilogue(const EpiParams& ep, uint8_t*
   }
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+// BN_T: the tile's columns, 256, or 128 for the gated block's dgrad-1 where 256 would keep at most half of the pairs busy
+// (n512 d1024 m4096: 32 tiles).
+template <bool A_MN, bool B_MN, int EPI, int BN_T = BN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                           const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_c2,
@@ -1292,8 +1295,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int num_pairs = static_cast<int>(gridDim.x >> 1);
   const int num_mb = (M + 2 * BM - 1) / (2 * BM);
   // kEpiGate: 128 columns of Y a tile, from 128 gate and 128 up columns of A
-  constexpr int kTileN = EPI == kEpiGate ? BN_HALF : BN;
-  const int num_nb = kGated<EPI> ? gated_blocks(N, ep.unit, kTileN) : (N + BN - 1) / BN;
+  constexpr int kTileN = EPI == kEpiGate ? BN_T / 2 : BN_T;
+  constexpr int kChunks = BN_T / 32 / (NUM_EPI_WARPS / 4);  // of 32 columns per epilogue warp
+  constexpr uint32_t kStageTx = 2 * (A_STAGE_BYTES + BN_T / 2 * BK * 2);
+  static_assert(BN_T == BN || EPI == kEpiGateGrad, "narrow tiles");
+  const int num_nb = kGated<EPI> ? gated_blocks(N, ep.unit, kTileN) : (N + BN_T - 1) / BN_T;
   const int num_tiles = num_mb * num_nb;
   // group > 0: bands of `group` pair-rows, each walked N-block by N-block (M fastest);
   // group < 0: bands of -group N-blocks, walked pair-row by pair-row (N fastest).
@@ -1363,8 +1369,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int mb, nb;
         coords(tile, mb, nb);
         const int a_row = mb * 2 * BM + static_cast<int>(rank) * BM;
-        const int y0 = kGated<EPI> ? gated_column(nb, ep.unit, kTileN) : nb * BN;
-        const int b_col = y0 + static_cast<int>(rank) * BN_HALF;
+        const int y0 = kGated<EPI> ? gated_column(nb, ep.unit, kTileN) : nb * BN_T;
+        const int b_col = y0 + static_cast<int>(rank) * (BN_T / 2);
+        int b_box[BN_T / 128];  // columns of an MN-major B's boxes, kept out of the k-loop (divisions)
+#pragma unroll
+        for (int j = 0; j < BN_T / 128; ++j) b_box[j] = EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_col + j * 64;
         const unsigned int active = static_cast<unsigned int>(min(num_pairs, num_tiles - round * num_pairs));
         for (int kb = 0; kb < num_kb; ++kb) {
           if (pacer && kb % kPaceKb == 0) {
@@ -1378,7 +1387,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * PAIR_STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], kStageTx);
           // K runs backwards in odd rounds: a round starts on the k-blocks that the previous round
           // (which shares its A panels in the band order) touched last, so more of them are in L2.
           const int kbl = (round & 1) ? num_kb - 1 - kb : kb;
@@ -1395,9 +1404,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tma_load_2d_pair(sb, &tmap_b, full0, kbl * BK, b_col);
           } else {
 #pragma unroll
-            for (int j = 0; j < BN_HALF / 64; ++j)
-              tma_load_2d_pair(sb + j * MN_BOX_BYTES, &tmap_b, full0,
-                               EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_col + j * 64, kbl * BK);
+            for (int j = 0; j < BN_T / 128; ++j)
+              tma_load_2d_pair(sb + j * MN_BOX_BYTES, &tmap_b, full0, b_box[j], kbl * BK);
           }
           ++kiter;
         }
@@ -1411,7 +1419,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ---------------------------------------------------------------- MMA issuer (even CTA)
-      constexpr uint32_t kIdesc = idesc_bf16_f32(2 * BM, BN, A_MN, B_MN);
+      constexpr uint32_t kIdesc = idesc_bf16_f32(2 * BM, BN_T, A_MN, B_MN);
       int kiter = 0, it = 0;
       bool ok = true;
       for (int tile = pair; tile < num_tiles; tile += num_pairs, ++it) {
@@ -1453,19 +1461,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------------ epilogue (both CTAs)
     grid_wait_for_previous();  // Z may be what it writes, the outputs what it reads
     const int q = warp & 3;
-    const int c_begin = ((warp - 2) / 4) * kEpiChunks;
+    const int c_begin = ((warp - 2) / 4) * kChunks;
     const CUtensorMap* tm_out = (tma_out & 1) ? &tmap_c : nullptr;  // bulk stores of ep.out / ep.out2
     const CUtensorMap* tm_out2 = (tma_out & 2) ? &tmap_c2 : nullptr;
     int it = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs, ++it) {
       const int acc = it & 1;
       const uint32_t use = static_cast<uint32_t>(it >> 1);
-      const bool ok = mbar_wait(&tfull_bar[acc], use & 1, status, 16);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
       int mb, nb;
       coords(tile, mb, nb);
       const int64_t row = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32 + lane;
+      uint4 zg[4], zu[4];  // kEpiGateGrad: the first block's Z comes while the accumulator is waited for
+      if constexpr (EPI == kEpiGateGrad) {
+        const int y0 = gated_column(nb, ep.unit, kTileN);
+        load_gate_z(zg, zu, ep, row, M, y0 + c_begin * 32, y0);
+      }
+      const bool ok = mbar_wait(&tfull_bar[acc], use & 1, status, 16);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
       uint8_t* buf = epi_stage + (warp - 2) * EPI_STAGE_BYTES;
       if constexpr (EPI == kEpiGate) {
@@ -1474,9 +1487,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           gate_epilogue(ep, buf, lane, static_cast<int>(row) - lane, y, t_row + c_begin * 16, tm_out, tm_out2);
       } else if constexpr (EPI == kEpiGateGrad) {
         const int y0 = gated_column(nb, ep.unit, kTileN), y = y0 + c_begin * 32;
-        uint4 zg[4], zu[4];
-        load_gate_z(zg, zu, ep, row, M, y, y0);
-        gate_grad_epilogue(ep, buf, lane, row, M, y, y0, t_row + c_begin * 32, -1, zg, zu, tm_out);
+        gate_grad_epilogue<kChunks>(ep, buf, lane, row, M, y, y0, t_row + c_begin * 32, -1, zg, zu, tm_out);
       } else {
         epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, buf, lane, row, M, N, nb * BN, c_begin, t_row, 0, 1.f,
                                                             row, nb, num_nb, tm_out, tm_out2);
@@ -1672,6 +1683,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int a_row = mb * 2 * BM + static_cast<int>(rank) * BM;
         const unsigned int active = static_cast<unsigned int>(
             round < rounds_full ? min(num_pairs, num_tiles - round * num_pairs) : 2 * tail_tiles);
+        // First column of each half's chunk of this CTA, and of its 64-column boxes where B is MN-major: kept out of the
+        // k-loop (the gated block's take divisions, which cost the producer more than a k-block has room for).
+        int b_first[2], b_box[2][BN_HALF / 64];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int y0 = kGated<EPI> ? gated_column(nb, ep.unit, 2 * kHalfN) + h * kHalfN : nb * WIDE_BN + h * BN;
+          b_first[h] = y0 + static_cast<int>(rank) * BN_HALF;
+#pragma unroll
+          for (int j = 0; j < BN_HALF / 64; ++j)
+            b_box[h][j] = EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_first[h] + j * 64;
+        }
         const uint32_t stage_tx = half < 0 ? 2 * WIDE_STAGE_BYTES : 2 * (A_STAGE_BYTES + WIDE_CHUNK_BYTES);
         for (int kb = 0; kb < num_kb; ++kb) {
           if constexpr (EPI == kEpiDGelu) {
@@ -1716,16 +1738,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // this CTA's 128 columns of each 256-column half
             if (half >= 0 && h != half) continue;
-            const int y0 = kGated<EPI> ? gated_column(nb, ep.unit, 2 * kHalfN) + h * kHalfN : nb * WIDE_BN + h * BN;
-            const int b_col = y0 + static_cast<int>(rank) * BN_HALF;
             uint8_t* sbh = sb + h * WIDE_CHUNK_BYTES;
             if constexpr (!B_MN) {
-              tma_load_2d_pair(sbh, &tmap_b, full0, kbl * BK, b_col);
+              tma_load_2d_pair(sbh, &tmap_b, full0, kbl * BK, b_first[h]);
             } else {
 #pragma unroll
               for (int j = 0; j < BN_HALF / 64; ++j)
-                tma_load_2d_pair(sbh + j * MN_BOX_BYTES, &tmap_b, full0,
-                                 EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_col + j * 64, kbl * BK);
+                tma_load_2d_pair(sbh + j * MN_BOX_BYTES, &tmap_b, full0, b_box[h][j], kbl * BK);
             }
           }
           ++kiter;
@@ -1920,7 +1939,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const int y = y0 + h * BN + c_begin * 32;
-          gate_grad_epilogue(ep, buf, lane, row, M, y, y0,
+          gate_grad_epilogue<kEpiChunks>(ep, buf, lane, row, M, y, y0,
                              tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * BN + c_begin * 32),
                              h < h_last ? y + BN : -1, zg, zu, tm_out);
           tc_fence_before();
@@ -2118,13 +2137,14 @@ int pair_group(bool wide = false) {
   return g != 0 ? g : (wide ? WIDE_GROUP_M : PAIR_GROUP_M);
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+template <bool A_MN, bool B_MN, int EPI, int BN_T = BN>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutMaps& om, int M, int N, int K,
                         const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx) {
-  auto kernel = gemm_bf16_pair_kernel<A_MN, B_MN, EPI>;
+  auto kernel = gemm_bf16_pair_kernel<A_MN, B_MN, EPI, BN_T>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * n_blocks<EPI>(N, ep, false);
+  const int64_t nb = BN_T == BN ? n_blocks<EPI>(N, ep, false) : gated_blocks(N, ep.unit, BN_T);
+  const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * nb;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
@@ -2265,8 +2285,11 @@ int pair_kernel_choice() { return g_pair_kernel.load(std::memory_order_relaxed);
 // u 0.92, e 200; GeLU' (reads Z, pipelined) u 0.87, e 570; the row-dot epilogue u 0.91, e 450;
 // dropout + residual (per-thread hash, residual loads, remapped stores) u 0.91, e 2000 (the SP
 // block's FC2: 602 us on 256 x 256 tiles, 618 us on split 256 x 512 ones). The fp32
-// read-add-write epilogue is not fitted and keeps the earlier, cautious u 0.91 with e 400.
-bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiKind epi, int pairs) {
+// read-add-write epilogue is not fitted and keeps the earlier, cautious u 0.91 with e 400. The gated block's FC1
+// (d4096 m16384, n8192, 256 x 256 against 256 x 512 tiles: 1177 / 1210 us with Z, 1137 / 1125 without; n16384 d8192 m32768:
+// 10360 / 9775, 10279 / 9623) u 0.86, e 690 and u 0.883, e 430; its dgrad-1 reads and writes 8 bytes a value in the
+// epilogue, which only the 256 x 256 tiles hide (649 / 807, 5216 / 5728 us).
+bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiKind epi, int pairs, bool z_saved = false) {
   const int64_t mb = (M + 2 * BM - 1) / (2 * BM);
   const int64_t t256 = mb * nb256, t512 = mb * nb512;
   const int64_t w256 = (t256 + pairs - 1) / pairs, w512 = (t512 + pairs - 1) / pairs;
@@ -2278,6 +2301,8 @@ bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiK
     case kEpiStoreRowDot: u = 0.91; e = 450.0; break;
     case kEpiDropoutResidual: u = 0.91; e = 2000.0; break;
     case kEpiAccumF32: u = 0.91; e = 400.0; break;
+    case kEpiGate: u = z_saved ? 0.86 : 0.883; e = z_saved ? 690.0 : 430.0; break;
+    case kEpiGateGrad: return false;
     default: break;
   }
   const double unit = u + e / static_cast<double>(K);
@@ -2412,12 +2437,17 @@ cudaError_t gated_gemm(int64_t M, int64_t N, int64_t K, const Operand& a, const 
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
   const int choice = pair_kernel_choice();
   const bool wide = choice == 3 || (choice == 1 && prefer_wide_blocks(M, n_blocks<EPI>(n, ep, false),
-                                                                      n_blocks<EPI>(n, ep, true), K, static_cast<EpiKind>(EPI), ctx.num_sms / 2));
+                                                                      n_blocks<EPI>(n, ep, true), K, static_cast<EpiKind>(EPI), ctx.num_sms / 2, ep.out != nullptr));
+  const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * n_blocks<EPI>(n, ep, false);
+  const bool narrow = EPI == kEpiGateGrad && choice == 1 && 2 * tiles <= ctx.num_sms / 2;
   CUtensorMap ta, tb;
   cudaError_t e = make_tmap(&ta, a, 64, BM);
   if (e != cudaSuccess) return e;
-  e = make_tmap(&tb, b, 64, b.mn_major ? BK : BN_HALF);
+  e = make_tmap(&tb, b, 64, b.mn_major ? BK : narrow ? BN_HALF / 2 : BN_HALF);
   if (e != cudaSuccess) return e;
+  if constexpr (EPI == kEpiGateGrad) {
+    if (narrow) return launch_pair<false, false, EPI, BN_HALF>(ta, tb, om, m, n, k, ep, stream, ctx);
+  }
   const EpiKind epi = static_cast<EpiKind>(EPI);
   return wide ? dispatch_pair<true>(false, b.mn_major, epi, ta, tb, om, m, n, k, ep, stream, ctx)
               : dispatch_pair<false>(false, b.mn_major, epi, ta, tb, om, m, n, k, ep, stream, ctx);
