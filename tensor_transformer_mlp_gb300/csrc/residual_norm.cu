@@ -131,8 +131,8 @@ struct RowRing {
     for (int st = 0; st < stages; ++st) mbar_init(&full[st], 1);
     fence_mbar_init();
   }
-  __device__ __forceinline__ void issue(int64_t i) const {
-    const int st = static_cast<int>(i % stages);
+  // Row i of the CTA into stage st.
+  __device__ __forceinline__ void issue(int64_t i, int st) const {
     uint8_t* dst = smem + static_cast<size_t>(st) * stage_bytes();
     uint32_t n = 0;
 #pragma unroll
@@ -142,12 +142,26 @@ struct RowRing {
     for (int k = 0; k < NTEN; ++k)
       if (src[k]) bulk_load(dst + k * row_bytes, src[k] + i * row_bytes, row_bytes, &full[st]);
   }
-  __device__ __forceinline__ bool wait(int64_t i, unsigned int* status, unsigned int where) const {
-    return mbar_wait(&full[i % stages], static_cast<uint32_t>((i / stages) & 1), status, where);
-  }
   template <typename T>
-  __device__ __forceinline__ const T* at(int64_t i, int k) const {
-    return reinterpret_cast<const T*>(smem + static_cast<size_t>(i % stages) * stage_bytes() + k * row_bytes);
+  __device__ __forceinline__ const T* at(int st, int k) const {
+    return reinterpret_cast<const T*>(smem + st * stage_bytes() + k * row_bytes);
+  }
+  // Waits (bounded) for the copies of rows [from, to), which are all in flight or there.
+  __device__ __forceinline__ void drain(int64_t from, int64_t to, unsigned int* status, unsigned int where) const {
+    for (int64_t k = from; k < to; ++k) mbar_wait(&full[k % stages], static_cast<uint32_t>((k / stages) & 1), status, where);
+  }
+};
+
+// A row's stage and its barrier's phase, counted along instead of divided out (a 64-bit division a row and thread costs
+// the backward 15 %).
+struct RowStage {
+  int st = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1;
+    }
   }
 };
 
@@ -179,7 +193,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
   __syncthreads();
   int64_t issued = min(n, static_cast<int64_t>(stages));  // meaningful in thread 0
   if (tid == 0)
-    for (int64_t i = 0; i < issued; ++i) ring.issue(i);
+    for (int64_t i = 0; i < issued; ++i) ring.issue(i, static_cast<int>(i));
 
   F2 wt[CH][4], pre[CH][4];
   int64_t seq = -1, seq_end = 0;  // the sequence whose gate wt holds, and its last row's successor
@@ -188,7 +202,8 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
   const F2 alpha = f2_make(p.alpha, p.alpha), zero = f2_make(0.f, 0.f);
   int64_t i = 0;
   int aborted = 0;
-  for (; i < n; ++i) {
+  RowStage at;
+  for (; i < n; ++i, at.next(stages)) {
     const int64_t row = first + i;
     if (row >= seq_end) {
       seq = row / p.s;
@@ -203,7 +218,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
         for (int e = 0; e < 4; ++e) wt[c][e] = f2_mul(wt[c][e], g[e]);
       }
     }
-    const bool ok = ring.wait(i, status, 61);
+    const bool ok = mbar_wait(&ring.full[at.st], at.phase, status, 61);
     Vec8<T> xv[CH], yv[CH];
     F2 ss = zero;
 #pragma unroll
@@ -212,8 +227,8 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
       xv[c].zero();
       yv[c].zero();
       if (col < p.h) {
-        xv[c].load(ring.at<T>(i, 0) + col);
-        yv[c].load(ring.at<T>(i, 1) + col);
+        xv[c].load(ring.at<T>(at.st, 0) + col);
+        yv[c].load(ring.at<T>(at.st, 1) + col);
       }
       F2 f[4];
       yv[c].unpack(f);
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
     aborted = __syncthreads_or(!ok);  // the row is in registers everywhere
     if (aborted) break;
     if (tid == 0 && i + stages < n) {
-      ring.issue(i + stages);
+      ring.issue(i + stages, at.st);
       issued = i + stages + 1;
     }
     const float ry = p.post ? rsqrtf(fmaf(lane_sum<NW>(red[par][0][lane & (NW - 1)]), p.inv_h, p.eps)) : 1.f;
@@ -262,8 +277,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
       }
     }
   }
-  if (aborted && tid == 0)
-    for (int64_t k = i; k < issued; ++k) ring.wait(k, status, 62);  // copies in flight
+  if (aborted && tid == 0) ring.drain(i, issued, status, 62);  // copies in flight
 }
 
 // The backward's six sums of a row; everything that follows from them.
@@ -370,8 +384,13 @@ __device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// One barrier a row: all six sums are taken at once.
-template <typename T, int NT, int CH, int MINB>
+// One barrier a row: all six sums are taken at once. Between two barriers a thread works out a row's gradients and takes
+// the next row's sums, both from the ring, so that neither the sums' way through the CTA nor registers for a whole row hold
+// anything up.
+// HOLD: a row stays in registers from its sums to its gradients instead, and its stage is refilled at once (for fp32, whose
+// rows leave no room for a ring of three and more in flight).
+// RING: else rows are read where they lie.
+template <typename T, int NT, int CH, int MINB, bool HOLD, bool RING>
 __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(const __grid_constant__ Backward p, int stages,
                                                                               unsigned int* status) {
   constexpr int NW = NT / 32;
@@ -387,14 +406,17 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
   const void* src[4] = {p.y, p.r, p.dr, p.du};
 #pragma unroll
   for (int k = 0; k < 4; ++k) ring.src[k] = src[k] ? static_cast<const uint8_t*>(src[k]) + first * ring.row_bytes : nullptr;
-  if (tid == 0) ring.init();
-  __syncthreads();
   int64_t issued = min(n, static_cast<int64_t>(stages));  // meaningful in thread 0
-  if (tid == 0)
-    for (int64_t i = 0; i < issued; ++i) ring.issue(i);
+  if constexpr (RING) {
+    if (tid == 0) ring.init();
+    __syncthreads();
+    if (tid == 0)
+      for (int64_t i = 0; i < issued; ++i) ring.issue(i, static_cast<int>(i));
+  }
 
   const F2 zero = f2_make(0.f, 0.f);
   F2 wt[CH][4], pre[CH][4], acc_s[CH][4], acc_pre[CH][4];
+  GradColumns<T> held[HOLD ? CH : 1];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     load_gain(pre[c], p.pre, (tid + c * NT) * 8, p.h);
@@ -403,9 +425,23 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
   }
   int64_t seq = -1, seq_end = first;
   bool none_left = true;  // no sequence of the CTA has ended yet
-  int64_t i = 0;
-  int aborted = 0;
-  for (; i < n; ++i) {
+  auto columns = [&](int64_t i, int st, int col) {
+    auto row_of = [&](int k) {
+      if constexpr (RING) return ring.template at<T>(st, k) + col;
+      return reinterpret_cast<const T*>(ring.src[k] + i * ring.row_bytes) + col;
+    };
+    GradColumns<T> v;
+    v.zero();
+    if (col < p.h) {
+      if (p.y) v.y.load(row_of(0));
+      if (p.r) v.r.load(row_of(1));
+      if (p.dr) v.dr.load(row_of(2));
+      if (p.du) v.du.load(row_of(3));
+    }
+    return v;
+  };
+  // Row i's sums, behind the end of the sequence before it if there is one.
+  auto take_sums = [&](int64_t i, const RowStage& at) {
     const int64_t row = first + i;
     if (row >= seq_end) {
 #pragma unroll
@@ -428,37 +464,42 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
         for (int e = 0; e < 4; ++e) wt[c][e] = f2_mul(wt[c][e], g[e]);
       }
     }
-    const bool ok = ring.wait(i, status, 63);
-    GradColumns<T> v[CH];
+    const bool ok = !RING || mbar_wait(&ring.full[at.st], at.phase, status, 63);
     F2 s2[6] = {zero, zero, zero, zero, zero, zero};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (tid + c * NT) * 8;
-      v[c].zero();
-      if (col < p.h) {
-        if (p.y) v[c].y.load(ring.at<T>(i, 0) + col);
-        if (p.r) v[c].r.load(ring.at<T>(i, 1) + col);
-        if (p.dr) v[c].dr.load(ring.at<T>(i, 2) + col);
-        if (p.du) v[c].du.load(ring.at<T>(i, 3) + col);
-      }
-      v[c].sums(wt[c], pre[c], s2);
+      const GradColumns<T> v = columns(i, at.st, (tid + c * NT) * 8);
+      if constexpr (HOLD) held[c] = v;
+      v.sums(wt[c], pre[c], s2);
     }
-    const int par = static_cast<int>(i & 1);
     float s8[8] = {sum2(s2[0]), sum2(s2[1]), sum2(s2[2]), sum2(s2[3]), sum2(s2[4]), sum2(s2[5]), 0.f, 0.f};
     const float mine = warp_sums8(s8, lane);
-    if ((lane & 3) == 0) red[par][w][lane >> 2] = mine;
-    aborted = __syncthreads_or(!ok);  // the row is in registers everywhere, the warps' sums are out
+    if ((lane & 3) == 0) red[i & 1][w][lane >> 2] = mine;
+    return ok;
+  };
+  RowStage before, here, next;  // of rows i - 1, i and i + 1
+  bool ok = take_sums(0, next);
+  int64_t i = 0;
+  int aborted = 0;
+  for (; i < n; ++i) {
+    before = here;
+    here = next;
+    next.next(stages);
+    aborted = __syncthreads_or(!ok);  // row i's sums are out, and nobody reads row i - 1 any more
     if (aborted) break;
-    if (tid == 0 && i + stages < n) {
-      ring.issue(i + stages);
-      issued = i + stages + 1;
+    if (RING && tid == 0) {  // the stage that nobody reads any more: this row's where it is in registers, else the last one's
+      const int64_t done = HOLD ? i : i - 1;
+      if (done >= 0 && done + stages < n) {
+        ring.issue(done + stages, HOLD ? here.st : before.st);
+        issued = done + stages + 1;
+      }
     }
     // lane l adds value l & 7 of the warps l >> 3, + 4, ..: the same order in every warp
     float part = 0.f;
 #pragma unroll
     for (int k = 0; k < (NW + 3) / 4; ++k) {
       const int warp = (lane >> 3) + 4 * k;
-      if (warp < NW) part += red[par][warp][lane & 7];
+      if (warp < NW) part += red[i & 1][warp][lane & 7];
     }
     part += __shfl_xor_sync(0xffffffffu, part, 8);
     part += __shfl_xor_sync(0xffffffffu, part, 16);
@@ -466,21 +507,26 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
 #pragma unroll
     for (int k = 0; k < 6; ++k) total[k] = __shfl_sync(0xffffffffu, part, k);
     const RowFactors f(total, p);
+    const int64_t row = first + i;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (tid + c * NT) * 8;
       F2 ox[4], oy[4];
-      v[c].stay_packed();
-      v[c].grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
+      if constexpr (HOLD) {
+        held[c].stay_packed();
+        held[c].grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
+      } else {
+        columns(i, here.st, col).grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
+      }
       if (col < p.h) {
         Vec8<T>::store(static_cast<T*>(p.dx) + row * p.h + col, ox);
         Vec8<T>::store(static_cast<T*>(p.dy) + row * p.h + col, oy);
       }
     }
+    if (i + 1 < n) ok = take_sums(i + 1, next);
   }
   grid_dependents_may_start();  // the sums below may be scheduled; they wait for this grid's end
-  if (aborted && tid == 0)
-    for (int64_t k = i; k < issued; ++k) ring.wait(k, status, 64);
+  if (RING && aborted && tid == 0) ring.drain(i, issued, status, 64);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int col = (tid + c * NT) * 8;
@@ -499,53 +545,69 @@ __device__ __forceinline__ float group_sum(float v, int group) {
   return v;
 }
 
+// A group's rows are `groups` apart; the next one's values are on their way while one is worked on (65536 rows of 256 and
+// 512: 32.3 and 51.3 us without, see below).
 template <typename T, int CH>
 __global__ void __launch_bounds__(kSmallThreads) residual_norm_small_kernel(const __grid_constant__ Forward p, int group) {
   const int gl = threadIdx.x & (group - 1);
   const int64_t groups = static_cast<int64_t>(gridDim.x) * (kSmallThreads / group);
   const F2 alpha = f2_make(p.alpha, p.alpha), zero = f2_make(0.f, 0.f);
   // all lanes of a warp make the same number of rounds: the shuffles need them
-  const int64_t lead = static_cast<int64_t>(blockIdx.x) * (kSmallThreads / group) + threadIdx.x / group;
-  const int64_t warp_lead = lead - (threadIdx.x & 31) / group;
-  for (int64_t at = 0; warp_lead + at < p.rows; at += groups) {
-    const bool live = lead + at < p.rows;
-    const int64_t row = live ? lead + at : p.rows - 1;
-    const int64_t seq = p.gate ? row / p.s : 0;
-    Vec8<T> xv[CH], yv[CH];
-    F2 ss = zero;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (kSmallThreads / group) + threadIdx.x / group;
+  int64_t warp_row = row - (threadIdx.x & 31) / group;
+  F2 wt[CH][4], pre[CH][4];
+  int64_t seq_end = 0;  // of the sequence whose gate wt holds
+#pragma unroll
+  for (int c = 0; c < CH; ++c) load_gain(pre[c], p.pre, (gl + c * group) * 8, p.h);
+  Vec8<T> xv[CH], yv[CH];
+  auto load = [&](int64_t r) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (gl + c * group) * 8;
       xv[c].zero();
       yv[c].zero();
-      if (col < p.h) {
-        xv[c].load(static_cast<const T*>(p.x) + row * p.h + col);
-        yv[c].load(static_cast<const T*>(p.y) + row * p.h + col);
+      if (r < p.rows && col < p.h) {
+        xv[c].load(static_cast<const T*>(p.x) + r * p.h + col);
+        yv[c].load(static_cast<const T*>(p.y) + r * p.h + col);
       }
-      F2 f[4];
-      yv[c].unpack(f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ss = f2_fma(f[e], f[e], ss);
     }
+  };
+  load(row);
+  for (; warp_row < p.rows; row += groups, warp_row += groups) {
+    const bool live = row < p.rows;
+    if (live && row >= seq_end) {
+      const int64_t seq = row / p.s;
+      seq_end = (seq + 1) * p.s;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (gl + c * group) * 8;
+        F2 g[4];
+        load_gain(wt[c], p.post, col, p.h);
+        load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wt[c][e] = f2_mul(wt[c][e], g[e]);
+      }
+    }
+    F2 xf[CH][4], yf[CH][4], ss = zero;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      xv[c].unpack(xf[c]);
+      yv[c].unpack(yf[c]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ss = f2_fma(yf[c][e], yf[c][e], ss);
+    }
+    load(row + groups);
     float sum = group_sum(sum2(ss), group);
     const float ry = p.post ? rsqrtf(fmaf(sum, p.inv_h, p.eps)) : 1.f;
     const F2 ry2 = f2_make(ry, ry);
-    F2 rf[CH][4];
     ss = zero;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (gl + c * group) * 8;
-      F2 xf[4], yf[4], wt[4], g[4];
-      xv[c].unpack(xf);
-      yv[c].unpack(yf);
-      load_gain(wt, p.post, col, p.h);
-      load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        rf[c][e] = f2_fma(f2_mul(yf[e], ry2), f2_mul(wt[e], g[e]), f2_mul(alpha, xf[e]));
-        ss = f2_fma(rf[c][e], rf[c][e], ss);
+        xf[c][e] = f2_fma(f2_mul(yf[c][e], ry2), wt[c][e], f2_mul(alpha, xf[c][e]));  // r
+        ss = f2_fma(xf[c][e], xf[c][e], ss);
       }
-    }
     sum = group_sum(sum2(ss), group);
     const float rr = rsqrtf(fmaf(sum, p.inv_h, p.eps));
     const F2 rr2 = f2_make(rr, rr);
@@ -553,13 +615,11 @@ __global__ void __launch_bounds__(kSmallThreads) residual_norm_small_kernel(cons
     for (int c = 0; c < CH; ++c) {
       const int col = (gl + c * group) * 8;
       if (!live || col >= p.h) continue;
-      Vec8<T>::store(static_cast<T*>(p.r) + row * p.h + col, rf[c]);
+      Vec8<T>::store(static_cast<T*>(p.r) + row * p.h + col, xf[c]);
       if (p.pre) {
-        F2 pre[4];
-        load_gain(pre, p.pre, col, p.h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rf[c][e] = f2_mul(f2_mul(rf[c][e], rr2), pre[e]);
-        Vec8<T>::store(static_cast<T*>(p.u) + row * p.h + col, rf[c]);
+        for (int e = 0; e < 4; ++e) xf[c][e] = f2_mul(f2_mul(xf[c][e], rr2), pre[c][e]);
+        Vec8<T>::store(static_cast<T*>(p.u) + row * p.h + col, xf[c]);
       }
     }
   }
@@ -630,23 +690,32 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
         acc_s[c][e] = zero;
       }
     }
-    for (; at < end; at += ngroups) {  // the same for every thread
-      const int64_t row = at + tid / group;
-      const bool live = row < end;
-      GradColumns<T> v[CH];
-      F2 s2[6] = {zero, zero, zero, zero, zero, zero};
+    GradColumns<T> v[CH];
+    auto load = [&](int64_t row) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = (gl + c * group) * 8;
         v[c].zero();
-        if (live && col < p.h) {
+        if (row < end && col < p.h) {
           if (p.y) v[c].y.load(static_cast<const T*>(p.y) + row * p.h + col);
           if (p.r) v[c].r.load(static_cast<const T*>(p.r) + row * p.h + col);
           if (p.dr) v[c].dr.load(static_cast<const T*>(p.dr) + row * p.h + col);
           if (p.du) v[c].du.load(static_cast<const T*>(p.du) + row * p.h + col);
         }
-        v[c].sums(wt[c], pre[c], s2);
       }
+    };
+    load(at + tid / group);
+    for (; at < end; at += ngroups) {  // the same for every thread
+      const int64_t row = at + tid / group;
+      const bool live = row < end;
+      F2 s2[6] = {zero, zero, zero, zero, zero, zero};
+      GradColumns<T> now[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        now[c] = v[c];
+        now[c].sums(wt[c], pre[c], s2);
+      }
+      if constexpr (sizeof(T) == 2 || CH == 1) load(row + ngroups);  // (no registers for it in the others)
       float total[6];
 #pragma unroll
       for (int k = 0; k < 6; ++k) total[k] = group_sum(sum2(s2[k]), group);
@@ -655,13 +724,14 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       for (int c = 0; c < CH; ++c) {
         const int col = (gl + c * group) * 8;
         F2 ox[4], oy[4];
-        v[c].stay_packed();
-        v[c].grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
+        now[c].stay_packed();
+        now[c].grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
         if (live && col < p.h) {
           Vec8<T>::store(static_cast<T*>(p.dx) + row * p.h + col, ox);
           Vec8<T>::store(static_cast<T*>(p.dy) + row * p.h + col, oy);
         }
       }
+      if constexpr (sizeof(T) == 4 && CH == 2) load(row + ngroups);
     }
     at = end;
     if (p.slots || p.post) {
@@ -790,7 +860,7 @@ cudaError_t forward_for(const Forward& p, cudaStream_t stream, const DeviceCtx& 
   if (p.h <= kSmallH) {
     const int group = small_group(p.h);
     const int64_t need = (p.rows * group + kSmallThreads - 1) / kSmallThreads;
-    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(ctx.num_sms) * 32));
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(ctx.num_sms) * 4));
     if (p.h <= 256)
       residual_norm_small_kernel<T, 1><<<ctas, kSmallThreads, 0, stream>>>(p, group);
     else
@@ -803,11 +873,12 @@ cudaError_t forward_for(const Forward& p, cudaStream_t stream, const DeviceCtx& 
   return forward_rows<T, 512, 2>(p, stream, ctx);
 }
 
-template <typename T, int NT, int CH, int MINB>
-cudaError_t backward_rows(Backward p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
+template <typename T, int NT, int CH, int MINB, bool HOLD, bool RING = true>
+cudaError_t backward_rows(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
   static SmemLimit limit;
-  const int stages = std::max(1, std::min<int>(3, static_cast<int>(200 * 1024 / ring_smem(4, p.h, sizeof(T), 1))));
-  auto kernel = residual_norm_row_backward_kernel<T, NT, CH, MINB>;
+  // the row whose gradients are worked out, the next one, and one on its way
+  const int stages = RING ? std::min<int>(3, static_cast<int>(200 * 1024 / ring_smem(4, p.h, sizeof(T), 1))) : 0;
+  auto kernel = residual_norm_row_backward_kernel<T, NT, CH, MINB, HOLD, RING>;
   const size_t smem = ring_smem(4, p.h, sizeof(T), stages);
   cudaError_t e = allow_smem(&limit, kernel, 200 * 1024, ctx);
   if (e != cudaSuccess) return e;
@@ -828,15 +899,17 @@ cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, 
       residual_norm_small_backward_kernel<T, 2><<<static_cast<unsigned>(*ctas), kSmallThreads, 0, stream>>>(p, group);
     return cudaGetLastError();
   }
-  if (p.h <= 1024) return backward_rows<T, 128, 1, 4>(p, ctas, stream, ctx);
+  constexpr bool kHold = sizeof(T) == 4;
+  if (p.h <= 1024) return backward_rows<T, 128, 1, 4, kHold>(p, ctas, stream, ctx);
   if constexpr (sizeof(T) == 2) {
-    if (p.h <= 2048) return backward_rows<T, 128, 2, 4>(p, ctas, stream, ctx);
-    if (p.h <= 4096) return backward_rows<T, 256, 2, 2>(p, ctas, stream, ctx);
+    if (p.h <= 2048) return backward_rows<T, 128, 2, 4, kHold>(p, ctas, stream, ctx);
+    if (p.h <= 4096) return backward_rows<T, 256, 2, 2, kHold>(p, ctas, stream, ctx);
   } else {
-    if (p.h <= 2048) return backward_rows<T, 256, 1, 2>(p, ctas, stream, ctx);
-    if (p.h <= 4096) return backward_rows<T, 512, 1, 1>(p, ctas, stream, ctx);
+    if (p.h <= 2048) return backward_rows<T, 256, 1, 2, kHold>(p, ctas, stream, ctx);
+    if (p.h <= 4096) return backward_rows<T, 512, 1, 1, kHold>(p, ctas, stream, ctx);
+    if (p.h > 6392) return backward_rows<T, 512, 2, 1, false, false>(p, ctas, stream, ctx);  // two rows do not fit
   }
-  return backward_rows<T, 512, 2, 1>(p, ctas, stream, ctx);
+  return backward_rows<T, 512, 2, 1, kHold>(p, ctas, stream, ctx);
 }
 
 tpmlp_status check_norm_shape(float alpha, float eps, int64_t b, int64_t s, int64_t h, tpmlp_dtype dt) {
