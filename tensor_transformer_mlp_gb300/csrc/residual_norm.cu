@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
   constexpr int NW = NT / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][2][NW];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nt = blockDim.x;  // at most NT, what the row needs
+  const int wl = lane & (NW - 1);  // the warp whose share this lane adds
   const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), n = first_row(p.rows, blockIdx.x + 1, gridDim.x) - first;
   RowRing<2> ring;
   ring.smem = smem;
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
   F2 wt[CH][4], pre[CH][4];
   int64_t seq = -1, seq_end = 0;  // the sequence whose gate wt holds, and its last row's successor
 #pragma unroll
-  for (int c = 0; c < CH; ++c) load_gain(pre[c], p.pre, (tid + c * NT) * 8, p.h);
+  for (int c = 0; c < CH; ++c) load_gain(pre[c], p.pre, (tid + c * nt) * 8, p.h);
   const F2 alpha = f2_make(p.alpha, p.alpha), zero = f2_make(0.f, 0.f);
   int64_t i = 0;
   int aborted = 0;
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
       seq_end = (seq + 1) * p.s;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int col = (tid + c * NT) * 8;
+        const int col = (tid + c * nt) * 8;
         F2 g[4];
         load_gain(wt[c], p.post, col, p.h);
         load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
     F2 ss = zero;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (tid + c * NT) * 8;
+      const int col = (tid + c * nt) * 8;
       xv[c].zero();
       yv[c].zero();
       if (col < p.h) {
@@ -244,13 +245,13 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
       ring.issue(i + stages, at.st);
       issued = i + stages + 1;
     }
-    const float ry = p.post ? rsqrtf(fmaf(lane_sum<NW>(red[par][0][lane & (NW - 1)]), p.inv_h, p.eps)) : 1.f;
+    const float ry = p.post ? rsqrtf(fmaf(lane_sum<NW>(wl * 32 < nt ? red[par][0][wl] : 0.f), p.inv_h, p.eps)) : 1.f;
     F2 rf[CH][4];
     ss = zero;
     const F2 ry2 = f2_make(ry, ry);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (tid + c * NT) * 8;
+      const int col = (tid + c * nt) * 8;
       F2 xf[4], yf[4];
       yv[c].stay_packed();
       xv[c].unpack(xf);
@@ -266,11 +267,11 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
       const float rs = lane_sum<32>(sum2(ss));
       if (lane == 0) red[par][1][w] = rs;
       __syncthreads();
-      const float rr = rsqrtf(fmaf(lane_sum<NW>(red[par][1][lane & (NW - 1)]), p.inv_h, p.eps));
+      const float rr = rsqrtf(fmaf(lane_sum<NW>(wl * 32 < nt ? red[par][1][wl] : 0.f), p.inv_h, p.eps));
       const F2 rr2 = f2_make(rr, rr);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int col = (tid + c * NT) * 8;
+        const int col = (tid + c * nt) * 8;
 #pragma unroll
         for (int e = 0; e < 4; ++e) rf[c][e] = f2_mul(f2_mul(rf[c][e], rr2), pre[c][e]);
         if (col < p.h) Vec8<T>::store(static_cast<T*>(p.u) + row * p.h + col, rf[c]);
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
   constexpr int NW = NT / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][NW][8];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nt = blockDim.x;  // at most NT, what the row needs
   const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), n = first_row(p.rows, blockIdx.x + 1, gridDim.x) - first;
   RowRing<4> ring;
   ring.smem = smem;
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
   GradColumns<T> held[HOLD ? CH : 1];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    load_gain(pre[c], p.pre, (tid + c * NT) * 8, p.h);
+    load_gain(pre[c], p.pre, (tid + c * nt) * 8, p.h);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc_s[c][e] = acc_pre[c][e] = zero;
   }
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
     if (row >= seq_end) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int col = (tid + c * NT) * 8;
+        const int col = (tid + c * nt) * 8;
         if (seq >= 0 && col < p.h) leave_sequence(p, seq, col, acc_s[c], none_left);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc_s[c][e] = zero;
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
       seq_end = (seq + 1) * p.s;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int col = (tid + c * NT) * 8;
+        const int col = (tid + c * nt) * 8;
         F2 g[4];
         load_gain(wt[c], p.post, col, p.h);
         load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
     F2 s2[6] = {zero, zero, zero, zero, zero, zero};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const GradColumns<T> v = columns(i, at.st, (tid + c * NT) * 8);
+      const GradColumns<T> v = columns(i, at.st, (tid + c * nt) * 8);
       if constexpr (HOLD) held[c] = v;
       v.sums(wt[c], pre[c], s2);
     }
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
 #pragma unroll
     for (int k = 0; k < (NW + 3) / 4; ++k) {
       const int warp = (lane >> 3) + 4 * k;
-      if (warp < NW) part += red[i & 1][warp][lane & 7];
+      if (warp * 32 < nt) part += red[i & 1][warp][lane & 7];
     }
     part += __shfl_xor_sync(0xffffffffu, part, 8);
     part += __shfl_xor_sync(0xffffffffu, part, 16);
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
     const int64_t row = first + i;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (tid + c * NT) * 8;
+      const int col = (tid + c * nt) * 8;
       F2 ox[4], oy[4];
       if constexpr (HOLD) {
         held[c].stay_packed();
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
   if (RING && aborted && tid == 0) ring.drain(i, issued, status, 64);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int col = (tid + c * NT) * 8;
+    const int col = (tid + c * nt) * 8;
     if (col < p.h) {
       leave_sequence(p, seq, col, acc_s[c], none_left);
       Vec8<float>::store(p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * p.h + col, acc_pre[c]);
@@ -841,6 +842,9 @@ size_t ring_smem(int tensors, int h, size_t size, int stages) {
   return stages * (static_cast<size_t>(tensors) * h * size + sizeof(uint64_t));
 }
 
+// Threads of a CTA: a row's vectors of 8 columns, CH a thread, in whole warps.
+int row_threads(int h, int ch) { return ((h + 8 * ch - 1) / (8 * ch) + 31) / 32 * 32; }
+
 template <typename T, int NT, int CH>
 cudaError_t forward_rows(const Forward& p, cudaStream_t stream, const DeviceCtx& ctx) {
   static SmemLimit limit;
@@ -850,8 +854,9 @@ cudaError_t forward_rows(const Forward& p, cudaStream_t stream, const DeviceCtx&
   cudaError_t e = allow_smem(&limit, kernel, 200 * 1024, ctx);
   if (e != cudaSuccess) return e;
   int64_t ctas;
-  if ((e = wave(&ctas, kernel, NT, smem, p.rows, ctx)) != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(ctas), NT, smem, stream>>>(p, std::max(stages, 2), ctx.status);
+  const int threads = row_threads(p.h, CH);
+  if ((e = wave(&ctas, kernel, threads, smem, p.rows, ctx)) != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(ctas), threads, smem, stream>>>(p, std::max(stages, 2), ctx.status);
   return cudaGetLastError();
 }
 
@@ -867,7 +872,7 @@ cudaError_t forward_for(const Forward& p, cudaStream_t stream, const DeviceCtx& 
       residual_norm_small_kernel<T, 2><<<ctas, kSmallThreads, 0, stream>>>(p, group);
     return cudaGetLastError();
   }
-  if (p.h <= 1024) return forward_rows<T, 128, 1>(p, stream, ctx);
+  if (p.h <= 1024) return forward_rows<T, 64, 2>(p, stream, ctx);
   if (p.h <= 2048) return forward_rows<T, 128, 2>(p, stream, ctx);
   if (p.h <= 4096) return forward_rows<T, 256, 2>(p, stream, ctx);
   return forward_rows<T, 512, 2>(p, stream, ctx);
@@ -882,8 +887,9 @@ cudaError_t backward_rows(const Backward& p, int64_t* ctas, cudaStream_t stream,
   const size_t smem = ring_smem(4, p.h, sizeof(T), stages);
   cudaError_t e = allow_smem(&limit, kernel, 200 * 1024, ctx);
   if (e != cudaSuccess) return e;
-  if ((e = wave(ctas, kernel, NT, smem, std::min<int64_t>(p.rows, kMaxCtas), ctx)) != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(*ctas), NT, smem, stream>>>(p, stages, ctx.status);
+  const int threads = row_threads(p.h, CH);
+  if ((e = wave(ctas, kernel, threads, smem, std::min<int64_t>(p.rows, kMaxCtas), ctx)) != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(*ctas), threads, smem, stream>>>(p, stages, ctx.status);
   return cudaGetLastError();
 }
 
