@@ -97,6 +97,7 @@ struct Forward {
   float alpha, eps, inv_h;
   int64_t rows, s;
   int h;
+  bool run_of_rows;  // a CTA's rows lie behind one another
 };
 
 struct Backward {
@@ -124,6 +125,7 @@ struct RowRing {
   uint8_t* smem;
   uint64_t* full;
   uint32_t row_bytes;
+  int64_t step;  // bytes between the CTA's rows
   int stages;
   const uint8_t* src[NTEN];  // the CTA's first row of each tensor; null: none
   __device__ __forceinline__ uint32_t stage_bytes() const { return NTEN * row_bytes; }
@@ -140,7 +142,7 @@ struct RowRing {
     mbar_arrive_expect_tx(&full[st], n);
 #pragma unroll
     for (int k = 0; k < NTEN; ++k)
-      if (src[k]) bulk_load(dst + k * row_bytes, src[k] + i * row_bytes, row_bytes, &full[st]);
+      if (src[k]) bulk_load(dst + k * row_bytes, src[k] + i * step, row_bytes, &full[st]);
   }
   template <typename T>
   __device__ __forceinline__ const T* at(int st, int k) const {
@@ -172,7 +174,7 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// Rows [first, first + n) go through the ring; a row's two sums each meet behind one barrier, every warp adding the
+// Rows go through the ring; a row's two sums each meet behind one barrier, every warp adding the
 // warps' shares in the same order. A wait that runs out ends the CTA at the next barrier.
 template <typename T, int NT, int CH>
 __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_constant__ Forward p, int stages,
@@ -182,10 +184,14 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
   __shared__ float red[2][2][NW];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nt = blockDim.x;  // at most NT, what the row needs
   const int wl = lane & (NW - 1);  // the warp whose share this lane adds
-  const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), n = first_row(p.rows, blockIdx.x + 1, gridDim.x) - first;
+  // Every gridDim.x-th row, so that all CTAs are at neighbouring rows (b2 s4096 h4096: 46.8 us, with a run of rows each
+  // 49.1); but a run of rows where that would bring another sequence's gate with nearly every row (b40 s512 h640 20.0, 25.1).
+  const int64_t by = p.run_of_rows ? 1 : gridDim.x, first = p.run_of_rows ? first_row(p.rows, blockIdx.x, gridDim.x) : blockIdx.x;
+  const int64_t n = p.run_of_rows ? first_row(p.rows, blockIdx.x + 1, gridDim.x) - first : (p.rows - first + by - 1) / by;
   RowRing<2> ring;
   ring.smem = smem;
   ring.row_bytes = static_cast<uint32_t>(p.h) * sizeof(T);
+  ring.step = by * ring.row_bytes;
   ring.stages = stages;
   ring.full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(stages) * ring.stage_bytes());
   ring.src[0] = static_cast<const uint8_t*>(p.x) + first * ring.row_bytes;
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
   int aborted = 0;
   RowStage at;
   for (; i < n; ++i, at.next(stages)) {
-    const int64_t row = first + i;
+    const int64_t row = first + i * by;
     if (row >= seq_end) {
       seq = row / p.s;
       seq_end = (seq + 1) * p.s;
@@ -402,6 +408,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
   RowRing<4> ring;
   ring.smem = smem;
   ring.row_bytes = static_cast<uint32_t>(p.h) * sizeof(T);
+  ring.step = ring.row_bytes;
   ring.stages = stages;
   ring.full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(stages) * ring.stage_bytes());
   const void* src[4] = {p.y, p.r, p.dr, p.du};
@@ -846,7 +853,7 @@ size_t ring_smem(int tensors, int h, size_t size, int stages) {
 int row_threads(int h, int ch) { return ((h + 8 * ch - 1) / (8 * ch) + 31) / 32 * 32; }
 
 template <typename T, int NT, int CH>
-cudaError_t forward_rows(const Forward& p, cudaStream_t stream, const DeviceCtx& ctx) {
+cudaError_t forward_rows(Forward p, cudaStream_t stream, const DeviceCtx& ctx) {
   static SmemLimit limit;
   const int stages = std::min<int>(4, static_cast<int>(100 * 1024 / ring_smem(2, p.h, sizeof(T), 1)));
   auto kernel = residual_norm_row_kernel<T, NT, CH>;
@@ -856,6 +863,7 @@ cudaError_t forward_rows(const Forward& p, cudaStream_t stream, const DeviceCtx&
   int64_t ctas;
   const int threads = row_threads(p.h, CH);
   if ((e = wave(&ctas, kernel, threads, smem, p.rows, ctx)) != cudaSuccess) return e;
+  p.run_of_rows = p.gate && p.s < 4 * ctas && p.s < p.rows;
   kernel<<<static_cast<unsigned>(ctas), threads, smem, stream>>>(p, std::max(stages, 2), ctx.status);
   return cudaGetLastError();
 }
@@ -960,7 +968,7 @@ tpmlp_status tpmlp_residual_norm(const void* x, const void* y, const float* gamm
     return err(TPMLP_ERR_INVALID, "r or u overlaps another tensor of the call (they may be x or y)");
   DeviceCtx ctx;
   TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
-  const Forward p{x, y, gamma_post, gate, gamma_pre, r, u, alpha, eps, 1.0f / static_cast<float>(h), rows, s, static_cast<int>(h)};
+  const Forward p{x, y, gamma_post, gate, gamma_pre, r, u, alpha, eps, 1.0f / static_cast<float>(h), rows, s, static_cast<int>(h), false};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   TPMLP_PASS_CUDA(dt == TPMLP_BF16 ? forward_for<__nv_bfloat16>(p, st, ctx) : forward_for<float>(p, st, ctx), "residual norm");
   return TPMLP_OK;
