@@ -725,7 +725,7 @@ def _scratch(nbytes: int, like: torch.Tensor):
     """A workspace of nbytes on like's device and its address; none for 0 bytes."""
     if nbytes == 0:
         return None, None
-    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     return ws, ws.data_ptr()
 
 
@@ -737,8 +737,8 @@ def gated_forward(X, A, B, t: int = 1, act: str = "silu", save: bool = True, str
     here, st = _where(_device(X, A, B), stream)
     with here:
         O = torch.empty_like(X)
-        Z = X.new_empty(n, 2 * m) if save else None
-        Y = X.new_empty(n, m)
+        Z = torch.empty((n, 2 * m), dtype=X.dtype, device=X.device) if save else None
+        Y = torch.empty((n, m), dtype=X.dtype, device=X.device)
         ws_bytes = lib.tpmlp_gated_forward_workspace_size(n, d, m, t, dt)
         ws, ws_ptr = _scratch(ws_bytes, X)
         _check(lib.tpmlp_gated_forward(X.data_ptr(), A.data_ptr(), B.data_ptr(), O.data_ptr(), _ptr(Z), Y.data_ptr(), n, d,
@@ -843,8 +843,8 @@ def residual_norm_backward(y, r, dr, du, gamma_post=None, gate=None, gamma_pre=N
     dx and dy. Returns (dx, dy, dgamma_post, dgate, dgamma_pre), None for a gain or gate that is not there."""
     like = y if y is not None else dr if dr is not None else du
     shape, dtype = like.shape, like.dtype
-    for name, t in (("y", y), ("r", r), ("dr", dr), ("du", du), ("dx", dx), ("dy", dy)):
-        if t is not None:
+    for t, name in ((y, "y"), (r, "r"), (dr, "dr"), (du, "du"), (dx, "dx"), (dy, "dy")):
+        if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
             _alike(t, shape, dtype, name)
     b, s, h = _residual_args(like, gamma_post, gate, gamma_pre)
     dt = _dt(like)

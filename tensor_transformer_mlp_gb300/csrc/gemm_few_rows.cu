@@ -31,7 +31,6 @@ constexpr int kSmemBudget = 220 * 1024;
 constexpr int kBarrierBytes = 256;
 constexpr int kThreads = 320;           // producer, MMA issuer, eight epilogue warps
 constexpr int kSms = 152;               // what splits and workspaces are chosen for, with or without a device
-constexpr int kMaxItems = 4 * kSms;     // CTAs' shares of a product
 
 struct Plan {
   int n, cols, num_kb;   // tokens, output columns (of Y for the gate), k-blocks
@@ -418,13 +417,13 @@ __global__ void __launch_bounds__(kJoinThreads) few_rows_join_kernel(const __gri
 
 // Estimated time of a product, in us: rounds of items, each k-block at the slowest of the weights' share of HBM
 // (6.7 TB/s), the tensor core (12.7 TFLOP/s an SM) and what an SM takes in (72 KB a us; measured 65 at 37 tokens and
-// K = 1024, 83 at 256 and K = 16384); what a round costs beside its k-blocks; the shares' way to L2 and back (8 TB/s) and the second kernel; the
-// launch of pairs.
+// K = 1024, 83 at 256 and K = 16384); what a round costs beside its k-blocks; the shares' way to L2 and back (5 TB/s) and
+// the second kernel; the launch of pairs.
 double plan_time(const Plan& p) {
   const double ctas = static_cast<double>(p.items) * p.ranks, busy = std::min<double>(ctas, kSms);
   const double kb = std::max({kWeightBytes * busy / 6.7e6, 2.0 * kTileCols * p.nt * kBK / 12.7e6, plan_stage_bytes(p) / 72e3});
   const double rounds = std::ceil(ctas / kSms), blocks = std::ceil(static_cast<double>(p.num_kb) / p.splits);
-  return rounds * (blocks * kb + 1.0 + p.nt / 64.0) + (p.splits > 1 ? 5.0 + ctas * p.nt * kTileCols * 8.0 / 8e6 : 0.0) +
+  return rounds * (blocks * kb + 1.0 + p.nt / (p.splits > 1 ? 64.0 : 20.0)) + (p.splits > 1 ? 3.0 + ctas * p.nt * kTileCols * 8.0 / 5e6 : 0.0) +
          (p.ranks - 1) * 2.0;
 }
 
@@ -448,8 +447,11 @@ Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool gate) 
     p.col_tiles = static_cast<int>(gate ? m / p.unit * ((p.unit + w - 1) / w) : (cols + w - 1) / w);
     p.tiles = p.col_tiles * p.token_tiles;
     p.stages = std::min<int>(kMaxStages, (kSmemBudget - kBarrierBytes - 1024) / plan_stage_bytes(p));
-    const int most = std::min(p.num_kb, std::max(1, kMaxItems / (p.tiles * ranks)));
-    for (p.splits = 1; p.splits <= most; ++p.splits) {
+    // the numbers of splits that fill one, two and three waves of CTAs, parts of the first, and one
+    const int wave = kSms / (p.tiles * ranks);
+    for (const int splits : {1, wave / 4, wave / 2, 3 * wave / 4, wave, 2 * kSms / (p.tiles * ranks), 3 * kSms / (p.tiles * ranks)}) {
+      p.splits = std::min(splits, p.num_kb);
+      if (p.splits < 1) continue;
       p.items = p.tiles * p.splits;
       const double time = plan_time(p);
       if (best.tiles == 0 || time < best_time) {
@@ -541,14 +543,20 @@ cudaError_t run(const Plan& p, const void* tokens, int64_t k, const void* w, int
 
 }  // namespace
 
-// Against the SM-pair GEMM (gemm_tc.cu), whose launch takes some 7 us and 0.36 us a k-block for each wave of 256 x 256
-// tiles over 76 pairs.
+// Against the SM-pair GEMM (gemm_tc.cu), whose launch takes some 6 us and 0.36 us a k-block for each wave of 256 x 256
+// accumulators over 76 pairs. Measured, d4096 m16384: FC1 of 4 tokens 46.5 us here and 52 there, of 200 tokens 58 and 52; FC2
+// of 200 tokens 36 and 91.
+bool pays(const Plan& p, int64_t pair_tiles) {
+  return 4.5 + plan_time(p) < 6.0 + 0.36 * static_cast<double>(p.num_kb) * std::ceil(static_cast<double>(pair_tiles) / (kSms / 2));
+}
+
 bool gemm_takes_few_rows(int64_t n, int64_t cols, int64_t k) {
   const int64_t tiles = (n + 255) / 256 * ((cols + 255) / 256);
-  if (tiles > 76) return false;
-  return 5.0 + plan_time(make_plan(n, cols, k, 0, 1, false)) < 7.0 + 0.36 * static_cast<double>((k + kBK - 1) / kBK);
+  return tiles <= kSms && pays(make_plan(n, cols, k, 0, 1, false), tiles);
 }
-bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m) { return n <= kMaxTokens; }
+bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m, int t) {
+  return n <= kMaxTokens && pays(make_plan(n, m, d, m, t, true), (m + kBlock - 1) / kBlock);
+}
 
 size_t gated_fc1_few_rows_workspace(int64_t n, int64_t d, int64_t m, int t) { return slot_bytes(make_plan(n, m, d, m, t, true)); }
 

@@ -1185,6 +1185,16 @@ __device__ __forceinline__ void load_gate_z(uint4 (&zg)[4], uint4 (&zu)[4], cons
   }
 }
 
+// Both parts of Z into L2: N blocks of 64 columns from y on (in a tile that starts at y_block), 128 rows from row on.
+template <int N>
+__device__ __forceinline__ void prefetch_gate_z(const EpiParams& ep, const CUtensorMap* tm_z, int y, int y_block, int row) {
+  for (int j = 0; j < N && gated_in_run(y + j * 64, y_block, ep.unit); ++j) {
+    const int shard = (y + j * 64) / ep.shard, x = y + j * 64 - shard * ep.shard;
+    tma_prefetch_l2_3d(tm_z, x, 2 * shard, row);
+    tma_prefetch_l2_3d(tm_z, x, 2 * shard + 1, row);
+  }
+}
+
 // D of two columns for the forms kept out of line: {gate word, up word}.
 __device__ __noinline__ uint2 gate_grad_other2(float a0, float a1, uint32_t zg, uint32_t zu, int kind) {
   const float2 g = unpack_bf16x2(zg), u = unpack_bf16x2(zu);
@@ -1376,6 +1386,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int j = 0; j < BN_T / 128; ++j) b_box[j] = EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_col + j * 64;
         const unsigned int active = static_cast<unsigned int>(min(num_pairs, num_tiles - round * num_pairs));
         for (int kb = 0; kb < num_kb; ++kb) {
+          if constexpr (EPI == kEpiGateGrad) {  // Z of this CTA's rows into L2 some k-blocks before the epilogue reads it
+            if (kb == max(0, num_kb - kAuxPrefetchKb)) prefetch_gate_z<kTileN / 64>(ep, &tmap_c2, y0, y0, a_row);
+          }
           if (pacer && kb % kPaceKb == 0) {
             pace_wait(pace, pace_target, kPaceWaitNs);
             atomicAdd(pace, 1u);
@@ -1705,12 +1718,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if constexpr (EPI == kEpiGateGrad) {
             if (kb == max(0, num_kb - kAuxPrefetchKb)) {
               const int y0 = gated_column(nb, ep.unit, 2 * kHalfN);
-              for (int j = (half == 1 ? 4 : 0); j < (half == 0 ? 4 : 8); ++j) {
-                const int y = y0 + j * 64, shard = y / ep.shard;
-                if (!gated_in_run(y, y0, ep.unit)) break;
-                tma_prefetch_l2_3d(&tmap_c2, y - shard * ep.shard, 2 * shard, a_row);
-                tma_prefetch_l2_3d(&tmap_c2, y - shard * ep.shard, 2 * shard + 1, a_row);
-              }
+              if (half != 1) prefetch_gate_z<kHalfN / 64>(ep, &tmap_c2, y0, y0, a_row);
+              if (half != 0) prefetch_gate_z<kHalfN / 64>(ep, &tmap_c2, y0 + kHalfN, y0, a_row);
             }
           }
           if (pacer && kb % kPaceKb == 0) {
@@ -2141,7 +2150,8 @@ template <bool A_MN, bool B_MN, int EPI, int BN_T = BN>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutMaps& om, int M, int N, int K,
                         const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx) {
   auto kernel = gemm_bf16_pair_kernel<A_MN, B_MN, EPI, BN_T>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM_BYTES);
+  static SmemLimit limit;
+  cudaError_t e = allow_smem(&limit, kernel, PAIR_SMEM_BYTES, ctx);
   if (e != cudaSuccess) return e;
   const int64_t nb = BN_T == BN ? n_blocks<EPI>(N, ep, false) : gated_blocks(N, ep.unit, BN_T);
   const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * nb;
@@ -2192,7 +2202,8 @@ template <bool A_MN, bool B_MN, int EPI>
 cudaError_t launch_wide(const CUtensorMap& ta, const CUtensorMap& tb, const OutMaps& om, int M, int N, int K,
                         const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx) {
   auto kernel = gemm_bf16_wide_kernel<A_MN, B_MN, EPI>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM_BYTES);
+  static SmemLimit limit;
+  cudaError_t e = allow_smem(&limit, kernel, WIDE_SMEM_BYTES, ctx);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * n_blocks<EPI>(N, ep, true);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;

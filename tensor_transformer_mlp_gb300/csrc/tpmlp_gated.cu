@@ -39,7 +39,7 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspaces of the products that may run with few rows: one after another in the forward.
 size_t fc1_bytes(int64_t n, int64_t d, int64_t m, int t) {
-  return gated_fc1_takes_few_rows(n, d, m) ? round256(gated_fc1_few_rows_workspace(n, d, m, t)) : 0;
+  return gated_fc1_takes_few_rows(n, d, m, t) ? round256(gated_fc1_few_rows_workspace(n, d, m, t)) : 0;
 }
 size_t rows_bytes(int64_t n, int64_t cols, int64_t k) {
   return gemm_takes_few_rows(n, cols, k) ? round256(gemm_few_rows_workspace(n, cols, k)) : 0;
@@ -77,7 +77,7 @@ tpmlp_status tpmlp_gated_forward(const void* X, const void* A, const void* B, vo
   DeviceCtx ctx;
   TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool few = few_rows_allowed(), few1 = few && gated_fc1_takes_few_rows(n, d, m);
+  const bool few = few_rows_allowed(), few1 = few && gated_fc1_takes_few_rows(n, d, m, t);
   if (few1) {
     TPMLP_PASS_CUDA(gated_fc1_few_rows(X, A, Z_save, Y_save, n, d, m, t, act, workspace, st, ctx), "gated FC1, few rows");
   } else {

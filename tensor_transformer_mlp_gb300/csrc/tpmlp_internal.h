@@ -162,7 +162,7 @@ cudaError_t gated_dgrad1_tc(const void* g, const void* b, const void* z, void* d
 // [cols][k], bf16. `dependent`: a programmatic dependent (EpiParams::dependent) of the kernel in front, which writes no weights. Workspaces
 // 256-byte aligned, their sizes independent of the device.
 bool few_rows_allowed();  // by tpmlp_set_gemm_variant: the per-product choice is on
-bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m);
+bool gated_fc1_takes_few_rows(int64_t n, int64_t d, int64_t m, int t);
 size_t gated_fc1_few_rows_workspace(int64_t n, int64_t d, int64_t m, int t);
 cudaError_t gated_fc1_few_rows(const void* x, const void* a, void* z, void* y, int64_t n, int64_t d, int64_t m, int t, int act,
                                void* workspace, cudaStream_t stream, const DeviceCtx& ctx);
