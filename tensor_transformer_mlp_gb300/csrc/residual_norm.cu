@@ -104,8 +104,9 @@ struct Backward {
   const void *y, *r, *dr, *du;
   const float *post, *gate, *pre;
   void *dx, *dy;
-  // partials [gridDim.x][2][h]: the CTA's shares of dgamma_post and dgamma_pre; slots [gridDim.x + b][h]: S of CTA c's
-  // rows of sequence q at c + q (both only grow along the rows, so no two share a slot)
+  float* dgate;
+  // partials [gridDim.x][2][h]: the CTA's shares of dgamma_post and dgamma_pre; slots [gridDim.x][2][h] (with a gate): S of
+  // the CTA's rows of a sequence that starts before them, and of one that starts in them and ends behind them
   float *partials, *slots;
   float alpha, eps, inv_h;
   int64_t rows, s;
@@ -357,15 +358,28 @@ struct GradColumns {
   }
 };
 
-// A thread's share of what a CTA leaves of a sequence: S to its slot, and gate S added to the CTA's dgamma_post.
-__device__ __forceinline__ void leave_sequence(const Backward& p, int64_t seq, int col, const F2 (&acc)[4], bool first) {
+// A thread's share of what a CTA (rows [first, end)) leaves of a sequence: its gate's gradient, or S to a slot where other CTAs
+// have rows of it too; and gate S added to the CTA's dgamma_post.
+__device__ __forceinline__ void leave_sequence(const Backward& p, int64_t seq, int64_t first, int64_t end, int col,
+                                               const F2 (&acc)[4], bool none_left) {
   F2 g[4];
   load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
-  if (p.slots) Vec8<float>::store(p.slots + (blockIdx.x + seq) * p.h + col, acc);
+  if (p.gate) {
+    const bool starts_here = seq * p.s >= first, ends_here = (seq + 1) * p.s <= end;
+    if (starts_here && ends_here) {
+      F2 post[4], out[4];
+      load_gain(post, p.post, col, p.h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = f2_mul(post[e], acc[e]);
+      Vec8<float>::store(p.dgate + seq * p.h + col, out);
+    } else {
+      Vec8<float>::store(p.slots + (2 * static_cast<int64_t>(blockIdx.x) + (starts_here ? 1 : 0)) * p.h + col, acc);
+    }
+  }
   if (p.post) {
     float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.h + col;
     F2 old[4] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f), f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-    if (!first) {
+    if (!none_left) {
       Vec8<float> t;
       t.load(out);
       t.unpack(old);
@@ -455,7 +469,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = (tid + c * nt) * 8;
-        if (seq >= 0 && col < p.h) leave_sequence(p, seq, col, acc_s[c], none_left);
+        if (seq >= 0 && col < p.h) leave_sequence(p, seq, first, first + n, col, acc_s[c], none_left);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc_s[c][e] = zero;
       }
@@ -539,7 +553,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
   for (int c = 0; c < CH; ++c) {
     const int col = (tid + c * nt) * 8;
     if (col < p.h) {
-      leave_sequence(p, seq, col, acc_s[c], none_left);
+      leave_sequence(p, seq, first, first + n, col, acc_s[c], none_left);
       Vec8<float>::store(p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * p.h + col, acc_pre[c]);
     }
   }
@@ -742,10 +756,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       if constexpr (sizeof(T) == 4 && CH == 2) load(row + ngroups);
     }
     at = end;
-    if (p.slots || p.post) {
+    if (p.gate || p.post) {
       F2 sum[4];
       gather(acc_s, sum);
-      if (tid * 8 < p.h) leave_sequence(p, seq, tid * 8, sum, none_left);
+      if (tid * 8 < p.h) leave_sequence(p, seq, first, last, tid * 8, sum, none_left);
     }
     none_left = false;
   }
@@ -758,47 +772,51 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 // ------------------------------------------------------------------ the sums over CTAs
 
 // 32 columns a CTA. Groups of 8 threads each add every 32nd row of partials, then the groups' sums are added by a fixed
-// tree. CTAs [0, slices) sum dgamma_post, [slices, 2 slices) dgamma_pre, the others dgate, a sequence's slices after
-// another's. Launched as a programmatic dependent of the backward kernel.
+// tree. CTAs [0, slices) sum dgamma_post, [slices, 2 slices) dgamma_pre, the others dgate of the sequences that several CTAs
+// had rows of: found by sequence, or by the ends of CTAs' rows where there are fewer of those. Launched as a programmatic
+// dependent of the backward kernel.
 constexpr int kFinishThreads = 256;
 struct Finish {
   const float *partials, *slots, *post;
   float *dpost, *dpre, *dgate;
   int64_t rows, s;
   int h, slices, ctas;
+  bool by_cta;
 };
 __global__ void __launch_bounds__(kFinishThreads) residual_norm_finish_kernel(const __grid_constant__ Finish p) {
   grid_wait_for_previous();
   constexpr int kQuads = 8, kGroups = kFinishThreads / kQuads;
   __shared__ float4 grp[kGroups][kQuads];
   const int q = threadIdx.x % kQuads, g = threadIdx.x / kQuads;
-  const int64_t part = blockIdx.x / p.slices;
+  const int part = blockIdx.x / p.slices;
   const int col = (blockIdx.x % p.slices) * 32 + q * 4;
   const bool in = col < p.h;
   const float* src;
-  int64_t n, stride;
+  int64_t n, stride = 2 * static_cast<int64_t>(p.h);
   float* out;
   if (part < 2) {
     src = p.partials + part * p.h;
     n = p.ctas;
-    stride = 2 * static_cast<int64_t>(p.h);
     out = part == 0 ? p.dpost : p.dpre;
     if (!out) return;
   } else {
-    // sequence seq's rows: those of the CTAs c0 .. c1, CTA c's at slot c + seq
-    const int64_t seq = part - 2, a = seq * p.s, z = a + p.s - 1, each = p.rows / p.ctas, more = p.rows % p.ctas;
-    auto cta_of = [&](int64_t row) { return row < more * (each + 1) ? row / (each + 1) : more + (row - more * (each + 1)) / each; };
-    const int64_t c0 = cta_of(a);
-    n = cta_of(z) - c0 + 1;
-    src = p.slots + (c0 + seq) * p.h;
-    stride = p.h;
+    auto cta_of = [&](int64_t row) {
+      const int64_t each = p.rows / p.ctas, more = p.rows % p.ctas;
+      return row < more * (each + 1) ? row / (each + 1) : more + (row - more * (each + 1)) / each;
+    };
+    const int64_t seq = p.by_cta ? (first_row(p.rows, part - 1, p.ctas) - 1) / p.s : part - 2;
+    const int64_t c0 = cta_of(seq * p.s), c1 = cta_of((seq + 1) * p.s - 1);
+    if (c0 == c1 || (p.by_cta && c0 != part - 2)) return;  // written by its CTA; found at an earlier end too
+    src = p.slots + (2 * c0 + 1) * p.h;  // then slots 2 c0 + 2, 2 c0 + 4, ..
+    n = c1 - c0 + 1;
     out = p.dgate + seq * p.h;
   }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (in) {
 #pragma unroll 8
     for (int64_t k = g; k < n; k += kGroups) {
-      const float4 v = *reinterpret_cast<const float4*>(src + k * stride + col);
+      const float* from = part < 2 || k == 0 ? src + k * stride : src + k * stride - p.h;
+      const float4 v = *reinterpret_cast<const float4*>(from + col);
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
@@ -915,15 +933,15 @@ cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, 
   }
   constexpr bool kHold = sizeof(T) == 4;
   if (p.h <= 1024) return backward_rows<T, 128, 1, 4, kHold>(p, ctas, stream, ctx);
-  if constexpr (sizeof(T) == 2) {
+  if constexpr (!kHold) {
     if (p.h <= 2048) return backward_rows<T, 128, 2, 4, kHold>(p, ctas, stream, ctx);
     if (p.h <= 4096) return backward_rows<T, 256, 2, 2, kHold>(p, ctas, stream, ctx);
   } else {
     if (p.h <= 2048) return backward_rows<T, 256, 1, 2, kHold>(p, ctas, stream, ctx);
     if (p.h <= 4096) return backward_rows<T, 512, 1, 1, kHold>(p, ctas, stream, ctx);
-    if (p.h > 6392) return backward_rows<T, 512, 2, 1, false, false>(p, ctas, stream, ctx);  // two rows do not fit
+    return backward_rows<T, 512, 2, 1, false, false>(p, ctas, stream, ctx);  // no ring of two rows, nor registers for one
   }
-  return backward_rows<T, 512, 2, 1, kHold>(p, ctas, stream, ctx);
+  return backward_rows<T, 512, 2, 1, false>(p, ctas, stream, ctx);
 }
 
 tpmlp_status check_norm_shape(float alpha, float eps, int64_t b, int64_t s, int64_t h, tpmlp_dtype dt) {
@@ -940,7 +958,7 @@ constexpr const char* kAlign = "pointers must be 16-byte aligned";
 
 size_t partials_bytes(int64_t b, int64_t s, int64_t h, bool gate) {
   const int64_t rows = std::min<int64_t>(b * s, kMaxCtas);
-  return static_cast<size_t>(2 * rows + (gate ? rows + b : 0)) * h * sizeof(float);
+  return static_cast<size_t>(gate ? 4 : 2) * rows * h * sizeof(float);
 }
 
 }  // namespace
@@ -1025,19 +1043,24 @@ tpmlp_status tpmlp_residual_norm_backward(const void* y, const void* r, const vo
   if (bad) return err(TPMLP_ERR_INVALID, "an output or the workspace overlaps another tensor of the call (dx and dy may be y, r, dr or du)");
   DeviceCtx ctx;
   TPMLP_PASS_CUDA(get_device_ctx(&ctx), "device context");
+  if (!gate) {  // one run of tokens
+    s = rows;
+    b = 1;
+  }
   float* partials = static_cast<float*>(workspace);
   float* slots = gate ? partials + 2 * std::min<int64_t>(rows, kMaxCtas) * h : nullptr;
-  const Backward p{y, r, dr, du, gamma_post, gate, gamma_pre, dx, dy, partials, slots, alpha, eps,
+  const Backward p{y, r, dr, du, gamma_post, gate, gamma_pre, dx, dy, dgate, partials, slots, alpha, eps,
                    1.0f / static_cast<float>(h), rows, s, static_cast<int>(h)};
   int64_t ctas = 0;
   TPMLP_PASS_CUDA(dt == TPMLP_BF16 ? backward_for<__nv_bfloat16>(p, &ctas, st, ctx) : backward_for<float>(p, &ctas, st, ctx),
                   "residual norm backward");
   if (!dgamma_post && !dgamma_pre && !dgate) return TPMLP_OK;
   const int slices = static_cast<int>((h + 31) / 32);
+  const bool by_cta = b > ctas - 1;
   const Finish f{partials, slots, gamma_post, dgamma_post, dgamma_pre, dgate, rows, s, static_cast<int>(h), slices,
-                 static_cast<int>(ctas)};
+                 static_cast<int>(ctas), by_cta};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((2 + (gate ? b : 0)) * slices), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((2 + (!gate ? 0 : by_cta ? ctas - 1 : b)) * slices), 1, 1);
   cfg.blockDim = dim3(kFinishThreads, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
