@@ -255,3 +255,59 @@ def test_two_calls_at_once(n):
         torch.cuda.synchronize()
         for w, g in zip(want, got):
             assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+# ----------------------------------------------------------------------- sums split across the SMs
+
+# Few tokens or small outputs with a long sum (n, d, m, t). FC1 split, with shards of whole column blocks and with ragged
+# ones; on pairs of SMs; unsplit. FC2 and dX split; of two and three tiles of tokens; on pairs of SMs; output columns that
+# end inside a tile and inside a CTA's half of it.
+SPLIT = [(5, 4096, 256, 2), (5, 4096, 264, 3), (150, 4096, 1000, 5), (200, 16384, 1024, 1), (4, 512, 16384, 8),
+         (33, 264, 8192, 4), (300, 256, 4096, 2), (520, 512, 4096, 1), (600, 264, 4096, 1), (130, 1024, 8192, 1),
+         (1, 72, 8192, 1)]
+
+
+@pytest.mark.parametrize("shape", SPLIT)
+def test_split_sums(shape):
+    run_and_check(*shape, kind=ACTS[shape[0] % 3], wgrad="operand", seed=shape[0])
+
+
+@pytest.mark.parametrize("shape", [(5, 4096, 256, 2), (200, 4096, 768, 4), (300, 256, 4096, 2)])
+def test_split_sums_are_the_same_every_time(shape):
+    n, d, m, t = shape
+    X, A, B, G = inputs(n, d, m)
+    want = tp.gated_forward(X, A, B, t)
+    gwant = tp.gated_backward(X, A, B, G, want[1], want[2], t)
+    for _ in range(10):
+        got = tp.gated_forward(X, A, B, t)
+        ggot = tp.gated_backward(X, A, B, G, want[1], want[2], t)
+        assert all(torch.equal(a, b) for a, b in zip(want + gwant, got + ggot))
+
+
+def on_gpu(X, A, B, kind):
+    """Y and O in 64 bits, and the deviations that check_forward allows (t = 1), for sizes that are too large for the host."""
+    x, a, b = (v.double() for v in (X, A, B))
+    m = b.shape[0]
+    z, slip = x @ a, acc(a.shape[0]) * (x.abs() @ a.abs())
+    g, u = z[:, :m], z[:, m:]
+    assert kind == "silu"
+    sig = torch.sigmoid(g)
+    y = g * sig * u
+    off = 1.2 * slip[:, :m] * u.abs() + (g * sig).abs() * slip[:, m:] + 2.0 ** -20 * (1 + g.abs()) * u.abs()
+    o = y @ b
+    dev = ((U / 3 ** 0.5 * y) ** 2 + off ** 2) @ (b * b)
+    return y, U * y.abs() + 2 * off, o, U * o.abs() + 7 * dev.sqrt() + acc(m) * (y.abs() @ b.abs())
+
+
+@pytest.mark.parametrize("shape", [(3, 32768, 1024), (200, 16384, 16384), (64, 4096, 16384)])
+def test_unsplit_sums_of_large_weights(shape):
+    # many column tiles: the products' own epilogues write O and Y, on single SMs and on pairs
+    n, d, m = shape
+    X, A, B, _ = inputs(n, d, m)
+    O, Z, Y = tp.gated_forward(X, A, B, 1, "silu", save=False)
+    y, y_bound, o, o_bound = on_gpu(X, A, B, "silu")
+    assert ((Y.double() - y).abs() <= y_bound).all() and ((O.double() - o).abs() <= o_bound).all()
+    O2, Z2, Y2 = tp.gated_forward(X, A, B, 1, "silu")
+    assert torch.equal(O, O2) and torch.equal(Y, Y2)
+    z = X.double() @ A.double()
+    assert ((Z2.double() - z).abs() <= U * z.abs() + acc(d) * (X.double().abs() @ A.double().abs())).all()
