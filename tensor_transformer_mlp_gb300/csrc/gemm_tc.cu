@@ -2296,11 +2296,12 @@ int pair_kernel_choice() { return g_pair_kernel.load(std::memory_order_relaxed);
 // u 0.92, e 200; GeLU' (reads Z, pipelined) u 0.87, e 570; the row-dot epilogue u 0.91, e 450;
 // dropout + residual (per-thread hash, residual loads, remapped stores) u 0.91, e 2000 (the SP
 // block's FC2: 602 us on 256 x 256 tiles, 618 us on split 256 x 512 ones). The fp32
-// read-add-write epilogue is not fitted and keeps the earlier, cautious u 0.91 with e 400. The gated block's FC1
-// (d4096 m16384, n8192, 256 x 256 against 256 x 512 tiles: 1177 / 1210 us with Z, 1137 / 1125 without; n16384 d8192 m32768:
-// 10360 / 9775, 10279 / 9623) u 0.86, e 690 and u 0.883, e 430; its dgrad-1 reads and writes 8 bytes a value in the
-// epilogue, which only the 256 x 256 tiles hide (649 / 807, 5216 / 5728 us).
-bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiKind epi, int pairs, bool z_saved = false) {
+// read-add-write epilogue is not fitted and keeps the earlier, cautious u 0.91 with e 400. The gated block's FC1 without Z
+// (256 x 256 against 256 x 512 tiles: n8192 d4096 m16384 1137 / 1125 us, n16384 d8192 m32768 10279 / 9623) u 0.883, e 430;
+// with Z the first is 1160 to 1177 / 1160 to 1210 us by itself, but a forward in a loop, under the power cap, takes 2035 /
+// 1945. Its dgrad-1 reads and writes 8 bytes a value in the epilogue, which only the 256 x 256 tiles hide (649 / 807,
+// 5216 / 5728 us; a backward under the cap 3892 / 3946).
+bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiKind epi, int pairs) {
   const int64_t mb = (M + 2 * BM - 1) / (2 * BM);
   const int64_t t256 = mb * nb256, t512 = mb * nb512;
   const int64_t w256 = (t256 + pairs - 1) / pairs, w512 = (t512 + pairs - 1) / pairs;
@@ -2312,7 +2313,7 @@ bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiK
     case kEpiStoreRowDot: u = 0.91; e = 450.0; break;
     case kEpiDropoutResidual: u = 0.91; e = 2000.0; break;
     case kEpiAccumF32: u = 0.91; e = 400.0; break;
-    case kEpiGate: u = z_saved ? 0.86 : 0.883; e = z_saved ? 690.0 : 430.0; break;
+    case kEpiGate: u = 0.883; e = 430.0; break;
     case kEpiGateGrad: return false;
     default: break;
   }
@@ -2448,7 +2449,7 @@ cudaError_t gated_gemm(int64_t M, int64_t N, int64_t K, const Operand& a, const 
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
   const int choice = pair_kernel_choice();
   const bool wide = choice == 3 || (choice == 1 && prefer_wide_blocks(M, n_blocks<EPI>(n, ep, false),
-                                                                      n_blocks<EPI>(n, ep, true), K, static_cast<EpiKind>(EPI), ctx.num_sms / 2, ep.out != nullptr));
+                                                                      n_blocks<EPI>(n, ep, true), K, static_cast<EpiKind>(EPI), ctx.num_sms / 2));
   const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * n_blocks<EPI>(n, ep, false);
   const bool narrow = EPI == kEpiGateGrad && choice == 1 && 2 * tiles <= ctx.num_sms / 2;
   CUtensorMap ta, tb;

@@ -856,6 +856,10 @@ int small_group(int h) {
 // CTAs of one resident wave of `kernel`, at most `most`.
 template <typename K>
 cudaError_t wave(int64_t* ctas, K kernel, int threads, size_t smem, int64_t most, const DeviceCtx& ctx) {
+  if (most <= ctx.num_sms) {  // nothing to ask
+    *ctas = most;
+    return cudaSuccess;
+  }
   int per_sm = 0;
   const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
   if (e != cudaSuccess) return e;
