@@ -1031,12 +1031,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 constexpr int PAIR_STAGES = 6;
 constexpr int BN_HALF = BN / 2;                               // B columns loaded per CTA
 constexpr int PAIR_STAGE_BYTES = A_STAGE_BYTES + BN_HALF * BK * 2;  // 32 KiB
-constexpr int PAIR_SMEM_BYTES = PAIR_STAGES * PAIR_STAGE_BYTES + NUM_EPI_WARPS * EPI_STAGE_BYTES + BARRIER_BYTES + 1024;
+// kEpiGateGrad: a stage less, for kZBufs blocks of 32 rows x 32 columns x {gate, up} of Z and D an epilogue warp (4 stages
+// and 3 blocks: n8192 d4096 m16384 638 -> 700 us, n1111 d1000 m2736 20.6 -> 20.0).
+template <int EPI>
+struct PairCfg {
+  static constexpr int kZBufs = EPI == kEpiGateGrad ? 2 : 0;
+  static constexpr int kStages = EPI == kEpiGateGrad ? 5 : PAIR_STAGES;
+  static constexpr int kWarpBytes = kZBufs > 0 ? kZBufs * EPI_STAGE_BYTES : EPI_STAGE_BYTES;
+  static constexpr int kBarrierBytes = kZBufs > 0 ? 2 * BARRIER_BYTES : BARRIER_BYTES;
+  static constexpr int kSmemBytes = kStages * PAIR_STAGE_BYTES + NUM_EPI_WARPS * kWarpBytes + kBarrierBytes + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget (pair kernel)");
+  static_assert((2 * kStages + 2 * NUM_ACC + 1 + NUM_EPI_WARPS * kZBufs) * 8 + 4 <= kBarrierBytes, "barrier area");
+};
 // Tile band in 256-row pair blocks. Measured on the GPT MLP shape (where the wave model still
 // sends GEMMs here): 16 pair-rows 3654 us for the six GEMMs serialised, 12: 3668, 8: 3683, 4: 3724.
 constexpr int PAIR_GROUP_M = 16;
-static_assert(PAIR_SMEM_BYTES <= 227 * 1024, "shared memory budget (pair kernel)");
-static_assert((2 * PAIR_STAGES + 2 * NUM_ACC + 1) * 8 + 4 <= BARRIER_BYTES, "barrier area");
 
 constexpr int kPaceKb = 16;                 // k-blocks between pacing points (16 and 32 measured alike; 64: +0.4 %)
 // GeLU' epilogue of the wide kernel: the producer prefetches the tile's Z rows into L2 this many
@@ -1167,34 +1176,6 @@ __device__ __forceinline__ void gate_epilogue(const EpiParams& ep, uint8_t* buf,
   }
 }
 
-// The lane's row of Z, 32 columns of the gate and of the up part from column y on, in a block of tiles that starts at
-// y_block (zeros past M, past the shard and past the block's run).
-__device__ __forceinline__ void load_gate_z(uint4 (&zg)[4], uint4 (&zu)[4], const EpiParams& ep, int64_t row, int M, int y,
-                                            int y_block) {
-  const int shard = y / ep.shard, j = y - shard * ep.shard;
-  const bool in = row < M && gated_in_run(y, y_block, ep.unit);
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(ep.aux) + row * ep.ldo +
-                             2 * static_cast<int64_t>(shard) * ep.shard + j;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    zg[i] = zu[i] = make_uint4(0, 0, 0, 0);
-    if (in && j + 8 * i < ep.shard) {
-      zg[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-      zu[i] = *reinterpret_cast<const uint4*>(src + ep.shard + 8 * i);
-    }
-  }
-}
-
-// Both parts of Z into L2: N blocks of 64 columns from y on (in a tile that starts at y_block), 128 rows from row on.
-template <int N>
-__device__ __forceinline__ void prefetch_gate_z(const EpiParams& ep, const CUtensorMap* tm_z, int y, int y_block, int row) {
-  for (int j = 0; j < N && gated_in_run(y + j * 64, y_block, ep.unit); ++j) {
-    const int shard = (y + j * 64) / ep.shard, x = y + j * 64 - shard * ep.shard;
-    tma_prefetch_l2_3d(tm_z, x, 2 * shard, row);
-    tma_prefetch_l2_3d(tm_z, x, 2 * shard + 1, row);
-  }
-}
-
 // D of two columns for the forms kept out of line: {gate word, up word}.
 __device__ __noinline__ uint2 gate_grad_other2(float a0, float a1, uint32_t zg, uint32_t zu, int kind) {
   const float2 g = unpack_bf16x2(zg), u = unpack_bf16x2(zu);
@@ -1237,47 +1218,95 @@ __device__ __forceinline__ void gate_grad_32(uint4 (&zg)[4], uint4 (&zu)[4], con
   }
 }
 
-// One epilogue warp's kPasses blocks of 32 columns of dY from column y on (t_addr: their tensor-memory address): D of
-// both parts. zg, zu hold the first block's Z and receive that of the block at y_next (< 0: none), so that a block's Z is
-// on its way while the one before is worked on. The two 2 KB blocks of a pass leave through the warp's buffer in the
-// 64-byte-swizzled layout of the map.
-template <int kPasses>
-__device__ __forceinline__ void gate_grad_epilogue(const EpiParams& ep, uint8_t* buf, int lane, int64_t row, int M, int y,
-                                                   int y_block, uint32_t t_addr, int y_next, uint4 (&zg)[4], uint4 (&zu)[4],
-                                                   const CUtensorMap* tm_d) {
-#pragma unroll 1
-  for (int p = 0; p < kPasses; ++p) {
-    const int col = y + p * 32;
-    uint4 dg[4], du[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dg[i] = zg[i];
-      du[i] = zu[i];
-    }
-    const int next = p + 1 < kPasses ? col + 32 : y_next;
-    if (next >= 0) load_gate_z(zg, zu, ep, row, M, next, y_block);
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(t_addr + static_cast<uint32_t>(p * 32), v);
-    tmem_ld_wait();
-    gate_grad_32(dg, du, v, ep.gelu);
-    if (!gated_in_run(col, y_block, ep.unit)) continue;  // uniform across the warp
-    buf_acquire(lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4);
-      *reinterpret_cast<uint4*>(buf + at) = dg[i];
-      *reinterpret_cast<uint4*>(buf + 2048 + at) = du[i];
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      const int shard = col / ep.shard, j = col - shard * ep.shard, row0 = static_cast<int>(row);
-      tma_store_3d(tm_d, buf, j, 2 * shard, row0);
-      tma_store_3d(tm_d, buf + 2048, j, 2 * shard + 1, row0);
-      bulk_commit_group();
+// One epilogue warp's blocks of 32 columns of dY, tile after tile: each block's Z (gate and up, 2 KB each, in the
+// 64-byte-swizzled layout of the maps) comes by tensor copies into one of N buffers, N - 1 blocks ahead and across tiles, D
+// replaces it there and leaves by tensor copies. Z read straight into registers one block ahead held a block up for 2.3 us
+// (each lane its own row: 32 lines a load, and the latency of HBM).
+struct GateBlocks {
+  int row0, y, n;  // first row and column, and the number of blocks
+};
+template <int N>
+struct GateGradStream {
+  uint8_t* bufs;
+  uint64_t* bars;
+  const CUtensorMap *tm_z, *tm_d;
+  int lane;
+  GateBlocks now{0, 0, 0}, next{0, 0, 0};
+  int ahead = 0;              // blocks of `now` (and then `next`) whose Z has been asked for
+  int issued = 0, used = 0;   // blocks in all
+
+  // Asks for Z while a buffer is free whose last D left two blocks ago.
+  __device__ __forceinline__ void fill(int shard) {
+    while (issued < used + N - 1) {
+      const bool in_now = ahead < now.n;
+      if (!in_now && ahead - now.n >= next.n) return;
+      const int y = in_now ? now.y + 32 * ahead : next.y + 32 * (ahead - now.n), row0 = in_now ? now.row0 : next.row0;
+      if (lane == 0) {
+        const int part = y / shard, b = issued % N;
+        mbar_arrive_expect_tx(&bars[b], EPI_STAGE_BYTES);
+        tma_load_3d(bufs + b * EPI_STAGE_BYTES, tm_z, &bars[b], y - part * shard, 2 * part, row0);
+        tma_load_3d(bufs + b * EPI_STAGE_BYTES + EPI_STAGE_BYTES / 2, tm_z, &bars[b], y - part * shard, 2 * part + 1, row0);
+      }
+      ++issued;
+      ++ahead;
     }
   }
-}
+  // A tile, and the one behind it.
+  __device__ __forceinline__ void enter(const GateBlocks& tile, const GateBlocks& behind, int shard) {
+    ahead -= now.n;
+    now = tile;
+    next = behind;
+    fill(shard);
+  }
+  // The tile's blocks, dY from tensor memory at t_addr. False: a wait ran out.
+  __device__ __forceinline__ bool run(uint32_t t_addr, int shard, int act, unsigned int* status) {
+#pragma unroll 1
+    for (int p = 0; p < now.n; ++p) {
+      const int b = used % N;
+      uint8_t* buf = bufs + b * EPI_STAGE_BYTES;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[b], static_cast<uint32_t>((used / N) & 1), status, 17))) return false;
+      uint4 g[4], u[4];
+      const int at = lane * 64, sw = (lane >> 1) & 3;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        g[i] = *reinterpret_cast<const uint4*>(buf + at + ((i ^ sw) << 4));
+        u[i] = *reinterpret_cast<const uint4*>(buf + EPI_STAGE_BYTES / 2 + at + ((i ^ sw) << 4));
+      }
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(t_addr + static_cast<uint32_t>(p * 32), v);
+      tmem_ld_wait();
+      gate_grad_32(g, u, v, act);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *reinterpret_cast<uint4*>(buf + at + ((i ^ sw) << 4)) = g[i];
+        *reinterpret_cast<uint4*>(buf + EPI_STAGE_BYTES / 2 + at + ((i ^ sw) << 4)) = u[i];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int y = now.y + 32 * p, part = y / shard;
+        tma_store_3d(tm_d, buf, y - part * shard, 2 * part, now.row0);
+        tma_store_3d(tm_d, buf + EPI_STAGE_BYTES / 2, y - part * shard, 2 * part + 1, now.row0);
+        bulk_commit_group();
+        bulk_wait_group_read<1>();  // all but this block's D have left their buffers
+      }
+      ++used;
+      fill(shard);
+    }
+    return true;
+  }
+  // Copies still in flight finish before shared memory goes away (none on the normal path).
+  __device__ __forceinline__ void drain(unsigned int* status) {
+    for (; used < issued; ++used) mbar_wait(&bars[used % N], static_cast<uint32_t>((used / N) & 1), status, 18);
+  }
+};
+template <>
+struct GateGradStream<0> {
+  uint8_t* bufs;
+  uint64_t* bars;
+  const CUtensorMap *tm_z, *tm_d;
+  int lane;
+};
 
 // BN_T: the tile's columns, 256, or 128 for the gated block's dgrad-1 where 256 would keep at most half of the pairs busy
 // (n512 d1024 m4096: 32 tiles).
@@ -1290,13 +1319,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  using Cfg = PairCfg<EPI>;
+  constexpr int PAIR_STAGES = Cfg::kStages;
   uint8_t* epi_stage = smem + PAIR_STAGES * PAIR_STAGE_BYTES;
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(epi_stage + NUM_EPI_WARPS * EPI_STAGE_BYTES);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(epi_stage + NUM_EPI_WARPS * Cfg::kWarpBytes);
   uint64_t* empty_bar = full_bar + PAIR_STAGES;
   uint64_t* tfull_bar = empty_bar + PAIR_STAGES;
   uint64_t* tempty_bar = tfull_bar + NUM_ACC;
   uint64_t* drain_bar = tempty_bar + NUM_ACC;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  uint64_t* z_bar = drain_bar + 1;  // kEpiGateGrad: Cfg::kZBufs per epilogue warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(z_bar + NUM_EPI_WARPS * Cfg::kZBufs);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1347,6 +1379,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&tempty_bar[a], 2 * NUM_EPI_THREADS);
     }
     mbar_init(drain_bar, 1);
+    for (int i = 0; i < NUM_EPI_WARPS * Cfg::kZBufs; ++i) mbar_init(&z_bar[i], 1);
     fence_mbar_init();
     tma_prefetch_desc(&tmap_a);
     tma_prefetch_desc(&tmap_b);
@@ -1386,9 +1419,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int j = 0; j < BN_T / 128; ++j) b_box[j] = EPI == kEpiGate ? gate_column(ep, y0 + j * 64, rank) : b_col + j * 64;
         const unsigned int active = static_cast<unsigned int>(min(num_pairs, num_tiles - round * num_pairs));
         for (int kb = 0; kb < num_kb; ++kb) {
-          if constexpr (EPI == kEpiGateGrad) {  // Z of this CTA's rows into L2 some k-blocks before the epilogue reads it
-            if (kb == max(0, num_kb - kAuxPrefetchKb)) prefetch_gate_z<kTileN / 64>(ep, &tmap_c2, y0, y0, a_row);
-          }
           if (pacer && kb % kPaceKb == 0) {
             pace_wait(pace, pace_target, kPaceWaitNs);
             atomicAdd(pace, 1u);
@@ -1477,6 +1507,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int c_begin = ((warp - 2) / 4) * kChunks;
     const CUtensorMap* tm_out = (tma_out & 1) ? &tmap_c : nullptr;  // bulk stores of ep.out / ep.out2
     const CUtensorMap* tm_out2 = (tma_out & 2) ? &tmap_c2 : nullptr;
+    [[maybe_unused]] GateGradStream<Cfg::kZBufs> stream{epi_stage + (warp - 2) * Cfg::kWarpBytes,
+                                                        z_bar + (warp - 2) * Cfg::kZBufs, &tmap_c2, &tmap_c, lane};
+    // kEpiGateGrad: a warp's blocks of 32 columns in a tile, none past the end of the tile's run
+    [[maybe_unused]] auto blocks_of = [&](int tile) {
+      GateBlocks b{0, 0, 0};
+      if (tile < num_tiles) {
+        int mb, nb;
+        coords(tile, mb, nb);
+        const int y0 = gated_column(nb, ep.unit, kTileN);
+        b.row0 = mb * 2 * BM + static_cast<int>(rank) * BM + q * 32;
+        b.y = y0 + c_begin * 32;
+        b.n = max(0, min(kChunks, ((y0 / ep.unit + 1) * ep.unit - b.y + 31) / 32));
+      }
+      return b;
+    };
+    [[maybe_unused]] GateBlocks next_blocks{0, 0, 0};
+    if constexpr (EPI == kEpiGateGrad) next_blocks = blocks_of(pair);
     int it = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs, ++it) {
       const int acc = it & 1;
@@ -1484,23 +1531,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int mb, nb;
       coords(tile, mb, nb);
       const int64_t row = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32 + lane;
-      uint4 zg[4], zu[4];  // kEpiGateGrad: the first block's Z comes while the accumulator is waited for
-      if constexpr (EPI == kEpiGateGrad) {
-        const int y0 = gated_column(nb, ep.unit, kTileN);
-        load_gate_z(zg, zu, ep, row, M, y0 + c_begin * 32, y0);
+      if constexpr (EPI == kEpiGateGrad) {  // the first blocks' Z comes while the accumulator is waited for
+        const GateBlocks now = next_blocks;
+        next_blocks = blocks_of(tile + num_pairs);
+        stream.enter(now, next_blocks, ep.shard);
       }
       const bool ok = mbar_wait(&tfull_bar[acc], use & 1, status, 16);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
-      uint8_t* buf = epi_stage + (warp - 2) * EPI_STAGE_BYTES;
+      [[maybe_unused]] uint8_t* buf = epi_stage + (warp - 2) * EPI_STAGE_BYTES;
       if constexpr (EPI == kEpiGate) {
         const int y0 = gated_column(nb, ep.unit, kTileN), y = y0 + c_begin * 16;  // 64 columns a warp
         if (gated_in_run(y, y0, ep.unit))
           gate_epilogue(ep, buf, lane, static_cast<int>(row) - lane, y, t_row + c_begin * 16, tm_out, tm_out2);
       } else if constexpr (EPI == kEpiGateGrad) {
-        const int y0 = gated_column(nb, ep.unit, kTileN), y = y0 + c_begin * 32;
-        gate_grad_epilogue<kChunks>(ep, buf, lane, row, M, y, y0, t_row + c_begin * 32, -1, zg, zu, tm_out);
+        if (!stream.run(t_row + c_begin * 32, ep.shard, ep.gelu, status)) break;
       } else {
         epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, buf, lane, row, M, N, nb * BN, c_begin, t_row, 0, 1.f,
                                                             row, nb, num_nb, tm_out, tm_out2);
@@ -1508,6 +1554,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_before();
       mbar_arrive_cluster(map_to_cta(&tempty_bar[acc], 0));
     }
+    if constexpr (EPI == kEpiGateGrad) stream.drain(status);
     if (lane == 0) bulk_wait_group_all();  // the last bulk stores have completed
     __syncwarp();
   }
@@ -1714,13 +1761,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if ((tma_out & 4) && kb == max(0, num_kb - kAuxPrefetchKb))
               for (int j = (half == 1 ? 4 : 0); j < (half == 0 ? 4 : 8); ++j)
                 tma_prefetch_l2_2d(&tmap_c2, nb * WIDE_BN + j * 64, a_row);
-          }
-          if constexpr (EPI == kEpiGateGrad) {
-            if (kb == max(0, num_kb - kAuxPrefetchKb)) {
-              const int y0 = gated_column(nb, ep.unit, 2 * kHalfN);
-              if (half != 1) prefetch_gate_z<kHalfN / 64>(ep, &tmap_c2, y0, y0, a_row);
-              if (half != 0) prefetch_gate_z<kHalfN / 64>(ep, &tmap_c2, y0 + kHalfN, y0, a_row);
-            }
           }
           if (pacer && kb % kPaceKb == 0) {
             pace_wait(pace, pace_target, kPaceWaitNs);
@@ -1931,30 +1971,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_arrive_cluster(map_to_cta(&tempty_bar[h], 0));
         }
       }
-    } else if constexpr (EPI == kEpiGateGrad) {
-      uint8_t* buf = epi_stage + (warp - 2) * EPI_STAGE_BYTES;
-      int tile, half;
-      for (; ok && work(it, tile, half); ++it) {
-        int mb, nb;
-        coords(tile, mb, nb);
-        const int64_t row = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32 + lane;
-        const int y0 = gated_column(nb, ep.unit, 2 * kHalfN);
-        const int h_first = half < 0 ? 0 : half, h_last = half < 0 ? 1 : half;
-        uint4 zg[4], zu[4];
-        load_gate_z(zg, zu, ep, row, M, y0 + h_first * BN + c_begin * 32, y0);
-#pragma unroll 1
-        for (int h = h_first; h <= h_last; ++h) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[h], static_cast<uint32_t>(it & 1), status, 36));
-          if (!ok) break;
-          tc_fence_after();
-          const int y = y0 + h * BN + c_begin * 32;
-          gate_grad_epilogue<kEpiChunks>(ep, buf, lane, row, M, y, y0,
-                             tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * BN + c_begin * 32),
-                             h < h_last ? y + BN : -1, zg, zu, tm_out);
-          tc_fence_before();
-          mbar_arrive_cluster(map_to_cta(&tempty_bar[h], 0));
-        }
-      }
     } else {
       int tile, half;
       for (; ok && work(it, tile, half); ++it) {
@@ -2150,15 +2166,16 @@ template <bool A_MN, bool B_MN, int EPI, int BN_T = BN>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutMaps& om, int M, int N, int K,
                         const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx) {
   auto kernel = gemm_bf16_pair_kernel<A_MN, B_MN, EPI, BN_T>;
+  constexpr int kSmem = PairCfg<EPI>::kSmemBytes;
   static SmemLimit limit;
-  cudaError_t e = allow_smem(&limit, kernel, PAIR_SMEM_BYTES, ctx);
+  cudaError_t e = allow_smem(&limit, kernel, kSmem, ctx);
   if (e != cudaSuccess) return e;
   const int64_t nb = BN_T == BN ? n_blocks<EPI>(N, ep, false) : gated_blocks(N, ep.unit, BN_T);
   const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * nb;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = PAIR_SMEM_BYTES;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -2268,7 +2285,9 @@ cudaError_t dispatch_pair(bool a_mn, bool b_mn, EpiKind epi, const CUtensorMap& 
     if (epi == kEpiGate) TPMLP_PAIR_LAUNCH(false, true, kEpiGate);
   } else if (!a_mn && !b_mn) {
     if (epi == kEpiDGelu) TPMLP_PAIR_LAUNCH(false, false, kEpiDGelu);
-    if (epi == kEpiGateGrad) TPMLP_PAIR_LAUNCH(false, false, kEpiGateGrad);
+    if constexpr (!kWide) {
+      if (epi == kEpiGateGrad) return launch_pair<false, false, kEpiGateGrad>(ta, tb, om, m, n, k, ep, stream, ctx);
+    }
     if (epi == kEpiStore) TPMLP_PAIR_LAUNCH(false, false, kEpiStore);
     if (epi == kEpiStoreRowDot) TPMLP_PAIR_LAUNCH(false, false, kEpiStoreRowDot);
     if (epi == kEpiStoreF32) TPMLP_PAIR_LAUNCH(false, false, kEpiStoreF32);
@@ -2314,7 +2333,6 @@ bool prefer_wide_blocks(int64_t M, int64_t nb256, int64_t nb512, int64_t K, EpiK
     case kEpiDropoutResidual: u = 0.91; e = 2000.0; break;
     case kEpiAccumF32: u = 0.91; e = 400.0; break;
     case kEpiGate: u = 0.883; e = 430.0; break;
-    case kEpiGateGrad: return false;
     default: break;
   }
   const double unit = u + e / static_cast<double>(K);
@@ -2448,8 +2466,8 @@ cudaError_t gated_gemm(int64_t M, int64_t N, int64_t K, const Operand& a, const 
                        const OutMaps& om, cudaStream_t stream, const DeviceCtx& ctx) {
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
   const int choice = pair_kernel_choice();
-  const bool wide = choice == 3 || (choice == 1 && prefer_wide_blocks(M, n_blocks<EPI>(n, ep, false),
-                                                                      n_blocks<EPI>(n, ep, true), K, static_cast<EpiKind>(EPI), ctx.num_sms / 2));
+  const bool wide = EPI != kEpiGateGrad && (choice == 3 || (choice == 1 && prefer_wide_blocks(M, n_blocks<EPI>(n, ep, false),
+                                                                      n_blocks<EPI>(n, ep, true), K, static_cast<EpiKind>(EPI), ctx.num_sms / 2)));
   const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * n_blocks<EPI>(n, ep, false);
   const bool narrow = EPI == kEpiGateGrad && choice == 1 && 2 * tiles <= ctx.num_sms / 2;
   CUtensorMap ta, tb;
@@ -2497,7 +2515,7 @@ cudaError_t gated_dgrad1_tc(const void* g, const void* b, const void* z, void* d
   OutMaps om;
   cudaError_t e = make_part_map(&om.c, dz, n, 2 * t, ep.shard, 32, 32);
   if (e != cudaSuccess) return e;
-  e = make_part_map(&om.c2, z, n, 2 * t, ep.shard, 64, BM);  // for the producer's L2 prefetch
+  e = make_part_map(&om.c2, z, n, 2 * t, ep.shard, 32, 32);
   if (e != cudaSuccess) return e;
   om.flags = 1;
   return gated_gemm<kEpiGateGrad>(n, m, d, Operand{g, n, d, d, false}, Operand{b, m, d, d, false}, ep, om, stream, ctx);
