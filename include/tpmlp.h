@@ -566,9 +566,9 @@ tpmlp_status tpmlp_residual_norm_backward(const void* y, const void* r, const vo
  *   pair_kernel 1: clusters of two SMs, on 256 x 512 or 256 x 256 tiles per GEMM by a model of
  *                  the launch's waves; 2: clusters of two SMs on 256 x 256 tiles only; 3: on
  *                  256 x 512 tiles only (a last round that would keep at most half the SM pairs
- *                  busy runs as 256 x 256 half-tiles, one per pair); 0: 128 x 256 tiles on one SM (the gated
- *                  block's products with an elementwise part then run as with 2). The gated block's products of few
- *                  tokens, which split their sum over the SMs, run with 1 only.
+ *                  busy runs as 256 x 256 half-tiles, one per pair); 0: 128 x 256 tiles on one SM. The gated
+ *                  block's first product then runs as with 2, its dgrad-1 always does, and its products of few tokens,
+ *                  which split their sum over the SMs, run with 1 only.
  *   pair_pacing 1: pairs wait at intervals of 16 k-blocks for the pairs of the same round of
  *                  tiles, which keeps shared operand panels in L2; 0: no pacing.
  *   pair_group  0: the default tile band (16 pair-rows walked along N, for 256 x 256 and

@@ -5,10 +5,12 @@
 //   dgrad-1  D = (G B^T) * gelu'(Z)
 //   wgrad    dB = Y^T G, dA = X^T D                 (fp32 out, K = tokens)
 //   dgrad-2  dX = D A^T         K-loop over all t shards = the f sum
+// and of the gated block, whose FC1 and dgrad-1 have epilogues of their own (kEpiGate, kEpiGateGrad).
 //
 // Two persistent kernels, one CTA per SM, sharing the epilogue code:
 //   gemm_bf16_pair_kernel (plain GEMMs): 256 x 256 tiles on clusters of two SMs
 //               (tcgen05 cta_group::2), 6-stage ring of 32 KB per SM, paced pairs
+//               (gated dgrad-1: 256 x 128 tiles too, 5 stages)
 //   gemm_bf16_wide_kernel (plain GEMMs whose wave count favours it): 256 x 512 tiles on
 //               SM pairs, 4-stage ring of 48 KB per SM, 25 % fewer operand bytes per FLOP
 //   gemm_bf16_kernel (batched GEMMs, or all of them when tpmlp_set_gemm_variant asks): 128 x 256
@@ -1073,6 +1075,12 @@ __device__ __forceinline__ void pace_wait(const unsigned int* ctr, unsigned int 
 // columns, 2 i + 1 its up columns, so copies are clipped where a shard ends inside a block. Tiles divide runs of
 // ep.unit columns: all of them where shards end on the epilogue's column blocks, else shard by shard (the columns a
 // block has past its shard are computed and dropped).
+//   FC1 (kEpiGate): one product with the columns of both projections, 4 n d m operations: tensor bound. In each 256-column
+//   accumulator the even CTA's B chunk is 128 gate columns and the odd CTA's the up columns that go with them, so operands
+//   are read as in the plain GEMMs and one warp has g and u of the same column. n8192 d4096 m16384: 1120-1170 us with Z
+//   (1880-1960 TFLOP/s), 1080-1125 without; torch's bare product of that size 1090.
+//   dgrad-1 (kEpiGateGrad): 2 n d m operations, and an epilogue that moves 8 bytes a value of dY while the next tile's products
+//   run: 640-700 us there (1570-1720 TFLOP/s); torch's bare product 537.
 template <int EPI>
 constexpr bool kGated = EPI == kEpiGate || EPI == kEpiGateGrad;
 
@@ -1220,8 +1228,8 @@ __device__ __forceinline__ void gate_grad_32(uint4 (&zg)[4], uint4 (&zu)[4], con
 
 // One epilogue warp's blocks of 32 columns of dY, tile after tile: each block's Z (gate and up, 2 KB each, in the
 // 64-byte-swizzled layout of the maps) comes by tensor copies into one of N buffers, N - 1 blocks ahead and across tiles, D
-// replaces it there and leaves by tensor copies. Z read straight into registers one block ahead held a block up for 2.3 us
-// (each lane its own row: 32 lines a load, and the latency of HBM).
+// replaces it there and leaves by tensor copies (n1111 d1000 m2736: 20.6 us a launch; 24.6 with Z read straight into
+// registers a block ahead, each lane its own row: 32 lines a load).
 struct GateBlocks {
   int row0, y, n;  // first row and column, and the number of blocks
 };
