@@ -300,10 +300,11 @@ struct RowFactors {
   float ry, ky;  // dy = ry w g - ky y
   __device__ __forceinline__ RowFactors(const float (&s)[6], const Backward& p) {
     rr = p.pre ? rsqrtf(fmaf(s[0], p.inv_h, p.eps)) : 0.f;
-    kr = rr * rr * rr * s[1] * p.inv_h;
+    // multiplied out from the sums on: the cube of a root of 1e15 or 1e-15 is none that fp32 holds
+    kr = rr * (rr * (rr * (s[1] * p.inv_h)));
     ry = p.post ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.f;
     // the sum of w g y needs no pass of its own: g is a sum of three terms
-    ky = p.post ? ry * ry * ry * p.inv_h * (s[3] + (rr * s[4] - kr * s[5])) : 0.f;
+    ky = p.post ? ry * (ry * (ry * (p.inv_h * (s[3] + (rr * s[4] - kr * s[5]))))) : 0.f;
   }
 };
 

@@ -248,3 +248,20 @@ def test_on_another_stream_from_a_graph_and_again(h):
     for a, b in zip((r, u) + want, cap[:2] + cap[2]):
         assert torch.equal(a, b)
     tp.tpmlp_device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("h", [256, 520, 2048])
+def test_gradients_of_rows_of_zeros_and_large_values(h, dtype, monkeypatch):
+    # roots from 1e15 (an eps of 1e-30 alone) to 1e-15, whose cubes fp32 does not hold
+    monkeypatch.setitem(globals(), "EPS", 1e-30)
+    for dr in (True, False):
+        c = case(2, 40, h, dtype)
+        c["x"][0, 5], c["y"][0, 5] = 0, 0
+        c["x"][0, 6:8] *= 1e15
+        c["y"][0, 8:10] *= 1e15
+        c["x"][1, 7] *= 1e15
+        c["y"][1, 7] *= 1e15
+        if not dr:
+            c["dr"] = None
+        run(c)
