@@ -10,6 +10,9 @@ square; at most 8 rounded tensors stand between an input and a result (u0, Z, Y,
 products pass a relative error on, and the gate's product adds two: sqrt(8 + 2) 2^-8 / sqrt(3) = 0.0071, and twice that for
 what passes both parts of a sum that partly cancel."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -94,3 +97,29 @@ def test_layer_captured_and_replayed():
     torch.cuda.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     assert all(torch.equal(want[2][k], got[2][k]) for k in want[2])
+
+
+COLD = """
+import torch
+from tests import test_gpu_gated_block as block
+import tensor_transformer_mlp_gb300 as tp
+p, dr1, du1 = block.make(*{shape})
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = block.layer(p, 2, dr1, du1)
+graph.replay()
+torch.cuda.synchronize()
+want = block.layer(p, 2, dr1, du1)
+assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+assert all(torch.equal(want[2][k], got[2][k]) for k in want[2])
+tp.tpmlp_device_status()
+print("same")
+"""
+
+
+@pytest.mark.parametrize("shape", [(3, 1, 512, 1024), (2, 900, 1024, 2048)])
+def test_a_process_whose_first_calls_are_captured(shape):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", COLD.format(shape=shape)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]

@@ -265,3 +265,18 @@ def test_gradients_of_rows_of_zeros_and_large_values(h, dtype, monkeypatch):
         if not dr:
             c["dr"] = None
         run(c)
+
+
+def test_backward_on_two_streams_at_once():
+    cs = [case(3, 700, 2048, torch.bfloat16, seed=k) for k in range(2)]
+    want = [run(c)[2] for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(4):
+        for k, (c, s) in enumerate(zip(cs, streams)):
+            got[k] = run(c, check=False, stream=s)[2]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+    tp.tpmlp_device_status()
