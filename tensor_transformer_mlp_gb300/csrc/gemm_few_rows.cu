@@ -9,9 +9,9 @@
 //  * with one split the kernel's epilogue applies the gate and rounds. Otherwise a CTA leaves its fp32 share in a slot of
 //    its own and a second kernel adds a tile's shares in order (no atomics). The kernels of a call are programmatic
 //    dependents of one another: the second product's ring fills with weights while the first one ends.
-// Measured, the SM-pair GEMM in brackets. d4096 m16384 (268 MB of A, 134 MB of B), 4 tokens: FC1 46.5 us, 5.8 TB/s (62); FC2
-// 21.5 us after FC1's end and 4.5 us of joining (82). 200 tokens: FC2 28 and 7 us (84); its FC1 fills the SMs without a split
-// and stays there. n512 d1024 m4096: FC2 13 and 6 us (24), dX 18 and 6 us (43).
+// Measured, the SM-pair GEMM in brackets. d4096 m16384 (268 MB of A, 134 MB of B), 4 tokens: FC1 45.5 us, 5.9 TB/s (64); FC2
+// 22 us after FC1's end and 3 us of joining (87). 200 tokens: FC2 28 and 7 us (87). n512 d1024 m4096: FC2 12.4 and 5.7 us
+// (24), dX 14 and 7 us (43).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -40,7 +40,7 @@ struct Plan {
   int nt, token_tiles;   // tokens of a tile (a multiple of 16) and tiles of them
   int col_tiles, tiles, splits, items, ctas;  // items = tiles * splits
   int shard, unit;       // the gated block's columns (EpiParams), 0: plain
-  int ranks;             // CTAs of a tile: 2 are a pair of SMs that take half of the tokens in each
+  int ranks;             // CTAs of a tile: 2 are a pair of SMs that take half of the tokens in each (with one split only)
   int stages;
 };
 
@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(ntp + t0), b);
         tmem_ld_wait();
         const int64_t token = token0 + t0;
-        if (p.splits > 1) {
-          float* out = o.slots + ((static_cast<int64_t>(at.item) * p.ranks + rank) * p.nt + t0) * kTileCols + q * 32 + lane;
+        if (!PAIR && p.splits > 1) {
+          float* out = o.slots + (static_cast<int64_t>(at.item) * p.nt + t0) * kTileCols + q * 32 + lane;
           each(tokens - t0, [&](int i) {
             out[i * kTileCols] = __uint_as_float(a[i]);
             out[i * kTileCols + kBlock] = __uint_as_float(b[i]);
@@ -378,19 +378,28 @@ __global__ void __launch_bounds__(kJoinThreads) few_rows_join_kernel(const __gri
   const int quad = static_cast<int>(item % kQuads);
   const int64_t rest = item / kQuads;
   const int ct = static_cast<int>(rest / p.n), token = static_cast<int>(rest - static_cast<int64_t>(ct) * p.n);
-  const int ti = token / p.nt, tile = ct / p.ranks * p.token_tiles + ti, rank = ct % p.ranks;
-  const int col0 = tile_column(p, tile), col = col0 + rank * cta_columns(p) + quad * 4;
-  const bool in = ct < p.col_tiles * p.ranks && (GATE ? col / p.unit == col0 / p.unit : col < p.cols);
+  const int ti = token / p.nt, tile = ct * p.token_tiles + ti;
+  const int col0 = tile_column(p, tile), col = col0 + quad * 4;
+  const bool in = ct < p.col_tiles && (GATE ? col / p.unit == col0 / p.unit : col < p.cols);
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f), u = a;
+  const int64_t share = static_cast<int64_t>(p.nt) * kTileCols, stride = p.tiles * share;
+  const float* src = o.slots + tile * share + (token - ti * p.nt) * kTileCols + quad * 4;
   if (in) {
-    const int64_t share = static_cast<int64_t>(p.nt) * kTileCols, stride = p.ranks * p.tiles * share;
-    const float* src = o.slots + (static_cast<int64_t>(tile) * p.ranks + rank) * share + (token - ti * p.nt) * kTileCols + quad * 4;
 #pragma unroll 4
     for (int c = sub; c < p.splits; c += subs) {
       add4(a, *reinterpret_cast<const float4*>(src + c * stride));
       if constexpr (GATE) add4(u, *reinterpret_cast<const float4*>(src + c * stride + kBlock));
     }
   }
+  // The shares' lines in L2 are given up: dirty, they would be written to HBM when the next product's weights take their place
+  // (d4096 m16384, 30 MB of them at 200 tokens: 90 -> 85 us a forward; 128 tokens 85 -> 82; n512 d1024 m4096, where they would
+  // stay in L2, 30.8 -> 31.0). A line is read by 8 neighbouring lanes, and by nobody else.
+  __syncwarp();
+  if (in && (quad & 7) == 0)
+    for (int c = sub; c < p.splits; c += subs) {
+      l2_discard(src + c * stride);
+      if constexpr (GATE) l2_discard(src + c * stride + kBlock);
+    }
   if (subs > 1) {
     sums[0][threadIdx.x] = a;
     if constexpr (GATE) sums[1][threadIdx.x] = u;
@@ -418,19 +427,27 @@ __global__ void __launch_bounds__(kJoinThreads) few_rows_join_kernel(const __gri
 
 // ---------------------------------------------------------------------- host side
 
-// Estimated time of a product, in us: rounds of items, each k-block at the slowest of the weights' share of HBM
-// (6.7 TB/s), the tensor core (12.7 TFLOP/s an SM) and what an SM takes in (72 KB a us; measured 65 at 37 tokens and
-// K = 1024, 83 at 256 and K = 16384); what a round costs beside its k-blocks; the shares' way to L2 and back (5 TB/s) and
-// the second kernel; the launch of pairs.
+// Estimated time of a product, in us: rounds of items, each k-block at the slowest of the weights' share of HBM (7.2 TB/s, what
+// reads alone reach), an SM's weights from HBM (70 KB a us) and all that it takes in (110), and the tensor core (15 TFLOP/s
+// an SM); what a launch (FC1: no kernel in front) and a round cost beside the k-blocks; the shares' way to L2 and back
+// (9.3 TB/s) and the second kernel. Measured / estimated:
+//   FC1, one split, m16384: d1024, 4 tokens 18.0 / 17.7, 200 24.0 / 24.8; d4096, 4 46 / 46, 64 46 / 47, 128 48 / 49, 200 50 / 52,
+//   256 51 / 54; d8192, 4 84 / 82, 200 89 / 90
+//   splits, from the end of the kernel in front: 4 tokens K16384 4096 columns, 4 splits 37 / 36, 8 27 / 26, 9 28 / 25; 200
+//   tokens there, 5 40 / 42, 9 33 / 34; n512 K8192 1024 columns, 4 29 / 27, 9 22 / 21, 19 21 / 22; 37 tokens K4096, 19 9 / 9
 double plan_time(const Plan& p) {
   const double ctas = static_cast<double>(p.items) * p.ranks, busy = std::min<double>(ctas, kSms);
-  const double kb = std::max({kWeightBytes * busy / 6.7e6, 2.0 * kTileCols * p.nt * kBK / 12.7e6, plan_stage_bytes(p) / 72e3});
+  const double kb = std::max({kWeightBytes * busy / 7.2e6, kWeightBytes / 70e3, plan_stage_bytes(p) / 110e3, 2.0 * kTileCols * p.nt * kBK / 15e6});
   const double rounds = std::ceil(ctas / kSms), blocks = std::ceil(static_cast<double>(p.num_kb) / p.splits);
-  return rounds * (blocks * kb + 1.0 + p.nt / (p.splits > 1 ? 64.0 : 20.0)) + (p.splits > 1 ? 3.0 + ctas * p.nt * kTileCols * 8.0 / 5e6 : 0.0) +
-         (p.ranks - 1) * 2.0;
+  if (p.splits == 1) {
+    const double tokens = p.ranks == 1 ? std::max(0, p.nt - kBlock) * 7e-4 : 0.0;  // beyond 128 a ring of 3 stages falls behind
+    return rounds * (blocks * (kb + tokens) + 3.3 + p.nt / 30.0) + 4.5 + (p.ranks - 1) * 0.3;
+  }
+  return rounds * (blocks * kb + 2.5 + p.nt / 100.0) + 3.8 + (p.shard ? 5.0 : 0.0) + ctas * p.nt * kTileCols * 8.0 / 9.3e6;
 }
 
-// The plan with the least estimated time over single CTAs and pairs and the number of splits.
+// The plan with the least estimated time over single CTAs, pairs (whose split sums were slower than single CTAs' at every size:
+// n200 K16384 4096 columns 34.9 us against 33.2, n512 K8192 1024 columns 22.8 against 21.0) and the number of splits.
 Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool gate) {
   Plan best{};
   double best_time = 0;
@@ -450,11 +467,11 @@ Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool gate) 
     p.col_tiles = static_cast<int>(gate ? m / p.unit * ((p.unit + w - 1) / w) : (cols + w - 1) / w);
     p.tiles = p.col_tiles * p.token_tiles;
     p.stages = std::min<int>(kMaxStages, (kSmemBudget - kBarrierBytes - 1024) / plan_stage_bytes(p));
-    // the numbers of splits that fill one, two and three waves of CTAs, parts of the first, and one
+    // one split, and the numbers that fill one, two and three waves of CTAs or parts of the first
     const int wave = kSms / (p.tiles * ranks);
-    for (const int splits : {1, wave / 4, wave / 2, 3 * wave / 4, wave, 2 * kSms / (p.tiles * ranks), 3 * kSms / (p.tiles * ranks)}) {
+    for (const int splits : {1, wave / 4, wave / 2, 3 * wave / 4, wave - 1, wave, 2 * kSms / (p.tiles * ranks), 3 * kSms / (p.tiles * ranks)}) {
       p.splits = std::min(splits, p.num_kb);
-      if (p.splits < 1) continue;
+      if (p.splits < 1 || (p.splits > 1 && ranks > 1)) continue;
       p.items = p.tiles * p.splits;
       const double time = plan_time(p);
       if (best.tiles == 0 || time < best_time) {
@@ -467,7 +484,7 @@ Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool gate) 
 }
 
 size_t slot_bytes(const Plan& p) {
-  return p.splits > 1 ? static_cast<size_t>(p.items) * p.ranks * p.nt * kTileCols * sizeof(float) : 0;
+  return p.splits > 1 ? static_cast<size_t>(p.items) * p.nt * kTileCols * sizeof(float) : 0;
 }
 
 cudaError_t encode_2d(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, uint32_t box_rows) {
@@ -532,7 +549,7 @@ cudaError_t run_ranks(Plan p, const void* tokens, int64_t k, const void* w, int6
   const int smem = p.stages * plan_stage_bytes(p) + kBarrierBytes + 1024;
   if ((e = launch_after(kernel, p.ctas, p.ranks, kThreads, smem, dependent, stream, tw, tt, p, o, ctx.status)) != cudaSuccess) return e;
   if (p.splits == 1) return cudaSuccess;
-  const int64_t threads = static_cast<int64_t>(p.col_tiles) * p.ranks * p.n * ((GATE ? kBlock : kTileCols) / 4);
+  const int64_t threads = static_cast<int64_t>(p.col_tiles) * p.n * ((GATE ? kBlock : kTileCols) / 4);
   const int subs = join_subs(p.splits, threads), here = kJoinThreads / subs;
   return launch_after(few_rows_join_kernel<GATE>, (threads + here - 1) / here, 1, kJoinThreads, 0, true, stream, p, o, subs);
 }
@@ -546,11 +563,15 @@ cudaError_t run(const Plan& p, const void* tokens, int64_t k, const void* w, int
 
 }  // namespace
 
-// Against the SM-pair GEMM (gemm_tc.cu), whose launch takes some 6 us and 0.36 us a k-block for each wave of 256 x 256
-// accumulators over 76 pairs. Measured, d4096 m16384: FC1 of 4 tokens 46.5 us here and 52 there, of 200 tokens 58 and 52; FC2
-// of 200 tokens 36 and 91.
+// Against the SM-pair GEMM (gemm_tc.cu): for each wave of 256 x 256 accumulators over 76 pairs some 0.32 us a k-block (FC1:
+// 0.35, 0.29 in a single wave) beside 6 us (7.5). Measured here and there:
+//   FC1, m16384: d4096, 4 tokens 46 and 64 us, 64 46 and 52, 128 48 and 51, 200 50 and 51, 256 51 and 51; d1024, 4 18 and 25,
+//   128 20 and 19.6, 200 24 and 20; d8192, 200 89 and 96; m4096 d4096, 4 21 and 25.5, 64 24 and 26, 200 29 and 26
+//   others: n200 K16384 4096 columns 33 and 87, n512 1024 columns K4096 19 and 24, K8192 21 and 43, n1111 1000 columns K2736 18
+//   and 20, n2048 K16384 4096 columns (one split) 147 and 151
 bool pays(const Plan& p, int64_t pair_tiles) {
-  return 4.5 + plan_time(p) < 6.0 + 0.36 * static_cast<double>(p.num_kb) * std::ceil(static_cast<double>(pair_tiles) / (kSms / 2));
+  const double waves = std::ceil(static_cast<double>(pair_tiles) / (kSms / 2)), blocks = p.num_kb * waves;
+  return plan_time(p) < (p.shard ? 7.5 + (waves > 1 ? 0.35 : 0.29) * blocks : 6.0 + 0.32 * blocks);
 }
 
 bool gemm_takes_few_rows(int64_t n, int64_t cols, int64_t k) {
