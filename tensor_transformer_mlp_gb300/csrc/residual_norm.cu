@@ -13,7 +13,7 @@
 // mean(w g y_hat) is a sum of three products that need no other sum.
 // Measured, share of the copy rate: b2 s4096 h4096 with gates of two sequences, bf16 forward 45 us (0.88), backward 76 us with 5 us
 // of sums over CTAs (0.78); fp32 94 (0.84) and 128 us (0.93). Rows of 8192 46 (0.86) and 78 (0.76), of 2048 the same, 65536 rows of
-// 512 45 (0.89) and 85 (0.70), of 256 23 (0.85) and 48 (0.62); b40 s512 h640 20 (0.78) and 54 (0.43). Four single tokens 3.3 and 8 us.
+// 512 45 (0.89) and 72 (0.83), of 256 23 (0.85) and 48 (0.62); b40 s512 h640 20 (0.78) and 46 (0.51). Four single tokens 3.3 and 8 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -653,14 +653,51 @@ __global__ void __launch_bounds__(kSmallThreads) residual_norm_small_kernel(cons
   }
 }
 
+// The CTA's sum of acc, groups of `group` lanes holding the same columns: columns 8 tid .. 8 tid + 7 end in thread tid's `out`.
+// red: [NW][cols / 4] of shared memory.
+template <int NW, int CH>
+__device__ __forceinline__ void cta_sum(float4* red, int cols, int h, int group, F2 (&acc)[CH][4], F2 (&out)[4]) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gl = tid & (group - 1);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = f2_split(acc[c][e]);
+      v[2 * e] = t.x;
+      v[2 * e + 1] = t.y;
+    }
+    for (int o = 16; o >= group; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+    const int col = (gl + c * group) * 8;
+    if (lane < group && col < h) {
+      red[w * cols / 4 + col / 4] = make_float4(v[0], v[1], v[2], v[3]);
+      red[w * cols / 4 + col / 4 + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = f2_make(0.f, 0.f);
+  if (tid * 8 < h)
+    for (int k = 0; k < NW; ++k) {
+      const float4 a = red[k * cols / 4 + 2 * tid], b = red[k * cols / 4 + 2 * tid + 1];
+      out[0] = f2_add(out[0], f2_make(a.x, a.y));
+      out[1] = f2_add(out[1], f2_make(a.z, a.w));
+      out[2] = f2_add(out[2], f2_make(b.x, b.y));
+      out[3] = f2_add(out[3], f2_make(b.z, b.w));
+    }
+  __syncthreads();
+}
+
 // A CTA's rows are worked on sequence by sequence, each group taking every (256 / group)-th row; what the groups have
 // added up meets in shared memory when the sequence, or the CTA's part of it, ends.
 template <typename T, int CH>
 __global__ void __launch_bounds__(kSmallThreads, 2)
     residual_norm_small_backward_kernel(const __grid_constant__ Backward p, int group) {
   constexpr int NW = kSmallThreads / 32;
-  __shared__ float4 red[NW][kSmallH / 4];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gl = tid & (group - 1), ngroups = kSmallThreads / group;
+  __shared__ float4 red[NW * kSmallH / 4];
+  const int tid = threadIdx.x, gl = tid & (group - 1), ngroups = kSmallThreads / group;
   const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), last = first_row(p.rows, blockIdx.x + 1, gridDim.x);
   const F2 zero = f2_make(0.f, 0.f);
   F2 wt[CH][4], pre[CH][4], acc_s[CH][4], acc_pre[CH][4];
@@ -670,39 +707,6 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc_pre[c][e] = zero;
   }
-  // the CTA's sum of acc: columns 8 tid .. 8 tid + 7 end in thread tid's `out`
-  auto gather = [&](F2 (&acc)[CH][4], F2 (&out)[4]) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 t = f2_split(acc[c][e]);
-        v[2 * e] = t.x;
-        v[2 * e + 1] = t.y;
-      }
-      for (int o = 16; o >= group; o >>= 1)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
-      const int col = (gl + c * group) * 8;
-      if (lane < group && col < p.h) {
-        red[w][col / 4] = make_float4(v[0], v[1], v[2], v[3]);
-        red[w][col / 4 + 1] = make_float4(v[4], v[5], v[6], v[7]);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = zero;
-    if (tid * 8 < p.h)
-      for (int k = 0; k < NW; ++k) {
-        const float4 a = red[k][2 * tid], b = red[k][2 * tid + 1];
-        out[0] = f2_add(out[0], f2_make(a.x, a.y));
-        out[1] = f2_add(out[1], f2_make(a.z, a.w));
-        out[2] = f2_add(out[2], f2_make(b.x, b.y));
-        out[3] = f2_add(out[3], f2_make(b.z, b.w));
-      }
-    __syncthreads();
-  };
   bool none_left = true;
   for (int64_t at = first; at < last;) {
     const int64_t seq = at / p.s, end = min(last, (seq + 1) * p.s);
@@ -764,14 +768,146 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     at = end;
     if (p.gate || p.post) {
       F2 sum[4];
-      gather(acc_s, sum);
+      cta_sum<NW>(red, kSmallH, p.h, group, acc_s, sum);
       if (tid * 8 < p.h) leave_sequence(p, seq, first, last, tid * 8, sum, none_left);
     }
     none_left = false;
   }
   grid_dependents_may_start();
   F2 sum[4];
-  gather(acc_pre, sum);
+  cta_sum<NW>(red, kSmallH, p.h, group, acc_pre, sum);
+  if (tid * 8 < p.h) Vec8<float>::store(p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * p.h + tid * 8, sum);
+}
+
+// ------------------------------------------------------------------ a warp for a row
+
+// The backward of rows of 257 to 512 columns, and of bf16 rows of up to 1024, where sequences are long: a warp takes a row, every
+// NW-th of its CTA's part of a sequence, from a ring of bulk copies of its own, so that no barrier stands between two rows.
+// NW: a multiple of the SM's four schedulers (10 and 14 warps are slower than 8 and 12), as many as registers (CH vectors of 8
+// columns a lane) allow. Against a lane group's or a CTA's rows: bf16, 65536 rows of 512 72 us for 86, 384 71 for 81; 32768 of 768
+// 60 for 80, 640 59 for 80, 1024 74 for 93 (0.80 of the copy rate); fp32, 32768 of 512 70 for 79, 264 47 for 60.
+template <typename T, int NW, int CH>
+__global__ void __launch_bounds__(NW * 32, 1)
+    residual_norm_warp_backward_kernel(const __grid_constant__ Backward p, int stages, unsigned int* status) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int64_t first = first_row(p.rows, blockIdx.x, gridDim.x), last = first_row(p.rows, blockIdx.x + 1, gridDim.x);
+  RowRing<4> ring;  // the warp's, of rows counted from the tensors' first
+  ring.row_bytes = static_cast<uint32_t>(p.h) * sizeof(T);
+  ring.step = ring.row_bytes;
+  ring.stages = stages;
+  const size_t ring_bytes = static_cast<size_t>(stages) * ring.stage_bytes();
+  ring.smem = smem + w * ring_bytes;
+  float4* red = reinterpret_cast<float4*>(smem + NW * ring_bytes);  // [NW][h / 4]
+  ring.full = reinterpret_cast<uint64_t*>(red + NW * p.h / 4) + w * stages;
+  const void* src[4] = {p.y, p.r, p.dr, p.du};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ring.src[k] = static_cast<const uint8_t*>(src[k]);
+
+  // The warp's rows in order, as far as they have been asked for (lane 0).
+  int64_t ask_end = min(last, (first / p.s + 1) * p.s), ask = first + w;
+  RowStage into;
+  auto ask_next = [&](int64_t& count) {
+    while (ask >= ask_end && ask_end < last) {
+      ask = ask_end + w;
+      ask_end = min(last, ask_end + p.s);
+    }
+    if (ask >= ask_end) return;
+    ring.issue(ask, into.st);
+    into.next(stages);
+    ask += NW;
+    ++count;
+  };
+  int64_t asked = 0, used = 0;
+  if (lane == 0) {
+    ring.init();
+    for (int i = 0; i < stages; ++i) ask_next(asked);
+  }
+  __syncthreads();
+
+  const F2 zero = f2_make(0.f, 0.f);
+  F2 wt[CH][4], pre[CH][4], acc_s[CH][4], acc_pre[CH][4];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_gain(pre[c], p.pre, (lane + c * 32) * 8, p.h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc_pre[c][e] = zero;
+  }
+  RowStage at;
+  bool ok = true, none_left = true;
+  for (int64_t begin = first; begin < last;) {
+    const int64_t seq = begin / p.s, end = min(last, (seq + 1) * p.s);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (lane + c * 32) * 8;
+      F2 g[4];
+      load_gain(wt[c], p.post, col, p.h);
+      load_gain(g, p.gate ? p.gate + seq * p.h : nullptr, col, p.h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        wt[c][e] = f2_mul(wt[c][e], g[e]);
+        acc_s[c][e] = zero;
+      }
+    }
+    // A row's sums go through the warp while the row before it has its gradients worked out.
+    auto columns = [&](int c, int st) {
+      const int col = (lane + c * 32) * 8;
+      GradColumns<T> v;
+      v.zero();
+      if (col < p.h) {
+        if (p.y) v.y.load(ring.template at<T>(st, 0) + col);
+        if (p.r) v.r.load(ring.template at<T>(st, 1) + col);
+        if (p.dr) v.dr.load(ring.template at<T>(st, 2) + col);
+        if (p.du) v.du.load(ring.template at<T>(st, 3) + col);
+      }
+      return v;
+    };
+    RowStage here;
+    float total[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t row = begin + w - NW; row < end && ok; row += NW) {
+      const bool next = row + NW < end, now = row >= begin;
+      F2 s2[6] = {zero, zero, zero, zero, zero, zero};
+      if (next) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[at.st], at.phase, status, 65));
+        if (!ok) break;
+        ++used;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) columns(c, at.st).sums(wt[c], pre[c], s2);
+      }
+      const RowFactors f(total, p);
+      float s8[8] = {sum2(s2[0]), sum2(s2[1]), sum2(s2[2]), sum2(s2[3]), sum2(s2[4]), sum2(s2[5]), 0.f, 0.f};
+      const float mine = warp_sums8(s8, lane);
+#pragma unroll
+      for (int k = 0; k < 6; ++k) total[k] = __shfl_sync(0xffffffffu, mine, 4 * k);
+      if (now) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int col = (lane + c * 32) * 8;
+          F2 ox[4], oy[4];
+          columns(c, here.st).grads(wt[c], pre[c], f, p.alpha, ox, oy, acc_s[c], acc_pre[c]);
+          if (col < p.h) {
+            Vec8<T>::store(static_cast<T*>(p.dx) + row * p.h + col, ox);
+            Vec8<T>::store(static_cast<T*>(p.dy) + row * p.h + col, oy);
+          }
+        }
+        __syncwarp();  // nobody reads the stage any more
+        if (lane == 0) ask_next(asked);
+      }
+      here = at;
+      if (next) at.next(stages);
+    }
+    begin = end;
+    if (p.gate || p.post) {
+      F2 sum[4];
+      cta_sum<NW>(red, p.h, p.h, 32, acc_s, sum);
+      if (tid * 8 < p.h) leave_sequence(p, seq, first, last, tid * 8, sum, none_left);
+    }
+    none_left = false;
+  }
+  grid_dependents_may_start();
+  if (!ok && lane == 0) ring.drain(used, asked, status, 66);
+  F2 sum[4];
+  cta_sum<NW>(red, p.h, p.h, 32, acc_pre, sum);
   if (tid * 8 < p.h) Vec8<float>::store(p.partials + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * p.h + tid * 8, sum);
 }
 
@@ -929,8 +1065,28 @@ cudaError_t backward_rows(const Backward& p, int64_t* ctas, cudaStream_t stream,
   return cudaGetLastError();
 }
 
+template <typename T, int NW, int CH>
+cudaError_t backward_warps(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
+  static SmemLimit limit;
+  constexpr size_t kSmem = 226 * 1024;
+  const size_t sums = static_cast<size_t>(NW) * p.h * sizeof(float);
+  const int stages = std::min<int>(6, static_cast<int>((kSmem - sums) / NW / ring_smem(4, p.h, sizeof(T), 1)));
+  // a row whose gradients are worked out and the next one, at the widest rows too
+  static_assert((kSmem - NW * CH * 1024) / NW / (4 * CH * 256 * sizeof(T) + sizeof(uint64_t)) >= 2, "two stages a warp");
+  auto kernel = residual_norm_warp_backward_kernel<T, NW, CH>;
+  const cudaError_t e = allow_smem(&limit, kernel, kSmem, ctx);
+  if (e != cudaSuccess) return e;
+  *ctas = std::min<int64_t>((p.rows + NW - 1) / NW, ctx.num_sms);
+  kernel<<<static_cast<unsigned>(*ctas), NW * 32, NW * ring_smem(4, p.h, sizeof(T), stages) + sums, stream>>>(p, stages, ctx.status);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
+  // Each sequence costs a CTA the sums over its warps, and a warp wants rows to have the next one's loads under way (bf16 rows of
+  // 1000 or so: 1400 in all 13.7 us against a CTA's 11.3, 8192 26 against 29; sequences of 64, 8320 rows 40.4 and 41.5).
+  const bool warps = p.s >= 64 && p.rows >= 4800;
+  if (warps && p.h > 256 && p.h <= kSmallH) return backward_warps<T, 12, 2>(p, ctas, stream, ctx);
   if (p.h <= kSmallH) {
     const int group = small_group(p.h);
     const int64_t need = (p.rows * group + kSmallThreads - 1) / kSmallThreads;
@@ -942,6 +1098,10 @@ cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, 
     return cudaGetLastError();
   }
   constexpr bool kHold = sizeof(T) == 4;
+  if constexpr (!kHold) {
+    if (warps && p.h <= 768) return backward_warps<T, 8, 3>(p, ctas, stream, ctx);
+    if (warps && p.h <= 1024) return backward_warps<T, 8, 4>(p, ctas, stream, ctx);
+  }
   if (p.h <= 1024) return backward_rows<T, 128, 1, 4, kHold>(p, ctas, stream, ctx);
   if constexpr (!kHold) {
     if (p.h <= 2048) return backward_rows<T, 128, 2, 4, kHold>(p, ctas, stream, ctx);

@@ -280,3 +280,37 @@ def test_backward_on_two_streams_at_once():
     for w, g in zip(want, got):
         assert all(torch.equal(a, b) for a, b in zip(w, g))
     tp.tpmlp_device_status()
+
+
+# from 4800 rows on in sequences of 64 tokens and more: a warp takes a row of 257 to 512 columns (bf16: 1024)
+@pytest.mark.parametrize("h,dtype", [(264, torch.float32), (512, torch.float32), (264, torch.bfloat16), (512, torch.bfloat16),
+                                     (520, torch.bfloat16), (768, torch.bfloat16), (776, torch.bfloat16), (1024, torch.bfloat16)])
+@pytest.mark.parametrize("b,s", [(1, 4800), (75, 64), (53, 100), (3, 1733), (7, 1000)])
+def test_rows_of_a_warp(b, s, h, dtype):
+    run(case(b, s, h, dtype), alpha=0.75)
+
+
+@pytest.mark.parametrize("form", list(itertools.product([False, True], repeat=3)))
+def test_rows_of_a_warp_in_every_form(form):
+    run(case(2, 2500, 904, torch.bfloat16, form), alpha=-1.5)
+    run(case(2, 2500, 312, torch.float32, form), alpha=-1.5)
+
+
+def test_rows_of_a_warp_in_place_and_alone():
+    c = case(2, 2600, 1000, torch.bfloat16)
+    r, u, want = run(c)
+    gains = dict(gamma_post=c["post"], gate=c["gate"], gamma_pre=c["pre"], eps=EPS)
+    for first, second in itertools.permutations(("y", "r", "dr", "du"), 2):
+        t = {k: (r if k == "r" else c[k]).clone() for k in ("y", "r", "dr", "du")}
+        got = tp.residual_norm_backward(t["y"], t["r"], t["dr"], t["du"], **gains, dx=t[first], dy=t[second])
+        assert got[0] is t[first] and got[1] is t[second]
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    bad = {k: v.clone() for k, v in (("y", c["y"]), ("r", r), ("dr", c["dr"]), ("du", c["du"]))}
+    bad["dr"][1, 18, 3] = float("nan")
+    got = tp.residual_norm_backward(*bad.values(), **gains)
+    keep = torch.ones(2, 2600, dtype=torch.bool, device="cuda")
+    keep[1, 18] = False
+    assert torch.equal(want[0][keep], got[0][keep]) and torch.equal(want[1][keep], got[1][keep])
+    assert torch.isnan(got[0][1, 18]).any() and torch.isnan(got[3]).any()
+    no_dr = tp.residual_norm_backward(c["y"], r, None, c["du"], **gains)
+    check_backward({**c, "dr": None}, r, no_dr, 1.0)
