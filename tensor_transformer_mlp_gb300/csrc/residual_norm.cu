@@ -416,7 +416,8 @@ __device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
 // anything up.
 // HOLD: a row stays in registers from its sums to its gradients instead, and its stage is refilled at once (for fp32, whose
 // rows leave no room for a ring of three and more in flight).
-// RING: else rows are read where they lie.
+// RING: else rows are read where they lie (fp32 rows of more than 4096 columns: 2048 of 8192 105 us, of 5120 74; held in registers
+// beside a ring of one or two, with w and gamma_pre in shared memory, 108 and 78).
 template <typename T, int NT, int CH, int MINB, bool HOLD, bool RING>
 __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(const __grid_constant__ Backward p, int stages,
                                                                               unsigned int* status) {
@@ -1106,12 +1107,12 @@ cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, 
   if constexpr (!kHold) {
     if (p.h <= 2048) return backward_rows<T, 128, 2, 4, kHold>(p, ctas, stream, ctx);
     if (p.h <= 4096) return backward_rows<T, 256, 2, 2, kHold>(p, ctas, stream, ctx);
+    return backward_rows<T, 512, 2, 1, kHold>(p, ctas, stream, ctx);
   } else {
     if (p.h <= 2048) return backward_rows<T, 256, 1, 2, kHold>(p, ctas, stream, ctx);
     if (p.h <= 4096) return backward_rows<T, 512, 1, 1, kHold>(p, ctas, stream, ctx);
     return backward_rows<T, 512, 2, 1, false, false>(p, ctas, stream, ctx);  // no ring of two rows, nor registers for one
   }
-  return backward_rows<T, 512, 2, 1, false>(p, ctas, stream, ctx);
 }
 
 tpmlp_status check_norm_shape(float alpha, float eps, int64_t b, int64_t s, int64_t h, tpmlp_dtype dt) {

@@ -314,3 +314,19 @@ def test_rows_of_a_warp_in_place_and_alone():
     assert torch.isnan(got[0][1, 18]).any() and torch.isnan(got[3]).any()
     no_dr = tp.residual_norm_backward(c["y"], r, None, c["du"], **gains)
     check_backward({**c, "dr": None}, r, no_dr, 1.0)
+
+
+@pytest.mark.parametrize("form", list(itertools.product([False, True], repeat=3)))
+@pytest.mark.parametrize("h", [4104, 5120, 8192])
+def test_wide_fp32_rows(h, form):
+    run(case(3, 167, h, torch.float32, form), alpha=0.75)
+
+
+def test_wide_fp32_rows_in_place():
+    c = case(2, 200, 6152, torch.float32)
+    r, u, want = run(c)
+    gains = dict(gamma_post=c["post"], gate=c["gate"], gamma_pre=c["pre"], eps=EPS)
+    for first, second in itertools.permutations(range(4), 2):
+        ins = [v.clone() for v in (c["y"], r, c["dr"], c["du"])]
+        got = tp.residual_norm_backward(*ins, **gains, dx=ins[first], dy=ins[second])
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
