@@ -34,8 +34,10 @@
 // records a timeout, drains its own copies and MMAs, frees tensor memory and returns.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "device_common.cuh"
 
@@ -1318,12 +1320,21 @@ struct GateGradStream<0> {
 
 // BN_T: the tile's columns, 256, or 128 for the gated block's dgrad-1 where 256 would keep at most half of the pairs busy
 // (n512 d1024 m4096: 32 tiles).
-template <bool A_MN, bool B_MN, int EPI, int BN_T = BN>
+// TWIN: a second product of the same K and layout, whose tiles follow the first one's in the same launch; both outputs leave by
+// tensor copies.
+struct NoTwin {};
+struct Twin {
+  CUtensorMap a, b, c;
+  int M, N;
+};
+template <bool A_MN, bool B_MN, int EPI, int BN_T = BN, typename TWIN = NoTwin>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                           const __grid_constant__ CUtensorMap tmap_c, const __grid_constant__ CUtensorMap tmap_c2,
                           int tma_out, int M, int N, int K, EpiParams ep, unsigned int* status, int group,
-                          unsigned int* pace) {
+                          unsigned int* pace, const __grid_constant__ TWIN twin) {
+  constexpr bool kTwin = std::is_same_v<TWIN, Twin>;
+  static_assert(!kTwin || ((EPI == kEpiStore || EPI == kEpiStoreF32) && BN_T == BN), "twin products");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -1343,17 +1354,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t rank = cluster_ctarank();  // 0: issues the MMAs; 1: its peer
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int num_pairs = static_cast<int>(gridDim.x >> 1);
-  const int num_mb = (M + 2 * BM - 1) / (2 * BM);
+  const int num_mb_1 = (M + 2 * BM - 1) / (2 * BM);
   // kEpiGate: 128 columns of Y a tile, from 128 gate and 128 up columns of A
   constexpr int kTileN = EPI == kEpiGate ? BN_T / 2 : BN_T;
   constexpr int kChunks = BN_T / 32 / (NUM_EPI_WARPS / 4);  // of 32 columns per epilogue warp
   constexpr uint32_t kStageTx = 2 * (A_STAGE_BYTES + BN_T / 2 * BK * 2);
   static_assert(BN_T == BN || EPI == kEpiGateGrad, "narrow tiles");
-  const int num_nb = kGated<EPI> ? gated_blocks(N, ep.unit, kTileN) : (N + BN_T - 1) / BN_T;
-  const int num_tiles = num_mb * num_nb;
+  const int num_nb_1 = kGated<EPI> ? gated_blocks(N, ep.unit, kTileN) : (N + BN_T - 1) / BN_T;
+  const int tiles_1 = num_mb_1 * num_nb_1;
+  int num_mb_2 = 0, num_nb_2 = 0;  // the twin's
+  if constexpr (kTwin) {
+    num_mb_2 = (twin.M + 2 * BM - 1) / (2 * BM);
+    num_nb_2 = (twin.N + BN_T - 1) / BN_T;
+  }
+  const int num_tiles = tiles_1 + num_mb_2 * num_nb_2;
+  auto is_twin = [&](int tile) { return kTwin && tile >= tiles_1; };
   // group > 0: bands of `group` pair-rows, each walked N-block by N-block (M fastest);
   // group < 0: bands of -group N-blocks, walked pair-row by pair-row (N fastest).
   auto coords = [&](int tile, int& mb, int& nb) {
+    const bool second = is_twin(tile);
+    const int num_mb = second ? num_mb_2 : num_mb_1, num_nb = second ? num_nb_2 : num_nb_1;
+    tile -= second ? tiles_1 : 0;
     if (group > 0) {
       const int group_size = group * num_nb;
       const int g = tile / group_size;
@@ -1419,6 +1440,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int tile = pair, round = 0; tile < num_tiles && ok; tile += num_pairs, ++round) {
         int mb, nb;
         coords(tile, mb, nb);
+        const CUtensorMap *map_a = &tmap_a, *map_b = &tmap_b;
+        if constexpr (kTwin) {
+          if (is_twin(tile)) {
+            map_a = &twin.a;
+            map_b = &twin.b;
+          }
+        }
         const int a_row = mb * 2 * BM + static_cast<int>(rank) * BM;
         const int y0 = kGated<EPI> ? gated_column(nb, ep.unit, kTileN) : nb * BN_T;
         const int b_col = y0 + static_cast<int>(rank) * (BN_T / 2);
@@ -1446,17 +1474,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint8_t* sa = smem + s * PAIR_STAGE_BYTES;
           uint8_t* sb = sa + A_STAGE_BYTES;
           if constexpr (!A_MN) {
-            tma_load_2d_pair(sa, &tmap_a, full0, kbl * BK, a_row);
+            tma_load_2d_pair(sa, map_a, full0, kbl * BK, a_row);
           } else {
 #pragma unroll
-            for (int j = 0; j < BM / 64; ++j) tma_load_2d_pair(sa + j * MN_BOX_BYTES, &tmap_a, full0, a_row + j * 64, kbl * BK);
+            for (int j = 0; j < BM / 64; ++j) tma_load_2d_pair(sa + j * MN_BOX_BYTES, map_a, full0, a_row + j * 64, kbl * BK);
           }
           if constexpr (!B_MN) {
-            tma_load_2d_pair(sb, &tmap_b, full0, kbl * BK, b_col);
+            tma_load_2d_pair(sb, map_b, full0, kbl * BK, b_col);
           } else {
 #pragma unroll
             for (int j = 0; j < BN_T / 128; ++j)
-              tma_load_2d_pair(sb + j * MN_BOX_BYTES, &tmap_b, full0, b_box[j], kbl * BK);
+              tma_load_2d_pair(sb + j * MN_BOX_BYTES, map_b, full0, b_box[j], kbl * BK);
           }
           ++kiter;
         }
@@ -1556,8 +1584,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       } else if constexpr (EPI == kEpiGateGrad) {
         if (!stream.run(t_row + c_begin * 32, ep.shard, ep.gelu, status)) break;
       } else {
-        epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, buf, lane, row, M, N, nb * BN, c_begin, t_row, 0, 1.f,
-                                                            row, nb, num_nb, tm_out, tm_out2);
+        int rows = M, cols = N;
+        const CUtensorMap* to = tm_out;
+        if constexpr (kTwin) {
+          to = &tmap_c;
+          if (is_twin(tile)) {
+            rows = twin.M;
+            cols = twin.N;
+            to = &twin.c;
+          }
+        }
+        epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, buf, lane, row, rows, cols, nb * BN, c_begin, t_row, 0, 1.f,
+                                                            row, nb, num_nb_1, to, tm_out2);
       }
       tc_fence_before();
       mbar_arrive_cluster(map_to_cta(&tempty_bar[acc], 0));
@@ -2170,16 +2208,18 @@ int pair_group(bool wide = false) {
   return g != 0 ? g : (wide ? WIDE_GROUP_M : PAIR_GROUP_M);
 }
 
-template <bool A_MN, bool B_MN, int EPI, int BN_T = BN>
+template <bool A_MN, bool B_MN, int EPI, int BN_T = BN, typename TWIN = NoTwin>
 cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutMaps& om, int M, int N, int K,
-                        const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx) {
-  auto kernel = gemm_bf16_pair_kernel<A_MN, B_MN, EPI, BN_T>;
+                        const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx, const TWIN& twin = {}) {
+  auto kernel = gemm_bf16_pair_kernel<A_MN, B_MN, EPI, BN_T, TWIN>;
   constexpr int kSmem = PairCfg<EPI>::kSmemBytes;
   static SmemLimit limit;
   cudaError_t e = allow_smem(&limit, kernel, kSmem, ctx);
   if (e != cudaSuccess) return e;
   const int64_t nb = BN_T == BN ? n_blocks<EPI>(N, ep, false) : gated_blocks(N, ep.unit, BN_T);
-  const int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * nb;
+  int64_t tiles = (M + 2 * BM - 1) / (2 * BM) * nb;
+  if constexpr (std::is_same_v<TWIN, Twin>)
+    tiles += static_cast<int64_t>((twin.M + 2 * BM - 1) / (2 * BM)) * ((twin.N + BN - 1) / BN);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
@@ -2218,7 +2258,7 @@ cudaError_t launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const OutM
     if (e != cudaSuccess) return e;
   }
   cfg.numAttrs = ep.dependent ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, om.c, om.c2, om.flags, M, N, K, ep, ctx.status, pair_group(), pace);
+  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, om.c, om.c2, om.flags, M, N, K, ep, ctx.status, pair_group(), pace, twin);
 }
 
 // The wide pair kernel, launched like the 256 x 256 pair kernel (persistent grid of resident pairs,
@@ -2449,6 +2489,47 @@ cudaError_t gemm_bf16_tc(int64_t M, int64_t N, int64_t K, const Operand& a, cons
     if (epi == kEpiAccumF32) return launch<true, true, kEpiAccumF32>(ta, tb, m, n, k, ep, stream, ctx);
   }
   return cudaErrorNotSupported;
+}
+
+// Two products of one K, both operands MN-major (a layer's weight gradients). Where both would run on 256 x 256 tiles they are
+// one launch: it fills the waves that the two would leave open, and has one beginning and end for two. dB and dA in bf16,
+// apart and together: n512 d1024 m4096 22 and 17 us, n1111 d1000 m2736 33 and 20, n256 d1024 m4096 17 and 12, n1024 d2048 m8192
+// 99 and 78, n300 d4096 m16384 150 and 133. Where one of them is better on 256 x 512 tiles they stay apart: n4096 d1024 m4096 82
+// and 89, n2048 d4096 m16384 468 and 495.
+cudaError_t gemm_bf16_twin(const Product& p, const Product& q, int64_t K, EpiKind epi, EpiParams ep, cudaStream_t stream,
+                           const DeviceCtx& ctx) {
+  const int choice = pair_kernel_choice(), pairs = ctx.num_sms / 2;
+  auto params = [&](const Product& x) {
+    EpiParams e = ep;
+    e.out = x.out;
+    e.ldo = x.N;
+    return e;
+  };
+  OutMaps om, om2;
+  cudaError_t e;
+  if ((e = make_out_maps(&om, epi, params(p), p.M, p.N, false)) != cudaSuccess ||
+      (e = make_out_maps(&om2, epi, params(q), q.M, q.N, false)) != cudaSuccess)
+    return e;
+  const bool maps = (om.flags & om2.flags & 1) != 0;  // not where sums are added to what is there
+  const bool wide = choice == 3 || (choice == 1 && (prefer_wide(p.M, p.N, K, epi, pairs) || prefer_wide(q.M, q.N, K, epi, pairs)));
+  if (!maps || wide || choice == 0) {
+    e = gemm_bf16_tc(p.M, p.N, K, p.a, p.b, epi, params(p), stream, ctx);
+    return e != cudaSuccess ? e : gemm_bf16_tc(q.M, q.N, K, q.a, q.b, epi, params(q), stream, ctx);
+  }
+  CUtensorMap ta, tb;
+  Twin twin;
+  if ((e = make_tmap(&ta, p.a, 64, BK)) != cudaSuccess || (e = make_tmap(&tb, p.b, 64, BK)) != cudaSuccess ||
+      (e = make_tmap(&twin.a, q.a, 64, BK)) != cudaSuccess || (e = make_tmap(&twin.b, q.b, 64, BK)) != cudaSuccess)
+    return e;
+  twin.c = om2.c;
+  twin.M = static_cast<int>(q.M);
+  twin.N = static_cast<int>(q.N);
+  const int m = static_cast<int>(p.M), n = static_cast<int>(p.N), k = static_cast<int>(K);
+  switch (epi) {
+    case kEpiStore: return launch_pair<true, true, kEpiStore, BN, Twin>(ta, tb, om, m, n, k, params(p), stream, ctx, twin);
+    case kEpiStoreF32: return launch_pair<true, true, kEpiStoreF32, BN, Twin>(ta, tb, om, m, n, k, params(p), stream, ctx, twin);
+    default: return cudaErrorNotSupported;
+  }
 }
 
 namespace {

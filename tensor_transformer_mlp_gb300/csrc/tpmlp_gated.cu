@@ -131,12 +131,10 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* A, const void* B, c
   const EpiKind wepi = wgrad == TPMLP_WGRAD_OPERAND ? kEpiStore : wgrad == TPMLP_WGRAD_F32 ? kEpiStoreF32 : kEpiAccumF32;
   // D = [dY act'(Z_gate) Z_up | dY act(Z_gate)] shard by shard, laid out as Z
   TPMLP_PASS_CUDA(gated_dgrad1_tc(G, B, Z_save, workspace, n, d, m, t, act, st, ctx), "gated dgrad-1 GEMM");
-  TPMLP_PASS_CUDA(gemm_bf16_tc(m, d, n, Operand{Y_save, n, m, m, true}, Operand{G, n, d, d, true}, wepi, plain(dB, d), st,
-                               ctx),
-                  "gated wgrad-2 GEMM");
-  TPMLP_PASS_CUDA(gemm_bf16_tc(d, 2 * m, n, Operand{X, n, d, d, true}, Operand{workspace, n, 2 * m, 2 * m, true}, wepi,
-                               plain(dA, 2 * m), st, ctx),
-                  "gated wgrad-1 GEMM");
+  TPMLP_PASS_CUDA(gemm_bf16_twin(Product{m, d, Operand{Y_save, n, m, m, true}, Operand{G, n, d, d, true}, dB},
+                                 Product{d, 2 * m, Operand{X, n, d, d, true}, Operand{workspace, n, 2 * m, 2 * m, true}, dA}, n,
+                                 wepi, plain(nullptr, 0), st, ctx),
+                  "gated wgrad GEMMs");
   // both projections' shares of dX are one sum over the 2 m columns of D
   if (few_rows_allowed() && gemm_takes_few_rows(n, d, 2 * m)) {
     TPMLP_PASS_CUDA(gemm_few_rows(workspace, A, false, dX, n, d, 2 * m, static_cast<char*>(workspace) + dz_bytes(n, m), true, st,

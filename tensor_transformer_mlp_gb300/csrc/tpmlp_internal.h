@@ -150,6 +150,15 @@ void set_gemm_variant(int pair_kernel, int pair_pacing, int pair_group);
 cudaError_t gemm_bf16_tc(int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b, EpiKind epi,
                          const EpiParams& ep, cudaStream_t stream, const DeviceCtx& ctx);
 
+// One of two products of the same K and epilogue (ep: what they share); M, N, K below 2^31.
+struct Product {
+  int64_t M, N;
+  Operand a, b;
+  void* out;  // [M][N]
+};
+cudaError_t gemm_bf16_twin(const Product& p, const Product& q, int64_t K, EpiKind epi, EpiParams ep, cudaStream_t stream,
+                           const DeviceCtx& ctx);
+
 // The gated block's two products with an elementwise part, on SM pairs whatever the variant (bf16, m / t a multiple of 8):
 //   Z = X A and Y = act(Z_gate) * Z_up (z may be null);   D from dY = G B^T and Z.
 cudaError_t gated_fc1_tc(const void* x, const void* a, void* z, void* y, int64_t n, int64_t d, int64_t m, int t, int act,
