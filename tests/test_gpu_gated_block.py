@@ -123,3 +123,43 @@ def test_a_process_whose_first_calls_are_captured(shape):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     out = subprocess.run([sys.executable, "-c", COLD.format(shape=shape)], cwd=root, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
+
+
+# What the memory of the workspaces and outputs held before must not matter: it is handed out full of NaN.
+@pytest.mark.parametrize("wgrad", ["f32", "operand"])
+@pytest.mark.parametrize("shape", [(4, 512, 4096, 2), (130, 264, 720, 3), (300, 1024, 2048, 1), (700, 520, 1040, 2), (1111, 1000, 2736, 3)])
+def test_memory_full_of_nan(shape, wgrad):
+    n, d, m, t = shape
+    p, dr, du = make(1, n, d, m)
+    gains = dict(gamma_post=p["post_a"], gate=p["gate_a"], gamma_pre=p["pre_f"], eps=EPS)
+    X, G = p["x"][0], dr[0]
+
+    def spoil():
+        torch.cuda.synchronize()
+        held = [torch.full((size,), float("nan"), device="cuda") for size in 8 * [1 << 14] + 8 * [1 << 18] + 8 * [1 << 22]]
+        del held
+
+    def steps():
+        out = []
+        for f in (lambda: tp.gated_forward(X, p["A"], p["B"], t),
+                  lambda: tp.gated_backward(X, p["A"], p["B"], G, out[0][1], out[0][2], t, wgrad=wgrad),
+                  lambda: tp.residual_norm(p["x"], p["a"], **gains),
+                  lambda: tp.residual_norm_backward(p["a"], out[2][0], dr, du, **gains)):
+            spoil()
+            out.append(f())
+        return [v for o in out for v in o]
+    first, second = steps(), steps()
+    torch.cuda.synchronize()
+    tp.tpmlp_device_status()
+    for a, b in zip(first, second):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+    Z, Y = first[1].double(), first[2].double()
+    parts = Z.view(n, t, 2, m // t)
+    noise = 2.0 ** -8 / 3 ** 0.5
+
+    def near(a, b, roundings):  # root mean squares: each rounding is off by half a step at most, evenly
+        return ((a.double() - b).norm() / b.norm()).item() <= 1.25 * roundings ** 0.5 * noise
+    assert near(Z, X.double() @ p["A"].double(), 1)
+    assert near(Y, (torch.nn.functional.silu(parts[:, :, 0]) * parts[:, :, 1]).reshape(n, m), 4)
+    assert near(first[0], Y @ p["B"].double(), 1)
+    assert near(first[5], Y.T @ G.double(), 1)
