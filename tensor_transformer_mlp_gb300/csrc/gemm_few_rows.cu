@@ -40,7 +40,7 @@ struct Plan {
   int nt, token_tiles;   // tokens of a tile (a multiple of 16) and tiles of them
   int col_tiles, tiles, splits, items, ctas;  // items = tiles * splits
   int shard, unit;       // the gated block's columns (EpiParams), 0: plain
-  int ranks;             // CTAs of a tile: 2 are a pair of SMs that take half of the tokens in each (with one split only)
+  int ranks;             // CTAs of a tile: 2 are a pair of SMs that take half of the tokens in each (FC1 with one split)
   int stages;
 };
 
@@ -446,12 +446,13 @@ double plan_time(const Plan& p) {
   return rounds * (blocks * kb + 2.5 + p.nt / 100.0) + 3.8 + (p.shard ? 5.0 : 0.0) + ctas * p.nt * kTileCols * 8.0 / 9.3e6;
 }
 
-// The plan with the least estimated time over single CTAs, pairs (whose split sums were slower than single CTAs' at every size:
-// n200 K16384 4096 columns 34.9 us against 33.2, n512 K8192 1024 columns 22.8 against 21.0) and the number of splits.
+// The plan with the least estimated time over the number of splits and, for FC1 without a split, single CTAs and pairs (whose split
+// sums were slower than single CTAs' at every size: n200 K16384 4096 columns 34.9 us against 33.2, n512 K8192 1024 columns 22.8
+// against 21.0).
 Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool gate) {
   Plan best{};
   double best_time = 0;
-  for (int ranks = 1; ranks <= 2; ++ranks) {
+  for (int ranks = 1; ranks <= (gate ? 2 : 1); ++ranks) {
     Plan p{};
     p.n = static_cast<int>(n);
     p.cols = static_cast<int>(cols);
@@ -536,7 +537,7 @@ cudaError_t launch_after(void (*kernel)(P...), int64_t ctas, int cluster, int th
 }
 
 template <bool W_MN, bool GATE, bool PAIR>
-cudaError_t run_ranks(Plan p, const void* tokens, int64_t k, const void* w, int64_t w_rows, int64_t w_cols, const Outputs& o,
+cudaError_t run(Plan p, const void* tokens, int64_t k, const void* w, int64_t w_rows, int64_t w_cols, const Outputs& o,
                 bool dependent, cudaStream_t stream, const DeviceCtx& ctx) {
   CUtensorMap tw, tt;
   cudaError_t e = encode_2d(&tw, w, w_rows, w_cols, W_MN ? kBK : kBlock);
@@ -554,13 +555,6 @@ cudaError_t run_ranks(Plan p, const void* tokens, int64_t k, const void* w, int6
   return launch_after(few_rows_join_kernel<GATE>, (threads + here - 1) / here, 1, kJoinThreads, 0, true, stream, p, o, subs);
 }
 
-template <bool W_MN, bool GATE>
-cudaError_t run(const Plan& p, const void* tokens, int64_t k, const void* w, int64_t w_rows, int64_t w_cols, const Outputs& o,
-                bool dependent, cudaStream_t stream, const DeviceCtx& ctx) {
-  return p.ranks == 2 ? run_ranks<W_MN, GATE, true>(p, tokens, k, w, w_rows, w_cols, o, dependent, stream, ctx)
-                      : run_ranks<W_MN, GATE, false>(p, tokens, k, w, w_rows, w_cols, o, dependent, stream, ctx);
-}
-
 }  // namespace
 
 // Against the SM-pair GEMM (gemm_tc.cu): for each wave of 256 x 256 accumulators over 76 pairs some 0.32 us a k-block (FC1:
@@ -568,7 +562,7 @@ cudaError_t run(const Plan& p, const void* tokens, int64_t k, const void* w, int
 //   FC1, m16384: d4096, 4 tokens 46 and 64 us, 64 46 and 52, 128 48 and 51, 200 50 and 51, 256 51 and 51; d1024, 4 18 and 25,
 //   128 20 and 19.6, 200 24 and 20; d8192, 200 89 and 96; m4096 d4096, 4 21 and 25.5, 64 24 and 26, 200 29 and 26
 //   others: n200 K16384 4096 columns 33 and 87, n512 1024 columns K4096 19 and 24, K8192 21 and 43, n1111 1000 columns K2736 18
-//   and 20, n2048 K16384 4096 columns (one split) 147 and 151
+//   and 20
 bool pays(const Plan& p, int64_t pair_tiles) {
   const double waves = std::ceil(static_cast<double>(pair_tiles) / (kSms / 2)), blocks = p.num_kb * waves;
   return plan_time(p) < (p.shard ? 7.5 + (waves > 1 ? 0.35 : 0.29) * blocks : 6.0 + 0.32 * blocks);
@@ -587,7 +581,9 @@ size_t gated_fc1_few_rows_workspace(int64_t n, int64_t d, int64_t m, int t) { re
 cudaError_t gated_fc1_few_rows(const void* x, const void* a, void* z, void* y, int64_t n, int64_t d, int64_t m, int t, int act,
                                void* workspace, cudaStream_t stream, const DeviceCtx& ctx) {
   const Outputs o{static_cast<__nv_bfloat16*>(y), static_cast<__nv_bfloat16*>(z), static_cast<float*>(workspace), act};
-  return run<true, true>(make_plan(n, m, d, m, t, true), x, d, a, d, 2 * m, o, false, stream, ctx);
+  const Plan p = make_plan(n, m, d, m, t, true);
+  return p.ranks == 2 ? run<true, true, true>(p, x, d, a, d, 2 * m, o, false, stream, ctx)
+                      : run<true, true, false>(p, x, d, a, d, 2 * m, o, false, stream, ctx);
 }
 
 size_t gemm_few_rows_workspace(int64_t n, int64_t cols, int64_t k) { return slot_bytes(make_plan(n, cols, k, 0, 1, false)); }
@@ -596,8 +592,8 @@ cudaError_t gemm_few_rows(const void* tokens, const void* w, bool w_mn, void* ou
                           void* workspace, bool dependent, cudaStream_t stream, const DeviceCtx& ctx) {
   const Plan p = make_plan(n, cols, k, 0, 1, false);
   const Outputs o{static_cast<__nv_bfloat16*>(out), nullptr, static_cast<float*>(workspace), 0};
-  return w_mn ? run<true, false>(p, tokens, k, w, k, cols, o, dependent, stream, ctx)
-              : run<false, false>(p, tokens, k, w, cols, k, o, dependent, stream, ctx);
+  return w_mn ? run<true, false, false>(p, tokens, k, w, k, cols, o, dependent, stream, ctx)
+              : run<false, false, false>(p, tokens, k, w, cols, k, o, dependent, stream, ctx);
 }
 
 }  // namespace tpmlp

@@ -311,3 +311,23 @@ def test_unsplit_sums_of_large_weights(shape):
     assert torch.equal(O, O2) and torch.equal(Y, Y2)
     z = X.double() @ A.double()
     assert ((Z2.double() - z).abs() <= U * z.abs() + acc(d) * (X.double().abs() @ A.double().abs())).all()
+
+
+@pytest.mark.parametrize("shape", [(8, 20000, 1024), (1000, 5000, 8192), (200, 1024, 16384)])
+def test_products_of_many_columns_and_of_several_rounds(shape):
+    # FC2 and dX unsplit, split over three rounds of CTAs, and split with hundreds of k-blocks each
+    n, d, m = shape
+    X, A, B, G = inputs(n, d, m)
+    O, Z, Y = tp.gated_forward(X, A, B, 1, "silu")
+    y, y_bound, o, o_bound = on_gpu(X, A, B, "silu")
+    assert ((Y.double() - y).abs() <= y_bound).all() and ((O.double() - o).abs() <= o_bound).all()
+    dX = tp.gated_backward(X, A, B, G, Z, Y, 1, wgrad="operand")[0]
+    tp.tpmlp_device_status()
+    zz = Z.double().requires_grad_()
+    D, = torch.autograd.grad(torch.nn.functional.silu(zz[:, :m]) * zz[:, m:], zz, G.double() @ B.double().T)
+    a = A.double()
+    want = D @ a.T
+    # D is rounded once, and its dY is a sum of d terms: as one more rounding of the magnitudes that it is made of
+    mag = torch.cat([zz[:, m:].abs(), zz[:, :m].abs() + 1], 1) * (G.double().abs() @ B.double().abs().T).repeat(1, 2)
+    dev = ((U / 3 ** 0.5 * D) ** 2 + (1.2 * acc(d) * mag) ** 2) @ (a * a).T
+    assert ((dX.double() - want).abs() <= U * want.abs() + 7 * dev.sqrt() + acc(2 * m) * (D.abs() @ a.abs().T)).all()
