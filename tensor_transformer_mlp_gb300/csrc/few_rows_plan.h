@@ -30,7 +30,7 @@ constexpr int kSms = 152;               // what splits and workspaces are chosen
 
 struct Plan {
   int n, cols, num_kb;   // tokens, output columns (of Y for the gate), k-blocks
-  int nt, token_tiles;   // tokens of a tile (a multiple of 16) and tiles of them
+  int nt, token_tiles;   // tokens of a tile (a multiple of 16, on a pair of 32) and tiles of them
   int col_tiles, tiles, splits, items, ctas;  // items = tiles * splits
   int shard, unit;       // the gated block's columns (EpiParams), 0: plain
   int ranks;             // CTAs of a tile: 2 are a pair of SMs that take half of the tokens in each (FC1 with one split)
@@ -80,7 +80,9 @@ inline Plan make_plan(int64_t n, int64_t cols, int64_t k, int64_t m, int t, bool
     p.cols = static_cast<int>(cols);
     p.num_kb = static_cast<int>((k + kBK - 1) / kBK);
     p.token_tiles = static_cast<int>((n + kMaxTokens - 1) / kMaxTokens);
-    p.nt = static_cast<int>(((n + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16);
+    // the tensor core's instruction takes N in steps of 16 (M = 128, one SM) or of 32 (M = 256, a pair)
+    const int64_t step = 16 * ranks;
+    p.nt = static_cast<int>(((n + p.token_tiles - 1) / p.token_tiles + step - 1) / step * step);
     p.ranks = ranks;
     if (gate) {
       p.shard = static_cast<int>(m / t);
