@@ -128,7 +128,9 @@ inline bool gemm_pays(int64_t n, int64_t cols, int64_t k) {
   return tiles <= kSms && pays(make_plan(n, cols, k, 0, 1, false), tiles);
 }
 inline bool gated_fc1_pays(int64_t n, int64_t d, int64_t m, int t) {
-  return n <= kMaxTokens && pays(make_plan(n, m, d, m, t, true), (m + kBlock - 1) / kBlock);
+  if (n > kMaxTokens) return false;
+  const Plan p = make_plan(n, m, d, m, t, true);
+  return pays(p, m / p.unit * ((p.unit + kBlock - 1) / kBlock));  // that GEMM's tiles divide runs of `unit` columns too
 }
 
 }  // namespace few_rows

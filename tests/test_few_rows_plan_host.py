@@ -38,3 +38,13 @@ def test_plain_products():
     for shape, p in zip(s, few_rows_plan.plain(s)):
         if p["takes"]:
             check(p, shape[0])
+
+
+def test_fc1_against_the_tiles_that_the_pair_gemm_really_has():
+    # shards that end inside a block are tiled one by one there: 32 shards of 264 columns are 96 tiles of 128 (two waves of 76 pairs),
+    # not the 66 of 8448 columns in a run
+    ragged, whole = few_rows_plan.fc1([(4, 8192, 8448, 32), (4, 8192, 8448, 1)])
+    assert ragged["unit"] == 264 and whole["unit"] == 8448
+    assert ragged["takes"]
+    for n in (1, 64, 128):
+        assert few_rows_plan.fc1([(n, 8192, 8448, 32)])[0]["takes"]

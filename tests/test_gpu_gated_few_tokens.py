@@ -81,3 +81,10 @@ def test_single_sms(shape):
     plan, = few_rows_plan.fc1([shape])
     assert plan["takes"] and plan["ranks"] == 1 and plan["splits"] == 1
     run_and_check(*shape)
+
+
+@pytest.mark.parametrize("shape", [(4, 8192, 8448, 32), (128, 4096, 8448, 32)])
+def test_many_ragged_shards(shape):
+    plan, = few_rows_plan.fc1([shape])
+    assert plan["takes"] and plan["splits"] == 1 and plan["unit"] == 264
+    run_and_check(*shape)
