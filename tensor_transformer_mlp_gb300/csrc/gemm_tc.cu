@@ -323,7 +323,8 @@ constexpr int kEpiChunks = BN / 32 / (NUM_EPI_WARPS / 4);  // 32-column chunks p
 
 // tm_out / tm_out2 (non-null: the plain store kinds in the pair kernels, rows not remapped) send
 // ep.out / ep.out2 through bulk tensor stores instead of store_staged. kTmaOnly (GeLU in the pair
-// kernels: both outputs always have tensor maps) compiles the bulk-store path alone. The wide
+// kernels, and the joint launch of two products, whose ep knows no output's address: all outputs have
+// tensor maps) compiles the bulk-store path alone. The wide
 // kernel has its own GeLU' epilogue; the 256 x 256 kernel's, which overlaps the next tile's main
 // loop, measured 15 % slower with bulk stores or with an L2 prefetch of Z, so it keeps both out.
 template <int EPI>
@@ -339,9 +340,11 @@ __device__ __forceinline__ void epilogue_tile(const EpiParams& ep, uint8_t* buf,
   if constexpr (EPI == kEpiStore || EPI == kEpiStoreF32) {
     constexpr bool kF32 = EPI == kEpiStoreF32;
     constexpr int kCols = kF32 ? 32 : 64;  // 128 bytes of output per row per pass
-    const int64_t prow = row < M ? remap_row(ep.remap, row) : -1;
-    void* out = kF32 ? static_cast<void*>(static_cast<float*>(ep.out) + out_off)
-                     : static_cast<void*>(static_cast<__nv_bfloat16*>(ep.out) + out_off);
+    // store_staged's destination
+    [[maybe_unused]] const int64_t prow = kTmaOnly ? -1 : row < M ? remap_row(ep.remap, row) : -1;
+    [[maybe_unused]] void* out = kTmaOnly ? nullptr
+                                 : kF32   ? static_cast<void*>(static_cast<float*>(ep.out) + out_off)
+                                          : static_cast<void*>(static_cast<__nv_bfloat16*>(ep.out) + out_off);
 #pragma unroll 1
     for (int c = c_begin; c < c_begin + kChunks; c += kCols / 32) {
       const int col0 = col_tile0 + c * 32;
@@ -368,10 +371,14 @@ __device__ __forceinline__ void epilogue_tile(const EpiParams& ep, uint8_t* buf,
                               pack_bf16x2(a[6], a[7]));
         }
       }
-      if (tm_out)
+      if constexpr (kTmaOnly) {
         store_tma(buf, seg, lane, tm_out, col0, row0);
-      else
-        store_staged<kF32>(buf, seg, lane, prow, out, ep.ldo, col0, N);
+      } else {
+        if (tm_out)
+          store_tma(buf, seg, lane, tm_out, col0, row0);
+        else
+          store_staged<kF32>(buf, seg, lane, prow, out, ep.ldo, col0, N);
+      }
     }
   } else if constexpr (EPI == kEpiStoreRowDot) {
     // bf16 stores as kEpiStore (64 columns per pass, staged), and each row's dot product of the
@@ -1594,8 +1601,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             to = &twin.c;
           }
         }
-        epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI>>(ep, buf, lane, row, rows, cols, nb * BN, c_begin, t_row, 0, 1.f,
-                                                            row, nb, num_nb_1, to, tm_out2);
+        // a tile of either product of a joint launch: no address but its tensor map's
+        epilogue_tile<EPI, false, kEpiChunks, kTmaEpi<EPI> || kTwin>(ep, buf, lane, row, rows, cols, nb * BN, c_begin, t_row, 0,
+                                                                     1.f, row, nb, num_nb_1, to, tm_out2);
       }
       tc_fence_before();
       mbar_arrive_cluster(map_to_cta(&tempty_bar[acc], 0));
@@ -2525,9 +2533,11 @@ cudaError_t gemm_bf16_twin(const Product& p, const Product& q, int64_t K, EpiKin
   twin.M = static_cast<int>(q.M);
   twin.N = static_cast<int>(q.N);
   const int m = static_cast<int>(p.M), n = static_cast<int>(p.N), k = static_cast<int>(K);
+  ep.out = nullptr;  // the outputs' maps are all that the joint launch knows of them
+  ep.ldo = 0;
   switch (epi) {
-    case kEpiStore: return launch_pair<true, true, kEpiStore, BN, Twin>(ta, tb, om, m, n, k, params(p), stream, ctx, twin);
-    case kEpiStoreF32: return launch_pair<true, true, kEpiStoreF32, BN, Twin>(ta, tb, om, m, n, k, params(p), stream, ctx, twin);
+    case kEpiStore: return launch_pair<true, true, kEpiStore, BN, Twin>(ta, tb, om, m, n, k, ep, stream, ctx, twin);
+    case kEpiStoreF32: return launch_pair<true, true, kEpiStoreF32, BN, Twin>(ta, tb, om, m, n, k, ep, stream, ctx, twin);
     default: return cudaErrorNotSupported;
   }
 }
