@@ -295,6 +295,9 @@ __global__ void __launch_bounds__(NT) residual_norm_row_kernel(const __grid_cons
 
 // The backward's six sums of a row; everything that follows from them.
 //   sums: r^2, du' r, y^2, (w y) dr, (w y) du', (w y) r with du' = du gamma_pre
+// NORMED: with gamma_post. Without it dy = w g whatever y holds: an infinite y times a ky of 0 would be NaN. A template: b2 s4096
+// h4096 bf16 73.2 us, chosen at run time for each value 77.2, by a branch for eight columns 79.6.
+template <bool NORMED>
 struct RowFactors {
   float rr, kr;  // g = dr + rr du' - kr r
   float ry, ky;  // dy = ry w g - ky y
@@ -302,9 +305,9 @@ struct RowFactors {
     rr = p.pre ? rsqrtf(fmaf(s[0], p.inv_h, p.eps)) : 0.f;
     // multiplied out from the sums on: the cube of a root of 1e15 or 1e-15 is none that fp32 holds
     kr = rr * (rr * (rr * (s[1] * p.inv_h)));
-    ry = p.post ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.f;
+    ry = NORMED ? rsqrtf(fmaf(s[2], p.inv_h, p.eps)) : 1.f;
     // the sum of w g y needs no pass of its own: g is a sum of three terms
-    ky = p.post ? ry * (ry * (ry * (p.inv_h * (s[3] + (rr * s[4] - kr * s[5]))))) : 0.f;
+    ky = NORMED ? ry * (ry * (ry * (p.inv_h * (s[3] + (rr * s[4] - kr * s[5]))))) : 0.f;
   }
 };
 
@@ -342,8 +345,9 @@ struct GradColumns {
     }
   }
   // dx and dy into ox, oy; adds to S and dgamma_pre.
-  __device__ __forceinline__ void grads(const F2 (&wt)[4], const F2 (&pre)[4], const RowFactors& k, float alpha, F2 (&ox)[4],
-                                        F2 (&oy)[4], F2 (&acc_s)[4], F2 (&acc_pre)[4]) const {
+  template <bool NORMED>
+  __device__ __forceinline__ void grads(const F2 (&wt)[4], const F2 (&pre)[4], const RowFactors<NORMED>& k, float alpha,
+                                        F2 (&ox)[4], F2 (&oy)[4], F2 (&acc_s)[4], F2 (&acc_pre)[4]) const {
     F2 yf[4], rf[4], drf[4], duf[4];
     y.unpack(yf);
     r.unpack(rf);
@@ -359,7 +363,7 @@ struct GradColumns {
       const F2 gy = f2_mul(g, ry);
       acc_s[e] = f2_fma(gy, yf[e], acc_s[e]);
       ox[e] = f2_mul(a, g);
-      oy[e] = f2_fma(gy, wt[e], f2_mul(nky, yf[e]));
+      oy[e] = NORMED ? f2_fma(gy, wt[e], f2_mul(nky, yf[e])) : f2_mul(gy, wt[e]);
     }
   }
 };
@@ -418,7 +422,7 @@ __device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
 // rows leave no room for a ring of three and more in flight).
 // RING: else rows are read where they lie (fp32 rows of more than 4096 columns: 2048 of 8192 105 us, of 5120 74; held in registers
 // beside a ring of one or two, with w and gamma_pre in shared memory, 108 and 78).
-template <typename T, int NT, int CH, int MINB, bool HOLD, bool RING>
+template <typename T, int NT, int CH, int MINB, bool HOLD, bool RING, bool NORMED>
 __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(const __grid_constant__ Backward p, int stages,
                                                                               unsigned int* status) {
   constexpr int NW = NT / 32;
@@ -535,7 +539,7 @@ __global__ void __launch_bounds__(NT, MINB) residual_norm_row_backward_kernel(co
     float total[6];
 #pragma unroll
     for (int k = 0; k < 6; ++k) total[k] = __shfl_sync(0xffffffffu, part, k);
-    const RowFactors f(total, p);
+    const RowFactors<NORMED> f(total, p);
     const int64_t row = first + i;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -693,7 +697,7 @@ __device__ __forceinline__ void cta_sum(float4* red, int cols, int h, int group,
 
 // A CTA's rows are worked on sequence by sequence, each group taking every (256 / group)-th row; what the groups have
 // added up meets in shared memory when the sequence, or the CTA's part of it, ends.
-template <typename T, int CH>
+template <typename T, int CH, bool NORMED>
 __global__ void __launch_bounds__(kSmallThreads, 2)
     residual_norm_small_backward_kernel(const __grid_constant__ Backward p, int group) {
   constexpr int NW = kSmallThreads / 32;
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       float total[6];
 #pragma unroll
       for (int k = 0; k < 6; ++k) total[k] = group_sum(sum2(s2[k]), group);
-      const RowFactors f(total, p);
+      const RowFactors<NORMED> f(total, p);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = (gl + c * group) * 8;
@@ -787,7 +791,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 // NW: a multiple of the SM's four schedulers (10 and 14 warps are slower than 8 and 12), as many as registers (CH vectors of 8
 // columns a lane) allow. Against a lane group's or a CTA's rows: bf16, 65536 rows of 512 72 us for 86, 384 71 for 81; 32768 of 768
 // 60 for 80, 640 59 for 80, 1024 74 for 93 (0.80 of the copy rate); fp32, 32768 of 512 70 for 79, 264 47 for 60.
-template <typename T, int NW, int CH>
+template <typename T, int NW, int CH, bool NORMED>
 __global__ void __launch_bounds__(NW * 32, 1)
     residual_norm_warp_backward_kernel(const __grid_constant__ Backward p, int stages, unsigned int* status) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
         for (int c = 0; c < CH; ++c) columns(c, at.st).sums(wt[c], pre[c], s2);
       }
-      const RowFactors f(total, p);
+      const RowFactors<NORMED> f(total, p);
       float s8[8] = {sum2(s2[0]), sum2(s2[1]), sum2(s2[2]), sum2(s2[3]), sum2(s2[4]), sum2(s2[5]), 0.f, 0.f};
       const float mine = warp_sums8(s8, lane);
 #pragma unroll
@@ -1051,12 +1055,12 @@ cudaError_t forward_for(const Forward& p, cudaStream_t stream, const DeviceCtx& 
   return forward_rows<T, 512, 2>(p, stream, ctx);
 }
 
-template <typename T, int NT, int CH, int MINB, bool HOLD, bool RING = true>
+template <typename T, bool NORMED, int NT, int CH, int MINB, bool HOLD, bool RING = true>
 cudaError_t backward_rows(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
   static SmemLimit limit;
   // the row whose gradients are worked out, the next one, and one on its way
   const int stages = RING ? std::min<int>(3, static_cast<int>(200 * 1024 / ring_smem(4, p.h, sizeof(T), 1))) : 0;
-  auto kernel = residual_norm_row_backward_kernel<T, NT, CH, MINB, HOLD, RING>;
+  auto kernel = residual_norm_row_backward_kernel<T, NT, CH, MINB, HOLD, RING, NORMED>;
   const size_t smem = ring_smem(4, p.h, sizeof(T), stages);
   cudaError_t e = allow_smem(&limit, kernel, 200 * 1024, ctx);
   if (e != cudaSuccess) return e;
@@ -1066,7 +1070,7 @@ cudaError_t backward_rows(const Backward& p, int64_t* ctas, cudaStream_t stream,
   return cudaGetLastError();
 }
 
-template <typename T, int NW, int CH>
+template <typename T, bool NORMED, int NW, int CH>
 cudaError_t backward_warps(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
   static SmemLimit limit;
   constexpr size_t kSmem = 226 * 1024;
@@ -1074,7 +1078,7 @@ cudaError_t backward_warps(const Backward& p, int64_t* ctas, cudaStream_t stream
   const int stages = std::min<int>(6, static_cast<int>((kSmem - sums) / NW / ring_smem(4, p.h, sizeof(T), 1)));
   // a row whose gradients are worked out and the next one, at the widest rows too
   static_assert((kSmem - NW * CH * 1024) / NW / (4 * CH * 256 * sizeof(T) + sizeof(uint64_t)) >= 2, "two stages a warp");
-  auto kernel = residual_norm_warp_backward_kernel<T, NW, CH>;
+  auto kernel = residual_norm_warp_backward_kernel<T, NW, CH, NORMED>;
   const cudaError_t e = allow_smem(&limit, kernel, kSmem, ctx);
   if (e != cudaSuccess) return e;
   *ctas = std::min<int64_t>((p.rows + NW - 1) / NW, ctx.num_sms);
@@ -1082,37 +1086,42 @@ cudaError_t backward_warps(const Backward& p, int64_t* ctas, cudaStream_t stream
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool NORMED>
 cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
   // Each sequence costs a CTA the sums over its warps, and a warp wants rows to have the next one's loads under way (bf16 rows of
   // 1000 or so: 1400 in all 13.7 us against a CTA's 11.3, 8192 26 against 29; sequences of 64, 8320 rows 40.4 and 41.5).
   const bool warps = p.s >= 64 && p.rows >= 4800;
-  if (warps && p.h > 256 && p.h <= kSmallH) return backward_warps<T, 12, 2>(p, ctas, stream, ctx);
+  if (warps && p.h > 256 && p.h <= kSmallH) return backward_warps<T, NORMED, 12, 2>(p, ctas, stream, ctx);
   if (p.h <= kSmallH) {
     const int group = small_group(p.h);
     const int64_t need = (p.rows * group + kSmallThreads - 1) / kSmallThreads;
     *ctas = std::min<int64_t>(need, std::min<int64_t>(static_cast<int64_t>(ctx.num_sms) * 2, kMaxCtas));
     if (p.h <= 256)
-      residual_norm_small_backward_kernel<T, 1><<<static_cast<unsigned>(*ctas), kSmallThreads, 0, stream>>>(p, group);
+      residual_norm_small_backward_kernel<T, 1, NORMED><<<static_cast<unsigned>(*ctas), kSmallThreads, 0, stream>>>(p, group);
     else
-      residual_norm_small_backward_kernel<T, 2><<<static_cast<unsigned>(*ctas), kSmallThreads, 0, stream>>>(p, group);
+      residual_norm_small_backward_kernel<T, 2, NORMED><<<static_cast<unsigned>(*ctas), kSmallThreads, 0, stream>>>(p, group);
     return cudaGetLastError();
   }
   constexpr bool kHold = sizeof(T) == 4;
   if constexpr (!kHold) {
-    if (warps && p.h <= 768) return backward_warps<T, 8, 3>(p, ctas, stream, ctx);
-    if (warps && p.h <= 1024) return backward_warps<T, 8, 4>(p, ctas, stream, ctx);
+    if (warps && p.h <= 768) return backward_warps<T, NORMED, 8, 3>(p, ctas, stream, ctx);
+    if (warps && p.h <= 1024) return backward_warps<T, NORMED, 8, 4>(p, ctas, stream, ctx);
   }
-  if (p.h <= 1024) return backward_rows<T, 128, 1, 4, kHold>(p, ctas, stream, ctx);
+  if (p.h <= 1024) return backward_rows<T, NORMED, 128, 1, 4, kHold>(p, ctas, stream, ctx);
   if constexpr (!kHold) {
-    if (p.h <= 2048) return backward_rows<T, 128, 2, 4, kHold>(p, ctas, stream, ctx);
-    if (p.h <= 4096) return backward_rows<T, 256, 2, 2, kHold>(p, ctas, stream, ctx);
-    return backward_rows<T, 512, 2, 1, kHold>(p, ctas, stream, ctx);
+    if (p.h <= 2048) return backward_rows<T, NORMED, 128, 2, 4, kHold>(p, ctas, stream, ctx);
+    if (p.h <= 4096) return backward_rows<T, NORMED, 256, 2, 2, kHold>(p, ctas, stream, ctx);
+    return backward_rows<T, NORMED, 512, 2, 1, kHold>(p, ctas, stream, ctx);
   } else {
-    if (p.h <= 2048) return backward_rows<T, 256, 1, 2, kHold>(p, ctas, stream, ctx);
-    if (p.h <= 4096) return backward_rows<T, 512, 1, 1, kHold>(p, ctas, stream, ctx);
-    return backward_rows<T, 512, 2, 1, false, false>(p, ctas, stream, ctx);  // no ring of two rows, nor registers for one
+    if (p.h <= 2048) return backward_rows<T, NORMED, 256, 1, 2, kHold>(p, ctas, stream, ctx);
+    if (p.h <= 4096) return backward_rows<T, NORMED, 512, 1, 1, kHold>(p, ctas, stream, ctx);
+    return backward_rows<T, NORMED, 512, 2, 1, false, false>(p, ctas, stream, ctx);  // no ring of two rows, nor registers for one
   }
+}
+
+template <typename T>
+cudaError_t backward_for(const Backward& p, int64_t* ctas, cudaStream_t stream, const DeviceCtx& ctx) {
+  return p.post ? backward_for<T, true>(p, ctas, stream, ctx) : backward_for<T, false>(p, ctas, stream, ctx);
 }
 
 tpmlp_status check_norm_shape(float alpha, float eps, int64_t b, int64_t s, int64_t h, tpmlp_dtype dt) {
