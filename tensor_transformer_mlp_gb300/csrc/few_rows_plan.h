@@ -53,8 +53,8 @@ TPMLP_HOST_DEVICE int tile_column(const Plan& p, int tile) {
 // reads alone reach), an SM's weights from HBM (70 KB a us) and all that it takes in (110), and the tensor core (15 TFLOP/s
 // an SM); what a launch (FC1: no kernel in front) and a round cost beside the k-blocks; the shares' way to L2 and back
 // (9.3 TB/s) and the second kernel. Measured / estimated:
-//   FC1, one split, m16384: d1024, 4 tokens 18.0 / 17.7, 200 24.0 / 24.8; d4096, 4 46 / 46, 64 46 / 47, 128 48 / 49, 200 50 / 52,
-//   256 51 / 54; d8192, 4 84 / 82, 200 89 / 90
+//   FC1, one split, m16384: d1024, 4 tokens 18.0 / 17.7, 200 22.4 / 24.9; d4096, 4 46 / 46, 64 46 / 47, 128 48 / 49, 200 51 / 53,
+//   256 52 / 54; d8192, 4 84 / 82, 200 88 / 90, 256 91 / 91; d4096 m11008, 200 45 / 47
 //   splits, from the end of the kernel in front: 4 tokens K16384 4096 columns, 4 splits 37 / 36, 8 27 / 26, 9 28 / 25; 200
 //   tokens there, 5 40 / 42, 9 33 / 34; n512 K8192 1024 columns, 4 29 / 27, 9 22 / 21, 19 21 / 22; 37 tokens K4096, 19 9 / 9
 inline double plan_time(const Plan& p) {
@@ -114,8 +114,9 @@ inline size_t slot_bytes(const Plan& p) {
 
 // Against the SM-pair GEMM (gemm_tc.cu): for each wave of 256 x 256 accumulators over 76 pairs some 0.32 us a k-block (FC1:
 // 0.35, 0.29 in a single wave) beside 6 us (7.5). Measured here and there:
-//   FC1, m16384: d4096, 4 tokens 46 and 64 us, 64 46 and 52, 128 48 and 51, 200 50 and 51, 256 51 and 51; d1024, 4 18 and 25,
-//   128 20 and 19.6, 200 24 and 20; d8192, 200 89 and 96; m4096 d4096, 4 21 and 25.5, 64 24 and 26, 200 29 and 26
+//   FC1, m16384: d4096, 4 tokens 46 and 64 us, 64 46 and 52, 128 48 and 51, 200 51 and 51, 256 52 and 51; d1024, 4 18 and 25,
+//   128 20 and 19.6, 200 22 and 20; d8192, 200 88 and 96; m4096 d4096, 4 21 and 25.5, 64 24 and 26, 200 29 and 26; a forward of
+//   d8192 m8448 in 32 ragged shards, 4 tokens 95 and 121, 128 100 and 121
 //   others: n200 K16384 4096 columns 33 and 87, n512 1024 columns K4096 19 and 24, K8192 21 and 43, n1111 1000 columns K2736 18
 //   and 20
 inline bool pays(const Plan& p, int64_t pair_tiles) {

@@ -1236,9 +1236,10 @@ __device__ __forceinline__ void gate_grad_32(uint4 (&zg)[4], uint4 (&zu)[4], con
 }
 
 // One epilogue warp's blocks of 32 columns of dY, tile after tile: each block's Z (gate and up, 2 KB each, in the
-// 64-byte-swizzled layout of the maps) comes by tensor copies into one of N buffers, N - 1 blocks ahead and across tiles, D
-// replaces it there and leaves by tensor copies (n1111 d1000 m2736: 20.6 us a launch; 24.6 with Z read straight into
-// registers a block ahead, each lane its own row: 32 lines a load).
+// 64-byte-swizzled layout of the maps) comes by tensor copies into one of N buffers, D replaces it there and leaves by tensor
+// copies. A block's Z is asked for once N - 1 blocks at most are unfinished: with two buffers when the block in front is done, so
+// that it comes while that block's D leaves, and a tile's first while its accumulator is waited for (n1111 d1000 m2736: 20.6 us a
+// launch; 24.6 with Z read straight into registers a block ahead, each lane its own row: 32 lines a load).
 struct GateBlocks {
   int row0, y, n;  // first row and column, and the number of blocks
 };
@@ -2503,7 +2504,10 @@ cudaError_t gemm_bf16_tc(int64_t M, int64_t N, int64_t K, const Operand& a, cons
 // one launch: it fills the waves that the two would leave open, and has one beginning and end for two. dB and dA in bf16,
 // apart and together: n512 d1024 m4096 22 and 17 us, n1111 d1000 m2736 33 and 20, n256 d1024 m4096 17 and 12, n1024 d2048 m8192
 // 99 and 78, n300 d4096 m16384 150 and 133. Where one of them is better on 256 x 512 tiles they stay apart: n4096 d1024 m4096 82
-// and 89, n2048 d4096 m16384 468 and 495.
+// and 89, n2048 d4096 m16384 468 and 495. The whole backward with fp32 gradients, apart and together: n256 d1024 m4096 48.1 and
+// 43.9, n300 d4096 m16384 325 and 313 (taken together); n4096 d1024 m4096 167 and 174, n2048 d4096 m16384 1073 and 1101 (apart).
+// The rule also keeps apart some fp32 ones that would gain, because each alone is better on 256 x 512 tiles: n512 d1024 m4096 56.7
+// and 51.4, n1111 d1000 m2736 69.3 and 59.1, n1024 d4096 m16384 639 and 612.
 cudaError_t gemm_bf16_twin(const Product& p, const Product& q, int64_t K, EpiKind epi, EpiParams ep, cudaStream_t stream,
                            const DeviceCtx& ctx) {
   const int choice = pair_kernel_choice(), pairs = ctx.num_sms / 2;

@@ -11,9 +11,10 @@
 // left out. Both directions are bound by memory: 4 values of T a column forward, 6 backward; the backward also by its
 // arithmetic, some 19 fp32 operations a value. A row's statistics are one barrier each; the backward has one in all, since
 // mean(w g y_hat) is a sum of three products that need no other sum.
-// Measured, share of the copy rate: b2 s4096 h4096 with gates of two sequences, bf16 forward 45 us (0.88), backward 76 us with 5 us
-// of sums over CTAs (0.78); fp32 94 (0.84) and 128 us (0.93). Rows of 8192 46 (0.86) and 78 (0.76), of 2048 the same, 65536 rows of
-// 512 45 (0.89) and 72 (0.83), of 256 23 (0.85) and 48 (0.62); b40 s512 h640 20 (0.78) and 46 (0.51). Four single tokens 3.3 and 8 us.
+// Measured, share of the copy rate: b2 s4096 h4096 with gates of two sequences, bf16 forward 45 to 47 us (0.84 to 0.88), backward
+// 73 us with 5 us of sums over CTAs (0.81); fp32 94 (0.84) and 130 us (0.92). 4096 rows of 8192 45 (0.87) and 77 (0.77), 16384 of
+// 2048 47 (0.84) and 73 (0.81), 65536 of 512 44 (0.89) and 71 (0.83), of 256 23 (0.86) and 48 (0.62); b40 s512 h640 21 (0.75) and 45
+// (0.52). Four single tokens 3.2 and 7.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -789,8 +790,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 // The backward of rows of 257 to 512 columns, and of bf16 rows of up to 1024, where sequences are long: a warp takes a row, every
 // NW-th of its CTA's part of a sequence, from a ring of bulk copies of its own, so that no barrier stands between two rows.
 // NW: a multiple of the SM's four schedulers (10 and 14 warps are slower than 8 and 12), as many as registers (CH vectors of 8
-// columns a lane) allow. Against a lane group's or a CTA's rows: bf16, 65536 rows of 512 72 us for 86, 384 71 for 81; 32768 of 768
-// 60 for 80, 640 59 for 80, 1024 74 for 93 (0.80 of the copy rate); fp32, 32768 of 512 70 for 79, 264 47 for 60.
+// columns a lane) allow. Against a lane group's or a CTA's rows: bf16, 65536 rows of 512 71 us for 86, 384 70 for 81; 32768 of 768
+// 59 for 80, 640 59 for 80, 1024 72 for 93 (0.82 of the copy rate); fp32, 32768 of 512 70 for 79, 264 47 for 60.
 template <typename T, int NW, int CH, bool NORMED>
 __global__ void __launch_bounds__(NW * 32, 1)
     residual_norm_warp_backward_kernel(const __grid_constant__ Backward p, int stages, unsigned int* status) {

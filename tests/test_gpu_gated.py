@@ -259,9 +259,9 @@ def test_two_calls_at_once(n):
 
 # ----------------------------------------------------------------------- sums split across the SMs
 
-# Few tokens or small outputs with a long sum (n, d, m, t). FC1 split, with shards of whole column blocks and with ragged
-# ones; on pairs of SMs; unsplit. FC2 and dX split; of two and three tiles of tokens; on pairs of SMs; output columns that
-# end inside a tile and inside a CTA's half of it.
+# Few tokens or small outputs with a long sum (n, d, m, t), all on single SMs. FC1 split, with shards of whole column blocks and with
+# ragged ones; unsplit; on the SM-pair GEMM. FC2 and dX split; of two and three tiles of tokens; output columns that end inside a
+# tile and inside its first half.
 SPLIT = [(5, 4096, 256, 2), (5, 4096, 264, 3), (150, 4096, 1000, 5), (200, 16384, 1024, 1), (4, 512, 16384, 8),
          (33, 264, 8192, 4), (300, 256, 4096, 2), (520, 512, 4096, 1), (600, 264, 4096, 1), (130, 1024, 8192, 1),
          (1, 72, 8192, 1)]
